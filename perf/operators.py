@@ -1,0 +1,482 @@
+"""Measured cases of the 8-bit paged KV cache: its page tables, its writer and the attention that reads it.
+
+A cache layer holds e4m3 codes k8, v8 [pages, page_size, kv heads, 128] and one exponent per page and kv head,
+k_exp, v_exp int8 [pages, kv heads]; the value of a code is code * 2^exp. Four operators:
+
+- tables:  the page table in CSR form, the slots and the positions of the step's new tokens, from request lengths
+- append:  new keys and values quantised into the cache through the slots
+- decode:  one query per request over its cached tokens
+- prefill: several queries per request, causal, over its cached tokens
+
+Where ``own`` is false, run() computes them in elementary torch operations; where it is true, through the package.
+"""
+import math
+import random
+
+import numpy as np
+import torch
+
+own = False
+
+D = 128  # head dimension of the cache
+
+
+# ---------------------------------------------------------------- cases
+def listed():
+    return [
+        # one step of a small batch: 4 requests growing by one token each, as between two decode steps
+        dict(name="tables_decode_4", op="tables", batch=4, ps=16, lo=100, hi=2000, new=1, pad=0, ls=1),
+        # a full decode batch of 256 requests, padded for a captured graph
+        dict(name="tables_decode_256", op="tables", batch=256, ps=16, lo=500, hi=16384, new=1, pad=64, ls=2),
+        # page size 1 and whole prompts: a million table entries and as many slots
+        dict(name="tables_prompts_page1", op="tables", batch=64, ps=1, lo=0, hi=2000, new=16384, pad=0, ls=3),
+        # the new token of each of 64 decoding requests
+        dict(name="append_decode_64", op="append", batch=64, ps=16, hk=8, lo=1, hi=4096, new=1, f32=False, ls=4),
+        # ragged prompts appended behind what is cached (second turns of a chat)
+        dict(name="append_ragged", op="append", batch=16, ps=16, hk=8, lo=0, hi=900, new=2048, f32=False, ls=5),
+        # long prompts into large pages, keys and values still in 32 bits
+        dict(name="append_prompts_f32", op="append", batch=8, ps=64, hk=8, lo=0, hi=0, new=8192, f32=True, ls=6),
+        # one request with a short cache: latency
+        dict(name="decode_1_short", op="decode", batch=1, ps=16, hq=32, hk=8, lo=333, hi=333, window=0, cap=0.0, ls=7),
+        # the batched decode of an 8-billion-parameter layer shape: 64 requests, up to 8192 tokens, 16-token pages
+        dict(name="decode_64", op="decode", batch=64, ps=16, hq=32, hk=8, lo=512, hi=8192, window=0, cap=0.0, ls=8),
+        # page size 1 (every token its own block), 64 query heads over 8
+        dict(name="decode_page1", op="decode", batch=32, ps=1, hq=64, hk=8, lo=4096, hi=4096, window=0, cap=0.0, ls=9),
+        # a short prompt against a short cache: latency
+        dict(name="prefill_small", op="prefill", batch=2, ps=16, hq=32, hk=8, lo=0, hi=150, new=70, window=0, cap=0.0,
+             ls=10),
+        # 16 ragged prompts, nothing cached before
+        dict(name="prefill_ragged", op="prefill", batch=16, ps=16, hq=32, hk=8, lo=0, hi=0, new=2048, window=0,
+             cap=0.0, ls=11),
+        # chunks of long prompts behind a long cache
+        dict(name="prefill_chunks", op="prefill", batch=4, ps=64, hq=32, hk=8, lo=12000, hi=15000, new=1024, window=0,
+             cap=0.0, ls=12),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["tables", "append", "decode", "decode", "prefill", "prefill"])
+    ls = rng.randrange(1 << 20)
+    ps = rng.choice([1, 5, 8, 12, 16, 32, 64, 128])
+    if op == "tables":
+        batch = _log_int(rng, 1, 512)
+        hi = _log_int(rng, 16, max(32, min(16384, 2000000 // batch)))
+        new = rng.choice([1, 1, _log_int(rng, 2, max(3, min(16384, 1000000 // batch)))])
+        if (hi + new) * batch > 1000000 * ps:
+            ps = 16
+        return dict(op=op, batch=batch, ps=ps, lo=0, hi=hi, new=new, pad=rng.choice([0, 7, 128]), ls=ls)
+    if op == "append":
+        batch = _log_int(rng, 1, 256)
+        new = rng.choice([1, _log_int(rng, 2, max(3, min(4096, 30000 // batch)))])
+        hi = _log_int(rng, 1, max(2, min(4096, 100000 // batch)))
+        return dict(op=op, batch=batch, ps=ps, hk=rng.choice([1, 2, 8]), lo=0, hi=hi, new=new,
+                    f32=rng.random() < 0.25, ls=ls)
+    if op == "decode":
+        hq, hk = rng.choice([(32, 8), (64, 8), (16, 2), (12, 4), (8, 8), (32, 2), (40, 8), (5, 1)])
+        batch = _log_int(rng, 1, 128)
+        hi = _log_int(rng, 8, max(16, min(65536, 2200000 // (batch * hk))))
+        return dict(op=op, batch=batch, ps=ps, hq=hq, hk=hk, lo=max(1, hi // 8), hi=hi,
+                    window=rng.choice([0, 0, 0, max(1, hi // 3)]), cap=rng.choice([0.0, 0.0, 30.0]), ls=ls)
+    hq, hk = rng.choice([(32, 8), (16, 2), (8, 8), (32, 2), (4, 1)])
+    batch = _log_int(rng, 1, 16)
+    new = _log_int(rng, 2, max(3, min(2048, 8192 // batch)))
+    hi = _log_int(rng, 1, max(2, 16384 // batch))
+    return dict(op=op, batch=batch, ps=ps, hq=hq, hk=hk, lo=0, hi=hi, new=new,
+                window=rng.choice([0, 0, 0, max(1, hi // 2)]), cap=rng.choice([0.0, 0.0, 30.0]), ls=ls)
+
+
+def _lens(case):
+    """(cached tokens, new tokens) of each request: fixed by the case, inclusive draws."""
+    r = np.random.default_rng(case["ls"])
+    cached = r.integers(case["lo"], case["hi"] + 1, size=case["batch"]).astype(np.int64)
+    if case["op"] == "decode":
+        return cached - 1, np.ones(case["batch"], np.int64)
+    n = case["new"]
+    new = np.ones(case["batch"], np.int64) if n == 1 else r.integers((n + 1) // 2, n + 1, size=case["batch"])
+    return cached, new.astype(np.int64)
+
+
+def _pages(lens, ps):
+    return (lens + ps - 1) // ps
+
+
+def _visible(cached, new, window):
+    """Visible (query, key) pairs per head: query i of a request sees keys up to cached + i, within the window."""
+    total = 0
+    for c, n in zip(cached.tolist(), new.tolist()):
+        seen = np.arange(c + 1, c + n + 1, dtype=np.int64)
+        total += int((np.minimum(seen, window + 1) if window else seen).sum())
+    return total
+
+
+def work(case):
+    cached, new = _lens(case)
+    ps, B = case["ps"], case["batch"]
+    n, total = int(new.sum()), _pages(cached + new, ps)
+    grown, tokens = int((total - _pages(cached, ps)).sum()), n
+    if case["op"] == "tables":
+        # lengths, old entries read, free pages read, new entries written, CSR written, slots and positions written
+        b = 8 * B + 4 * (int(total.sum()) - grown) + 4 * grown + 4 * grown + 4 * (int(total.sum()) + case["pad"])
+        b += 12 * (tokens + case["pad"]) + 4 * (2 * (B + 1) + B)
+        return {"bytes": b, "flops": 0}
+    hk = case["hk"]
+    if case["op"] == "append":
+        touched = int((total - cached // ps).sum())
+        return {"bytes": n * (hk * D * 2 * ((4 if case["f32"] else 2) + 1) + 8) + 2 * touched * hk, "flops": 0}
+    w = case["window"]
+    pairs = _visible(cached, new, w)
+    kv = cached + new
+    read = np.minimum(kv, w + new) if w else kv
+    pages = int(_pages(read, ps).sum())
+    b = int(read.sum()) * hk * D * 2 + pages * (2 * hk + 4) + n * case["hq"] * (D * 4 + 4)
+    return {"bytes": b, "flops": 4 * D * case["hq"] * pairs}
+
+
+# ---------------------------------------------------------------- inputs
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(int(seed))
+    return g
+
+
+def _i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+
+def _indptr(counts):
+    return np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+
+
+def _slots(block_table, cached, new, ps):
+    """Slots of the new tokens (int64) through a block table on the GPU."""
+    req = torch.from_numpy(np.repeat(np.arange(len(new)), new)).cuda()
+    pos = torch.from_numpy(np.concatenate([np.arange(c, c + m) for c, m in zip(cached.tolist(), new.tolist())])).cuda()
+    return block_table[req, pos // ps].long() * ps + pos % ps
+
+
+def _cache(g, num_pages, ps, hk):
+    """A filled cache: normal values whose size differs from page to page and head to head, as e4m3 and exponents."""
+    e = torch.randint(-7, -3, (num_pages, hk), generator=g, device="cuda", dtype=torch.int32)
+    codes = torch.empty((num_pages, ps, hk, D), dtype=torch.float8_e4m3fn, device="cuda")
+    step = max(1, (1 << 26) // (ps * hk * D))
+    for i in range(0, num_pages, step):
+        x = torch.randn((min(step, num_pages - i), ps, hk, D), generator=g, device="cuda")
+        codes[i:i + step] = (x * 100.0).clamp_(-448.0, 448.0).to(torch.float8_e4m3fn)
+    return codes, e.to(torch.int8)
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    cached, new = _lens(case)
+    ps, B = case["ps"], case["batch"]
+    total = _pages(cached + new, ps)
+    if case["op"] == "tables":
+        old = _pages(cached, ps)
+        need = int(total.sum())
+        ids = torch.randperm(need + 50, generator=g, device="cuda").to(torch.int32)
+        width = int(total.max()) + 3
+        table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+        row = torch.from_numpy(np.repeat(np.arange(B), old)).cuda()
+        col = torch.from_numpy(np.concatenate([np.arange(k) for k in old.tolist()])).cuda()
+        n_old = int(old.sum())
+        table[row, col] = ids[:n_old]
+        free = ids[n_old:].contiguous()
+        num_free = torch.tensor([free.numel()], dtype=torch.int32, device="cuda")
+        s = dict(case=case, cached=_i32(cached), new=_i32(new), table=table, free=free, num_free=num_free,
+                 cap_pages=need + case["pad"], cap_tokens=int(new.sum()) + case["pad"])
+        return s
+    hk = case["hk"]
+    num_pages = int(total.sum()) + 5
+    perm = torch.randperm(num_pages, generator=g, device="cuda").to(torch.int32)
+    kv_indptr = _indptr(total)
+    if case["op"] == "append":
+        width = max(1, int(total.max()))
+        table = torch.zeros((B, width), dtype=torch.int32, device="cuda")
+        row = torch.from_numpy(np.repeat(np.arange(B), total)).cuda()
+        col = torch.from_numpy(np.concatenate([np.arange(k) for k in total.tolist()])).cuda()
+        table[row, col] = perm[:int(total.sum())]
+        k8, k_exp = _cache(g, num_pages, ps, hk)
+        v8, v_exp = _cache(g, num_pages, ps, hk)
+        n = int(new.sum())
+        # keys and values as slices of one projection's output: [n, query heads | key heads | value heads]
+        proj = torch.randn((n, (2 + 2 * hk) * D), generator=g, device="cuda")
+        size = torch.exp2(torch.rand((n, 1), generator=g, device="cuda") * 2 - 1)  # tokens differ in size
+        proj = (proj * size).to(torch.float32 if case["f32"] else torch.bfloat16)
+        k = proj[:, 2 * D:(2 + hk) * D].unflatten(1, (hk, D))
+        v = proj[:, (2 + hk) * D:].unflatten(1, (hk, D))
+        return dict(case=case, k=k, v=v, slots=_slots(table, cached, new, ps), k8=k8, v8=v8, k_exp=k_exp, v_exp=v_exp)
+    k8, k_exp = _cache(g, num_pages, ps, hk)
+    v8, v_exp = _cache(g, num_pages, ps, hk)
+    n, hq = int(new.sum()), case["hq"]
+    q = torch.randn((n, hq, D), generator=g, device="cuda").to(torch.bfloat16)
+    kv_indices = perm[:int(total.sum())].contiguous()
+    last = np.where(total > 0, (cached + new - 1) % ps + 1, 0)
+    s = dict(case=case, q=q, k8=k8, v8=v8, k_exp=k_exp, v_exp=v_exp, kv_indices=kv_indices, kv_indptr=kv_indptr,
+             last=last, qo_indptr=_indptr(new), scale=1.0 / math.sqrt(D))
+    if own:
+        import block_sparse_paged_gb300 as bsp
+        decode = case["op"] == "decode"
+        pa = bsp.PagedAttention(case["op"], hq, hk, D, ps, causal=not decode, dtype=torch.bfloat16, max_batch=B,
+                                max_qo_tokens=n, window_left=case["window"], logits_soft_cap=case["cap"])
+        pa.plan(kv_indptr, last, qo_indptr=None if decode else s["qo_indptr"])
+        s["attention"] = pa
+    return s
+
+
+# ---------------------------------------------------------------- plain forms
+def _plain_tables(s):
+    ps = s["case"]["ps"]
+    dev = s["table"].device
+    cached, new = s["cached"].long(), s["new"].long()
+    B, zero = cached.numel(), torch.zeros(1, dtype=torch.int64, device=dev)
+    old = (cached + ps - 1) // ps
+    total = (cached + new + ps - 1) // ps
+    grow = total - old
+    kv_indptr = torch.cat([zero, torch.cumsum(total, 0)])
+    qo_indptr = torch.cat([zero, torch.cumsum(new, 0)])
+    first = torch.cumsum(grow, 0) - grow
+    # new table entries: column old + j of a row takes free page first + j
+    col = torch.arange(s["table"].shape[1], device=dev)[None, :]
+    fresh = (col >= old[:, None]) & (col < total[:, None])
+    take = (first[:, None] + col - old[:, None]).clamp(0, s["free"].numel() - 1)
+    table = torch.where(fresh, s["free"][take], s["table"])
+    e = torch.arange(s["cap_pages"], device=dev)
+    b = torch.searchsorted(kv_indptr[1:], e, right=True).clamp(max=B - 1)
+    inside = e < kv_indptr[-1]
+    idx = table[b, torch.where(inside, e - kv_indptr[b], 0)]
+    kv_indices = torch.where(inside, idx, 0).int()
+    t = torch.arange(s["cap_tokens"], device=dev)
+    b = torch.searchsorted(qo_indptr[1:], t, right=True).clamp(max=B - 1)
+    inside = t < qo_indptr[-1]
+    pos = torch.where(inside, cached[b] + t - qo_indptr[b], 0)
+    slot = torch.where(inside, table[b, pos // ps].long() * ps + pos % ps, -1)
+    last = torch.where(total > 0, (cached + new - 1) % ps + 1, 0)
+    counts = torch.stack([kv_indptr[-1], qo_indptr[-1], grow.sum(), torch.zeros_like(qo_indptr[-1])])
+    return {"block_table": table, "kv_indptr": kv_indptr.int(), "last_page_len": last.int(), "kv_indices": kv_indices,
+            "qo_indptr": qo_indptr.int(), "slot_map": slot, "positions": pos.int(), "counts": counts.int()}
+
+
+def _pow2(e):
+    """2^e in 32 bits, exactly, for whole e in [-126, 127] (below: 2^-126)."""
+    return ((e.int().clamp(-126, 127) + 127) << 23).view(torch.float32)
+
+
+def _take(codes, at):
+    """codes[at] of an e4m3 array, as 32-bit values (indexed as bytes)."""
+    return codes.view(torch.uint8)[at].view(torch.float8_e4m3fn).float()
+
+
+def _put(codes, at, values):
+    """codes[at] = values rounded to e4m3 (ties to even)."""
+    codes.view(torch.uint8)[at] = values.to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _plain_append_one(x, slots, codes, exps, ps):
+    """Quantises x [n, heads, D] into codes / exps in place, page by page."""
+    n, hk, _ = x.shape
+    x = x.float()
+    page = slots // ps
+    lead = torch.ones(n, dtype=torch.bool, device=x.device)
+    lead[1:] = page[1:] != page[:-1]
+    run = torch.cumsum(lead, 0) - 1
+    amax_t = x.abs().amax(dim=2)
+    amax = torch.zeros((n, hk), device=x.device).scatter_reduce(0, run[:, None].expand(n, hk), amax_t, "amax")
+    # least e with amax <= 448 * 2^e: amax = m * 2^x with m in [0.5, 1), 448 = 0.875 * 2^9
+    m, ex = torch.frexp(amax)
+    need = torch.where(m <= 0.875, ex - 9, ex - 8)
+    need = torch.where(amax > 0, need, -117).clamp(-117, 119).to(torch.int32)
+    at = torch.nonzero(lead).squeeze(1)  # first token of each run
+    need, pages, off = need[: at.numel()], page[at], slots[at] % ps
+    had = exps[pages].int()
+    e = torch.where((off > 0)[:, None], torch.maximum(need, had), need)
+    # codes that were there before, of pages whose exponent rose
+    part = torch.nonzero(off > 0).squeeze(1)
+    if part.numel():
+        before = _take(codes, pages[part])
+        old = before * _pow2((had - e)[part])[:, None, :, None]
+        keep = torch.arange(ps, device=x.device)[None, :, None, None] < off[part][:, None, None, None]
+        _put(codes, pages[part], torch.where(keep, old, before))
+    exps[pages] = e.to(torch.int8)
+    y = (x * _pow2(-e[run])[:, :, None]).clamp(-448.0, 448.0)
+    _put(codes.view(-1, hk, D), slots, y)
+
+
+def _plain_append(s):
+    ps = s["case"]["ps"]
+    _plain_append_one(s["k"], s["slots"], s["k8"], s["k_exp"], ps)
+    _plain_append_one(s["v"], s["slots"], s["v8"], s["v_exp"], ps)
+    return {"k8": s["k8"], "v8": s["v8"], "k_exp": s["k_exp"], "v_exp": s["v_exp"]}
+
+
+def _plain_attention(s):
+    """Padded to the longest request: pages gathered and dequantised in 32 bits, scores, mask, softmax, product."""
+    c = s["case"]
+    ps, hq, hk = c["ps"], c["hq"], c["hk"]
+    g, dev = hq // hk, s["q"].device
+    kvp = torch.from_numpy(s["kv_indptr"]).to(dev)
+    qop = torch.from_numpy(s["qo_indptr"]).to(dev)
+    last = torch.from_numpy(s["last"]).to(dev)
+    np_ = kvp[1:] - kvp[:-1]
+    kv_len = torch.where(np_ > 0, (np_ - 1) * ps + last, 0)
+    nq = qop[1:] - qop[:-1]
+    B, P, Q = nq.numel(), int(np.diff(s["kv_indptr"]).max()), int(np.diff(s["qo_indptr"]).max())
+    T = P * ps
+    # padded queries [B, heads, g * Q, D]
+    i = torch.arange(Q, device=dev)
+    row = (qop[:-1, None] + i[None, :]).clamp(max=s["q"].shape[0] - 1)
+    live = i[None, :] < nq[:, None]
+    q = s["q"][row].float().view(B, Q, hk, g, D).permute(0, 2, 3, 1, 4).reshape(B, hk, g * Q, D)
+    # padded keys and values [B, heads, T, D]
+    j = torch.arange(P, device=dev)
+    pages = s["kv_indices"].long()[(kvp[:-1, None] + j[None, :]).clamp(max=s["kv_indices"].numel() - 1)]
+    k = _take(s["k8"], pages) * _pow2(s["k_exp"][pages])[:, :, None, :, None]
+    k = k.reshape(B, T, hk, D).permute(0, 2, 3, 1)
+    x = torch.matmul(q, k).view(B, hk, g, Q, T)
+    del k
+    x = x * s["scale"]
+    if c["cap"] > 0:
+        x = torch.tanh(x / c["cap"]) * c["cap"]
+    t = torch.arange(T, device=dev)
+    pos = (kv_len - nq)[:, None] + i[None, :]  # a query's own position
+    see = (t[None, None, :] <= pos[:, :, None]) & (t[None, None, :] < kv_len[:, None, None])
+    if c["window"] > 0:
+        see = see & (t[None, None, :] >= pos[:, :, None] - c["window"])
+    x.masked_fill_(~see[:, None, None], -math.inf)
+    m = x.amax(dim=-1, keepdim=True)
+    m = torch.where(torch.isinf(m), 0.0, m)
+    x = torch.exp(x.sub_(m))
+    l = x.sum(dim=-1, keepdim=True)
+    v = _take(s["v8"], pages) * _pow2(s["v_exp"][pages])[:, :, None, :, None]
+    seen = t[None, :] < kv_len[:, None]
+    v = torch.where(seen[:, None, :, None], v.reshape(B, T, hk, D).permute(0, 2, 1, 3), 0.0)
+    o = torch.matmul(x.view(B, hk, g * Q, T), v).view(B, hk, g, Q, D) / l
+    lse = (m + torch.log(l)).squeeze(-1)
+    o = o.permute(0, 3, 1, 2, 4).reshape(B, Q, hq, D)[live]
+    lse = lse.permute(0, 3, 1, 2).reshape(B, Q, hq)[live]
+    return {"o": o.to(torch.bfloat16), "lse": lse}
+
+
+# ---------------------------------------------------------------- one pass
+def run(state):
+    s = state
+    op = s["case"]["op"]
+    if own:
+        import block_sparse_paged_gb300 as bsp
+        if op == "tables":
+            t = bsp.build_page_tables(s["cached"], s["new"], s["free"], s["num_free"], s["table"], s["case"]["ps"],
+                                      s["cap_pages"], s["cap_tokens"])
+            return {"block_table": s["table"], "kv_indptr": t.kv_indptr, "last_page_len": t.last_page_len,
+                    "kv_indices": t.kv_indices, "qo_indptr": t.qo_indptr, "slot_map": t.slot_map,
+                    "positions": t.positions, "counts": t.counts}
+        if op == "append":
+            bsp.append_kv(s["k"], s["v"], s["slots"], s["k8"], s["v8"], s["k_exp"], s["v_exp"])
+            return {"k8": s["k8"], "v8": s["v8"], "k_exp": s["k_exp"], "v_exp": s["v_exp"]}
+        o, lse = s["attention"].run(s["q"], s["k8"], s["v8"], s["kv_indices"], s["scale"], k_exp=s["k_exp"],
+                                    v_exp=s["v_exp"])
+        return {"o": o, "lse": lse}
+    if op == "tables":
+        return _plain_tables(s)
+    if op == "append":
+        return _plain_append(s)
+    return _plain_attention(s)
+
+
+# ---------------------------------------------------------------- 64 bits
+def _two_to(e):
+    """2^e in 64 bits from its bits, for whole e in [-1022, 1023]."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def _e4m3_64(y):
+    """Nearest e4m3 value (ties to even) of float64 y with |y| <= 448: three bits after the leading one, spacing at
+    least 2^-9."""
+    _, ex = torch.frexp(y.abs())  # |y| = m 2^ex, m in [0.5, 1)
+    step = _two_to((ex - 4).clamp(min=-9))
+    return torch.round(y / step) * step  # torch.round: half to even
+
+
+def _exact_append_one(x, slots, codes, exps, ps):
+    """One page after the other, in 64 bits; returns the pool's codes as values."""
+    x, pool = x.double(), codes.double()
+    sl = slots.cpu().numpy()
+    page = sl // ps
+    cut = np.flatnonzero(np.concatenate([[True], page[1:] != page[:-1], [True]]))
+    amax = x.abs().amax(dim=2).cpu().numpy()
+    had = exps.cpu().numpy().astype(np.int64)
+    lead, end = cut[:-1], cut[1:]
+    e_run = np.empty((len(lead), x.shape[1]), np.int64)
+    for r in range(len(lead)):
+        a = amax[lead[r]:end[r]].max(axis=0)
+        with np.errstate(divide="ignore"):
+            need = np.where(a > 0, np.ceil(np.log2(np.where(a > 0, a, 1.0) / 448.0)), -117.0).astype(np.int64)
+        need = np.where(a > 448.0 * np.exp2(need.astype(np.float64)), need + 1, need)
+        need = np.where(a <= 448.0 * np.exp2(need - 1.0), need - 1, need)
+        need = np.clip(need, -117, 119)
+        p, off = int(page[lead[r]]), int(sl[lead[r]] % ps)
+        e = np.maximum(need, had[p]) if off else need
+        if off and (e > had[p]).any():
+            f = _two_to(torch.from_numpy(had[p] - e).to(pool.device))
+            pool[p, :off] = _e4m3_64(pool[p, :off] * f[None, :, None])
+        e_run[r] = e
+    e_tok = torch.from_numpy(np.repeat(e_run, end - lead, axis=0)).to(x.device)
+    y = (x * _two_to(-e_tok)[:, :, None]).clamp(-448.0, 448.0)
+    pool.view(-1, x.shape[1], D)[slots] = _e4m3_64(y)
+    return pool
+
+
+def _exact_attention(s):
+    """Request by request and kv head by kv head, in 64 bits, each query against the keys that it sees."""
+    c = s["case"]
+    ps, hq, hk = c["ps"], c["hq"], c["hk"]
+    g = hq // hk
+    n = s["q"].shape[0]
+    o = torch.zeros((n, hq, D), dtype=torch.float64, device="cuda")
+    lse = torch.zeros((n, hq), dtype=torch.float64, device="cuda")
+    for b in range(c["batch"]):
+        p0, p1 = int(s["kv_indptr"][b]), int(s["kv_indptr"][b + 1])
+        q0, q1 = int(s["qo_indptr"][b]), int(s["qo_indptr"][b + 1])
+        L, N = (p1 - p0 - 1) * ps + int(s["last"][b]), q1 - q0
+        ids = s["kv_indices"][p0:p1].long()
+        k8, v8 = (s[x].view(torch.uint8)[ids].view(torch.float8_e4m3fn).double() for x in ("k8", "v8"))
+        key = torch.arange(L, device="cuda")
+        own_pos = torch.arange(L - N, L, device="cuda")
+        gone = key[None, :] > own_pos[:, None]
+        if c["window"] > 0:
+            gone |= key[None, :] + c["window"] < own_pos[:, None]
+        for h in range(hk):
+            k = (k8[:, :, h] * _two_to(s["k_exp"][ids, h])[:, None, None]).reshape(-1, D)[:L]
+            v = (v8[:, :, h] * _two_to(s["v_exp"][ids, h])[:, None, None]).reshape(-1, D)[:L]
+            for r in range(g * h, g * h + g):
+                z = (s["q"][q0:q1, r].double() @ k.T) * s["scale"]
+                if c["cap"] > 0:
+                    z = c["cap"] * torch.tanh(z / c["cap"])
+                z[gone] = -math.inf
+                lse[q0:q1, r] = torch.logsumexp(z, dim=1)
+                o[q0:q1, r] = torch.exp(z - lse[q0:q1, r][:, None]) @ v
+    return {"o": o, "lse": lse}
+
+
+def exact(case, seed):
+    global own
+    if case["op"] == "tables":
+        return None  # whole numbers
+    keep, own = own, False
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = keep
+    if case["op"] == "append":
+        return {"k8": _exact_append_one(s["k"], s["slots"], s["k8"], s["k_exp"], case["ps"]),
+                "v8": _exact_append_one(s["v"], s["slots"], s["v8"], s["v_exp"], case["ps"]),
+                "k_exp": None, "v_exp": None}
+    return _exact_attention(s)
+
+
+if __name__ == "__main__":
+    r = random.Random(1)
+    for case_ in listed() + [draw(r) for _ in range(6)]:
+        print(case_, work(case_))
