@@ -188,6 +188,9 @@ def prepare(case, seed):
         num_free = torch.tensor([free.numel()], dtype=torch.int32, device="cuda")
         s = dict(case=case, cached=_i32(cached), new=_i32(new), table=table, free=free, num_free=num_free,
                  cap_pages=need + case["pad"], cap_tokens=int(new.sum()) + case["pad"])
+        if own:  # the buffers that a serving loop keeps from step to step
+            import block_sparse_paged_gb300 as bsp
+            s["out"] = bsp.PageTables.empty(B, s["cap_pages"], s["cap_tokens"])
         return s
     hk = case["hk"]
     num_pages = int(total.sum()) + 5
@@ -368,7 +371,7 @@ def run(state):
         import block_sparse_paged_gb300 as bsp
         if op == "tables":
             t = bsp.build_page_tables(s["cached"], s["new"], s["free"], s["num_free"], s["table"], s["case"]["ps"],
-                                      s["cap_pages"], s["cap_tokens"])
+                                      s["cap_pages"], s["cap_tokens"], out=s["out"])
             return {"block_table": s["table"], "kv_indptr": t.kv_indptr, "last_page_len": t.last_page_len,
                     "kv_indices": t.kv_indices, "qo_indptr": t.qo_indptr, "slot_map": t.slot_map,
                     "positions": t.positions, "counts": t.counts}
