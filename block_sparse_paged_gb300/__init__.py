@@ -7,11 +7,13 @@ library is loaded on first use (so that ``block_sparse_paged_gb300.build`` can
 rebuild it first); every entry point raises if it has not been built.
 """
 from . import _native
-from ._native import (BSP_DTYPE_BF16, BSP_DTYPE_F32, BSP_MODE_DECODE, BSP_MODE_PREFILL, BspError, Capacity,
-                      PlanInfo, Problem)
-from .api import PagedAttention, default_num_ctas, make_problem, merge_state, plan_host, read_plan
+from ._native import (BSP_DTYPE_BF16, BSP_DTYPE_F32, BSP_MODE_DECODE, BSP_MODE_PREFILL, BSP_TABLES_BAD_LENGTH,
+                      BSP_TABLES_OUT_OF_PAGES, BSP_TABLES_OVER_CAPACITY, BspError, Capacity, PlanInfo, Problem)
+from .api import (PagedAttention, PageTables, append_kv, build_page_tables, default_num_ctas, make_problem,
+                  merge_state, plan_host, read_plan)
 
 
-__all__ = ["PagedAttention", "merge_state", "plan_host", "read_plan", "default_num_ctas", "make_problem",
-           "Problem", "Capacity", "PlanInfo", "BspError", "BSP_DTYPE_BF16", "BSP_DTYPE_F32",
-           "BSP_MODE_DECODE", "BSP_MODE_PREFILL"]
+__all__ = ["PagedAttention", "PageTables", "build_page_tables", "append_kv", "merge_state", "plan_host", "read_plan",
+           "default_num_ctas", "make_problem", "Problem", "Capacity", "PlanInfo", "BspError", "BSP_DTYPE_BF16",
+           "BSP_DTYPE_F32", "BSP_MODE_DECODE", "BSP_MODE_PREFILL", "BSP_TABLES_BAD_LENGTH",
+           "BSP_TABLES_OUT_OF_PAGES", "BSP_TABLES_OVER_CAPACITY"]

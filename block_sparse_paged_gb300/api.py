@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -279,3 +280,105 @@ def merge_state(o_a: torch.Tensor, lse_a: torch.Tensor, o_b: torch.Tensor, lse_b
                                     _dev(lse_out, "lse_out", torch.float32), n, H, D, _DTYPES[dt],
                                     _stream_handle(stream)))
     return out, lse_out
+
+
+def _call(dev: torch.device, stream, fn, *args):
+    """fn(*args, stream handle) with `dev` current, on `stream` or dev's current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            N.check(fn(*args, _stream_handle(stream)))
+    else:
+        N.check(fn(*args, _stream_handle(stream)))
+
+
+class PageTables(NamedTuple):
+    """What build_page_tables writes (int32 but slot_map, int64), for B requests:
+    kv_indptr [B + 1], last_page_len [B], kv_indices [max_table_pages], qo_indptr
+    [B + 1], slot_map [max_new_tokens], positions [max_new_tokens], counts [4]:
+    table pages, new tokens, pages taken, error bits (BSP_TABLES_*)."""
+    kv_indptr: torch.Tensor
+    last_page_len: torch.Tensor
+    kv_indices: torch.Tensor
+    qo_indptr: torch.Tensor
+    slot_map: torch.Tensor
+    positions: torch.Tensor
+    counts: torch.Tensor
+
+    @classmethod
+    def empty(cls, batch: int, max_table_pages: int, max_new_tokens: int, device=None) -> "PageTables":
+        """Buffers for `batch` requests, to be passed as `out` every step."""
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        sizes = (batch + 1, batch, max_table_pages, batch + 1, max_new_tokens, max_new_tokens, 4)
+        return cls(*(torch.empty(n, dtype=torch.int64 if f == "slot_map" else torch.int32, device=dev)
+                     for f, n in zip(cls._fields, sizes)))
+
+
+def build_page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+                      num_free: torch.Tensor, block_table: torch.Tensor, page_size: int, max_table_pages: int,
+                      max_new_tokens: int, out: PageTables | None = None, stream=None) -> PageTables:
+    """Page table (CSR), slots and positions of one step from the request lengths
+    on the device (bsp_build_page_tables).
+
+    cached_lens, new_lens: int32 [B], tokens in the cache and tokens added by this
+    step. block_table: int32 [B, width], rows of adjacent entries; the rows' pages
+    for the cached tokens are read, the pages that the new tokens need are taken
+    from free_pages (int32, the first num_free [1] of them) and written.
+    max_table_pages / max_new_tokens: sizes of kv_indices and of slot_map and
+    positions, whose tails are filled with 0, -1 and 0. Nothing is read back: whether
+    all fitted stands in counts[3]."""
+    if block_table.dim() != 2 or (block_table.numel() and block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [B, width] with adjacent entries in a row")
+    B, width = block_table.shape
+    dev = block_table.device
+    if not block_table.is_cuda or block_table.dtype != torch.int32:
+        raise ValueError("block_table must be a CUDA tensor of torch.int32")
+    if cached_lens.shape != (B,) or new_lens.shape != (B,):
+        raise ValueError(f"cached_lens and new_lens must be [{B}]")
+    if free_pages.dim() != 1 or num_free.numel() != 1:
+        raise ValueError("free_pages must be one-dimensional and num_free hold one value")
+    if out is None:
+        out = PageTables.empty(B, max_table_pages, max_new_tokens, dev)
+    sizes = (B + 1, B, max_table_pages, B + 1, max_new_tokens, max_new_tokens, 4)
+    for t, n, f in zip(out, sizes, PageTables._fields):
+        if t.shape != (n,):
+            raise ValueError(f"out.{f} must be [{n}]")
+    i32 = torch.int32
+    o = [_dev(t, f, torch.int64 if f == "slot_map" else i32, dev) for t, f in zip(out, PageTables._fields)]
+    stride = block_table.stride(0) if B > 1 else max(width, block_table.stride(0))
+    _call(dev, stream, N.load().bsp_build_page_tables, B, page_size, _dev(cached_lens, "cached_lens", i32, dev),
+          _dev(new_lens, "new_lens", i32, dev), _dev(free_pages, "free_pages", i32, dev), free_pages.numel(),
+          _dev(num_free, "num_free", i32, dev), block_table.data_ptr(), stride, width, o[0], o[1], o[2],
+          max_table_pages, o[3], o[4], o[5], max_new_tokens, o[6])
+    return out
+
+
+def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              k_exp: torch.Tensor, v_exp: torch.Tensor, stream=None) -> None:
+    """Quantise new keys and values into the e4m3 cache, in place (bsp_append_kv_fp8).
+
+    k, v: [n, H_kv, 128] bfloat16 or float32, slices of larger tensors allowed (the
+    values of a row adjacent, 16-byte aligned rows). slot_map: int64 [n], page *
+    page_size + place, as build_page_tables gives it; tokens with a slot outside the
+    pool are skipped. k_pages, v_pages: float8_e4m3fn [num_pages, page_size, H_kv,
+    128]; k_exp, v_exp: int8 [num_pages, H_kv], value = code * 2^exp."""
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages / v_pages must be [num_pages, page_size, H_kv, D]")
+    P, ps, H, D = k_pages.shape
+    n = k.shape[0]
+    if k.shape != (n, H, D) or v.shape != k.shape or v.dtype != k.dtype or k.dtype not in _DTYPES:
+        raise ValueError(f"k and v must be [n, {H}, {D}] in bfloat16 or float32, of one type")
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("the values of a row of k and v must be adjacent")
+    if slot_map.shape != (n,):
+        raise ValueError(f"slot_map must be [{n}]")
+    if k_exp.shape != (P, H) or v_exp.shape != (P, H):
+        raise ValueError(f"k_exp / v_exp must be [{P}, {H}]")
+    dev = k_pages.device
+    if not k.is_cuda or not v.is_cuda or k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must be CUDA tensors on {dev}")
+    f8, i8 = torch.float8_e4m3fn, torch.int8
+    # a dimension of size 1 is never stepped over: its stride says nothing
+    st = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in (0, 1)]
+    _call(dev, stream, N.load().bsp_append_kv_fp8, k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], st[3],
+          _DTYPES[k.dtype], n, _dev(slot_map, "slot_map", torch.int64, dev), _dev(k_pages, "k_pages", f8, dev),
+          _dev(v_pages, "v_pages", f8, dev), _dev(k_exp, "k_exp", i8, dev), _dev(v_exp, "v_exp", i8, dev), P, ps, H, D)

@@ -1,5 +1,6 @@
 // C-ABI entry points of libbsp.so other than the planner: argument checks,
 // launch of the run kernels, merge_state, error reporting.
+#include <climits>
 #include <cstring>
 #include <string>
 
@@ -156,6 +157,63 @@ extern "C" int bsp_merge_state(const void *o_a, const float *lse_a, const void *
     if (n_rows > 0 && (!o_a || !lse_a || !o_b || !lse_b || !o_out || !lse_out))
         return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
     return launch_merge_state(o_a, lse_a, o_b, lse_b, o_out, lse_out, n_rows, num_heads, head_dim, dtype, stream);
+}
+
+extern "C" int bsp_build_page_tables(int32_t batch, int32_t page_size, const int32_t *cached_lens,
+                                     const int32_t *new_lens, const int32_t *free_pages, int64_t free_capacity,
+                                     const int32_t *num_free, int32_t *block_table, int64_t block_table_stride,
+                                     int32_t max_pages_per_request, int32_t *kv_indptr, int32_t *last_page_len,
+                                     int32_t *kv_indices, int64_t max_table_pages, int32_t *qo_indptr,
+                                     int64_t *slot_map, int32_t *positions, int64_t max_new_tokens, int32_t *counts,
+                                     bsp_stream_t stream) {
+    clear_error();
+    if (batch < 0 || page_size < 1) return fail(BSP_ERR_INVALID_ARG, "batch must be >= 0 and page_size >= 1");
+    if (free_capacity < 0 || max_table_pages < 0 || max_new_tokens < 0 || max_pages_per_request < 0)
+        return fail(BSP_ERR_INVALID_ARG, "a capacity is negative");
+    if (free_capacity > INT32_MAX || max_table_pages > INT32_MAX || max_new_tokens > INT32_MAX)
+        return fail(BSP_ERR_INVALID_ARG, "a capacity exceeds 2^31 - 1");
+    if (block_table_stride < max_pages_per_request)
+        return fail(BSP_ERR_INVALID_ARG, "block_table_stride is below max_pages_per_request");
+    if (!kv_indptr || !qo_indptr || !counts || !num_free) return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    if (batch > 0 && (!cached_lens || !new_lens || !last_page_len || (max_pages_per_request > 0 && !block_table)))
+        return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    if ((free_capacity > 0 && !free_pages) || (max_table_pages > 0 && !kv_indices) ||
+        (max_new_tokens > 0 && (!slot_map || !positions)))
+        return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    if (reinterpret_cast<uintptr_t>(kv_indices) % 16 || reinterpret_cast<uintptr_t>(slot_map) % 16 ||
+        reinterpret_cast<uintptr_t>(positions) % 16)
+        return fail(BSP_ERR_INVALID_ARG, "kv_indices, slot_map and positions must be 16-byte aligned");
+    return launch_page_tables(batch, page_size, cached_lens, new_lens, free_pages, free_capacity, num_free, block_table,
+                              block_table_stride, max_pages_per_request, kv_indptr, last_page_len, kv_indices,
+                              max_table_pages, qo_indptr, slot_map, positions, max_new_tokens, counts, stream);
+}
+
+extern "C" int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int64_t k_head_stride,
+                                 int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t n_tokens,
+                                 const int64_t *slot_map, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
+                                 int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                                 bsp_stream_t stream) {
+    clear_error();
+    if (dtype != BSP_DTYPE_BF16 && dtype != BSP_DTYPE_F32) return fail(BSP_ERR_INVALID_ARG, "bad dtype");
+    if (head_dim != 128) return fail(BSP_ERR_UNSUPPORTED, "the e4m3 cache has head_dim 128");
+    if (n_tokens < 0 || num_pages < 1 || num_pages > INT32_MAX || page_size < 1 || num_kv_heads < 1)
+        return fail(BSP_ERR_INVALID_ARG, "bad append sizes");
+    if (num_kv_heads > 32767 || n_tokens > (int64_t{1} << 37))
+        return fail(BSP_ERR_UNSUPPORTED, "append takes at most 32767 kv heads and 2^37 tokens");
+    if (n_tokens == 0) return BSP_OK;
+    if (!k || !v || !slot_map || !k_pages || !v_pages || !k_exp || !v_exp)
+        return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    const int64_t elem = dtype == BSP_DTYPE_F32 ? 4 : 2;
+    const int64_t st[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+    for (int i = 0; i < 4; ++i)
+        if (st[i] % (16 / elem) != 0)
+            return fail(BSP_ERR_INVALID_ARG, "the strides of k and v must be multiples of 16 bytes");
+    const void *ptr[4] = {k, v, k_pages, v_pages};
+    for (int i = 0; i < 4; ++i)
+        if (reinterpret_cast<uintptr_t>(ptr[i]) % 16 != 0)
+            return fail(BSP_ERR_INVALID_ARG, "k, v and the page pools must be 16-byte aligned");
+    return launch_append_kv(k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride, dtype, n_tokens,
+                            slot_map, k_pages, v_pages, k_exp, v_exp, num_pages, page_size, num_kv_heads, stream);
 }
 
 extern "C" int bsp_check_device_error(const bsp_plan_info *plan, void *workspace, bsp_stream_t stream,

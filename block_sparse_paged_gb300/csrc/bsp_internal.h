@@ -94,5 +94,17 @@ int launch_merge_state(const void *o_a, const float *lse_a, const void *o_b, con
                        void *o_out, float *lse_out, int64_t n_rows, int32_t num_heads,
                        int32_t head_dim, int32_t dtype, cudaStream_t stream);
 int decode_ctas_per_sm(int head_dim, int dtype);
+// Page tables, slots and positions from request lengths (arguments as in bsp_build_page_tables, checked).
+int launch_page_tables(int32_t batch, int32_t page_size, const int32_t *cached_lens, const int32_t *new_lens,
+                       const int32_t *free_pages, int64_t free_capacity, const int32_t *num_free, int32_t *block_table,
+                       int64_t block_table_stride, int32_t max_pages_per_request, int32_t *kv_indptr,
+                       int32_t *last_page_len, int32_t *kv_indices, int64_t cap_pages, int32_t *qo_indptr,
+                       int64_t *slot_map, int32_t *positions, int64_t cap_tokens, int32_t *counts,
+                       cudaStream_t stream);
+// Quantising append into the e4m3 cache (arguments as in bsp_append_kv_fp8, checked; n_tokens > 0).
+int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64_t k_head_stride,
+                     int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t n_tokens,
+                     const int64_t *slot_map, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
+                     int64_t num_pages, int32_t page_size, int32_t num_kv_heads, cudaStream_t stream);
 
 }  // namespace bsp

@@ -72,15 +72,6 @@ constexpr long long kWaitLimitCycles = 4000000000ll;  // about 2 s at 2 GHz: a f
 // reduction-map entries a CTA completes and folds after its queue (more are folded at once)
 constexpr int kMaxPendingFolds = 32;
 
-// Four e4m3 values (the bytes of x, lowest first) to two f16x2: lo = bytes 0
-// and 1, hi = bytes 2 and 3, the lower byte in the lower half. Exact: every
-// e4m3 value is an f16 value.
-__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t &lo, uint32_t &hi) {
-    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-        : "=r"(lo), "=r"(hi)
-        : "r"(x));
-}
-
 // Transpose of an 8 x 8 matrix of 16-bit values held as one register per lane
 // (lane l: row l / 4, columns 2 (l % 4) and 2 (l % 4) + 1).
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {

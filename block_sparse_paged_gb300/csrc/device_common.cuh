@@ -97,6 +97,15 @@ __device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
     return r;
 }
 
+// Four e4m3 values (the bytes of x, lowest first) to two f16x2: lo = bytes 0
+// and 1, hi = bytes 2 and 3, the lower byte in the lower half. Exact: every
+// e4m3 value is an f16 value.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 

@@ -1,0 +1,587 @@
+// The paged KV cache beside the attention that reads it: the page table and the
+// slots of a step's new tokens from request lengths, and the append that
+// quantises new keys and values into an e4m3 cache with one power-of-two
+// exponent per (page, kv head).
+#include <algorithm>
+#include <climits>
+
+#include <cuda_fp16.h>
+
+#include "bsp_internal.h"
+#include "device_common.cuh"
+
+namespace bsp {
+namespace {
+
+// ---------------------------------------------------------------- page tables
+// For request b with c cached and m new tokens: old = ceil(c / ps) entries of its
+// table row hold pages, all = ceil((c + m) / ps) shall; the all - old missing ones
+// come from the free list, requests in order. Three exclusive sums over the
+// requests (pages, free pages taken, new tokens) place everything.
+//
+// Every CTA computes the sums of all requests for itself, in shared memory, and
+// then expands its share of the entries and tokens: one launch, no pass over
+// global memory between the sums and their use, no atomics. The lengths are at
+// most 128 KB, read from L2.
+constexpr int kTabThreads = 256;
+constexpr int kTabUnit = 4;  // consecutive entries (tokens) per thread: one search, vector stores
+constexpr int kTabMaxBatch = 16384;
+
+struct TableParams {
+    const int32_t *cached, *fresh;
+    const int32_t *free_pages, *num_free;
+    long long free_capacity;
+    int32_t *table;
+    long long table_stride;
+    int width, batch, ps;
+    int32_t *kv_indptr, *last_page_len, *kv_indices, *qo_indptr, *positions, *counts;
+    long long *slots;
+    long long cap_pages, cap_tokens;
+};
+
+// Lengths of one request: negative ones read as 0, pages clipped to the row.
+struct TableRow {
+    int cached, fresh, old_pages, all_pages;
+    int flags;
+};
+__device__ __forceinline__ TableRow table_row(const TableParams &p, int b) {
+    TableRow r;
+    const int c = __ldg(p.cached + b), m = __ldg(p.fresh + b);
+    r.flags = (c < 0 || m < 0) ? BSP_TABLES_BAD_LENGTH : 0;
+    r.cached = max(c, 0);
+    r.fresh = max(m, 0);
+    const long long total = (long long)r.cached + r.fresh;
+    const long long all = (total + p.ps - 1) / p.ps;
+    if (all > p.width) r.flags |= BSP_TABLES_OVER_CAPACITY;
+    r.all_pages = (int)min(all, (long long)p.width);
+    r.old_pages = min((int)(((long long)r.cached + p.ps - 1) / p.ps), r.all_pages);
+    return r;
+}
+
+// Largest b with start[b] <= x, for x in [0, start[n]).
+__device__ __forceinline__ int find_row(const int *start, int n, int x) {
+    int lo = 0, hi = n;  // start[lo] <= x < start[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TableParams p) {
+    extern __shared__ int sm[];
+    const int B = p.batch;
+    int *s_pages = sm, *s_take = sm + (B + 1), *s_tok = sm + 2 * (B + 1);
+    __shared__ long long s_part[3][kTabThreads / 32];
+    __shared__ int s_flags;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s_flags = 0;
+    __syncthreads();
+
+    // exclusive sums in 64 bits, kept saturated to int32 (an output that needs more
+    // is over its capacity anyway)
+    long long base[3] = {0, 0, 0};
+    for (int b0 = 0; b0 < B; b0 += kTabThreads) {
+        const int b = b0 + tid;
+        long long v[3] = {0, 0, 0};
+        if (b < B) {
+            const TableRow r = table_row(p, b);
+            v[0] = r.all_pages;
+            v[1] = r.all_pages - r.old_pages;
+            v[2] = r.fresh;
+            if (r.flags) atomicOr(&s_flags, r.flags);
+        }
+        long long inc[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            inc[j] = v[j];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, inc[j], o);
+                if (lane >= o) inc[j] += up;
+            }
+            if (lane == 31) s_part[j][warp] = inc[j];
+        }
+        __syncthreads();
+        long long sum[3] = {0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            long long before = base[j];
+#pragma unroll
+            for (int w = 0; w < kTabThreads / 32; ++w) {
+                before += w < warp ? s_part[j][w] : 0;
+                sum[j] += s_part[j][w];
+            }
+            if (b < B) sm[j * (B + 1) + b] = (int)min(before + inc[j] - v[j], (long long)INT32_MAX);
+            base[j] += sum[j];
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) sm[j * (B + 1) + B] = (int)min(base[j], (long long)INT32_MAX);
+    }
+    __syncthreads();
+    const int n_pages = s_pages[B], n_tok = s_tok[B];
+    const int n_free = (int)max(0ll, min((long long)__ldg(p.num_free), p.free_capacity));
+
+    if (blockIdx.x == 0) {
+        for (int b = tid; b <= B; b += kTabThreads) {
+            p.kv_indptr[b] = s_pages[b];
+            p.qo_indptr[b] = s_tok[b];
+            if (b < B) {
+                const TableRow r = table_row(p, b);
+                const long long total = min((long long)r.cached + r.fresh, (long long)r.all_pages * p.ps);
+                p.last_page_len[b] = r.all_pages > 0 ? (int)((total - 1) % p.ps) + 1 : 0;
+            }
+        }
+        if (tid == 0) {
+            int f = s_flags;
+            if (s_take[B] > n_free) f |= BSP_TABLES_OUT_OF_PAGES;
+            if (base[0] > p.cap_pages || base[2] > p.cap_tokens) f |= BSP_TABLES_OVER_CAPACITY;
+            p.counts[0] = n_pages;
+            p.counts[1] = n_tok;
+            p.counts[2] = min(s_take[B], n_free);
+            p.counts[3] = f;
+        }
+    }
+
+    // page of column i of request b: from the row, or from the free list (-1: none left)
+    auto page_of = [&](int b, int old_pages, int i) -> int {
+        if (i < old_pages) return p.table[(long long)b * p.table_stride + i];
+        const int k = s_take[b] + (i - old_pages);
+        return k < n_free ? __ldg(p.free_pages + k) : -1;
+    };
+
+    const long long gsize = (long long)gridDim.x * kTabThreads * kTabUnit;
+    const long long g0 = ((long long)blockIdx.x * kTabThreads + tid) * kTabUnit;
+    // table entries: CSR copy of every row, new entries also into the row; the CSR
+    // tail up to its capacity is 0
+    const long long n_ent = max((long long)n_pages, p.cap_pages);
+    for (long long e0 = g0; e0 < n_ent; e0 += gsize) {
+        int id[kTabUnit];
+        int b = 0, old_pages = 0, end = -1, begin = 0;
+#pragma unroll
+        for (int u = 0; u < kTabUnit; ++u) {
+            const long long e = e0 + u;
+            id[u] = 0;
+            if (e < n_pages) {
+                if ((int)e >= end) {
+                    b = end < 0 ? find_row(s_pages, B, (int)e) : b + 1;
+                    while (s_pages[b + 1] <= (int)e) ++b;  // rows without pages
+                    begin = s_pages[b];
+                    end = s_pages[b + 1];
+                    old_pages = table_row(p, b).old_pages;
+                }
+                const int i = (int)e - begin;
+                const int pg = page_of(b, old_pages, i);
+                if (i >= old_pages) p.table[(long long)b * p.table_stride + i] = pg;
+                id[u] = max(pg, 0);
+            }
+        }
+        if (e0 + kTabUnit <= p.cap_pages) {
+            *reinterpret_cast<int4 *>(p.kv_indices + e0) = make_int4(id[0], id[1], id[2], id[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kTabUnit; ++u)
+                if (e0 + u < p.cap_pages) p.kv_indices[e0 + u] = id[u];
+        }
+    }
+    // tokens: slot and position of every new token; the tail is -1 and 0
+    for (long long t0 = g0; t0 < p.cap_tokens; t0 += gsize) {
+        long long slot[kTabUnit];
+        int pos[kTabUnit];
+        int b = 0, end = -1, begin = 0;
+        int col = 0, off = 0;
+        TableRow r{};
+#pragma unroll
+        for (int u = 0; u < kTabUnit; ++u) {
+            const long long t = t0 + u;
+            slot[u] = -1;
+            pos[u] = 0;
+            if (t < n_tok) {
+                if ((int)t >= end) {
+                    b = end < 0 ? find_row(s_tok, B, (int)t) : b + 1;
+                    while (s_tok[b + 1] <= (int)t) ++b;  // requests without new tokens
+                    begin = s_tok[b];
+                    end = s_tok[b + 1];
+                    r = table_row(p, b);
+                    const long long x = (long long)r.cached + ((int)t - begin);
+                    col = (int)(x / p.ps);
+                    off = (int)(x - (long long)col * p.ps);
+                } else if (++off == p.ps) {
+                    off = 0;
+                    ++col;
+                }
+                pos[u] = (int)min((long long)r.cached + ((int)t - begin), (long long)INT32_MAX);
+                if (col < r.all_pages) {
+                    const int pg = page_of(b, r.old_pages, col);
+                    if (pg >= 0) slot[u] = (long long)pg * p.ps + off;
+                }
+            }
+        }
+        if (t0 + kTabUnit <= p.cap_tokens) {
+            *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            reinterpret_cast<longlong2 *>(p.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
+            reinterpret_cast<longlong2 *>(p.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kTabUnit; ++u)
+                if (t0 + u < p.cap_tokens) {
+                    p.slots[t0 + u] = slot[u];
+                    p.positions[t0 + u] = pos[u];
+                }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- append
+// A page's exponent for one kv head is the least e with amax <= 448 * 2^e over the
+// tokens that the page holds (448: the largest e4m3 value), within [kExpMin,
+// kExpMax], where every code * 2^e is a normal bf16 value. A power of two costs an
+// e4m3 code no precision against amax / 448, and moving stored codes to a larger
+// exponent only shifts them.
+//
+// One CTA per (window of 128 tokens, kv head, K or V); 8 warps hold 16 tokens
+// each in registers from the first read to the stored codes, so keys and values are
+// read once. The tokens of a page stand next to each other (a run): token maxima
+// meet in shared memory per run. A run that goes past the window is measured by
+// every CTA that holds a part of it (its outside tokens are read for their maximum
+// alone, from L2); all get the same exponent, and the CTA with the run's first
+// token writes it and rescales the codes that the page held before. A CTA that
+// reads the exponent after that write gets max(need, e) = e: the same.
+constexpr int kAppTokens = 128;
+constexpr int kAppWarps = 8;
+constexpr int kAppPerWarp = kAppTokens / kAppWarps;  // 16
+constexpr int kExpMin = -117, kExpMax = 119;
+constexpr int kCacheD = 128;
+
+struct AppendParams {
+    const char *x[2];             // new keys, values
+    long long tok_bytes[2], head_bytes[2];
+    uint8_t *codes[2];
+    int8_t *exps[2];
+    const long long *slots;
+    long long n, rows;             // tokens; slots of the pool
+    int ps, H;
+};
+
+// 2^e for e in [-149, 127]
+__device__ __forceinline__ float pow2i(int e) {
+    return __int_as_float(e >= -126 ? (e + 127) << 23 : 0x00400000 >> (-127 - e));
+}
+
+// Least e with amax <= 448 * 2^e for the bits of a finite amax >= 0, clamped.
+__device__ __forceinline__ int exponent_for(uint32_t amax_bits) {
+    // amax = 1.f * 2^(x - 127) for normal values; 448 = 1.75 * 2^8. Subnormal maxima
+    // have x = 0 and clamp to kExpMin like every value below 448 * 2^kExpMin.
+    const int x = (int)(amax_bits >> 23);
+    const int e = x - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return max(kExpMin, min(kExpMax, e));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// One lane's 16-byte piece of a token row: 8 bf16 or 4 fp32 values.
+template <bool kF32>
+struct Piece {
+    static constexpr int kN = kF32 ? 4 : 8;
+    static constexpr int kLanes = kCacheD / kN;          // lanes per token row
+    static constexpr int kPer = 32 / kLanes;             // tokens per warp-wide load
+    static constexpr int kLoads = kAppPerWarp / kPer;    // loads of a warp's 16 tokens
+    __device__ static __forceinline__ void values(const uint4 &w, float (&f)[kN]) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (kF32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(u[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = dev::bf16_lo(u[i]);
+                f[2 * i + 1] = dev::bf16_hi(u[i]);
+            }
+        }
+    }
+    // largest finite |value| as bits
+    __device__ static __forceinline__ uint32_t amax(const uint4 &w) {
+        float f[kN];
+        values(w, f);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+        if (m >= 0x7f800000u) {  // an infinity or NaN among them
+            m = 0;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
+                if (a < 0x7f800000u) m = max(m, a);
+            }
+        }
+        return m;
+    }
+    // codes of the piece at scale 2^-e (kN bytes, lowest first). The format has no
+    // infinities: infinite values become NaN.
+    __device__ static __forceinline__ uint2 codes(const uint4 &w, float s) {
+        float f[kN];
+        values(w, f);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            f[i] = (__float_as_uint(f[i]) & 0x7fffffffu) == 0x7f800000u ? __int_as_float(0x7fffffff) : f[i] * s;
+        uint2 r;
+        r.x = e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
+        r.y = kF32 ? 0u : (e4m3x2(f[kN - 4], f[kN - 3]) | (e4m3x2(f[kN - 2], f[kN - 1]) << 16));
+        return r;
+    }
+};
+
+// Four stored codes times s (a power of two <= 1), rounded to nearest even.
+__device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float s) {
+    uint32_t h0, h1;
+    dev::e4m3x4_to_f16x4(w, h0, h1);
+    const __half2 a = *reinterpret_cast<__half2 *>(&h0), b = *reinterpret_cast<__half2 *>(&h1);
+    const float2 fa = __half22float2(a), fb = __half22float2(b);
+    return e4m3x2(fa.x * s, fa.y * s) | (e4m3x2(fb.x * s, fb.y * s) << 16);
+}
+
+template <bool kF32>
+__global__ void __launch_bounds__(32 * kAppWarps) append_kernel(const AppendParams p) {
+    using PC = Piece<kF32>;
+    __shared__ int s_page[kAppTokens];       // page of each token, or -1
+    __shared__ int s_off[kAppTokens];        // its place in the page
+    __shared__ uint32_t s_lead[kAppTokens / 32], s_grow[kAppTokens / 32];
+    __shared__ uint32_t s_max[kAppTokens];   // by the run's first token in the window
+    __shared__ float s_scale[kAppTokens];    // 2^-e of the run
+    __shared__ int s_drop[kAppTokens];       // old exponent - e, where it rose
+    __shared__ int s_left, s_right;          // tokens of the first / last run outside the window
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int which = blockIdx.y >= (unsigned)p.H ? 1 : 0;
+    const int h = blockIdx.y - which * p.H;
+    const long long T0 = (long long)blockIdx.x * kAppTokens;
+    const int nt = (int)min((long long)kAppTokens, p.n - T0);
+    const char *x = p.x[which] + h * p.head_bytes[which];
+    const long long tb = p.tok_bytes[which];
+    const int sub = lane / PC::kLanes, piece = lane % PC::kLanes;
+
+    // this warp's 16 tokens, all loads in flight together
+    uint4 w[PC::kLoads];
+#pragma unroll
+    for (int i = 0; i < PC::kLoads; ++i) {
+        const int t = warp * kAppPerWarp + i * PC::kPer + sub;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (t < nt) w[i] = __ldg(reinterpret_cast<const uint4 *>(x + (T0 + t) * tb) + piece);
+    }
+    auto slot_of = [&](long long t) -> long long {
+        const long long s = __ldg(p.slots + t);
+        return s >= 0 && s < p.rows ? s : -1;
+    };
+    if (tid < kAppTokens) {
+        const long long s = tid < nt ? slot_of(T0 + tid) : -1;
+        s_page[tid] = s >= 0 ? (int)(s / p.ps) : -1;
+        s_off[tid] = s >= 0 ? (int)(s % p.ps) : 0;
+        s_max[tid] = 0;
+    }
+    if (tid == 0) s_left = s_right = 0;
+    __syncthreads();
+    if (tid < kAppTokens) {
+        const int pg = s_page[tid];
+        const bool lead = pg >= 0 && (tid == 0 || s_page[tid - 1] != pg);
+        const uint32_t m = __ballot_sync(0xffffffffu, lead);
+        if (lane == 0) s_lead[warp] = m;
+    } else if (warp == kAppTokens / 32 || warp == kAppTokens / 32 + 1) {
+        // how far the first (last) run goes on before (behind) the window
+        const bool left = warp == kAppTokens / 32;
+        const int pg = left ? s_page[0] : s_page[nt - 1];
+        int got = 0;
+        if (pg >= 0) {
+            for (;;) {
+                const long long t = left ? T0 - 1 - got - lane : T0 + nt + got + lane;
+                bool same = false;
+                if (t >= 0 && t < p.n) {
+                    const long long s = slot_of(t);
+                    same = s >= 0 && (int)(s / p.ps) == pg;
+                }
+                const uint32_t m = __ballot_sync(0xffffffffu, same);
+                const int k = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+                got += k;
+                if (k < 32) break;
+            }
+        }
+        if (lane == 0) (left ? s_left : s_right) = got;
+    }
+    __syncthreads();
+    // first token of the run that token t (with a page) belongs to, within the window
+    auto run_of = [&](int t) -> int {
+        int k = t >> 5;
+        uint32_t m = s_lead[k] & (0xffffffffu >> (31 - (t & 31)));
+        while (m == 0) m = s_lead[--k];
+        return 32 * k + 31 - __clz(m);
+    };
+#pragma unroll
+    for (int i = 0; i < PC::kLoads; ++i) {
+        uint32_t m = PC::amax(w[i]);
+#pragma unroll
+        for (int o = PC::kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int t = warp * kAppPerWarp + i * PC::kPer + sub;
+        if (piece == 0 && s_page[t] >= 0) atomicMax(&s_max[run_of(t)], m);
+    }
+    if (s_left | s_right) {
+        const int outside = s_left + s_right;
+        for (int j = warp * PC::kPer; j < outside; j += kAppWarps * PC::kPer) {
+            const int jj = j + sub;
+            uint32_t m = 0;
+            if (jj < outside) {
+                const long long t = jj < s_left ? T0 - 1 - jj : T0 + nt + (jj - s_left);
+                m = PC::amax(__ldg(reinterpret_cast<const uint4 *>(x + t * tb) + piece));
+            }
+#pragma unroll
+            for (int o = PC::kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (piece == 0 && jj < outside) atomicMax(&s_max[jj < s_left ? 0 : run_of(nt - 1)], m);
+        }
+    }
+    __syncthreads();
+    if (tid < kAppTokens) {
+        bool grow = false;
+        if (s_lead[warp] >> lane & 1) {
+            const int need = exponent_for(s_max[tid]);
+            const bool mine = tid > 0 || s_left == 0;  // the run's first token is in this window
+            const int off = mine ? s_off[tid] : (int)(slot_of(T0 - s_left) % p.ps);
+            int8_t *ep = p.exps[which] + (long long)s_page[tid] * p.H + h;
+            const int had = off > 0 ? *reinterpret_cast<volatile int8_t *>(ep) : need;
+            const int e = max(need, had);
+            s_scale[tid] = pow2i(-e);
+            s_drop[tid] = had - e;
+            grow = mine && off > 0 && e > had;
+            if (mine) *ep = (int8_t)e;
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, grow);
+        if (lane == 0) s_grow[warp] = m;
+    }
+    __syncthreads();
+    uint8_t *codes = p.codes[which] + (long long)h * kCacheD;
+    const long long row_bytes = (long long)p.H * kCacheD;
+#pragma unroll
+    for (int i = 0; i < PC::kLoads; ++i) {
+        const int t = warp * kAppPerWarp + i * PC::kPer + sub;
+        const int pg = s_page[t];
+        if (pg >= 0) {
+            const uint2 c = PC::codes(w[i], s_scale[run_of(t)]);
+            uint8_t *dst = codes + ((long long)pg * p.ps + s_off[t]) * row_bytes + piece * PC::kN;
+            if constexpr (kF32) *reinterpret_cast<uint32_t *>(dst) = c.x;
+            else *reinterpret_cast<uint2 *>(dst) = c;
+        }
+    }
+    // codes that a page held before its exponent rose: rows 0 .. off - 1, one run per
+    // warp, four rows of 8 lanes x 16 bytes at a time
+    int turn = 0;
+    for (int k = 0; k < kAppTokens / 32; ++k) {
+        for (uint32_t m = s_grow[k]; m; m &= m - 1, ++turn) {
+            if (turn % kAppWarps != warp) continue;
+            const int t = 32 * k + __ffs(m) - 1;
+            const float s = pow2i(max(s_drop[t], -126));
+            uint8_t *page = codes + (long long)s_page[t] * p.ps * row_bytes;
+            for (int r = lane >> 3; r < s_off[t]; r += 4) {
+                uint4 *at = reinterpret_cast<uint4 *>(page + r * row_bytes) + (lane & 7);
+                uint4 c = *at;
+                c.x = rescale_codes(c.x, s);
+                c.y = rescale_codes(c.y, s);
+                c.z = rescale_codes(c.z, s);
+                c.w = rescale_codes(c.w, s);
+                *at = c;
+            }
+        }
+    }
+}
+
+int current_sms(int *dev_out) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+        return -1;
+    if (dev_out) *dev_out = dev;
+    return sms;
+}
+
+}  // namespace
+
+int launch_page_tables(int32_t batch, int32_t page_size, const int32_t *cached_lens, const int32_t *new_lens,
+                       const int32_t *free_pages, int64_t free_capacity, const int32_t *num_free, int32_t *block_table,
+                       int64_t block_table_stride, int32_t max_pages_per_request, int32_t *kv_indptr,
+                       int32_t *last_page_len, int32_t *kv_indices, int64_t cap_pages, int32_t *qo_indptr,
+                       int64_t *slot_map, int32_t *positions, int64_t cap_tokens, int32_t *counts,
+                       cudaStream_t stream) {
+    if (batch > kTabMaxBatch)
+        return fail(BSP_ERR_UNSUPPORTED, "build_page_tables takes at most " + std::to_string(kTabMaxBatch) + " requests");
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    TableParams p;
+    p.cached = cached_lens;
+    p.fresh = new_lens;
+    p.free_pages = free_pages;
+    p.num_free = num_free;
+    p.free_capacity = free_capacity;
+    p.table = block_table;
+    p.table_stride = block_table_stride;
+    p.width = max_pages_per_request;
+    p.batch = batch;
+    p.ps = page_size;
+    p.kv_indptr = kv_indptr;
+    p.last_page_len = last_page_len;
+    p.kv_indices = kv_indices;
+    p.qo_indptr = qo_indptr;
+    p.positions = positions;
+    p.counts = counts;
+    p.slots = reinterpret_cast<long long *>(slot_map);
+    p.cap_pages = cap_pages;
+    p.cap_tokens = cap_tokens;
+    const size_t smem = 3 * sizeof(int) * (size_t)(batch + 1);
+    static bool configured[64] = {false};
+    if (smem > 48 * 1024 && !configured[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(3 * sizeof(int) * (kTabMaxBatch + 1)));
+        if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("page tables smem attribute: ") + cudaGetErrorString(e));
+        configured[dev] = true;
+    }
+    const int64_t per = kTabThreads * kTabUnit, work = std::max<int64_t>(cap_pages, cap_tokens);
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((work + per - 1) / per, 4ll * sms));
+    page_tables_kernel<<<(unsigned)grid, kTabThreads, smem, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("page tables launch: ") + cudaGetErrorString(e));
+    return BSP_OK;
+}
+
+int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64_t k_head_stride,
+                     int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t n_tokens,
+                     const int64_t *slot_map, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
+                     int64_t num_pages, int32_t page_size, int32_t num_kv_heads, cudaStream_t stream) {
+    const int64_t elem = dtype == BSP_DTYPE_F32 ? 4 : 2;
+    AppendParams p;
+    p.x[0] = static_cast<const char *>(k);
+    p.x[1] = static_cast<const char *>(v);
+    p.tok_bytes[0] = k_token_stride * elem;
+    p.tok_bytes[1] = v_token_stride * elem;
+    p.head_bytes[0] = k_head_stride * elem;
+    p.head_bytes[1] = v_head_stride * elem;
+    p.codes[0] = static_cast<uint8_t *>(k_pages);
+    p.codes[1] = static_cast<uint8_t *>(v_pages);
+    p.exps[0] = k_exp;
+    p.exps[1] = v_exp;
+    p.slots = reinterpret_cast<const long long *>(slot_map);
+    p.n = n_tokens;
+    p.rows = (long long)num_pages * page_size;
+    p.ps = page_size;
+    p.H = num_kv_heads;
+    const dim3 grid((unsigned)((n_tokens + kAppTokens - 1) / kAppTokens), 2u * (unsigned)num_kv_heads);
+    if (dtype == BSP_DTYPE_F32) append_kernel<true><<<grid, 32 * kAppWarps, 0, stream>>>(p);
+    else append_kernel<false><<<grid, 32 * kAppWarps, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("append launch: ") + cudaGetErrorString(e));
+    return BSP_OK;
+}
+
+}  // namespace bsp

@@ -372,6 +372,93 @@ int bsp_merge_state(const void *o_a, const float *lse_a, const void *o_b, const 
                     int32_t head_dim, int32_t dtype, bsp_stream_t stream);
 
 /*
+ * ---- the 8-bit KV cache: tables, append, attention -------------------------
+ *
+ * One layer's cache (no counterpart on the pages, whose e4m3 cache is a
+ * configuration name): e4m3 codes k_pages, v_pages [num_pages, page_size, H_kv,
+ * 128] and one exponent per page and kv head, k_exp, v_exp int8 [num_pages,
+ * H_kv]. The value of a code is code * 2^exp. Exponents lie in [-117, 119]
+ * (bsp_append_kv_fp8 writes no others): code * 2^exp is then exactly a bf16
+ * value.
+ *
+ * The step of a serving loop, every call stream-ordered and capturable:
+ *   bsp_build_page_tables   lengths -> page table (CSR), slots, positions
+ *   bsp_append_kv_fp8       new keys and values -> cache, through the slots
+ *   bsp_decode_run_fp8_block / bsp_prefill_run_fp8_block   attention over it
+ */
+
+/* counts[3] of bsp_build_page_tables: bits */
+#define BSP_TABLES_OUT_OF_PAGES   1 /* the free list holds too few pages            */
+#define BSP_TABLES_OVER_CAPACITY  2 /* a row, kv_indices or slot_map is too small    */
+#define BSP_TABLES_BAD_LENGTH     4 /* a negative length (read as 0)                 */
+
+/*
+ * Page table, slots and positions of one step from the request lengths, all on
+ * the device (one launch, no atomics, the same result every time).
+ *   batch              requests, at most 16384; requests with 0 tokens are allowed
+ *   cached_lens        device, int32 [batch], tokens of each request in the cache
+ *   new_lens           device, int32 [batch], tokens that this step adds behind them
+ *   free_pages         device, int32 [free_capacity], page ids to take from, in order
+ *   num_free           device, int32 [1], how many of them are free (not changed:
+ *                      the caller drops the counts[2] pages taken)
+ *   block_table        device, int32 [batch, max_pages_per_request] with row stride
+ *                      block_table_stride: row b holds request b's pages. The first
+ *                      ceil(cached / page_size) entries are read; the further ones up
+ *                      to ceil((cached + new) / page_size) are taken from the free
+ *                      list, requests in order, and written; the rest is left alone
+ *   kv_indptr, last_page_len, qo_indptr
+ *                      device, int32 [batch + 1], [batch], [batch + 1], written: the
+ *                      metadata of a plan over the grown requests (bsp_plan takes
+ *                      host copies, which follow from the same lengths)
+ *   kv_indices         device, int32 [max_table_pages], written: all rows, CSR;
+ *                      entries behind the last page are 0
+ *   slot_map,
+ *   positions          device, int64 and int32 [max_new_tokens], written: for each new
+ *                      token, requests in order, its slot page * page_size + place and
+ *                      its position in the request; -1 and 0 behind the last token, so
+ *                      that a padded append skips them
+ *   counts             device, int32 [4], written: table pages, new tokens, pages
+ *                      taken, BSP_TABLES_* bits (0: everything fits)
+ * Where something does not fit, nothing is written out of bounds: missing pages
+ * are -1 in block_table, 0 in kv_indices, and their tokens' slots are -1; pages
+ * beyond a row are not part of kv_indptr. kv_indices, slot_map and positions are
+ * 16-byte aligned.
+ */
+int bsp_build_page_tables(int32_t batch, int32_t page_size, const int32_t *cached_lens, const int32_t *new_lens,
+                          const int32_t *free_pages, int64_t free_capacity, const int32_t *num_free,
+                          int32_t *block_table, int64_t block_table_stride, int32_t max_pages_per_request,
+                          int32_t *kv_indptr, int32_t *last_page_len, int32_t *kv_indices, int64_t max_table_pages,
+                          int32_t *qo_indptr, int64_t *slot_map, int32_t *positions, int64_t max_new_tokens,
+                          int32_t *counts, bsp_stream_t stream);
+
+/*
+ * Append: quantise new keys and values into the cache, in place.
+ *   k, v               device, [n_tokens, H_kv, 128] in `dtype` (BSP_DTYPE_BF16 or
+ *                      BSP_DTYPE_F32), element strides per token and head, the 128
+ *                      values of a row adjacent; 16-byte aligned, strides in
+ *                      multiples of 16 bytes
+ *   slot_map           device, int64 [n_tokens]: page * page_size + place; tokens
+ *                      with a slot outside [0, num_pages * page_size) are skipped.
+ *                      The tokens of one page stand next to each other, in
+ *                      ascending slots, each slot once (as bsp_build_page_tables
+ *                      writes them); otherwise what that page holds is unspecified
+ *   k_pages, v_pages,
+ *   k_exp, v_exp       device, the cache, updated
+ * Per page touched and kv head: need = the least e >= -117 with
+ * max |x| <= 448 * 2^e over its new tokens (at most 119). The page's exponent
+ * becomes need when its first new token stands at place 0, else max(need, old),
+ * and the codes before that token are rescaled to it (rounded to nearest even).
+ * New codes are x * 2^-e rounded to nearest even. Infinities and NaN become the
+ * format's NaN and do not count in max |x|; finite values beyond 448 * 2^119
+ * saturate. Codes behind the last new token of a page are left as they are.
+ */
+int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int64_t k_head_stride,
+                      int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t n_tokens,
+                      const int64_t *slot_map, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
+                      int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                      bsp_stream_t stream);
+
+/*
  * Decode run without any device allocation by the caller or the library.
  *
  * The paper has no counterpart: this is a convenience of this library. It is

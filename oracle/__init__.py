@@ -8,6 +8,7 @@ do. It shares no code with the CUDA path.
   fp64, one output at a time (loaded here through ctypes).
 - ``plan.py``: the load-balanced plan in plain Python.
 - ``fp8.py``: values of e4m3 KV codes (for the e4m3 KV-cache decode).
+- ``kv_cache.py``: page tables and the quantising append of the 8-bit cache.
 
 ``build()`` compiles ``attention.c`` with gcc into ``liboracle.so`` next to it.
 """
@@ -20,6 +21,7 @@ import subprocess
 import numpy as np
 
 from . import fp8 as fp8  # noqa: F401  (re-export)
+from . import kv_cache as kv_cache  # noqa: F401  (re-export)
 from . import plan as plan  # noqa: F401  (re-export)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

@@ -1,0 +1,128 @@
+"""The 8-bit KV cache on the host: the oracle's append and tables against facts
+worked out by hand, and what the entry points refuse (argument checks run before
+any device call; the pointers here are never followed)."""
+import numpy as np
+import pytest
+
+import oracle
+from oracle import kv_cache as kc
+
+
+@pytest.fixture(scope="module")
+def native():
+    from block_sparse_paged_gb300 import build
+    build.build()
+    from block_sparse_paged_gb300 import _native
+    _native.load()
+    return _native
+
+
+# ---- oracle pins ---------------------------------------------------------------
+def test_encode_is_the_nearest_code_with_ties_to_even():
+    vals = np.array([oracle.fp8.e4m3_value(c) for c in range(127)])
+    assert np.array_equal(kc.encode(vals), np.arange(127))           # every code maps to itself
+    assert np.array_equal(kc.encode(-vals[1:]), np.arange(1, 127) + 128)
+    mid = (vals[1:] + vals[:-1]) / 2
+    even = np.where(np.arange(126) % 2 == 0, np.arange(126), np.arange(1, 127))
+    assert np.array_equal(kc.encode(mid), even)                      # ties
+    assert np.array_equal(kc.encode(np.nextafter(mid, 0)), np.arange(126))
+    assert np.array_equal(kc.encode(np.nextafter(mid, 1e9)), np.arange(1, 127))
+    assert list(kc.encode(np.array([1e30, np.inf, np.nan, -500.0]))) == [126, 127, 127, 254]
+
+
+@pytest.mark.parametrize("amax,e", [(448.0, 0), (448.0001, 1), (224.0, -1), (1.0, -8), (0.875, -9), (0.0, -117),
+                                    (2.0 ** -140, -117), (3.3e38, 119), (1.75, -8), (1.7500001, -7)])
+def test_exponent(amax, e):
+    assert kc.exponent_for(amax) == e
+
+
+def test_append_rescales_what_a_page_held():
+    codes = np.zeros((2, 4, 1, 2), np.uint8)
+    exps = np.full((2, 1), -5, np.int8)
+    codes[1, :2, 0] = kc.encode(np.array([[448.0, 1.0], [-2.0, 2.0 ** -9]]))
+    x = np.array([[[56.0, 0.0]]])                                   # needs exponent -3
+    c, e = kc.append(x, [6], codes, exps)
+    assert list(e[:, 0]) == [-5, -3]
+    got = kc.values(c, e)[1, :, 0]
+    assert got[0].tolist() == [14.0, 1.0 / 32] and got[1].tolist() == [-1 / 16, 0.0]  # 2^-14 -> tie to zero
+    assert got[2].tolist() == [56.0, 0.0] and np.array_equal(c[0], codes[0])
+
+
+def test_tables_worked_example():
+    bt = np.array([[7, 3, -1], [-1, -1, -1], [2, -1, -1]], np.int32)
+    t = kc.tables([5, 0, 3], [4, 0, 1], [9, 8, 1], 3, bt, 4, 6, 7)
+    assert t["block_table"].tolist() == [[7, 3, 9], [-1, -1, -1], [2, -1, -1]]
+    assert t["kv_indptr"].tolist() == [0, 3, 3, 4] and t["last_page_len"].tolist() == [1, 0, 4]
+    assert t["kv_indices"].tolist() == [7, 3, 9, 2, 0, 0] and t["qo_indptr"].tolist() == [0, 4, 4, 5]
+    assert t["slot_map"].tolist() == [13, 14, 15, 36, 11, -1, -1]
+    assert t["positions"].tolist() == [5, 6, 7, 8, 3, 0, 0] and t["counts"].tolist() == [4, 5, 1, 0]
+
+
+# ---- refusals ------------------------------------------------------------------
+A = 256  # an aligned address that is never followed
+
+
+def tables_args(**kw):
+    d = dict(batch=2, ps=16, cached=A, new=A, free=A, free_cap=8, num_free=A, table=A, stride=4, width=4, kvp=A, last=A,
+             idx=A, cap_pages=8, qop=A, slots=A, pos=A, cap_tok=8, counts=A)
+    d.update(kw)
+    return list(d.values()) + [None]
+
+
+@pytest.mark.parametrize("kw", [dict(batch=-1), dict(ps=0), dict(free_cap=-1), dict(cap_pages=-1), dict(cap_tok=-1),
+                                dict(width=-1), dict(stride=3), dict(cached=None), dict(new=None), dict(table=None),
+                                dict(num_free=None), dict(free=None), dict(idx=None), dict(slots=None), dict(pos=None),
+                                dict(counts=None), dict(kvp=None), dict(qop=None), dict(last=None),
+                                dict(cap_tok=1 << 31), dict(slots=A + 8), dict(idx=A + 4), dict(pos=A + 4)],
+                         ids=lambda kw: "_".join(kw))
+def test_tables_refuse(native, kw):
+    lib = native.load()
+    assert lib.bsp_build_page_tables(*tables_args(**kw)) == native.BSP_ERR_INVALID_ARG
+    assert lib.bsp_last_error()
+
+
+def test_tables_refuse_a_batch_past_shared_memory(native):
+    assert native.load().bsp_build_page_tables(*tables_args(batch=16385)) == native.BSP_ERR_UNSUPPORTED
+
+
+def append_args(**kw):
+    d = dict(k=A, v=A, kt=1024, kh=128, vt=1024, vh=128, dtype=0, n=3, slots=A, kp=A, vp=A, ke=A, ve=A, pages=4, ps=16,
+             H=8, D=128)
+    d.update(kw)
+    return list(d.values()) + [None]
+
+
+@pytest.mark.parametrize("kw", [dict(k=None), dict(v=None), dict(slots=None), dict(kp=None), dict(vp=None),
+                                dict(ke=None), dict(ve=None), dict(n=-1), dict(pages=0), dict(ps=0), dict(H=0),
+                                dict(dtype=7), dict(k=A + 2), dict(v=A + 8), dict(kp=A + 4), dict(kt=1025),
+                                dict(vh=132, dtype=0), dict(pages=1 << 31)], ids=lambda kw: "_".join(kw))
+def test_append_refuses(native, kw):
+    assert native.load().bsp_append_kv_fp8(*append_args(**kw)) == native.BSP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(D=64), dict(D=256), dict(H=40000)])
+def test_append_unsupported(native, kw):
+    assert native.load().bsp_append_kv_fp8(*append_args(**kw)) == native.BSP_ERR_UNSUPPORTED
+
+
+def test_append_of_nothing_is_fine(native):
+    assert native.load().bsp_append_kv_fp8(*append_args(n=0, k=None, slots=None)) == native.BSP_OK
+
+
+def test_python_entries_refuse_host_tensors(native):
+    import torch
+    import block_sparse_paged_gb300 as bsp
+    i32 = torch.int32
+    z = torch.zeros(2, dtype=i32)
+    with pytest.raises(ValueError, match="block_table"):
+        bsp.build_page_tables(z, z, z, z[:1], torch.zeros(2, 3, dtype=i32), 16, 4, 4)
+    p = torch.zeros(2, 4, 1, 128).to(torch.float8_e4m3fn)
+    e = torch.zeros(2, 1, dtype=torch.int8)
+    k = torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+    for bad in (lambda: bsp.append_kv(k, k, torch.zeros(1, dtype=torch.int64), p, p, e, e),
+                lambda: bsp.append_kv(k[:, :, ::2], k[:, :, ::2], torch.zeros(1, dtype=torch.int64), p, p, e, e),
+                lambda: bsp.append_kv(k, k.float(), torch.zeros(1, dtype=torch.int64), p, p, e, e),
+                lambda: bsp.append_kv(k, k, torch.zeros(2, dtype=torch.int64), p, p, e, e),
+                lambda: bsp.append_kv(k, k, torch.zeros(1, dtype=torch.int64), p, p, e[:1], e)):
+        with pytest.raises(ValueError):
+            bad()
