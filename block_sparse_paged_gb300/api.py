@@ -170,10 +170,13 @@ class PagedAttention:
     def run(self, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_indices: torch.Tensor,
             sm_scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
             stream=None, return_lse: bool = True, k_scale: float = 1.0, v_scale: float = 1.0,
-            sink: torch.Tensor | None = None):
+            sink: torch.Tensor | None = None, k_exp: torch.Tensor | None = None, v_exp: torch.Tensor | None = None):
         """Attention of the planned batch. k_pages / v_pages are in the
         problem's dtype, or, for bf16 decode, torch.float8_e4m3fn pools read as
-        k_scale * k_pages and v_scale * v_pages (one scale per pool). sink:
+        k_scale * k_pages and v_scale * v_pages (one scale per pool), or, for bf16
+        decode and prefill with head_dim 128 and any page size, such pools with one
+        exponent per page and kv head: k_exp, v_exp int8 [num_pages, H_kv], value =
+        code * 2^exp (the cache that append_kv writes). sink:
         float32 [H_qo] on the device, one extra softmax logit per query head
         without a value row (the attention-sink variant), or None."""
         if self.info is None:
@@ -192,6 +195,9 @@ class PagedAttention:
             lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         dev = self.device
         fp8 = k_pages.dtype == torch.float8_e4m3fn
+        if k_exp is not None or v_exp is not None:
+            return self._run_fp8_block(q, k_pages, v_pages, k_exp, v_exp, kv_indices, sm_scale, out, lse, stream,
+                                       return_lse, k_scale, v_scale, sink)
         if fp8 and (self.mode != N.BSP_MODE_DECODE or self.dtype != torch.bfloat16):
             raise ValueError("e4m3 KV pools are read by the bf16 decode run only")
         kv_dt = torch.float8_e4m3fn if fp8 else self.dtype
@@ -213,6 +219,29 @@ class PagedAttention:
                 N.check(self.lib.bsp_decode_run(*args, k_pages.shape[0], *tail, s))
             else:
                 N.check(self.lib.bsp_prefill_run(*args, k_pages.shape[0], *tail, s))
+        return (out, lse) if return_lse else out
+
+    def _run_fp8_block(self, q, k_pages, v_pages, k_exp, v_exp, kv_indices, sm_scale, out, lse, stream, return_lse,
+                       k_scale, v_scale, sink):
+        """run() over an e4m3 cache with one exponent per page and kv head."""
+        if k_exp is None or v_exp is None:
+            raise ValueError("k_exp and v_exp are given together")
+        if k_scale != 1.0 or v_scale != 1.0:
+            raise ValueError("k_scale / v_scale do not apply to pools with exponents")
+        want = (k_pages.shape[0], k_pages.shape[2])
+        if k_exp.shape != want or v_exp.shape != want:
+            raise ValueError(f"k_exp / v_exp must be [{want[0]}, {want[1]}]")
+        if self.dtype != torch.bfloat16:
+            raise ValueError("pools with exponents are read by bfloat16 problems")
+        dev, f8, i8 = self.device, torch.float8_e4m3fn, torch.int8
+        self._set_sink(sink)
+        fn = self.lib.bsp_decode_run_fp8_block if self.mode == N.BSP_MODE_DECODE else self.lib.bsp_prefill_run_fp8_block
+        _call(dev, stream, fn, ctypes.byref(self.info), _dev(q, "q", self.dtype, dev),
+              _dev(k_pages, "k_pages", f8, dev), _dev(v_pages, "v_pages", f8, dev), _dev(k_exp, "k_exp", i8, dev),
+              _dev(v_exp, "v_exp", i8, dev),
+              _dev(kv_indices, "kv_indices", torch.int32, dev) if kv_indices.numel() else None, want[0], sm_scale,
+              _dev(out, "out", self.dtype, dev), None if lse is None else _dev(lse, "lse", torch.float32, dev),
+              self.workspace.data_ptr())
         return (out, lse) if return_lse else out
 
     def _set_sink(self, sink):

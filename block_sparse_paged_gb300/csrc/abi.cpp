@@ -112,6 +112,45 @@ extern "C" int bsp_prefill_run(const bsp_plan_info *plan, const void *q, const v
     return launch_reduce(plan, o, lse, workspace, stream);
 }
 
+namespace {
+
+int check_fp8_block(const bsp_plan_info *plan, int mode, const void *q, const void *k_pages, const void *v_pages,
+                    const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
+                    const void *o, const void *workspace) {
+    clear_error();
+    int rc = check_plan(plan, mode, workspace);
+    if (rc != BSP_OK) return rc;
+    if (!q || !k_pages || !v_pages || !k_exp || !v_exp || !o) return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    if (num_pages < 1 || num_pages > INT32_MAX) return fail(BSP_ERR_INVALID_ARG, "num_pages must be in [1, 2^31 - 1]");
+    if (!kv_indices && plan->num_table_pages > 0)
+        return fail(BSP_ERR_INVALID_ARG, "kv_indices is NULL but the page table has pages");
+    return check_aligned16(q, k_pages, v_pages, o, workspace);
+}
+
+}  // namespace
+
+extern "C" int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages,
+                                        const void *v_pages, const int8_t *k_exp, const int8_t *v_exp,
+                                        const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o,
+                                        float *lse, void *workspace, bsp_stream_t stream) {
+    int rc = check_fp8_block(plan, BSP_MODE_DECODE, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, o, workspace);
+    if (rc != BSP_OK) return rc;
+    return launch_decode_fp8_block(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse,
+                                   workspace, stream);
+}
+
+extern "C" int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages,
+                                         const void *v_pages, const int8_t *k_exp, const int8_t *v_exp,
+                                         const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o,
+                                         float *lse, void *workspace, bsp_stream_t stream) {
+    int rc = check_fp8_block(plan, BSP_MODE_PREFILL, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, o, workspace);
+    if (rc != BSP_OK) return rc;
+    rc = launch_prefill_fp8_block(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse,
+                                  workspace, stream);
+    if (rc != BSP_OK) return rc;
+    return launch_reduce(plan, o, lse, workspace, stream);
+}
+
 extern "C" int bsp_run_attention(const bsp_plan_info *plan, const void *q, const void *k_pages,
                                  const void *v_pages, const int32_t *kv_indices, int64_t num_pages,
                                  float sm_scale, void *o, float *lse, void *workspace, bsp_stream_t stream) {

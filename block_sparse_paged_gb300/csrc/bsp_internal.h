@@ -82,6 +82,13 @@ int launch_decode_fp8(const bsp_plan_info *plan, const void *q, const void *k_pa
 int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages,
                    const void *v_pages, const int32_t *kv_indices, int64_t num_pages,
                    float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream);
+// Decode and prefill over an e4m3 cache with one exponent per (page, kv head); num_pages in 1 .. 2^31 - 1.
+int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
+                            const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
+                            float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream);
+int launch_prefill_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
+                             const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
+                             float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream);
 // Copy the page table's first n_pages pages of K and V, in table order, into
 // the plan's gather region (prefill with a region); ids outside [0, num_pages)
 // give zero pages and set the workspace status word.

@@ -80,6 +80,12 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return r;
 }
 
+__device__ __forceinline__ float ex2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
@@ -91,7 +97,10 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 // kFp8 (with kTma, D = 128): the ring holds e4m3 rows (128 bytes, one swizzle
 // row); the compute warps read the bytes straight into f16 tensor-core
 // fragments (no staging copy).
-template <int D, bool kTma, bool kFp8 = false, int kNH = 1>
+// kBlk (with kFp8): one exponent per (page, kv head) beside the codes; the ring
+// carries them as bytes, one per 8 tokens (TMA: pages of 8 tokens or more) or per
+// token (cp.async), K's then V's.
+template <int D, bool kTma, bool kFp8 = false, int kNH = 1, bool kBlk = false>
 struct DecodeLayout {
     // bf16: 3 stages of 128 tokens (64 KB), each of the 4 compute warps taking
     // two 16-token sub-blocks per stage. Fewer, larger stages: a stage's fixed
@@ -101,7 +110,7 @@ struct DecodeLayout {
     // each (the head-major scratch needs only 8 rows per warp then); g > 8:
     // 128-token stages, 5 of them.
     static constexpr int kTK = kFp8 ? (kNH == 1 ? 4 * kTileK : 2 * kTileK) : 2 * kTileK;
-    static constexpr int kS = (kFp8 && kNH == 2) ? kStages : 3;  // ring stages
+    static constexpr int kS = (kFp8 && kNH == 2) ? (kBlk && !kTma ? kStages - 1 : kStages) : 3;  // ring stages
     static constexpr int kCons = kFp8 ? 8 : 4;                               // compute warps
     static constexpr int kSubB = kTK / (16 * kCons);                         // 16-token sub-blocks per warp and stage
     static constexpr int kScrRows = kFp8 ? 8 * kNH : kMmaRows;               // scratch rows per warp
@@ -123,7 +132,11 @@ struct DecodeLayout {
     static constexpr int kNumBars = 2 * kS + 3;             // full[S], empty[S], merge_in, merge_mid, merge_out
     // after the barriers: abort flag, pending-fold count and list
     static constexpr int kFlagBytes = 8 + 4 * (1 + kMaxPendingFolds);
-    static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + kFlagBytes + (kTma ? 1024 : 0);  // TMA: 1024-byte alignment slack
+    static constexpr int kExpOff = kBarOff + kNumBars * 8 + kFlagBytes;     // exponents [stage][K, V][kExpN]
+    static constexpr int kExpTok = kTma ? 8 : 1;                            // tokens per exponent
+    static constexpr int kExpN = kTK / kExpTok;
+    static constexpr int kExpBytes = kBlk ? kS * 2 * kExpN : 0;
+    static constexpr int kSmemBytes = kExpOff + kExpBytes + (kTma ? 1024 : 0);  // TMA: 1024-byte alignment slack
     static_assert(kSmemBytes <= 227 * 1024, "decode ring exceeds shared memory");
     // byte offset of 16-byte chunk c (of D / 8) of ring row r inside a K or V tile
     __device__ static __forceinline__ uint32_t chunk(int r, int c) {
@@ -148,6 +161,8 @@ struct DecodeParams {
     float cap_in, cap_out;   // sm_scale / c and c * log2(e)
     float v_scale;           // output factor (per-tensor V scale of an e4m3 pool; else 1)
     const float *sink;       // per-qo-head sink logits, or null
+    const int8_t *k_exp, *v_exp;  // kBlk: exponents [num_pages][H_kv]
+    int num_pages;                // kBlk: page ids outside [0, num_pages) read as zero codes
 };
 
 // Fold of one (row r, columns 4 cq .. 4 cq + 3) unit of a reduction-map entry
@@ -223,6 +238,7 @@ __device__ __forceinline__ void merge_entry(const DecodeParams &p, const bsp_mer
 constexpr int kStatusProducerWait = 0x101;
 constexpr int kStatusConsumerWait = 0x102;
 constexpr int kStatusMergeWait = 0x103;
+constexpr int kStatusPageIndex = 0x302;  // kBlk: a page id outside the pool
 constexpr int kStatusProbeWait = 0x1ff;  // wait_probe_kernel
 
 // Bounded mbarrier wait that also gives up as soon as another warp aborted.
@@ -254,12 +270,13 @@ __global__ void wait_probe_kernel(long long limit_cycles, int *status) {
 }
 
 // kNH (e4m3 only): 8-head tiles per kv head, ceil(g / 8)
-template <int D, bool kTma, bool kFp8 = false, int kNH = 1>
-__global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
+template <int D, bool kTma, bool kFp8 = false, int kNH = 1, bool kBlk = false>
+__global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThreads, 1)
     decode_bf16_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                        const DecodeParams p) {
-    static_assert(!kFp8 || (kTma && D == 128), "e4m3 pools: TMA gather, head_dim 128");
-    using LY = DecodeLayout<D, kTma, kFp8, kNH>;
+    static_assert(!kFp8 || ((kTma || kBlk) && D == 128), "e4m3 pools: head_dim 128; TMA gather or block exponents");
+    static_assert(kFp8 || !kBlk, "block exponents belong to e4m3 pools");
+    using LY = DecodeLayout<D, kTma, kFp8, kNH, kBlk>;
     constexpr int kSR = LY::kScrRows;
     constexpr int kStages = LY::kS;
     constexpr int kConsumers = LY::kCons;
@@ -290,7 +307,8 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
     sm100::fence_proxy_async_smem();
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            sm100::mbar_init(full0 + 8 * s, kTma ? 2 : 32 * LY::kLoad);  // TMA: one per producer warp; else per lane
+            // TMA: one arrival per producer warp; else per lane (with exponents also one for their store)
+            sm100::mbar_init(full0 + 8 * s, kTma ? 2 : 32 * LY::kLoad * (kBlk ? 2 : 1));
             sm100::mbar_init(empty0 + 8 * s, kConsumers);
         }
         sm100::mbar_init(merge_in, kConsumers);
@@ -330,6 +348,20 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
             };
             int cur = nt > 0 ? fetch_batch(0) : 0;
             int nxt = spb < nt ? fetch_batch(1) : 0;
+            // kBlk: lane l < kExpN reads the exponent of tokens 8l .. 8l + 7 of a stage, one
+            // stage ahead of its copies; tokens past the chunk and bad pages have 0
+            auto fetch_exp = [&](int tt, int ids) -> int {
+                const int gpg = __shfl_sync(0xffffffffu, ids, (tt % spb) * bps + (lane < kTK / 8 ? lane * 8 / br : 0));
+                const bool in = lane < kTK / 8 && tt * kTK + lane * 8 < len && gpg >= 0 && gpg < p.num_pages;
+                return in ? __ldg((is_v ? p.v_exp : p.k_exp) + (size_t)gpg * p.H_kv + w.kv_head) : 0;
+            };
+            int ex_cur = 0, ex_nxt = 0;
+            if constexpr (kBlk) {
+                if (nt > 0) ex_nxt = fetch_exp(0, cur);
+            }
+            (void)fetch_exp;
+            (void)ex_cur;
+            (void)ex_nxt;
             for (int t = 0; t < nt; ++t, ++k) {
                 if (t > 0 && t % spb == 0) {
                     cur = nxt;
@@ -338,19 +370,37 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
                 const int pg = __shfl_sync(0xffffffffu, cur, (t % spb) * bps + (lane < bps ? lane : 0));
                 const int n = min(kTK, len - t * kTK);
                 const int nbox = (n + br - 1) / br;
-                const int row0 = pg * p.page_size + (w.kv_start + t * kTK + lane * br) % p.page_size;
+                int row0 = pg * p.page_size + (w.kv_start + t * kTK + lane * br) % p.page_size;
+                if constexpr (kBlk) {
+                    ex_cur = ex_nxt;
+                    if (t + 1 < nt) ex_nxt = fetch_exp(t + 1, (t + 1) % spb == 0 ? nxt : cur);
+                    if (lane < nbox && (pg < 0 || pg >= p.num_pages)) {
+                        row0 = -br;  // a box outside the pool reads as zeros
+                        atomicCAS(status, 0, kStatusPageIndex);
+                    }
+                }
                 const int s = k % kStages;
                 const bool ok = wait_or_abort(empty0 + 8 * s, ((k / kStages) & 1) ^ 1, abort_flag, status,
                                               kStatusProducerWait);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                if (lane == 0) sm100::mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(nbox * br * D * LY::kElem));
-                __syncwarp();
+                if constexpr (!kBlk) {
+                    if (lane == 0) sm100::mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(nbox * br * D * LY::kElem));
+                    __syncwarp();
+                }
                 if (lane < nbox) {
                     const uint32_t dst = sbase + s * LY::kStageBytes + part + (uint32_t)(lane * br * 128);
 #pragma unroll
                     for (int h = 0; h < D * LY::kElem / 128; ++h)  // one copy per 128-byte-wide slab
                         sm100::tma_load_3d(dst + h * LY::kSlab, map, full0 + 8 * s, h * (128 / LY::kElem), w.kv_head,
                                            row0);
+                }
+                if constexpr (kBlk) {
+                    // the copies are under way: their bytes may land before the arrival that
+                    // expects them, which also publishes the exponents
+                    if (lane < kTK / 8)
+                        smem[LY::kExpOff + (s * 2 + (is_v ? 1 : 0)) * LY::kExpN + lane] = (uint8_t)ex_cur;
+                    __syncwarp();
+                    if (lane == 0) sm100::mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(nbox * br * D * LY::kElem));
                 }
             }
         }
@@ -363,8 +413,10 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
         // `lane + 32` of the half into byte offsets of their rows (one division
         // each), then every warp instruction copies T = 32 / C whole rows, C =
         // D / 8 chunks of 16 bytes per row, taking the row offsets by shuffle.
-        constexpr int C = D / 8, T = 32 / C;
+        constexpr int C = D * LY::kElem / 16, T = 32 / C;
         constexpr int kHalfTK = kTK / 2;  // tokens of a stage per loader warp
+        constexpr uint64_t kBadRow = ~uint64_t(0);  // kBlk: offset of a token whose page id is outside the pool
+        (void)kBadRow;
         const bool is_v = warp >= kConsumers + 2;
         const int tok_base = ((warp - kConsumers) & 1) * kHalfTK;
         const char *src = static_cast<const char *>(is_v ? p.v : p.k);
@@ -394,8 +446,22 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
 #pragma unroll
                 for (int jj = 0; jj < kJ; ++jj) {
                     const int tok = w.kv_start + t * kTK + tok_base + lane + 32 * jj;
-                    off[jj] = (((uint64_t)pg[jj] * p.page_size + tok % p.page_size) * p.H_kv + w.kv_head) * (D * 2);
+                    off[jj] = (((uint64_t)pg[jj] * p.page_size + tok % p.page_size) * p.H_kv + w.kv_head) * (D * LY::kElem);
                 }
+                int ex[kJ];
+                if constexpr (kBlk) {
+#pragma unroll
+                    for (int jj = 0; jj < kJ; ++jj) {
+                        const bool live = t * kTK + tok_base + lane + 32 * jj < len;
+                        const bool in = pg[jj] >= 0 && pg[jj] < p.num_pages;
+                        ex[jj] = live && in ? __ldg((is_v ? p.v_exp : p.k_exp) + (size_t)pg[jj] * p.H_kv + w.kv_head) : 0;
+                        if (live && !in) {
+                            off[jj] = kBadRow;  // copied as zeros
+                            atomicCAS(status, 0, kStatusPageIndex);
+                        }
+                    }
+                }
+                (void)ex;
                 if (t + 1 < nt) fetch(t + 1, pg);
                 const int s = k % kStages;
                 const bool ok = wait_or_abort(empty0 + 8 * s, ((k / kStages) & 1) ^ 1, abort_flag, status,
@@ -409,7 +475,18 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
                     const int j = tok_base + jl;                      // token within the stage
                     const int half = (i * T) >> 5;                    // same for the whole warp: T divides 32
                     const uint64_t o = __shfl_sync(0xffffffffu, off[half], jl & 31);
-                    if (j < n) cp_async_16(dst + LY::chunk(j, my_chunk), src + o + my_chunk * 16, 16);
+                    if constexpr (kBlk) {
+                        const bool in = o != kBadRow;
+                        if (j < n) cp_async_16(dst + LY::chunk(j, my_chunk), in ? src + o + my_chunk * 16 : src, in ? 16 : 0);
+                    } else {
+                        if (j < n) cp_async_16(dst + LY::chunk(j, my_chunk), src + o + my_chunk * 16, 16);
+                    }
+                }
+                if constexpr (kBlk) {
+#pragma unroll
+                    for (int jj = 0; jj < kJ; ++jj)
+                        smem[LY::kExpOff + (s * 2 + (is_v ? 1 : 0)) * LY::kExpN + tok_base + lane + 32 * jj] = (uint8_t)ex[jj];
+                    sm100::mbar_arrive(full0 + 8 * s);  // publishes this lane's exponents
                 }
                 // arrive on full[s] once this lane's copies have landed
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(full0 + 8 * s) : "memory");
@@ -464,10 +541,15 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
             }
             // per head (2c, 2c + 1 of each 8-head tile): running max, this lane's share
             // of the sum (its tokens r, r + 8), O^T accumulators
+            // kBlk: oh, the running maximum of score + V exponent, is the reference of O
+            // (token weights 2^(s + e_v), whatever the exponents' spread); mh stays that of
+            // the sum. At the end O moves to mh.
             float mh[kNH][2], lh[kNH][2], oacc[D / 16][kNH][4];
+            float oh[kNH][2];
 #pragma unroll
             for (int nh = 0; nh < kNH; ++nh) {
                 mh[nh][0] = mh[nh][1] = -INFINITY;
+                oh[nh][0] = oh[nh][1] = -INFINITY;
                 lh[nh][0] = lh[nh][1] = 0.f;
 #pragma unroll
                 for (int dt = 0; dt < D / 16; ++dt) oacc[dt][nh][0] = oacc[dt][nh][1] = oacc[dt][nh][2] = oacc[dt][nh][3] = 0.f;
@@ -508,6 +590,21 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
                     const int rr = 2 * c + (i & 1) + 8 * (i >> 1), R = row0 + rr;
                     vw[i] = sm100::ld_shared_v4(vb + R * 128 + ((qn ^ (R & 7)) << 4));
                 }
+                // factors of this lane's tokens qn and qn + 8: 2^e_k on the score, e_v on its weight
+                float kf[2], ve[2];
+                if constexpr (kBlk) {
+                    const int8_t *ek = reinterpret_cast<const int8_t *>(smem) + LY::kExpOff + s * 2 * LY::kExpN;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int at = kTma ? row0 / 8 + i : row0 + 8 * i + qn;
+                        const int e = ek[at];
+                        kf[i] = __int_as_float(e >= -126 ? (e + 127) << 23 : 0x00400000 >> (-127 - e)) *
+                                (p.soft_cap_on ? p.cap_in : p.scale_log2);
+                        ve[i] = (float)ek[LY::kExpN + at];
+                    }
+                }
+                (void)kf;
+                (void)ve;
                 if (valid < 16) {  // the chunk ends inside this warp's rows (warp-uniform)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -544,10 +641,50 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
                     for (int e = 0; e < 4; ++e) {
                         const float v = st[nh][0][e] + st[nh][1][e];
                         const int tk = qn + 8 * (e >> 1);
-                        const float x = p.soft_cap_on ? tanh_ex2(v * p.cap_in) * p.cap_out : v * p.scale_log2;
+                        float x;
+                        if constexpr (kBlk) {
+                            x = v * kf[e >> 1];
+                            if (p.soft_cap_on) x = tanh_ex2(x) * p.cap_out;
+                        } else {
+                            x = p.soft_cap_on ? tanh_ex2(v * p.cap_in) * p.cap_out : v * p.scale_log2;
+                        }
                         sv[e] = (tk < valid && tk >= lo_rel) ? x : -INFINITY;
                     }
                     float mx0 = fmaxf(sv[0], sv[2]), mx1 = fmaxf(sv[1], sv[3]);
+                    if constexpr (kBlk) {
+                        float so[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) so[e] = sv[e] + ve[e >> 1];
+                        float my0 = fmaxf(so[0], so[2]), my1 = fmaxf(so[1], so[3]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) {
+                            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                            my0 = fmaxf(my0, __shfl_xor_sync(0xffffffffu, my0, o));
+                            my1 = fmaxf(my1, __shfl_xor_sync(0xffffffffu, my1, o));
+                        }
+                        const float n0 = fmaxf(mh[nh][0], mx0), n1 = fmaxf(mh[nh][1], mx1);
+                        const float q0 = fmaxf(oh[nh][0], my0), q1 = fmaxf(oh[nh][1], my1);
+                        const float ref0 = n0 == -INFINITY ? 0.f : n0, ref1 = n1 == -INFINITY ? 0.f : n1;
+                        const float rq0 = q0 == -INFINITY ? 0.f : q0, rq1 = q1 == -INFINITY ? 0.f : q1;
+                        lh[nh][0] = lh[nh][0] * ex2_ftz(mh[nh][0] - ref0) + (ex2_ftz(sv[0] - ref0) + ex2_ftz(sv[2] - ref0));
+                        lh[nh][1] = lh[nh][1] * ex2_ftz(mh[nh][1] - ref1) + (ex2_ftz(sv[1] - ref1) + ex2_ftz(sv[3] - ref1));
+                        const float b0 = ex2_ftz(oh[nh][0] - rq0), b1 = ex2_ftz(oh[nh][1] - rq1);
+                        mh[nh][0] = n0;
+                        mh[nh][1] = n1;
+                        oh[nh][0] = q0;
+                        oh[nh][1] = q1;
+                        if (__any_sync(0xffffffffu, b0 != 1.f || b1 != 1.f)) {
+#pragma unroll
+                            for (int dt = 0; dt < D / 16; ++dt) {
+                                oacc[dt][nh][0] *= b0; oacc[dt][nh][1] *= b1;
+                                oacc[dt][nh][2] *= b0; oacc[dt][nh][3] *= b1;
+                            }
+                        }
+                        pb[nh][0] = movmatrix_trans(pack_f16_sat(ex2_ftz(so[0] - rq0), ex2_ftz(so[1] - rq1)));
+                        pb[nh][1] = movmatrix_trans(pack_f16_sat(ex2_ftz(so[2] - rq0), ex2_ftz(so[3] - rq1)));
+                        continue;
+                    }
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) {
                         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
@@ -603,6 +740,15 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH>::kThreads, 1)
                 for (int o = 4; o < 32; o <<= 1) {
                     lh[nh][0] += __shfl_xor_sync(0xffffffffu, lh[nh][0], o);
                     lh[nh][1] += __shfl_xor_sync(0xffffffffu, lh[nh][1], o);
+                }
+                if constexpr (kBlk) {
+                    const float f0 = oh[nh][0] == -INFINITY ? 0.f : exp2f(oh[nh][0] - mh[nh][0]);
+                    const float f1 = oh[nh][1] == -INFINITY ? 0.f : exp2f(oh[nh][1] - mh[nh][1]);
+#pragma unroll
+                    for (int dt = 0; dt < D / 16; ++dt) {
+                        oacc[dt][nh][0] *= f0; oacc[dt][nh][1] *= f1;
+                        oacc[dt][nh][2] *= f0; oacc[dt][nh][3] *= f1;
+                    }
                 }
                 const int h0 = 8 * nh + 2 * c;
                 if (qn == 0) {
@@ -983,20 +1129,21 @@ int num_sms_of_current_device(int *dev_out) {
     return sms[dev];
 }
 
-template <int D, bool kTma, bool kFp8 = false, int kNH = 1>
+template <int D, bool kTma, bool kFp8 = false, int kNH = 1, bool kBlk = false>
 int launch_decode_bf16(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeParams &p, int grid,
                        cudaStream_t stream) {
     static bool configured[64] = {false};
     int dev = 0;
     if (num_sms_of_current_device(&dev) < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
-    constexpr int kSmem = DecodeLayout<D, kTma, kFp8, kNH>::kSmemBytes;
+    using LY = DecodeLayout<D, kTma, kFp8, kNH, kBlk>;
+    constexpr int kSmem = LY::kSmemBytes;
     if (!configured[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(decode_bf16_kernel<D, kTma, kFp8, kNH>,
+        cudaError_t e = cudaFuncSetAttribute(decode_bf16_kernel<D, kTma, kFp8, kNH, kBlk>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("decode smem attribute: ") + cudaGetErrorString(e));
         configured[dev] = true;
     }
-    decode_bf16_kernel<D, kTma, kFp8, kNH><<<grid, DecodeLayout<D, kTma, kFp8, kNH>::kThreads, kSmem, stream>>>(tk, tv, p);
+    decode_bf16_kernel<D, kTma, kFp8, kNH, kBlk><<<grid, LY::kThreads, kSmem, stream>>>(tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("decode launch: ") + cudaGetErrorString(e));
     return BSP_OK;
@@ -1062,6 +1209,8 @@ int decode_params(const bsp_plan_info *plan, const void *q, const void *k_pages,
     p.scale_log2 = qk_scale * kLog2e;
     p.v_scale = v_scale;
     p.sink = P.sink;
+    p.k_exp = p.v_exp = nullptr;
+    p.num_pages = 0;
     p.window_left = P.window_left;
     p.soft_cap_on = P.logits_soft_cap > 0.f;
     p.cap_in = p.soft_cap_on ? qk_scale / P.logits_soft_cap : 0.f;
@@ -1150,6 +1299,38 @@ int launch_decode_fp8(const bsp_plan_info *plan, const void *q, const void *k_pa
     if (rc != BSP_OK) return rc;
     return plan->group <= 8 ? launch_decode_bf16<128, true, true, 1>(tk, tv, p, grid, stream)
                             : launch_decode_bf16<128, true, true, 2>(tk, tv, p, grid, stream);
+}
+
+int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
+                            const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
+                            float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream) {
+    const bsp_problem &P = plan->problem;
+    if (P.dtype != BSP_DTYPE_BF16 || P.head_dim != 128)
+        return fail(BSP_ERR_UNSUPPORTED, "e4m3 KV decode needs a bf16 problem (queries, outputs) with head_dim 128");
+    if (plan->group > kMmaRows) return fail(BSP_ERR_UNSUPPORTED, "e4m3 KV decode needs num_qo_heads / num_kv_heads <= 16");
+    DecodeParams p;
+    const int grid = decode_params(plan, q, k_pages, v_pages, kv_indices, sm_scale, 1.f, 1.f, o, lse, workspace, p);
+    if (grid < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    p.k_exp = k_exp;
+    p.v_exp = v_exp;
+    p.num_pages = (int)num_pages;
+    // the TMA gather's rule is decode's: pages of 8 or more tokens, powers of two, rows within int32
+    const int ps = P.page_size;
+    const bool tma = ps >= 8 && (ps & (ps - 1)) == 0 && num_pages * (int64_t)ps <= INT32_MAX;
+    CUtensorMap tk, tv;
+    std::memset(&tk, 0, sizeof(tk));
+    std::memset(&tv, 0, sizeof(tv));
+    p.box_rows = tma ? (ps < kTileK ? ps : kTileK) : 0;
+    if (tma) {
+        const uint64_t rows = (uint64_t)num_pages * ps;
+        int rc = make_tmap(&tk, k_pages, 1, P.head_dim, P.num_kv_heads, rows, 1, p.box_rows);
+        if (rc == BSP_OK) rc = make_tmap(&tv, v_pages, 1, P.head_dim, P.num_kv_heads, rows, 1, p.box_rows);
+        if (rc != BSP_OK) return rc;
+        return plan->group <= 8 ? launch_decode_bf16<128, true, true, 1, true>(tk, tv, p, grid, stream)
+                                : launch_decode_bf16<128, true, true, 2, true>(tk, tv, p, grid, stream);
+    }
+    return plan->group <= 8 ? launch_decode_bf16<128, false, true, 1, true>(tk, tv, p, grid, stream)
+                            : launch_decode_bf16<128, false, true, 2, true>(tk, tv, p, grid, stream);
 }
 
 int launch_wait_probe(long long limit_cycles, int *status, cudaStream_t stream) {

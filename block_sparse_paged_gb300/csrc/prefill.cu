@@ -41,6 +41,7 @@
 // up sets the workspace status word and an abort flag, and the CTA finishes
 // without further work.
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 #include <climits>
@@ -65,6 +66,10 @@ constexpr int kThreads = 320;     // warp 0 TMA, warp 1 MMA, warps 2-9 softmax
 // cannot keep enough 16-byte copies in flight)
 constexpr int kThreadsGather = 352;
 constexpr int kVWarp = 10;
+// e4m3 cache: warp 0 copies Q alone, warps 10 and 11 read K's and V's codes and write
+// them converted into the rings
+constexpr int kThreadsFp8 = 384;
+constexpr int kCvtWarp = 10;
 constexpr int kHalf = 16384;      // [128 rows][64 bf16], 128-byte swizzle
 constexpr int kTile = 2 * kHalf;  // [128 rows][128 bf16]
 
@@ -92,6 +97,7 @@ static_assert(kSmemBytes <= 227 * 1024, "prefill tiles exceed shared memory");
 constexpr uint32_t kTmemCols = 512;
 constexpr long long kWaitLimitCycles = 4000000000ll;  // about 2 s at 2 GHz: a fault, not a stall
 constexpr int kStatusWait = 0x201;
+constexpr int kStatusPageIndex = 0x302;  // e4m3 cache: a page id outside the pool
 constexpr float kRescaleThreshold = 8.f;  // log2 units
 
 struct PrefillParams {
@@ -110,6 +116,8 @@ struct PrefillParams {
     int soft_cap_on;         // scores become tanh(s * cap_in); scale_log2 is then c * log2(e)
     float cap_in;            // sm_scale / c
     const float *sink;       // per-qo-head sink logits, or null (applied to finished rows)
+    const int8_t *k_exp, *v_exp;  // e4m3 cache: exponents [num_pages][H_kv]
+    int num_pages;                // e4m3 cache: page ids outside [0, num_pages) read as zero codes
 };
 
 struct Ctx {
@@ -160,13 +168,27 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Four e4m3 codes (lowest byte first) times s, a power of two, as four bf16 values.
+// Exact for exponents in [-117, 119]: every code is an f16 value, the product an fp32
+// one with 4 significant bits, and that a bf16 one. NaN codes stay NaN.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, float s) {
+    uint32_t h0, h1;
+    dev::e4m3x4_to_f16x4(w, h0, h1);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
+    return make_uint2(dev::pack_bf16(a.x * s, a.y * s), dev::pack_bf16(b.x * s, b.y * s));
+}
+
 // kTma: K and V tiles arrive by TMA tensor copies, one per page box (pages of
 // 8 or more tokens); otherwise by 16-byte cp.async copies written straight into
 // the same 128-byte-swizzled layout (pages of any size, e.g. 1).
 // kVar: the sliding window and logits soft-cap variants are compiled in (the
 // default instantiation has neither, at no cost).
-template <bool kTma, bool kVar>
-__global__ void __launch_bounds__(kTma ? kThreads : kThreadsGather, 1)
+// kFp8 (with kTma false): K and V are e4m3 codes with an exponent per (page, kv
+// head), converted to bf16 on their way into the tiles; everything behind the rings
+// is the bf16 kernel.
+template <bool kTma, bool kVar, bool kFp8 = false>
+__global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTma ? kThreads : kThreadsGather, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const PrefillParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -243,6 +265,7 @@ __global__ void __launch_bounds__(kTma ? kThreads : kThreadsGather, 1)
                 }
             };
             (void)lookup;
+            if constexpr (kFp8) continue;  // K and V: the converting warps
             for (int t = 0; t < nt; ++t, ++j) {
                 const int tok0 = w.kv_start + t * kKvTile;
                 const int valid = min(kKvTile, len - t * kKvTile);
@@ -313,7 +336,92 @@ __global__ void __launch_bounds__(kTma ? kThreads : kThreadsGather, 1)
             }
         }
         if constexpr (!kTma) asm volatile("cp.async.wait_all;\n" ::: "memory");  // nothing in flight at exit
-    } else if (!kTma && warp == kVWarp) {
+    } else if (kFp8 && warp >= kCvtWarp) {
+        // ------------------------------------------- K (warp 10) and V (warp 11), e4m3
+        // Lane l looks up the pages and exponents of keys l + 32 i one tile ahead. Each
+        // warp-wide load then takes the codes of four keys (8 lanes x 16 codes), eight
+        // loads in flight, the next eight issued before these are converted; a lane's 16
+        // values are two 16-byte chunks of its key's swizzled row. Keys past the chunk end
+        // are written as zeros (P = 0 there must meet finite values of V).
+        constexpr int kBatch = 8;
+        constexpr int kNB = kKvTile / 4 / kBatch;
+        const bool is_v = warp == kCvtWarp + 1;
+        const char *src = is_v ? p.v : p.k;
+        const int8_t *exps = is_v ? p.v_exp : p.k_exp;
+        const uint32_t ring = sb + (is_v ? kOffV : kOffK);
+        const int full0 = is_v ? kVFull0 : kKFull0, empty0 = is_v ? kVEmpty0 : kKEmpty0;
+        static_assert(kKStages == kVStages, "one ring position for both");
+        constexpr long long kNoRow = -1;
+        const int c = lane & 7, sub4 = lane >> 3;
+        const bool hi = c >= 4;  // these lanes store their second chunk first: no bank is met twice
+        int j = 0;
+        bool ok = true;
+        for (int it = it0; it < it1 && ok; ++it) {
+            const bsp_work_item w = items[it];
+            const int len = w.kv_end - w.kv_start;
+            const int nt = (len + kKvTile - 1) / kKvTile;
+            int pg[kKvTile / 32], ex[kKvTile / 32];
+            auto lookup = [&](int tt) {
+#pragma unroll
+                for (int i = 0; i < kKvTile / 32; ++i) {
+                    const int key = tt * kKvTile + lane + 32 * i;
+                    pg[i] = key < len ? __ldg(p.kv_indices + w.page_base + (w.kv_start + key) / p.page_size) : -1;
+                    if (key < len && (pg[i] < 0 || pg[i] >= p.num_pages)) {
+                        pg[i] = -1;
+                        atomicCAS(ctx.status, 0, kStatusPageIndex);
+                    }
+                    ex[i] = pg[i] >= 0 ? __ldg(exps + (size_t)pg[i] * p.H_kv + w.kv_head) : 0;
+                }
+            };
+            if (nt > 0) lookup(0);
+            for (int t = 0; t < nt; ++t, ++j) {
+                const int tok0 = w.kv_start + t * kKvTile;
+                const int st = j % kKStages, rd = j / kKStages;
+                long long off[kKvTile / 32];
+                float scale[kKvTile / 32];
+#pragma unroll
+                for (int i = 0; i < kKvTile / 32; ++i) {
+                    off[i] = pg[i] >= 0 ? (((long long)pg[i] * p.page_size + (tok0 + lane + 32 * i) % p.page_size) *
+                                               p.H_kv + w.kv_head) * kD
+                                        : kNoRow;
+                    scale[i] = __int_as_float(ex[i] >= -126 ? (ex[i] + 127) << 23 : 0x00400000 >> (-127 - ex[i]));
+                }
+                auto load = [&](uint4 (&d)[kBatch], int b) {
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int key = 4 * (b * kBatch + i) + sub4;  // key >> 5 == b: the same for the whole batch
+                        const long long o = __shfl_sync(0xffffffffu, off[b], key & 31);
+                        d[i] = make_uint4(0, 0, 0, 0);
+                        if (o != kNoRow) d[i] = __ldg(reinterpret_cast<const uint4 *>(src + o) + c);
+                    }
+                };
+                static_assert(4 * kBatch == 32, "a batch is the 32 keys of one lookup register");
+                uint4 d[2][kBatch];
+                load(d[0], 0);
+                if (!(ok = wait_bar_warp(ctx, bar(empty0 + st), (rd & 1) ^ 1))) break;
+                const uint32_t dst = ring + st * kTile;
+#pragma unroll
+                for (int b = 0; b < kNB; ++b) {
+                    if (b + 1 < kNB) load(d[(b + 1) & 1], b + 1);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int key = 4 * (b * kBatch + i) + sub4;
+                        const float s = __shfl_sync(0xffffffffu, scale[b], key & 31);
+                        const uint4 x = d[b & 1][i];
+                        const uint2 a0 = e4m3x4_to_bf16x4(hi ? x.z : x.x, s), a1 = e4m3x4_to_bf16x4(hi ? x.w : x.y, s);
+                        const uint2 b0 = e4m3x4_to_bf16x4(hi ? x.x : x.z, s), b1 = e4m3x4_to_bf16x4(hi ? x.y : x.w, s);
+                        const uint32_t row = dst + (c >> 2) * kHalf + key * 128;
+                        const int cc = (2 * c + (hi ? 1 : 0)) & 7;
+                        st_shared_v4(row + ((cc ^ (key & 7)) << 4), a0.x, a0.y, a1.x, a1.y);
+                        st_shared_v4(row + (((cc ^ 1) ^ (key & 7)) << 4), b0.x, b0.y, b1.x, b1.y);
+                    }
+                }
+                if (t + 1 < nt) lookup(t + 1);
+                fence_proxy_async_smem();
+                mbar_arrive(bar(full0 + st));
+            }
+        }
+    } else if (!kTma && !kFp8 && warp == kVWarp) {
         // ------------------------------------------------ V gather (cp.async)
         // The same items and tiles as warp 0, V rows only: lane l looks up keys
         // l + 32 i one tile ahead, each warp instruction copies two keys' sixteen
@@ -740,9 +848,13 @@ int launch_gather_pages(const bsp_plan_info *plan, const void *k_pages, const vo
     return BSP_OK;
 }
 
-int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
-                   const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o, float *lse,
-                   void *workspace, cudaStream_t stream) {
+namespace {
+
+// Prefill over bf16 pools, or (k_exp, v_exp given) over an e4m3 cache with exponents.
+int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
+                       const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
+                       float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream) {
+    const bool fp8 = k_exp != nullptr;
     const bsp_problem &P = plan->problem;
     const int g = plan->group;
     if (P.dtype != BSP_DTYPE_BF16) return fail(BSP_ERR_UNSUPPORTED, "prefill supports bf16 only");
@@ -755,8 +867,8 @@ int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages
     // table order, and every request's keys are then one contiguous run of
     // rows read by 128-row TMA boxes; otherwise 16-byte cp.async copies.
     const int ps = P.page_size;
-    const bool direct = ps >= 8 && (ps & (ps - 1)) == 0 && num_pages * (int64_t)ps <= INT32_MAX;
-    const bool gather = !direct && plan->off_gather != 0 && plan->num_table_pages <= plan->capacity.max_gather_pages;
+    const bool direct = !fp8 && ps >= 8 && (ps & (ps - 1)) == 0 && num_pages * (int64_t)ps <= INT32_MAX;
+    const bool gather = !fp8 && !direct && plan->off_gather != 0 && plan->num_table_pages <= plan->capacity.max_gather_pages;
     const bool tma = direct || gather;
 
     CUtensorMap tq, tk, tv;
@@ -795,6 +907,9 @@ int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages
     p.soft_cap_on = P.logits_soft_cap > 0.f;
     p.cap_in = p.soft_cap_on ? sm_scale / P.logits_soft_cap : 0.f;
     p.sink = P.sink;
+    p.k_exp = k_exp;
+    p.v_exp = v_exp;
+    p.num_pages = (int)num_pages;
     if (p.soft_cap_on) p.scale_log2 = P.logits_soft_cap * dev::kLog2e;
     p.H_qo = P.num_qo_heads;
     p.g = g;
@@ -804,13 +919,14 @@ int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages
     p.causal = P.causal;
     p.tile_rows = plan->tile_rows;
 
-    static bool configured[4][64] = {{false}};
+    static bool configured[6][64] = {{false}};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(BSP_ERR_CUDA, "no current CUDA device");
     const bool var = P.window_left > 0 || P.logits_soft_cap > 0.f;
-    auto kern = tma ? (var ? prefill_kernel<true, true> : prefill_kernel<true, false>)
+    auto kern = fp8 ? (var ? prefill_kernel<false, true, true> : prefill_kernel<false, false, true>)
+                : tma ? (var ? prefill_kernel<true, true> : prefill_kernel<true, false>)
                     : (var ? prefill_kernel<false, true> : prefill_kernel<false, false>);
-    const int which = (tma ? 2 : 0) + (var ? 1 : 0);
+    const int which = (fp8 ? 4 : tma ? 2 : 0) + (var ? 1 : 0);
     if (!configured[which][dev]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("prefill smem attribute: ") + cudaGetErrorString(e));
@@ -823,10 +939,26 @@ int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages
     p.num_queues = plan->capacity.num_ctas;
     p.queues_per_cta = (p.num_queues + sms - 1) / sms;
     const int grid = (p.num_queues + p.queues_per_cta - 1) / p.queues_per_cta;
-    kern<<<grid, tma ? kThreads : kThreadsGather, kSmemBytes, stream>>>(tq, tk, tv, p);
+    kern<<<grid, fp8 ? kThreadsFp8 : tma ? kThreads : kThreadsGather, kSmemBytes, stream>>>(tq, tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("prefill launch: ") + cudaGetErrorString(e));
     return BSP_OK;
+}
+
+}  // namespace
+
+int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
+                   const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o, float *lse,
+                   void *workspace, cudaStream_t stream) {
+    return launch_prefill_any(plan, q, k_pages, v_pages, nullptr, nullptr, kv_indices, num_pages, sm_scale, o, lse,
+                              workspace, stream);
+}
+
+int launch_prefill_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
+                             const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
+                             float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream) {
+    return launch_prefill_any(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse,
+                              workspace, stream);
 }
 
 }  // namespace bsp

@@ -459,6 +459,26 @@ int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int6
                       bsp_stream_t stream);
 
 /*
+ * Attention over the 8-bit cache: bsp_decode_run and bsp_prefill_run with k =
+ * code * 2^k_exp[page, kv head] and v alike; plan, q, o, lse, window, soft-cap,
+ * sink and workspace as there, queries and outputs bf16, head_dim 128.
+ *   k_pages, v_pages   device, e4m3 bytes [num_pages, page_size, H_kv, 128]
+ *   k_exp, v_exp       device, int8 [num_pages, H_kv]
+ *   num_pages          pages in each pool, 1 .. 2^31 - 1
+ * Any page size. Decode: g <= 16; scores and sums fp32, token weights times
+ * 2^v_exp in f16 against their own running maximum. Prefill: codes converted to
+ * bf16 (exact for exponents in [-117, 119]) on their way to the tensor cores;
+ * 128 % g == 0. A page id outside [0, num_pages) reads as zero codes and sets the
+ * workspace status word (0x302, bsp_check_device_error).
+ */
+int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
+                             const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
+                             float sm_scale, void *o, float *lse, void *workspace, bsp_stream_t stream);
+int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
+                              const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
+                              float sm_scale, void *o, float *lse, void *workspace, bsp_stream_t stream);
+
+/*
  * Decode run without any device allocation by the caller or the library.
  *
  * The paper has no counterpart: this is a convenience of this library. It is

@@ -1,6 +1,8 @@
 """The 8-bit KV cache on the host: the oracle's append and tables against facts
 worked out by hand, and what the entry points refuse (argument checks run before
 any device call; the pointers here are never followed)."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -126,3 +128,45 @@ def test_python_entries_refuse_host_tensors(native):
                 lambda: bsp.append_kv(k, k, torch.zeros(1, dtype=torch.int64), p, p, e[:1], e)):
         with pytest.raises(ValueError):
             bad()
+
+
+# ---- attention over the cache ----------------------------------------------------
+def block_plan(mode, H=8, Hkv=2, D=128, dtype=None):
+    """A plan info that claims to be copied to a device (the checks need no more)."""
+    import torch
+    import block_sparse_paged_gb300 as bsp
+    prob = bsp.make_problem(mode, H, Hkv, D, 16, False, dtype or torch.bfloat16)
+    cap = bsp.Capacity(2, 4, 64, 1, 0, 0)
+    info = bsp.plan_host(prob, cap, [0, 2, 3], [3, 16], [0, 1, 2])[0]
+    info.valid = 1
+    return info
+
+
+def run_args(info, **kw):
+    d = dict(q=A, k=A, v=A, ke=A, ve=A, idx=A, pages=4, scale=0.1, o=A, lse=None, ws=A)
+    d.update(kw)
+    return [ctypes.byref(info)] + list(d.values()) + [None]
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("kw", [dict(q=None), dict(k=None), dict(v=None), dict(ke=None), dict(ve=None), dict(idx=None),
+                                dict(pages=0), dict(pages=-1), dict(pages=1 << 31), dict(o=None), dict(ws=None),
+                                dict(q=A + 8), dict(k=A + 4), dict(o=A + 2)], ids=lambda kw: "_".join(kw))
+def test_block_runs_refuse(native, mode, kw):
+    lib = native.load()
+    fn = lib.bsp_decode_run_fp8_block if mode == 0 else lib.bsp_prefill_run_fp8_block
+    assert fn(*run_args(block_plan(mode), **kw)) == native.BSP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+def test_block_runs_refuse_plans(native, mode):
+    import torch
+    lib = native.load()
+    fn = lib.bsp_decode_run_fp8_block if mode == 0 else lib.bsp_prefill_run_fp8_block
+    assert fn(*run_args(block_plan(1 - mode))) == native.BSP_ERR_INVALID_ARG      # the other mode's plan
+    host = block_plan(mode)
+    host.valid = 2
+    assert fn(*run_args(host)) == native.BSP_ERR_INVALID_ARG                      # a host-only plan
+    if mode == 0:
+        assert fn(*run_args(block_plan(0, D=64))) == native.BSP_ERR_UNSUPPORTED
+        assert fn(*run_args(block_plan(0, dtype=torch.float32))) == native.BSP_ERR_UNSUPPORTED
