@@ -235,12 +235,23 @@ class PagedAttention:
             raise ValueError("pools with exponents are read by bfloat16 problems")
         dev, f8, i8 = self.device, torch.float8_e4m3fn, torch.int8
         self._set_sink(sink)
-        fn = self.lib.bsp_decode_run_fp8_block if self.mode == N.BSP_MODE_DECODE else self.lib.bsp_prefill_run_fp8_block
-        _call(dev, stream, fn, ctypes.byref(self.info), _dev(q, "q", self.dtype, dev),
+        info = ctypes.byref(self.info)
+        region = ()
+        if self.mode == N.BSP_MODE_DECODE:
+            fn = self.lib.bsp_decode_run_fp8_block
+        else:
+            fn = self.lib.bsp_prefill_run_fp8_block
+            nbytes = self.lib.bsp_prefill_fp8_region_size(info)
+            copy = None
+            if nbytes:  # a bf16 copy of the plan's pages, for this run alone
+                with torch.cuda.stream(stream):  # (None: the current one)
+                    copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            region = (None if copy is None else copy.data_ptr(), nbytes)
+        _call(dev, stream, fn, info, _dev(q, "q", self.dtype, dev),
               _dev(k_pages, "k_pages", f8, dev), _dev(v_pages, "v_pages", f8, dev), _dev(k_exp, "k_exp", i8, dev),
               _dev(v_exp, "v_exp", i8, dev),
               _dev(kv_indices, "kv_indices", torch.int32, dev) if kv_indices.numel() else None, want[0], sm_scale,
-              _dev(out, "out", self.dtype, dev), None if lse is None else _dev(lse, "lse", torch.float32, dev),
+              _dev(out, "out", self.dtype, dev), None if lse is None else _dev(lse, "lse", torch.float32, dev), *region,
               self.workspace.data_ptr())
         return (out, lse) if return_lse else out
 

@@ -1,5 +1,6 @@
 // C-ABI entry points of libbsp.so other than the planner: argument checks,
 // launch of the run kernels, merge_state, error reporting.
+#include <algorithm>
 #include <climits>
 #include <cstring>
 #include <string>
@@ -114,6 +115,10 @@ extern "C" int bsp_prefill_run(const bsp_plan_info *plan, const void *q, const v
 
 namespace {
 
+// Prefill over the 8-bit cache converts it into a bf16 copy first where at least this
+// many query tiles read a cached token on average.
+constexpr int64_t kRegionTiles = 1;
+
 int check_fp8_block(const bsp_plan_info *plan, int mode, const void *q, const void *k_pages, const void *v_pages,
                     const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
                     const void *o, const void *workspace) {
@@ -139,14 +144,34 @@ extern "C" int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q
                                    workspace, stream);
 }
 
+extern "C" size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan) {
+    clear_error();
+    if (!plan || plan->problem.mode != BSP_MODE_PREFILL || plan->num_table_pages <= 0) return 0;
+    const int64_t tokens = (int64_t)plan->num_table_pages * plan->problem.page_size;
+    if (tokens > INT32_MAX) return 0;
+    // query tiles that read a cached token, on average
+    if (plan->total_work < kRegionTiles * tokens * plan->problem.num_kv_heads) return 0;
+    return (size_t)tokens * plan->problem.num_kv_heads * 512;
+}
+
 extern "C" int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages,
                                          const void *v_pages, const int8_t *k_exp, const int8_t *v_exp,
                                          const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o,
-                                         float *lse, void *workspace, bsp_stream_t stream) {
+                                         float *lse, void *region, size_t region_bytes, void *workspace,
+                                         bsp_stream_t stream) {
     int rc = check_fp8_block(plan, BSP_MODE_PREFILL, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, o, workspace);
     if (rc != BSP_OK) return rc;
+    int64_t pages = 0;
+    if (region) {
+        if (reinterpret_cast<uintptr_t>(region) % 32 != 0)
+            return fail(BSP_ERR_INVALID_ARG, "the region is not 32-byte aligned");
+        const size_t per_page = (size_t)plan->problem.page_size * plan->problem.num_kv_heads * 512;  // bf16 K and V
+        pages = (int64_t)std::min<size_t>(region_bytes / per_page, (size_t)(INT32_MAX / plan->problem.page_size));
+        if (pages < plan->num_table_pages) return fail(BSP_ERR_CAPACITY, "the region is too small for the plan's page table");
+        if (pages == 0) region = nullptr;
+    }
     rc = launch_prefill_fp8_block(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse,
-                                  workspace, stream);
+                                  region, pages, workspace, stream);
     if (rc != BSP_OK) return rc;
     return launch_reduce(plan, o, lse, workspace, stream);
 }

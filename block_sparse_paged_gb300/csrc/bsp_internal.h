@@ -26,7 +26,8 @@ struct DevHeader {
     int32_t group;
     int32_t num_ctas;
     int32_t chunk_len;
-    int32_t reserved[9];
+    int32_t num_table_pages;
+    int32_t reserved[8];
 };
 static_assert(sizeof(DevHeader) == 64, "DevHeader is 64 bytes");
 static_assert(sizeof(bsp_work_item) == 64, "bsp_work_item is 64 bytes");
@@ -86,9 +87,11 @@ int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages
 int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                             const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
                             float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream);
+// region (or NULL): bf16 K copy, then V copy, of region_pages pages each.
 int launch_prefill_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                              const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
-                             float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream);
+                             float sm_scale, void *o, float *lse, void *region, int64_t region_pages, void *workspace,
+                             cudaStream_t stream);
 // Copy the page table's first n_pages pages of K and V, in table order, into
 // the plan's gather region (prefill with a region); ids outside [0, num_pages)
 // give zero pages and set the workspace status word.

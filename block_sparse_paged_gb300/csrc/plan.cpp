@@ -339,6 +339,7 @@ extern "C" int bsp_plan(const bsp_problem *problem, const bsp_capacity *capacity
     hdr.group = g;
     hdr.num_ctas = C;
     hdr.chunk_len = (int32_t)Lc;
+    hdr.num_table_pages = kv_indptr_h[batch];
     std::memcpy(st + lay.off_header, &hdr, sizeof(hdr));
     int32_t *qptr = reinterpret_cast<int32_t *>(st + lay.off_queue_indptr);
     bsp_work_item *items = reinterpret_cast<bsp_work_item *>(st + lay.off_items);

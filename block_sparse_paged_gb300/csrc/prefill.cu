@@ -821,6 +821,67 @@ __global__ void __launch_bounds__(256) gather_pages_kernel(const uint4 *__restri
     }
 }
 
+// The page table's pages of an e4m3 cache into a bf16 copy, in table order (the
+// gather region's layout): one warp per (page, K or V, piece of 256 16-byte
+// vectors), 8 loads of 16 codes per lane in flight, 32-byte stores. HBM-bound: one
+// byte read and two written per value. The number of table pages is the current
+// plan's (read from the workspace, so that a captured launch follows later plans);
+// pages beyond the region are not copied and set the status word.
+constexpr int kStatusRegion = 0x303;
+constexpr int kCvtVecs = 256;  // 16-byte vectors of codes per warp and turn
+
+__device__ __forceinline__ void st_global_v8(void *p, uint2 a, uint2 b, uint2 c, uint2 d) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(a.x), "r"(a.y), "r"(b.x),
+                 "r"(b.y), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(256) convert_pages_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
+                                                            const int8_t *__restrict__ ke,
+                                                            const int8_t *__restrict__ ve, uint8_t *__restrict__ gk,
+                                                            uint8_t *__restrict__ gv, const int32_t *__restrict__ idx,
+                                                            const DevHeader *__restrict__ hdr, int region_pages,
+                                                            int num_pages, int page_vecs, int H, int *status) {
+    const int lane = threadIdx.x & 31;
+    const int warp0 = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5), nwarps = (int)((gridDim.x * blockDim.x) >> 5);
+    const int n = min(hdr->num_table_pages, region_pages);
+    if (hdr->num_table_pages > region_pages && warp0 == 0 && lane == 0) atomicCAS(status, 0, kStatusRegion);
+    const int per_page = (page_vecs + kCvtVecs - 1) / kCvtVecs;
+    const long long tasks = 2ll * n * per_page;
+    for (long long task = warp0; task < tasks; task += nwarps) {
+        const long long pw = task / per_page;
+        const int base = (int)(task - pw * per_page) * kCvtVecs;
+        const int pg = (int)(pw >> 1);
+        const bool is_v = pw & 1;
+        const int id = __ldg(idx + pg);
+        const bool in = id >= 0 && id < num_pages;
+        if (!in && lane == 0) atomicCAS(status, 0, kStatusPageIndex);
+        const uint4 *src = (is_v ? v : k) + (in ? (long long)id * page_vecs : 0);
+        const int8_t *ex = (is_v ? ve : ke) + (in ? (long long)id * H : 0);
+        uint8_t *dst = (is_v ? gv : gk) + (long long)pg * page_vecs * 32;
+        uint4 x[kCvtVecs / 32];
+        int e[kCvtVecs / 32];
+#pragma unroll
+        for (int i = 0; i < kCvtVecs / 32; ++i) {
+            const int u = base + i * 32 + lane;
+            x[i] = make_uint4(0, 0, 0, 0);
+            e[i] = 0;
+            if (in && u < page_vecs) {
+                x[i] = __ldg(src + u);
+                e[i] = __ldg(ex + (u >> 3) % H);  // 8 vectors per (token, head) row
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kCvtVecs / 32; ++i) {
+            const int u = base + i * 32 + lane;
+            const float s = __int_as_float(e[i] >= -126 ? (e[i] + 127) << 23 : 0x00400000 >> (-127 - e[i]));
+            if (u < page_vecs)
+                st_global_v8(dst + (long long)u * 32, e4m3x4_to_bf16x4(x[i].x, s), e4m3x4_to_bf16x4(x[i].y, s),
+                             e4m3x4_to_bf16x4(x[i].z, s), e4m3x4_to_bf16x4(x[i].w, s));
+        }
+    }
+}
+
 }  // namespace
 
 int launch_gather_pages(const bsp_plan_info *plan, const void *k_pages, const void *v_pages,
@@ -853,8 +914,10 @@ namespace {
 // Prefill over bf16 pools, or (k_exp, v_exp given) over an e4m3 cache with exponents.
 int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                        const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
-                       float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream) {
-    const bool fp8 = k_exp != nullptr;
+                       float sm_scale, void *o, float *lse, void *region8, int64_t region_pages, void *workspace,
+                       cudaStream_t stream) {
+    const bool copied = region8 != nullptr;                // e4m3 cache, converted into region8 first
+    const bool fp8 = k_exp != nullptr && !copied;          // e4m3 cache, converted inside the kernel
     const bsp_problem &P = plan->problem;
     const int g = plan->group;
     if (P.dtype != BSP_DTYPE_BF16) return fail(BSP_ERR_UNSUPPORTED, "prefill supports bf16 only");
@@ -867,14 +930,14 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
     // table order, and every request's keys are then one contiguous run of
     // rows read by 128-row TMA boxes; otherwise 16-byte cp.async copies.
     const int ps = P.page_size;
-    const bool direct = !fp8 && ps >= 8 && (ps & (ps - 1)) == 0 && num_pages * (int64_t)ps <= INT32_MAX;
-    const bool gather = !fp8 && !direct && plan->off_gather != 0 && plan->num_table_pages <= plan->capacity.max_gather_pages;
-    const bool tma = direct || gather;
+    const bool direct = !fp8 && !copied && ps >= 8 && (ps & (ps - 1)) == 0 && num_pages * (int64_t)ps <= INT32_MAX;
+    const bool gather = !fp8 && !copied && !direct && plan->off_gather != 0 && plan->num_table_pages <= plan->capacity.max_gather_pages;
+    const bool tma = direct || gather || copied;
 
     CUtensorMap tq, tk, tv;
     std::memset(&tk, 0, sizeof(tk));
     std::memset(&tv, 0, sizeof(tv));
-    const int box_rows = gather ? kKvTile : tma ? (ps < kKvTile ? ps : kKvTile) : 1;
+    const int box_rows = gather || copied ? kKvTile : tma ? (ps < kKvTile ? ps : kKvTile) : 1;
     int rc = make_tmap_bf16(&tq, q, kD, P.num_qo_heads, (uint64_t)(plan->num_qo_tokens > 0 ? plan->num_qo_tokens : 1), g,
                       kRows / g);
     if (gather) {
@@ -883,6 +946,28 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
         if (rc == BSP_OK) rc = make_tmap_bf16(&tk, region, kD, P.num_kv_heads, rows, 1, box_rows);
         if (rc == BSP_OK) rc = make_tmap_bf16(&tv, region + plan->gather_pool_bytes, kD, P.num_kv_heads, rows, 1, box_rows);
         if (rc == BSP_OK) rc = launch_gather_pages(plan, k_pages, v_pages, kv_indices, num_pages, workspace, stream);
+    } else if (copied) {
+        const uint64_t rows = (uint64_t)region_pages * ps;
+        const int64_t pool = (int64_t)rows * P.num_kv_heads * kD * 2;  // bytes of one bf16 copy
+        uint8_t *gk = static_cast<uint8_t *>(region8), *gv = gk + pool;
+        if (rc == BSP_OK) rc = make_tmap_bf16(&tk, gk, kD, P.num_kv_heads, rows, 1, box_rows);
+        if (rc == BSP_OK) rc = make_tmap_bf16(&tv, gv, kD, P.num_kv_heads, rows, 1, box_rows);
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return fail(BSP_ERR_CUDA, "no current CUDA device");
+        if (rc == BSP_OK) {
+            const int64_t vecs = (int64_t)ps * P.num_kv_heads * kD / 16;
+            const int64_t tasks = 2 * region_pages * ((vecs + kCvtVecs - 1) / kCvtVecs);
+            uint8_t *ws = static_cast<uint8_t *>(workspace);
+            convert_pages_kernel<<<(unsigned)std::max<int64_t>(1, std::min<int64_t>((tasks + 7) / 8, (int64_t)sms * 8)), 256,
+                                   0, stream>>>(
+                static_cast<const uint4 *>(k_pages), static_cast<const uint4 *>(v_pages), k_exp, v_exp, gk, gv, kv_indices,
+                reinterpret_cast<const DevHeader *>(ws + plan->off_header), (int)region_pages, (int)num_pages, (int)vecs,
+                P.num_kv_heads, reinterpret_cast<int *>(ws + plan->off_status));
+            cudaError_t e = cudaGetLastError();
+            if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("convert launch: ") + cudaGetErrorString(e));
+        }
     } else if (tma) {
         if (rc == BSP_OK) rc = make_tmap_bf16(&tk, k_pages, kD, P.num_kv_heads, (uint64_t)num_pages * ps, 1, box_rows);
         if (rc == BSP_OK) rc = make_tmap_bf16(&tv, v_pages, kD, P.num_kv_heads, (uint64_t)num_pages * ps, 1, box_rows);
@@ -915,7 +1000,7 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
     p.g = g;
     p.page_size = P.page_size;
     p.box_rows = box_rows;
-    p.contig = gather ? 1 : 0;
+    p.contig = gather || copied ? 1 : 0;
     p.causal = P.causal;
     p.tile_rows = plan->tile_rows;
 
@@ -951,14 +1036,15 @@ int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages
                    const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o, float *lse,
                    void *workspace, cudaStream_t stream) {
     return launch_prefill_any(plan, q, k_pages, v_pages, nullptr, nullptr, kv_indices, num_pages, sm_scale, o, lse,
-                              workspace, stream);
+                              nullptr, 0, workspace, stream);
 }
 
 int launch_prefill_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                              const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
-                             float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream) {
-    return launch_prefill_any(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse,
-                              workspace, stream);
+                             float sm_scale, void *o, float *lse, void *region, int64_t region_pages, void *workspace,
+                             cudaStream_t stream) {
+    return launch_prefill_any(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse, region,
+                              region_pages, workspace, stream);
 }
 
 }  // namespace bsp

@@ -466,9 +466,15 @@ int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int6
  *   k_exp, v_exp       device, int8 [num_pages, H_kv]
  *   num_pages          pages in each pool, 1 .. 2^31 - 1
  * Any page size. Decode: g <= 16; scores and sums fp32, token weights times
- * 2^v_exp in f16 against their own running maximum. Prefill: codes converted to
- * bf16 (exact for exponents in [-117, 119]) on their way to the tensor cores;
- * 128 % g == 0. A page id outside [0, num_pages) reads as zero codes and sets the
+ * 2^v_exp in f16 against their own running maximum. Prefill: 128 % g == 0; codes are
+ * converted to bf16 (exact for exponents in [-117, 119]), either on their way to
+ * the tensor cores (region NULL) or, once for all query tiles, into a copy in
+ *   region             device scratch, 32-byte aligned, region_bytes >=
+ *                      num_table_pages * page_size * H_kv * 512 (else
+ *                      BSP_ERR_CAPACITY); contents undefined before and after.
+ * bsp_prefill_fp8_region_size tells which is faster. A captured run replayed after
+ * a plan with a larger page table than its region holds sets the status word
+ * (0x303). A page id outside [0, num_pages) reads as zero codes and sets the
  * workspace status word (0x302, bsp_check_device_error).
  */
 int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
@@ -476,7 +482,13 @@ int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q, const voi
                              float sm_scale, void *o, float *lse, void *workspace, bsp_stream_t stream);
 int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                               const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
-                              float sm_scale, void *o, float *lse, void *workspace, bsp_stream_t stream);
+                              float sm_scale, void *o, float *lse, void *region, size_t region_bytes,
+                              void *workspace, bsp_stream_t stream);
+
+/* Bytes of the region that bsp_prefill_run_fp8_block wants for this plan (a bf16
+ * copy of its page table's K and V), or 0 where few query tiles read each cached
+ * token and converting inside the attention kernel is faster. */
+size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan);
 
 /*
  * Decode run without any device allocation by the caller or the library.

@@ -12,6 +12,7 @@ prefill; A = sum_j p_j |v_j|, from the oracle):
   by 2^-25 of the largest (at most 448 / |code| of it in a dimension: taken as 2^-25
   n_keys against the row's largest A, times 448), and half a bf16 step of O itself.
 """
+import ctypes
 import math
 
 import numpy as np
@@ -142,6 +143,67 @@ def test_prefill(bsp, case):
     out, lse, pa = run_block(bsp, b, c8, num_ctas=C, repeats=2)
     check(out, lse, reference(b, c8), 2.0 ** -8, b)
     assert pa.check_device_error() == 0
+
+
+@pytest.mark.parametrize("case", PREFILL, ids=[f"p{c[0]}" for c in PREFILL])
+def test_prefill_converted_before_and_inside_the_kernel(bsp, case):
+    """The C entry with a region (larger than needed, full of NaN) and without one: the same tiles, the same bits."""
+    seed, qo, kv, hq, hk, ps, C, w, cap = case
+    b = workloads.paged_batch(seed, qo, kv, hq, hk, 128, ps, "bf16", causal=True, extra_pages=2)
+    b.window_left, b.soft_cap = w, cap
+    c8 = cache8(b, seed, ke=(-20, -5), ve=(-12, 3))
+    pa = bsp.PagedAttention("prefill", hq, hk, 128, ps, True, torch.bfloat16, max_batch=b.batch,
+                            max_qo_tokens=int(b.qo_indptr[-1]), num_ctas=C, window_left=w, logits_soft_cap=cap)
+    pa.plan(b.kv_indptr, b.last_page_len, qo_indptr=b.qo_indptr)
+    k8, ke, v8, ve = (torch.from_numpy(a).cuda() for a in c8)
+    idx = torch.from_numpy(np.ascontiguousarray(b.kv_indices, np.int32)).cuda()
+    q = b.q.cuda()
+    got = []
+    for pages in (0, len(b.kv_indices), len(b.kv_indices) + 7):
+        region = torch.full((pages * ps * hk * 256,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        o, l = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        rc = pa.lib.bsp_prefill_run_fp8_block(
+            ctypes.byref(pa.info), q.data_ptr(), k8.data_ptr(), v8.data_ptr(), ke.data_ptr(), ve.data_ptr(), idx.data_ptr(),
+            k8.shape[0], b.sm_scale, o.data_ptr(), l.data_ptr(), region.data_ptr() if pages else None, region.numel() * 2,
+            pa.workspace.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert pa.check_device_error() == 0
+        got.append((o, l))
+    check(*got[0], reference(b, c8), 2.0 ** -8, b)
+    for o, l in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
+
+
+def test_region_too_small_for_a_later_plan(bsp):
+    """A captured run whose region holds the captured plan's pages, replayed after a plan with more: the status word."""
+    a = workloads.paged_batch(240, [300], [300], 8, 2, 128, 16, "bf16", causal=True)
+    b = workloads.paged_batch(241, [300], [900], 8, 2, 128, 16, "bf16", causal=True)
+    pa = bsp.PagedAttention("prefill", 8, 2, 128, 16, True, torch.bfloat16, max_batch=1, max_qo_tokens=300)
+    k8, ke, v8, ve = (torch.from_numpy(x).cuda() for x in cache8(b, 241))
+    f8 = torch.float8_e4m3fn
+    idx = torch.arange(60, dtype=torch.int32, device="cuda")
+    q = a.q.cuda()
+    o, l = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+
+    def run():
+        pa.run(q, k8.view(f8), v8.view(f8), idx, out=o, lse=l, k_exp=ke, v_exp=ve)
+    pa.plan(a.kv_indptr, a.last_page_len, qo_indptr=a.qo_indptr)
+    assert pa.lib.bsp_prefill_fp8_region_size(ctypes.byref(pa.info)) > 0
+    run()
+    torch.cuda.synchronize()
+    want = o.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    g.replay()
+    assert pa.check_device_error() == 0 and torch.equal(o, want)
+    pa.plan(b.kv_indptr, b.last_page_len, qo_indptr=b.qo_indptr)
+    g.replay()
+    assert pa.check_device_error() == 0x303
+    pa.plan(a.kv_indptr, a.last_page_len, qo_indptr=a.qo_indptr)
+    g.replay()
+    assert pa.check_device_error() == 0 and torch.equal(o, want)
 
 
 @pytest.mark.parametrize("kind", ["decode", "prefill"])

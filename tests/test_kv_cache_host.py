@@ -145,7 +145,10 @@ def block_plan(mode, H=8, Hkv=2, D=128, dtype=None):
 def run_args(info, **kw):
     d = dict(q=A, k=A, v=A, ke=A, ve=A, idx=A, pages=4, scale=0.1, o=A, lse=None, ws=A)
     d.update(kw)
-    return [ctypes.byref(info)] + list(d.values()) + [None]
+    a = [ctypes.byref(info)] + list(d.values()) + [None]
+    if info.problem.mode == 1:  # no region
+        a[-2:-2] = [None, 0]
+    return a
 
 
 @pytest.mark.parametrize("mode", [0, 1])
@@ -163,10 +166,31 @@ def test_block_runs_refuse_plans(native, mode):
     import torch
     lib = native.load()
     fn = lib.bsp_decode_run_fp8_block if mode == 0 else lib.bsp_prefill_run_fp8_block
-    assert fn(*run_args(block_plan(1 - mode))) == native.BSP_ERR_INVALID_ARG      # the other mode's plan
+    other = block_plan(mode)
+    other.problem.mode = 1 - mode
+    args = run_args(block_plan(mode))
+    assert fn(ctypes.byref(other), *args[1:]) == native.BSP_ERR_INVALID_ARG       # the other mode's plan
     host = block_plan(mode)
     host.valid = 2
     assert fn(*run_args(host)) == native.BSP_ERR_INVALID_ARG                      # a host-only plan
     if mode == 0:
         assert fn(*run_args(block_plan(0, D=64))) == native.BSP_ERR_UNSUPPORTED
         assert fn(*run_args(block_plan(0, dtype=torch.float32))) == native.BSP_ERR_UNSUPPORTED
+
+
+def test_region_size_and_refusals(native):
+    """A region is wanted where query tiles read every cached token, and must hold the page table."""
+    lib = native.load()
+    info = block_plan(1, H=8, Hkv=2)
+    assert lib.bsp_prefill_fp8_region_size(ctypes.byref(info)) in (0, 3 * 16 * 2 * 512)
+    import torch
+    import block_sparse_paged_gb300 as bsp
+    prob = bsp.make_problem(1, 8, 2, 128, 16, True, torch.bfloat16)
+    big = bsp.plan_host(prob, bsp.Capacity(2, 4, 900, 1, 0, 0), [0, 32], [16], [0, 512])[0]
+    assert lib.bsp_prefill_fp8_region_size(ctypes.byref(big)) == 512 * 2 * 512    # tokens x heads x 4 bytes x 128
+    big.valid = 1
+    for region, nbytes, rc in ((A, 512 * 2 * 512 - 1, native.BSP_ERR_CAPACITY), (A + 16, 1 << 30, native.BSP_ERR_INVALID_ARG)):
+        a = run_args(big)
+        a[-4:-2] = [region, nbytes]
+        assert lib.bsp_prefill_run_fp8_block(*a) == rc
+    assert lib.bsp_prefill_fp8_region_size(ctypes.byref(block_plan(0))) == 0
