@@ -247,11 +247,11 @@ class PagedAttention:
                 with torch.cuda.stream(stream):  # (None: the current one)
                     copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             region = (None if copy is None else copy.data_ptr(), nbytes)
-        _call(dev, stream, fn, info, _dev(q, "q", self.dtype, dev),
-              _dev(k_pages, "k_pages", f8, dev), _dev(v_pages, "v_pages", f8, dev), _dev(k_exp, "k_exp", i8, dev),
-              _dev(v_exp, "v_exp", i8, dev),
-              _dev(kv_indices, "kv_indices", torch.int32, dev) if kv_indices.numel() else None, want[0], sm_scale,
-              _dev(out, "out", self.dtype, dev), None if lse is None else _dev(lse, "lse", torch.float32, dev), *region,
+        _call(dev, stream, fn, info, _addr(q, "q", self.dtype, dev),
+              _addr(k_pages, "k_pages", f8, dev), _addr(v_pages, "v_pages", f8, dev), _addr(k_exp, "k_exp", i8, dev),
+              _addr(v_exp, "v_exp", i8, dev),
+              _addr(kv_indices, "kv_indices", torch.int32, dev) if kv_indices.numel() else None, want[0], sm_scale,
+              _addr(out, "out", self.dtype, dev), None if lse is None else _addr(lse, "lse", torch.float32, dev), *region,
               self.workspace.data_ptr())
         return (out, lse) if return_lse else out
 
@@ -322,13 +322,24 @@ def merge_state(o_a: torch.Tensor, lse_a: torch.Tensor, o_b: torch.Tensor, lse_b
     return out, lse_out
 
 
+def _addr(t: torch.Tensor, name: str, dtype, dev: torch.device) -> int:
+    """Address of a contiguous tensor of `dtype` on `dev`; _dev's errors otherwise (short calls: checked once, in the
+    order of what is cheap to ask)."""
+    if t.dtype is dtype and t.is_contiguous() and t.device == dev:
+        return t.data_ptr()
+    return _dev(t, name, dtype, dev).value
+
+
 def _call(dev: torch.device, stream, fn, *args):
     """fn(*args, stream handle) with `dev` current, on `stream` or dev's current stream."""
+    handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            N.check(fn(*args, _stream_handle(stream)))
+            rc = fn(*args, handle)
     else:
-        N.check(fn(*args, _stream_handle(stream)))
+        rc = fn(*args, handle)
+    if rc != N.BSP_OK:
+        N.check(rc)
 
 
 class PageTables(NamedTuple):
@@ -349,8 +360,10 @@ class PageTables(NamedTuple):
         """Buffers for `batch` requests, to be passed as `out` every step."""
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         sizes = (batch + 1, batch, max_table_pages, batch + 1, max_new_tokens, max_new_tokens, 4)
-        return cls(*(torch.empty(n, dtype=torch.int64 if f == "slot_map" else torch.int32, device=dev)
-                     for f, n in zip(cls._fields, sizes)))
+        return cls(*(torch.empty(n, dtype=d, device=dev) for d, n in zip(_TABLE_DTYPES, sizes)))
+
+
+_TABLE_DTYPES = tuple(torch.int64 if f == "slot_map" else torch.int32 for f in PageTables._fields)
 
 
 def build_page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
@@ -379,15 +392,15 @@ def build_page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pa
     if out is None:
         out = PageTables.empty(B, max_table_pages, max_new_tokens, dev)
     sizes = (B + 1, B, max_table_pages, B + 1, max_new_tokens, max_new_tokens, 4)
-    for t, n, f in zip(out, sizes, PageTables._fields):
-        if t.shape != (n,):
-            raise ValueError(f"out.{f} must be [{n}]")
     i32 = torch.int32
-    o = [_dev(t, f, torch.int64 if f == "slot_map" else i32, dev) for t, f in zip(out, PageTables._fields)]
+    o = [_addr(t, f, d, dev) for t, f, d in zip(out, PageTables._fields, _TABLE_DTYPES)]
+    for t, n, f in zip(out, sizes, PageTables._fields):
+        if t.numel() != n or t.dim() != 1:
+            raise ValueError(f"out.{f} must be [{n}]")
     stride = block_table.stride(0) if B > 1 else max(width, block_table.stride(0))
-    _call(dev, stream, N.load().bsp_build_page_tables, B, page_size, _dev(cached_lens, "cached_lens", i32, dev),
-          _dev(new_lens, "new_lens", i32, dev), _dev(free_pages, "free_pages", i32, dev), free_pages.numel(),
-          _dev(num_free, "num_free", i32, dev), block_table.data_ptr(), stride, width, o[0], o[1], o[2],
+    _call(dev, stream, N.load().bsp_build_page_tables, B, page_size, _addr(cached_lens, "cached_lens", i32, dev),
+          _addr(new_lens, "new_lens", i32, dev), _addr(free_pages, "free_pages", i32, dev), free_pages.numel(),
+          _addr(num_free, "num_free", i32, dev), block_table.data_ptr(), stride, width, o[0], o[1], o[2],
           max_table_pages, o[3], o[4], o[5], max_new_tokens, o[6])
     return out
 
@@ -420,5 +433,5 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pages:
     # a dimension of size 1 is never stepped over: its stride says nothing
     st = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in (0, 1)]
     _call(dev, stream, N.load().bsp_append_kv_fp8, k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], st[3],
-          _DTYPES[k.dtype], n, _dev(slot_map, "slot_map", torch.int64, dev), _dev(k_pages, "k_pages", f8, dev),
-          _dev(v_pages, "v_pages", f8, dev), _dev(k_exp, "k_exp", i8, dev), _dev(v_exp, "v_exp", i8, dev), P, ps, H, D)
+          _DTYPES[k.dtype], n, _addr(slot_map, "slot_map", torch.int64, dev), _addr(k_pages, "k_pages", f8, dev),
+          _addr(v_pages, "v_pages", f8, dev), _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev), P, ps, H, D)

@@ -262,8 +262,8 @@ extern "C" int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_s
     if (head_dim != 128) return fail(BSP_ERR_UNSUPPORTED, "the e4m3 cache has head_dim 128");
     if (n_tokens < 0 || num_pages < 1 || num_pages > INT32_MAX || page_size < 1 || num_kv_heads < 1)
         return fail(BSP_ERR_INVALID_ARG, "bad append sizes");
-    if (num_kv_heads > 32767 || n_tokens > (int64_t{1} << 37))
-        return fail(BSP_ERR_UNSUPPORTED, "append takes at most 32767 kv heads and 2^37 tokens");
+    if (num_kv_heads > 32767 || n_tokens > INT32_MAX)
+        return fail(BSP_ERR_UNSUPPORTED, "append takes at most 32767 kv heads and 2^31 - 1 tokens");
     if (n_tokens == 0) return BSP_OK;
     if (!k || !v || !slot_map || !k_pages || !v_pages || !k_exp || !v_exp)
         return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");

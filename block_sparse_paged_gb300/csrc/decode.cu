@@ -440,6 +440,26 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                 }
             };
             if (nt > 0) fetch(0, pg);
+            // kBlk: page ids two stages ahead, exponents one: neither latency stands between
+            // a stage's copies and its arrival
+            int pg2[kJ], ex[kJ], ex2[kJ];
+            auto fetch_exp = [&](int t, const int (&ids)[kJ], int (&dst)[kJ]) {
+#pragma unroll
+                for (int jj = 0; jj < kJ; ++jj) {
+                    const bool in = t * kTK + tok_base + lane + 32 * jj < len && ids[jj] >= 0 && ids[jj] < p.num_pages;
+                    dst[jj] = in ? __ldg((is_v ? p.v_exp : p.k_exp) + (size_t)ids[jj] * p.H_kv + w.kv_head) : 0;
+                }
+            };
+            if constexpr (kBlk) {
+#pragma unroll
+                for (int jj = 0; jj < kJ; ++jj) pg2[jj] = 0;
+                if (nt > 1) fetch(1, pg2);
+                if (nt > 0) fetch_exp(0, pg, ex2);
+            }
+            (void)pg2;
+            (void)ex;
+            (void)ex2;
+            (void)fetch_exp;
             for (int t = 0; t < nt; ++t, ++k) {
                 // byte offsets of this lane's two rows, then the next tile's page ids
                 uint64_t off[kJ];
@@ -448,21 +468,21 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                     const int tok = w.kv_start + t * kTK + tok_base + lane + 32 * jj;
                     off[jj] = (((uint64_t)pg[jj] * p.page_size + tok % p.page_size) * p.H_kv + w.kv_head) * (D * LY::kElem);
                 }
-                int ex[kJ];
                 if constexpr (kBlk) {
 #pragma unroll
                     for (int jj = 0; jj < kJ; ++jj) {
-                        const bool live = t * kTK + tok_base + lane + 32 * jj < len;
-                        const bool in = pg[jj] >= 0 && pg[jj] < p.num_pages;
-                        ex[jj] = live && in ? __ldg((is_v ? p.v_exp : p.k_exp) + (size_t)pg[jj] * p.H_kv + w.kv_head) : 0;
-                        if (live && !in) {
+                        if (t * kTK + tok_base + lane + 32 * jj < len && (pg[jj] < 0 || pg[jj] >= p.num_pages)) {
                             off[jj] = kBadRow;  // copied as zeros
                             atomicCAS(status, 0, kStatusPageIndex);
                         }
+                        ex[jj] = ex2[jj];
+                        pg[jj] = pg2[jj];
                     }
+                    if (t + 1 < nt) fetch_exp(t + 1, pg, ex2);
+                    if (t + 2 < nt) fetch(t + 2, pg2);
+                } else {
+                    if (t + 1 < nt) fetch(t + 1, pg);
                 }
-                (void)ex;
-                if (t + 1 < nt) fetch(t + 1, pg);
                 const int s = k % kStages;
                 const bool ok = wait_or_abort(empty0 + 8 * s, ((k / kStages) & 1) ^ 1, abort_flag, status,
                                               kStatusProducerWait);
@@ -555,7 +575,165 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                 for (int dt = 0; dt < D / 16; ++dt) oacc[dt][nh][0] = oacc[dt][nh][1] = oacc[dt][nh][2] = oacc[dt][nh][3] = 0.f;
             }
 
-            for (int t = 0; t < nt; ++t, ++k) {
+            if constexpr (kBlk) {
+                // Block exponents: a warp takes all its sub-blocks of a stage together (one
+                // maximum and one rescale per stage, their score products independent).
+                constexpr int kSB = LY::kSubB;
+                for (int t = 0; t < nt; ++t, ++k) {
+                    const int s = k % kStages;
+                    const bool ok = wait_or_abort(full0 + 8 * s, (k / kStages) & 1, abort_flag, status, kStatusConsumerWait);
+                    if (!__all_sync(0xffffffffu, ok)) return;
+                    const int left = min(kTK, len - t * kTK);
+                    if (left <= warp * 16) {  // no token of this warp
+                        __syncwarp();
+                        if (lane == 0) sm100::mbar_arrive(empty0 + 8 * s);
+                        continue;
+                    }
+                    const int lo_stage = p.window_left > 0
+                                             ? w.pos0 + w.kv_len - w.qo_len - p.window_left - (w.kv_start + t * kTK)
+                                             : INT_MIN;
+                    const uint32_t kb = sbase + s * LY::kStageBytes, vb = kb + LY::kTileBytes;
+                    const int8_t *ek = reinterpret_cast<const int8_t *>(smem) + LY::kExpOff + s * 2 * LY::kExpN;
+                    float sv[kSB][kNH][4], so[kSB][kNH][4];
+#pragma unroll
+                    for (int sb = 0; sb < kSB; ++sb) {
+                        const int row0 = (sb * kConsumers + warp) * 16;
+                        // K rows r, r + 8 (dims 64h + 16c .. + 15)
+                        uint4 kw[2][2];
+#pragma unroll
+                        for (int t2 = 0; t2 < 2; ++t2)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int R = row0 + 8 * t2 + qn;
+                                kw[t2][h] = sm100::ld_shared_v4(kb + R * 128 + (((4 * h + c) ^ (R & 7)) << 4));
+                            }
+                        // factors of this lane's tokens qn and qn + 8: 2^e_k on the score, e_v on its weight
+                        float kf[2], ve[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int at = kTma ? row0 / 8 + i : row0 + 8 * i + qn;
+                            const int e = ek[at];
+                            kf[i] = __int_as_float(e >= -126 ? (e + 127) << 23 : 0x00400000 >> (-127 - e)) *
+                                    (p.soft_cap_on ? p.cap_in : p.scale_log2);
+                            ve[i] = (float)ek[LY::kExpN + at];
+                        }
+                        float st[kNH][2][4];  // two accumulators per head tile (even / odd kk) to halve the chain
+#pragma unroll
+                        for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) st[nh][e][0] = st[nh][e][1] = st[nh][e][2] = st[nh][e][3] = 0.f;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const int h = kk >> 2, j = kk & 3;
+                            const uint32_t w0 = j == 0 ? kw[0][h].x : j == 1 ? kw[0][h].y : j == 2 ? kw[0][h].z : kw[0][h].w;
+                            const uint32_t w1 = j == 0 ? kw[1][h].x : j == 1 ? kw[1][h].y : j == 2 ? kw[1][h].z : kw[1][h].w;
+                            uint32_t a[4];  // rows r, r + 8 x dims {0, 1}, then {2, 3}
+                            e4m3x4_to_f16x4(w0, a[0], a[2]);
+                            e4m3x4_to_f16x4(w1, a[1], a[3]);
+#pragma unroll
+                            for (int nh = 0; nh < kNH; ++nh) mma_f16_16816(st[nh][kk & 1], a, qf[kk][nh][0], qf[kk][nh][1]);
+                        }
+#pragma unroll
+                        for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int tk = row0 + qn + 8 * (e >> 1);
+                                float x = (st[nh][0][e] + st[nh][1][e]) * kf[e >> 1];
+                                if (p.soft_cap_on) x = tanh_ex2(x) * p.cap_out;
+                                sv[sb][nh][e] = (tk < left && tk >= lo_stage) ? x : -INFINITY;
+                                so[sb][nh][e] = sv[sb][nh][e] + ve[e >> 1];
+                            }
+                    }
+                    uint32_t pb[kSB][kNH][2];
+#pragma unroll
+                    for (int nh = 0; nh < kNH; ++nh) {
+                        float mx0 = -INFINITY, mx1 = -INFINITY, my0 = -INFINITY, my1 = -INFINITY;
+#pragma unroll
+                        for (int sb = 0; sb < kSB; ++sb) {
+                            mx0 = fmaxf(mx0, fmaxf(sv[sb][nh][0], sv[sb][nh][2]));
+                            mx1 = fmaxf(mx1, fmaxf(sv[sb][nh][1], sv[sb][nh][3]));
+                            my0 = fmaxf(my0, fmaxf(so[sb][nh][0], so[sb][nh][2]));
+                            my1 = fmaxf(my1, fmaxf(so[sb][nh][1], so[sb][nh][3]));
+                        }
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) {
+                            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                            my0 = fmaxf(my0, __shfl_xor_sync(0xffffffffu, my0, o));
+                            my1 = fmaxf(my1, __shfl_xor_sync(0xffffffffu, my1, o));
+                        }
+                        const float n0 = fmaxf(mh[nh][0], mx0), n1 = fmaxf(mh[nh][1], mx1);
+                        const float q0 = fmaxf(oh[nh][0], my0), q1 = fmaxf(oh[nh][1], my1);
+                        const float ref0 = n0 == -INFINITY ? 0.f : n0, ref1 = n1 == -INFINITY ? 0.f : n1;
+                        const float rq0 = q0 == -INFINITY ? 0.f : q0, rq1 = q1 == -INFINITY ? 0.f : q1;
+                        lh[nh][0] *= ex2_ftz(mh[nh][0] - ref0);
+                        lh[nh][1] *= ex2_ftz(mh[nh][1] - ref1);
+                        const float b0 = ex2_ftz(oh[nh][0] - rq0), b1 = ex2_ftz(oh[nh][1] - rq1);
+                        mh[nh][0] = n0;
+                        mh[nh][1] = n1;
+                        oh[nh][0] = q0;
+                        oh[nh][1] = q1;
+#pragma unroll
+                        for (int sb = 0; sb < kSB; ++sb) {
+                            lh[nh][0] += ex2_ftz(sv[sb][nh][0] - ref0) + ex2_ftz(sv[sb][nh][2] - ref0);
+                            lh[nh][1] += ex2_ftz(sv[sb][nh][1] - ref1) + ex2_ftz(sv[sb][nh][3] - ref1);
+                            // weights (tokens x heads) as two 8 x 8 f16 blocks -> transposed: P^T fragments
+                            pb[sb][nh][0] = movmatrix_trans(
+                                pack_f16_sat(ex2_ftz(so[sb][nh][0] - rq0), ex2_ftz(so[sb][nh][1] - rq1)));
+                            pb[sb][nh][1] = movmatrix_trans(
+                                pack_f16_sat(ex2_ftz(so[sb][nh][2] - rq0), ex2_ftz(so[sb][nh][3] - rq1)));
+                        }
+                        if (__any_sync(0xffffffffu, b0 != 1.f || b1 != 1.f)) {
+#pragma unroll
+                            for (int dt = 0; dt < D / 16; ++dt) {
+                                oacc[dt][nh][0] *= b0; oacc[dt][nh][1] *= b1;
+                                oacc[dt][nh][2] *= b0; oacc[dt][nh][3] *= b1;
+                            }
+                        }
+                    }
+                    // O^T += V^T P^T: V rows 2c, 2c + 1, 2c + 8, 2c + 9 (dims 16r .. + 15), zero past
+                    // the chunk end; word m of the rows feeds dim tiles 2m and 2m + 1
+#pragma unroll
+                    for (int sb = 0; sb < kSB; ++sb) {
+                        const int row0 = (sb * kConsumers + warp) * 16, valid = left - row0;
+                        uint4 vw[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int R = row0 + 2 * c + (i & 1) + 8 * (i >> 1);
+                            vw[i] = sm100::ld_shared_v4(vb + R * 128 + ((qn ^ (R & 7)) << 4));
+                        }
+                        if (sb == kSB - 1) {  // the last loads of the stage
+                            __syncwarp();
+                            if (lane == 0) sm100::mbar_arrive(empty0 + 8 * s);
+                        }
+                        if (valid < 16) {  // the chunk ends inside (or before) this sub-block (warp-uniform)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (2 * c + (i & 1) + 8 * (i >> 1) >= valid) vw[i] = make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const uint32_t va = m == 0 ? vw[0].x : m == 1 ? vw[0].y : m == 2 ? vw[0].z : vw[0].w;
+                            const uint32_t vb2 = m == 0 ? vw[1].x : m == 1 ? vw[1].y : m == 2 ? vw[1].z : vw[1].w;
+                            const uint32_t vc = m == 0 ? vw[2].x : m == 1 ? vw[2].y : m == 2 ? vw[2].z : vw[2].w;
+                            const uint32_t vd = m == 0 ? vw[3].x : m == 1 ? vw[3].y : m == 2 ? vw[3].z : vw[3].w;
+                            const uint32_t lo01 = prmt(va, vb2, 0x5140), lo23 = prmt(va, vb2, 0x7362);
+                            const uint32_t hi01 = prmt(vc, vd, 0x5140), hi23 = prmt(vc, vd, 0x7362);
+                            uint32_t a_e[4], a_o[4];
+                            e4m3x4_to_f16x4(lo01, a_e[0], a_e[1]);
+                            e4m3x4_to_f16x4(hi01, a_e[2], a_e[3]);
+                            e4m3x4_to_f16x4(lo23, a_o[0], a_o[1]);
+                            e4m3x4_to_f16x4(hi23, a_o[2], a_o[3]);
+#pragma unroll
+                            for (int nh = 0; nh < kNH; ++nh) {
+                                mma_f16_16816(oacc[2 * m][nh], a_e, pb[sb][nh][0], pb[sb][nh][1]);
+                                mma_f16_16816(oacc[2 * m + 1][nh], a_o, pb[sb][nh][0], pb[sb][nh][1]);
+                            }
+                        }
+                    }
+                }
+            }
+            for (int t = 0; t < (kBlk ? 0 : nt); ++t, ++k) {
                 const int s = k % kStages;
                 const bool ok = wait_or_abort(full0 + 8 * s, (k / kStages) & 1, abort_flag, status, kStatusConsumerWait);
                 if (!__all_sync(0xffffffffu, ok)) return;
@@ -590,21 +768,6 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                     const int rr = 2 * c + (i & 1) + 8 * (i >> 1), R = row0 + rr;
                     vw[i] = sm100::ld_shared_v4(vb + R * 128 + ((qn ^ (R & 7)) << 4));
                 }
-                // factors of this lane's tokens qn and qn + 8: 2^e_k on the score, e_v on its weight
-                float kf[2], ve[2];
-                if constexpr (kBlk) {
-                    const int8_t *ek = reinterpret_cast<const int8_t *>(smem) + LY::kExpOff + s * 2 * LY::kExpN;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int at = kTma ? row0 / 8 + i : row0 + 8 * i + qn;
-                        const int e = ek[at];
-                        kf[i] = __int_as_float(e >= -126 ? (e + 127) << 23 : 0x00400000 >> (-127 - e)) *
-                                (p.soft_cap_on ? p.cap_in : p.scale_log2);
-                        ve[i] = (float)ek[LY::kExpN + at];
-                    }
-                }
-                (void)kf;
-                (void)ve;
                 if (valid < 16) {  // the chunk ends inside this warp's rows (warp-uniform)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -641,50 +804,10 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                     for (int e = 0; e < 4; ++e) {
                         const float v = st[nh][0][e] + st[nh][1][e];
                         const int tk = qn + 8 * (e >> 1);
-                        float x;
-                        if constexpr (kBlk) {
-                            x = v * kf[e >> 1];
-                            if (p.soft_cap_on) x = tanh_ex2(x) * p.cap_out;
-                        } else {
-                            x = p.soft_cap_on ? tanh_ex2(v * p.cap_in) * p.cap_out : v * p.scale_log2;
-                        }
+                        const float x = p.soft_cap_on ? tanh_ex2(v * p.cap_in) * p.cap_out : v * p.scale_log2;
                         sv[e] = (tk < valid && tk >= lo_rel) ? x : -INFINITY;
                     }
                     float mx0 = fmaxf(sv[0], sv[2]), mx1 = fmaxf(sv[1], sv[3]);
-                    if constexpr (kBlk) {
-                        float so[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) so[e] = sv[e] + ve[e >> 1];
-                        float my0 = fmaxf(so[0], so[2]), my1 = fmaxf(so[1], so[3]);
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) {
-                            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-                            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-                            my0 = fmaxf(my0, __shfl_xor_sync(0xffffffffu, my0, o));
-                            my1 = fmaxf(my1, __shfl_xor_sync(0xffffffffu, my1, o));
-                        }
-                        const float n0 = fmaxf(mh[nh][0], mx0), n1 = fmaxf(mh[nh][1], mx1);
-                        const float q0 = fmaxf(oh[nh][0], my0), q1 = fmaxf(oh[nh][1], my1);
-                        const float ref0 = n0 == -INFINITY ? 0.f : n0, ref1 = n1 == -INFINITY ? 0.f : n1;
-                        const float rq0 = q0 == -INFINITY ? 0.f : q0, rq1 = q1 == -INFINITY ? 0.f : q1;
-                        lh[nh][0] = lh[nh][0] * ex2_ftz(mh[nh][0] - ref0) + (ex2_ftz(sv[0] - ref0) + ex2_ftz(sv[2] - ref0));
-                        lh[nh][1] = lh[nh][1] * ex2_ftz(mh[nh][1] - ref1) + (ex2_ftz(sv[1] - ref1) + ex2_ftz(sv[3] - ref1));
-                        const float b0 = ex2_ftz(oh[nh][0] - rq0), b1 = ex2_ftz(oh[nh][1] - rq1);
-                        mh[nh][0] = n0;
-                        mh[nh][1] = n1;
-                        oh[nh][0] = q0;
-                        oh[nh][1] = q1;
-                        if (__any_sync(0xffffffffu, b0 != 1.f || b1 != 1.f)) {
-#pragma unroll
-                            for (int dt = 0; dt < D / 16; ++dt) {
-                                oacc[dt][nh][0] *= b0; oacc[dt][nh][1] *= b1;
-                                oacc[dt][nh][2] *= b0; oacc[dt][nh][3] *= b1;
-                            }
-                        }
-                        pb[nh][0] = movmatrix_trans(pack_f16_sat(ex2_ftz(so[0] - rq0), ex2_ftz(so[1] - rq1)));
-                        pb[nh][1] = movmatrix_trans(pack_f16_sat(ex2_ftz(so[2] - rq0), ex2_ftz(so[3] - rq1)));
-                        continue;
-                    }
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) {
                         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));

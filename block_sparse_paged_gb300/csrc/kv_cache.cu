@@ -50,11 +50,11 @@ __device__ __forceinline__ TableRow table_row(const TableParams &p, int b) {
     r.flags = (c < 0 || m < 0) ? BSP_TABLES_BAD_LENGTH : 0;
     r.cached = max(c, 0);
     r.fresh = max(m, 0);
-    const long long total = (long long)r.cached + r.fresh;
-    const long long all = (total + p.ps - 1) / p.ps;
-    if (all > p.width) r.flags |= BSP_TABLES_OVER_CAPACITY;
-    r.all_pages = (int)min(all, (long long)p.width);
-    r.old_pages = min((int)(((long long)r.cached + p.ps - 1) / p.ps), r.all_pages);
+    const uint32_t ps = (uint32_t)p.ps, total = (uint32_t)r.cached + (uint32_t)r.fresh;  // at most 2^32 - 2
+    const uint32_t all = total ? (total - 1) / ps + 1 : 0;
+    if (all > (uint32_t)p.width) r.flags |= BSP_TABLES_OVER_CAPACITY;
+    r.all_pages = (int)min(all, (uint32_t)p.width);
+    r.old_pages = min((int)(r.cached ? ((uint32_t)r.cached - 1) / ps + 1 : 0), r.all_pages);
     return r;
 }
 
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     __shared__ int s_flags;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s_flags = 0;
+    const int n_free = (int)max(0ll, min((long long)__ldg(p.num_free), p.free_capacity));
     __syncthreads();
 
     // exclusive sums in 64 bits, kept saturated to int32 (an output that needs more
@@ -124,7 +125,6 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     }
     __syncthreads();
     const int n_pages = s_pages[B], n_tok = s_tok[B];
-    const int n_free = (int)max(0ll, min((long long)__ldg(p.num_free), p.free_capacity));
 
     if (blockIdx.x == 0) {
         for (int b = tid; b <= B; b += kTabThreads) {
@@ -154,42 +154,46 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
         return k < n_free ? __ldg(p.free_pages + k) : -1;
     };
 
-    const long long gsize = (long long)gridDim.x * kTabThreads * kTabUnit;
-    const long long g0 = ((long long)blockIdx.x * kTabThreads + tid) * kTabUnit;
-    // table entries: CSR copy of every row, new entries also into the row; the CSR
-    // tail up to its capacity is 0
+    // One index space: groups of kTabUnit table entries, then groups of tokens, so that
+    // a small step's entries and tokens are worked on at the same time.
     const long long n_ent = max((long long)n_pages, p.cap_pages);
-    for (long long e0 = g0; e0 < n_ent; e0 += gsize) {
-        int id[kTabUnit];
-        int b = 0, old_pages = 0, end = -1, begin = 0;
+    const long long g_ent = (n_ent + kTabUnit - 1) / kTabUnit, g_all = g_ent + (p.cap_tokens + kTabUnit - 1) / kTabUnit;
+    for (long long gi = (long long)blockIdx.x * kTabThreads + tid; gi < g_all; gi += (long long)gridDim.x * kTabThreads) {
+        if (gi < g_ent) {
+            // table entries: CSR copy of every row, new entries also into the row; the CSR
+            // tail up to its capacity is 0
+            const long long e0 = gi * kTabUnit;
+            int id[kTabUnit];
+            int b = 0, old_pages = 0, end = -1, begin = 0;
 #pragma unroll
-        for (int u = 0; u < kTabUnit; ++u) {
-            const long long e = e0 + u;
-            id[u] = 0;
-            if (e < n_pages) {
-                if ((int)e >= end) {
-                    b = end < 0 ? find_row(s_pages, B, (int)e) : b + 1;
-                    while (s_pages[b + 1] <= (int)e) ++b;  // rows without pages
-                    begin = s_pages[b];
-                    end = s_pages[b + 1];
-                    old_pages = table_row(p, b).old_pages;
+            for (int u = 0; u < kTabUnit; ++u) {
+                const long long e = e0 + u;
+                id[u] = 0;
+                if (e < n_pages) {
+                    if ((int)e >= end) {
+                        b = end < 0 ? find_row(s_pages, B, (int)e) : b + 1;
+                        while (s_pages[b + 1] <= (int)e) ++b;  // rows without pages
+                        begin = s_pages[b];
+                        end = s_pages[b + 1];
+                        old_pages = table_row(p, b).old_pages;
+                    }
+                    const int i = (int)e - begin;
+                    const int pg = page_of(b, old_pages, i);
+                    if (i >= old_pages) p.table[(long long)b * p.table_stride + i] = pg;
+                    id[u] = max(pg, 0);
                 }
-                const int i = (int)e - begin;
-                const int pg = page_of(b, old_pages, i);
-                if (i >= old_pages) p.table[(long long)b * p.table_stride + i] = pg;
-                id[u] = max(pg, 0);
             }
-        }
-        if (e0 + kTabUnit <= p.cap_pages) {
-            *reinterpret_cast<int4 *>(p.kv_indices + e0) = make_int4(id[0], id[1], id[2], id[3]);
-        } else {
+            if (e0 + kTabUnit <= p.cap_pages) {
+                *reinterpret_cast<int4 *>(p.kv_indices + e0) = make_int4(id[0], id[1], id[2], id[3]);
+            } else {
 #pragma unroll
-            for (int u = 0; u < kTabUnit; ++u)
-                if (e0 + u < p.cap_pages) p.kv_indices[e0 + u] = id[u];
+                for (int u = 0; u < kTabUnit; ++u)
+                    if (e0 + u < p.cap_pages) p.kv_indices[e0 + u] = id[u];
+            }
+            continue;
         }
-    }
-    // tokens: slot and position of every new token; the tail is -1 and 0
-    for (long long t0 = g0; t0 < p.cap_tokens; t0 += gsize) {
+        // tokens: slot and position of every new token; the tail is -1 and 0
+        const long long t0 = (gi - g_ent) * kTabUnit;
         long long slot[kTabUnit];
         int pos[kTabUnit];
         int b = 0, end = -1, begin = 0;
@@ -207,9 +211,9 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
                     begin = s_tok[b];
                     end = s_tok[b + 1];
                     r = table_row(p, b);
-                    const long long x = (long long)r.cached + ((int)t - begin);
-                    col = (int)(x / p.ps);
-                    off = (int)(x - (long long)col * p.ps);
+                    const uint32_t x = (uint32_t)r.cached + (uint32_t)((int)t - begin);
+                    col = (int)(x / (uint32_t)p.ps);
+                    off = (int)(x - (uint32_t)col * (uint32_t)p.ps);
                 } else if (++off == p.ps) {
                     off = 0;
                     ++col;
@@ -243,25 +247,25 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
 // e4m3 code no precision against amax / 448, and moving stored codes to a larger
 // exponent only shifts them.
 //
-// One CTA per (window of 128 tokens, kv head, K or V); 8 warps hold 16 tokens
-// each in registers from the first read to the stored codes, so keys and values are
-// read once. The tokens of a page stand next to each other (a run): token maxima
-// meet in shared memory per run. A run that goes past the window is measured by
-// every CTA that holds a part of it (its outside tokens are read for their maximum
-// alone, from L2); all get the same exponent, and the CTA with the run's first
+// One CTA per (window of tokens, kv head, K or V); 8 warps hold 16 (bf16) or 8 (fp32)
+// tokens each in registers from the first read to the stored codes, so keys and values
+// are read once: HBM-bound, the heads of a window in neighbouring CTAs so that whole
+// token rows are read together. The tokens of a page stand next to each other (a run):
+// token maxima meet in shared memory per run. A run that goes past the window is
+// measured by every CTA that holds a part of it (its outside tokens are read for their
+// maximum alone, from L2); all get the same exponent, and the CTA with the run's first
 // token writes it and rescales the codes that the page held before. A CTA that
 // reads the exponent after that write gets max(need, e) = e: the same.
-constexpr int kAppTokens = 128;
 constexpr int kAppWarps = 8;
-constexpr int kAppPerWarp = kAppTokens / kAppWarps;  // 16
+constexpr int kAppLoads = 8;  // 16-byte loads in flight per lane
 constexpr int kExpMin = -117, kExpMax = 119;
 constexpr int kCacheD = 128;
 
 struct AppendParams {
-    const char *x[2];             // new keys, values
-    long long tok_bytes[2], head_bytes[2];
-    uint8_t *codes[2];
-    int8_t *exps[2];
+    const char *k, *v;             // new keys, values
+    long long k_tok, k_head, v_tok, v_head;  // byte strides
+    uint8_t *k_codes, *v_codes;
+    int8_t *k_exp, *v_exp;
     const long long *slots;
     long long n, rows;             // tokens; slots of the pool
     int ps, H;
@@ -291,50 +295,58 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 template <bool kF32>
 struct Piece {
     static constexpr int kN = kF32 ? 4 : 8;
-    static constexpr int kLanes = kCacheD / kN;          // lanes per token row
-    static constexpr int kPer = 32 / kLanes;             // tokens per warp-wide load
-    static constexpr int kLoads = kAppPerWarp / kPer;    // loads of a warp's 16 tokens
+    static constexpr int kLanes = kCacheD / kN;              // lanes per token row
+    static constexpr int kPer = 32 / kLanes;                 // tokens per warp-wide load
+    static constexpr int kPerWarp = kAppLoads * kPer;        // tokens per warp
+    static constexpr int kTokens = kAppWarps * kPerWarp;     // tokens per window: 128 (bf16), 64 (fp32)
+    // largest |value| as fp32 bits; infinities and NaN included (>= 0x7f800000)
+    __device__ static __forceinline__ uint32_t amax(const uint4 &w) {
+        if constexpr (kF32) {
+            constexpr uint32_t m = 0x7fffffffu;
+            return max(max(w.x & m, w.y & m), max(w.z & m, w.w & m));
+        } else {
+            constexpr uint32_t m = 0x7fff7fffu;
+            const uint32_t a = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+            return max(a << 16, a & 0xffff0000u);
+        }
+    }
     __device__ static __forceinline__ void values(const uint4 &w, float (&f)[kN]) {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        if constexpr (kF32) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(u[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kF32) {
+                f[i] = __uint_as_float(u[i]);
+            } else {
                 f[2 * i] = dev::bf16_lo(u[i]);
                 f[2 * i + 1] = dev::bf16_hi(u[i]);
             }
         }
     }
-    // largest finite |value| as bits
-    __device__ static __forceinline__ uint32_t amax(const uint4 &w) {
+    // the same over the finite values alone
+    __device__ static __noinline__ uint32_t amax_finite(uint4 w) {
         float f[kN];
         values(w, f);
-        uint32_t m = 0;
+        uint32_t r = 0;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-        if (m >= 0x7f800000u) {  // an infinity or NaN among them
-            m = 0;
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
-                if (a < 0x7f800000u) m = max(m, a);
-            }
+        for (int i = 0; i < kN; ++i) {
+            const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
+            if (a < 0x7f800000u) r = max(r, a);
         }
-        return m;
+        return r;
     }
-    // codes of the piece at scale 2^-e (kN bytes, lowest first). The format has no
-    // infinities: infinite values become NaN.
-    __device__ static __forceinline__ uint2 codes(const uint4 &w, float s) {
+    // codes of the piece at scale s = 2^-e (kN bytes, lowest first); `inf`: the piece may
+    // hold infinities, which become NaN (the format has none)
+    __device__ static __forceinline__ uint2 codes(const uint4 &w, float s, bool inf) {
         float f[kN];
         values(w, f);
+        if (inf) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-            f[i] = (__float_as_uint(f[i]) & 0x7fffffffu) == 0x7f800000u ? __int_as_float(0x7fffffff) : f[i] * s;
+            for (int i = 0; i < kN; ++i)
+                if ((__float_as_uint(f[i]) & 0x7fffffffu) == 0x7f800000u) f[i] = __int_as_float(0x7fffffff);
+        }
         uint2 r;
-        r.x = e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
-        r.y = kF32 ? 0u : (e4m3x2(f[kN - 4], f[kN - 3]) | (e4m3x2(f[kN - 2], f[kN - 1]) << 16));
+        r.x = e4m3x2(f[0] * s, f[1] * s) | (e4m3x2(f[2] * s, f[3] * s) << 16);
+        r.y = kF32 ? 0u : (e4m3x2(f[kN - 4] * s, f[kN - 3] * s) | (e4m3x2(f[kN - 2] * s, f[kN - 1] * s) << 16));
         return r;
     }
 };
@@ -349,62 +361,75 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float s) {
 }
 
 template <bool kF32>
-__global__ void __launch_bounds__(32 * kAppWarps) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendParams p) {
     using PC = Piece<kF32>;
-    __shared__ int s_page[kAppTokens];       // page of each token, or -1
-    __shared__ int s_off[kAppTokens];        // its place in the page
-    __shared__ uint32_t s_lead[kAppTokens / 32], s_grow[kAppTokens / 32];
-    __shared__ uint32_t s_max[kAppTokens];   // by the run's first token in the window
-    __shared__ float s_scale[kAppTokens];    // 2^-e of the run
-    __shared__ int s_drop[kAppTokens];       // old exponent - e, where it rose
-    __shared__ int s_left, s_right;          // tokens of the first / last run outside the window
+    constexpr int kTok = PC::kTokens, kWords = kTok / 32;
+    __shared__ int s_page[kTok];       // page of each token, or -1
+    __shared__ int s_off[kTok];        // its place in the page
+    __shared__ uint32_t s_lead[kWords], s_grow[kWords];
+    __shared__ uint32_t s_max[kTok];   // by the run's first token in the window
+    __shared__ float s_scale[kTok];    // 2^-e of the run
+    __shared__ int s_drop[kTok];       // old exponent - e, where it rose
+    __shared__ int s_left, s_right;    // tokens of the first / last run outside the window
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int which = blockIdx.y >= (unsigned)p.H ? 1 : 0;
-    const int h = blockIdx.y - which * p.H;
-    const long long T0 = (long long)blockIdx.x * kAppTokens;
-    const int nt = (int)min((long long)kAppTokens, p.n - T0);
-    const char *x = p.x[which] + h * p.head_bytes[which];
-    const long long tb = p.tok_bytes[which];
+    const long long win = blockIdx.x / (2 * p.H);
+    const int hv = (int)(blockIdx.x - win * (2 * p.H));
+    const bool is_v = hv >= p.H;
+    const int h = is_v ? hv - p.H : hv;
+    const long long T0 = win * kTok;
+    const int nt = (int)min((long long)kTok, p.n - T0);
+    const long long tb = is_v ? p.v_tok : p.k_tok;
+    const char *x = is_v ? p.v + h * p.v_head : p.k + h * p.k_head;
+    int8_t *exps = (is_v ? p.v_exp : p.k_exp) + h;
     const int sub = lane / PC::kLanes, piece = lane % PC::kLanes;
+    const int t_first = warp * PC::kPerWarp + sub;  // token of this lane's load i: t_first + i * kPer
 
-    // this warp's 16 tokens, all loads in flight together
-    uint4 w[PC::kLoads];
+    uint4 w[kAppLoads];
 #pragma unroll
-    for (int i = 0; i < PC::kLoads; ++i) {
-        const int t = warp * kAppPerWarp + i * PC::kPer + sub;
+    for (int i = 0; i < kAppLoads; ++i) {
+        const int t = t_first + i * PC::kPer;
         w[i] = make_uint4(0, 0, 0, 0);
         if (t < nt) w[i] = __ldg(reinterpret_cast<const uint4 *>(x + (T0 + t) * tb) + piece);
     }
-    auto slot_of = [&](long long t) -> long long {
-        const long long s = __ldg(p.slots + t);
-        return s >= 0 && s < p.rows ? s : -1;
+    // page and place of a slot; page -1 outside the pool
+    auto place = [&](long long t, int &off) -> int {
+        const long long sl = __ldg(p.slots + t);
+        off = 0;
+        if (sl < 0 || sl >= p.rows) return -1;
+        if (sl <= (long long)UINT32_MAX) {
+            const uint32_t pg = (uint32_t)sl / (uint32_t)p.ps;
+            off = (int)((uint32_t)sl - pg * (uint32_t)p.ps);
+            return (int)pg;
+        }
+        off = (int)(sl % p.ps);
+        return (int)(sl / p.ps);
     };
-    if (tid < kAppTokens) {
-        const long long s = tid < nt ? slot_of(T0 + tid) : -1;
-        s_page[tid] = s >= 0 ? (int)(s / p.ps) : -1;
-        s_off[tid] = s >= 0 ? (int)(s % p.ps) : 0;
+    int my_page = -1, my_off = 0;
+    if (tid < kTok) {
+        if (tid < nt) my_page = place(T0 + tid, my_off);
+        s_page[tid] = my_page;
+        s_off[tid] = my_off;
         s_max[tid] = 0;
     }
     if (tid == 0) s_left = s_right = 0;
     __syncthreads();
-    if (tid < kAppTokens) {
-        const int pg = s_page[tid];
-        const bool lead = pg >= 0 && (tid == 0 || s_page[tid - 1] != pg);
+    bool lead = false;
+    int had = 0;
+    if (tid < kTok) {
+        lead = my_page >= 0 && (tid == 0 || s_page[tid - 1] != my_page);
+        if (lead) had = *reinterpret_cast<volatile int8_t *>(exps + (long long)my_page * p.H);
         const uint32_t m = __ballot_sync(0xffffffffu, lead);
         if (lane == 0) s_lead[warp] = m;
-    } else if (warp == kAppTokens / 32 || warp == kAppTokens / 32 + 1) {
+    } else if (warp == kAppWarps - 2 || warp == kAppWarps - 1) {
         // how far the first (last) run goes on before (behind) the window
-        const bool left = warp == kAppTokens / 32;
+        const bool left = warp == kAppWarps - 2;
         const int pg = left ? s_page[0] : s_page[nt - 1];
         int got = 0;
         if (pg >= 0) {
             for (;;) {
                 const long long t = left ? T0 - 1 - got - lane : T0 + nt + got + lane;
-                bool same = false;
-                if (t >= 0 && t < p.n) {
-                    const long long s = slot_of(t);
-                    same = s >= 0 && (int)(s / p.ps) == pg;
-                }
+                int off;
+                const bool same = t >= 0 && t < p.n && place(t, off) == pg;
                 const uint32_t m = __ballot_sync(0xffffffffu, same);
                 const int k = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
                 got += k;
@@ -421,12 +446,17 @@ __global__ void __launch_bounds__(32 * kAppWarps) append_kernel(const AppendPara
         while (m == 0) m = s_lead[--k];
         return 32 * k + 31 - __clz(m);
     };
+    uint32_t odd = 0;  // loads whose piece holds an infinity or NaN
 #pragma unroll
-    for (int i = 0; i < PC::kLoads; ++i) {
+    for (int i = 0; i < kAppLoads; ++i) {
         uint32_t m = PC::amax(w[i]);
+        if (m >= 0x7f800000u) {
+            odd |= 1u << i;
+            m = PC::amax_finite(w[i]);
+        }
 #pragma unroll
         for (int o = PC::kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int t = warp * kAppPerWarp + i * PC::kPer + sub;
+        const int t = t_first + i * PC::kPer;
         if (piece == 0 && s_page[t] >= 0) atomicMax(&s_max[run_of(t)], m);
     }
     if (s_left | s_right) {
@@ -436,7 +466,9 @@ __global__ void __launch_bounds__(32 * kAppWarps) append_kernel(const AppendPara
             uint32_t m = 0;
             if (jj < outside) {
                 const long long t = jj < s_left ? T0 - 1 - jj : T0 + nt + (jj - s_left);
-                m = PC::amax(__ldg(reinterpret_cast<const uint4 *>(x + t * tb) + piece));
+                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(x + t * tb) + piece);
+                m = PC::amax(y);
+                if (m >= 0x7f800000u) m = PC::amax_finite(y);
             }
 #pragma unroll
             for (int o = PC::kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -444,32 +476,31 @@ __global__ void __launch_bounds__(32 * kAppWarps) append_kernel(const AppendPara
         }
     }
     __syncthreads();
-    if (tid < kAppTokens) {
+    if (tid < kTok) {
         bool grow = false;
-        if (s_lead[warp] >> lane & 1) {
+        if (lead) {
             const int need = exponent_for(s_max[tid]);
             const bool mine = tid > 0 || s_left == 0;  // the run's first token is in this window
-            const int off = mine ? s_off[tid] : (int)(slot_of(T0 - s_left) % p.ps);
-            int8_t *ep = p.exps[which] + (long long)s_page[tid] * p.H + h;
-            const int had = off > 0 ? *reinterpret_cast<volatile int8_t *>(ep) : need;
-            const int e = max(need, had);
+            int off = my_off;
+            if (!mine) place(T0 - s_left, off);
+            const int e = off > 0 ? max(need, had) : need;
             s_scale[tid] = pow2i(-e);
             s_drop[tid] = had - e;
             grow = mine && off > 0 && e > had;
-            if (mine) *ep = (int8_t)e;
+            if (mine) exps[(long long)my_page * p.H] = (int8_t)e;
         }
         const uint32_t m = __ballot_sync(0xffffffffu, grow);
         if (lane == 0) s_grow[warp] = m;
     }
     __syncthreads();
-    uint8_t *codes = p.codes[which] + (long long)h * kCacheD;
+    uint8_t *codes = (is_v ? p.v_codes : p.k_codes) + (long long)h * kCacheD;
     const long long row_bytes = (long long)p.H * kCacheD;
 #pragma unroll
-    for (int i = 0; i < PC::kLoads; ++i) {
-        const int t = warp * kAppPerWarp + i * PC::kPer + sub;
+    for (int i = 0; i < kAppLoads; ++i) {
+        const int t = t_first + i * PC::kPer;
         const int pg = s_page[t];
         if (pg >= 0) {
-            const uint2 c = PC::codes(w[i], s_scale[run_of(t)]);
+            const uint2 c = PC::codes(w[i], s_scale[run_of(t)], odd >> i & 1);
             uint8_t *dst = codes + ((long long)pg * p.ps + s_off[t]) * row_bytes + piece * PC::kN;
             if constexpr (kF32) *reinterpret_cast<uint32_t *>(dst) = c.x;
             else *reinterpret_cast<uint2 *>(dst) = c;
@@ -478,7 +509,7 @@ __global__ void __launch_bounds__(32 * kAppWarps) append_kernel(const AppendPara
     // codes that a page held before its exponent rose: rows 0 .. off - 1, one run per
     // warp, four rows of 8 lanes x 16 bytes at a time
     int turn = 0;
-    for (int k = 0; k < kAppTokens / 32; ++k) {
+    for (int k = 0; k < kWords; ++k) {
         for (uint32_t m = s_grow[k]; m; m &= m - 1, ++turn) {
             if (turn % kAppWarps != warp) continue;
             const int t = 32 * k + __ffs(m) - 1;
@@ -547,8 +578,8 @@ int launch_page_tables(int32_t batch, int32_t page_size, const int32_t *cached_l
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("page tables smem attribute: ") + cudaGetErrorString(e));
         configured[dev] = true;
     }
-    const int64_t per = kTabThreads * kTabUnit, work = std::max<int64_t>(cap_pages, cap_tokens);
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((work + per - 1) / per, 4ll * sms));
+    const int64_t groups = (cap_pages + kTabUnit - 1) / kTabUnit + (cap_tokens + kTabUnit - 1) / kTabUnit;
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((groups + kTabThreads - 1) / kTabThreads, 4ll * sms));
     page_tables_kernel<<<(unsigned)grid, kTabThreads, smem, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("page tables launch: ") + cudaGetErrorString(e));
@@ -560,25 +591,27 @@ int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64
                      const int64_t *slot_map, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
                      int64_t num_pages, int32_t page_size, int32_t num_kv_heads, cudaStream_t stream) {
     const int64_t elem = dtype == BSP_DTYPE_F32 ? 4 : 2;
+    const int tok = dtype == BSP_DTYPE_F32 ? Piece<true>::kTokens : Piece<false>::kTokens;
+    const int64_t ctas = (n_tokens + tok - 1) / tok * 2 * num_kv_heads;
+    if (ctas > INT32_MAX) return fail(BSP_ERR_UNSUPPORTED, "too many tokens for one append");
     AppendParams p;
-    p.x[0] = static_cast<const char *>(k);
-    p.x[1] = static_cast<const char *>(v);
-    p.tok_bytes[0] = k_token_stride * elem;
-    p.tok_bytes[1] = v_token_stride * elem;
-    p.head_bytes[0] = k_head_stride * elem;
-    p.head_bytes[1] = v_head_stride * elem;
-    p.codes[0] = static_cast<uint8_t *>(k_pages);
-    p.codes[1] = static_cast<uint8_t *>(v_pages);
-    p.exps[0] = k_exp;
-    p.exps[1] = v_exp;
+    p.k = static_cast<const char *>(k);
+    p.v = static_cast<const char *>(v);
+    p.k_tok = k_token_stride * elem;
+    p.k_head = k_head_stride * elem;
+    p.v_tok = v_token_stride * elem;
+    p.v_head = v_head_stride * elem;
+    p.k_codes = static_cast<uint8_t *>(k_pages);
+    p.v_codes = static_cast<uint8_t *>(v_pages);
+    p.k_exp = k_exp;
+    p.v_exp = v_exp;
     p.slots = reinterpret_cast<const long long *>(slot_map);
     p.n = n_tokens;
     p.rows = (long long)num_pages * page_size;
     p.ps = page_size;
     p.H = num_kv_heads;
-    const dim3 grid((unsigned)((n_tokens + kAppTokens - 1) / kAppTokens), 2u * (unsigned)num_kv_heads);
-    if (dtype == BSP_DTYPE_F32) append_kernel<true><<<grid, 32 * kAppWarps, 0, stream>>>(p);
-    else append_kernel<false><<<grid, 32 * kAppWarps, 0, stream>>>(p);
+    if (dtype == BSP_DTYPE_F32) append_kernel<true><<<(unsigned)ctas, 32 * kAppWarps, 0, stream>>>(p);
+    else append_kernel<false><<<(unsigned)ctas, 32 * kAppWarps, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("append launch: ") + cudaGetErrorString(e));
     return BSP_OK;
