@@ -247,16 +247,16 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
 // e4m3 code no precision against amax / 448, and moving stored codes to a larger
 // exponent only shifts them.
 //
-// One CTA per (window of tokens, kv head, K or V); 8 warps hold 16 (bf16) or 8 (fp32)
-// tokens each in registers from the first read to the stored codes, so keys and values
-// are read once: HBM-bound, the heads of a window in neighbouring CTAs so that whole
+// One CTA per (window of 128 tokens, kv head, K or V); its 8 (bf16) or 16 (fp32) warps
+// hold the tokens in registers from the first read to the stored codes, so keys and
+// values are read once: HBM-bound, the heads of a window in neighbouring CTAs so that whole
 // token rows are read together. The tokens of a page stand next to each other (a run):
 // token maxima meet in shared memory per run. A run that goes past the window is
 // measured by every CTA that holds a part of it (its outside tokens are read for their
 // maximum alone, from L2); all get the same exponent, and the CTA with the run's first
 // token writes it and rescales the codes that the page held before. A CTA that
 // reads the exponent after that write gets max(need, e) = e: the same.
-constexpr int kAppWarps = 8;
+constexpr int kAppTokens = 128;
 constexpr int kAppLoads = 8;  // 16-byte loads in flight per lane
 constexpr int kExpMin = -117, kExpMax = 119;
 constexpr int kCacheD = 128;
@@ -298,7 +298,7 @@ struct Piece {
     static constexpr int kLanes = kCacheD / kN;              // lanes per token row
     static constexpr int kPer = 32 / kLanes;                 // tokens per warp-wide load
     static constexpr int kPerWarp = kAppLoads * kPer;        // tokens per warp
-    static constexpr int kTokens = kAppWarps * kPerWarp;     // tokens per window: 128 (bf16), 64 (fp32)
+    static constexpr int kWarps = kAppTokens / kPerWarp;     // 8 (bf16), 16 (fp32)
     // largest |value| as fp32 bits; infinities and NaN included (>= 0x7f800000)
     __device__ static __forceinline__ uint32_t amax(const uint4 &w) {
         if constexpr (kF32) {
@@ -360,17 +360,39 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float s) {
     return e4m3x2(fa.x * s, fa.y * s) | (e4m3x2(fb.x * s, fb.y * s) << 16);
 }
 
+// Maxima of a warp's tokens: v[i] is this lane's part of load i. The eight values are
+// halved while the lanes are folded (4 + 2 + 1 exchanges, then plain folds): lane l of a
+// row ends with the maximum of load (l / (kLanes / 8)) of its row.
+template <int kLanes>
+__device__ __forceinline__ uint32_t fold_max(uint32_t (&v)[kAppLoads], int piece) {
+#pragma unroll
+    for (int n = kAppLoads / 2, o = kLanes / 2; n >= 1; n >>= 1, o >>= 1) {
+        const bool up = piece & o;  // keeps the upper half of the values
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint32_t keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+            v[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, o));
+        }
+    }
+#pragma unroll
+    for (int o = kLanes / 16; o >= 1; o >>= 1) v[0] = max(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    return v[0];
+}
+
 template <bool kF32>
-__global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append_kernel(const AppendParams p) {
     using PC = Piece<kF32>;
-    constexpr int kTok = PC::kTokens, kWords = kTok / 32;
-    __shared__ int s_page[kTok];       // page of each token, or -1
-    __shared__ int s_off[kTok];        // its place in the page
+    constexpr int kTok = kAppTokens, kWords = kTok / 32, kWarps = PC::kWarps;
+    __shared__ int s_page[kTok];         // page of each token, or -1
+    __shared__ long long s_row[kTok];    // byte offset of its row in the pool, or -1
     __shared__ uint32_t s_lead[kWords], s_grow[kWords];
-    __shared__ uint32_t s_max[kTok];   // by the run's first token in the window
-    __shared__ float s_scale[kTok];    // 2^-e of the run
-    __shared__ int s_drop[kTok];       // old exponent - e, where it rose
-    __shared__ int s_left, s_right;    // tokens of the first / last run outside the window
+    __shared__ uint32_t s_tmax[kTok];    // token maxima
+    __shared__ int s_run[kTok];          // the window's first token of its run
+    __shared__ uint32_t s_max[kTok];     // by run: maximum,
+    __shared__ float s_scale[kTok];      // 2^-e,
+    __shared__ int s_drop[kTok];         // old exponent - e, where it rose,
+    __shared__ int s_held[kTok];         // and the rows that the page held before
+    __shared__ int s_left, s_right;      // tokens of the first / last run outside the window
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long win = blockIdx.x / (2 * p.H);
     const int hv = (int)(blockIdx.x - win * (2 * p.H));
@@ -385,11 +407,11 @@ __global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendP
     const int t_first = warp * PC::kPerWarp + sub;  // token of this lane's load i: t_first + i * kPer
 
     uint4 w[kAppLoads];
+    const char *src = x + (T0 + t_first) * tb + piece * 16;
 #pragma unroll
     for (int i = 0; i < kAppLoads; ++i) {
-        const int t = t_first + i * PC::kPer;
         w[i] = make_uint4(0, 0, 0, 0);
-        if (t < nt) w[i] = __ldg(reinterpret_cast<const uint4 *>(x + (T0 + t) * tb) + piece);
+        if (t_first + i * PC::kPer < nt) w[i] = __ldg(reinterpret_cast<const uint4 *>(src + i * PC::kPer * tb));
     }
     // page and place of a slot; page -1 outside the pool
     auto place = [&](long long t, int &off) -> int {
@@ -404,11 +426,12 @@ __global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendP
         off = (int)(sl % p.ps);
         return (int)(sl / p.ps);
     };
+    const long long row_bytes = (long long)p.H * kCacheD;
     int my_page = -1, my_off = 0;
     if (tid < kTok) {
         if (tid < nt) my_page = place(T0 + tid, my_off);
         s_page[tid] = my_page;
-        s_off[tid] = my_off;
+        s_row[tid] = my_page >= 0 ? ((long long)my_page * p.ps + my_off) * row_bytes : -1;
         s_max[tid] = 0;
     }
     if (tid == 0) s_left = s_right = 0;
@@ -420,9 +443,9 @@ __global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendP
         if (lead) had = *reinterpret_cast<volatile int8_t *>(exps + (long long)my_page * p.H);
         const uint32_t m = __ballot_sync(0xffffffffu, lead);
         if (lane == 0) s_lead[warp] = m;
-    } else if (warp == kAppWarps - 2 || warp == kAppWarps - 1) {
+    } else if (warp >= kWarps - 2) {
         // how far the first (last) run goes on before (behind) the window
-        const bool left = warp == kAppWarps - 2;
+        const bool left = warp == kWarps - 2;
         const int pg = left ? s_page[0] : s_page[nt - 1];
         int got = 0;
         if (pg >= 0) {
@@ -438,6 +461,21 @@ __global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendP
         }
         if (lane == 0) (left ? s_left : s_right) = got;
     }
+    uint32_t odd = 0;  // loads whose piece holds an infinity or NaN
+    {
+        uint32_t v[kAppLoads];
+#pragma unroll
+        for (int i = 0; i < kAppLoads; ++i) {
+            v[i] = PC::amax(w[i]);
+            if (v[i] >= 0x7f800000u) {
+                odd |= 1u << i;
+                v[i] = PC::amax_finite(w[i]);
+            }
+        }
+        const uint32_t m = fold_max<PC::kLanes>(v, piece);
+        constexpr int kShare = PC::kLanes / kAppLoads;  // lanes that hold the same maximum
+        if (piece % kShare == 0) s_tmax[t_first + piece / kShare * PC::kPer] = m;
+    }
     __syncthreads();
     // first token of the run that token t (with a page) belongs to, within the window
     auto run_of = [&](int t) -> int {
@@ -446,33 +484,34 @@ __global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendP
         while (m == 0) m = s_lead[--k];
         return 32 * k + 31 - __clz(m);
     };
-    uint32_t odd = 0;  // loads whose piece holds an infinity or NaN
-#pragma unroll
-    for (int i = 0; i < kAppLoads; ++i) {
-        uint32_t m = PC::amax(w[i]);
-        if (m >= 0x7f800000u) {
-            odd |= 1u << i;
-            m = PC::amax_finite(w[i]);
-        }
-#pragma unroll
-        for (int o = PC::kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int t = t_first + i * PC::kPer;
-        if (piece == 0 && s_page[t] >= 0) atomicMax(&s_max[run_of(t)], m);
+    if (tid < kTok && my_page >= 0) {
+        const int r = run_of(tid);
+        s_run[tid] = r;
+        atomicMax(&s_max[r], s_tmax[tid]);
     }
     if (s_left | s_right) {
-        const int outside = s_left + s_right;
-        for (int j = warp * PC::kPer; j < outside; j += kAppWarps * PC::kPer) {
-            const int jj = j + sub;
-            uint32_t m = 0;
-            if (jj < outside) {
-                const long long t = jj < s_left ? T0 - 1 - jj : T0 + nt + (jj - s_left);
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(x + t * tb) + piece);
-                m = PC::amax(y);
-                if (m >= 0x7f800000u) m = PC::amax_finite(y);
+        const int outside = s_left + s_right, last_run = run_of(nt - 1);
+        constexpr int kStep = kWarps * PC::kPer, kFly = 2;
+        for (int j = warp * PC::kPer + sub; j - sub < outside; j += kFly * kStep) {
+            uint4 y[kFly];
+#pragma unroll
+            for (int f = 0; f < kFly; ++f) {
+                const int jj = j + f * kStep;
+                y[f] = make_uint4(0, 0, 0, 0);
+                if (jj < outside) {
+                    const long long t = jj < s_left ? T0 - 1 - jj : T0 + nt + (jj - s_left);
+                    y[f] = __ldg(reinterpret_cast<const uint4 *>(x + t * tb) + piece);
+                }
             }
 #pragma unroll
-            for (int o = PC::kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (piece == 0 && jj < outside) atomicMax(&s_max[jj < s_left ? 0 : run_of(nt - 1)], m);
+            for (int f = 0; f < kFly; ++f) {
+                const int jj = j + f * kStep;
+                uint32_t m = PC::amax(y[f]);
+                if (m >= 0x7f800000u) m = PC::amax_finite(y[f]);
+#pragma unroll
+                for (int o = PC::kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (piece == 0 && jj < outside) atomicMax(&s_max[jj < s_left ? 0 : last_run], m);
+            }
         }
     }
     __syncthreads();
@@ -486,6 +525,7 @@ __global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendP
             const int e = off > 0 ? max(need, had) : need;
             s_scale[tid] = pow2i(-e);
             s_drop[tid] = had - e;
+            s_held[tid] = off;
             grow = mine && off > 0 && e > had;
             if (mine) exps[(long long)my_page * p.H] = (int8_t)e;
         }
@@ -494,14 +534,13 @@ __global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendP
     }
     __syncthreads();
     uint8_t *codes = (is_v ? p.v_codes : p.k_codes) + (long long)h * kCacheD;
-    const long long row_bytes = (long long)p.H * kCacheD;
 #pragma unroll
     for (int i = 0; i < kAppLoads; ++i) {
         const int t = t_first + i * PC::kPer;
-        const int pg = s_page[t];
-        if (pg >= 0) {
-            const uint2 c = PC::codes(w[i], s_scale[run_of(t)], odd >> i & 1);
-            uint8_t *dst = codes + ((long long)pg * p.ps + s_off[t]) * row_bytes + piece * PC::kN;
+        const long long row = s_row[t];
+        if (row >= 0) {
+            const uint2 c = PC::codes(w[i], s_scale[s_run[t]], odd >> i & 1);
+            uint8_t *dst = codes + row + piece * PC::kN;
             if constexpr (kF32) *reinterpret_cast<uint32_t *>(dst) = c.x;
             else *reinterpret_cast<uint2 *>(dst) = c;
         }
@@ -511,11 +550,11 @@ __global__ void __launch_bounds__(32 * kAppWarps, 4) append_kernel(const AppendP
     int turn = 0;
     for (int k = 0; k < kWords; ++k) {
         for (uint32_t m = s_grow[k]; m; m &= m - 1, ++turn) {
-            if (turn % kAppWarps != warp) continue;
+            if (turn % kWarps != warp) continue;
             const int t = 32 * k + __ffs(m) - 1;
             const float s = pow2i(max(s_drop[t], -126));
             uint8_t *page = codes + (long long)s_page[t] * p.ps * row_bytes;
-            for (int r = lane >> 3; r < s_off[t]; r += 4) {
+            for (int r = lane >> 3; r < s_held[t]; r += 4) {
                 uint4 *at = reinterpret_cast<uint4 *>(page + r * row_bytes) + (lane & 7);
                 uint4 c = *at;
                 c.x = rescale_codes(c.x, s);
@@ -591,8 +630,7 @@ int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64
                      const int64_t *slot_map, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
                      int64_t num_pages, int32_t page_size, int32_t num_kv_heads, cudaStream_t stream) {
     const int64_t elem = dtype == BSP_DTYPE_F32 ? 4 : 2;
-    const int tok = dtype == BSP_DTYPE_F32 ? Piece<true>::kTokens : Piece<false>::kTokens;
-    const int64_t ctas = (n_tokens + tok - 1) / tok * 2 * num_kv_heads;
+    const int64_t ctas = (n_tokens + kAppTokens - 1) / kAppTokens * 2 * num_kv_heads;
     if (ctas > INT32_MAX) return fail(BSP_ERR_UNSUPPORTED, "too many tokens for one append");
     AppendParams p;
     p.k = static_cast<const char *>(k);
@@ -610,8 +648,8 @@ int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64
     p.rows = (long long)num_pages * page_size;
     p.ps = page_size;
     p.H = num_kv_heads;
-    if (dtype == BSP_DTYPE_F32) append_kernel<true><<<(unsigned)ctas, 32 * kAppWarps, 0, stream>>>(p);
-    else append_kernel<false><<<(unsigned)ctas, 32 * kAppWarps, 0, stream>>>(p);
+    if (dtype == BSP_DTYPE_F32) append_kernel<true><<<(unsigned)ctas, 32 * Piece<true>::kWarps, 0, stream>>>(p);
+    else append_kernel<false><<<(unsigned)ctas, 32 * Piece<false>::kWarps, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("append launch: ") + cudaGetErrorString(e));
     return BSP_OK;
