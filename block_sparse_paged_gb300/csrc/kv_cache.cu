@@ -291,6 +291,20 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// lo * s and hi * s as two e4m3 codes
+__device__ __forceinline__ uint32_t e4m3x2_scaled(float lo, float hi, float s) {
+    asm("{ .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mul.rn.f32x2 a, a, b;\n"
+        " mov.b64 {%0, %1}, a;\n}"
+        : "+f"(lo), "+f"(hi)
+        : "f"(s));
+    return e4m3x2(lo, hi);
+}
+
 // One lane's 16-byte piece of a token row: 8 bf16 or 4 fp32 values.
 template <bool kF32>
 struct Piece {
@@ -306,7 +320,7 @@ struct Piece {
             return max(max(w.x & m, w.y & m), max(w.z & m, w.w & m));
         } else {
             constexpr uint32_t m = 0x7fff7fffu;
-            const uint32_t a = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+            const uint32_t a = max2(max2(w.x & m, w.y & m), max2(w.z & m, w.w & m));
             return max(a << 16, a & 0xffff0000u);
         }
     }
@@ -345,8 +359,8 @@ struct Piece {
                 if ((__float_as_uint(f[i]) & 0x7fffffffu) == 0x7f800000u) f[i] = __int_as_float(0x7fffffff);
         }
         uint2 r;
-        r.x = e4m3x2(f[0] * s, f[1] * s) | (e4m3x2(f[2] * s, f[3] * s) << 16);
-        r.y = kF32 ? 0u : (e4m3x2(f[kN - 4] * s, f[kN - 3] * s) | (e4m3x2(f[kN - 2] * s, f[kN - 1] * s) << 16));
+        r.x = e4m3x2_scaled(f[0], f[1], s) | (e4m3x2_scaled(f[2], f[3], s) << 16);
+        r.y = kF32 ? 0u : (e4m3x2_scaled(f[kN - 4], f[kN - 3], s) | (e4m3x2_scaled(f[kN - 2], f[kN - 1], s) << 16));
         return r;
     }
 };
@@ -384,14 +398,11 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
     using PC = Piece<kF32>;
     constexpr int kTok = kAppTokens, kWords = kTok / 32, kWarps = PC::kWarps;
     __shared__ int s_page[kTok];         // page of each token, or -1
-    __shared__ long long s_row[kTok];    // byte offset of its row in the pool, or -1
-    __shared__ uint32_t s_lead[kWords], s_grow[kWords];
+    __shared__ int s_off[kTok];          // its place in the page
+    __shared__ int s_had[kTok];          // the page's exponent before (of first tokens)
+    __shared__ uint32_t s_lead[kWords];  // tokens that begin a run in this window
     __shared__ uint32_t s_tmax[kTok];    // token maxima
-    __shared__ int s_run[kTok];          // the window's first token of its run
-    __shared__ uint32_t s_max[kTok];     // by run: maximum,
-    __shared__ float s_scale[kTok];      // 2^-e,
-    __shared__ int s_drop[kTok];         // old exponent - e, where it rose,
-    __shared__ int s_held[kTok];         // and the rows that the page held before
+    __shared__ uint32_t s_max[kTok];     // maxima of runs, by their first token in the window
     __shared__ int s_left, s_right;      // tokens of the first / last run outside the window
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long win = blockIdx.x / (2 * p.H);
@@ -426,32 +437,25 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
         off = (int)(sl % p.ps);
         return (int)(sl / p.ps);
     };
-    const long long row_bytes = (long long)p.H * kCacheD;
-    int my_page = -1, my_off = 0;
     if (tid < kTok) {
-        if (tid < nt) my_page = place(T0 + tid, my_off);
-        s_page[tid] = my_page;
-        s_row[tid] = my_page >= 0 ? ((long long)my_page * p.ps + my_off) * row_bytes : -1;
+        int off = 0, off_before;
+        const int page = tid < nt ? place(T0 + tid, off) : -1;
+        // (of token 0 the run may begin before the window: s_left tells)
+        const bool lead = page >= 0 && (tid == 0 || place(T0 + tid - 1, off_before) != page);
+        s_page[tid] = page;
+        s_off[tid] = off;
         s_max[tid] = 0;
-    }
-    if (tid == 0) s_left = s_right = 0;
-    __syncthreads();
-    bool lead = false;
-    int had = 0;
-    if (tid < kTok) {
-        lead = my_page >= 0 && (tid == 0 || s_page[tid - 1] != my_page);
-        if (lead) had = *reinterpret_cast<volatile int8_t *>(exps + (long long)my_page * p.H);
+        if (lead) s_had[tid] = *reinterpret_cast<volatile int8_t *>(exps + (long long)page * p.H);
         const uint32_t m = __ballot_sync(0xffffffffu, lead);
         if (lane == 0) s_lead[warp] = m;
     } else if (warp >= kWarps - 2) {
         // how far the first (last) run goes on before (behind) the window
         const bool left = warp == kWarps - 2;
-        const int pg = left ? s_page[0] : s_page[nt - 1];
-        int got = 0;
+        int got = 0, off;
+        const int pg = place(left ? T0 : T0 + nt - 1, off);
         if (pg >= 0) {
             for (;;) {
                 const long long t = left ? T0 - 1 - got - lane : T0 + nt + got + lane;
-                int off;
                 const bool same = t >= 0 && t < p.n && place(t, off) == pg;
                 const uint32_t m = __ballot_sync(0xffffffffu, same);
                 const int k = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
@@ -484,13 +488,9 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
         while (m == 0) m = s_lead[--k];
         return 32 * k + 31 - __clz(m);
     };
-    if (tid < kTok && my_page >= 0) {
-        const int r = run_of(tid);
-        s_run[tid] = r;
-        atomicMax(&s_max[r], s_tmax[tid]);
-    }
+    if (tid < kTok && s_page[tid] >= 0) atomicMax(&s_max[run_of(tid)], s_tmax[tid]);
     if (s_left | s_right) {
-        const int outside = s_left + s_right, last_run = run_of(nt - 1);
+        const int outside = s_left + s_right, last_run = s_page[nt - 1] >= 0 ? run_of(nt - 1) : 0;
         constexpr int kStep = kWarps * PC::kPer, kFly = 2;
         for (int j = warp * PC::kPer + sub; j - sub < outside; j += kFly * kStep) {
             uint4 y[kFly];
@@ -515,54 +515,56 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
         }
     }
     __syncthreads();
-    if (tid < kTok) {
-        bool grow = false;
-        if (lead) {
-            const int need = exponent_for(s_max[tid]);
-            const bool mine = tid > 0 || s_left == 0;  // the run's first token is in this window
-            int off = my_off;
-            if (!mine) place(T0 - s_left, off);
-            const int e = off > 0 ? max(need, had) : need;
-            s_scale[tid] = pow2i(-e);
-            s_drop[tid] = had - e;
-            s_held[tid] = off;
-            grow = mine && off > 0 && e > had;
-            if (mine) exps[(long long)my_page * p.H] = (int8_t)e;
-        }
-        const uint32_t m = __ballot_sync(0xffffffffu, grow);
-        if (lane == 0) s_grow[warp] = m;
-    }
-    __syncthreads();
+    // Lane l < kPerWarp: the exponent of the warp's token l and where its codes go
     uint8_t *codes = (is_v ? p.v_codes : p.k_codes) + (long long)h * kCacheD;
+    const long long row_bytes = (long long)p.H * kCacheD;
+    long long row = -1;
+    float scale = 0.f;
+    bool grow = false;
+    int drop = 0, held = 0;
+    if (lane < PC::kPerWarp) {
+        const int t = warp * PC::kPerWarp + lane, page = s_page[t];
+        if (page >= 0) {
+            row = ((long long)page * p.ps + s_off[t]) * row_bytes;
+            const int r = run_of(t), need = exponent_for(s_max[r]);
+            const bool inside = r > 0 || s_left == 0;  // the run's first token is in this window
+            held = s_off[r];
+            if (!inside) place(T0 - s_left, held);
+            const int e = held > 0 ? max(need, s_had[r]) : need;
+            scale = pow2i(-e);
+            if (inside && r == t) {
+                drop = s_had[t] - e;
+                grow = held > 0 && drop < 0;
+                exps[(long long)page * p.H] = (int8_t)e;
+            }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kAppLoads; ++i) {
-        const int t = t_first + i * PC::kPer;
-        const long long row = s_row[t];
-        if (row >= 0) {
-            const uint2 c = PC::codes(w[i], s_scale[s_run[t]], odd >> i & 1);
-            uint8_t *dst = codes + row + piece * PC::kN;
+        const long long to = __shfl_sync(0xffffffffu, row, i * PC::kPer + sub);
+        const float sc = __shfl_sync(0xffffffffu, scale, i * PC::kPer + sub);
+        if (to >= 0) {
+            const uint2 c = PC::codes(w[i], sc, odd >> i & 1);
+            uint8_t *dst = codes + to + piece * PC::kN;
             if constexpr (kF32) *reinterpret_cast<uint32_t *>(dst) = c.x;
             else *reinterpret_cast<uint2 *>(dst) = c;
         }
     }
-    // codes that a page held before its exponent rose: rows 0 .. off - 1, one run per
-    // warp, four rows of 8 lanes x 16 bytes at a time
-    int turn = 0;
-    for (int k = 0; k < kWords; ++k) {
-        for (uint32_t m = s_grow[k]; m; m &= m - 1, ++turn) {
-            if (turn % kWarps != warp) continue;
-            const int t = 32 * k + __ffs(m) - 1;
-            const float s = pow2i(max(s_drop[t], -126));
-            uint8_t *page = codes + (long long)s_page[t] * p.ps * row_bytes;
-            for (int r = lane >> 3; r < s_held[t]; r += 4) {
-                uint4 *at = reinterpret_cast<uint4 *>(page + r * row_bytes) + (lane & 7);
-                uint4 c = *at;
-                c.x = rescale_codes(c.x, s);
-                c.y = rescale_codes(c.y, s);
-                c.z = rescale_codes(c.z, s);
-                c.w = rescale_codes(c.w, s);
-                *at = c;
-            }
+    // codes that a page held before its exponent rose: rows 0 .. held - 1, four rows of
+    // 8 lanes x 16 bytes at a time
+    for (uint32_t m = __ballot_sync(0xffffffffu, grow); m; m &= m - 1) {
+        const int l = __ffs(m) - 1;
+        const int rows = __shfl_sync(0xffffffffu, held, l);
+        const float sc = pow2i(max(__shfl_sync(0xffffffffu, drop, l), -126));
+        uint8_t *page = codes + __shfl_sync(0xffffffffu, row, l) - rows * row_bytes;
+        for (int r = lane >> 3; r < rows; r += 4) {
+            uint4 *at = reinterpret_cast<uint4 *>(page + r * row_bytes) + (lane & 7);
+            uint4 c = *at;
+            c.x = rescale_codes(c.x, sc);
+            c.y = rescale_codes(c.y, sc);
+            c.z = rescale_codes(c.z, sc);
+            c.w = rescale_codes(c.w, sc);
+            *at = c;
         }
     }
 }
