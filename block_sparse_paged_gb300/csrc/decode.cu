@@ -324,7 +324,180 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
     }
     __syncthreads();
 
-    if (kTma && warp >= kConsumers) {
+    if constexpr (kBlk) {
+        if (warp >= kConsumers) {
+            // -------- producers of a cache with exponents: warps of K, then warps of V ------
+            // A producer's own instructions bound it (3,100 cycles per 64 KB stage with
+            // divisions in the loop, the ring never full), so page and place advance by
+            // additions and shifts, ids are read two stages ahead and exponents one.
+            constexpr int kPerOp = LY::kLoad / 2;
+            const bool is_v = warp >= kConsumers + kPerOp;
+            const int8_t *exps = (is_v ? p.v_exp : p.k_exp);
+            uint8_t *ex_smem = smem + LY::kExpOff + (is_v ? LY::kExpN : 0);
+            const uint32_t part = is_v ? LY::kTileBytes : 0;
+            int st = 0, ph = 1;  // ring position: stage, parity of its empty wait
+            if constexpr (kTma) {
+                // Lane l looks after box l of a stage (box_rows rows of one page, one copy) and
+                // the exponent of tokens 8l .. 8l + 7. br, bps, spb: powers of two.
+                const CUtensorMap *map = is_v ? &tv : &tk;
+                const int br_s = 31 - __clz(p.box_rows), ps_s = 31 - __clz(p.page_size);
+                constexpr int kTK_s = kTK == 256 ? 8 : 7;
+                static_assert(kTK == 1 << kTK_s, "stage size");
+                const int bps_s = kTK_s - br_s, spb_s = 5 - bps_s;  // boxes per stage, stages per 32 ids
+                for (int it = it0; it < it1 && !*abort_flag; ++it) {
+                    const bsp_work_item w = items[it];
+                    const int len = w.kv_end - w.kv_start;
+                    const int nt = (len + kTK - 1) / kTK;
+                    const int32_t *ids = p.kv_indices + w.page_base;
+                    // page ids in batches of 32 (lane l: box l of the batch), one batch ahead
+                    auto fetch_batch = [&](int b) -> int {
+                        const int r = ((b << 5) + lane) << br_s;
+                        return r < len ? __ldg(ids + ((w.kv_start + r) >> ps_s)) : 0;
+                    };
+                    auto fetch_exp = [&](int tt, int batch) -> int {
+                        const int box = ((tt & ((1 << spb_s) - 1)) << bps_s) + ((lane << 3) >> br_s);
+                        const int g = __shfl_sync(0xffffffffu, batch, box & 31);
+                        const bool in = lane < kTK / 8 && (tt << kTK_s) + (lane << 3) < len && (unsigned)g < (unsigned)p.num_pages;
+                        return in ? __ldg(exps + (size_t)g * p.H_kv + w.kv_head) : 0;
+                    };
+                    int cur = nt > 0 ? fetch_batch(0) : 0;
+                    int nxt = (1 << spb_s) < nt ? fetch_batch(1) : 0;
+                    int ex = nt > 0 ? fetch_exp(0, cur) : 0;
+                    for (int t = 0; t < nt; ++t) {
+                        const int in_b = t & ((1 << spb_s) - 1);
+                        if (t > 0 && in_b == 0) {
+                            cur = nxt;
+                            if (t + (1 << spb_s) < nt) nxt = fetch_batch((t >> spb_s) + 1);
+                        }
+                        const int pg = __shfl_sync(0xffffffffu, cur, ((in_b << bps_s) + lane) & 31);
+                        const int n = min(kTK, len - (t << kTK_s));
+                        const int nbox = (n + (1 << br_s) - 1) >> br_s;
+                        int row0 = (pg << ps_s) + ((w.kv_start + (t << kTK_s) + (lane << br_s)) & (p.page_size - 1));
+                        if (lane < nbox && (unsigned)pg >= (unsigned)p.num_pages) {
+                            row0 = -p.box_rows;  // a box outside the pool reads as zeros
+                            atomicCAS(status, 0, kStatusPageIndex);
+                        }
+                        const int ex_now = ex;
+                        if (t + 1 < nt) ex = fetch_exp(t + 1, ((t + 1) & ((1 << spb_s) - 1)) == 0 ? nxt : cur);
+                        const bool ok = wait_or_abort(empty0 + 8 * st, ph, abort_flag, status, kStatusProducerWait);
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        if (lane < nbox)
+                            sm100::tma_load_3d(sbase + st * LY::kStageBytes + part + (uint32_t)(lane << (br_s + 7)), map,
+                                               full0 + 8 * st, 0, w.kv_head, row0);
+                        // the copies are under way: their bytes may land before the arrival that
+                        // expects them, which also publishes the exponents
+                        if (lane < kTK / 8) ex_smem[st * 2 * LY::kExpN + lane] = (uint8_t)ex_now;
+                        __syncwarp();
+                        if (lane == 0) sm100::mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(nbox << (br_s + 7)));
+                        if (++st == kStages) { st = 0; ph ^= 1; }
+                    }
+                }
+                return;
+            }
+            // 16-byte cp.async: a warp copies half of a stage's tokens, four rows (8 lanes x 16
+            // bytes each) per instruction. Lane l looks after tokens l + 32 j of the half.
+            constexpr int kHalfTK = kTK / kPerOp, kJ = kHalfTK / 32;
+            static_assert(D == 128 && kHalfTK % 32 == 0, "rows of 128 codes");
+            const int tok_base = ((warp - kConsumers) % kPerOp) * kHalfTK;
+            const char *src = static_cast<const char *>(is_v ? p.v : p.k);
+            const int c16 = lane & 7, sub = lane >> 3;
+            const uint32_t row_bytes = (uint32_t)p.H_kv * D;
+            const int step_q = kTK / p.page_size, step_r = kTK % p.page_size;  // a stage's advance in pages and rows
+            constexpr uint32_t kBadRow = ~0u;  // a token whose page id is outside the pool: copied as zeros
+            for (int it = it0; it < it1 && !*abort_flag; ++it) {
+                const bsp_work_item w = items[it];
+                const int len = w.kv_end - w.kv_start;
+                const int nt = (len + kTK - 1) / kTK;
+                const int32_t *ids = p.kv_indices + w.page_base;
+                const char *base = src + (size_t)w.kv_head * D + c16 * 16;
+                // table column and place in its page of this lane's tokens: of the stage whose
+                // ids are read next (q, r)
+                int q[kJ], r[kJ], id1[kJ], r1[kJ], ex1[kJ];
+                uint32_t row0[kJ];
+                auto fetch = [&](int t) {  // ids of stage t into id1 / r1; advances (q, r)
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) {
+                        id1[j] = t * kTK + tok_base + lane + 32 * j < len ? __ldg(ids + q[j]) : 0;
+                        r1[j] = r[j];
+                        q[j] += step_q;
+                        r[j] += step_r;
+                        if (r[j] >= p.page_size) { r[j] -= p.page_size; ++q[j]; }
+                    }
+                };
+                auto turn = [&](int t) -> bool {  // id1 / r1 of stage t into rows and exponents
+                    bool bad = false;
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) {
+                        const bool live = t * kTK + tok_base + lane + 32 * j < len;
+                        const bool in = (unsigned)id1[j] < (unsigned)p.num_pages;
+                        row0[j] = in ? (uint32_t)id1[j] * (uint32_t)p.page_size + (uint32_t)r1[j] : kBadRow;
+                        ex1[j] = live && in ? __ldg(exps + (size_t)id1[j] * p.H_kv + w.kv_head) : 0;
+                        bad |= live && !in;
+                    }
+                    if (bad) atomicCAS(status, 0, kStatusPageIndex);
+                    return __any_sync(0xffffffffu, bad);
+                };
+                bool bad = false;
+                if (nt > 0) {
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) {
+                        const int tok = w.kv_start + tok_base + lane + 32 * j;
+                        q[j] = tok / p.page_size;
+                        r[j] = tok - q[j] * p.page_size;
+                    }
+                    fetch(0);
+                    bad = turn(0);
+                    if (nt > 1) fetch(1);
+                }
+                for (int t = 0; t < nt; ++t) {
+                    uint32_t row[kJ];
+                    int ex[kJ];
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) { row[j] = row0[j]; ex[j] = ex1[j]; }
+                    const bool bad_now = bad;
+                    if (t + 1 < nt) {
+                        bad = turn(t + 1);
+                        if (t + 2 < nt) fetch(t + 2);
+                    }
+                    const bool ok = wait_or_abort(empty0 + 8 * st, ph, abort_flag, status, kStatusProducerWait);
+                    if (!__all_sync(0xffffffffu, ok)) break;  // warp-uniform: every lane leaves together
+                    const int n = min(kTK, len - t * kTK) - tok_base;  // tokens of this half
+                    // row 4i + sub: 128-byte rows, chunks swizzled by row & 7 = 4 (i & 1) + sub
+                    const uint32_t d0 = sbase + st * LY::kStageBytes + part + (uint32_t)(tok_base + sub) * 128;
+                    const uint32_t d_even = d0 + (uint32_t)((c16 ^ sub) << 4), d_odd = d0 + (uint32_t)((c16 ^ (4 + sub)) << 4);
+                    if (n >= kHalfTK && !bad_now) {
+#pragma unroll
+                        for (int i = 0; i < kHalfTK / 4; ++i) {
+                            const uint32_t rw = __shfl_sync(0xffffffffu, row[i >> 3], (4 * i + sub) & 31);
+                            cp_async_16((i & 1 ? d_odd : d_even) + i * 512, base + (size_t)rw * row_bytes, 16);
+                        }
+                    } else {
+#pragma unroll 4
+                        for (int i = 0; i < kHalfTK / 4; ++i) {
+                            uint32_t rw = 0;
+#pragma unroll
+                            for (int j = 0; j < kJ; ++j) {
+                                const uint32_t x = __shfl_sync(0xffffffffu, row[j], (4 * i + sub) & 31);
+                                if (j == i >> 3) rw = x;
+                            }
+                            const bool in = rw != kBadRow;
+                            if (4 * i + sub < n)
+                                cp_async_16((i & 1 ? d_odd : d_even) + i * 512, in ? base + (size_t)rw * row_bytes : src, in ? 16 : 0);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) ex_smem[st * 2 * LY::kExpN + tok_base + lane + 32 * j] = (uint8_t)ex[j];
+                    sm100::mbar_arrive(full0 + 8 * st);  // publishes this lane's exponents
+                    // arrive once this lane's copies have landed
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(full0 + 8 * st) : "memory");
+                    if (++st == kStages) { st = 0; ph ^= 1; }
+                }
+            }
+            asm volatile("cp.async.wait_all;\n" ::: "memory");  // nothing may still be in flight when the CTA exits
+            return;
+        }
+    }
+    if (kTma && !kBlk && warp >= kConsumers) {
         // ---------------- producers (TMA): warp 4 copies K, warp 5 V --------
         // Lane i issues box i of the stage (box_rows rows of one page, D / 64
         // tensor copies); lane 0 first posts the stage's byte count.
@@ -348,20 +521,6 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
             };
             int cur = nt > 0 ? fetch_batch(0) : 0;
             int nxt = spb < nt ? fetch_batch(1) : 0;
-            // kBlk: lane l < kExpN reads the exponent of tokens 8l .. 8l + 7 of a stage, one
-            // stage ahead of its copies; tokens past the chunk and bad pages have 0
-            auto fetch_exp = [&](int tt, int ids) -> int {
-                const int gpg = __shfl_sync(0xffffffffu, ids, (tt % spb) * bps + (lane < kTK / 8 ? lane * 8 / br : 0));
-                const bool in = lane < kTK / 8 && tt * kTK + lane * 8 < len && gpg >= 0 && gpg < p.num_pages;
-                return in ? __ldg((is_v ? p.v_exp : p.k_exp) + (size_t)gpg * p.H_kv + w.kv_head) : 0;
-            };
-            int ex_cur = 0, ex_nxt = 0;
-            if constexpr (kBlk) {
-                if (nt > 0) ex_nxt = fetch_exp(0, cur);
-            }
-            (void)fetch_exp;
-            (void)ex_cur;
-            (void)ex_nxt;
             for (int t = 0; t < nt; ++t, ++k) {
                 if (t > 0 && t % spb == 0) {
                     cur = nxt;
@@ -370,23 +529,13 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                 const int pg = __shfl_sync(0xffffffffu, cur, (t % spb) * bps + (lane < bps ? lane : 0));
                 const int n = min(kTK, len - t * kTK);
                 const int nbox = (n + br - 1) / br;
-                int row0 = pg * p.page_size + (w.kv_start + t * kTK + lane * br) % p.page_size;
-                if constexpr (kBlk) {
-                    ex_cur = ex_nxt;
-                    if (t + 1 < nt) ex_nxt = fetch_exp(t + 1, (t + 1) % spb == 0 ? nxt : cur);
-                    if (lane < nbox && (pg < 0 || pg >= p.num_pages)) {
-                        row0 = -br;  // a box outside the pool reads as zeros
-                        atomicCAS(status, 0, kStatusPageIndex);
-                    }
-                }
+                const int row0 = pg * p.page_size + (w.kv_start + t * kTK + lane * br) % p.page_size;
                 const int s = k % kStages;
                 const bool ok = wait_or_abort(empty0 + 8 * s, ((k / kStages) & 1) ^ 1, abort_flag, status,
                                               kStatusProducerWait);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                if constexpr (!kBlk) {
-                    if (lane == 0) sm100::mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(nbox * br * D * LY::kElem));
-                    __syncwarp();
-                }
+                if (lane == 0) sm100::mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(nbox * br * D * LY::kElem));
+                __syncwarp();
                 if (lane < nbox) {
                     const uint32_t dst = sbase + s * LY::kStageBytes + part + (uint32_t)(lane * br * 128);
 #pragma unroll
@@ -394,19 +543,11 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                         sm100::tma_load_3d(dst + h * LY::kSlab, map, full0 + 8 * s, h * (128 / LY::kElem), w.kv_head,
                                            row0);
                 }
-                if constexpr (kBlk) {
-                    // the copies are under way: their bytes may land before the arrival that
-                    // expects them, which also publishes the exponents
-                    if (lane < kTK / 8)
-                        smem[LY::kExpOff + (s * 2 + (is_v ? 1 : 0)) * LY::kExpN + lane] = (uint8_t)ex_cur;
-                    __syncwarp();
-                    if (lane == 0) sm100::mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(nbox * br * D * LY::kElem));
-                }
             }
         }
         return;
     }
-    if (!kTma && warp >= kConsumers) {
+    if (!kTma && !kBlk && warp >= kConsumers) {
         // ---------------- producers: warps 4, 5 copy K rows, warps 6, 7 V rows ----
         // Warp 4 (6) takes the first half of each stage's tokens, warp 5 (7) the
         // second. Each lane first turns the page ids of its tokens `lane` and
@@ -415,8 +556,6 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
         // D / 8 chunks of 16 bytes per row, taking the row offsets by shuffle.
         constexpr int C = D * LY::kElem / 16, T = 32 / C;
         constexpr int kHalfTK = kTK / 2;  // tokens of a stage per loader warp
-        constexpr uint64_t kBadRow = ~uint64_t(0);  // kBlk: offset of a token whose page id is outside the pool
-        (void)kBadRow;
         const bool is_v = warp >= kConsumers + 2;
         const int tok_base = ((warp - kConsumers) & 1) * kHalfTK;
         const char *src = static_cast<const char *>(is_v ? p.v : p.k);
@@ -440,26 +579,6 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                 }
             };
             if (nt > 0) fetch(0, pg);
-            // kBlk: page ids two stages ahead, exponents one: neither latency stands between
-            // a stage's copies and its arrival
-            int pg2[kJ], ex[kJ], ex2[kJ];
-            auto fetch_exp = [&](int t, const int (&ids)[kJ], int (&dst)[kJ]) {
-#pragma unroll
-                for (int jj = 0; jj < kJ; ++jj) {
-                    const bool in = t * kTK + tok_base + lane + 32 * jj < len && ids[jj] >= 0 && ids[jj] < p.num_pages;
-                    dst[jj] = in ? __ldg((is_v ? p.v_exp : p.k_exp) + (size_t)ids[jj] * p.H_kv + w.kv_head) : 0;
-                }
-            };
-            if constexpr (kBlk) {
-#pragma unroll
-                for (int jj = 0; jj < kJ; ++jj) pg2[jj] = 0;
-                if (nt > 1) fetch(1, pg2);
-                if (nt > 0) fetch_exp(0, pg, ex2);
-            }
-            (void)pg2;
-            (void)ex;
-            (void)ex2;
-            (void)fetch_exp;
             for (int t = 0; t < nt; ++t, ++k) {
                 // byte offsets of this lane's two rows, then the next tile's page ids
                 uint64_t off[kJ];
@@ -468,21 +587,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                     const int tok = w.kv_start + t * kTK + tok_base + lane + 32 * jj;
                     off[jj] = (((uint64_t)pg[jj] * p.page_size + tok % p.page_size) * p.H_kv + w.kv_head) * (D * LY::kElem);
                 }
-                if constexpr (kBlk) {
-#pragma unroll
-                    for (int jj = 0; jj < kJ; ++jj) {
-                        if (t * kTK + tok_base + lane + 32 * jj < len && (pg[jj] < 0 || pg[jj] >= p.num_pages)) {
-                            off[jj] = kBadRow;  // copied as zeros
-                            atomicCAS(status, 0, kStatusPageIndex);
-                        }
-                        ex[jj] = ex2[jj];
-                        pg[jj] = pg2[jj];
-                    }
-                    if (t + 1 < nt) fetch_exp(t + 1, pg, ex2);
-                    if (t + 2 < nt) fetch(t + 2, pg2);
-                } else {
-                    if (t + 1 < nt) fetch(t + 1, pg);
-                }
+                if (t + 1 < nt) fetch(t + 1, pg);
                 const int s = k % kStages;
                 const bool ok = wait_or_abort(empty0 + 8 * s, ((k / kStages) & 1) ^ 1, abort_flag, status,
                                               kStatusProducerWait);
@@ -495,18 +600,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                     const int j = tok_base + jl;                      // token within the stage
                     const int half = (i * T) >> 5;                    // same for the whole warp: T divides 32
                     const uint64_t o = __shfl_sync(0xffffffffu, off[half], jl & 31);
-                    if constexpr (kBlk) {
-                        const bool in = o != kBadRow;
-                        if (j < n) cp_async_16(dst + LY::chunk(j, my_chunk), in ? src + o + my_chunk * 16 : src, in ? 16 : 0);
-                    } else {
-                        if (j < n) cp_async_16(dst + LY::chunk(j, my_chunk), src + o + my_chunk * 16, 16);
-                    }
-                }
-                if constexpr (kBlk) {
-#pragma unroll
-                    for (int jj = 0; jj < kJ; ++jj)
-                        smem[LY::kExpOff + (s * 2 + (is_v ? 1 : 0)) * LY::kExpN + tok_base + lane + 32 * jj] = (uint8_t)ex[jj];
-                    sm100::mbar_arrive(full0 + 8 * s);  // publishes this lane's exponents
+                    if (j < n) cp_async_16(dst + LY::chunk(j, my_chunk), src + o + my_chunk * 16, 16);
                 }
                 // arrive on full[s] once this lane's copies have landed
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(full0 + 8 * s) : "memory");
