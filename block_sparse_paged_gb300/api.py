@@ -128,6 +128,7 @@ class PagedAttention:
         self.workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=self.device)
         self.staging = torch.zeros(st_bytes, dtype=torch.uint8, pin_memory=True)
         self._copied = None  # event after the last plan copy
+        self._q_tail, self._page_tail = (num_qo_heads, head_dim), (page_size, num_kv_heads, head_dim)
         self.info = None
 
     # ---- plan ---------------------------------------------------------------
@@ -181,6 +182,9 @@ class PagedAttention:
         without a value row (the attention-sink variant), or None."""
         if self.info is None:
             raise RuntimeError("plan() must be called before run()")
+        if k_exp is not None or v_exp is not None:
+            return self._run_fp8_block(q, k_pages, v_pages, k_exp, v_exp, kv_indices, sm_scale, out, lse, stream,
+                                       return_lse, k_scale, v_scale, sink)
         P = self.problem
         D = P.head_dim
         if q.dim() != 3 or q.shape[1] != P.num_qo_heads or q.shape[2] != D:
@@ -195,9 +199,6 @@ class PagedAttention:
             lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         dev = self.device
         fp8 = k_pages.dtype == torch.float8_e4m3fn
-        if k_exp is not None or v_exp is not None:
-            return self._run_fp8_block(q, k_pages, v_pages, k_exp, v_exp, kv_indices, sm_scale, out, lse, stream,
-                                       return_lse, k_scale, v_scale, sink)
         if fp8 and (self.mode != N.BSP_MODE_DECODE or self.dtype != torch.bfloat16):
             raise ValueError("e4m3 KV pools are read by the bf16 decode run only")
         kv_dt = torch.float8_e4m3fn if fp8 else self.dtype
@@ -224,35 +225,50 @@ class PagedAttention:
     def _run_fp8_block(self, q, k_pages, v_pages, k_exp, v_exp, kv_indices, sm_scale, out, lse, stream, return_lse,
                        k_scale, v_scale, sink):
         """run() over an e4m3 cache with one exponent per page and kv head."""
+        info, dev, f8, i8 = self.info, self.device, torch.float8_e4m3fn, torch.int8
         if k_exp is None or v_exp is None:
             raise ValueError("k_exp and v_exp are given together")
         if k_scale != 1.0 or v_scale != 1.0:
             raise ValueError("k_scale / v_scale do not apply to pools with exponents")
-        want = (k_pages.shape[0], k_pages.shape[2])
-        if k_exp.shape != want or v_exp.shape != want:
-            raise ValueError(f"k_exp / v_exp must be [{want[0]}, {want[1]}]")
-        if self.dtype != torch.bfloat16:
+        if self.dtype is not torch.bfloat16:
             raise ValueError("pools with exponents are read by bfloat16 problems")
-        dev, f8, i8 = self.device, torch.float8_e4m3fn, torch.int8
+        q_shape, pool = q.shape, k_pages.shape
+        if q_shape[1:] != self._q_tail or q_shape[0] < info.num_qo_tokens:
+            raise ValueError(f"q must be [n_tokens, {self._q_tail[0]}, {self._q_tail[1]}] with the plan's tokens")
+        if pool[1:] != self._page_tail or v_pages.shape != pool:
+            raise ValueError("k_pages / v_pages must be [num_pages, %d, %d, %d]" % self._page_tail)
+        if k_exp.shape != (pool[0], pool[2]) or v_exp.shape != k_exp.shape:
+            raise ValueError(f"k_exp / v_exp must be [{pool[0]}, {pool[2]}]")
+        if kv_indices.dim() != 1 or kv_indices.shape[0] < info.num_table_pages:
+            raise ValueError(f"kv_indices must hold the plan's {info.num_table_pages} pages")
+        if out is None:
+            out = torch.empty_like(q)
+        elif out.shape != q_shape:
+            raise ValueError("out must have the shape of q")
+        if lse is None:
+            if return_lse:
+                lse = torch.empty(q_shape[:2], dtype=torch.float32, device=dev)
+        elif lse.shape != q_shape[:2]:
+            raise ValueError("lse must be [n_tokens, H_qo]")
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(self._q_tail[1])
         self._set_sink(sink)
-        info = ctypes.byref(self.info)
-        region = ()
+        ref = ctypes.byref(info)
+        args = (ref, _addr(q, "q", torch.bfloat16, dev), _addr(k_pages, "k_pages", f8, dev),
+                _addr(v_pages, "v_pages", f8, dev), _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev),
+                _addr(kv_indices, "kv_indices", torch.int32, dev) or None, pool[0], sm_scale,
+                _addr(out, "out", torch.bfloat16, dev),
+                None if lse is None else _addr(lse, "lse", torch.float32, dev))
         if self.mode == N.BSP_MODE_DECODE:
-            fn = self.lib.bsp_decode_run_fp8_block
+            _call(dev, stream, self.lib.bsp_decode_run_fp8_block, *args, self.workspace.data_ptr())
         else:
-            fn = self.lib.bsp_prefill_run_fp8_block
-            nbytes = self.lib.bsp_prefill_fp8_region_size(info)
+            nbytes = self.lib.bsp_prefill_fp8_region_size(ref)
             copy = None
             if nbytes:  # a bf16 copy of the plan's pages, for this run alone
                 with torch.cuda.stream(stream):  # (None: the current one)
                     copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            region = (None if copy is None else copy.data_ptr(), nbytes)
-        _call(dev, stream, fn, info, _addr(q, "q", self.dtype, dev),
-              _addr(k_pages, "k_pages", f8, dev), _addr(v_pages, "v_pages", f8, dev), _addr(k_exp, "k_exp", i8, dev),
-              _addr(v_exp, "v_exp", i8, dev),
-              _addr(kv_indices, "kv_indices", torch.int32, dev) if kv_indices.numel() else None, want[0], sm_scale,
-              _addr(out, "out", self.dtype, dev), None if lse is None else _addr(lse, "lse", torch.float32, dev), *region,
-              self.workspace.data_ptr())
+            _call(dev, stream, self.lib.bsp_prefill_run_fp8_block, *args, None if copy is None else copy.data_ptr(),
+                  nbytes, self.workspace.data_ptr())
         return (out, lse) if return_lse else out
 
     def _set_sink(self, sink):
@@ -332,6 +348,7 @@ def _addr(t: torch.Tensor, name: str, dtype, dev: torch.device) -> int:
 
 def _call(dev: torch.device, stream, fn, *args):
     """fn(*args, stream handle) with `dev` current, on `stream` or dev's current stream."""
+    # (the handle of torch.cuda.current_stream(dev), without making the object)
     handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -379,11 +396,14 @@ def build_page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pa
     max_table_pages / max_new_tokens: sizes of kv_indices and of slot_map and
     positions, whose tails are filled with 0, -1 and 0. Nothing is read back: whether
     all fitted stands in counts[3]."""
-    if block_table.dim() != 2 or (block_table.numel() and block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    if block_table.dim() != 2:
         raise ValueError("block_table must be [B, width] with adjacent entries in a row")
     B, width = block_table.shape
+    stride, step = block_table.stride()
+    if step != 1 and B > 0 and width > 1:
+        raise ValueError("block_table must be [B, width] with adjacent entries in a row")
     dev = block_table.device
-    if not block_table.is_cuda or block_table.dtype != torch.int32:
+    if not block_table.is_cuda or block_table.dtype is not torch.int32:
         raise ValueError("block_table must be a CUDA tensor of torch.int32")
     if cached_lens.shape != (B,) or new_lens.shape != (B,):
         raise ValueError(f"cached_lens and new_lens must be [{B}]")
@@ -391,13 +411,13 @@ def build_page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pa
         raise ValueError("free_pages must be one-dimensional and num_free hold one value")
     if out is None:
         out = PageTables.empty(B, max_table_pages, max_new_tokens, dev)
-    sizes = (B + 1, B, max_table_pages, B + 1, max_new_tokens, max_new_tokens, 4)
     i32 = torch.int32
     o = [_addr(t, f, d, dev) for t, f, d in zip(out, PageTables._fields, _TABLE_DTYPES)]
-    for t, n, f in zip(out, sizes, PageTables._fields):
-        if t.numel() != n or t.dim() != 1:
-            raise ValueError(f"out.{f} must be [{n}]")
-    stride = block_table.stride(0) if B > 1 else max(width, block_table.stride(0))
+    sizes = [B + 1, B, max_table_pages, B + 1, max_new_tokens, max_new_tokens, 4]
+    if [t.numel() for t in out] != sizes:
+        raise ValueError(f"out must hold {sizes} values (PageTables.empty)")
+    if B <= 1:
+        stride = max(width, stride)
     _call(dev, stream, N.load().bsp_build_page_tables, B, page_size, _addr(cached_lens, "cached_lens", i32, dev),
           _addr(new_lens, "new_lens", i32, dev), _addr(free_pages, "free_pages", i32, dev), free_pages.numel(),
           _addr(num_free, "num_free", i32, dev), block_table.data_ptr(), stride, width, o[0], o[1], o[2],
@@ -420,7 +440,8 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pages:
     n = k.shape[0]
     if k.shape != (n, H, D) or v.shape != k.shape or v.dtype != k.dtype or k.dtype not in _DTYPES:
         raise ValueError(f"k and v must be [n, {H}, {D}] in bfloat16 or float32, of one type")
-    if k.stride(2) != 1 or v.stride(2) != 1:
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1:
         raise ValueError("the values of a row of k and v must be adjacent")
     if slot_map.shape != (n,):
         raise ValueError(f"slot_map must be [{n}]")
@@ -431,7 +452,10 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pages:
         raise ValueError(f"k and v must be CUDA tensors on {dev}")
     f8, i8 = torch.float8_e4m3fn, torch.int8
     # a dimension of size 1 is never stepped over: its stride says nothing
-    st = [t.stride(i) if t.shape[i] > 1 else 0 for t in (k, v) for i in (0, 1)]
-    _call(dev, stream, N.load().bsp_append_kv_fp8, k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], st[3],
+    if n == 1:
+        ks, vs = (0,) + ks[1:], (0,) + vs[1:]
+    if H == 1:
+        ks, vs = (ks[0], 0), (vs[0], 0)
+    _call(dev, stream, N.load().bsp_append_kv_fp8, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
           _DTYPES[k.dtype], n, _addr(slot_map, "slot_map", torch.int64, dev), _addr(k_pages, "k_pages", f8, dev),
           _addr(v_pages, "v_pages", f8, dev), _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev), P, ps, H, D)

@@ -302,8 +302,9 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
     volatile int *pending = abort_flag + 2;
 
     // Rows past a chunk's end are never copied: zero the ring once so that
-    // they hold finite values (their probabilities are exactly 0).
-    for (int i = tid; i < LY::kRingBytes / 16; i += kWsThreads) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+    // they hold finite values (their probabilities are exactly 0). (kBlk: the consumers
+    // zero what they read of V past a chunk's end themselves.)
+    for (int i = kBlk ? LY::kRingBytes : tid; i < LY::kRingBytes / 16; i += kWsThreads) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
     sm100::fence_proxy_async_smem();
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {

@@ -66,10 +66,6 @@ constexpr int kThreads = 320;     // warp 0 TMA, warp 1 MMA, warps 2-9 softmax
 // cannot keep enough 16-byte copies in flight)
 constexpr int kThreadsGather = 352;
 constexpr int kVWarp = 10;
-// e4m3 cache: warp 0 copies Q alone, warps 10 and 11 read K's and V's codes and write
-// them converted into the rings
-constexpr int kThreadsFp8 = 384;
-constexpr int kCvtWarp = 10;
 constexpr int kHalf = 16384;      // [128 rows][64 bf16], 128-byte swizzle
 constexpr int kTile = 2 * kHalf;  // [128 rows][128 bf16]
 
@@ -143,6 +139,12 @@ __device__ __forceinline__ void fma2_bcast(float &d0, float &d1, float a0, float
         : "=f"(d0), "=f"(d1)
         : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
+__device__ __forceinline__ void mul2_bcast(float &d0, float &d1, float a0, float a1, float b) {
+    asm("{ .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %4};\n mul.rn.f32x2 rd, ra, rb;\n"
+        " mov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b));
+}
 __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1) {
     asm("{ .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rd, ra, rb;\n"
         " mov.b64 {%0, %1}, rd;\n}"
@@ -162,6 +164,12 @@ __device__ __forceinline__ int ld_nc_s32(const int *p) {
     return v;
 }
 
+__device__ __forceinline__ int ld_nc_s8(const int8_t *p) {
+    int v;
+    asm volatile("ld.global.nc.s8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -176,7 +184,10 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, float s) {
     dev::e4m3x4_to_f16x4(w, h0, h1);
     const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
     const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
-    return make_uint2(dev::pack_bf16(a.x * s, a.y * s), dev::pack_bf16(b.x * s, b.y * s));
+    float x0, x1, y0, y1;
+    mul2_bcast(x0, x1, a.x, a.y, s);
+    mul2_bcast(y0, y1, b.x, b.y, s);
+    return make_uint2(dev::pack_bf16(x0, x1), dev::pack_bf16(y0, y1));
 }
 
 // kTma: K and V tiles arrive by TMA tensor copies, one per page box (pages of
@@ -185,10 +196,11 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, float s) {
 // kVar: the sliding window and logits soft-cap variants are compiled in (the
 // default instantiation has neither, at no cost).
 // kFp8 (with kTma false): K and V are e4m3 codes with an exponent per (page, kv
-// head), converted to bf16 on their way into the tiles; everything behind the rings
-// is the bf16 kernel.
+// head), converted to bf16 on their way into the tiles by the softmax warps, in the
+// time in which they would wait for their next S; everything behind the rings is the
+// bf16 kernel.
 template <bool kTma, bool kVar, bool kFp8 = false>
-__global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTma ? kThreads : kThreadsGather, 1)
+__global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const PrefillParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -211,7 +223,8 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTma ? kThreads : kThread
         for (int i = 0; i < kNumBars; ++i) {
             const bool softmax_arrivals = i == kPFull0 || i == kPFull1 || i == kOFree0 || i == kOFree1;
             const bool kv_full = (i >= kKFull0 && i < kKFull0 + kKStages) || (i >= kVFull0 && i < kVFull0 + kVStages);
-            mbar_init(bar(i), softmax_arrivals ? 128 : (kv_full && !kTma) ? 32 : 1);  // cp.async: one per lane
+            // cp.async: one per lane; e4m3: one per converting warp
+            mbar_init(bar(i), softmax_arrivals ? 128 : (kv_full && !kTma) ? (kFp8 ? 4 : 32) : 1);
         }
         *ctx.abort_flag = 0;
         fence_barrier_init();
@@ -265,7 +278,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTma ? kThreads : kThread
                 }
             };
             (void)lookup;
-            if constexpr (kFp8) continue;  // K and V: the converting warps
+            if constexpr (kFp8) continue;  // K and V: the softmax warps
             for (int t = 0; t < nt; ++t, ++j) {
                 const int tok0 = w.kv_start + t * kKvTile;
                 const int valid = min(kKvTile, len - t * kKvTile);
@@ -336,91 +349,6 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTma ? kThreads : kThread
             }
         }
         if constexpr (!kTma) asm volatile("cp.async.wait_all;\n" ::: "memory");  // nothing in flight at exit
-    } else if (kFp8 && warp >= kCvtWarp) {
-        // ------------------------------------------- K (warp 10) and V (warp 11), e4m3
-        // Lane l looks up the pages and exponents of keys l + 32 i one tile ahead. Each
-        // warp-wide load then takes the codes of four keys (8 lanes x 16 codes), eight
-        // loads in flight, the next eight issued before these are converted; a lane's 16
-        // values are two 16-byte chunks of its key's swizzled row. Keys past the chunk end
-        // are written as zeros (P = 0 there must meet finite values of V).
-        constexpr int kBatch = 8;
-        constexpr int kNB = kKvTile / 4 / kBatch;
-        const bool is_v = warp == kCvtWarp + 1;
-        const char *src = is_v ? p.v : p.k;
-        const int8_t *exps = is_v ? p.v_exp : p.k_exp;
-        const uint32_t ring = sb + (is_v ? kOffV : kOffK);
-        const int full0 = is_v ? kVFull0 : kKFull0, empty0 = is_v ? kVEmpty0 : kKEmpty0;
-        static_assert(kKStages == kVStages, "one ring position for both");
-        constexpr long long kNoRow = -1;
-        const int c = lane & 7, sub4 = lane >> 3;
-        const bool hi = c >= 4;  // these lanes store their second chunk first: no bank is met twice
-        int j = 0;
-        bool ok = true;
-        for (int it = it0; it < it1 && ok; ++it) {
-            const bsp_work_item w = items[it];
-            const int len = w.kv_end - w.kv_start;
-            const int nt = (len + kKvTile - 1) / kKvTile;
-            int pg[kKvTile / 32], ex[kKvTile / 32];
-            auto lookup = [&](int tt) {
-#pragma unroll
-                for (int i = 0; i < kKvTile / 32; ++i) {
-                    const int key = tt * kKvTile + lane + 32 * i;
-                    pg[i] = key < len ? __ldg(p.kv_indices + w.page_base + (w.kv_start + key) / p.page_size) : -1;
-                    if (key < len && (pg[i] < 0 || pg[i] >= p.num_pages)) {
-                        pg[i] = -1;
-                        atomicCAS(ctx.status, 0, kStatusPageIndex);
-                    }
-                    ex[i] = pg[i] >= 0 ? __ldg(exps + (size_t)pg[i] * p.H_kv + w.kv_head) : 0;
-                }
-            };
-            if (nt > 0) lookup(0);
-            for (int t = 0; t < nt; ++t, ++j) {
-                const int tok0 = w.kv_start + t * kKvTile;
-                const int st = j % kKStages, rd = j / kKStages;
-                long long off[kKvTile / 32];
-                float scale[kKvTile / 32];
-#pragma unroll
-                for (int i = 0; i < kKvTile / 32; ++i) {
-                    off[i] = pg[i] >= 0 ? (((long long)pg[i] * p.page_size + (tok0 + lane + 32 * i) % p.page_size) *
-                                               p.H_kv + w.kv_head) * kD
-                                        : kNoRow;
-                    scale[i] = __int_as_float(ex[i] >= -126 ? (ex[i] + 127) << 23 : 0x00400000 >> (-127 - ex[i]));
-                }
-                auto load = [&](uint4 (&d)[kBatch], int b) {
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int key = 4 * (b * kBatch + i) + sub4;  // key >> 5 == b: the same for the whole batch
-                        const long long o = __shfl_sync(0xffffffffu, off[b], key & 31);
-                        d[i] = make_uint4(0, 0, 0, 0);
-                        if (o != kNoRow) d[i] = __ldg(reinterpret_cast<const uint4 *>(src + o) + c);
-                    }
-                };
-                static_assert(4 * kBatch == 32, "a batch is the 32 keys of one lookup register");
-                uint4 d[2][kBatch];
-                load(d[0], 0);
-                if (!(ok = wait_bar_warp(ctx, bar(empty0 + st), (rd & 1) ^ 1))) break;
-                const uint32_t dst = ring + st * kTile;
-#pragma unroll
-                for (int b = 0; b < kNB; ++b) {
-                    if (b + 1 < kNB) load(d[(b + 1) & 1], b + 1);
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int key = 4 * (b * kBatch + i) + sub4;
-                        const float s = __shfl_sync(0xffffffffu, scale[b], key & 31);
-                        const uint4 x = d[b & 1][i];
-                        const uint2 a0 = e4m3x4_to_bf16x4(hi ? x.z : x.x, s), a1 = e4m3x4_to_bf16x4(hi ? x.w : x.y, s);
-                        const uint2 b0 = e4m3x4_to_bf16x4(hi ? x.x : x.z, s), b1 = e4m3x4_to_bf16x4(hi ? x.y : x.w, s);
-                        const uint32_t row = dst + (c >> 2) * kHalf + key * 128;
-                        const int cc = (2 * c + (hi ? 1 : 0)) & 7;
-                        st_shared_v4(row + ((cc ^ (key & 7)) << 4), a0.x, a0.y, a1.x, a1.y);
-                        st_shared_v4(row + (((cc ^ 1) ^ (key & 7)) << 4), b0.x, b0.y, b1.x, b1.y);
-                    }
-                }
-                if (t + 1 < nt) lookup(t + 1);
-                fence_proxy_async_smem();
-                mbar_arrive(bar(full0 + st));
-            }
-        }
     } else if (!kTma && !kFp8 && warp == kVWarp) {
         // ------------------------------------------------ V gather (cp.async)
         // The same items and tiles as warp 0, V rows only: lane l looks up keys
@@ -579,6 +507,99 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTma ? kThreads : kThread
         float *po = reinterpret_cast<float *>(const_cast<uint8_t *>(p.ws) + p.off_po);
         int s_cnt = 0, o_cnt = 0, j = 0;
         bool ok = true;
+        // e4m3 cache: the group of subtile 0 converts K tiles, that of subtile 1 V tiles, 32
+        // keys per warp, two tiles ahead of the one that it works on (the rings' depth), over
+        // the CTA's items as one sequence. The codes come by cp.async into the warp's staging
+        // buffer, one tile ahead of their conversion (read straight into registers they cost
+        // 3,000-4,600 cycles of waiting per tile); page ids one tile before that. A warp-wide
+        // copy takes the codes of four keys (8 lanes x 16 codes), each lane reads back what it
+        // copied, and its 16 values become two 16-byte chunks of the key's swizzled row. Keys
+        // past the chunk's end are written as zeros (P = 0 there must meet finite values of V).
+        // The epilogue uses the staging buffer too: the copies of an item's last tile wait for it.
+        constexpr uint32_t kNoRow = ~0u;
+        int c_it = it0 - 1, c_t = 0, c_nt = 0, c_start = 0, c_end = 0, c_base = 0, c_head = 0, c_n = 0;
+        int c_pg = 0, c_off = -1;  // page id and place of this lane's key (-1: none)
+        auto look_up = [&]() {     // the next tile of the sequence: its item, this lane's key
+            while (c_t >= c_nt) {
+                if (++c_it >= it1) return;
+                c_start = items[c_it].kv_start;
+                c_end = items[c_it].kv_end;
+                c_base = items[c_it].page_base;
+                c_head = items[c_it].kv_head;
+                c_nt = (c_end - c_start + kKvTile - 1) / kKvTile;
+                c_t = 0;
+            }
+            const int tok = c_start + c_t * kKvTile + q4 * 32 + lane;
+            c_off = -1;
+            if (tok < c_end) {
+                const int col = tok / p.page_size;
+                c_off = tok - col * p.page_size;
+                c_pg = ld_nc_s32(p.kv_indices + c_base + col);
+            }
+        };
+        bool raw_live = false;  // the staging buffer holds (or awaits) a tile's codes
+        int raw_e = 0;          // the exponent of this lane's key of that tile
+        const uint32_t raw = sb + kOffStg + (warp - 2) * kStgWarp + (lane >> 3) * 128 + (lane & 7) * 16;
+        auto fetch_raw = [&]() {  // the looked-up tile's codes on their way, then the next look-up
+            raw_live = c_it < it1;
+            if (!raw_live) return;
+            uint32_t row = kNoRow;
+            raw_e = 0;
+            if (c_off >= 0) {
+                if ((unsigned)c_pg < (unsigned)p.num_pages) {
+                    row = (uint32_t)c_pg * (uint32_t)p.page_size + (uint32_t)c_off;
+                    raw_e = ld_nc_s8((sub == 0 ? p.k_exp : p.v_exp) + (size_t)c_pg * p.H_kv + c_head);
+                } else {
+                    atomicCAS(ctx.status, 0, kStatusPageIndex);
+                }
+            }
+            const char *src = (sub == 0 ? p.k : p.v) + (size_t)c_head * kD + (lane & 7) * 16;
+            const uint32_t row_bytes = (uint32_t)p.H_kv * kD;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t r = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
+                const bool in = r != kNoRow;
+                dev::cp_async_16(raw + i * 512, in ? src + (size_t)r * row_bytes : src, in ? 16 : 0);
+            }
+            dev::cp_async_commit();
+            ++c_t;
+            look_up();
+        };
+        auto convert = [&](bool more) -> bool {
+            if (!raw_live) return true;
+            const int st = c_n % kKStages, rd = c_n / kKStages;
+            ++c_n;
+            dev::cp_async_wait<0>();
+            if (!wait_bar_warp(ctx, bar((sub == 0 ? kKEmpty0 : kVEmpty0) + st), (rd & 1) ^ 1)) return false;
+            const float scale = __int_as_float(raw_e >= -126 ? (raw_e + 127) << 23 : 0x00400000 >> (-127 - raw_e));
+            const int c = lane & 7;
+            const bool hi = c >= 4;  // these lanes store their second chunk first: no bank is met twice
+            const int cc = (2 * c + (hi ? 1 : 0)) & 7, k7 = lane >> 3;
+            // key 32 q4 + 4 i + k7: chunks swizzled by key & 7 = 4 (i & 1) + k7
+            const uint32_t dst = sb + (sub == 0 ? kOffK : kOffV) + st * kTile + (c >> 2) * kHalf + (q4 * 32 + k7) * 128;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float s = __shfl_sync(0xffffffffu, scale, 4 * i + (lane >> 3));
+                const uint4 d = ld_shared_v4(raw + i * 512);
+                const uint2 a0 = e4m3x4_to_bf16x4(hi ? d.z : d.x, s), a1 = e4m3x4_to_bf16x4(hi ? d.w : d.y, s);
+                const uint2 b0 = e4m3x4_to_bf16x4(hi ? d.x : d.z, s), b1 = e4m3x4_to_bf16x4(hi ? d.y : d.w, s);
+                const int sw = cc ^ (4 * (i & 1) + k7);
+                st_shared_v4(dst + i * 512 + (sw << 4), a0.x, a0.y, a1.x, a1.y);
+                st_shared_v4(dst + i * 512 + ((sw ^ 1) << 4), b0.x, b0.y, b1.x, b1.y);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar((sub == 0 ? kKFull0 : kVFull0) + st));
+            raw_live = false;
+            if (more) fetch_raw();
+            return true;
+        };
+        if constexpr (kFp8) {
+            static_assert(kKStages == 2 && kVStages == 2, "two tiles ahead");
+            look_up();
+            fetch_raw();
+            ok = convert(true) && convert(true);
+        }
         for (int it = it0; it < it1 && ok; ++it) {
             const bsp_work_item w = items[it];
             const int len = w.kv_end - w.kv_start;
@@ -689,6 +710,9 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTma ? kThreads : kThread
                 }
                 tc_fence_before();
                 mbar_arrive(bar(kPFull0 + sub));
+                if constexpr (kFp8) {
+                    if (!(ok = convert(t + 1 < nt))) break;
+                }
             }
             if (!ok) break;
             // ---- epilogue: O / l, LSE; final output or partial state ----
@@ -720,7 +744,14 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTma ? kThreads : kThread
             const size_t prow = (size_t)w.slot * p.tile_rows + rt;
             const int n_rows = w.n_pos * g;  // real rows of the tile
             if (p.sink && w.slot < 0 && rt < n_rows) inv *= dev::fold_sink(lse_v, p.sink[w.kv_head * g + rt % g]);
-            if (w.slot < 0) {
+            if (kFp8 && w.slot < 0 && nt == 0) {
+                // no key: zeros, straight to memory (the staging may hold the next tile's codes)
+                if (rt < n_rows) {
+#pragma unroll
+                    for (int q = 0; q < kD / 8; ++q)
+                        reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + orow * kD)[q] = make_uint4(0, 0, 0, 0);
+                }
+            } else if (w.slot < 0) {
                 // bf16 output through this warp's swizzled staging, 64 columns at a
                 // time: each thread writes its row, then every store instruction
                 // covers four whole 128-byte lines (lane l: row 4i + l/8, chunk l%8)
@@ -764,7 +795,11 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kTma ? kThreads : kThread
                     plse[prow] = lse_v;
                 }
             }
+            if constexpr (kFp8) {
+                if (nt > 0) fetch_raw();  // the staging is free again
+            }
         }
+        if constexpr (kFp8) dev::cp_async_wait<0>();  // nothing in flight at exit
     }
 
     __syncwarp();
@@ -1024,7 +1059,7 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
     p.num_queues = plan->capacity.num_ctas;
     p.queues_per_cta = (p.num_queues + sms - 1) / sms;
     const int grid = (p.num_queues + p.queues_per_cta - 1) / p.queues_per_cta;
-    kern<<<grid, fp8 ? kThreadsFp8 : tma ? kThreads : kThreadsGather, kSmemBytes, stream>>>(tq, tk, tv, p);
+    kern<<<grid, tma || fp8 ? kThreads : kThreadsGather, kSmemBytes, stream>>>(tq, tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("prefill launch: ") + cudaGetErrorString(e));
     return BSP_OK;
