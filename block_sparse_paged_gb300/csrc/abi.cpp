@@ -115,9 +115,14 @@ extern "C" int bsp_prefill_run(const bsp_plan_info *plan, const void *q, const v
 
 namespace {
 
-// Prefill over the 8-bit cache converts it into a bf16 copy first where at least this
-// many query tiles read a cached token on average.
-constexpr int64_t kRegionTiles = 1;
+// Prefill over the 8-bit cache converts the plan's pages into a bf16 copy first where a
+// cached token is read by 1.5 query tiles or more on average and a CTA has four 128-key
+// tiles or more to work on. Measured (copy first / converted inside the kernel): 2 tiles
+// per token, 16 x 8192 tokens 358 / 461 us, 24 tiles, 16 x 1536 343 / 563 us; one tile
+// per token, 16 x 8192 267 / 254 us, 1 x 32768 75 / 64 us; under a wave of work, 2 x 150
+// tokens 19.5 / 16.4 us (a launch less).
+constexpr int64_t kRegionReads2 = 3;       // twice the query tiles per cached token
+constexpr int64_t kRegionTokens = 4 * 128;  // KV tokens of work per CTA
 
 int check_fp8_block(const bsp_plan_info *plan, int mode, const void *q, const void *k_pages, const void *v_pages,
                     const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
@@ -149,8 +154,9 @@ extern "C" size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan) {
     if (!plan || plan->problem.mode != BSP_MODE_PREFILL || plan->num_table_pages <= 0) return 0;
     const int64_t tokens = (int64_t)plan->num_table_pages * plan->problem.page_size;
     if (tokens > INT32_MAX) return 0;
-    // query tiles that read a cached token, on average
-    if (plan->total_work < kRegionTiles * tokens * plan->problem.num_kv_heads) return 0;
+    if (2 * plan->total_work < kRegionReads2 * tokens * plan->problem.num_kv_heads ||
+        plan->total_work < kRegionTokens * plan->capacity.num_ctas)
+        return 0;
     return (size_t)tokens * plan->problem.num_kv_heads * 512;
 }
 

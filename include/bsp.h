@@ -486,8 +486,9 @@ int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const vo
                               void *workspace, bsp_stream_t stream);
 
 /* Bytes of the region that bsp_prefill_run_fp8_block wants for this plan (a bf16
- * copy of its page table's K and V), or 0 where few query tiles read each cached
- * token and converting inside the attention kernel is faster. */
+ * copy of its page table's K and V), or 0 where converting inside the attention
+ * kernel is faster: under 1.5 query tiles per cached token on average, or under
+ * four 128-key tiles of work per CTA. */
 size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan);
 
 /*

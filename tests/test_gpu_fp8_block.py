@@ -179,7 +179,7 @@ def test_region_too_small_for_a_later_plan(bsp):
     """A captured run whose region holds the captured plan's pages, replayed after a plan with more: the status word."""
     a = workloads.paged_batch(240, [300], [300], 8, 2, 128, 16, "bf16", causal=True)
     b = workloads.paged_batch(241, [300], [900], 8, 2, 128, 16, "bf16", causal=True)
-    pa = bsp.PagedAttention("prefill", 8, 2, 128, 16, True, torch.bfloat16, max_batch=1, max_qo_tokens=300)
+    pa = bsp.PagedAttention("prefill", 8, 2, 128, 16, True, torch.bfloat16, max_batch=1, max_qo_tokens=300, num_ctas=4)
     k8, ke, v8, ve = (torch.from_numpy(x).cuda() for x in cache8(b, 241))
     f8 = torch.float8_e4m3fn
     idx = torch.arange(60, dtype=torch.int32, device="cuda")

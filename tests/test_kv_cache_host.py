@@ -179,10 +179,10 @@ def test_block_runs_refuse_plans(native, mode):
 
 
 def test_region_size_and_refusals(native):
-    """A region is wanted where query tiles read every cached token, and must hold the page table."""
+    """A region is wanted where query tiles read cached tokens often enough, and must hold the page table."""
     lib = native.load()
     info = block_plan(1, H=8, Hkv=2)
-    assert lib.bsp_prefill_fp8_region_size(ctypes.byref(info)) in (0, 3 * 16 * 2 * 512)
+    assert lib.bsp_prefill_fp8_region_size(ctypes.byref(info)) == 0               # one tile per request
     import torch
     import block_sparse_paged_gb300 as bsp
     prob = bsp.make_problem(1, 8, 2, 128, 16, True, torch.bfloat16)
