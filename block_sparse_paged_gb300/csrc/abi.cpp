@@ -132,6 +132,8 @@ int check_fp8_block(const bsp_plan_info *plan, int mode, const void *q, const vo
     if (rc != BSP_OK) return rc;
     if (!q || !k_pages || !v_pages || !k_exp || !v_exp || !o) return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
     if (num_pages < 1 || num_pages > INT32_MAX) return fail(BSP_ERR_INVALID_ARG, "num_pages must be in [1, 2^31 - 1]");
+    if (num_pages * plan->problem.page_size >= UINT32_MAX)
+        return fail(BSP_ERR_UNSUPPORTED, "the 8-bit cache takes at most 2^32 - 2 slots");
     if (!kv_indices && plan->num_table_pages > 0)
         return fail(BSP_ERR_INVALID_ARG, "kv_indices is NULL but the page table has pages");
     return check_aligned16(q, k_pages, v_pages, o, workspace);
@@ -268,8 +270,8 @@ extern "C" int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_s
     if (head_dim != 128) return fail(BSP_ERR_UNSUPPORTED, "the e4m3 cache has head_dim 128");
     if (n_tokens < 0 || num_pages < 1 || num_pages > INT32_MAX || page_size < 1 || num_kv_heads < 1)
         return fail(BSP_ERR_INVALID_ARG, "bad append sizes");
-    if (num_kv_heads > 32767 || n_tokens > INT32_MAX)
-        return fail(BSP_ERR_UNSUPPORTED, "append takes at most 32767 kv heads and 2^31 - 1 tokens");
+    if (num_kv_heads > 32767 || n_tokens > INT32_MAX || num_pages * page_size >= UINT32_MAX)
+        return fail(BSP_ERR_UNSUPPORTED, "append takes at most 32767 kv heads, 2^31 - 1 tokens and 2^32 - 2 slots");
     if (n_tokens == 0) return BSP_OK;
     if (!k || !v || !slot_map || !k_pages || !v_pages || !k_exp || !v_exp)
         return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");

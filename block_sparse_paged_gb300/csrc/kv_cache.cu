@@ -257,7 +257,6 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
 // token writes it and rescales the codes that the page held before. A CTA that
 // reads the exponent after that write gets max(need, e) = e: the same.
 constexpr int kAppTokens = 128;
-constexpr int kAppLoads = 8;  // 16-byte loads in flight per lane
 constexpr int kExpMin = -117, kExpMax = 119;
 constexpr int kCacheD = 128;
 
@@ -305,65 +304,79 @@ __device__ __forceinline__ uint32_t e4m3x2_scaled(float lo, float hi, float s) {
     return e4m3x2(lo, hi);
 }
 
-// One lane's 16-byte piece of a token row: 8 bf16 or 4 fp32 values.
+// One lane's piece of a token row: 8 values of 128, 16 lanes to a row, as one (bf16) or
+// two (fp32) 16-byte vectors.
+constexpr int kPieceLanes = 16, kPer = 32 / kPieceLanes;  // lanes per row, rows per warp-wide load
 template <bool kF32>
 struct Piece {
-    static constexpr int kN = kF32 ? 4 : 8;
-    static constexpr int kLanes = kCacheD / kN;              // lanes per token row
-    static constexpr int kPer = 32 / kLanes;                 // tokens per warp-wide load
-    static constexpr int kPerWarp = kAppLoads * kPer;        // tokens per warp
-    static constexpr int kWarps = kAppTokens / kPerWarp;     // 8 (bf16), 16 (fp32)
+    static constexpr int kVecs = kF32 ? 2 : 1;
+    static constexpr int kLoads = kF32 ? 4 : 8;               // rows in flight per lane: 32 registers
+    static constexpr int kPerWarp = kLoads * kPer;            // tokens per warp
+    static constexpr int kWarps = kAppTokens / kPerWarp;      // 8 (bf16), 16 (fp32)
+    uint4 w[kVecs];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void load(const char *p) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    }
     // largest |value| as fp32 bits; infinities and NaN included (>= 0x7f800000)
-    __device__ static __forceinline__ uint32_t amax(const uint4 &w) {
+    __device__ __forceinline__ uint32_t amax() const {
         if constexpr (kF32) {
             constexpr uint32_t m = 0x7fffffffu;
-            return max(max(w.x & m, w.y & m), max(w.z & m, w.w & m));
+            return max(max(max(w[0].x & m, w[0].y & m), max(w[0].z & m, w[0].w & m)),
+                       max(max(w[1].x & m, w[1].y & m), max(w[1].z & m, w[1].w & m)));
         } else {
             constexpr uint32_t m = 0x7fff7fffu;
-            const uint32_t a = max2(max2(w.x & m, w.y & m), max2(w.z & m, w.w & m));
+            const uint32_t a = max2(max2(w[0].x & m, w[0].y & m), max2(w[0].z & m, w[0].w & m));
             return max(a << 16, a & 0xffff0000u);
         }
     }
-    __device__ static __forceinline__ void values(const uint4 &w, float (&f)[kN]) {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    __device__ __forceinline__ void values(float (&f)[8]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (kF32) {
-                f[i] = __uint_as_float(u[i]);
-            } else {
-                f[2 * i] = dev::bf16_lo(u[i]);
-                f[2 * i + 1] = dev::bf16_hi(u[i]);
+        for (int v = 0; v < kVecs; ++v) {
+            const uint32_t u[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kF32) {
+                    f[4 * v + i] = __uint_as_float(u[i]);
+                } else {
+                    f[2 * i] = dev::bf16_lo(u[i]);
+                    f[2 * i + 1] = dev::bf16_hi(u[i]);
+                }
             }
         }
     }
-    // the same over the finite values alone
-    __device__ static __noinline__ uint32_t amax_finite(uint4 w) {
-        float f[kN];
-        values(w, f);
-        uint32_t r = 0;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
-            if (a < 0x7f800000u) r = max(r, a);
-        }
-        return r;
-    }
-    // codes of the piece at scale s = 2^-e (kN bytes, lowest first); `inf`: the piece may
-    // hold infinities, which become NaN (the format has none)
-    __device__ static __forceinline__ uint2 codes(const uint4 &w, float s, bool inf) {
-        float f[kN];
-        values(w, f);
+    // codes of the piece at scale s = 2^-e (lowest first); `inf`: the piece may hold
+    // infinities, which become NaN (the format has none)
+    __device__ __forceinline__ uint2 codes(float s, bool inf) const {
+        float f[8];
+        values(f);
         if (inf) {
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
+            for (int i = 0; i < 8; ++i)
                 if ((__float_as_uint(f[i]) & 0x7fffffffu) == 0x7f800000u) f[i] = __int_as_float(0x7fffffff);
         }
-        uint2 r;
-        r.x = e4m3x2_scaled(f[0], f[1], s) | (e4m3x2_scaled(f[2], f[3], s) << 16);
-        r.y = kF32 ? 0u : (e4m3x2_scaled(f[kN - 4], f[kN - 3], s) | (e4m3x2_scaled(f[kN - 2], f[kN - 1], s) << 16));
-        return r;
+        return make_uint2(e4m3x2_scaled(f[0], f[1], s) | (e4m3x2_scaled(f[2], f[3], s) << 16),
+                          e4m3x2_scaled(f[4], f[5], s) | (e4m3x2_scaled(f[6], f[7], s) << 16));
     }
 };
+// largest finite |value| of a piece, as fp32 bits
+template <bool kF32>
+__device__ __noinline__ uint32_t amax_finite(Piece<kF32> x) {
+    float f[8];
+    x.values(f);
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
+        if (a < 0x7f800000u) r = max(r, a);
+    }
+    return r;
+}
 
 // Four stored codes times s (a power of two <= 1), rounded to nearest even.
 __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float s) {
@@ -374,13 +387,13 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float s) {
     return e4m3x2(fa.x * s, fa.y * s) | (e4m3x2(fb.x * s, fb.y * s) << 16);
 }
 
-// Maxima of a warp's tokens: v[i] is this lane's part of load i. The eight values are
-// halved while the lanes are folded (4 + 2 + 1 exchanges, then plain folds): lane l of a
-// row ends with the maximum of load (l / (kLanes / 8)) of its row.
-template <int kLanes>
-__device__ __forceinline__ uint32_t fold_max(uint32_t (&v)[kAppLoads], int piece) {
+// Maxima of a warp's tokens: v[i] is this lane's part of load i. The values are halved
+// while the lanes are folded (then plain folds): lane l of a row ends with the maximum of
+// load (l / (kPieceLanes / kN)) of its row.
+template <int kN>
+__device__ __forceinline__ uint32_t fold_max(uint32_t (&v)[kN], int piece) {
 #pragma unroll
-    for (int n = kAppLoads / 2, o = kLanes / 2; n >= 1; n >>= 1, o >>= 1) {
+    for (int n = kN / 2, o = kPieceLanes / 2; n >= 1; n >>= 1, o >>= 1) {
         const bool up = piece & o;  // keeps the upper half of the values
 #pragma unroll
         for (int i = 0; i < n; ++i) {
@@ -389,7 +402,7 @@ __device__ __forceinline__ uint32_t fold_max(uint32_t (&v)[kAppLoads], int piece
         }
     }
 #pragma unroll
-    for (int o = kLanes / 16; o >= 1; o >>= 1) v[0] = max(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    for (int o = kPieceLanes / kN / 2; o >= 1; o >>= 1) v[0] = max(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
     return v[0];
 }
 
@@ -414,28 +427,25 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
     const long long tb = is_v ? p.v_tok : p.k_tok;
     const char *x = is_v ? p.v + h * p.v_head : p.k + h * p.k_head;
     int8_t *exps = (is_v ? p.v_exp : p.k_exp) + h;
-    const int sub = lane / PC::kLanes, piece = lane % PC::kLanes;
+    constexpr int kLoads = PC::kLoads, kBytes = 16 * PC::kVecs;  // bytes of a piece
+    const int sub = lane / kPieceLanes, piece = lane % kPieceLanes;
     const int t_first = warp * PC::kPerWarp + sub;  // token of this lane's load i: t_first + i * kPer
 
-    uint4 w[kAppLoads];
-    const char *src = x + (T0 + t_first) * tb + piece * 16;
+    PC w[kLoads];
+    const char *src = x + (T0 + t_first) * tb + piece * kBytes;
 #pragma unroll
-    for (int i = 0; i < kAppLoads; ++i) {
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (t_first + i * PC::kPer < nt) w[i] = __ldg(reinterpret_cast<const uint4 *>(src + i * PC::kPer * tb));
+    for (int i = 0; i < kLoads; ++i) {
+        w[i].clear();
+        if (t_first + i * kPer < nt) w[i].load(src + i * kPer * tb);
     }
     // page and place of a slot; page -1 outside the pool
     auto place = [&](long long t, int &off) -> int {
         const long long sl = __ldg(p.slots + t);
         off = 0;
         if (sl < 0 || sl >= p.rows) return -1;
-        if (sl <= (long long)UINT32_MAX) {
-            const uint32_t pg = (uint32_t)sl / (uint32_t)p.ps;
-            off = (int)((uint32_t)sl - pg * (uint32_t)p.ps);
-            return (int)pg;
-        }
-        off = (int)(sl % p.ps);
-        return (int)(sl / p.ps);
+        const uint32_t pg = (uint32_t)sl / (uint32_t)p.ps;  // (rows fit 32 bits: checked by the caller)
+        off = (int)((uint32_t)sl - pg * (uint32_t)p.ps);
+        return (int)pg;
     };
     if (tid < kTok) {
         int off = 0, off_before;
@@ -467,18 +477,18 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
     }
     uint32_t odd = 0;  // loads whose piece holds an infinity or NaN
     {
-        uint32_t v[kAppLoads];
+        uint32_t v[kLoads];
 #pragma unroll
-        for (int i = 0; i < kAppLoads; ++i) {
-            v[i] = PC::amax(w[i]);
+        for (int i = 0; i < kLoads; ++i) {
+            v[i] = w[i].amax();
             if (v[i] >= 0x7f800000u) {
                 odd |= 1u << i;
-                v[i] = PC::amax_finite(w[i]);
+                v[i] = amax_finite(w[i]);
             }
         }
-        const uint32_t m = fold_max<PC::kLanes>(v, piece);
-        constexpr int kShare = PC::kLanes / kAppLoads;  // lanes that hold the same maximum
-        if (piece % kShare == 0) s_tmax[t_first + piece / kShare * PC::kPer] = m;
+        const uint32_t m = fold_max(v, piece);
+        constexpr int kShare = kPieceLanes / kLoads;  // lanes that hold the same maximum
+        if (piece % kShare == 0) s_tmax[t_first + piece / kShare * kPer] = m;
     }
     __syncthreads();
     // first token of the run that token t (with a page) belongs to, within the window
@@ -491,25 +501,22 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
     if (tid < kTok && s_page[tid] >= 0) atomicMax(&s_max[run_of(tid)], s_tmax[tid]);
     if (s_left | s_right) {
         const int outside = s_left + s_right, last_run = s_page[nt - 1] >= 0 ? run_of(nt - 1) : 0;
-        constexpr int kStep = kWarps * PC::kPer, kFly = 2;
-        for (int j = warp * PC::kPer + sub; j - sub < outside; j += kFly * kStep) {
-            uint4 y[kFly];
+        constexpr int kStep = kWarps * kPer, kFly = 4 / PC::kVecs;
+        for (int j = warp * kPer + sub; j - sub < outside; j += kFly * kStep) {
+            PC y[kFly];
 #pragma unroll
             for (int f = 0; f < kFly; ++f) {
                 const int jj = j + f * kStep;
-                y[f] = make_uint4(0, 0, 0, 0);
-                if (jj < outside) {
-                    const long long t = jj < s_left ? T0 - 1 - jj : T0 + nt + (jj - s_left);
-                    y[f] = __ldg(reinterpret_cast<const uint4 *>(x + t * tb) + piece);
-                }
+                y[f].clear();
+                if (jj < outside) y[f].load(x + (jj < s_left ? T0 - 1 - jj : T0 + nt + (jj - s_left)) * tb + piece * kBytes);
             }
 #pragma unroll
             for (int f = 0; f < kFly; ++f) {
                 const int jj = j + f * kStep;
-                uint32_t m = PC::amax(y[f]);
-                if (m >= 0x7f800000u) m = PC::amax_finite(y[f]);
+                uint32_t m = y[f].amax();
+                if (m >= 0x7f800000u) m = amax_finite(y[f]);
 #pragma unroll
-                for (int o = PC::kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                for (int o = kPieceLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
                 if (piece == 0 && jj < outside) atomicMax(&s_max[jj < s_left ? 0 : last_run], m);
             }
         }
@@ -518,14 +525,15 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
     // Lane l < kPerWarp: the exponent of the warp's token l and where its codes go
     uint8_t *codes = (is_v ? p.v_codes : p.k_codes) + (long long)h * kCacheD;
     const long long row_bytes = (long long)p.H * kCacheD;
-    long long row = -1;
+    constexpr uint32_t kNoRow = ~0u;
+    uint32_t row = kNoRow;
     float scale = 0.f;
     bool grow = false;
     int drop = 0, held = 0;
     if (lane < PC::kPerWarp) {
         const int t = warp * PC::kPerWarp + lane, page = s_page[t];
         if (page >= 0) {
-            row = ((long long)page * p.ps + s_off[t]) * row_bytes;
+            row = (uint32_t)page * (uint32_t)p.ps + (uint32_t)s_off[t];
             const int r = run_of(t), need = exponent_for(s_max[r]);
             const bool inside = r > 0 || s_left == 0;  // the run's first token is in this window
             held = s_off[r];
@@ -540,15 +548,10 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
         }
     }
 #pragma unroll
-    for (int i = 0; i < kAppLoads; ++i) {
-        const long long to = __shfl_sync(0xffffffffu, row, i * PC::kPer + sub);
-        const float sc = __shfl_sync(0xffffffffu, scale, i * PC::kPer + sub);
-        if (to >= 0) {
-            const uint2 c = PC::codes(w[i], sc, odd >> i & 1);
-            uint8_t *dst = codes + to + piece * PC::kN;
-            if constexpr (kF32) *reinterpret_cast<uint32_t *>(dst) = c.x;
-            else *reinterpret_cast<uint2 *>(dst) = c;
-        }
+    for (int i = 0; i < kLoads; ++i) {
+        const uint32_t to = __shfl_sync(0xffffffffu, row, i * kPer + sub);
+        const float sc = __shfl_sync(0xffffffffu, scale, i * kPer + sub);
+        if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + to * row_bytes + piece * 8) = w[i].codes(sc, odd >> i & 1);
     }
     // codes that a page held before its exponent rose: rows 0 .. held - 1, four rows of
     // 8 lanes x 16 bytes at a time
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
         const int l = __ffs(m) - 1;
         const int rows = __shfl_sync(0xffffffffu, held, l);
         const float sc = pow2i(max(__shfl_sync(0xffffffffu, drop, l), -126));
-        uint8_t *page = codes + __shfl_sync(0xffffffffu, row, l) - rows * row_bytes;
+        uint8_t *page = codes + (long long)(__shfl_sync(0xffffffffu, row, l) - rows) * row_bytes;
         for (int r = lane >> 3; r < rows; r += 4) {
             uint4 *at = reinterpret_cast<uint4 *>(page + r * row_bytes) + (lane & 7);
             uint4 c = *at;

@@ -102,7 +102,7 @@ def test_append_refuses(native, kw):
     assert native.load().bsp_append_kv_fp8(*append_args(**kw)) == native.BSP_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("kw", [dict(D=64), dict(D=256), dict(H=40000)])
+@pytest.mark.parametrize("kw", [dict(D=64), dict(D=256), dict(H=40000), dict(pages=1 << 28), dict(n=1 << 31)])
 def test_append_unsupported(native, kw):
     assert native.load().bsp_append_kv_fp8(*append_args(**kw)) == native.BSP_ERR_UNSUPPORTED
 
