@@ -241,24 +241,29 @@ class PagedAttention:
             raise ValueError(f"k_exp / v_exp must be [{pool[0]}, {pool[2]}]")
         if kv_indices.dim() != 1 or kv_indices.shape[0] < info.num_table_pages:
             raise ValueError(f"kv_indices must hold the plan's {info.num_table_pages} pages")
+        q_p = _addr(q, "q", torch.bfloat16, dev)
         if out is None:
             out = torch.empty_like(q)
-        elif out.shape != q_shape:
-            raise ValueError("out must have the shape of q")
-        if lse is None:
-            if return_lse:
-                lse = torch.empty(q_shape[:2], dtype=torch.float32, device=dev)
-        elif lse.shape != q_shape[:2]:
-            raise ValueError("lse must be [n_tokens, H_qo]")
+            out_p = out.data_ptr()
+        else:
+            if out.shape != q_shape:
+                raise ValueError("out must have the shape of q")
+            out_p = _addr(out, "out", torch.bfloat16, dev)
+        lse_p = None
+        if lse is not None:
+            if lse.shape != q_shape[:2]:
+                raise ValueError("lse must be [n_tokens, H_qo]")
+            lse_p = _addr(lse, "lse", torch.float32, dev)
+        elif return_lse:
+            lse = torch.empty(q_shape[:2], dtype=torch.float32, device=dev)
+            lse_p = lse.data_ptr()
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(self._q_tail[1])
         self._set_sink(sink)
         ref = ctypes.byref(info)
-        args = (ref, _addr(q, "q", torch.bfloat16, dev), _addr(k_pages, "k_pages", f8, dev),
-                _addr(v_pages, "v_pages", f8, dev), _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev),
-                _addr(kv_indices, "kv_indices", torch.int32, dev) or None, pool[0], sm_scale,
-                _addr(out, "out", torch.bfloat16, dev),
-                None if lse is None else _addr(lse, "lse", torch.float32, dev))
+        args = (ref, q_p, _addr(k_pages, "k_pages", f8, dev), _addr(v_pages, "v_pages", f8, dev),
+                _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev),
+                _addr(kv_indices, "kv_indices", torch.int32, dev) or None, pool[0], sm_scale, out_p, lse_p)
         if self.mode == N.BSP_MODE_DECODE:
             _call(dev, stream, self.lib.bsp_decode_run_fp8_block, *args, self.workspace.data_ptr())
         else:

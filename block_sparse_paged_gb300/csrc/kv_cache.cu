@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
     if (tid < kTok && s_page[tid] >= 0) atomicMax(&s_max[run_of(tid)], s_tmax[tid]);
     if (s_left | s_right) {
         const int outside = s_left + s_right, last_run = s_page[nt - 1] >= 0 ? run_of(nt - 1) : 0;
-        constexpr int kStep = kWarps * kPer, kFly = 4 / PC::kVecs;
+        constexpr int kStep = kWarps * kPer, kFly = 2;
         for (int j = warp * kPer + sub; j - sub < outside; j += kFly * kStep) {
             PC y[kFly];
 #pragma unroll
