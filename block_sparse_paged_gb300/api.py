@@ -7,7 +7,6 @@ from __future__ import annotations
 
 import ctypes
 import math
-from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -364,28 +363,37 @@ def _call(dev: torch.device, stream, fn, *args):
         N.check(rc)
 
 
-class PageTables(NamedTuple):
-    """What build_page_tables writes (int32 but slot_map, int64), for B requests:
-    kv_indptr [B + 1], last_page_len [B], kv_indices [max_table_pages], qo_indptr
-    [B + 1], slot_map [max_new_tokens], positions [max_new_tokens], counts [4]:
-    table pages, new tokens, pages taken, error bits (BSP_TABLES_*)."""
-    kv_indptr: torch.Tensor
-    last_page_len: torch.Tensor
-    kv_indices: torch.Tensor
-    qo_indptr: torch.Tensor
-    slot_map: torch.Tensor
-    positions: torch.Tensor
-    counts: torch.Tensor
+class PageTables:
+    """What build_page_tables writes, for up to the given sizes: int32 kv_indptr
+    [batch + 1], last_page_len [batch], kv_indices [max_table_pages], qo_indptr
+    [batch + 1], positions [max_new_tokens], counts [4] (table pages, new tokens,
+    pages taken, error bits BSP_TABLES_*) and int64 slot_map [max_new_tokens]. The
+    int32 arrays are parts of one buffer; to be kept and passed as `out` every step."""
+    _fields = ("kv_indptr", "last_page_len", "kv_indices", "qo_indptr", "slot_map", "positions", "counts")
+
+    def __init__(self, batch: int, max_table_pages: int, max_new_tokens: int, device=None):
+        if min(batch, max_table_pages, max_new_tokens) < 0:
+            raise ValueError("sizes must not be negative")
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.sizes = (batch, max_table_pages, max_new_tokens)
+        parts = [("kv_indices", max_table_pages), ("positions", max_new_tokens), ("kv_indptr", batch + 1),
+                 ("qo_indptr", batch + 1), ("last_page_len", batch), ("counts", 4)]
+        at, offsets = 0, {}
+        for f, n in parts:  # every part 16-byte aligned
+            offsets[f] = at
+            at += (n + 3) // 4 * 4
+        self._ints = torch.empty(at, dtype=torch.int32, device=dev)
+        self.slot_map = torch.empty(max_new_tokens, dtype=torch.int64, device=dev)
+        for f, n in parts:
+            setattr(self, f, self._ints[offsets[f]:offsets[f] + n])
+        self._offsets = tuple(4 * offsets[f] for f in ("kv_indptr", "last_page_len", "kv_indices", "qo_indptr",
+                                                       "positions", "counts"))
+        self.device = self._ints.device
 
     @classmethod
     def empty(cls, batch: int, max_table_pages: int, max_new_tokens: int, device=None) -> "PageTables":
-        """Buffers for `batch` requests, to be passed as `out` every step."""
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        sizes = (batch + 1, batch, max_table_pages, batch + 1, max_new_tokens, max_new_tokens, 4)
-        return cls(*(torch.empty(n, dtype=d, device=dev) for d, n in zip(_TABLE_DTYPES, sizes)))
-
-
-_TABLE_DTYPES = tuple(torch.int64 if f == "slot_map" else torch.int32 for f in PageTables._fields)
+        """Buffers of these sizes, not yet written."""
+        return cls(batch, max_table_pages, max_new_tokens, device)
 
 
 def build_page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
@@ -415,18 +423,18 @@ def build_page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pa
     if free_pages.dim() != 1 or num_free.numel() != 1:
         raise ValueError("free_pages must be one-dimensional and num_free hold one value")
     if out is None:
-        out = PageTables.empty(B, max_table_pages, max_new_tokens, dev)
-    i32 = torch.int32
-    o = [_addr(t, f, d, dev) for t, f, d in zip(out, PageTables._fields, _TABLE_DTYPES)]
-    sizes = [B + 1, B, max_table_pages, B + 1, max_new_tokens, max_new_tokens, 4]
-    if [t.numel() for t in out] != sizes:
-        raise ValueError(f"out must hold {sizes} values (PageTables.empty)")
+        out = PageTables(B, max_table_pages, max_new_tokens, dev)
+    elif out.sizes != (B, max_table_pages, max_new_tokens) or out.device != dev:
+        raise ValueError(f"out is for {out.sizes} (batch, pages, tokens) on {out.device}")
     if B <= 1:
         stride = max(width, stride)
+    i32 = torch.int32
+    o = out._ints.data_ptr()
+    kv_indptr, last, indices, qo_indptr, pos, counts = out._offsets
     _call(dev, stream, N.load().bsp_build_page_tables, B, page_size, _addr(cached_lens, "cached_lens", i32, dev),
-          _addr(new_lens, "new_lens", i32, dev), _addr(free_pages, "free_pages", i32, dev), free_pages.numel(),
-          _addr(num_free, "num_free", i32, dev), block_table.data_ptr(), stride, width, o[0], o[1], o[2],
-          max_table_pages, o[3], o[4], o[5], max_new_tokens, o[6])
+          _addr(new_lens, "new_lens", i32, dev), _addr(free_pages, "free_pages", i32, dev), free_pages.shape[0],
+          _addr(num_free, "num_free", i32, dev), block_table.data_ptr(), stride, width, o + kv_indptr, o + last,
+          o + indices, max_table_pages, o + qo_indptr, out.slot_map.data_ptr(), o + pos, max_new_tokens, o + counts)
     return out
 
 
