@@ -387,6 +387,32 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float s) {
     return e4m3x2(fa.x * s, fa.y * s) | (e4m3x2(fb.x * s, fb.y * s) << 16);
 }
 
+// Page and place of token t's slot; page -1 outside the pool or the list.
+__device__ __forceinline__ int place_of(const AppendParams &p, long long t, int &off) {
+    off = 0;
+    if (t < 0 || t >= p.n) return -1;
+    const long long sl = __ldg(p.slots + t);
+    if (sl < 0 || sl >= p.rows) return -1;
+    const uint32_t pg = (uint32_t)sl / (uint32_t)p.ps;  // (rows fit 32 bits: checked by the caller)
+    off = (int)((uint32_t)sl - pg * (uint32_t)p.ps);
+    return (int)pg;
+}
+
+// A warp: codes of rows 0 .. held - 1 of a page whose exponent rose by -drop, four rows of
+// 8 lanes x 16 bytes at a time. page: the page's codes of this kv head.
+__device__ __forceinline__ void rescale_rows(uint8_t *page, long long row_bytes, int held, int drop, int lane) {
+    const float s = pow2i(max(drop, -126));
+    for (int r = lane >> 3; r < held; r += 4) {
+        uint4 *at = reinterpret_cast<uint4 *>(page + r * row_bytes) + (lane & 7);
+        uint4 c = *at;
+        c.x = rescale_codes(c.x, s);
+        c.y = rescale_codes(c.y, s);
+        c.z = rescale_codes(c.z, s);
+        c.w = rescale_codes(c.w, s);
+        *at = c;
+    }
+}
+
 // Maxima of a warp's tokens: v[i] is this lane's part of load i. The values are halved
 // while the lanes are folded (then plain folds): lane l of a row ends with the maximum of
 // load (l / (kPieceLanes / kN)) of its row.
@@ -438,20 +464,11 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
         w[i].clear();
         if (t_first + i * kPer < nt) w[i].load(src + i * kPer * tb);
     }
-    // page and place of a slot; page -1 outside the pool
-    auto place = [&](long long t, int &off) -> int {
-        const long long sl = __ldg(p.slots + t);
-        off = 0;
-        if (sl < 0 || sl >= p.rows) return -1;
-        const uint32_t pg = (uint32_t)sl / (uint32_t)p.ps;  // (rows fit 32 bits: checked by the caller)
-        off = (int)((uint32_t)sl - pg * (uint32_t)p.ps);
-        return (int)pg;
-    };
     if (tid < kTok) {
         int off = 0, off_before;
-        const int page = tid < nt ? place(T0 + tid, off) : -1;
+        const int page = tid < nt ? place_of(p, T0 + tid, off) : -1;
         // (of token 0 the run may begin before the window: s_left tells)
-        const bool lead = page >= 0 && (tid == 0 || place(T0 + tid - 1, off_before) != page);
+        const bool lead = page >= 0 && (tid == 0 || place_of(p, T0 + tid - 1, off_before) != page);
         s_page[tid] = page;
         s_off[tid] = off;
         s_max[tid] = 0;
@@ -462,11 +479,11 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
         // how far the first (last) run goes on before (behind) the window
         const bool left = warp == kWarps - 2;
         int got = 0, off;
-        const int pg = place(left ? T0 : T0 + nt - 1, off);
+        const int pg = place_of(p, left ? T0 : T0 + nt - 1, off);
         if (pg >= 0) {
             for (;;) {
                 const long long t = left ? T0 - 1 - got - lane : T0 + nt + got + lane;
-                const bool same = t >= 0 && t < p.n && place(t, off) == pg;
+                const bool same = place_of(p, t, off) == pg;
                 const uint32_t m = __ballot_sync(0xffffffffu, same);
                 const int k = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
                 got += k;
@@ -537,7 +554,7 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
             const int r = run_of(t), need = exponent_for(s_max[r]);
             const bool inside = r > 0 || s_left == 0;  // the run's first token is in this window
             held = s_off[r];
-            if (!inside) place(T0 - s_left, held);
+            if (!inside) place_of(p, T0 - s_left, held);
             const int e = held > 0 ? max(need, s_had[r]) : need;
             scale = pow2i(-e);
             if (inside && r == t) {
@@ -553,22 +570,171 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
         const float sc = __shfl_sync(0xffffffffu, scale, i * kPer + sub);
         if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + to * row_bytes + piece * 8) = w[i].codes(sc, odd >> i & 1);
     }
-    // codes that a page held before its exponent rose: rows 0 .. held - 1, four rows of
-    // 8 lanes x 16 bytes at a time
-    for (uint32_t m = __ballot_sync(0xffffffffu, grow); m; m &= m - 1) {
+    for (uint32_t m = __ballot_sync(0xffffffffu, grow); m; m &= m - 1) {  // codes that such a page held before
         const int l = __ffs(m) - 1;
         const int rows = __shfl_sync(0xffffffffu, held, l);
-        const float sc = pow2i(max(__shfl_sync(0xffffffffu, drop, l), -126));
         uint8_t *page = codes + (long long)(__shfl_sync(0xffffffffu, row, l) - rows) * row_bytes;
-        for (int r = lane >> 3; r < rows; r += 4) {
-            uint4 *at = reinterpret_cast<uint4 *>(page + r * row_bytes) + (lane & 7);
-            uint4 c = *at;
-            c.x = rescale_codes(c.x, sc);
-            c.y = rescale_codes(c.y, sc);
-            c.z = rescale_codes(c.z, sc);
-            c.w = rescale_codes(c.w, sc);
-            *at = c;
+        rescale_rows(page, row_bytes, rows, __shfl_sync(0xffffffffu, drop, l), lane);
+    }
+}
+
+// The same by runs: a warp owns the runs that begin among its 16 tokens, for one kv head's
+// K or V, and reads exactly their tokens. Everything meets by shuffles, no barrier, and no
+// token is read twice where runs have at most 16 tokens; a longer run is read once for its
+// maximum and once more (from L2) for its codes, 16 tokens at a time.
+// CTA: 8 warps on neighbouring heads of the same tokens.
+constexpr int kSeg = 16;
+
+template <bool kF32>
+__global__ void __launch_bounds__(256, kF32 ? 2 : 4) append_runs_kernel(const AppendParams p) {
+    using PC = Piece<kF32>;
+    constexpr int kLoads = kSeg / kPer, kBytes = 16 * PC::kVecs;
+    const int lane = threadIdx.x & 31;
+    const int units = 2 * p.H;  // of a segment: K heads, then V heads
+    const uint32_t gw = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const uint32_t seg = gw / (uint32_t)units;
+    const int hv = (int)(gw - seg * (uint32_t)units);
+    const long long T0 = (long long)seg * kSeg;
+    if (T0 >= p.n) return;
+    // lane l: token T0 - 1 + l
+    int off;
+    const int page = place_of(p, T0 - 1 + lane, off);
+    const int before = __shfl_up_sync(0xffffffffu, page, 1);
+    const uint32_t change = __ballot_sync(0xffffffffu, lane > 0 && page != before);
+    const uint32_t lead = __ballot_sync(0xffffffffu, lane > 0 && page >= 0 && page != before);
+    const uint32_t mine = lead & 0x1fffeu;  // runs that begin at tokens T0 .. T0 + 15
+    if (mine == 0) return;
+    const int last = 31 - __clz(mine);  // lane of the last of them; it ends at the next change
+    const uint32_t after = change & ~((2u << last) - 1u);
+    int end = after ? __ffs(after) - 1 : 32;  // lanes [first, end) are this warp's tokens,
+    long long tail = 0;                        // and `tail` more tokens behind lane 31
+    if (!after && last < 32) {
+        const int pg = __shfl_sync(0xffffffffu, page, 31);
+        for (;;) {
+            int o;
+            const uint32_t m = __ballot_sync(0xffffffffu, place_of(p, T0 + 31 + tail + lane, o) == pg);
+            const int k = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+            tail += k;
+            if (k < 32) break;
         }
+    }
+    const bool is_v = hv >= p.H;
+    const int h = is_v ? hv - p.H : hv;
+    const long long tb = is_v ? p.v_tok : p.k_tok;
+    const int sub = lane / kPieceLanes, piece = lane % kPieceLanes;
+    const char *x = (is_v ? p.v + h * p.v_head : p.k + h * p.k_head) + (T0 - 1 + sub) * tb + piece * kBytes;
+    int8_t *exps = (is_v ? p.v_exp : p.k_exp) + h;
+    uint8_t *codes = (is_v ? p.v_codes : p.k_codes) + (long long)h * kCacheD;
+    const long long row_bytes = (long long)p.H * kCacheD;
+    constexpr uint32_t kNoRow = ~0u;
+
+    PC w[kLoads];
+    uint32_t odd = 0;  // loads whose piece holds an infinity or NaN
+    // tokens T0 - 1 + at .. + count - 1 into w; lane l < 16: the maximum of token l
+    auto read = [&](long long at, int count) -> uint32_t {
+        const char *src = x + at * tb;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            w[i].clear();
+            if (i * kPer + sub < count) w[i].load(src + i * kPer * tb);
+        }
+        odd = 0;
+        uint32_t v[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            v[i] = w[i].amax();
+            if (v[i] >= 0x7f800000u) {
+                odd |= 1u << i;
+                v[i] = amax_finite(w[i]);
+            }
+        }
+        const uint32_t m = fold_max(v, piece);  // lane (sub, piece): token 2 (piece / 2) + sub
+        static_assert(kPieceLanes / kLoads == 2 && kPer == 2, "eight loads of two rows");
+        return __shfl_sync(0xffffffffu, m, (lane & 1) * kPieceLanes + (lane & 14));
+    };
+    // codes of the tokens in w: lane l < 16 has token l's row (kNoRow: none) and 2^-e
+    auto write = [&](uint32_t row, float scale) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t to = __shfl_sync(0xffffffffu, row, i * kPer + sub);
+            const float sc = __shfl_sync(0xffffffffu, scale, i * kPer + sub);
+            if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + to * row_bytes + piece * 8) = w[i].codes(sc, odd >> i & 1);
+        }
+    };
+    // exponent of a run that begins at place `held` of its page; writes it
+    auto exponent = [&](uint32_t amax, int pg, int held, int had, int &drop) -> int {
+        const int need = exponent_for(amax), e = held > 0 ? max(need, had) : need;
+        drop = held > 0 ? had - e : 0;
+        exps[(long long)pg * p.H] = (int8_t)e;
+        return e;
+    };
+    auto rescale = [&](int pg, int held, int drop) {
+        rescale_rows(codes + (long long)pg * p.ps * row_bytes, row_bytes, held, drop, lane);
+    };
+
+    for (int at = __ffs(mine) - 1; at < end;) {
+        // up to 16 tokens that end with a run
+        const uint32_t upto = at + kSeg >= 31 ? ~0u : (2u << (at + kSeg)) - 1u;  // lanes up to at + 16
+        uint32_t stops = change & upto & ~((2u << at) - 1u);                     // run ends in (at, at + 16]
+        if (end <= at + kSeg && end < 32) stops |= 1u << end;
+        int stop = stops ? 31 - __clz(stops) : 0;
+        if (end == 32 && tail == 0 && at + kSeg >= 32) stop = 32;
+        if (stop > end) stop = end;
+        if (stop > at) {
+            // lane l < 16: token lane at + l
+            const int src = min(at + lane, 31);
+            int pg = __shfl_sync(0xffffffffu, page, src);
+            const int o = __shfl_sync(0xffffffffu, off, src);
+            const int count = stop - at;
+            if (lane >= count) pg = -1;
+            int had = 0;
+            if (pg >= 0) had = *reinterpret_cast<volatile int8_t *>(exps + (long long)pg * p.H);
+            const uint32_t first = __ballot_sync(0xffffffffu, pg >= 0 && (lead >> src & 1));
+            uint32_t m = read(at, count);
+            // maximum of the run at its first token: fold over the following tokens of the page
+#pragma unroll
+            for (int d = 1; d < kSeg; d <<= 1) {
+                const uint32_t mu = __shfl_down_sync(0xffffffffu, m, d);
+                const int pu = __shfl_down_sync(0xffffffffu, pg, d);
+                if (pu == pg) m = max(m, mu);
+            }
+            const uint32_t upto_me = first & (0xffffffffu >> (31 - lane));
+            const int head = pg >= 0 && upto_me ? 31 - __clz(upto_me) : lane;
+            int drop = 0, e = 0;
+            if (pg >= 0 && head == lane) e = exponent(m, pg, o, had, drop);
+            e = __shfl_sync(0xffffffffu, e, head);
+            write(pg >= 0 ? (uint32_t)pg * (uint32_t)p.ps + (uint32_t)o : kNoRow, pow2i(-e));
+            for (uint32_t g = __ballot_sync(0xffffffffu, drop < 0); g; g &= g - 1) {
+                const int l = __ffs(g) - 1;
+                rescale(__shfl_sync(0xffffffffu, pg, l), __shfl_sync(0xffffffffu, o, l), __shfl_sync(0xffffffffu, drop, l));
+            }
+            at = stop;
+            continue;
+        }
+        // a run of more than 16 tokens, [at, at + len)
+        const uint32_t more = change & ~((2u << at) - 1u);
+        const long long len = more ? __ffs(more) - 1 - at : 32 - at + tail;
+        const int pg = __shfl_sync(0xffffffffu, page, at), held = __shfl_sync(0xffffffffu, off, at);
+        const int had = *reinterpret_cast<volatile int8_t *>(exps + (long long)pg * p.H);
+        uint32_t m = 0;
+        for (long long t = 0; t < len; t += kSeg) m = max(m, read(at + t, (int)min((long long)kSeg, len - t)));
+#pragma unroll
+        for (int d = kSeg / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        m = __shfl_sync(0xffffffffu, m, 0);
+        int drop = 0, e = 0;
+        if (lane == 0) e = exponent(m, pg, held, had, drop);
+        e = __shfl_sync(0xffffffffu, e, 0);
+        drop = __shfl_sync(0xffffffffu, drop, 0);
+        const float scale = pow2i(-e);
+        for (long long n_seg = (len + kSeg - 1) / kSeg, j = n_seg - 1; j >= 0; --j) {  // the last 16 are still there
+            const int count = (int)min((long long)kSeg, len - j * kSeg);
+            if (j != n_seg - 1) read(at + j * kSeg, count);
+            int o;
+            const int q = lane < count ? place_of(p, T0 - 1 + at + j * kSeg + lane, o) : -1;
+            write(q >= 0 ? (uint32_t)q * (uint32_t)p.ps + (uint32_t)o : kNoRow, scale);
+        }
+        if (drop < 0) rescale(pg, held, drop);
+        at = more ? at + (int)len : 32;
     }
 }
 
@@ -635,8 +801,17 @@ int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64
                      const int64_t *slot_map, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
                      int64_t num_pages, int32_t page_size, int32_t num_kv_heads, cudaStream_t stream) {
     const int64_t elem = dtype == BSP_DTYPE_F32 ? 4 : 2;
-    const int64_t ctas = (n_tokens + kAppTokens - 1) / kAppTokens * 2 * num_kv_heads;
-    if (ctas > INT32_MAX) return fail(BSP_ERR_UNSUPPORTED, "too many tokens for one append");
+    // By runs: pages of 2 to 16 tokens (24k ragged bf16 tokens into 16-token pages 31.2 us
+    // against 37.1 by windows, fp32 49.7 / 62.6; 256 tokens 4.0 / 4.2), and fp32 into pages
+    // of up to 64 where there are runs enough to fill the GPU (49k tokens 112 / 125; four
+    // prompts of 900 tokens 17.5 / 8.1). Windows: single-token pages (38.5 us against 43.0),
+    // and larger pages, whose runs a warp would walk alone (one prompt of 256 tokens into
+    // 128-token pages 4.0 us against 20.8).
+    const int64_t warps = (n_tokens + kSeg - 1) / kSeg * 2 * num_kv_heads;
+    const bool runs = page_size >= 2 && (page_size <= kSeg || (dtype == BSP_DTYPE_F32 && page_size <= 4 * kSeg &&
+                                                               n_tokens * 2 * num_kv_heads / page_size >= 4096));
+    const int64_t ctas = runs ? (warps + 7) / 8 : (n_tokens + kAppTokens - 1) / kAppTokens * 2 * num_kv_heads;
+    if (ctas > INT32_MAX / 8) return fail(BSP_ERR_UNSUPPORTED, "too many tokens for one append");
     AppendParams p;
     p.k = static_cast<const char *>(k);
     p.v = static_cast<const char *>(v);
@@ -653,7 +828,10 @@ int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64
     p.rows = (long long)num_pages * page_size;
     p.ps = page_size;
     p.H = num_kv_heads;
-    if (dtype == BSP_DTYPE_F32) append_kernel<true><<<(unsigned)ctas, 32 * Piece<true>::kWarps, 0, stream>>>(p);
+    if (runs) {
+        if (dtype == BSP_DTYPE_F32) append_runs_kernel<true><<<(unsigned)ctas, 256, 0, stream>>>(p);
+        else append_runs_kernel<false><<<(unsigned)ctas, 256, 0, stream>>>(p);
+    } else if (dtype == BSP_DTYPE_F32) append_kernel<true><<<(unsigned)ctas, 32 * Piece<true>::kWarps, 0, stream>>>(p);
     else append_kernel<false><<<(unsigned)ctas, 32 * Piece<false>::kWarps, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("append launch: ") + cudaGetErrorString(e));

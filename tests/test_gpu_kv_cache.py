@@ -177,6 +177,12 @@ CASES = [  # (seed, ps, H, cached, new, dtype, layout)
     (8, 300, 2, [0, 250], [700, 411], torch.bfloat16, "plain"),                        # a page over several windows
     (9, 8, 5, [0] * 40, [1] * 40, torch.float32, "plain"),
     (10, 1000, 1, [13], [900], torch.float32, "plain"),
+    # runs of a warp: pages of 2 to 16 tokens, gaps of all lengths, fp32 into larger pages with many runs
+    (11, 2, 3, [1, 0, 5] * 9, [1, 7, 4] * 9, torch.bfloat16, "heads"),
+    (12, 16, 1, list(range(17)) * 3, list(range(1, 52)), torch.bfloat16, "plain"),
+    (13, 7, 2, [3] * 30, [1, 20, 6] * 10, torch.float32, "fused"),
+    (14, 15, 1, [14, 15, 16], [47, 31, 500], torch.bfloat16, "plain"),
+    (16, 33, 16, [5, 0], [2000, 3001], torch.float32, "fused"),
 ]
 
 
@@ -226,6 +232,24 @@ def test_append_skips_slots_outside_the_pool(bsp):
     check_append(run_append(bsp, xk, xv, slots, kc_, vc_), xk, xv, slots, kc_, vc_)
     none = np.full(n, -1, np.int64)
     check_append(run_append(bsp, xk, xv, none, kc_, vc_), xk, xv, none, kc_, vc_)
+
+
+@pytest.mark.parametrize("ps", [1, 3, 16, 40])
+def test_append_with_skipped_tokens_anywhere(bsp, ps):
+    """Slots of -1 between the runs of pages, single ones and long stretches, at random."""
+    rng = np.random.default_rng(40 + ps)
+    H, P = 2, 120
+    slots, pages = [], rng.permutation(P)
+    for p in pages:
+        a = int(rng.integers(0, ps))
+        b = int(rng.integers(a, ps)) + 1
+        slots += list(range(int(p) * ps + a, int(p) * ps + b))
+        slots += [-1] * int(rng.choice([0, 0, 1, 2, 15, 16, 17, 40]))
+    slots = np.array(slots, np.int64)
+    n = len(slots)
+    xk, xv = values(rng, n, H, torch.bfloat16), values(rng, n, H, torch.bfloat16)
+    kc_, vc_ = make_cache(rng, P, ps, H), make_cache(rng, P, ps, H)
+    check_append(run_append(bsp, xk, xv, slots, kc_, vc_), xk, xv, slots, kc_, vc_)
 
 
 def test_append_one_token_at_a_time_equals_the_oracle(bsp):
