@@ -736,6 +736,52 @@ def fp8_decode(bsp, dev, steps, warm, pk, cpu_seconds=0.0):
                          "algorithmic_bytes_per_launch": nbytes}}
 
 
+def fp8_cache_step(bsp, dev, steps, warm, pk, cpu_seconds=0.0):
+    """A decode step over the 8-bit cache with an exponent per page and kv head:
+    page tables from the lengths, append of every request's new token, attention.
+    The batched decode workload's requests and heads; the algorithmic bytes are
+    the attention's (codes, exponents, Q, O, LSE, page ids)."""
+    import workloads
+    b = workloads.batched_decode_bf16()
+    B, H, ps = b.batch, b.num_kv_heads, b.page_size
+    P = b.k_pages.shape[0]
+    g = torch.Generator(device=dev)
+    g.manual_seed(2)
+    f8, i32 = torch.float8_e4m3fn, torch.int32
+    k8, v8 = ((torch.randn((P, ps, H, 128), generator=g, device=dev) * 60).clamp_(-448, 448).to(f8) for _ in range(2))
+    ke, ve = (torch.randint(-8, -4, (P, H), generator=g, device=dev).to(torch.int8) for _ in range(2))
+    q, k, v = (torch.randn((B, h, 128), generator=g, device=dev).bfloat16() for h in (b.num_qo_heads, H, H))
+    pages = np.diff(b.kv_indptr)
+    table = torch.zeros((B, int(pages.max()) + 1), dtype=i32, device=dev)
+    for r in range(B):
+        table[r, :pages[r]] = torch.from_numpy(b.kv_indices[b.kv_indptr[r]:b.kv_indptr[r + 1]].astype(np.int32))
+    cached = torch.from_numpy((b.kv_lens - 1).astype(np.int32)).to(dev)
+    ones, free, nfree = torch.ones_like(cached), torch.from_numpy(b.kv_indices.astype(np.int32)).to(dev), \
+        torch.tensor([P], dtype=i32, device=dev)
+    n_pages = int(b.kv_indptr[-1])
+    tables = bsp.PageTables(B, n_pages, B, dev)
+    pa = bsp.PagedAttention("decode", b.num_qo_heads, H, 128, ps, False, torch.bfloat16, max_batch=B, device=dev)
+    pa.plan(b.kv_indptr, b.last_page_len)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    st = torch.cuda.Stream(device=dev)
+    steps_of = {"tables": lambda: bsp.build_page_tables(cached, ones, free, nfree, table, ps, n_pages, B, out=tables,
+                                                        stream=st),
+                "append": lambda: bsp.append_kv(k, v, tables.slot_map, k8, v8, ke, ve, stream=st),
+                "attention": lambda: pa.run(q, k8, v8, tables.kv_indices, b.sm_scale, out=out, lse=lse, stream=st,
+                                            k_exp=ke, v_exp=ve)}
+
+    def step():
+        for f in steps_of.values():
+            f()
+    ms = {n: graph_time(f, st, steps, warm) for n, f in [*steps_of.items(), ("step", step)]}
+    nbytes = int(b.kv_lens.sum()) * H * 128 * 2 + n_pages * (2 * H + 4) + B * b.num_qo_heads * (128 * 4 + 4)
+    gbs = nbytes / (ms["attention"] * 1e-3) / 1e9
+    return {"ms": round(ms["step"], 4), "us": {n: round(t * 1e3, 2) for n, t in ms.items()},
+            "attention_GB/s": round(gbs, 1), "attention_frac_of_hbm": round(gbs / pk["hbm_gbs"], 4), "bytes": nbytes,
+            "workload": "64 requests, KV ~ U{512..8192}, page 16, 32/8 heads, D 128, e4m3 cache with an exponent per page "
+                        "and kv head: tables, append and decode of one step, 10 steps per graph replay"}
+
+
 def vector_sparse_prefill(bsp, dev, steps, warm, pk, cpu_seconds=0.0):
     """One 32768-token causal prefill with page size 1, once on permuted slots and
     once contiguous, each planned with a gather region for its page table (the
@@ -919,7 +965,8 @@ def run_reference(args, rank, world):
 
 
 # secondary workloads that `--case` runs alone (profiling)
-CASES = {"ragged_causal_prefill": ragged_prefill, "fp8_kv_decode": fp8_decode, "shared_prefix_decode": shared_prefix,
+CASES = {"ragged_causal_prefill": ragged_prefill, "fp8_kv_decode": fp8_decode, "fp8_cache_step": fp8_cache_step,
+         "shared_prefix_decode": shared_prefix,
          "vector_sparse_prefill": vector_sparse_prefill, "vector_sparse_decode": vector_sparse_decode,
          "bsr_prefill": bsr_prefill, "tiny_decode_f32": tiny_decode_f32}
 

@@ -412,3 +412,46 @@ def test_page_ids_outside_the_pool_read_as_zeros(bsp, kind, ps):
     out, lse, pa = run_block(bsp, b, c8, num_ctas=4)
     check(out, lse, ref, 2.0 ** -11 if kind == "decode" else 2.0 ** -8, b)
     assert pa.check_device_error() == 0x302 and pa.check_device_error() == 0
+
+
+def test_streams_given_to_the_calls(bsp):
+    """Every call on a stream passed to it, another one current, the copy region included."""
+    b = workloads.paged_batch(242, [300, 64], [300, 200], 8, 2, 128, 16, "bf16", causal=True)
+    c8 = cache8(b, 242)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse, pa = run_block(bsp, b, c8, num_ctas=3, stream=s)
+    assert pa.lib.bsp_prefill_fp8_region_size(ctypes.byref(pa.info)) > 0
+    check(out, lse, reference(b, c8), 2.0 ** -8, b)
+    d = workloads.paged_batch(243, [1, 1], [300, 200], 8, 2, 128, 16, "bf16")
+    d8 = cache8(d, 243)
+    out, lse, _ = run_block(bsp, d, d8, num_ctas=3, stream=s)
+    check(out, lse, reference(d, d8), 2.0 ** -11, d)
+
+
+def test_run_refuses(bsp):
+    """Shapes, types and sizes that do not go with the plan or the pools."""
+    b = workloads.paged_batch(244, [1, 1], [40, 20], 8, 2, 128, 16, "bf16")
+    k8, ke, v8, ve = (torch.from_numpy(a).cuda() for a in cache8(b, 244))
+    f8 = torch.float8_e4m3fn
+    k8, v8, q = k8.view(f8), v8.view(f8), b.q.cuda()
+    idx = torch.from_numpy(np.ascontiguousarray(b.kv_indices, np.int32)).cuda()
+    pa = bsp.PagedAttention("decode", 8, 2, 128, 16, False, torch.bfloat16, max_batch=2)
+    with pytest.raises(RuntimeError):
+        pa.run(q, k8, v8, idx, k_exp=ke, v_exp=ve)  # no plan
+    pa.plan(b.kv_indptr, b.last_page_len)
+    ok = dict(q=q, k_pages=k8, v_pages=v8, kv_indices=idx, k_exp=ke, v_exp=ve)
+    for bad in (dict(k_exp=None), dict(v_exp=None), dict(k_scale=2.0), dict(q=q[:1]), dict(q=q[:, :4]), dict(q=q.float()),
+                dict(k_pages=k8.view(torch.uint8)), dict(k_pages=k8[:, :8]), dict(v_pages=v8[:1]), dict(k_exp=ke[:1]),
+                dict(k_exp=ke.short()), dict(kv_indices=idx[:1]), dict(kv_indices=idx.long()), dict(out=q[:1].clone()),
+                dict(out=q.float()), dict(lse=torch.zeros(2, 4, device="cuda")), dict(q=q.cpu())):
+        with pytest.raises(ValueError):
+            pa.run(**{**ok, **bad})
+    g17 = bsp.PagedAttention("decode", 34, 2, 128, 16, False, torch.bfloat16, max_batch=2)
+    g17.plan(b.kv_indptr, b.last_page_len)
+    with pytest.raises(bsp.BspError, match="UNSUPPORTED"):
+        g17.run(torch.zeros(2, 34, 128, dtype=torch.bfloat16, device="cuda"), k8, v8, idx, k_exp=ke, v_exp=ve)
+    f32 = bsp.PagedAttention("decode", 8, 2, 128, 16, False, torch.float32, max_batch=2)
+    f32.plan(b.kv_indptr, b.last_page_len)
+    with pytest.raises(ValueError):
+        f32.run(**ok)
