@@ -782,6 +782,40 @@ def fp8_cache_step(bsp, dev, steps, warm, pk, cpu_seconds=0.0):
                         "and kv head: tables, append and decode of one step, 10 steps per graph replay"}
 
 
+def fp8_cache_prefill(bsp, dev, steps, warm, pk, cpu_seconds=0.0):
+    """The ragged causal prefill's prompts into the 8-bit cache and over it: append
+    of all keys and values, then attention (with the bf16 copy of the pages)."""
+    import workloads
+    b = workloads.ragged_causal_prefill_bf16()
+    H, ps, n = b.num_kv_heads, b.page_size, int(b.qo_indptr[-1])
+    P = b.k_pages.shape[0]
+    f8 = torch.float8_e4m3fn
+    k8, v8 = (torch.zeros((P, ps, H, 128), dtype=torch.uint8, device=dev).view(f8) for _ in range(2))
+    ke, ve = (torch.zeros((P, H), dtype=torch.int8, device=dev) for _ in range(2))
+    g = torch.Generator(device=dev)
+    g.manual_seed(4)
+    k, v = (torch.randn((n, H, 128), generator=g, device=dev).bfloat16() for _ in range(2))
+    slots = np.concatenate([b.kv_indices[i0 + np.arange(m) // ps].astype(np.int64) * ps + np.arange(m) % ps
+                            for i0, m in zip(b.kv_indptr[:-1], b.qo_lens)])
+    slots, idx = torch.from_numpy(slots).to(dev), torch.from_numpy(b.kv_indices.astype(np.int32)).to(dev)
+    q = b.q.to(dev)
+    pa = bsp.PagedAttention("prefill", b.num_qo_heads, H, 128, ps, True, torch.bfloat16, max_batch=b.batch,
+                            max_qo_tokens=n, num_ctas=2 * bsp.default_num_ctas(bsp.BSP_MODE_PREFILL, dev.index),
+                            device=dev)
+    pa.plan(b.kv_indptr, b.last_page_len, qo_indptr=b.qo_indptr)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    st = torch.cuda.Stream(device=dev)
+    us = {"append": graph_time(lambda: bsp.append_kv(k, v, slots, k8, v8, ke, ve, stream=st), st, steps, warm) * 1e3,
+          "attention": graph_time(lambda: pa.run(q, k8, v8, idx, b.sm_scale, out=out, lse=lse, stream=st, k_exp=ke,
+                                                 v_exp=ve), st, steps, warm) * 1e3}
+    tf = prefill_flops(b) / us["attention"] / 1e6
+    return {"us": {i: round(t, 2) for i, t in us.items()}, "TFLOP/s": round(tf, 1),
+            "frac_of_bf16": round(tf / pk["bf16_tflops"], 4),
+            "append_GB/s": round(n * H * 128 * 2 * 3 / us["append"] / 1e3, 1),
+            "workload": "16 ragged causal prompts, 32/8 heads, D 128, page 16, appended to the 8-bit cache and attended "
+                        "over it, plan of 2 queues per CTA, 10 runs per graph replay"}
+
+
 def vector_sparse_prefill(bsp, dev, steps, warm, pk, cpu_seconds=0.0):
     """One 32768-token causal prefill with page size 1, once on permuted slots and
     once contiguous, each planned with a gather region for its page table (the
@@ -966,6 +1000,7 @@ def run_reference(args, rank, world):
 
 # secondary workloads that `--case` runs alone (profiling)
 CASES = {"ragged_causal_prefill": ragged_prefill, "fp8_kv_decode": fp8_decode, "fp8_cache_step": fp8_cache_step,
+         "fp8_cache_prefill": fp8_cache_prefill,
          "shared_prefix_decode": shared_prefix,
          "vector_sparse_prefill": vector_sparse_prefill, "vector_sparse_decode": vector_sparse_decode,
          "bsr_prefill": bsr_prefill, "tiny_decode_f32": tiny_decode_f32}

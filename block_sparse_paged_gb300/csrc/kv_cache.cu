@@ -22,7 +22,9 @@ namespace {
 // Every CTA computes the sums of all requests for itself, in shared memory, and
 // then expands its share of the entries and tokens: one launch, no pass over
 // global memory between the sums and their use, no atomics. The lengths are at
-// most 128 KB, read from L2.
+// most 128 KB, read from L2. Bound by the latency of that chain (lengths, sums, search,
+// entry): 5.7 us for 4 requests, 10.5 us for 0.8 M entries and as many slots (20 MB);
+// 2 to 8 CTAs per SM and 128 to 512 threads measured equal or slower.
 constexpr int kTabThreads = 256;
 constexpr int kTabUnit = 4;  // consecutive entries (tokens) per thread: one search, vector stores
 constexpr int kTabMaxBatch = 16384;
@@ -256,6 +258,8 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
 // maximum alone, from L2); all get the same exponent, and the CTA with the run's first
 // token writes it and rescales the codes that the page held before. A CTA that
 // reads the exponent after that write gets max(need, e) = e: the same.
+// 24k ragged bf16 tokens x 8 heads 37 us (149 MB); 64, 128 and 256 tokens per window: 38.9,
+// 37.5, 41.6; 3 to 6 CTAs per SM: 43.5, 37.5, 40.7, 42.9 (spills from 5 on).
 constexpr int kAppTokens = 128;
 constexpr int kExpMin = -117, kExpMax = 119;
 constexpr int kCacheD = 128;
@@ -581,7 +585,9 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
 // The same by runs: a warp owns the runs that begin among its 16 tokens, for one kv head's
 // K or V, and reads exactly their tokens. Everything meets by shuffles, no barrier, and no
 // token is read twice where runs have at most 16 tokens; a longer run is read once for its
-// maximum and once more (from L2) for its codes, 16 tokens at a time.
+// maximum and once more (from L2) for its codes, 16 tokens at a time. 24k ragged bf16
+// tokens x 8 heads 31.4 us (4.5 TB/s, 0.66 of the measured copy bandwidth): issue slots
+// 63% busy, the rest waits for loads.
 // CTA: 8 warps on neighbouring heads of the same tokens.
 constexpr int kSeg = 16;
 

@@ -37,6 +37,9 @@
 // rescaled only then. MMAs of the CTA execute in issue order, so S(t+1) cannot
 // overwrite P(t) before PV(t) has read it, and once S(t) is complete PV(t-1)
 // is too.
+// An e4m3 cache with an exponent per (page, kv head) is either converted into a bf16
+// copy first (convert_pages_kernel) and read like any pages, or converted by the
+// softmax warps on its way into the tiles (kFp8).
 // Every wait is a bounded spin (SM clock cycles); a wait that gives
 // up sets the workspace status word and an abort flag, and the CTA finishes
 // without further work.
@@ -858,8 +861,9 @@ __global__ void __launch_bounds__(256) gather_pages_kernel(const uint4 *__restri
 
 // The page table's pages of an e4m3 cache into a bf16 copy, in table order (the
 // gather region's layout): one warp per (page, K or V, piece of 256 16-byte
-// vectors), 8 loads of 16 codes per lane in flight, 32-byte stores. HBM-bound: one
-// byte read and two written per value. The number of table pages is the current
+// vectors), 8 loads of 16 codes per lane in flight, 32-byte stores. One byte read and
+// two written per value, the writes mostly into L2: 130 MB in 20.7 us (21k tokens x 8
+// heads), 400 MB in 52 us; smaller pieces and other grids measured the same. The number of table pages is the current
 // plan's (read from the workspace, so that a captured launch follows later plans);
 // pages beyond the region are not copied and set the status word.
 constexpr int kStatusRegion = 0x303;
