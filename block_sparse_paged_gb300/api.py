@@ -91,7 +91,8 @@ class PagedAttention:
     one tile) or "prefill" (ragged queries, 256-row tiles, tensor cores).
     max_gather_pages (prefill): pages of a K / V copy region in the workspace;
     prefills whose pages are under 8 tokens (or not a power of two) and whose
-    page table fits it are gathered into it first and then read by TMA.
+    page table fits it are gathered into it first and then read by TMA; prefills
+    over an e4m3 cache with exponents convert its pages into it.
     schedule: "lpt" (the pages' plan) or "equal" (equal contiguous shares of
     the concatenated KV ranges per CTA, for batches of few, equal tiles).
     The workspace and pinned staging buffer are allocated once, for the
@@ -176,7 +177,10 @@ class PagedAttention:
         k_scale * k_pages and v_scale * v_pages (one scale per pool), or, for bf16
         decode and prefill with head_dim 128 and any page size, such pools with one
         exponent per page and kv head: k_exp, v_exp int8 [num_pages, H_kv], value =
-        code * 2^exp (the cache that append_kv writes). sink:
+        code * 2^exp (the cache that append_kv writes). A prefill over such pools
+        may convert the plan's pages into a bf16 copy first: in the workspace's copy
+        region where max_gather_pages covers the page table, else in a temporary
+        tensor of this call. sink:
         float32 [H_qo] on the device, one extra softmax logit per query head
         without a value row (the attention-sink variant), or None."""
         if self.info is None:
@@ -267,12 +271,15 @@ class PagedAttention:
             _call(dev, stream, self.lib.bsp_decode_run_fp8_block, *args, self.workspace.data_ptr())
         else:
             nbytes = self.lib.bsp_prefill_fp8_region_size(ref)
-            copy = None
-            if nbytes:  # a bf16 copy of the plan's pages, for this run alone
+            ws = self.workspace.data_ptr()
+            region = copy = None
+            if nbytes and self.capacity.max_gather_pages >= info.num_table_pages:
+                region, nbytes = ws + info.off_gather, 2 * info.gather_pool_bytes  # the workspace's copy region
+            elif nbytes:  # a bf16 copy of the plan's pages, for this run alone
                 with torch.cuda.stream(stream):  # (None: the current one)
                     copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            _call(dev, stream, self.lib.bsp_prefill_run_fp8_block, *args, None if copy is None else copy.data_ptr(),
-                  nbytes, self.workspace.data_ptr())
+                region = copy.data_ptr()
+            _call(dev, stream, self.lib.bsp_prefill_run_fp8_block, *args, region, nbytes, ws)
         return (out, lse) if return_lse else out
 
     def _set_sink(self, sink):

@@ -2,6 +2,7 @@
 // launch of the run kernels, merge_state, error reporting.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <string>
 
@@ -124,12 +125,19 @@ namespace {
 constexpr int64_t kRegionReads2 = 3;       // twice the query tiles per cached token
 constexpr int64_t kRegionTokens = 4 * 128;  // KV tokens of work per CTA
 
+// A plan without queries and the NULL pointers of empty tensors: nothing to do.
+bool no_queries(const bsp_plan_info *plan, int mode, const void *q, const void *o) {
+    clear_error();
+    return plan && plan->valid == 1 && plan->problem.mode == mode && plan->num_qo_tokens == 0 && !q && !o;
+}
+
 int check_fp8_block(const bsp_plan_info *plan, int mode, const void *q, const void *k_pages, const void *v_pages,
                     const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
-                    const void *o, const void *workspace) {
+                    float sm_scale, const void *o, const void *workspace) {
     clear_error();
     int rc = check_plan(plan, mode, workspace);
     if (rc != BSP_OK) return rc;
+    if (!std::isfinite(sm_scale)) return fail(BSP_ERR_INVALID_ARG, "sm_scale must be finite");
     if (!q || !k_pages || !v_pages || !k_exp || !v_exp || !o) return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
     if (num_pages < 1 || num_pages > INT32_MAX) return fail(BSP_ERR_INVALID_ARG, "num_pages must be in [1, 2^31 - 1]");
     if (num_pages * plan->problem.page_size >= UINT32_MAX)
@@ -145,7 +153,9 @@ extern "C" int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q
                                         const void *v_pages, const int8_t *k_exp, const int8_t *v_exp,
                                         const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o,
                                         float *lse, void *workspace, bsp_stream_t stream) {
-    int rc = check_fp8_block(plan, BSP_MODE_DECODE, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, o, workspace);
+    if (no_queries(plan, BSP_MODE_DECODE, q, o)) return BSP_OK;
+    int rc = check_fp8_block(plan, BSP_MODE_DECODE, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o,
+                             workspace);
     if (rc != BSP_OK) return rc;
     return launch_decode_fp8_block(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse,
                                    workspace, stream);
@@ -167,8 +177,11 @@ extern "C" int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *
                                          const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o,
                                          float *lse, void *region, size_t region_bytes, void *workspace,
                                          bsp_stream_t stream) {
-    int rc = check_fp8_block(plan, BSP_MODE_PREFILL, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, o, workspace);
+    if (no_queries(plan, BSP_MODE_PREFILL, q, o)) return BSP_OK;
+    int rc = check_fp8_block(plan, BSP_MODE_PREFILL, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o,
+                             workspace);
     if (rc != BSP_OK) return rc;
+    if (sm_scale <= 0.f) return fail(BSP_ERR_INVALID_ARG, "prefill needs a positive sm_scale");
     int64_t pages = 0;
     if (region) {
         if (reinterpret_cast<uintptr_t>(region) % 32 != 0)

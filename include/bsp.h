@@ -465,6 +465,7 @@ int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int6
  *   k_pages, v_pages   device, e4m3 bytes [num_pages, page_size, H_kv, 128]
  *   k_exp, v_exp       device, int8 [num_pages, H_kv]
  *   num_pages          pages in each pool, 1 .. 2^31 - 1
+ *   sm_scale           finite; > 0 for prefill
  * Any page size. Decode: g <= 16; scores and sums fp32, token weights times
  * 2^v_exp in f16 against their own running maximum. Prefill: 128 % g == 0; codes are
  * converted to bf16 (exact for exponents in [-117, 119]), either on their way to
@@ -472,6 +473,8 @@ int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int6
  *   region             device scratch, 32-byte aligned, region_bytes >=
  *                      num_table_pages * page_size * H_kv * 512 (else
  *                      BSP_ERR_CAPACITY); contents undefined before and after.
+ *                      (The plan's own copy region of capacity.max_gather_pages
+ *                      serves: workspace + off_gather, 2 * gather_pool_bytes.)
  * bsp_prefill_fp8_region_size tells which is faster. A captured run replayed after
  * a plan with a larger page table than its region holds sets the status word
  * (0x303). A page id outside [0, num_pages) reads as zero codes and sets the

@@ -455,3 +455,63 @@ def test_run_refuses(bsp):
     f32.plan(b.kv_indptr, b.last_page_len)
     with pytest.raises(ValueError):
         f32.run(**ok)
+
+
+def test_prefill_in_the_workspace_region(bsp):
+    """max_gather_pages: the copy goes into the plan's workspace, nothing is allocated by the run, the captured run
+    follows a plan with a larger table within the bound."""
+    a = workloads.paged_batch(245, [300], [300], 8, 2, 128, 16, "bf16", causal=True)
+    b = workloads.paged_batch(246, [300], [900], 8, 2, 128, 16, "bf16", causal=True)
+    pa = bsp.PagedAttention("prefill", 8, 2, 128, 16, True, torch.bfloat16, max_batch=1, max_qo_tokens=300, num_ctas=4,
+                            max_gather_pages=57)
+    f8 = torch.float8_e4m3fn
+    P = b.k_pages.shape[0]
+    pool = [torch.zeros((P,) + x.shape[1:], dtype=torch.from_numpy(x).dtype, device="cuda") for x in cache8(b, 246)]
+    idx = torch.zeros(64, dtype=torch.int32, device="cuda")
+    q, o, l = a.q.cuda(), torch.empty_like(a.q, device="cuda"), torch.empty(a.q.shape[:2], device="cuda")
+
+    def load(x, c8):
+        for t, h in zip(pool, c8):
+            t[:h.shape[0]].copy_(torch.from_numpy(h))
+        idx[:len(x.kv_indices)].copy_(torch.from_numpy(np.ascontiguousarray(x.kv_indices, np.int32)))
+        q.copy_(x.q)
+        pa.plan(x.kv_indptr, x.last_page_len, qo_indptr=x.qo_indptr)
+
+    def run():
+        pa.run(q, pool[0].view(f8), pool[2].view(f8), idx, out=o, lse=l, k_exp=pool[1], v_exp=pool[3])
+    ca, cb = cache8(a, 245), cache8(b, 246)
+    load(a, ca)
+    run()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    run()
+    assert torch.cuda.max_memory_allocated() == before
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for x, c in ((a, ca), (b, cb)):
+        load(x, c)
+        o.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        check(o, l, reference(x, c), 2.0 ** -8, x)
+    assert pa.check_device_error() == 0
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+def test_no_requests_and_no_keys(bsp, mode):
+    """An empty batch, and a batch whose requests are all empty: O = 0, LSE = -inf."""
+    b = workloads.paged_batch(247, [1, 1], [40, 20], 8, 2, 128, 16, "bf16")
+    k8, ke, v8, ve = (torch.from_numpy(a).cuda() for a in cache8(b, 247))
+    f8 = torch.float8_e4m3fn
+    pa = bsp.PagedAttention(mode, 8, 2, 128, 16, False, torch.bfloat16, max_batch=4, max_qo_tokens=8)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    pa.plan([0], [], qo_indptr=[0])
+    o, l = pa.run(torch.zeros(0, 8, 128, dtype=torch.bfloat16, device="cuda"), k8.view(f8), v8.view(f8), none, k_exp=ke,
+                  v_exp=ve)
+    assert o.shape == (0, 8, 128) and l.shape == (0, 8)
+    pa.plan([0, 0, 0], [0, 0], qo_indptr=[0, 1, 2])
+    o, l = pa.run(b.q.cuda(), k8.view(f8), v8.view(f8), none, k_exp=ke, v_exp=ve)
+    torch.cuda.synchronize()
+    assert (o == 0).all() and torch.isneginf(l).all() and pa.check_device_error() == 0

@@ -161,6 +161,14 @@ def test_block_runs_refuse(native, mode, kw):
     assert fn(*run_args(block_plan(mode), **kw)) == native.BSP_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("scale,modes", [(float("nan"), (0, 1)), (float("inf"), (0, 1)), (0.0, (1,)), (-1.0, (1,))])
+def test_block_runs_refuse_scales(native, scale, modes):
+    lib = native.load()
+    for mode in modes:
+        fn = lib.bsp_decode_run_fp8_block if mode == 0 else lib.bsp_prefill_run_fp8_block
+        assert fn(*run_args(block_plan(mode), scale=scale)) == native.BSP_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("mode", [0, 1])
 def test_block_runs_refuse_plans(native, mode):
     import torch
