@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     // page of column i of request b: from the row, or from the free list (-1: none left)
     auto page_of = [&](int b, int old_pages, int i) -> int {
         if (i < old_pages) return p.table[(long long)b * p.table_stride + i];
-        const int k = s_take[b] + (i - old_pages);
-        return k < n_free ? __ldg(p.free_pages + k) : -1;
+        const uint32_t k = (uint32_t)s_take[b] + (uint32_t)(i - old_pages);  // (s_take saturates at 2^31 - 1)
+        return k < (uint32_t)n_free ? __ldg(p.free_pages + k) : -1;
     };
 
     // One index space: groups of kTabUnit table entries, then groups of tokens, so that
@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
         long long slot[kTabUnit];
         int pos[kTabUnit];
         int b = 0, end = -1, begin = 0;
-        int col = 0, off = 0;
+        uint32_t col = 0;  // (past 2^31 with pages of one token)
+        int off = 0;
         TableRow r{};
 #pragma unroll
         for (int u = 0; u < kTabUnit; ++u) {
@@ -214,15 +215,15 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
                     end = s_tok[b + 1];
                     r = table_row(p, b);
                     const uint32_t x = (uint32_t)r.cached + (uint32_t)((int)t - begin);
-                    col = (int)(x / (uint32_t)p.ps);
-                    off = (int)(x - (uint32_t)col * (uint32_t)p.ps);
+                    col = x / (uint32_t)p.ps;
+                    off = (int)(x - col * (uint32_t)p.ps);
                 } else if (++off == p.ps) {
                     off = 0;
                     ++col;
                 }
                 pos[u] = (int)min((long long)r.cached + ((int)t - begin), (long long)INT32_MAX);
-                if (col < r.all_pages) {
-                    const int pg = page_of(b, r.old_pages, col);
+                if (col < (uint32_t)r.all_pages) {
+                    const int pg = page_of(b, r.old_pages, (int)col);
                     if (pg >= 0) slot[u] = (long long)pg * p.ps + off;
                 }
             }

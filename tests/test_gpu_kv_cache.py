@@ -112,6 +112,17 @@ def test_tables_huge_lengths_saturate(bsp):
     assert got["slot_map"].tolist() == [-1] * 8 and got["kv_indptr"].tolist() == [0, 3, 6]
 
 
+def test_tables_single_token_pages_past_31_bits(bsp):
+    """Columns of new tokens from 2^31 on, far past the row: no slot."""
+    cached, new = np.array([2 ** 31 - 1, 2 ** 31 - 2], np.int32), np.array([5, 3], np.int32)
+    bt = np.full((2, 3), 1, np.int32)
+    got = run_tables(bsp, cached, new, np.arange(4, dtype=np.int32), 4, bt, 1, 8, 10)
+    assert got["counts"].tolist() == [6, 8, 0, 2]
+    assert got["slot_map"].tolist() == [-1] * 10 and got["qo_indptr"].tolist() == [0, 5, 8]
+    assert got["positions"].tolist() == [2 ** 31 - 1] * 5 + [2 ** 31 - 2] + [2 ** 31 - 1] * 2 + [0, 0]
+    assert (got["block_table"] == 1).all()
+
+
 # ---- append --------------------------------------------------------------------
 def make_cache(rng, P, ps, H):
     codes = rng.integers(0, 256, (P, ps, H, 128)).astype(np.uint8)
