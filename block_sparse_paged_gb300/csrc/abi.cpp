@@ -124,6 +124,7 @@ namespace {
 // tokens 19.5 / 16.4 us (a launch less).
 constexpr int64_t kRegionReads2 = 3;       // twice the query tiles per cached token
 constexpr int64_t kRegionTokens = 4 * 128;  // KV tokens of work per CTA
+constexpr int64_t kRegionPageRows = 1 << 27;  // rows of a page, all heads: the copy counts a page's vectors in 32 bits
 
 // A plan without queries and the NULL pointers of empty tensors: nothing to do.
 bool no_queries(const bsp_plan_info *plan, int mode, const void *q, const void *o) {
@@ -165,7 +166,7 @@ extern "C" size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan) {
     clear_error();
     if (!plan || plan->problem.mode != BSP_MODE_PREFILL || plan->num_table_pages <= 0) return 0;
     const int64_t tokens = (int64_t)plan->num_table_pages * plan->problem.page_size;
-    if (tokens > INT32_MAX) return 0;
+    if (tokens > INT32_MAX || (int64_t)plan->problem.page_size * plan->problem.num_kv_heads > kRegionPageRows) return 0;
     if (2 * plan->total_work < kRegionReads2 * tokens * plan->problem.num_kv_heads ||
         plan->total_work < kRegionTokens * plan->capacity.num_ctas)
         return 0;
@@ -186,6 +187,8 @@ extern "C" int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *
     if (region) {
         if (reinterpret_cast<uintptr_t>(region) % 32 != 0)
             return fail(BSP_ERR_INVALID_ARG, "the region is not 32-byte aligned");
+        if ((int64_t)plan->problem.page_size * plan->problem.num_kv_heads > kRegionPageRows)
+            return fail(BSP_ERR_UNSUPPORTED, "a copy takes pages of at most 2^27 rows over all heads: pass no region");
         const size_t per_page = (size_t)plan->problem.page_size * plan->problem.num_kv_heads * 512;  // bf16 K and V
         pages = (int64_t)std::min<size_t>(region_bytes / per_page, (size_t)(INT32_MAX / plan->problem.page_size));
         if (pages < plan->num_table_pages) return fail(BSP_ERR_CAPACITY, "the region is too small for the plan's page table");

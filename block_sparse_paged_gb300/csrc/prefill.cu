@@ -863,9 +863,10 @@ __global__ void __launch_bounds__(256) gather_pages_kernel(const uint4 *__restri
 // gather region's layout): one warp per (page, K or V, piece of 256 16-byte
 // vectors), 8 loads of 16 codes per lane in flight, 32-byte stores. One byte read and
 // two written per value, the writes mostly into L2: 130 MB in 20.7 us (21k tokens x 8
-// heads), 400 MB in 52 us; smaller pieces and other grids measured the same. The number of table pages is the current
-// plan's (read from the workspace, so that a captured launch follows later plans);
-// pages beyond the region are not copied and set the status word.
+// heads), 400 MB in 52 us; smaller pieces and other grids measured the same. The number
+// of table pages is the current plan's (read from the workspace, so that a captured
+// launch follows later plans); pages beyond the region are not copied and set the
+// status word.
 constexpr int kStatusRegion = 0x303;
 constexpr int kCvtVecs = 256;  // 16-byte vectors of codes per warp and turn
 

@@ -472,7 +472,8 @@ int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int6
  * the tensor cores (region NULL) or, once for all query tiles, into a copy in
  *   region             device scratch, 32-byte aligned, region_bytes >=
  *                      num_table_pages * page_size * H_kv * 512 (else
- *                      BSP_ERR_CAPACITY); contents undefined before and after.
+ *                      BSP_ERR_CAPACITY), page_size * H_kv <= 2^27; contents
+ *                      undefined before and after.
  *                      (The plan's own copy region of capacity.max_gather_pages
  *                      serves: workspace + off_gather, 2 * gather_pool_bytes.)
  * bsp_prefill_fp8_region_size tells which is faster. A captured run replayed after

@@ -202,3 +202,17 @@ def test_region_size_and_refusals(native):
         a[-4:-2] = [region, nbytes]
         assert lib.bsp_prefill_run_fp8_block(*a) == rc
     assert lib.bsp_prefill_fp8_region_size(ctypes.byref(block_plan(0))) == 0
+
+
+def test_region_of_pages_past_the_conversion_kernel(native):
+    """Pages of 2^28 rows over all heads (32-bit vector counts): converted inside only."""
+    import torch
+    import block_sparse_paged_gb300 as bsp
+    lib = native.load()
+    prob = bsp.make_problem(1, 64, 2, 128, 1 << 27, True, torch.bfloat16)
+    info = bsp.plan_host(prob, bsp.Capacity(1, 2, 1 << 20, 1, 0, 0), [0, 1], [1 << 27], [0, 1 << 20])[0]
+    info.valid = 1
+    assert lib.bsp_prefill_fp8_region_size(ctypes.byref(info)) == 0
+    a = run_args(info)
+    a[-4:-2] = [A, 1 << 38]
+    assert lib.bsp_prefill_run_fp8_block(*a) == native.BSP_ERR_UNSUPPORTED
