@@ -37,7 +37,8 @@ _ERR_NAMES = {BSP_ERR_INVALID_ARG: "INVALID_ARG", BSP_ERR_CAPACITY: "CAPACITY", 
 EXPORTED = ["bsp_default_num_ctas", "bsp_workspace_size", "bsp_host_staging_size", "bsp_plan",
             "bsp_decode_run", "bsp_decode_run_fp8", "bsp_prefill_run", "bsp_run_attention", "bsp_run_merge_partials",
             "bsp_merge_state", "bsp_build_page_tables", "bsp_append_kv_fp8", "bsp_decode_run_fp8_block",
-            "bsp_prefill_run_fp8_block", "bsp_prefill_fp8_region_size", "bsp_decode_run_static", "bsp_check_device_error", "bsp_check_bounded_wait",
+            "bsp_prefill_run_fp8_block", "bsp_decode_fp8_region_size", "bsp_prefill_fp8_region_size",
+            "bsp_decode_run_static", "bsp_check_device_error", "bsp_check_bounded_wait",
             "bsp_last_error", "bsp_version"]
 
 
@@ -114,7 +115,9 @@ def load():
                                    vp], ctypes.c_int),
         "bsp_append_kv_fp8": ([vp, vp, i64, i64, i64, i64, i32, i64, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp],
                               ctypes.c_int),
-        "bsp_decode_run_fp8_block": ([PI, vp, vp, vp, vp, vp, vp, i64, f32, vp, vp, vp, vp], ctypes.c_int),
+        "bsp_decode_run_fp8_block": ([PI, vp, vp, vp, vp, vp, vp, i64, f32, vp, vp, vp, ctypes.c_size_t, vp, vp],
+                                     ctypes.c_int),
+        "bsp_decode_fp8_region_size": ([PI], ctypes.c_size_t),
         "bsp_prefill_run_fp8_block": ([PI, vp, vp, vp, vp, vp, vp, i64, f32, vp, vp, vp, ctypes.c_size_t, vp, vp],
                                       ctypes.c_int),
         "bsp_prefill_fp8_region_size": ([PI], ctypes.c_size_t),

@@ -267,19 +267,21 @@ class PagedAttention:
         args = (ref, q_p, _addr(k_pages, "k_pages", f8, dev), _addr(v_pages, "v_pages", f8, dev),
                 _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev),
                 _addr(kv_indices, "kv_indices", torch.int32, dev) or None, pool[0], sm_scale, out_p, lse_p)
-        if self.mode == N.BSP_MODE_DECODE:
-            _call(dev, stream, self.lib.bsp_decode_run_fp8_block, *args, self.workspace.data_ptr())
-        else:
-            nbytes = self.lib.bsp_prefill_fp8_region_size(ref)
-            ws = self.workspace.data_ptr()
-            region = copy = None
-            if nbytes and self.capacity.max_gather_pages >= info.num_table_pages:
-                region, nbytes = ws + info.off_gather, 2 * info.gather_pool_bytes  # the workspace's copy region
-            elif nbytes:  # a bf16 copy of the plan's pages, for this run alone
-                with torch.cuda.stream(stream):  # (None: the current one)
+        decode = self.mode == N.BSP_MODE_DECODE
+        nbytes = (self.lib.bsp_decode_fp8_region_size if decode else self.lib.bsp_prefill_fp8_region_size)(ref)
+        ws = self.workspace.data_ptr()
+        region = copy = None
+        if nbytes and not decode and self.capacity.max_gather_pages >= info.num_table_pages:
+            region, nbytes = ws + info.off_gather, 2 * info.gather_pool_bytes  # the workspace's copy region
+        elif nbytes:  # scratch of this run alone: the plan's exponents, or a bf16 copy of its pages
+            if stream is None:
+                copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            else:
+                with torch.cuda.stream(stream):
                     copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-                region = copy.data_ptr()
-            _call(dev, stream, self.lib.bsp_prefill_run_fp8_block, *args, region, nbytes, ws)
+            region = copy.data_ptr()
+        fn = self.lib.bsp_decode_run_fp8_block if decode else self.lib.bsp_prefill_run_fp8_block
+        _call(dev, stream, fn, *args, region, nbytes, ws)
         return (out, lse) if return_lse else out
 
     def _set_sink(self, sink):

@@ -84,10 +84,12 @@ int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages
                    const void *v_pages, const int32_t *kv_indices, int64_t num_pages,
                    float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream);
 // Decode and prefill over an e4m3 cache with one exponent per (page, kv head); num_pages in 1 .. 2^31 - 1.
+// region (or NULL), decode: K exponents by table entry, then V's, of region_entries entries per head each.
 int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                             const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
-                            float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream);
-// region (or NULL): bf16 K copy, then V copy, of region_pages pages each.
+                            float sm_scale, void *o, float *lse, void *region, int64_t region_entries, void *workspace,
+                            cudaStream_t stream);
+// region (or NULL), prefill: bf16 K copy, then V copy, of region_pages pages each.
 int launch_prefill_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                              const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
                              float sm_scale, void *o, float *lse, void *region, int64_t region_pages, void *workspace,

@@ -43,7 +43,7 @@
 // carried through the ring as bytes; scores times 2^e_k, token weights 2^(s + e_v)
 // against their own running maximum, so that they fit f16 however far exponents lie
 // apart. HBM-bound: 64 requests x 4,585 tokens 98-99 us, 6.1 TB/s, 0.90 of the measured
-// copy bandwidth; page size 1 (cp.async) 72 us for 268 MB.
+// copy bandwidth; page size 1 (cp.async) 57 us for 268 MB, exponents gathered first.
 // fp32 kernel: CUDA cores, fp32 throughout, same plan and merge.
 // Reduction kernel: the reduction map's slots of each split output, merged in
 // ascending order with a common maximum (technical review eq 6); used after the
@@ -168,6 +168,8 @@ struct DecodeParams {
     const float *sink;       // per-qo-head sink logits, or null
     const int8_t *k_exp, *v_exp;  // kBlk: exponents [num_pages][H_kv]
     int num_pages;                // kBlk: page ids outside [0, num_pages) read as zero codes
+    const int8_t *exp_table;      // kBlk, cp.async: exponents of the first exp_entries table
+    int exp_entries;              // entries, [K, V][H_kv][exp_entries]; the further ones by page
 };
 
 // Fold of one (row r, columns 4 cq .. 4 cq + 3) unit of a reduction-map entry
@@ -418,13 +420,16 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                 const char *base = src + (size_t)w.kv_head * D + c16 * 16;
                 // table column and place in its page of this lane's tokens: of the stage whose
                 // ids are read next (q, r)
-                int q[kJ], r[kJ], id1[kJ], r1[kJ], ex1[kJ];
+                int q[kJ], r[kJ], id1[kJ], r1[kJ], q1[kJ], ex1[kJ];
                 uint32_t row0[kJ];
+                const int8_t *by_page = exps + w.kv_head;
+                const int8_t *by_entry = p.exp_table + ((is_v ? p.H_kv : 0) + w.kv_head) * (size_t)p.exp_entries;
                 auto fetch = [&](int t) {  // ids of stage t into id1 / r1; advances (q, r)
 #pragma unroll
                     for (int j = 0; j < kJ; ++j) {
                         id1[j] = t * kTK + tok_base + lane + 32 * j < len ? __ldg(ids + q[j]) : 0;
                         r1[j] = r[j];
+                        q1[j] = w.page_base + q[j];
                         q[j] += step_q;
                         r[j] += step_r;
                         if (r[j] >= p.page_size) { r[j] -= p.page_size; ++q[j]; }
@@ -437,7 +442,8 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                         const bool live = t * kTK + tok_base + lane + 32 * j < len;
                         const bool in = (unsigned)id1[j] < (unsigned)p.num_pages;
                         row0[j] = in ? (uint32_t)id1[j] * (uint32_t)p.page_size + (uint32_t)r1[j] : kBadRow;
-                        ex1[j] = live && in ? __ldg(exps + (size_t)id1[j] * p.H_kv + w.kv_head) : 0;
+                        const int8_t *at = q1[j] < p.exp_entries ? by_entry + q1[j] : by_page + (size_t)id1[j] * p.H_kv;
+                        ex1[j] = live && in ? __ldg(at) : 0;
                         bad |= live && !in;
                     }
                     if (bad) atomicCAS(status, 0, kStatusPageIndex);
@@ -1339,6 +1345,60 @@ __global__ void __launch_bounds__(256) reduce_kernel(const ReduceParams p) {
     }
 }
 
+// The exponents of the page table's pages in table order, by head: out[K, V][H][entries].
+// With pages of one token the loader warps would ask for a 32-byte sector per byte, as many
+// requests as for the rows themselves, and each head again for the same sector: 20 of 72 us
+// for 32 requests x 4096 tokens x 8 heads. Here a thread takes kExpUnit entries of K or V,
+// all heads of each in one or two sectors; the loaders then read 32 adjacent bytes. About 4
+// us for 131k tokens, the launch included. The number of entries is the current plan's (from the
+// workspace, so that a captured run follows later plans); those beyond the region are
+// read by page.
+constexpr int kExpUnit = 4;
+
+__global__ void __launch_bounds__(256) gather_exponents_kernel(const int8_t *__restrict__ k, const int8_t *__restrict__ v,
+                                                               uint32_t *__restrict__ out,
+                                                               const int32_t *__restrict__ idx,
+                                                               const DevHeader *__restrict__ hdr, int entries,
+                                                               int num_pages, int H) {
+    const int n = min(hdr->num_table_pages, entries);
+    const int8_t *e = blockIdx.y ? v : k;
+    out += (size_t)blockIdx.y * H * (entries / kExpUnit);
+    const bool words = H % 4 == 0 && reinterpret_cast<uintptr_t>(e) % 4 == 0;
+    for (int u = blockIdx.x * 256 + threadIdx.x; u * (long long)kExpUnit < n; u += gridDim.x * 256) {
+        size_t at[kExpUnit];
+        bool in[kExpUnit];
+#pragma unroll
+        for (int i = 0; i < kExpUnit; ++i) {
+            const int id = u * kExpUnit + i < n ? __ldg(idx + u * kExpUnit + i) : -1;
+            in[i] = (unsigned)id < (unsigned)num_pages;
+            at[i] = in[i] ? (size_t)id * H : 0;
+        }
+        if (words) {
+#pragma unroll 2
+            for (int h = 0; h < H; h += 4) {
+                uint32_t x[kExpUnit];
+#pragma unroll
+                for (int i = 0; i < kExpUnit; ++i) x[i] = in[i] ? __ldg(reinterpret_cast<const uint32_t *>(e + at[i] + h)) : 0;
+                // 4 x 4 bytes transposed: word h of the result holds head h of the four entries
+                const uint32_t lo01 = prmt(x[0], x[1], 0x5140), hi01 = prmt(x[0], x[1], 0x7362);
+                const uint32_t lo23 = prmt(x[2], x[3], 0x5140), hi23 = prmt(x[2], x[3], 0x7362);
+                uint32_t *o = out + (size_t)h * (entries / kExpUnit) + u;
+                o[0] = prmt(lo01, lo23, 0x5410);
+                o[entries / kExpUnit] = prmt(lo01, lo23, 0x7632);
+                o[2 * (size_t)(entries / kExpUnit)] = prmt(hi01, hi23, 0x5410);
+                o[3 * (size_t)(entries / kExpUnit)] = prmt(hi01, hi23, 0x7632);
+            }
+        } else {
+            for (int h = 0; h < H; ++h) {
+                uint32_t x = 0;
+#pragma unroll
+                for (int i = 0; i < kExpUnit; ++i) x |= in[i] ? (uint32_t)(uint8_t)__ldg(e + at[i] + h) << (8 * i) : 0;
+                out[(size_t)h * (entries / kExpUnit) + u] = x;
+            }
+        }
+    }
+}
+
 int num_sms_of_current_device(int *dev_out) {
     static int sms[64] = {0};
     int dev = 0;
@@ -1434,6 +1494,8 @@ int decode_params(const bsp_plan_info *plan, const void *q, const void *k_pages,
     p.sink = P.sink;
     p.k_exp = p.v_exp = nullptr;
     p.num_pages = 0;
+    p.exp_table = nullptr;
+    p.exp_entries = 0;
     p.window_left = P.window_left;
     p.soft_cap_on = P.logits_soft_cap > 0.f;
     p.cap_in = p.soft_cap_on ? qk_scale / P.logits_soft_cap : 0.f;
@@ -1526,7 +1588,8 @@ int launch_decode_fp8(const bsp_plan_info *plan, const void *q, const void *k_pa
 
 int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                             const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
-                            float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream) {
+                            float sm_scale, void *o, float *lse, void *region, int64_t region_entries, void *workspace,
+                            cudaStream_t stream) {
     const bsp_problem &P = plan->problem;
     if (P.dtype != BSP_DTYPE_BF16 || P.head_dim != 128)
         return fail(BSP_ERR_UNSUPPORTED, "e4m3 KV decode needs a bf16 problem (queries, outputs) with head_dim 128");
@@ -1551,6 +1614,17 @@ int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void
         if (rc != BSP_OK) return rc;
         return plan->group <= 8 ? launch_decode_bf16<128, true, true, 1, true>(tk, tv, p, grid, stream)
                                 : launch_decode_bf16<128, true, true, 2, true>(tk, tv, p, grid, stream);
+    }
+    if (region) {
+        p.exp_table = static_cast<int8_t *>(region);
+        p.exp_entries = (int)region_entries;
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        const int64_t ctas = (region_entries / kExpUnit + 255) / 256;
+        gather_exponents_kernel<<<dim3((unsigned)std::min<int64_t>(ctas, 1024), 2), 256, 0, stream>>>(
+            k_exp, v_exp, static_cast<uint32_t *>(region), kv_indices, reinterpret_cast<const DevHeader *>(ws + plan->off_header),
+            (int)region_entries, (int)num_pages, P.num_kv_heads);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("exponents launch: ") + cudaGetErrorString(e));
     }
     return plan->group <= 8 ? launch_decode_bf16<128, false, true, 1, true>(tk, tv, p, grid, stream)
                             : launch_decode_bf16<128, false, true, 2, true>(tk, tv, p, grid, stream);

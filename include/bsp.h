@@ -466,28 +466,38 @@ int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int6
  *   k_exp, v_exp       device, int8 [num_pages, H_kv]
  *   num_pages          pages in each pool, 1 .. 2^31 - 1
  *   sm_scale           finite; > 0 for prefill
+ *   region             device scratch of region_bytes, or NULL; contents undefined
+ *                      before and after. bsp_decode_fp8_region_size and
+ *                      bsp_prefill_fp8_region_size give the bytes, 0 where the run is
+ *                      faster without; too small a region is BSP_ERR_CAPACITY
  * Any page size. Decode: g <= 16; scores and sums fp32, token weights times
- * 2^v_exp in f16 against their own running maximum. Prefill: 128 % g == 0; codes are
- * converted to bf16 (exact for exponents in [-117, 119]), either on their way to
- * the tensor cores (region NULL) or, once for all query tiles, into a copy in
- *   region             device scratch, 32-byte aligned, region_bytes >=
- *                      num_table_pages * page_size * H_kv * 512 (else
- *                      BSP_ERR_CAPACITY), page_size * H_kv <= 2^27; contents
- *                      undefined before and after.
- *                      (The plan's own copy region of capacity.max_gather_pages
- *                      serves: workspace + off_gather, 2 * gather_pool_bytes.)
- * bsp_prefill_fp8_region_size tells which is faster. A captured run replayed after
- * a plan with a larger page table than its region holds sets the status word
- * (0x303). A page id outside [0, num_pages) reads as zero codes and sets the
+ * 2^v_exp in f16 against their own running maximum. Its region (16-byte aligned,
+ * num_table_pages rounded up to 16, times 2 * H_kv bytes) takes the plan's exponents in
+ * table order (pages that are no power of two of 8 or more tokens; otherwise unused).
+ * A captured run may be replayed after a plan with a larger table than its region
+ * holds: the exponents beyond are read by page.
+ * Prefill: 128 % g == 0; codes are converted to bf16 (exact for exponents in [-117,
+ * 119]), either on their way to the tensor cores (region NULL) or, once for all
+ * query tiles, into a copy in the region (32-byte aligned, num_table_pages *
+ * page_size * H_kv * 512 bytes, page_size * H_kv <= 2^27). The plan's own copy region
+ * of capacity.max_gather_pages serves: workspace + off_gather, 2 * gather_pool_bytes.
+ * A captured run replayed after a plan with a larger page table than its region holds
+ * sets the status word (0x303). A page id outside [0, num_pages) reads as zero codes and sets the
  * workspace status word (0x302, bsp_check_device_error).
  */
 int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                              const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
-                             float sm_scale, void *o, float *lse, void *workspace, bsp_stream_t stream);
+                             float sm_scale, void *o, float *lse, void *region, size_t region_bytes, void *workspace,
+                             bsp_stream_t stream);
 int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                               const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
                               float sm_scale, void *o, float *lse, void *region, size_t region_bytes,
                               void *workspace, bsp_stream_t stream);
+
+/* Bytes of the region that bsp_decode_run_fp8_block wants for this plan (pages of one
+ * token and 2560 tokens of work or more per CTA, or of two and 5120), or 0 where it is
+ * faster without. */
+size_t bsp_decode_fp8_region_size(const bsp_plan_info *plan);
 
 /* Bytes of the region that bsp_prefill_run_fp8_block wants for this plan (a bf16
  * copy of its page table's K and V), or 0 where converting inside the attention

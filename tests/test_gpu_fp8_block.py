@@ -122,6 +122,71 @@ def test_decode(bsp, case):
     assert pa.check_device_error() == 0
 
 
+@pytest.mark.parametrize("case", DECODE, ids=[f"d{c[0]}" for c in DECODE])
+def test_decode_with_exponents_gathered_first(bsp, case):
+    """The C entry without a region, with one, with a larger one, and with one that the table outgrew since the
+    capture: the same bits."""
+    seed, kv, hq, hk, ps, C, w, cap = case
+    b = workloads.paged_batch(seed, [1] * len(kv), kv, hq, hk, 128, ps, "bf16", extra_pages=3)
+    b.window_left, b.soft_cap = w, cap
+    few = workloads.paged_batch(seed, [1] * len(kv), [min(n, 1 + i) for i, n in enumerate(kv)], hq, hk, 128, ps, "bf16")
+    c8 = cache8(b, seed)
+    pa = bsp.PagedAttention("decode", hq, hk, 128, ps, False, torch.bfloat16, max_batch=b.batch, max_qo_tokens=b.batch,
+                            num_ctas=C, window_left=w, logits_soft_cap=cap)
+    k8, ke, v8, ve = (torch.from_numpy(a).cuda() for a in c8)
+    idx = torch.from_numpy(np.ascontiguousarray(b.kv_indices, np.int32)).cuda()
+    q = b.q.cuda()
+    n, got = -(-len(idx) // 16) * 16, []
+    for entries in (0, n, n + 32, None):
+        region = torch.full(((n if entries is None else entries) * 2 * hk,), 0x7f, dtype=torch.uint8, device="cuda")
+        o, l = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+
+        def run(nbytes):
+            rc = pa.lib.bsp_decode_run_fp8_block(
+                ctypes.byref(pa.info), q.data_ptr(), k8.data_ptr(), v8.data_ptr(), ke.data_ptr(), ve.data_ptr(),
+                idx.data_ptr(), k8.shape[0], b.sm_scale, o.data_ptr(), l.data_ptr(), region.data_ptr() if nbytes else None,
+                nbytes, pa.workspace.data_ptr(), torch.cuda.current_stream().cuda_stream)
+            assert rc == 0
+        if entries is None:
+            pa.plan(few.kv_indptr, few.last_page_len, qo_indptr=few.qo_indptr)
+            small = -(-pa.info.num_table_pages // 16) * 16 * 2 * hk
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                run(small)
+            pa.plan(b.kv_indptr, b.last_page_len, qo_indptr=b.qo_indptr)
+            g.replay()
+            torch.cuda.synchronize()
+            assert (region[small:] == 0x7f).all()
+        else:
+            pa.plan(b.kv_indptr, b.last_page_len, qo_indptr=b.qo_indptr)
+            run(region.numel())
+            torch.cuda.synchronize()
+        assert pa.check_device_error() == 0
+        got.append((o, l))
+    check(*got[0], reference(b, c8), 2.0 ** -11, b)
+    for o, l in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
+
+
+def test_decode_gathers_by_the_rule(bsp):
+    """Pages of one token and work enough: run() gathers; a page id outside the pool reads as zeros all the same."""
+    b = workloads.paged_batch(248, [1] * 3, [9000, 4100, 300], 8, 2, 128, 1, "bf16", extra_pages=3)
+    c8 = cache8(b, 248)
+    b.kv_indices[5] = b.kv_indices[9001] = -1
+    pa = bsp.PagedAttention("decode", 8, 2, 128, 1, False, torch.bfloat16, max_batch=3, max_qo_tokens=3, num_ctas=4)
+    pa.plan(b.kv_indptr, b.last_page_len, qo_indptr=b.qo_indptr)
+    assert pa.lib.bsp_decode_fp8_region_size(ctypes.byref(pa.info)) == 13408 * 2 * 2
+    k8, ke, v8, ve = (torch.from_numpy(a).cuda() for a in c8)
+    f8 = torch.float8_e4m3fn
+    idx = torch.from_numpy(np.ascontiguousarray(b.kv_indices, np.int32)).cuda()
+    o, l = pa.run(b.q.cuda(), k8.view(f8), v8.view(f8), idx, k_exp=ke, v_exp=ve)
+    torch.cuda.synchronize()
+    assert pa.check_device_error() == 0x302
+    zero = [np.concatenate([c, np.zeros_like(c[:1])]) for c in c8]
+    b.kv_indices[[5, 9001]] = len(c8[0])
+    check(o, l, reference(b, zero), 2.0 ** -11, b)
+
+
 PREFILL = [
     # (seed, qo lens, kv lens, H_qo, H_kv, page, num_ctas, window, cap)
     (221, [100, 37, 1, 300], [100, 300, 5, 300], 32, 8, 16, None, -1, 0.0),

@@ -146,8 +146,7 @@ def run_args(info, **kw):
     d = dict(q=A, k=A, v=A, ke=A, ve=A, idx=A, pages=4, scale=0.1, o=A, lse=None, ws=A)
     d.update(kw)
     a = [ctypes.byref(info)] + list(d.values()) + [None]
-    if info.problem.mode == 1:  # no region
-        a[-2:-2] = [None, 0]
+    a[-2:-2] = [None, 0]  # no region
     return a
 
 
@@ -202,6 +201,31 @@ def test_region_size_and_refusals(native):
         a[-4:-2] = [region, nbytes]
         assert lib.bsp_prefill_run_fp8_block(*a) == rc
     assert lib.bsp_prefill_fp8_region_size(ctypes.byref(block_plan(0))) == 0
+
+
+def test_decode_region_size_and_refusals(native):
+    """A region is wanted for pages of one or two tokens and work enough, and must hold the page table."""
+    import torch
+    import block_sparse_paged_gb300 as bsp
+    lib = native.load()
+    assert lib.bsp_decode_fp8_region_size(ctypes.byref(block_plan(0))) == 0
+    assert lib.bsp_decode_fp8_region_size(ctypes.byref(block_plan(1))) == 0
+
+    def plan(ps, tokens):
+        prob = bsp.make_problem(0, 8, 2, 128, ps, False, torch.bfloat16)
+        info = bsp.plan_host(prob, bsp.Capacity(1, 2, 1, 1, 0, 0), [0, -(-tokens // ps)], [(tokens - 1) % ps + 1], [0, 1])[0]
+        info.valid = 1
+        return info
+    assert lib.bsp_decode_fp8_region_size(ctypes.byref(plan(3, 9000))) == 0
+    assert lib.bsp_decode_fp8_region_size(ctypes.byref(plan(2, 5000))) == 0
+    assert lib.bsp_decode_fp8_region_size(ctypes.byref(plan(2, 9000))) == 4512 * 2 * 2
+    assert lib.bsp_decode_fp8_region_size(ctypes.byref(plan(1, 2000))) == 0      # 2000 x 2 heads on 2 CTAs
+    big = plan(1, 2570)
+    assert lib.bsp_decode_fp8_region_size(ctypes.byref(big)) == 2576 * 2 * 2     # whole 16s x K, V x heads
+    for region, nbytes, rc in ((A, 2576 * 4 - 1, native.BSP_ERR_CAPACITY), (A + 8, 1 << 30, native.BSP_ERR_INVALID_ARG)):
+        a = run_args(big)
+        a[-4:-2] = [region, nbytes]
+        assert lib.bsp_decode_run_fp8_block(*a) == rc
 
 
 def test_region_of_pages_past_the_conversion_kernel(native):
