@@ -23,8 +23,10 @@ namespace {
 // then expands its share of the entries and tokens: one launch, no pass over
 // global memory between the sums and their use, no atomics. The lengths are at
 // most 128 KB, read from L2. Bound by the latency of that chain (lengths, sums, search,
-// entry): 5.7 us for 4 requests, 10.5 us for 0.8 M entries and as many slots (20 MB);
-// 2 to 8 CTAs per SM and 128 to 512 threads measured equal or slower.
+// entry): 4.9 us for 4 requests, 10.3-10.9 us for 0.8 M entries and as many slots (20 MB).
+// A thread's entries are addressed first, loaded together and then stored: 0.5-0.8 us less
+// than one after the other. 2 to 8 CTAs per SM, 128 to 512 threads and eight entries per
+// thread measured equal or slower.
 constexpr int kTabThreads = 256;
 constexpr int kTabUnit = 4;  // consecutive entries (tokens) per thread: one search, vector stores
 constexpr int kTabMaxBatch = 16384;
@@ -58,6 +60,13 @@ __device__ __forceinline__ TableRow table_row(const TableParams &p, int b) {
     r.all_pages = (int)min(all, (uint32_t)p.width);
     r.old_pages = min((int)(r.cached ? ((uint32_t)r.cached - 1) / ps + 1 : 0), r.all_pages);
     return r;
+}
+
+// The pages alone, out of line (used where sums are saturated).
+__device__ __noinline__ int table_row_pages(const TableParams &p, int b, int &old_pages) {
+    const TableRow r = table_row(p, b);
+    old_pages = r.old_pages;
+    return r.all_pages;
 }
 
 // Largest b with start[b] <= x, for x in [0, start[n]).
@@ -149,11 +158,19 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
         }
     }
 
-    // page of column i of request b: from the row, or from the free list (-1: none left)
-    auto page_of = [&](int b, int old_pages, int i) -> int {
-        if (i < old_pages) return p.table[(long long)b * p.table_stride + i];
+    // pages of request b, and how many of them its row held, from the sums (unless they
+    // are saturated)
+    auto pages_of = [&](int b, int &old_pages) -> int {
+        if (n_pages == INT32_MAX) return table_row_pages(p, b, old_pages);
+        const int all = s_pages[b + 1] - s_pages[b];
+        old_pages = all - (s_take[b + 1] - s_take[b]);
+        return all;
+    };
+    // where column i of request b stands: in the row, or in the free list (null: none left)
+    auto place = [&](int b, int old_pages, int i) -> const int32_t * {
+        if (i < old_pages) return p.table + (long long)b * p.table_stride + i;
         const uint32_t k = (uint32_t)s_take[b] + (uint32_t)(i - old_pages);  // (s_take saturates at 2^31 - 1)
-        return k < (uint32_t)n_free ? __ldg(p.free_pages + k) : -1;
+        return k < (uint32_t)n_free ? p.free_pages + k : nullptr;
     };
 
     // One index space: groups of kTabUnit table entries, then groups of tokens, so that
@@ -165,25 +182,35 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
             // table entries: CSR copy of every row, new entries also into the row; the CSR
             // tail up to its capacity is 0
             const long long e0 = gi * kTabUnit;
+            // (addresses of all entries first, then their loads together, then the stores)
+            const int32_t *from[kTabUnit];
+            int32_t *to[kTabUnit];  // where a new entry goes
             int id[kTabUnit];
-            int b = 0, old_pages = 0, end = -1, begin = 0;
+            int b = e0 < n_pages ? find_row(s_pages, B, (int)e0) - 1 : 0, old_pages = 0, end = -1, begin = 0;
 #pragma unroll
             for (int u = 0; u < kTabUnit; ++u) {
                 const long long e = e0 + u;
-                id[u] = 0;
+                from[u] = nullptr;
+                to[u] = nullptr;
                 if (e < n_pages) {
                     if ((int)e >= end) {
-                        b = end < 0 ? find_row(s_pages, B, (int)e) : b + 1;
-                        while (s_pages[b + 1] <= (int)e) ++b;  // rows without pages
+                        do ++b;
+                        while (s_pages[b + 1] <= (int)e);  // (passes rows without pages)
                         begin = s_pages[b];
                         end = s_pages[b + 1];
-                        old_pages = table_row(p, b).old_pages;
+                        pages_of(b, old_pages);
                     }
                     const int i = (int)e - begin;
-                    const int pg = page_of(b, old_pages, i);
-                    if (i >= old_pages) p.table[(long long)b * p.table_stride + i] = pg;
-                    id[u] = max(pg, 0);
+                    from[u] = place(b, old_pages, i);
+                    if (i >= old_pages) to[u] = p.table + (long long)b * p.table_stride + i;
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < kTabUnit; ++u) id[u] = from[u] ? *from[u] : -1;
+#pragma unroll
+            for (int u = 0; u < kTabUnit; ++u) {
+                if (to[u]) *to[u] = id[u];
+                id[u] = max(id[u], 0);
             }
             if (e0 + kTabUnit <= p.cap_pages) {
                 *reinterpret_cast<int4 *>(p.kv_indices + e0) = make_int4(id[0], id[1], id[2], id[3]);
@@ -196,37 +223,42 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
         }
         // tokens: slot and position of every new token; the tail is -1 and 0
         const long long t0 = (gi - g_ent) * kTabUnit;
+        const int32_t *from[kTabUnit];
+        int offs[kTabUnit], pos[kTabUnit];
         long long slot[kTabUnit];
-        int pos[kTabUnit];
-        int b = 0, end = -1, begin = 0;
+        int b = t0 < n_tok ? find_row(s_tok, B, (int)t0) - 1 : 0, end = -1, begin = 0;
         uint32_t col = 0;  // (past 2^31 with pages of one token)
-        int off = 0;
-        TableRow r{};
+        int off = 0, cached = 0, all_pages = 0, old_pages = 0;
 #pragma unroll
         for (int u = 0; u < kTabUnit; ++u) {
             const long long t = t0 + u;
-            slot[u] = -1;
+            from[u] = nullptr;
+            offs[u] = 0;
             pos[u] = 0;
             if (t < n_tok) {
                 if ((int)t >= end) {
-                    b = end < 0 ? find_row(s_tok, B, (int)t) : b + 1;
-                    while (s_tok[b + 1] <= (int)t) ++b;  // requests without new tokens
+                    do ++b;
+                    while (s_tok[b + 1] <= (int)t);  // (passes requests without new tokens)
                     begin = s_tok[b];
                     end = s_tok[b + 1];
-                    r = table_row(p, b);
-                    const uint32_t x = (uint32_t)r.cached + (uint32_t)((int)t - begin);
+                    all_pages = pages_of(b, old_pages);
+                    cached = max(__ldg(p.cached + b), 0);
+                    const uint32_t x = (uint32_t)cached + (uint32_t)((int)t - begin);
                     col = x / (uint32_t)p.ps;
                     off = (int)(x - col * (uint32_t)p.ps);
                 } else if (++off == p.ps) {
                     off = 0;
                     ++col;
                 }
-                pos[u] = (int)min((long long)r.cached + ((int)t - begin), (long long)INT32_MAX);
-                if (col < (uint32_t)r.all_pages) {
-                    const int pg = page_of(b, r.old_pages, (int)col);
-                    if (pg >= 0) slot[u] = (long long)pg * p.ps + off;
-                }
+                pos[u] = (int)min((long long)cached + ((int)t - begin), (long long)INT32_MAX);
+                offs[u] = off;
+                if (col < (uint32_t)all_pages) from[u] = place(b, old_pages, (int)col);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < kTabUnit; ++u) {
+            const int pg = from[u] ? *from[u] : -1;
+            slot[u] = pg >= 0 ? (long long)pg * p.ps + offs[u] : -1;
         }
         if (t0 + kTabUnit <= p.cap_tokens) {
             *reinterpret_cast<int4 *>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
