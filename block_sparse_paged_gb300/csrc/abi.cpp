@@ -117,12 +117,14 @@ extern "C" int bsp_prefill_run(const bsp_plan_info *plan, const void *q, const v
 namespace {
 
 // Prefill over the 8-bit cache converts the plan's pages into a bf16 copy first where a
-// cached token is read by 1.5 query tiles or more on average and a CTA has four 128-key
-// tiles or more to work on. Measured (copy first / converted inside the kernel): 2 tiles
-// per token, 16 x 8192 tokens 358 / 461 us, 24 tiles, 16 x 1536 343 / 563 us; one tile
-// per token, 16 x 8192 267 / 254 us, 1 x 32768 75 / 64 us; under a wave of work, 2 x 150
-// tokens 19.5 / 16.4 us (a launch less).
-constexpr int64_t kRegionReads2 = 3;       // twice the query tiles per cached token
+// cached token is read by 3 query tiles or more on average (pages of a power of two, 8 or
+// more tokens: the kernel that converts inside takes the codes by TMA) or 1.5 (by cp.async),
+// and a CTA has four 128-key tiles or more to work on. Measured (copy first / converted
+// inside the kernel), 16-token pages: 16 x 8192 tokens, one tile per token 263 / 194 us, 2
+// tiles 356 / 325, 3 tiles 475 / 475, 4 tiles 596 / 627; 24 tiles, 16 x 1536 343 / 411;
+// 12-token pages: one tile 276 / 260, page size 1 310 / 326, 8 tiles 552 / 1060; under a
+// wave of work, 2 x 150 tokens 19.5 / 16.4 us (a launch less).
+constexpr int64_t kRegionReads2Tma = 6, kRegionReads2 = 3;  // twice the query tiles per cached token
 constexpr int64_t kRegionTokens = 4 * 128;  // KV tokens of work per CTA
 constexpr int64_t kRegionPageRows = 1 << 27;  // rows of a page, all heads: the copy counts a page's vectors in 32 bits
 
@@ -193,7 +195,9 @@ extern "C" size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan) {
     if (!plan || plan->problem.mode != BSP_MODE_PREFILL || plan->num_table_pages <= 0) return 0;
     const int64_t tokens = (int64_t)plan->num_table_pages * plan->problem.page_size;
     if (tokens > INT32_MAX || (int64_t)plan->problem.page_size * plan->problem.num_kv_heads > kRegionPageRows) return 0;
-    if (2 * plan->total_work < kRegionReads2 * tokens * plan->problem.num_kv_heads ||
+    const int32_t ps = plan->problem.page_size;
+    const int64_t reads2 = ps >= 8 && (ps & (ps - 1)) == 0 ? kRegionReads2Tma : kRegionReads2;
+    if (2 * plan->total_work < reads2 * tokens * plan->problem.num_kv_heads ||
         plan->total_work < kRegionTokens * plan->capacity.num_ctas)
         return 0;
     return (size_t)tokens * plan->problem.num_kv_heads * 512;

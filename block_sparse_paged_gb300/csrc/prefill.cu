@@ -84,11 +84,14 @@ constexpr int kOffBar = kOffStg + 8 * kStgWarp;
 enum Bar {
     kQFull = 0, kQEmpty,
     kKFull0, kKEmpty0 = kKFull0 + kKStages, kVFull0 = kKEmpty0 + kKStages, kVEmpty0 = kVFull0 + kVStages,
-    kSFull0 = kVEmpty0 + kVStages, kSFull1, kPFull0, kPFull1, kODone0, kODone1, kOFree0, kOFree1, kNumBars
+    kSFull0 = kVEmpty0 + kVStages, kSFull1, kPFull0, kPFull1, kODone0, kODone1, kOFree0, kOFree1,
+    kRawFull0, kRawFull1, kRawEmpty0, kRawEmpty1,  // e4m3 codes by TMA in the staging: K, V
+    kNumBars
 };
 constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmemSlot + 8;
-constexpr int kSmemUsed = kOffAbort + 8;
+constexpr int kOffScale = kOffAbort + 8;          // e4m3 by TMA: 2^exponent of the staged keys, K then V
+constexpr int kSmemUsed = kOffScale + 2 * kKvTile * 4;
 constexpr int kSmemBytes = kSmemUsed + 1024;  // slack to align the base to 1024 bytes
 static_assert(kSmemBytes <= 227 * 1024, "prefill tiles exceed shared memory");
 
@@ -117,6 +120,7 @@ struct PrefillParams {
     const float *sink;       // per-qo-head sink logits, or null (applied to finished rows)
     const int8_t *k_exp, *v_exp;  // e4m3 cache: exponents [num_pages][H_kv]
     int num_pages;                // e4m3 cache: page ids outside [0, num_pages) read as zero codes
+    int raw_box;                  // e4m3 cache by TMA: rows of a box of codes
 };
 
 struct Ctx {
@@ -198,10 +202,10 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, float s) {
 // the same 128-byte-swizzled layout (pages of any size, e.g. 1).
 // kVar: the sliding window and logits soft-cap variants are compiled in (the
 // default instantiation has neither, at no cost).
-// kFp8 (with kTma false): K and V are e4m3 codes with an exponent per (page, kv
-// head), converted to bf16 on their way into the tiles by the softmax warps, in the
-// time in which they would wait for their next S; everything behind the rings is the
-// bf16 kernel.
+// kFp8: K and V are e4m3 codes with an exponent per (page, kv head), converted to bf16
+// on their way into the tiles by the softmax warps, in the time in which they would
+// wait for their next S; everything behind the rings is the bf16 kernel. The codes
+// come by TMA boxes (kTma) or cp.async, by the same rule.
 template <bool kTma, bool kVar, bool kFp8 = false>
 __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -226,8 +230,8 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
         for (int i = 0; i < kNumBars; ++i) {
             const bool softmax_arrivals = i == kPFull0 || i == kPFull1 || i == kOFree0 || i == kOFree1;
             const bool kv_full = (i >= kKFull0 && i < kKFull0 + kKStages) || (i >= kVFull0 && i < kVFull0 + kVStages);
-            // cp.async: one per lane; e4m3: one per converting warp
-            mbar_init(bar(i), softmax_arrivals ? 128 : (kv_full && !kTma) ? (kFp8 ? 4 : 32) : 1);
+            const bool converters = kFp8 && (kv_full || i == kRawEmpty0 || i == kRawEmpty1);  // one per warp
+            mbar_init(bar(i), softmax_arrivals ? 128 : converters ? 4 : kv_full && !kTma ? 32 : 1);  // cp.async: per lane
         }
         *ctx.abort_flag = 0;
         fence_barrier_init();
@@ -256,11 +260,71 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
         // ------------------------------------------------------------ TMA
         int q_cnt = 0, j = 0;  // j: KV tiles issued so far
         bool ok = true;
+        // e4m3 cache: codes by boxes of raw_box rows into the staging, K's into its first half, V's
+        // into the second, and the scales of the keys. Lane l looks after keys l + 32 i (scale) and
+        // box l (copy). A key past the chunk's end or outside the pool has scale 0; a box that
+        // begins with one is not copied.
+        constexpr int kI = kKvTile / 32;
+        const int ps_s = 31 - __clz(p.page_size), br_s = 31 - __clz(p.raw_box);  // (powers of two)
+        int x_pg[kI], x_e[2][kI], x_row = 0;  // page, exponents of this lane's keys (-1: no key); first row of its box
+        bool x_box = false;
+        auto look_up = [&](const bsp_work_item &w, int t) {
+            const int tok0 = w.kv_start + t * kKvTile;
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+                const int tok = tok0 + lane + 32 * i;
+                x_pg[i] = tok < w.kv_end ? ld_nc_s32(p.kv_indices + w.page_base + (tok >> ps_s)) : -1;
+            }
+            const int tb = tok0 + (lane << br_s);
+            const int pb = (lane << br_s) < kKvTile && tb < w.kv_end ? ld_nc_s32(p.kv_indices + w.page_base + (tb >> ps_s)) : -1;
+            x_box = (unsigned)pb < (unsigned)p.num_pages;
+            x_row = (pb << ps_s) + (tb & (p.page_size - 1));
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+                const bool in = (unsigned)x_pg[i] < (unsigned)p.num_pages;
+                bad |= !in && tok0 + lane + 32 * i < w.kv_end;
+                const size_t at = (size_t)x_pg[i] * p.H_kv + w.kv_head;
+                x_e[0][i] = in ? ld_nc_s8(p.k_exp + at) : INT_MIN;
+                x_e[1][i] = in ? ld_nc_s8(p.v_exp + at) : INT_MIN;
+            }
+            if (bad) atomicCAS(ctx.status, 0, kStatusPageIndex);
+        };
+        auto fetch_raw = [&](const bsp_work_item &w, int) -> bool {
+            float *scale = reinterpret_cast<float *>(smem + kOffScale);
+            const int boxes = __popc(__ballot_sync(0xffffffffu, x_box));
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                if (!wait_bar_warp(ctx, bar(kRawEmpty0 + v), (j & 1) ^ 1)) return false;
+#pragma unroll
+                for (int i = 0; i < kI; ++i) {
+                    const int e = x_e[v][i];
+                    scale[v * kKvTile + lane + 32 * i] =
+                        e == INT_MIN ? 0.f : __int_as_float(e >= -126 ? (e + 127) << 23 : 0x00400000 >> (-127 - e));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(bar(kRawFull0 + v), (uint32_t)boxes << (br_s + 7));
+                __syncwarp();
+                if (x_box)
+                    tma_load_3d(sb + kOffStg + v * 4 * kStgWarp + (lane << (br_s + 7)), v == 0 ? &tk : &tv, bar(kRawFull0 + v), 0,
+                                w.kv_head, x_row);
+            }
+            ++j;
+            return true;
+        };
+        (void)look_up;
+        (void)fetch_raw;
         for (int it = it0; it < it1 && ok; ++it) {
             const bsp_work_item w = items[it];
             const int len = w.kv_end - w.kv_start;
             const int nt = (len + kKvTile - 1) / kKvTile;
             if (nt == 0) continue;
+            if constexpr (kFp8 && kTma) {
+                // codes of the first tile before Q, which waits for the item before
+                look_up(w, 0);
+                if (!(ok = fetch_raw(w, 0))) break;
+                if (nt > 1) look_up(w, 1);
+            }
             if (!(ok = wait_bar_warp(ctx, bar(kQEmpty), (q_cnt & 1) ^ 1))) break;
             ++q_cnt;
             if (lane == 0) {
@@ -281,6 +345,12 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 }
             };
             (void)lookup;
+            if constexpr (kFp8 && kTma) {
+                for (int t = 1; t < nt; ++t) {
+                    if (!(ok = fetch_raw(w, t))) break;
+                    if (t + 1 < nt) look_up(w, t + 1);
+                }
+            }
             if constexpr (kFp8) continue;  // K and V: the softmax warps
             for (int t = 0; t < nt; ++t, ++j) {
                 const int tok0 = w.kv_start + t * kKvTile;
@@ -508,17 +578,21 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
         const uint32_t tS = tmem + tl + sub * 128, tO = tmem + tl + 256 + sub * 128;
         float *plse = reinterpret_cast<float *>(const_cast<uint8_t *>(p.ws) + p.off_plse);
         float *po = reinterpret_cast<float *>(const_cast<uint8_t *>(p.ws) + p.off_po);
+        const uint32_t stg = sb + kOffStg + (sub * 4 + q4) * kStgWarp;  // this warp's staging
         int s_cnt = 0, o_cnt = 0, j = 0;
         bool ok = true;
         // e4m3 cache: the group of subtile 0 converts K tiles, that of subtile 1 V tiles, 32
         // keys per warp, two tiles ahead of the one that it works on (the rings' depth), over
-        // the CTA's items as one sequence. The codes come by cp.async into the warp's staging
-        // buffer, one tile ahead of their conversion (read straight into registers they cost
-        // 3,000-4,600 cycles of waiting per tile); page ids one tile before that. A warp-wide
-        // copy takes the codes of four keys (8 lanes x 16 codes), each lane reads back what it
-        // copied, and its 16 values become two 16-byte chunks of the key's swizzled row. Keys
-        // past the chunk's end are written as zeros (P = 0 there must meet finite values of V).
-        // The epilogue uses the staging buffer too: the copies of an item's last tile wait for it.
+        // the CTA's items as one sequence. The codes come into the warp's staging buffer one
+        // tile ahead of their conversion: by TMA from warp 0, or (kTma false) by this warp's own
+        // cp.async, page ids one tile before that. (Read straight into registers they cost
+        // 3,000-4,600 cycles of waiting per tile; look-up and copies by the converting warps
+        // 1,900 by TMA and 2,000-2,400 by cp.async. 16 x 8192 tokens, 64 queries each: 194 us
+        // with warp 0 copying, 255 without.) Eight lanes hold the codes of a key, 16 each
+        // (with cp.async each lane reads back what it copied), and a lane's 16 values become two
+        // 16-byte chunks of the key's swizzled row. Keys past the chunk's end are written as
+        // zeros (P = 0 there must meet finite values of V). The epilogue uses the staging buffer
+        // too: the copies of an item's last tile wait for it.
         constexpr uint32_t kNoRow = ~0u;
         int c_it = it0 - 1, c_t = 0, c_nt = 0, c_start = 0, c_end = 0, c_base = 0, c_head = 0, c_n = 0;
         int c_pg = 0, c_off = -1;  // page id and place of this lane's key (-1: none)
@@ -542,7 +616,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
         };
         bool raw_live = false;  // the staging buffer holds (or awaits) a tile's codes
         int raw_e = 0;          // the exponent of this lane's key of that tile
-        const uint32_t raw = sb + kOffStg + (warp - 2) * kStgWarp + (lane >> 3) * 128 + (lane & 7) * 16;
+        const uint32_t raw = stg + (lane >> 3) * 128 + (lane & 7) * 16;
         auto fetch_raw = [&]() {  // the looked-up tile's codes on their way, then the next look-up
             raw_live = c_it < it1;
             if (!raw_live) return;
@@ -568,24 +642,48 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
             ++c_t;
             look_up();
         };
+        int c_total = 0;           // TMA: tiles of the CTA's items
+        auto release_raw = [&]() {  // the warp's share of the staging may be written again
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kRawEmpty0 + sub));
+        };
         auto convert = [&](bool more) -> bool {
-            if (!raw_live) return true;
-            const int st = c_n % kKStages, rd = c_n / kKStages;
+            if (kTma ? c_n >= c_total : !raw_live) return true;
+            const int st = c_n % kKStages, rd = c_n / kKStages, rp = c_n & 1;
             ++c_n;
-            dev::cp_async_wait<0>();
-            if (!wait_bar_warp(ctx, bar((sub == 0 ? kKEmpty0 : kVEmpty0) + st), (rd & 1) ^ 1)) return false;
-            const float scale = __int_as_float(raw_e >= -126 ? (raw_e + 127) << 23 : 0x00400000 >> (-127 - raw_e));
             const int c = lane & 7;
             const bool hi = c >= 4;  // these lanes store their second chunk first: no bank is met twice
             const int cc = (2 * c + (hi ? 1 : 0)) & 7, k7 = lane >> 3;
+            uint4 d[8];
+            float s[8];
+            if constexpr (kTma) {
+                if (!wait_bar_warp(ctx, bar(kRawFull0 + sub), rp)) return false;
+                const float *scale = reinterpret_cast<const float *>(smem + kOffScale) + sub * kKvTile + q4 * 32 + k7;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s[i] = scale[4 * i];
+                    d[i] = ld_shared_v4(stg + (4 * i + k7) * 128 + ((c ^ (4 * (i & 1) + k7)) << 4));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (s[i] == 0.f) d[i] = make_uint4(0, 0, 0, 0);
+                if (more) release_raw();
+            } else {
+                dev::cp_async_wait<0>();
+                const float scale = __int_as_float(raw_e >= -126 ? (raw_e + 127) << 23 : 0x00400000 >> (-127 - raw_e));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s[i] = __shfl_sync(0xffffffffu, scale, 4 * i + (lane >> 3));
+                    d[i] = ld_shared_v4(raw + i * 512);
+                }
+            }
+            if (!wait_bar_warp(ctx, bar((sub == 0 ? kKEmpty0 : kVEmpty0) + st), (rd & 1) ^ 1)) return false;
             // key 32 q4 + 4 i + k7: chunks swizzled by key & 7 = 4 (i & 1) + k7
             const uint32_t dst = sb + (sub == 0 ? kOffK : kOffV) + st * kTile + (c >> 2) * kHalf + (q4 * 32 + k7) * 128;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float s = __shfl_sync(0xffffffffu, scale, 4 * i + (lane >> 3));
-                const uint4 d = ld_shared_v4(raw + i * 512);
-                const uint2 a0 = e4m3x4_to_bf16x4(hi ? d.z : d.x, s), a1 = e4m3x4_to_bf16x4(hi ? d.w : d.y, s);
-                const uint2 b0 = e4m3x4_to_bf16x4(hi ? d.x : d.z, s), b1 = e4m3x4_to_bf16x4(hi ? d.y : d.w, s);
+                const uint2 a0 = e4m3x4_to_bf16x4(hi ? d[i].z : d[i].x, s[i]), a1 = e4m3x4_to_bf16x4(hi ? d[i].w : d[i].y, s[i]);
+                const uint2 b0 = e4m3x4_to_bf16x4(hi ? d[i].x : d[i].z, s[i]), b1 = e4m3x4_to_bf16x4(hi ? d[i].y : d[i].w, s[i]);
                 const int sw = cc ^ (4 * (i & 1) + k7);
                 st_shared_v4(dst + i * 512 + (sw << 4), a0.x, a0.y, a1.x, a1.y);
                 st_shared_v4(dst + i * 512 + ((sw ^ 1) << 4), b0.x, b0.y, b1.x, b1.y);
@@ -593,14 +691,19 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar((sub == 0 ? kKFull0 : kVFull0) + st));
-            raw_live = false;
-            if (more) fetch_raw();
+            raw_live = kTma && !more;  // TMA: released after the epilogue
+            if (!kTma && more) fetch_raw();
             return true;
         };
         if constexpr (kFp8) {
             static_assert(kKStages == 2 && kVStages == 2, "two tiles ahead");
-            look_up();
-            fetch_raw();
+            if constexpr (kTma) {
+                for (int i = it0 + lane; i < it1; i += 32) c_total += (items[i].kv_end - items[i].kv_start + kKvTile - 1) / kKvTile;
+                c_total = __reduce_add_sync(0xffffffffu, c_total);
+            } else {
+                look_up();
+                fetch_raw();
+            }
             ok = convert(true) && convert(true);
         }
         for (int it = it0; it < it1 && ok; ++it) {
@@ -758,7 +861,6 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 // bf16 output through this warp's swizzled staging, 64 columns at a
                 // time: each thread writes its row, then every store instruction
                 // covers four whole 128-byte lines (lane l: row 4i + l/8, chunk l%8)
-                const uint32_t stg = sb + kOffStg + (warp - 2) * kStgWarp;
                 const int cc = lane & 7;
                 const int rt_base = sub * kRows + q4 * 32;
                 unsigned long long orr[8];
@@ -799,10 +901,16 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 }
             }
             if constexpr (kFp8) {
-                if (nt > 0) fetch_raw();  // the staging is free again
+                // the staging is free again (what was written to it comes before TMA's next writes)
+                if (kTma && raw_live) {
+                    fence_proxy_async_smem();
+                    release_raw();
+                    raw_live = false;
+                }
+                if (!kTma && nt > 0) fetch_raw();
             }
         }
-        if constexpr (kFp8) dev::cp_async_wait<0>();  // nothing in flight at exit
+        if constexpr (kFp8 && !kTma) dev::cp_async_wait<0>();  // nothing in flight at exit
     }
 
     __syncwarp();
@@ -973,6 +1081,7 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
     const bool direct = !fp8 && !copied && ps >= 8 && (ps & (ps - 1)) == 0 && num_pages * (int64_t)ps <= INT32_MAX;
     const bool gather = !fp8 && !copied && !direct && plan->off_gather != 0 && plan->num_table_pages <= plan->capacity.max_gather_pages;
     const bool tma = direct || gather || copied;
+    const bool tma8 = fp8 && ps >= 8 && (ps & (ps - 1)) == 0 && num_pages * (int64_t)ps <= INT32_MAX;
 
     CUtensorMap tq, tk, tv;
     std::memset(&tk, 0, sizeof(tk));
@@ -1008,6 +1117,10 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
             cudaError_t e = cudaGetLastError();
             if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("convert launch: ") + cudaGetErrorString(e));
         }
+    } else if (tma8) {
+        const uint64_t rows = (uint64_t)num_pages * ps;
+        if (rc == BSP_OK) rc = make_tmap(&tk, k_pages, 1, kD, P.num_kv_heads, rows, 1, ps < kKvTile ? ps : kKvTile);
+        if (rc == BSP_OK) rc = make_tmap(&tv, v_pages, 1, kD, P.num_kv_heads, rows, 1, ps < kKvTile ? ps : kKvTile);
     } else if (tma) {
         if (rc == BSP_OK) rc = make_tmap_bf16(&tk, k_pages, kD, P.num_kv_heads, (uint64_t)num_pages * ps, 1, box_rows);
         if (rc == BSP_OK) rc = make_tmap_bf16(&tv, v_pages, kD, P.num_kv_heads, (uint64_t)num_pages * ps, 1, box_rows);
@@ -1035,6 +1148,7 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
     p.k_exp = k_exp;
     p.v_exp = v_exp;
     p.num_pages = (int)num_pages;
+    p.raw_box = ps < kKvTile ? ps : kKvTile;
     if (p.soft_cap_on) p.scale_log2 = P.logits_soft_cap * dev::kLog2e;
     p.H_qo = P.num_qo_heads;
     p.g = g;
@@ -1044,14 +1158,15 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
     p.causal = P.causal;
     p.tile_rows = plan->tile_rows;
 
-    static bool configured[6][64] = {{false}};
+    static bool configured[8][64] = {{false}};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(BSP_ERR_CUDA, "no current CUDA device");
     const bool var = P.window_left > 0 || P.logits_soft_cap > 0.f;
-    auto kern = fp8 ? (var ? prefill_kernel<false, true, true> : prefill_kernel<false, false, true>)
+    auto kern = tma8 ? (var ? prefill_kernel<true, true, true> : prefill_kernel<true, false, true>)
+                : fp8 ? (var ? prefill_kernel<false, true, true> : prefill_kernel<false, false, true>)
                 : tma ? (var ? prefill_kernel<true, true> : prefill_kernel<true, false>)
                     : (var ? prefill_kernel<false, true> : prefill_kernel<false, false>);
-    const int which = (fp8 ? 4 : tma ? 2 : 0) + (var ? 1 : 0);
+    const int which = (tma8 ? 6 : fp8 ? 4 : tma ? 2 : 0) + (var ? 1 : 0);
     if (!configured[which][dev]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("prefill smem attribute: ") + cudaGetErrorString(e));

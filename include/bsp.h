@@ -501,8 +501,9 @@ size_t bsp_decode_fp8_region_size(const bsp_plan_info *plan);
 
 /* Bytes of the region that bsp_prefill_run_fp8_block wants for this plan (a bf16
  * copy of its page table's K and V), or 0 where converting inside the attention
- * kernel is faster: under 1.5 query tiles per cached token on average, or under
- * four 128-key tiles of work per CTA. */
+ * kernel is faster: under 3 query tiles per cached token on average (1.5 with pages
+ * that are no power of two of 8 or more tokens), or under four 128-key tiles of work
+ * per CTA. */
 size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan);
 
 /*

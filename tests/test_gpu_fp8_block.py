@@ -196,6 +196,11 @@ PREFILL = [
     (225, [513], [4000], 8, 1, 128, 21, -1, 0.0),                           # chunk behind a long cache
     (226, [6, 2], [3, 2], 16, 2, 8, 4, -1, 0.0),                            # rows that see no key
     (227, [1, 1], [700, 1], 4, 1, 5, None, -1, 0.0),
+    # many short items per CTA: none, one, two or four tiles each, ends on and off a tile
+    (228, [1 + 7 * i % 50 for i in range(40)], [(37 * i) % 400 if i % 5 else 128 * (i % 4) for i in range(40)], 16, 2, 8, 3,
+     -1, 0.0),
+    (229, [1 + 11 * i % 90 for i in range(24)], [(53 * i) % 700 for i in range(24)], 8, 2, 32, 2, 100, 0.0),
+    (230, [1 + 7 * i % 50 for i in range(24)], [(37 * i) % 400 for i in range(24)], 16, 2, 6, 3, -1, 0.0),
 ]
 
 
