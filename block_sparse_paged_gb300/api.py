@@ -129,7 +129,9 @@ class PagedAttention:
         self.staging = torch.zeros(st_bytes, dtype=torch.uint8, pin_memory=True)
         self._copied = None  # event after the last plan copy
         self._q_tail, self._page_tail = (num_qo_heads, head_dim), (page_size, num_kv_heads, head_dim)
-        self.info = None
+        self._default_scale = 1.0 / math.sqrt(head_dim)
+        self.info = self._fp8_plan = self._fp8_shapes = None  # of the current plan
+        self._sink_on = False  # its info points to a sink
 
     # ---- plan ---------------------------------------------------------------
     # Default per-position cost alpha of the LPT plan (cost of a work item =
@@ -161,6 +163,8 @@ class PagedAttention:
             ev.record(stream if stream is not None else torch.cuda.current_stream())
             self._copied = ev
         self.info = info
+        self._fp8_plan = self._fp8_shapes = None
+        self._sink_on = False
         return info
 
     def plan_arrays(self):
@@ -227,8 +231,9 @@ class PagedAttention:
 
     def _run_fp8_block(self, q, k_pages, v_pages, k_exp, v_exp, kv_indices, sm_scale, out, lse, stream, return_lse,
                        k_scale, v_scale, sink):
-        """run() over an e4m3 cache with one exponent per page and kv head."""
-        info, dev, f8, i8 = self.info, self.device, torch.float8_e4m3fn, torch.int8
+        """run() over an e4m3 cache with one exponent per page and kv head. (A short step's time is this function's:
+        what depends on the plan and on shapes alone is looked at once per plan.)"""
+        dev, f8, i8 = self.device, torch.float8_e4m3fn, torch.int8
         if k_exp is None or v_exp is None:
             raise ValueError("k_exp and v_exp are given together")
         if k_scale != 1.0 or v_scale != 1.0:
@@ -236,14 +241,11 @@ class PagedAttention:
         if self.dtype is not torch.bfloat16:
             raise ValueError("pools with exponents are read by bfloat16 problems")
         q_shape, pool = q.shape, k_pages.shape
-        if q_shape[1:] != self._q_tail or q_shape[0] < info.num_qo_tokens:
-            raise ValueError(f"q must be [n_tokens, {self._q_tail[0]}, {self._q_tail[1]}] with the plan's tokens")
-        if pool[1:] != self._page_tail or v_pages.shape != pool:
-            raise ValueError("k_pages / v_pages must be [num_pages, %d, %d, %d]" % self._page_tail)
-        if k_exp.shape != (pool[0], pool[2]) or v_exp.shape != k_exp.shape:
-            raise ValueError(f"k_exp / v_exp must be [{pool[0]}, {pool[2]}]")
-        if kv_indices.dim() != 1 or kv_indices.shape[0] < info.num_table_pages:
-            raise ValueError(f"kv_indices must hold the plan's {info.num_table_pages} pages")
+        shapes = (q_shape, pool, v_pages.shape, k_exp.shape, v_exp.shape, kv_indices.shape)
+        if shapes != self._fp8_shapes:
+            self._check_fp8_shapes(*shapes)
+            self._fp8_shapes = shapes
+        ref, fn, region, nbytes, ws = self._fp8_plan or self._look_at_fp8_plan()
         q_p = _addr(q, "q", torch.bfloat16, dev)
         if out is None:
             out = torch.empty_like(q)
@@ -261,30 +263,48 @@ class PagedAttention:
             lse = torch.empty(q_shape[:2], dtype=torch.float32, device=dev)
             lse_p = lse.data_ptr()
         if sm_scale is None:
-            sm_scale = 1.0 / math.sqrt(self._q_tail[1])
-        self._set_sink(sink)
-        ref = ctypes.byref(info)
-        args = (ref, q_p, _addr(k_pages, "k_pages", f8, dev), _addr(v_pages, "v_pages", f8, dev),
-                _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev),
-                _addr(kv_indices, "kv_indices", torch.int32, dev) or None, pool[0], sm_scale, out_p, lse_p)
-        decode = self.mode == N.BSP_MODE_DECODE
-        nbytes = (self.lib.bsp_decode_fp8_region_size if decode else self.lib.bsp_prefill_fp8_region_size)(ref)
-        ws = self.workspace.data_ptr()
-        region = copy = None
-        if nbytes and not decode and self.capacity.max_gather_pages >= info.num_table_pages:
-            region, nbytes = ws + info.off_gather, 2 * info.gather_pool_bytes  # the workspace's copy region
-        elif nbytes:  # scratch of this run alone: the plan's exponents, or a bf16 copy of its pages
+            sm_scale = self._default_scale
+        if sink is not None or self._sink_on:
+            self._set_sink(sink)
+        copy = None
+        if nbytes and region is None:  # scratch of this run alone: the plan's exponents, or a bf16 copy of its pages
             if stream is None:
                 copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             else:
                 with torch.cuda.stream(stream):
                     copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             region = copy.data_ptr()
-        fn = self.lib.bsp_decode_run_fp8_block if decode else self.lib.bsp_prefill_run_fp8_block
-        _call(dev, stream, fn, *args, region, nbytes, ws)
+        _call(dev, stream, fn, ref, q_p, _addr(k_pages, "k_pages", f8, dev), _addr(v_pages, "v_pages", f8, dev),
+              _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev),
+              _addr(kv_indices, "kv_indices", torch.int32, dev) or None, pool[0], sm_scale, out_p, lse_p, region, nbytes, ws)
         return (out, lse) if return_lse else out
 
+    def _check_fp8_shapes(self, q, k_pages, v_pages, k_exp, v_exp, kv_indices):
+        info = self.info
+        if q[1:] != self._q_tail or q[0] < info.num_qo_tokens:
+            raise ValueError(f"q must be [n_tokens, {self._q_tail[0]}, {self._q_tail[1]}] with the plan's tokens")
+        if k_pages[1:] != self._page_tail or v_pages != k_pages:
+            raise ValueError("k_pages / v_pages must be [num_pages, %d, %d, %d]" % self._page_tail)
+        if k_exp != (k_pages[0], k_pages[2]) or v_exp != k_exp:
+            raise ValueError(f"k_exp / v_exp must be [{k_pages[0]}, {k_pages[2]}]")
+        if len(kv_indices) != 1 or kv_indices[0] < info.num_table_pages:
+            raise ValueError(f"kv_indices must hold the plan's {info.num_table_pages} pages")
+
+    def _look_at_fp8_plan(self):
+        """(plan info reference, entry, region in the workspace or None, region bytes, workspace) of the current plan."""
+        info, lib, ws, ref = self.info, self.lib, self.workspace.data_ptr(), ctypes.byref(self.info)
+        region = None
+        if self.mode == N.BSP_MODE_DECODE:
+            fn, nbytes = lib.bsp_decode_run_fp8_block, lib.bsp_decode_fp8_region_size(ref)
+        else:
+            fn, nbytes = lib.bsp_prefill_run_fp8_block, lib.bsp_prefill_fp8_region_size(ref)
+            if nbytes and self.capacity.max_gather_pages >= info.num_table_pages:
+                region, nbytes = ws + info.off_gather, 2 * info.gather_pool_bytes  # the workspace's copy region
+        self._fp8_plan = (ref, fn, region, nbytes, ws)
+        return self._fp8_plan
+
     def _set_sink(self, sink):
+        self._sink_on = sink is not None
         if sink is None:
             self.info.problem.sink = None
             return
@@ -363,7 +383,7 @@ def _call(dev: torch.device, stream, fn, *args):
     """fn(*args, stream handle) with `dev` current, on `stream` or dev's current stream."""
     # (the handle of torch.cuda.current_stream(dev), without making the object)
     handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             rc = fn(*args, handle)
     else:

@@ -585,3 +585,33 @@ def test_no_requests_and_no_keys(bsp, mode):
     o, l = pa.run(b.q.cuda(), k8.view(f8), v8.view(f8), none, k_exp=ke, v_exp=ve)
     torch.cuda.synchronize()
     assert (o == 0).all() and torch.isneginf(l).all() and pa.check_device_error() == 0
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+def test_runs_of_one_object_after_each_other(bsp, mode):
+    """A sink in one run only, a refused run in between, and a plan that needs more pages than the tensors before."""
+    a = workloads.paged_batch(249, [1, 1], [40, 20], 8, 2, 128, 16, "bf16")
+    b = workloads.paged_batch(250, [1, 1], [400, 90], 8, 2, 128, 16, "bf16")
+    f8, sink = torch.float8_e4m3fn, np.linspace(-1, 4, 8)
+    pa = bsp.PagedAttention(mode, 8, 2, 128, 16, False, torch.bfloat16, max_batch=2, max_qo_tokens=2)
+    t = {}
+    for x in (a, b):
+        c8 = cache8(x, 249)
+        k8, ke, v8, ve = (torch.from_numpy(z).cuda() for z in c8)
+        idx = torch.from_numpy(np.ascontiguousarray(x.kv_indices, np.int32)).cuda()
+        t[x.batch, int(x.kv_lens[0])] = (x.q.cuda(), k8.view(f8), v8.view(f8), idx, ke, ve)
+        q, k, v, idx, ke, ve = t[x.batch, int(x.kv_lens[0])]
+        pa.plan(x.kv_indptr, x.last_page_len, qo_indptr=x.qo_indptr)
+        if x is b:  # the tensors of the plan before
+            o = t[2, 40]
+            with pytest.raises(ValueError, match="kv_indices"):
+                pa.run(*o[:4], k_exp=o[4], v_exp=o[5])
+        u = 2.0 ** -11 if mode == "decode" else 2.0 ** -8
+        s = torch.tensor(sink, dtype=torch.float32, device="cuda")
+        for use in (False, True, False):
+            o, l = pa.run(q, k, v, idx, k_exp=ke, v_exp=ve, sink=s if use else None)
+            torch.cuda.synchronize()
+            check(o, l, reference(x, c8, sink if use else None), u, x)
+            with pytest.raises(ValueError, match="k_exp"):
+                pa.run(q, k, v, idx, k_exp=ke[:1], v_exp=ve)
+    assert pa.check_device_error() == 0
