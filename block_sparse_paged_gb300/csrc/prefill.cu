@@ -84,14 +84,15 @@ constexpr int kOffBar = kOffStg + 8 * kStgWarp;
 enum Bar {
     kQFull = 0, kQEmpty,
     kKFull0, kKEmpty0 = kKFull0 + kKStages, kVFull0 = kKEmpty0 + kKStages, kVEmpty0 = kVFull0 + kVStages,
-    kSFull0 = kVEmpty0 + kVStages, kSFull1, kPFull0, kPFull1, kODone0, kODone1, kOFree0, kOFree1,
-    kRawFull0, kRawFull1, kRawEmpty0, kRawEmpty1,  // e4m3 codes by TMA in the staging: K, V
-    kNumBars
+    kSFull0 = kVEmpty0 + kVStages, kSFull1, kPFull0, kPFull1, kODone0, kODone1, kOFree0, kOFree1, kNumBars,
+    // e4m3 codes by TMA in the staging, K and V (behind the other words, whose places stay)
+    kRawFull0 = kNumBars + 2, kRawFull1, kRawEmpty0, kRawEmpty1, kEndBars
 };
 constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmemSlot + 8;
-constexpr int kOffScale = kOffAbort + 8;          // e4m3 by TMA: 2^exponent of the staged keys, K then V
+constexpr int kOffScale = kOffBar + kEndBars * 8;  // e4m3 by TMA: 2^exponent of the staged keys, K then V
 constexpr int kSmemUsed = kOffScale + 2 * kKvTile * 4;
+static_assert(kOffBar + kRawFull0 * 8 == kOffAbort + 8, "barriers behind the abort flag");
 constexpr int kSmemBytes = kSmemUsed + 1024;  // slack to align the base to 1024 bytes
 static_assert(kSmemBytes <= 227 * 1024, "prefill tiles exceed shared memory");
 
@@ -230,8 +231,14 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
         for (int i = 0; i < kNumBars; ++i) {
             const bool softmax_arrivals = i == kPFull0 || i == kPFull1 || i == kOFree0 || i == kOFree1;
             const bool kv_full = (i >= kKFull0 && i < kKFull0 + kKStages) || (i >= kVFull0 && i < kVFull0 + kVStages);
-            const bool converters = kFp8 && (kv_full || i == kRawEmpty0 || i == kRawEmpty1);  // one per warp
-            mbar_init(bar(i), softmax_arrivals ? 128 : converters ? 4 : kv_full && !kTma ? 32 : 1);  // cp.async: per lane
+            // cp.async: one per lane; e4m3: one per converting warp
+            mbar_init(bar(i), softmax_arrivals ? 128 : (kv_full && (kFp8 || !kTma)) ? (kFp8 ? 4 : 32) : 1);
+        }
+        if constexpr (kFp8 && kTma) {
+            for (int v = 0; v < 2; ++v) {
+                mbar_init(bar(kRawFull0 + v), 1);
+                mbar_init(bar(kRawEmpty0 + v), 4);  // converting warps
+            }
         }
         *ctx.abort_flag = 0;
         fence_barrier_init();
@@ -290,7 +297,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
             }
             if (bad) atomicCAS(ctx.status, 0, kStatusPageIndex);
         };
-        auto fetch_raw = [&](const bsp_work_item &w, int) -> bool {
+        auto fetch_raw = [&](const bsp_work_item &w) -> bool {
             float *scale = reinterpret_cast<float *>(smem + kOffScale);
             const int boxes = __popc(__ballot_sync(0xffffffffu, x_box));
 #pragma unroll
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
             if constexpr (kFp8 && kTma) {
                 // codes of the first tile before Q, which waits for the item before
                 look_up(w, 0);
-                if (!(ok = fetch_raw(w, 0))) break;
+                if (!(ok = fetch_raw(w))) break;
                 if (nt > 1) look_up(w, 1);
             }
             if (!(ok = wait_bar_warp(ctx, bar(kQEmpty), (q_cnt & 1) ^ 1))) break;
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
             (void)lookup;
             if constexpr (kFp8 && kTma) {
                 for (int t = 1; t < nt; ++t) {
-                    if (!(ok = fetch_raw(w, t))) break;
+                    if (!(ok = fetch_raw(w))) break;
                     if (t + 1 < nt) look_up(w, t + 1);
                 }
             }
@@ -578,7 +585,6 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
         const uint32_t tS = tmem + tl + sub * 128, tO = tmem + tl + 256 + sub * 128;
         float *plse = reinterpret_cast<float *>(const_cast<uint8_t *>(p.ws) + p.off_plse);
         float *po = reinterpret_cast<float *>(const_cast<uint8_t *>(p.ws) + p.off_po);
-        const uint32_t stg = sb + kOffStg + (sub * 4 + q4) * kStgWarp;  // this warp's staging
         int s_cnt = 0, o_cnt = 0, j = 0;
         bool ok = true;
         // e4m3 cache: the group of subtile 0 converts K tiles, that of subtile 1 V tiles, 32
@@ -616,7 +622,8 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
         };
         bool raw_live = false;  // the staging buffer holds (or awaits) a tile's codes
         int raw_e = 0;          // the exponent of this lane's key of that tile
-        const uint32_t raw = stg + (lane >> 3) * 128 + (lane & 7) * 16;
+        const uint32_t raw_stg = sb + kOffStg + (sub * 4 + q4) * kStgWarp;  // (by key, not by warp)
+        const uint32_t raw = raw_stg + (lane >> 3) * 128 + (lane & 7) * 16;
         auto fetch_raw = [&]() {  // the looked-up tile's codes on their way, then the next look-up
             raw_live = c_it < it1;
             if (!raw_live) return;
@@ -662,7 +669,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     s[i] = scale[4 * i];
-                    d[i] = ld_shared_v4(stg + (4 * i + k7) * 128 + ((c ^ (4 * (i & 1) + k7)) << 4));
+                    d[i] = ld_shared_v4(raw_stg + (4 * i + k7) * 128 + ((c ^ (4 * (i & 1) + k7)) << 4));
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -861,6 +868,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 // bf16 output through this warp's swizzled staging, 64 columns at a
                 // time: each thread writes its row, then every store instruction
                 // covers four whole 128-byte lines (lane l: row 4i + l/8, chunk l%8)
+                const uint32_t stg = kFp8 ? raw_stg : sb + kOffStg + (warp - 2) * kStgWarp;
                 const int cc = lane & 7;
                 const int rt_base = sub * kRows + q4 * 32;
                 unsigned long long orr[8];
