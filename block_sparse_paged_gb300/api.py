@@ -477,21 +477,20 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pages:
     page_size + place, as build_page_tables gives it; tokens with a slot outside the
     pool are skipped. k_pages, v_pages: float8_e4m3fn [num_pages, page_size, H_kv,
     128]; k_exp, v_exp: int8 [num_pages, H_kv], value = code * 2^exp."""
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+    pool, shape, dtype, dev = k_pages.shape, k.shape, k.dtype, k_pages.device
+    if len(pool) != 4 or v_pages.shape != pool:
         raise ValueError("k_pages / v_pages must be [num_pages, page_size, H_kv, D]")
-    P, ps, H, D = k_pages.shape
-    n = k.shape[0]
-    if k.shape != (n, H, D) or v.shape != k.shape or v.dtype != k.dtype or k.dtype not in _DTYPES:
+    P, ps, H, D = pool
+    if len(shape) != 3 or shape[1] != H or shape[2] != D or v.shape != shape or v.dtype is not dtype or dtype not in _DTYPES:
         raise ValueError(f"k and v must be [n, {H}, {D}] in bfloat16 or float32, of one type")
-    ks, vs = k.stride(), v.stride()
+    n, ks, vs = shape[0], k.stride(), v.stride()
     if ks[2] != 1 or vs[2] != 1:
         raise ValueError("the values of a row of k and v must be adjacent")
-    if slot_map.shape != (n,):
+    if slot_map.dim() != 1 or slot_map.numel() != n:
         raise ValueError(f"slot_map must be [{n}]")
     if k_exp.shape != (P, H) or v_exp.shape != (P, H):
         raise ValueError(f"k_exp / v_exp must be [{P}, {H}]")
-    dev = k_pages.device
-    if not k.is_cuda or not v.is_cuda or k.device != dev or v.device != dev:
+    if not k.is_cuda or k.device != dev or v.device != dev:
         raise ValueError(f"k and v must be CUDA tensors on {dev}")
     f8, i8 = torch.float8_e4m3fn, torch.int8
     # a dimension of size 1 is never stepped over: its stride says nothing
@@ -500,5 +499,5 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pages:
     if H == 1:
         ks, vs = (ks[0], 0), (vs[0], 0)
     _call(dev, stream, N.load().bsp_append_kv_fp8, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
-          _DTYPES[k.dtype], n, _addr(slot_map, "slot_map", torch.int64, dev), _addr(k_pages, "k_pages", f8, dev),
+          _DTYPES[dtype], n, _addr(slot_map, "slot_map", torch.int64, dev), _addr(k_pages, "k_pages", f8, dev),
           _addr(v_pages, "v_pages", f8, dev), _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev), P, ps, H, D)
