@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
 // maximum alone, from L2); all get the same exponent, and the CTA with the run's first
 // token writes it and rescales the codes that the page held before. A CTA that
 // reads the exponent after that write gets max(need, e) = e: the same.
-// 24k ragged bf16 tokens x 8 heads 37 us (149 MB); 64, 128 and 256 tokens per window: 38.9,
-// 37.5, 41.6; 3 to 6 CTAs per SM: 43.5, 37.5, 40.7, 42.9 (spills from 5 on).
+// 24k ragged bf16 tokens x 8 heads 36 us (149 MB); with 37.5 us then: 64 and 256 tokens per
+// window 38.9, 41.6; 3, 5 and 6 CTAs per SM 43.5, 40.7, 42.9 (spills from 5 on).
 constexpr int kAppTokens = 128;
 constexpr int kExpMin = -117, kExpMax = 119;
 constexpr int kCacheD = 128;
@@ -305,6 +305,7 @@ struct AppendParams {
     const long long *slots;
     long long n, rows;             // tokens; slots of the pool
     int ps, H;
+    int ps_shift;                  // log2(ps), or -1
 };
 
 // 2^e for e in [-149, 127]
@@ -330,6 +331,12 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// max(|a|, |b|) per half (signs: the product's), of bf16 values; a NaN gives the other operand
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 // lo * s and hi * s as two e4m3 codes
@@ -360,16 +367,21 @@ struct Piece {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
     }
-    // largest |value| as fp32 bits; infinities and NaN included (>= 0x7f800000)
+    // Maxima of |value| are kept as bits: fp32 ones, or two bf16 ones (even and odd values).
+    // An infinity gives a maximum that is not finite(), so do values that are all NaN (fp32:
+    // one NaN).
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return kF32 ? max(a, b) : max2(a, b); }
+    static __device__ __forceinline__ bool finite(uint32_t m) {
+        return kF32 ? m < 0x7f800000u : ((m + 0x00800080u) & 0x80008000u) == 0;
+    }
+    static __device__ __forceinline__ uint32_t fp32_bits(uint32_t m) { return kF32 ? m : max(m << 16, m & 0xffff0000u); }
     __device__ __forceinline__ uint32_t amax() const {
         if constexpr (kF32) {
             constexpr uint32_t m = 0x7fffffffu;
             return max(max(max(w[0].x & m, w[0].y & m), max(w[0].z & m, w[0].w & m)),
                        max(max(w[1].x & m, w[1].y & m), max(w[1].z & m, w[1].w & m)));
         } else {
-            constexpr uint32_t m = 0x7fff7fffu;
-            const uint32_t a = max2(max2(w[0].x & m, w[0].y & m), max2(w[0].z & m, w[0].w & m));
-            return max(a << 16, a & 0xffff0000u);
+            return absmax_bf16x2(absmax_bf16x2(w[0].x, w[0].y), absmax_bf16x2(w[0].z, w[0].w)) & 0x7fff7fffu;
         }
     }
     __device__ __forceinline__ void values(float (&f)[8]) const {
@@ -387,21 +399,32 @@ struct Piece {
             }
         }
     }
-    // codes of the piece at scale s = 2^-e (lowest first); `inf`: the piece may hold
-    // infinities, which become NaN (the format has none)
-    __device__ __forceinline__ uint2 codes(float s, bool inf) const {
+    // infinities become NaN (the format has none)
+    __device__ __forceinline__ void no_infinities() {
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            uint32_t u[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kF32) {
+                    if ((u[i] & 0x7fffffffu) == 0x7f800000u) u[i] = 0x7fffffffu;
+                } else {
+                    if ((u[i] & 0x7fffu) == 0x7f80u) u[i] |= 0x7fu;
+                    if ((u[i] & 0x7fff0000u) == 0x7f800000u) u[i] |= 0x7f0000u;
+                }
+            }
+            w[v] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+    }
+    // codes of the piece at scale s = 2^-e (lowest first)
+    __device__ __forceinline__ uint2 codes(float s) const {
         float f[8];
         values(f);
-        if (inf) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if ((__float_as_uint(f[i]) & 0x7fffffffu) == 0x7f800000u) f[i] = __int_as_float(0x7fffffff);
-        }
         return make_uint2(e4m3x2_scaled(f[0], f[1], s) | (e4m3x2_scaled(f[2], f[3], s) << 16),
                           e4m3x2_scaled(f[4], f[5], s) | (e4m3x2_scaled(f[6], f[7], s) << 16));
     }
 };
-// largest finite |value| of a piece, as fp32 bits
+// the same maximum over the finite values
 template <bool kF32>
 __device__ __noinline__ uint32_t amax_finite(Piece<kF32> x) {
     float f[8];
@@ -412,7 +435,27 @@ __device__ __noinline__ uint32_t amax_finite(Piece<kF32> x) {
         const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
         if (a < 0x7f800000u) r = max(r, a);
     }
-    return r;
+    return kF32 ? r : r >> 16;
+}
+
+// Maxima of a lane's pieces, over their finite values; pieces with an infinity lose it. The
+// pieces that are not finite are looked at one by one.
+template <bool kF32, int kN>
+__device__ __forceinline__ void piece_maxima(Piece<kF32> (&w)[kN], uint32_t (&v)[kN]) {
+    using PC = Piece<kF32>;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        v[i] = w[i].amax();
+        top = PC::larger(top, v[i]);
+    }
+    if (PC::finite(top)) return;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        if (!PC::finite(v[i])) {
+            v[i] = amax_finite(w[i]);
+            w[i].no_infinities();
+        }
 }
 
 // Four stored codes times s (a power of two <= 1), rounded to nearest even.
@@ -430,7 +473,8 @@ __device__ __forceinline__ int place_of(const AppendParams &p, long long t, int 
     if (t < 0 || t >= p.n) return -1;
     const long long sl = __ldg(p.slots + t);
     if (sl < 0 || sl >= p.rows) return -1;
-    const uint32_t pg = (uint32_t)sl / (uint32_t)p.ps;  // (rows fit 32 bits: checked by the caller)
+    // (rows fit 32 bits: checked by the caller)
+    const uint32_t pg = p.ps_shift >= 0 ? (uint32_t)sl >> p.ps_shift : (uint32_t)sl / (uint32_t)p.ps;
     off = (int)((uint32_t)sl - pg * (uint32_t)p.ps);
     return (int)pg;
 }
@@ -453,7 +497,7 @@ __device__ __forceinline__ void rescale_rows(uint8_t *page, long long row_bytes,
 // Maxima of a warp's tokens: v[i] is this lane's part of load i. The values are halved
 // while the lanes are folded (then plain folds): lane l of a row ends with the maximum of
 // load (l / (kPieceLanes / kN)) of its row.
-template <int kN>
+template <class PC, int kN>
 __device__ __forceinline__ uint32_t fold_max(uint32_t (&v)[kN], int piece) {
 #pragma unroll
     for (int n = kN / 2, o = kPieceLanes / 2; n >= 1; n >>= 1, o >>= 1) {
@@ -461,12 +505,12 @@ __device__ __forceinline__ uint32_t fold_max(uint32_t (&v)[kN], int piece) {
 #pragma unroll
         for (int i = 0; i < n; ++i) {
             const uint32_t keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
-            v[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, o));
+            v[i] = PC::larger(keep, __shfl_xor_sync(0xffffffffu, give, o));
         }
     }
 #pragma unroll
-    for (int o = kPieceLanes / kN / 2; o >= 1; o >>= 1) v[0] = max(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-    return v[0];
+    for (int o = kPieceLanes / kN / 2; o >= 1; o >>= 1) v[0] = PC::larger(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    return PC::fp32_bits(v[0]);
 }
 
 template <bool kF32>
@@ -529,18 +573,10 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
         }
         if (lane == 0) (left ? s_left : s_right) = got;
     }
-    uint32_t odd = 0;  // loads whose piece holds an infinity or NaN
     {
         uint32_t v[kLoads];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            v[i] = w[i].amax();
-            if (v[i] >= 0x7f800000u) {
-                odd |= 1u << i;
-                v[i] = amax_finite(w[i]);
-            }
-        }
-        const uint32_t m = fold_max(v, piece);
+        piece_maxima(w, v);
+        const uint32_t m = fold_max<PC>(v, piece);
         constexpr int kShare = kPieceLanes / kLoads;  // lanes that hold the same maximum
         if (piece % kShare == 0) s_tmax[t_first + piece / kShare * kPer] = m;
     }
@@ -568,7 +604,8 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
             for (int f = 0; f < kFly; ++f) {
                 const int jj = j + f * kStep;
                 uint32_t m = y[f].amax();
-                if (m >= 0x7f800000u) m = amax_finite(y[f]);
+                if (!PC::finite(m)) m = amax_finite(y[f]);
+                m = PC::fp32_bits(m);
 #pragma unroll
                 for (int o = kPieceLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
                 if (piece == 0 && jj < outside) atomicMax(&s_max[jj < s_left ? 0 : last_run], m);
@@ -605,7 +642,7 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
     for (int i = 0; i < kLoads; ++i) {
         const uint32_t to = __shfl_sync(0xffffffffu, row, i * kPer + sub);
         const float sc = __shfl_sync(0xffffffffu, scale, i * kPer + sub);
-        if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + to * row_bytes + piece * 8) = w[i].codes(sc, odd >> i & 1);
+        if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + to * row_bytes + piece * 8) = w[i].codes(sc);
     }
     for (uint32_t m = __ballot_sync(0xffffffffu, grow); m; m &= m - 1) {  // codes that such a page held before
         const int l = __ffs(m) - 1;
@@ -619,8 +656,11 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
 // K or V, and reads exactly their tokens. Everything meets by shuffles, no barrier, and no
 // token is read twice where runs have at most 16 tokens; a longer run is read once for its
 // maximum and once more (from L2) for its codes, 16 tokens at a time. 24k ragged bf16
-// tokens x 8 heads 31.4 us (4.5 TB/s, 0.66 of the measured copy bandwidth): issue slots
-// 63% busy, the rest waits for loads.
+// tokens x 8 heads 27.5 us (5.4 TB/s, 0.80 of the measured copy bandwidth): instructions
+// and load latency. Each trimmed piece showed: infinities looked at once per lane instead of
+// per row, maxima as bf16 pairs (max.xorsign.abs), the last row again instead of zeros 31.4
+// -> 29.7; exponents read only where a run begins inside its page, runs from the ballot
+// instead of shuffled pages -> 27.7; shifts for pages of a power of two -> 27.5.
 // CTA: 8 warps on neighbouring heads of the same tokens.
 constexpr int kSeg = 16;
 
@@ -668,26 +708,15 @@ __global__ void __launch_bounds__(256, kF32 ? 2 : 4) append_runs_kernel(const Ap
     constexpr uint32_t kNoRow = ~0u;
 
     PC w[kLoads];
-    uint32_t odd = 0;  // loads whose piece holds an infinity or NaN
-    // tokens T0 - 1 + at .. + count - 1 into w; lane l < 16: the maximum of token l
+    // tokens T0 - 1 + at .. + count - 1 into w (the last one again where there are fewer than
+    // 16); lane l < 16: the maximum of token l
     auto read = [&](long long at, int count) -> uint32_t {
         const char *src = x + at * tb;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            w[i].clear();
-            if (i * kPer + sub < count) w[i].load(src + i * kPer * tb);
-        }
-        odd = 0;
+        for (int i = 0; i < kLoads; ++i) w[i].load(src + (min(i * kPer + sub, count - 1) - sub) * tb);
         uint32_t v[kLoads];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            v[i] = w[i].amax();
-            if (v[i] >= 0x7f800000u) {
-                odd |= 1u << i;
-                v[i] = amax_finite(w[i]);
-            }
-        }
-        const uint32_t m = fold_max(v, piece);  // lane (sub, piece): token 2 (piece / 2) + sub
+        piece_maxima(w, v);
+        const uint32_t m = fold_max<PC>(v, piece);  // lane (sub, piece): token 2 (piece / 2) + sub
         static_assert(kPieceLanes / kLoads == 2 && kPer == 2, "eight loads of two rows");
         return __shfl_sync(0xffffffffu, m, (lane & 1) * kPieceLanes + (lane & 14));
     };
@@ -697,7 +726,7 @@ __global__ void __launch_bounds__(256, kF32 ? 2 : 4) append_runs_kernel(const Ap
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t to = __shfl_sync(0xffffffffu, row, i * kPer + sub);
             const float sc = __shfl_sync(0xffffffffu, scale, i * kPer + sub);
-            if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + to * row_bytes + piece * 8) = w[i].codes(sc, odd >> i & 1);
+            if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + to * row_bytes + piece * 8) = w[i].codes(sc);
         }
     };
     // exponent of a run that begins at place `held` of its page; writes it
@@ -726,16 +755,18 @@ __global__ void __launch_bounds__(256, kF32 ? 2 : 4) append_runs_kernel(const Ap
             const int o = __shfl_sync(0xffffffffu, off, src);
             const int count = stop - at;
             if (lane >= count) pg = -1;
+            const bool begins = pg >= 0 && (lead >> src & 1);
             int had = 0;
-            if (pg >= 0) had = *reinterpret_cast<volatile int8_t *>(exps + (long long)pg * p.H);
-            const uint32_t first = __ballot_sync(0xffffffffu, pg >= 0 && (lead >> src & 1));
+            if (begins && o > 0) had = *reinterpret_cast<volatile int8_t *>(exps + (long long)pg * p.H);
+            const uint32_t first = __ballot_sync(0xffffffffu, begins);
+            const uint32_t next = change >> at & ~((2u << lane) - 1u);  // where this lane's run ends
+            const int run_end = next ? min(__ffs(next) - 1, count) : count;
             uint32_t m = read(at, count);
             // maximum of the run at its first token: fold over the following tokens of the page
 #pragma unroll
             for (int d = 1; d < kSeg; d <<= 1) {
                 const uint32_t mu = __shfl_down_sync(0xffffffffu, m, d);
-                const int pu = __shfl_down_sync(0xffffffffu, pg, d);
-                if (pu == pg) m = max(m, mu);
+                if (lane + d < run_end) m = max(m, mu);
             }
             const uint32_t upto_me = first & (0xffffffffu >> (31 - lane));
             const int head = pg >= 0 && upto_me ? 31 - __clz(upto_me) : lane;
@@ -754,7 +785,7 @@ __global__ void __launch_bounds__(256, kF32 ? 2 : 4) append_runs_kernel(const Ap
         const uint32_t more = change & ~((2u << at) - 1u);
         const long long len = more ? __ffs(more) - 1 - at : 32 - at + tail;
         const int pg = __shfl_sync(0xffffffffu, page, at), held = __shfl_sync(0xffffffffu, off, at);
-        const int had = *reinterpret_cast<volatile int8_t *>(exps + (long long)pg * p.H);
+        const int had = held > 0 ? *reinterpret_cast<volatile int8_t *>(exps + (long long)pg * p.H) : 0;
         uint32_t m = 0;
         for (long long t = 0; t < len; t += kSeg) m = max(m, read(at + t, (int)min((long long)kSeg, len - t)));
 #pragma unroll
@@ -840,15 +871,16 @@ int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64
                      const int64_t *slot_map, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
                      int64_t num_pages, int32_t page_size, int32_t num_kv_heads, cudaStream_t stream) {
     const int64_t elem = dtype == BSP_DTYPE_F32 ? 4 : 2;
-    // By runs: pages of 2 to 16 tokens (24k ragged bf16 tokens into 16-token pages 31.2 us
-    // against 37.1 by windows, fp32 49.7 / 62.6; 256 tokens 4.0 / 4.2), and fp32 into pages
-    // of up to 64 where there are runs enough to fill the GPU (49k tokens 112 / 125; four
-    // prompts of 900 tokens 17.5 / 8.1). Windows: single-token pages (38.5 us against 43.0),
-    // and larger pages, whose runs a warp would walk alone (one prompt of 256 tokens into
-    // 128-token pages 4.0 us against 20.8).
+    // By runs: pages of up to 16 tokens (24k ragged bf16 tokens into 16-token pages 27.5 us
+    // against 36.1 by windows, single-token pages 28.0 / 37.7, fp32 46.1 / 58.3; 256 tokens 3.5 /
+    // 3.7), and larger ones where their runs, each read by one warp, fill the GPU: 24k tokens
+    // into 64- and 128-token pages 36.1 / 38.4 and 42.3 / 46.3, 49k fp32 tokens into 64-token
+    // pages 101 / 116; about even at 3,100 runs (6.2k bf16 tokens into 32-token pages 10.5 /
+    // 10.5) and at half as many of fp32 (6.2k tokens into 64-token pages 16.3 / 16.5). Windows
+    // below that: 3.1k bf16 tokens into 32-token pages 8.1 / 5.8, one prompt of 256 tokens into
+    // 128-token pages 16.1 / 3.7.
     const int64_t warps = (n_tokens + kSeg - 1) / kSeg * 2 * num_kv_heads;
-    const bool runs = page_size >= 2 && (page_size <= kSeg || (dtype == BSP_DTYPE_F32 && page_size <= 4 * kSeg &&
-                                                               n_tokens * 2 * num_kv_heads / page_size >= 4096));
+    const bool runs = page_size <= kSeg || n_tokens * 2 * num_kv_heads / page_size * elem >= 3000 * 2;
     const int64_t ctas = runs ? (warps + 7) / 8 : (n_tokens + kAppTokens - 1) / kAppTokens * 2 * num_kv_heads;
     if (ctas > INT32_MAX / 8) return fail(BSP_ERR_UNSUPPORTED, "too many tokens for one append");
     AppendParams p;
@@ -867,6 +899,9 @@ int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64
     p.rows = (long long)num_pages * page_size;
     p.ps = page_size;
     p.H = num_kv_heads;
+    p.ps_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (page_size == 1 << i) p.ps_shift = i;
     if (runs) {
         if (dtype == BSP_DTYPE_F32) append_runs_kernel<true><<<(unsigned)ctas, 256, 0, stream>>>(p);
         else append_runs_kernel<false><<<(unsigned)ctas, 256, 0, stream>>>(p);

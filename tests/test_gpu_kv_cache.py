@@ -194,6 +194,7 @@ CASES = [  # (seed, ps, H, cached, new, dtype, layout)
     (13, 7, 2, [3] * 30, [1, 20, 6] * 10, torch.float32, "fused"),
     (14, 15, 1, [14, 15, 16], [47, 31, 500], torch.bfloat16, "plain"),
     (16, 33, 16, [5, 0], [2000, 3001], torch.float32, "fused"),
+    (17, 40, 16, [7, 0], [1800, 2100], torch.bfloat16, "heads"),
 ]
 
 
@@ -227,6 +228,25 @@ def test_append_special_values(bsp):
         xv = -xk
         slots = make_slots(rng, 9, ps, [0], [n])
         kc_, vc_ = make_cache(rng, 9, ps, H), make_cache(rng, 9, ps, H)
+        check_append(run_append(bsp, xk, xv, slots, kc_, vc_), xk, xv, slots, kc_, vc_)
+
+
+@pytest.mark.parametrize("ps,n", [(1, 40), (4, 100), (100, 150), (300, 290)])
+def test_append_infinities_and_nan_anywhere(bsp, ps, n):
+    """Either sign, next to each other and to finite values, whole rows of them: they become NaN and count for nothing."""
+    rng = np.random.default_rng(50 + ps)
+    H = 2
+    x = rng.standard_normal((n, H, 128)) * np.exp2(rng.uniform(-6, 6, (n, H, 1)))
+    for bad in (np.inf, -np.inf, np.nan):
+        x[rng.random(x.shape) < 0.02] = bad
+        x[rng.integers(0, n, 3), 1] = bad
+        x[rng.integers(0, n), 0, 8:24] = bad
+    P = -(-n // ps) + 2
+    for dtype in (torch.float32, torch.bfloat16):
+        xk = torch.from_numpy(x).to(dtype)
+        xv = xk.flip(0)
+        slots = make_slots(rng, P, ps, [0], [n])
+        kc_, vc_ = make_cache(rng, P, ps, H), make_cache(rng, P, ps, H)
         check_append(run_append(bsp, xk, xv, slots, kc_, vc_), xk, xv, slots, kc_, vc_)
 
 
