@@ -481,10 +481,10 @@ __device__ __forceinline__ int place_of(const AppendParams &p, long long t, int 
 
 // A warp: codes of rows 0 .. held - 1 of a page whose exponent rose by -drop, four rows of
 // 8 lanes x 16 bytes at a time. page: the page's codes of this kv head.
-__device__ __forceinline__ void rescale_rows(uint8_t *page, long long row_bytes, int held, int drop, int lane) {
+__device__ __forceinline__ void rescale_rows(uint8_t *page, uint32_t row_bytes, int held, int drop, int lane) {
     const float s = pow2i(max(drop, -126));
     for (int r = lane >> 3; r < held; r += 4) {
-        uint4 *at = reinterpret_cast<uint4 *>(page + r * row_bytes) + (lane & 7);
+        uint4 *at = reinterpret_cast<uint4 *>(page + (uint64_t)r * row_bytes) + (lane & 7);
         uint4 c = *at;
         c.x = rescale_codes(c.x, s);
         c.y = rescale_codes(c.y, s);
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
     __syncthreads();
     // Lane l < kPerWarp: the exponent of the warp's token l and where its codes go
     uint8_t *codes = (is_v ? p.v_codes : p.k_codes) + (long long)h * kCacheD;
-    const long long row_bytes = (long long)p.H * kCacheD;
+    const uint32_t row_bytes = (uint32_t)p.H * kCacheD;
     constexpr uint32_t kNoRow = ~0u;
     uint32_t row = kNoRow;
     float scale = 0.f;
@@ -642,12 +642,12 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
     for (int i = 0; i < kLoads; ++i) {
         const uint32_t to = __shfl_sync(0xffffffffu, row, i * kPer + sub);
         const float sc = __shfl_sync(0xffffffffu, scale, i * kPer + sub);
-        if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + to * row_bytes + piece * 8) = w[i].codes(sc);
+        if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + (uint64_t)to * row_bytes + piece * 8) = w[i].codes(sc);
     }
     for (uint32_t m = __ballot_sync(0xffffffffu, grow); m; m &= m - 1) {  // codes that such a page held before
         const int l = __ffs(m) - 1;
         const int rows = __shfl_sync(0xffffffffu, held, l);
-        uint8_t *page = codes + (long long)(__shfl_sync(0xffffffffu, row, l) - rows) * row_bytes;
+        uint8_t *page = codes + (uint64_t)(__shfl_sync(0xffffffffu, row, l) - rows) * row_bytes;
         rescale_rows(page, row_bytes, rows, __shfl_sync(0xffffffffu, drop, l), lane);
     }
 }
@@ -656,11 +656,12 @@ __global__ void __launch_bounds__(32 * Piece<kF32>::kWarps, kF32 ? 2 : 4) append
 // K or V, and reads exactly their tokens. Everything meets by shuffles, no barrier, and no
 // token is read twice where runs have at most 16 tokens; a longer run is read once for its
 // maximum and once more (from L2) for its codes, 16 tokens at a time. 24k ragged bf16
-// tokens x 8 heads 27.5 us (5.4 TB/s, 0.80 of the measured copy bandwidth): instructions
+// tokens x 8 heads 27.1 us (5.5 TB/s, 0.81 of the measured copy bandwidth): instructions
 // and load latency. Each trimmed piece showed: infinities looked at once per lane instead of
 // per row, maxima as bf16 pairs (max.xorsign.abs), the last row again instead of zeros 31.4
 // -> 29.7; exponents read only where a run begins inside its page, runs from the ballot
-// instead of shuffled pages -> 27.7; shifts for pages of a power of two -> 27.5.
+// instead of shuffled pages -> 27.7; shifts for pages of a power of two and 32-bit row bytes
+// -> 27.1.
 // CTA: 8 warps on neighbouring heads of the same tokens.
 constexpr int kSeg = 16;
 
@@ -704,7 +705,7 @@ __global__ void __launch_bounds__(256, kF32 ? 2 : 4) append_runs_kernel(const Ap
     const char *x = (is_v ? p.v + h * p.v_head : p.k + h * p.k_head) + (T0 - 1 + sub) * tb + piece * kBytes;
     int8_t *exps = (is_v ? p.v_exp : p.k_exp) + h;
     uint8_t *codes = (is_v ? p.v_codes : p.k_codes) + (long long)h * kCacheD;
-    const long long row_bytes = (long long)p.H * kCacheD;
+    const uint32_t row_bytes = (uint32_t)p.H * kCacheD;
     constexpr uint32_t kNoRow = ~0u;
 
     PC w[kLoads];
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(256, kF32 ? 2 : 4) append_runs_kernel(const Ap
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t to = __shfl_sync(0xffffffffu, row, i * kPer + sub);
             const float sc = __shfl_sync(0xffffffffu, scale, i * kPer + sub);
-            if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + to * row_bytes + piece * 8) = w[i].codes(sc);
+            if (to != kNoRow) *reinterpret_cast<uint2 *>(codes + (uint64_t)to * row_bytes + piece * 8) = w[i].codes(sc);
         }
     };
     // exponent of a run that begins at place `held` of its page; writes it
@@ -737,7 +738,7 @@ __global__ void __launch_bounds__(256, kF32 ? 2 : 4) append_runs_kernel(const Ap
         return e;
     };
     auto rescale = [&](int pg, int held, int drop) {
-        rescale_rows(codes + (long long)pg * p.ps * row_bytes, row_bytes, held, drop, lane);
+        rescale_rows(codes + (uint64_t)pg * p.ps * row_bytes, row_bytes, held, drop, lane);
     };
 
     for (int at = __ffs(mine) - 1; at < end;) {
