@@ -184,7 +184,8 @@ class PagedAttention:
         code * 2^exp (the cache that append_kv writes). A prefill over such pools
         may convert the plan's pages into a bf16 copy first: in the workspace's copy
         region where max_gather_pages covers the page table, else in a temporary
-        tensor of this call; a decode with pages of one or two tokens may gather the
+        tensor of this call (a captured run that follows plans with larger tables
+        needs the region: status 0x303 otherwise); a decode with pages of one or two tokens may gather the
         exponents into a temporary tensor. sink:
         float32 [H_qo] on the device, one extra softmax logit per query head
         without a value row (the attention-sink variant), or None."""
