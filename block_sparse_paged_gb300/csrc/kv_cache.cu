@@ -853,7 +853,7 @@ int launch_page_tables(int32_t batch, int32_t page_size, const int32_t *cached_l
     p.cap_tokens = cap_tokens;
     const size_t smem = 3 * sizeof(int) * (size_t)(batch + 1);
     static bool configured[64] = {false};
-    if (smem > 48 * 1024 && !configured[dev]) {
+    if (!configured[dev]) {  // (the default limit counts the kernel's static shared memory too)
         cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)(3 * sizeof(int) * (kTabMaxBatch + 1)));
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("page tables smem attribute: ") + cudaGetErrorString(e));
