@@ -42,7 +42,8 @@
 // e4m3 cache with an exponent per (page, kv head) (kBlk): the same, the exponents
 // carried through the ring as bytes; scores times 2^e_k, token weights 2^(s + e_v)
 // against their own running maximum, so that they fit f16 however far exponents lie
-// apart. HBM-bound: 64 requests x 4,585 tokens 98-99 us, 6.1 TB/s, 0.90 of the measured
+// apart, and lifted by 2^kLift within it, so that many small weights on full codes count
+// beside a large one on small codes. HBM-bound: 64 requests x 4,585 tokens 98-99 us, 6.1 TB/s, 0.90 of the measured
 // copy bandwidth; page size 1 (cp.async) 57 us for 268 MB, exponents gathered first.
 // fp32 kernel: CUDA cores, fp32 throughout, same plan and merge.
 // Reduction kernel: the reduction map's slots of each split output, merged in
@@ -74,6 +75,11 @@ constexpr int kConsumers = 4;
 constexpr int kTileK = 64;                   // unit of the stage sizes below; the largest page box (rows)
 constexpr int kStages = 5;
 constexpr long long kWaitLimitCycles = 4000000000ll;  // about 2 s at 2 GHz: a fault, not a stall
+// kBlk: token weights as f16 values up to 2^kLift (the largest power of two in range): those
+// down to 2^-29 of the largest keep 11 bits, smaller ones are off by at most 2^-40 of it. (As
+// values up to 1 they lost bits below 2^-14 and vanished from 2^-25 on: a token with nearly all
+// of the weight and values near zero hid the others.) 2^31 tokens times 448 are in fp32's range.
+constexpr float kLift = 15.f;
 // reduction-map entries a CTA completes and folds after its queue (more are folded at once)
 constexpr int kMaxPendingFolds = 32;
 
@@ -669,7 +675,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
             // of the sum (its tokens r, r + 8), O^T accumulators
             // kBlk: oh, the running maximum of score + V exponent, is the reference of O
             // (token weights 2^(s + e_v), whatever the exponents' spread); mh stays that of
-            // the sum. At the end O moves to mh.
+            // the sum. At the end O moves from oh - kLift to mh.
             float mh[kNH][2], lh[kNH][2], oacc[D / 16][kNH][4];
             float oh[kNH][2];
 #pragma unroll
@@ -771,10 +777,11 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                         const float n0 = fmaxf(mh[nh][0], mx0), n1 = fmaxf(mh[nh][1], mx1);
                         const float q0 = fmaxf(oh[nh][0], my0), q1 = fmaxf(oh[nh][1], my1);
                         const float ref0 = n0 == -INFINITY ? 0.f : n0, ref1 = n1 == -INFINITY ? 0.f : n1;
-                        const float rq0 = q0 == -INFINITY ? 0.f : q0, rq1 = q1 == -INFINITY ? 0.f : q1;
+                        const float z0 = q0 == -INFINITY ? 0.f : q0, z1 = q1 == -INFINITY ? 0.f : q1;
+                        const float rq0 = z0 - kLift, rq1 = z1 - kLift;
                         lh[nh][0] *= ex2_ftz(mh[nh][0] - ref0);
                         lh[nh][1] *= ex2_ftz(mh[nh][1] - ref1);
-                        const float b0 = ex2_ftz(oh[nh][0] - rq0), b1 = ex2_ftz(oh[nh][1] - rq1);
+                        const float b0 = ex2_ftz(oh[nh][0] - z0), b1 = ex2_ftz(oh[nh][1] - z1);
                         mh[nh][0] = n0;
                         mh[nh][1] = n1;
                         oh[nh][0] = q0;
@@ -971,8 +978,8 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                     lh[nh][1] += __shfl_xor_sync(0xffffffffu, lh[nh][1], o);
                 }
                 if constexpr (kBlk) {
-                    const float f0 = oh[nh][0] == -INFINITY ? 0.f : exp2f(oh[nh][0] - mh[nh][0]);
-                    const float f1 = oh[nh][1] == -INFINITY ? 0.f : exp2f(oh[nh][1] - mh[nh][1]);
+                    const float f0 = oh[nh][0] == -INFINITY ? 0.f : exp2f((oh[nh][0] - kLift) - mh[nh][0]);
+                    const float f1 = oh[nh][1] == -INFINITY ? 0.f : exp2f((oh[nh][1] - kLift) - mh[nh][1]);
 #pragma unroll
                     for (int dt = 0; dt < D / 16; ++dt) {
                         oacc[dt][nh][0] *= f0; oacc[dt][nh][1] *= f1;

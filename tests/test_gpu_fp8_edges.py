@@ -1,0 +1,53 @@
+"""Attention over the 8-bit cache where weights, queries and masked values are far from ordinary; decode against the fp64
+oracle within the row-wise bounds of fp8_bounds.py."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads
+from fp8_bounds import check, decode_bounds
+from gpu_helpers import lib
+from oracle import fp8
+from oracle import kv_cache as kc
+from test_gpu_fp8_block import cache8, run_block
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bsp():
+    return lib()
+
+
+def check_decode(bsp, b, c8, **kw):
+    """One run against the oracle; returns its outputs."""
+    out, lse, pa = run_block(bsp, b, c8, **kw)
+    k, v = kc.values(c8[0], c8[1]), kc.values(c8[2], c8[3])
+    O, L = oracle.attention_of(b, k=k, v=v)
+    A, _ = oracle.attention_of(b, k=k, v=np.abs(v))
+    check(out.double().cpu().numpy(), lse.double().cpu().numpy(), O, L,
+          *decode_bounds(b, k, fp8.dequantize(c8[2], 1.0), c8[3], O, L, A))
+    assert pa.check_device_error() == 0
+    return out, lse
+
+
+# ---- token weights -----------------------------------------------------------------
+@pytest.mark.parametrize("hq,ps", [(16, 16), (16, 1), (32, 8), (32, 12)])
+def test_a_token_of_great_weight_and_no_values(bsp, hq, ps):
+    """A first token that takes all but 2^-10 .. 2^-36 of the softmax and whose values are zero or nearly so: the outputs
+    are those of the others."""
+    b = workloads.paged_batch(301, [1, 1], [1500, 700], hq, 2, 128, ps, "bf16", extra_pages=2)
+    k8, ke, v8, ve = cache8(b, 301, ke=(0, 0), ve=(-6, -6))
+    rng = np.random.default_rng(301)
+    k8[:] = torch.from_numpy(rng.standard_normal(k8.shape)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    # a query of c in every dimension: the first token's score is 8 * 128 c / sqrt(128) / ln 2 = 130.6 c, the others'
+    # N(0, 1.44 c)
+    gaps = np.array([10, 14, 18, 22, 24, 26, 30, 36])[np.arange(hq) % 8]
+    b.q = torch.from_numpy(np.broadcast_to((gaps / 130.6)[None, :, None], b.q.shape).copy()).bfloat16()
+    for r in range(2):
+        first = b.kv_indices[b.kv_indptr[r]]
+        k8[first, 0] = 0x50  # 8
+        v8[first, 0] = 0
+        v8[first, 0, :, 64:] = 0x01  # 2^-9, the least code
+    check_decode(bsp, b, [k8, ke, v8, ve], num_ctas=7)
