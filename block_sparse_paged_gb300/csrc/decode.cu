@@ -97,6 +97,13 @@ __device__ __forceinline__ float ex2_ftz(float x) {
     return y;
 }
 
+// (lo, hi) -> f16x2; infinities and NaN stay
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
@@ -654,7 +661,13 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
             //     64h + 16c + 4j + {0, 1} and {2, 3};
             //   O^T tile dt: rows r and r + 8 are dims 16r + 2dt and 16r + 2dt + 1.
             const int c = lane & 3, qn = lane >> 2;
-            uint32_t qf[D / 16][kNH][2];  // Q^T fragments, f16 (exact for bf16 values 2^-14 .. 65504; larger saturate)
+            // Q^T fragments, f16 (exact for bf16 values 2^-14 .. 65504; larger saturate). kBlk: each
+            // head's row times a power of two that takes its largest value to 2^14 .. 2^15, so that
+            // small queries of large keys lose nothing (values from 2^-31 of the largest on are
+            // exact); hs takes it back, and scales, the scores of this lane's heads 2c, 2c + 1 of each
+            // tile.
+            uint32_t qf[D / 16][kNH][2];
+            float hs[kNH][2];
             {
                 const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q) +
                                           ((size_t)w.q_tok0 * p.H_qo + (size_t)w.kv_head * g) * D;
@@ -666,8 +679,28 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const int c2 = (64 * (kk >> 2) + 16 * c + 4 * (kk & 3)) >> 1;  // index in bf16 pairs
                         const uint32_t x = head < g ? __ldg(qr + c2) : 0u, y = head < g ? __ldg(qr + c2 + 1) : 0u;
-                        qf[kk][nh][0] = pack_f16_sat(bf16_lo(x), bf16_hi(x));
-                        qf[kk][nh][1] = pack_f16_sat(bf16_lo(y), bf16_hi(y));
+                        qf[kk][nh][0] = kBlk ? x : pack_f16_sat(bf16_lo(x), bf16_hi(x));
+                        qf[kk][nh][1] = kBlk ? y : pack_f16_sat(bf16_lo(y), bf16_hi(y));
+                    }
+                    if constexpr (kBlk) {
+                        uint32_t mx = 0;  // largest |q| of the row, as bf16 bits
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mx = __vmaxu2(mx, __vmaxu2(qf[kk][nh][0] & 0x7fff7fffu, qf[kk][nh][1] & 0x7fff7fffu));
+                        mx = max(mx & 0xffffu, mx >> 16);
+                        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        // 2^(E - 127) <= max |q| < 2^(E - 126); rows with an infinity or NaN as they are
+                        const int E = (int)(mx >> 7), up = E == 255 ? 0 : min(120, 141 - E);
+                        const float f = __int_as_float((up + 127) << 23);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                qf[kk][nh][i] = pack_f16(bf16_lo(qf[kk][nh][i]) * f, bf16_hi(qf[kk][nh][i]) * f);
+                        const float down = __int_as_float((127 - up) << 23) * (p.soft_cap_on ? p.cap_in : p.scale_log2);
+                        hs[nh][0] = __shfl_sync(0xffffffffu, down, 8 * c);
+                        hs[nh][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
                     }
                 }
             }
@@ -725,8 +758,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                         for (int i = 0; i < 2; ++i) {
                             const int at = kTma ? row0 / 8 + i : row0 + 8 * i + qn;
                             const int e = ek[at];
-                            kf[i] = __int_as_float(e >= -126 ? (e + 127) << 23 : 0x00400000 >> (-127 - e)) *
-                                    (p.soft_cap_on ? p.cap_in : p.scale_log2);
+                            kf[i] = __int_as_float(e >= -126 ? (e + 127) << 23 : 0x00400000 >> (-127 - e));
                             ve[i] = (float)ek[LY::kExpN + at];
                         }
                         float st[kNH][2][4];  // two accumulators per head tile (even / odd kk) to halve the chain
@@ -750,7 +782,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int tk = row0 + qn + 8 * (e >> 1);
-                                float x = (st[nh][0][e] + st[nh][1][e]) * kf[e >> 1];
+                                float x = (st[nh][0][e] + st[nh][1][e]) * (kf[e >> 1] * hs[nh][e & 1]);
                                 if (p.soft_cap_on) x = tanh_ex2(x) * p.cap_out;
                                 sv[sb][nh][e] = (tk < left && tk >= lo_stage) ? x : -INFINITY;
                                 so[sb][nh][e] = sv[sb][nh][e] + ve[e >> 1];

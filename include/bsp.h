@@ -472,7 +472,9 @@ int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int6
  *                      faster without; too small a region is BSP_ERR_CAPACITY
  * Any page size. Decode: g <= 16; scores and sums fp32, token weights times
  * 2^v_exp in f16 against their own running maximum (2^15 there: relative error 2^-11
- * down to 2^-29 of the maximum, below that at most 2^-40 of it). Its region (16-byte aligned,
+ * down to 2^-29 of the maximum, below that at most 2^-40 of it). Queries are f16 too,
+ * each head's row scaled by a power of two to the top of that range: any bf16 row is
+ * taken, its values exact down to 2^-31 of the row's largest. Its region (16-byte aligned,
  * num_table_pages rounded up to 16, times 2 * H_kv bytes) takes the plan's exponents in
  * table order (pages that are no power of two of 8 or more tokens; otherwise unused).
  * A captured run may be replayed after a plan with a larger table than its region

@@ -51,3 +51,43 @@ def test_a_token_of_great_weight_and_no_values(bsp, hq, ps):
         v8[first, 0] = 0
         v8[first, 0, :, 64:] = 0x01  # 2^-9, the least code
     check_decode(bsp, b, [k8, ke, v8, ve], num_ctas=7)
+
+
+# ---- queries -----------------------------------------------------------------------
+@pytest.mark.parametrize("by", [-100, -40, -20, 20, 40, 80])
+@pytest.mark.parametrize("hq,ps,cap", [(16, 16, 0.0), (32, 16, 0.0), (16, 1, 30.0), (32, 5, 0.0)])
+def test_queries_of_any_size(bsp, hq, ps, cap, by):
+    """q * 2^by over keys with exponents lower by as much: the same scores, the same bits."""
+    b = workloads.paged_batch(302, [1, 1, 1], [900, 77, 3], hq, 2, 128, ps, "bf16", extra_pages=1)
+    b.soft_cap = cap
+    k8, ke, v8, ve = cache8(b, 302)
+    used = np.unique(b.kv_indices)
+    want = check_decode(bsp, b, [k8, ke, v8, ve], num_ctas=5)
+    b.q = b.q * 2.0 ** by
+    ke = ke.copy()
+    ke[used] -= by
+    got = check_decode(bsp, b, [k8, ke, v8, ve], num_ctas=5)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("hq", [16, 32])
+def test_heads_of_different_sizes(bsp, hq):
+    """Rows of q from 2^-60 to 2^60, with a dimension far above the row's others, over keys near 1, and rows of zeros."""
+    b = workloads.paged_batch(303, [1, 1], [600, 40], hq, 2, 128, 16, "bf16")
+    c8 = cache8(b, 303)
+    scale = 2.0 ** np.linspace(-60, 60, hq).round()
+    q = b.q.float() * torch.from_numpy(scale).float()[None, :, None]
+    q[:, ::3, 5] *= 2.0 ** 14
+    q[1, hq // 2] = 0
+    b.q = q.bfloat16()
+    check_decode(bsp, b, c8, num_ctas=5)
+
+
+def test_subnormal_queries(bsp):
+    """bf16 values below the normal range, the largest of their row."""
+    b = workloads.paged_batch(304, [1], [300], 8, 1, 128, 16, "bf16")
+    k8, ke, v8, ve = cache8(b, 304)
+    b.q = (b.q.float() * 2.0 ** -129).bfloat16()
+    used = np.unique(b.kv_indices)
+    ke[used] = 118
+    check_decode(bsp, b, [k8, ke, v8, ve], num_ctas=2)
