@@ -851,10 +851,14 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                             __syncwarp();
                             if (lane == 0) sm100::mbar_arrive(empty0 + 8 * s);
                         }
-                        if (valid < 16) {  // the chunk ends inside (or before) this sub-block (warp-uniform)
+                        // the chunk ends inside (or before) this sub-block, or the window begins in it or
+                        // behind (warp-uniform): rows that no head sees may hold anything
+                        if (valid < 16 || lo_stage > row0) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (2 * c + (i & 1) + 8 * (i >> 1) >= valid) vw[i] = make_uint4(0, 0, 0, 0);
+                            for (int i = 0; i < 4; ++i) {
+                                const int at = 2 * c + (i & 1) + 8 * (i >> 1);
+                                if (at >= valid || row0 + at < lo_stage) vw[i] = make_uint4(0, 0, 0, 0);
+                            }
                         }
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {

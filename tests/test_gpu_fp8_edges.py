@@ -91,3 +91,19 @@ def test_subnormal_queries(bsp):
     used = np.unique(b.kv_indices)
     ke[used] = 118
     check_decode(bsp, b, [k8, ke, v8, ve], num_ctas=2)
+
+
+# ---- what no head sees -------------------------------------------------------------
+@pytest.mark.parametrize("hq,ps", [(16, 16), (32, 64), (16, 100), (32, 1)])
+def test_nan_codes_before_the_window(bsp, hq, ps):
+    """The page that the window begins in holds older tokens: their NaN codes reach nobody."""
+    b = workloads.paged_batch(306, [1, 1, 1], [900, 77, 250], hq, 2, 128, ps, "bf16", extra_pages=1)
+    b.window_left = 55
+    c8 = cache8(b, 306)
+    want = check_decode(bsp, b, c8, num_ctas=4)
+    for r, n in enumerate((900, 77, 250)):
+        for t in range(n - 1 - 55):
+            page = b.kv_indices[b.kv_indptr[r] + t // ps]
+            c8[0][page, t % ps] = c8[2][page, t % ps] = 0x7f
+    got = check_decode(bsp, b, c8, num_ctas=4)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
