@@ -1014,6 +1014,9 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                     lh[nh][1] += __shfl_xor_sync(0xffffffffu, lh[nh][1], o);
                 }
                 if constexpr (kBlk) {
+                    // scores that are all NaN: not an empty state
+                    if (lh[nh][0] != lh[nh][0] && mh[nh][0] == -INFINITY) mh[nh][0] = 0.f;
+                    if (lh[nh][1] != lh[nh][1] && mh[nh][1] == -INFINITY) mh[nh][1] = 0.f;
                     const float f0 = oh[nh][0] == -INFINITY ? 0.f : exp2f((oh[nh][0] - kLift) - mh[nh][0]);
                     const float f1 = oh[nh][1] == -INFINITY ? 0.f : exp2f((oh[nh][1] - kLift) - mh[nh][1]);
 #pragma unroll
@@ -1213,7 +1216,8 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
             if (w.slot < 0 && p.sink) inv *= fold_sink(lse_v, p.sink[w.kv_head * g + ct]);
 #pragma unroll
             for (int ww = 0; ww < kConsumers; ++ww) fac[ww * kSR + ct] = f[ww] * inv;
-            rlse[ct] = lse_v;
+            // (a partial state of NaN: +inf wins the fold's maximum and makes NaN of the row)
+            rlse[ct] = kBlk && w.slot >= 0 && lse_v != lse_v ? INFINITY : lse_v;
         }
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(merge_mid);

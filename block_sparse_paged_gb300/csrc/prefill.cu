@@ -207,7 +207,9 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, float s) {
 // on their way into the tiles by the softmax warps, in the time in which they would
 // wait for their next S; everything behind the rings is the bf16 kernel. The codes
 // come by TMA boxes (kTma) or cp.async, by the same rule.
-template <bool kTma, bool kVar, bool kFp8 = false>
+// kNan: a row whose sum is NaN is written as NaN (the e4m3 cache, its bf16 copy too; rows
+// over bf16 pools get an LSE of -inf then. Asking at run time cost those 0.5%).
+template <bool kTma, bool kVar, bool kFp8 = false, bool kNan = kFp8>
 __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const PrefillParams p) {
@@ -850,7 +852,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
 #pragma unroll
                 for (int i = 0; i < kD; ++i) ov[i] = 0.f;
             }
-            const bool has = l > 0.f;
+            const bool has = kNan ? !(l <= 0.f) : l > 0.f;
             float inv = has ? 1.f / l : 0.f;
             float lse_v = has ? (m + log2f(l)) * dev::kLn2 : -INFINITY;
             const size_t orow = (size_t)(w.q_tok0 + rt / g) * p.H_qo + (size_t)w.kv_head * g + (rt % g);
@@ -905,7 +907,8 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 if (w.slot < 0) {
                     if (p.lse) p.lse[orow] = lse_v;
                 } else {
-                    plse[prow] = lse_v;
+                    // (a partial state of NaN: +inf wins the fold's maximum and makes NaN of the row)
+                    plse[prow] = kNan && lse_v != lse_v ? INFINITY : lse_v;
                 }
             }
             if constexpr (kFp8) {
@@ -1166,15 +1169,16 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
     p.causal = P.causal;
     p.tile_rows = plan->tile_rows;
 
-    static bool configured[8][64] = {{false}};
+    static bool configured[10][64] = {{false}};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(BSP_ERR_CUDA, "no current CUDA device");
     const bool var = P.window_left > 0 || P.logits_soft_cap > 0.f;
     auto kern = tma8 ? (var ? prefill_kernel<true, true, true> : prefill_kernel<true, false, true>)
                 : fp8 ? (var ? prefill_kernel<false, true, true> : prefill_kernel<false, false, true>)
+                : copied ? (var ? prefill_kernel<true, true, false, true> : prefill_kernel<true, false, false, true>)
                 : tma ? (var ? prefill_kernel<true, true> : prefill_kernel<true, false>)
                     : (var ? prefill_kernel<false, true> : prefill_kernel<false, false>);
-    const int which = (tma8 ? 6 : fp8 ? 4 : tma ? 2 : 0) + (var ? 1 : 0);
+    const int which = (copied ? 8 : tma8 ? 6 : fp8 ? 4 : tma ? 2 : 0) + (var ? 1 : 0);
     if (!configured[which][dev]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("prefill smem attribute: ") + cudaGetErrorString(e));

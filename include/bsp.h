@@ -487,6 +487,10 @@ int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_stride, int6
  * A captured run replayed after a plan with a larger page table than its region holds
  * sets the status word (0x303). A page id outside [0, num_pages) reads as zero codes and sets the
  * workspace status word (0x302, bsp_check_device_error).
+ * NaN codes of K, and queries that are not finite, make NaN of O and LSE in the rows that
+ * see them; a NaN code of V makes NaN of its dimension of O there, and in a prefill also
+ * in the other rows of their query tile (256 / g positions). Codes that no row of the
+ * tile sees reach none.
  */
 int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                              const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,

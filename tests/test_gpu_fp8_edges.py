@@ -107,3 +107,43 @@ def test_nan_codes_before_the_window(bsp, hq, ps):
             c8[0][page, t % ps] = c8[2][page, t % ps] = 0x7f
     got = check_decode(bsp, b, c8, num_ctas=4)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---- NaN ---------------------------------------------------------------------------
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+def test_a_query_that_is_not_finite(bsp, mode, bad):
+    """It reaches its own row alone, split (the first request) or not."""
+    qo = [1, 1] if mode == "decode" else [9, 5]
+    b = workloads.paged_batch(305, qo, [3000, 40], 16, 2, 128, 16, "bf16", causal=mode == "prefill")
+    c8 = cache8(b, 305)
+    want = run_block(bsp, b, c8, num_ctas=7)
+    b.q = b.q.clone()
+    last = len(b.q) - 1
+    b.q[0, 3, 7] = b.q[last, 12, 100] = bad
+    got = run_block(bsp, b, c8, num_ctas=7)
+    for r, h in ((0, 3), (last, 12)):
+        assert torch.isnan(got[0][r, h]).all() and torch.isnan(got[1][r, h])
+        for t in want[:2] + got[:2]:
+            t[r, h] = 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("ps", [16, 12])
+def test_a_nan_key(bsp, mode, ps):
+    """Its codes reach the rows of its request and kv head that see it: outputs and LSE, in a split request, one that is
+    not split, and one that has no other key."""
+    qo, kv = ([1] * 4, [3000, 40, 1, 77]) if mode == "decode" else ([9, 5, 1, 20], [3000, 40, 1, 77])
+    b = workloads.paged_batch(307, qo, kv, 16, 2, 128, ps, "bf16", causal=mode == "prefill")
+    c8 = cache8(b, 307)
+    want = run_block(bsp, b, c8, num_ctas=9)
+    hit = torch.zeros(want[1].shape, dtype=torch.bool)
+    for r, (t, h) in enumerate(((1501, 1), (37, 0), (0, 1))):
+        c8[0][b.kv_indices[b.kv_indptr[r] + t // ps], t % ps, h, 5] = 0x7f
+        first = max(0, t - (kv[r] - qo[r]))  # the request's first position that sees token t
+        hit[b.qo_indptr[r] + first:b.qo_indptr[r + 1], 8 * h:8 * h + 8] = True
+    got = run_block(bsp, b, c8, num_ctas=9)
+    hit = hit.cuda()
+    assert torch.isnan(got[0][hit]).all() and torch.isnan(got[1][hit]).all()
+    assert torch.equal(got[0][~hit], want[0][~hit]) and torch.equal(got[1][~hit], want[1][~hit])
