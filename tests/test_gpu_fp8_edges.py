@@ -10,7 +10,7 @@ from fp8_bounds import check, decode_bounds
 from gpu_helpers import lib
 from oracle import fp8
 from oracle import kv_cache as kc
-from test_gpu_fp8_block import cache8, run_block
+from test_gpu_fp8_block import DECODE, cache8, run_block
 
 pytestmark = pytest.mark.gpu
 
@@ -147,3 +147,24 @@ def test_a_nan_key(bsp, mode, ps):
     hit = hit.cuda()
     assert torch.isnan(got[0][hit]).all() and torch.isnan(got[1][hit]).all()
     assert torch.equal(got[0][~hit], want[0][~hit]) and torch.equal(got[1][~hit], want[1][~hit])
+
+
+# ---- ordinary batches within the row-wise bounds -----------------------------------
+@pytest.mark.parametrize("case", DECODE, ids=[f"d{c[0]}" for c in DECODE])
+def test_decode_rows(bsp, case):
+    seed, kv, hq, hk, ps, C, w, cap = case
+    b = workloads.paged_batch(seed, [1] * len(kv), kv, hq, hk, 128, ps, "bf16", extra_pages=3)
+    b.window_left, b.soft_cap = w, cap
+    check_decode(bsp, b, cache8(b, seed), num_ctas=C)
+
+
+@pytest.mark.parametrize("ps", [1, 16])
+def test_exponents_far_apart_rows(bsp, ps):
+    b = workloads.paged_batch(231, [1, 1], [900, 77], 16, 2, 128, ps, "bf16", extra_pages=1)
+    check_decode(bsp, b, cache8(b, 231, ke=(-25, -5), ve=(-70, 50)), num_ctas=7)
+
+
+def test_full_size_rows(bsp):
+    """64 requests of up to 8192 tokens."""
+    b = workloads.batched_decode_bf16()
+    check_decode(bsp, b, cache8(b, 237))
