@@ -43,6 +43,20 @@ def _dev(t: torch.Tensor, name: str, dtype=None, device=None) -> ctypes.c_void_p
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _new(stream, make):
+    """make(), a tensor (or PageTables) that a call allocates for its results. It belongs to the stream that the call runs
+    on, so that it takes no memory that the current stream still uses nor gives up any that `stream` still writes; and
+    what the current stream does with it before it is freed comes before the memory's next use."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make()
+    if t.is_cuda:
+        t.record_stream(here)
+    return t
+
+
 def default_num_ctas(mode: int, device: int | None = None) -> int:
     dev = torch.cuda.current_device() if device is None else device
     out = ctypes.c_int32()
@@ -188,7 +202,8 @@ class PagedAttention:
         needs the region: status 0x303 otherwise); a decode with pages of one or two tokens may gather the
         exponents into a temporary tensor. sink:
         float32 [H_qo] on the device, one extra softmax logit per query head
-        without a value row (the attention-sink variant), or None."""
+        without a value row (the attention-sink variant), or None. out and lse,
+        where the call makes them, belong to `stream`."""
         if self.info is None:
             raise RuntimeError("plan() must be called before run()")
         if k_exp is not None or v_exp is not None:
@@ -203,9 +218,9 @@ class PagedAttention:
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(D)
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(stream, lambda: torch.empty_like(q))
         if lse is None and return_lse:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+            lse = _new(stream, lambda: torch.empty(q.shape[:2], dtype=torch.float32, device=q.device))
         dev = self.device
         fp8 = k_pages.dtype == torch.float8_e4m3fn
         if fp8 and (self.mode != N.BSP_MODE_DECODE or self.dtype != torch.bfloat16):
@@ -250,7 +265,7 @@ class PagedAttention:
         ref, fn, region, nbytes, ws = self._fp8_plan or self._look_at_fp8_plan()
         q_p = _addr(q, "q", torch.bfloat16, dev)
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(stream, lambda: torch.empty_like(q))
             out_p = out.data_ptr()
         else:
             if out.shape != q_shape:
@@ -262,7 +277,7 @@ class PagedAttention:
                 raise ValueError("lse must be [n_tokens, H_qo]")
             lse_p = _addr(lse, "lse", torch.float32, dev)
         elif return_lse:
-            lse = torch.empty(q_shape[:2], dtype=torch.float32, device=dev)
+            lse = _new(stream, lambda: torch.empty(q_shape[:2], dtype=torch.float32, device=dev))
             lse_p = lse.data_ptr()
         if sm_scale is None:
             sm_scale = self._default_scale
@@ -360,9 +375,9 @@ def merge_state(o_a: torch.Tensor, lse_a: torch.Tensor, o_b: torch.Tensor, lse_b
     if dt not in _DTYPES:
         raise ValueError("dtype must be bfloat16 or float32")
     if out is None:
-        out = torch.empty_like(o_a)
+        out = _new(stream, lambda: torch.empty_like(o_a))
     if lse_out is None:
-        lse_out = torch.empty_like(lse_a)
+        lse_out = _new(stream, lambda: torch.empty_like(lse_a))
     n, H, D = o_a.shape
     lib = N.load()
     with torch.cuda.device(o_a.device):
@@ -400,6 +415,7 @@ class PageTables:
     [batch + 1], positions [max_new_tokens], counts [4] (table pages, new tokens,
     pages taken, error bits BSP_TABLES_*) and int64 slot_map [max_new_tokens]. The
     int32 arrays are parts of one buffer; to be kept and passed as `out` every step."""
+    is_cuda = True
     _fields = ("kv_indptr", "last_page_len", "kv_indices", "qo_indptr", "slot_map", "positions", "counts")
 
     def __init__(self, batch: int, max_table_pages: int, max_new_tokens: int, device=None):
@@ -420,6 +436,11 @@ class PageTables:
         self._offsets = tuple(4 * offsets[f] for f in ("kv_indptr", "last_page_len", "kv_indices", "qo_indptr",
                                                        "positions", "counts"))
         self.device = self._ints.device
+
+    def record_stream(self, stream) -> None:
+        """As of a tensor: memory that `stream` uses too."""
+        self._ints.record_stream(stream)
+        self.slot_map.record_stream(stream)
 
     @classmethod
     def empty(cls, batch: int, max_table_pages: int, max_new_tokens: int, device=None) -> "PageTables":
@@ -454,7 +475,7 @@ def build_page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pa
     if free_pages.dim() != 1 or num_free.numel() != 1:
         raise ValueError("free_pages must be one-dimensional and num_free hold one value")
     if out is None:
-        out = PageTables(B, max_table_pages, max_new_tokens, dev)
+        out = _new(stream, lambda: PageTables(B, max_table_pages, max_new_tokens, dev))
     elif out.sizes != (B, max_table_pages, max_new_tokens) or out.device != dev:
         raise ValueError(f"out is for {out.sizes} (batch, pages, tokens) on {out.device}")
     if B <= 1:
