@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
         // `lane + 32` of the half into byte offsets of their rows (one division
         // each), then every warp instruction copies T = 32 / C whole rows, C =
         // D / 8 chunks of 16 bytes per row, taking the row offsets by shuffle.
-        constexpr int C = D * LY::kElem / 16, T = 32 / C;
+        constexpr int C = D / 8, T = 32 / C;
         constexpr int kHalfTK = kTK / 2;  // tokens of a stage per loader warp
         const bool is_v = warp >= kConsumers + 2;
         const int tok_base = ((warp - kConsumers) & 1) * kHalfTK;
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
 #pragma unroll
                 for (int jj = 0; jj < kJ; ++jj) {
                     const int tok = w.kv_start + t * kTK + tok_base + lane + 32 * jj;
-                    off[jj] = (((uint64_t)pg[jj] * p.page_size + tok % p.page_size) * p.H_kv + w.kv_head) * (D * LY::kElem);
+                    off[jj] = (((uint64_t)pg[jj] * p.page_size + tok % p.page_size) * p.H_kv + w.kv_head) * (D * 2);
                 }
                 if (t + 1 < nt) fetch(t + 1, pg);
                 const int s = k % kStages;

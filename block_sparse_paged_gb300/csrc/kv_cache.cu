@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(256, kF32 ? 2 : 4) append_runs_kernel(const Ap
     const uint32_t after = change & ~((2u << last) - 1u);
     int end = after ? __ffs(after) - 1 : 32;  // lanes [first, end) are this warp's tokens,
     long long tail = 0;                        // and `tail` more tokens behind lane 31
-    if (!after && last < 32) {
+    if (!after) {
         const int pg = __shfl_sync(0xffffffffu, page, 31);
         for (;;) {
             int o;
