@@ -168,3 +168,12 @@ def test_full_size_rows(bsp):
     """64 requests of up to 8192 tokens."""
     b = workloads.batched_decode_bf16()
     check_decode(bsp, b, cache8(b, 237))
+
+
+@pytest.mark.parametrize("ve", [(-117, -117), (-117, -100), (105, 108)])
+@pytest.mark.parametrize("ps", [1, 16])
+def test_exponents_at_the_ends(bsp, ps, ve):
+    """V values next to the ends of fp32's range (the sums of 1500 of them still within it): the outputs' factor,
+    2^(e - 15) of the running maxima, leaves the normal range at the low end and keeps 17 bits."""
+    b = workloads.paged_batch(308, [1, 1], [1500, 70], 16, 2, 128, ps, "bf16", extra_pages=1)
+    check_decode(bsp, b, cache8(b, 308, ve=ve), num_ctas=7)
