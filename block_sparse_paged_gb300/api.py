@@ -111,7 +111,8 @@ class PagedAttention:
     the concatenated KV ranges per CTA, for batches of few, equal tiles).
     The workspace and pinned staging buffer are allocated once, for the
     given bounds; plan() may then be called once per step and run() once per
-    layer, and run() can be captured in a CUDA graph.
+    layer, and run() can be captured in a CUDA graph. Runs of one object share
+    its workspace: one at a time, on one stream or ordered by the caller.
     """
 
     def __init__(self, mode: str, num_qo_heads: int, num_kv_heads: int, head_dim: int, page_size: int,

@@ -130,10 +130,10 @@ constexpr int64_t kRegionPageRows = 1 << 27;  // rows of a page, all heads: the 
 
 // Decode over it gathers the plan's exponents into table order first where pages have one
 // token and a CTA has 2560 tokens or more to work on, or two and twice that. Measured (read
-// by page / gathered first), 64/8 heads, one token: 32 requests x 4096 tokens 70.6 / 55.5 us,
-// 64 x 4585 159 / 124, 48 x 1024 (2587 tokens per CTA) 29.2 / 28.9, 40 x 1024 (2156) 25.9 /
-// 27.2; two: 32 x 4096 (6899) 60.6 / 55.4, 64 x 1024 (3449) 38.4 / 39.7; five: 32 x 4096
-// 51.8 / 55.2.
+// by page / gathered first), 64/8 heads, one token: 32 requests x 4096 tokens 71.7 / 57.1 us,
+// 64 x 4585 163 / 127, 48 x 1024 (2587 tokens per CTA) 31.2 / 29.8, about even at 40 x 1024
+// (2156) 28.5 / 28.0; two: 32 x 4096 (6899) 62.0 / 56.0, 64 x 1024 (3449) 39.6 / 40.2; five:
+// 32 x 4096 53.0 / 56.4.
 constexpr int64_t kGatherTokens = 2560;
 
 // A plan without queries and the NULL pointers of empty tensors: nothing to do.

@@ -43,8 +43,9 @@
 // carried through the ring as bytes; scores times 2^e_k, token weights 2^(s + e_v)
 // against their own running maximum, so that they fit f16 however far exponents lie
 // apart, and lifted by 2^kLift within it, so that many small weights on full codes count
-// beside a large one on small codes. HBM-bound: 64 requests x 4,585 tokens 98-99 us, 6.1 TB/s, 0.90 of the measured
-// copy bandwidth; page size 1 (cp.async) 57 us for 268 MB, exponents gathered first.
+// beside a large one on small codes; rows of Q scaled into f16's range. HBM-bound: 64
+// requests x 4,594 tokens 99-100 us, 6.1 TB/s, 0.89-0.90 of the measured copy bandwidth;
+// page size 1 (cp.async) 57-58 us for 268 MB, exponents gathered first.
 // fp32 kernel: CUDA cores, fp32 throughout, same plan and merge.
 // Reduction kernel: the reduction map's slots of each split output, merged in
 // ascending order with a common maximum (technical review eq 6); used after the
