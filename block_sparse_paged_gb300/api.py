@@ -524,3 +524,124 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pages:
     _call(dev, stream, N.load().bsp_append_kv_fp8, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
           _DTYPES[dtype], n, _addr(slot_map, "slot_map", torch.int64, dev), _addr(k_pages, "k_pages", f8, dev),
           _addr(v_pages, "v_pages", f8, dev), _addr(k_exp, "k_exp", i8, dev), _addr(v_exp, "v_exp", i8, dev), P, ps, H, D)
+
+
+def _table_args(kv_indptr, kv_indices, last_page_len, dev):
+    """(batch, kv_indptr, kv_indices, its entries, last_page_len) of a page table in CSR form on the device."""
+    if kv_indptr.dim() != 1 or kv_indptr.shape[0] < 1 or kv_indices.dim() != 1:
+        raise ValueError("kv_indptr must be [B + 1] and kv_indices one-dimensional")
+    B, i32 = kv_indptr.shape[0] - 1, torch.int32
+    if last_page_len.shape != (B,):
+        raise ValueError(f"last_page_len must be [{B}]")
+    return (B, _addr(kv_indptr, "kv_indptr", i32, dev), _addr(kv_indices, "kv_indices", i32, dev), kv_indices.shape[0],
+            _addr(last_page_len, "last_page_len", i32, dev))
+
+
+def accumulate_weights(q: torch.Tensor, lse: torch.Tensor, k_pages: torch.Tensor, weights: torch.Tensor,
+                       kv_indptr: torch.Tensor, kv_indices: torch.Tensor, last_page_len: torch.Tensor,
+                       qo_indptr: torch.Tensor | None = None, sm_scale: float | None = None, decay: float = 1.0,
+                       k_exp: torch.Tensor | None = None, lam: torch.Tensor | None = None, window_left: int = -1,
+                       logits_soft_cap: float = 0.0, stream=None) -> None:
+    """Each cached token's gathered attention weight, in place, after an attention run (bsp_accumulate_weights):
+    weights = decay * weights + the sum of exp(score - lse) over the queries and query heads that see it; the
+    queries' own keys (the last of each request) start from zero, with decay 0 all do.
+
+    q, lse: as the run got and gave them. k_pages: bfloat16 or float32, or with k_exp (int8 [num_pages, H_kv])
+    float8_e4m3fn. weights: float32 [num_pages, H_kv, page_size]. kv_indptr, kv_indices, last_page_len, qo_indptr:
+    int32 on the device, as build_page_tables gives them (qo_indptr None: one query per request). lam: float32 [H_qo]
+    after run_differential, whose lse is [n_tokens, H_qo, 2]. sm_scale, window_left, logits_soft_cap: the run's."""
+    dev = k_pages.device
+    if q.dim() != 3 or k_pages.dim() != 4:
+        raise ValueError("q must be [n_tokens, H_qo, D] and k_pages [num_pages, page_size, H_kv, D]")
+    (n, Hq, D), (P, ps, H, Dk) = q.shape, k_pages.shape
+    if Dk != D or Hq % H != 0:
+        raise ValueError(f"q has {Hq} heads of {D} values, k_pages {H} of {Dk}")
+    if q.dtype not in _DTYPES:
+        raise ValueError("q must be bfloat16 or float32")
+    if lse.shape != ((n, Hq) if lam is None else (n, Hq, 2)):
+        raise ValueError("lse must be [n_tokens, H_qo], or [n_tokens, H_qo, 2] with lam")
+    if weights.shape != (P, H, ps):
+        raise ValueError(f"weights must be [{P}, {H}, {ps}]")
+    if k_exp is not None and k_exp.shape != (P, H):
+        raise ValueError(f"k_exp must be [{P}, {H}]")
+    if lam is not None and lam.shape != (Hq,):
+        raise ValueError(f"lam must be [{Hq}]")
+    f32 = torch.float32
+    B, indptr, indices, entries, last = _table_args(kv_indptr, kv_indices, last_page_len, dev)
+    if qo_indptr is None:
+        if n < B:
+            raise ValueError(f"q must hold one query for each of the {B} requests")
+    elif qo_indptr.shape != (B + 1,):
+        raise ValueError(f"qo_indptr must be [{B + 1}]")
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D if lam is None else D // 2)
+    problem = N.Problem(N.BSP_MODE_DECODE, Hq, H, D, ps, 1, _DTYPES[q.dtype], int(window_left), float(logits_soft_cap))
+    _call(dev, stream, N.load().bsp_accumulate_weights, ctypes.byref(problem), _addr(q, "q", q.dtype, dev) or None,
+          _addr(lse, "lse", f32, dev) or None, n,
+          _addr(k_pages, "k_pages", torch.float8_e4m3fn if k_exp is not None else q.dtype, dev),
+          None if k_exp is None else _addr(k_exp, "k_exp", torch.int8, dev), P, _addr(weights, "weights", f32, dev), B,
+          None if qo_indptr is None else _addr(qo_indptr, "qo_indptr", torch.int32, dev), indptr, indices or None, entries,
+          last or None, sm_scale, decay, None if lam is None else _addr(lam, "lam", f32, dev))
+
+
+def select_tokens(weights: torch.Tensor, kv_indptr: torch.Tensor, kv_indices: torch.Tensor, last_page_len: torch.Tensor,
+                  budget: torch.Tensor, max_keep: int, sinks: int = 4, recent: int = 32, kept: torch.Tensor | None = None,
+                  new_lens: torch.Tensor | None = None, stream=None):
+    """The tokens to keep (bsp_select_tokens): per request and kv head the min(tokens, budget, max_keep) heaviest, the
+    first `sinks` and the last `recent` before all others, of equal ones the lower position. Returns (kept int32 [B,
+    H_kv, max_keep], ascending positions, -1 behind the last; new_lens int32 [B]); both may be given to be written.
+
+    weights: float32 [num_pages, H_kv, page_size]; budget: int32 [B]; the table as for accumulate_weights."""
+    dev, i32 = weights.device, torch.int32
+    if weights.dim() != 3:
+        raise ValueError("weights must be [num_pages, H_kv, page_size]")
+    P, H, ps = weights.shape
+    B, indptr, indices, entries, last = _table_args(kv_indptr, kv_indices, last_page_len, dev)
+    if budget.shape != (B,):
+        raise ValueError(f"budget must be [{B}]")
+    if max_keep < 0:
+        raise ValueError("max_keep must not be negative")
+    if kept is None:
+        kept = _new(stream, lambda: torch.empty((B, H, max_keep), dtype=i32, device=dev))
+    elif kept.shape != (B, H, max_keep):
+        raise ValueError(f"kept must be [{B}, {H}, {max_keep}]")
+    if new_lens is None:
+        new_lens = _new(stream, lambda: torch.empty((B,), dtype=i32, device=dev))
+    elif new_lens.shape != (B,):
+        raise ValueError(f"new_lens must be [{B}]")
+    _call(dev, stream, N.load().bsp_select_tokens, _addr(weights, "weights", torch.float32, dev), P, ps, H, B, indptr,
+          indices or None, entries, last or None, _addr(budget, "budget", i32, dev) or None, max_keep, sinks, recent,
+          _addr(kept, "kept", i32, dev) or None, _addr(new_lens, "new_lens", i32, dev) or None)
+    return kept, new_lens
+
+
+def compact_cache(kept: torch.Tensor, new_lens: torch.Tensor, kv_indptr: torch.Tensor, kv_indices: torch.Tensor,
+                  last_page_len: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                  weights: torch.Tensor | None = None, k_exp: torch.Tensor | None = None,
+                  v_exp: torch.Tensor | None = None, stream=None) -> None:
+    """The kept tokens' rows (and weights) move to the front of their request's pages, in place and in order
+    (bsp_compact_cache). Afterwards a request has new_lens[b] tokens, and its pages from ceil(new_lens[b] / page_size)
+    on are free. No page may belong to two requests.
+
+    kept, new_lens: as select_tokens gives them. k_pages, v_pages: pools [num_pages, page_size, H_kv, D] of one type;
+    with k_exp, v_exp (int8 [num_pages, H_kv]) e4m3 codes, whose pages take the largest exponent of their rows."""
+    dev, i32 = k_pages.device, torch.int32
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype is not k_pages.dtype:
+        raise ValueError("k_pages / v_pages must be [num_pages, page_size, H_kv, D], of one type")
+    P, ps, H, D = k_pages.shape
+    B, indptr, indices, entries, last = _table_args(kv_indptr, kv_indices, last_page_len, dev)
+    if kept.dim() != 3 or kept.shape[:2] != (B, H) or new_lens.shape != (B,):
+        raise ValueError(f"kept must be [{B}, {H}, max_keep] and new_lens [{B}]")
+    if weights is not None and weights.shape != (P, H, ps):
+        raise ValueError(f"weights must be [{P}, {H}, {ps}]")
+    if (k_exp is None) != (v_exp is None):
+        raise ValueError("k_exp and v_exp are given together")
+    if k_exp is not None and (k_exp.shape != (P, H) or v_exp.shape != (P, H)):
+        raise ValueError(f"k_exp / v_exp must be [{P}, {H}]")
+    dt = torch.float8_e4m3fn if k_exp is not None else k_pages.dtype
+    _call(dev, stream, N.load().bsp_compact_cache, _addr(kept, "kept", i32, dev) or None,
+          _addr(new_lens, "new_lens", i32, dev) or None, kept.shape[2], B, indptr, indices or None, entries, last or None,
+          _addr(k_pages, "k_pages", dt, dev), _addr(v_pages, "v_pages", dt, dev),
+          None if k_exp is None else _addr(k_exp, "k_exp", torch.int8, dev),
+          None if v_exp is None else _addr(v_exp, "v_exp", torch.int8, dev),
+          None if weights is None else _addr(weights, "weights", torch.float32, dev), P, ps, H, D * k_pages.element_size())

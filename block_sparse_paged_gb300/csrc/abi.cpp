@@ -334,6 +334,90 @@ extern "C" int bsp_append_kv_fp8(const void *k, const void *v, int64_t k_token_s
                             slot_map, k_pages, v_pages, k_exp, v_exp, num_pages, page_size, num_kv_heads, stream);
 }
 
+namespace {
+
+// The page table and pool that the eviction calls share.
+int check_table(int32_t batch, const int32_t *kv_indptr, const int32_t *kv_indices, int64_t max_table_pages,
+                const int32_t *last_page_len, int64_t num_pages, int32_t page_size, int32_t num_kv_heads) {
+    if (batch < 0 || batch > 65535) return fail(BSP_ERR_INVALID_ARG, "batch must be in [0, 65535]");
+    if (page_size < 1 || num_kv_heads < 1 || num_pages < 1 || num_pages > INT32_MAX)
+        return fail(BSP_ERR_INVALID_ARG, "page_size and num_kv_heads must be positive, num_pages in [1, 2^31 - 1]");
+    if (max_table_pages < 0 || max_table_pages > INT32_MAX) return fail(BSP_ERR_INVALID_ARG, "max_table_pages must be in [0, 2^31 - 1]");
+    if (num_kv_heads > 32767 || num_pages * page_size >= UINT32_MAX)
+        return fail(BSP_ERR_UNSUPPORTED, "at most 32767 kv heads and 2^32 - 2 slots");
+    if (max_table_pages * page_size / 64 * num_kv_heads >= INT32_MAX)
+        return fail(BSP_ERR_UNSUPPORTED, "the page table is too large: tokens x kv heads must stay below 2^37");
+    if (batch > 0 && (!kv_indptr || !last_page_len || (max_table_pages > 0 && !kv_indices)))
+        return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    return BSP_OK;
+}
+
+}  // namespace
+
+extern "C" int bsp_accumulate_weights(const bsp_problem *problem, const void *q, const float *lse, int64_t n_tokens,
+                                      const void *k_pages, const int8_t *k_exp, int64_t num_pages, float *weights,
+                                      int32_t batch, const int32_t *qo_indptr, const int32_t *kv_indptr,
+                                      const int32_t *kv_indices, int64_t max_table_pages, const int32_t *last_page_len,
+                                      float sm_scale, float decay, const float *lambda, bsp_stream_t stream) {
+    clear_error();
+    if (!problem) return fail(BSP_ERR_INVALID_ARG, "problem is NULL");
+    bsp_problem P = *problem;
+    P.mode = BSP_MODE_DECODE;  // (the mode's own limits say nothing here)
+    if (!check_problem(&P)) return last_code();
+    int rc = check_table(batch, kv_indptr, kv_indices, max_table_pages, last_page_len, num_pages, P.page_size, P.num_kv_heads);
+    if (rc != BSP_OK) return rc;
+    const int D = P.head_dim, g = P.num_qo_heads / P.num_kv_heads;
+    if (P.dtype == BSP_DTYPE_F32 ? (D != 32 && D != 64 && D != 128 && D != 256) : (D != 64 && D != 128))
+        return fail(BSP_ERR_UNSUPPORTED, "weights take head_dim 64 and 128 (bf16) or 32, 64, 128, 256 (fp32)");
+    if (k_exp && (P.dtype != BSP_DTYPE_BF16 || D != 128))
+        return fail(BSP_ERR_UNSUPPORTED, "weights over the 8-bit cache take bf16 queries with head_dim 128");
+    if (lambda && P.dtype != BSP_DTYPE_BF16) return fail(BSP_ERR_UNSUPPORTED, "differential weights are bf16 only");
+    if (!std::isfinite(sm_scale) || !std::isfinite(decay) || decay < 0.f)
+        return fail(BSP_ERR_INVALID_ARG, "sm_scale and decay must be finite, decay >= 0");
+    if (n_tokens < 0 || (n_tokens > 0 && n_tokens > INT32_MAX / g))
+        return fail(BSP_ERR_INVALID_ARG, "n_tokens must be >= 0, and n_tokens x group below 2^31");
+    if (batch == 0 || max_table_pages == 0) return BSP_OK;
+    if (!k_pages || !weights || (n_tokens > 0 && (!q || !lse))) return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    if ((rc = check_aligned16(q, k_pages, nullptr, nullptr, nullptr)) != BSP_OK) return rc;
+    return launch_accumulate_weights(&P, q, lse, n_tokens, k_pages, k_exp, num_pages, weights, batch, qo_indptr, kv_indptr,
+                                     kv_indices, max_table_pages, last_page_len, sm_scale, decay, lambda, stream);
+}
+
+extern "C" int bsp_select_tokens(const float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads,
+                                 int32_t batch, const int32_t *kv_indptr, const int32_t *kv_indices,
+                                 int64_t max_table_pages, const int32_t *last_page_len, const int32_t *budget,
+                                 int32_t max_keep, int32_t sinks, int32_t recent, int32_t *kept, int32_t *new_lens,
+                                 bsp_stream_t stream) {
+    clear_error();
+    int rc = check_table(batch, kv_indptr, kv_indices, max_table_pages, last_page_len, num_pages, page_size, num_kv_heads);
+    if (rc != BSP_OK) return rc;
+    if (max_keep < 0 || sinks < 0 || recent < 0) return fail(BSP_ERR_INVALID_ARG, "max_keep, sinks and recent must be >= 0");
+    if ((int64_t)batch * num_kv_heads > INT32_MAX / 8) return fail(BSP_ERR_UNSUPPORTED, "too many rows (requests x kv heads)");
+    if (batch == 0) return BSP_OK;
+    if (!weights || !budget || !new_lens || (max_keep > 0 && !kept)) return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    return launch_select_tokens(weights, num_pages, page_size, num_kv_heads, batch, kv_indptr, kv_indices, max_table_pages,
+                                last_page_len, budget, max_keep, sinks, recent, kept, new_lens, stream);
+}
+
+extern "C" int bsp_compact_cache(const int32_t *kept, const int32_t *new_lens, int32_t max_keep, int32_t batch,
+                                 const int32_t *kv_indptr, const int32_t *kv_indices, int64_t max_table_pages,
+                                 const int32_t *last_page_len, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
+                                 float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads,
+                                 int32_t row_bytes, bsp_stream_t stream) {
+    clear_error();
+    int rc = check_table(batch, kv_indptr, kv_indices, max_table_pages, last_page_len, num_pages, page_size, num_kv_heads);
+    if (rc != BSP_OK) return rc;
+    if (max_keep < 0) return fail(BSP_ERR_INVALID_ARG, "max_keep must be >= 0");
+    if (row_bytes < 16 || row_bytes % 16 != 0) return fail(BSP_ERR_INVALID_ARG, "row_bytes must be a positive multiple of 16");
+    if ((k_exp == nullptr) != (v_exp == nullptr)) return fail(BSP_ERR_INVALID_ARG, "k_exp and v_exp are given together");
+    if (k_exp && row_bytes != 128) return fail(BSP_ERR_UNSUPPORTED, "the e4m3 cache has head_dim 128");
+    if (batch == 0 || max_keep == 0 || max_table_pages == 0) return BSP_OK;
+    if (!kept || !new_lens || !k_pages || !v_pages) return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    if ((rc = check_aligned16(nullptr, k_pages, v_pages, nullptr, nullptr)) != BSP_OK) return rc;
+    return launch_compact_cache(kept, new_lens, max_keep, batch, kv_indptr, kv_indices, max_table_pages, last_page_len,
+                                k_pages, v_pages, k_exp, v_exp, weights, num_pages, page_size, num_kv_heads, row_bytes, stream);
+}
+
 extern "C" int bsp_check_device_error(const bsp_plan_info *plan, void *workspace, bsp_stream_t stream,
                                       int32_t *word_out) {
     clear_error();

@@ -118,5 +118,21 @@ int launch_append_kv(const void *k, const void *v, int64_t k_token_stride, int64
                      int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t n_tokens,
                      const int64_t *slot_map, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
                      int64_t num_pages, int32_t page_size, int32_t num_kv_heads, cudaStream_t stream);
+// Gathered attention weights: update, choice of the tokens to keep, move of their rows (arguments as in
+// bsp_accumulate_weights, bsp_select_tokens and bsp_compact_cache, checked; batch > 0).
+int launch_accumulate_weights(const bsp_problem *problem, const void *q, const float *lse, int64_t n_tokens,
+                              const void *k_pages, const int8_t *k_exp, int64_t num_pages, float *weights, int32_t batch,
+                              const int32_t *qo_indptr, const int32_t *kv_indptr, const int32_t *kv_indices,
+                              int64_t max_table_pages, const int32_t *last_page_len, float sm_scale, float decay,
+                              const float *lambda, cudaStream_t stream);
+int launch_select_tokens(const float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t batch,
+                         const int32_t *kv_indptr, const int32_t *kv_indices, int64_t max_table_pages,
+                         const int32_t *last_page_len, const int32_t *budget, int32_t max_keep, int32_t sinks,
+                         int32_t recent, int32_t *kept, int32_t *new_lens, cudaStream_t stream);
+int launch_compact_cache(const int32_t *kept, const int32_t *new_lens, int32_t max_keep, int32_t batch,
+                         const int32_t *kv_indptr, const int32_t *kv_indices, int64_t max_table_pages,
+                         const int32_t *last_page_len, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
+                         float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t row_bytes,
+                         cudaStream_t stream);
 
 }  // namespace bsp

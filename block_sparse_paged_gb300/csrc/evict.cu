@@ -1,0 +1,822 @@
+// Eviction of cached tokens by the attention weight that they gathered (no counterpart on
+// the pages): the weights' update after an attention run, the choice of the tokens to keep,
+// and the move of their rows to the front of their request's pages.
+//
+// Gathered weights: float [num_pages][H_kv][page_size], one per cached token and kv head.
+// Requests come as a page table in CSR form on the device (kv_indptr, kv_indices,
+// last_page_len), as bsp_build_page_tables writes it; nothing is planned on the host.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+
+#include "bsp_internal.h"
+#include "device_common.cuh"
+#include "sm100.cuh"
+
+namespace bsp {
+namespace {
+
+using namespace dev;
+namespace cg = cooperative_groups;
+
+constexpr uint32_t kNoRow = ~0u;  // a token that is not there, or whose page id is outside the pool
+
+// The page table of a batch. Values out of range are read as the nearest in range, so that a
+// malformed table reads and writes nothing outside the arrays.
+struct Csr {
+    const int32_t *kv_indptr, *kv_indices, *last_page_len;
+    int max_pages;  // entries of kv_indices
+    int batch, ps, num_pages;
+};
+
+struct Request {
+    int p0, len;  // first table entry, tokens
+};
+
+__device__ __forceinline__ int clamp_page(const Csr &c, int i) { return min(max(__ldg(c.kv_indptr + i), 0), c.max_pages); }
+
+__device__ __forceinline__ Request request(const Csr &c, int b) {
+    const int p0 = clamp_page(c, b), n = clamp_page(c, b + 1) - p0;
+    const int last = min(max(__ldg(c.last_page_len + b), 0), c.ps);
+    return {p0, n > 0 ? (int)min((long long)(n - 1) * c.ps + last, (long long)INT_MAX) : 0};
+}
+
+// Slot of token t of a request, or kNoRow (host: num_pages * ps < 2^32 - 1).
+__device__ __forceinline__ uint32_t slot_of(const Csr &c, const Request &r, int t, int &page, int &place) {
+    const int col = t / c.ps;
+    place = t - col * c.ps;
+    page = __ldg(c.kv_indices + r.p0 + col);
+    return (unsigned)page < (unsigned)c.num_pages ? (uint32_t)page * (uint32_t)c.ps + (uint32_t)place : kNoRow;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^e for e in [-149, 127]
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float(e >= -126 ? (e + 127) << 23 : 0x00400000 >> (-127 - e)); }
+
+// ---------------------------------------------------------------- gathered weights
+// For each key j of a request and kv head h:
+//   w[j, h] = base + sum over queries i that see j, heads r of h: p,   p = exp(s_ijr - LSE_ir)
+// (differential: p = |p1 - lam_r p2|), base = decay * w[j, h], or 0 for the last qo_len keys,
+// the queries' own. Every key is summed by one thread group in one order: no atomics, the
+// same result every time.
+struct WeightsParams {
+    Csr csr;
+    const int32_t *qo_indptr;  // or null: one query per request
+    const void *q, *k;
+    const float *lse, *lam;
+    const int8_t *k_exp;
+    float *weights;
+    int n_tokens, H_qo, H_kv, g;
+    float scale_log2, cap_in, cap_out, decay;
+    int soft_cap_on, window;
+};
+
+// Virtual blocks of kTaskTokens tokens: request b's begin at floor(kv_indptr[b] * ps / kTaskTokens) + b,
+// which leaves room for ceil(len / kTaskTokens) of them without a prefix sum over the requests.
+constexpr int kTaskTokens = 64;
+
+__device__ __forceinline__ long long block_start(const Csr &c, int b) {
+    return (long long)clamp_page(c, b) * c.ps / kTaskTokens + b;
+}
+
+// A warp: the request of virtual block x (the last that begins at or before it).
+__device__ __forceinline__ int find_request(const Csr &c, long long x, int lane) {
+    int lo = 0, hi = c.batch;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, m = lo + (lane + 1) * step;
+        const unsigned le = __ballot_sync(0xffffffffu, m < hi && block_start(c, m) <= x);
+        lo += __popc(le) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+struct Queries {
+    int q0, n;  // first row of q, queries of the request
+};
+
+__device__ __forceinline__ Queries queries(const WeightsParams &p, int b) {
+    if (!p.qo_indptr) return {min(b, p.n_tokens), b < p.n_tokens ? 1 : 0};
+    const int a = min(max(__ldg(p.qo_indptr + b), 0), p.n_tokens), e = min(max(__ldg(p.qo_indptr + b + 1), a), p.n_tokens);
+    return {a, e - a};
+}
+
+// bf16 pools (and e4m3 ones with exponents): a warp takes 64 keys of one kv head. K rows go
+// straight from memory into the fragments of S = K Q^T (m16n8k16: keys on the M side, queries
+// on the N side): the order of the head dimension inside a product is free, so that a lane's
+// 16 adjacent bytes of a row are fragment words as they are, and q rows are read the same way.
+// Bound by the read of K: no shared memory, no barriers, 8 KB per warp in flight.
+template <int D, bool kE4m3, bool kDiff>
+__global__ void __launch_bounds__(256, 2) weights_kernel(const WeightsParams p) {
+    constexpr int kRow = D * (kE4m3 ? 1 : 2);   // bytes of a K row
+    constexpr int kJ = kRow / 64;               // 16-byte chunks of a row per lane
+    constexpr int kRows = kJ >= 4 ? 4 : 8;      // rows of a lane in flight
+    constexpr int kSteps = D / 16;              // k16 steps of the product
+    constexpr int kCols = kDiff ? 4 : 8;        // (query, head) pairs per column tile
+    const int lane = threadIdx.x & 31, c = lane & 3, n = lane >> 2;
+    const int H = p.H_kv, g = p.g;
+    const long long blocks = block_start(p.csr, p.csr.batch);
+    const long long nwarps = (long long)gridDim.x * (blockDim.x >> 5);
+    for (long long task = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); task < blocks * H; task += nwarps) {
+        const long long blk = task / H;
+        const int h = (int)(task - blk * H);
+        const int b = find_request(p.csr, blk, lane);
+        const Request rq = request(p.csr, b);
+        const long long first = (blk - block_start(p.csr, b)) * kTaskTokens;
+        if (first >= rq.len) continue;
+        const int t0 = (int)first;
+        const Queries qs = queries(p, b);
+        const int off = rq.len - qs.n;  // position of the first query
+        // this lane's own tokens (to look up and to write): t0 + n + 8 c and 32 further
+        uint32_t slot[2];
+        float *at[2];
+        float old[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int t = t0 + n + 8 * c + 32 * u;
+            int page = 0, place = 0;
+            slot[u] = t < rq.len ? slot_of(p.csr, rq, t, page, place) : kNoRow;
+            at[u] = p.weights + ((size_t)page * H + h) * p.csr.ps + place;
+            old[u] = slot[u] != kNoRow && t < off && p.decay != 0.f ? *at[u] : 0.f;
+        }
+        const uint8_t *kb = static_cast<const uint8_t *>(p.k) + (size_t)h * kRow + c * 16;
+        const size_t row_stride = (size_t)H * kRow;
+        // columns (query i, head r) = i * g + r that any of the 64 keys can see
+        const int i_lo = max(0, t0 - off), i_hi = p.window > 0 ? (int)min((long long)qs.n, (long long)t0 + 64 + p.window - off) : qs.n;
+        const int col_lo = i_lo * g / kCols * kCols, col_hi = i_hi * g;  // (host: n_tokens * g < 2^31)
+        float own[2] = {0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 8 / kRows; ++half) {
+            uint4 kw[kRows][kJ];
+            float kf[kRows];
+            int tok[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int ii = half * kRows + i;  // row n + 8 ii
+                const uint32_t s = __shfl_sync(0xffffffffu, slot[ii >> 2], (lane & ~3) | (ii & 3));
+                tok[i] = t0 + n + 8 * ii;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+                    kw[i][j] = s != kNoRow ? __ldg(reinterpret_cast<const uint4 *>(kb + (size_t)s * row_stride + j * 64)) : make_uint4(0, 0, 0, 0);
+                kf[i] = 1.f;
+                if (kE4m3) kf[i] = s != kNoRow ? pow2i(__ldg(p.k_exp + (size_t)(s / (uint32_t)p.csr.ps) * H + h)) : 0.f;
+            }
+            float sum[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) sum[i] = 0.f;
+            for (int col = col_lo; col < col_hi; col += kCols) {
+                // this lane's column of Q^T, n: its query row, and the half of it (differential)
+                const int cn = col + (kDiff ? n >> 1 : n);
+                const int qi = cn / g, r = cn - qi * g;
+                const bool in = cn < col_hi;
+                const size_t qrow = (size_t)(qs.q0 + (in ? qi : 0)) * p.H_qo + (size_t)h * g + (in ? r : 0);
+                float lse2 = in ? __ldg(p.lse + (kDiff ? 2 * qrow + (n & 1) : qrow)) : -INFINITY;
+                const bool live = lse2 != -INFINITY;
+                lse2 *= kLog2e;
+                const float lam = kDiff ? (in ? __ldg(p.lam + h * g + r) : 0.f) : 0.f;
+                float scale = p.soft_cap_on ? p.cap_in : p.scale_log2;
+                uint32_t qf[kSteps][2];
+                const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + qrow * D) + (kE4m3 ? 2 * c : c);
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const bool mine = in && (!kDiff || (j >= kJ / 2) == (n & 1));
+#pragma unroll
+                    for (int e = 0; e < (kE4m3 ? 2 : 1); ++e) {
+                        const uint4 x = mine ? __ldg(qp + j * (kE4m3 ? 8 : 4) + e) : make_uint4(0, 0, 0, 0);
+                        const int st = kE4m3 ? 4 * j + 2 * e : 2 * j;
+                        qf[st][0] = x.x; qf[st][1] = x.y;
+                        qf[st + 1][0] = x.z; qf[st + 1][1] = x.w;
+                    }
+                }
+                if constexpr (kE4m3) {
+                    // bf16 -> f16: the row times the power of two that takes its largest value to
+                    // 2^14 .. 2^15 (values from 2^-31 of the largest on are exact); rows with an
+                    // infinity or NaN as they are
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int st = 0; st < kSteps; ++st)
+                        mx = __vmaxu2(mx, __vmaxu2(qf[st][0] & 0x7fff7fffu, qf[st][1] & 0x7fff7fffu));
+                    mx = max(mx & 0xffffu, mx >> 16);
+                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const int E = (int)(mx >> 7), up = E == 255 ? 0 : min(120, 141 - E);
+                    const float f = pow2i(up);
+#pragma unroll
+                    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float lo = bf16_lo(qf[st][e]) * f, hi = bf16_hi(qf[st][e]) * f;
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(qf[st][e]) : "f"(hi), "f"(lo));
+                        }
+                    scale *= pow2i(-up);
+                }
+                // of the columns 2c and 2c + 1 of the product
+                float lc[2], sc[2];
+                int pos[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int from = 4 * (2 * c + e);
+                    lc[e] = __shfl_sync(0xffffffffu, lse2, from);
+                    sc[e] = __shfl_sync(0xffffffffu, scale, from);
+                    const int i = __shfl_sync(0xffffffffu, qi, from);
+                    const bool l = __shfl_sync(0xffffffffu, (int)live, from);
+                    pos[e] = l ? off + i : -1;  // keys up to this place; -1: no key
+                }
+                const float lm = kDiff ? __shfl_sync(0xffffffffu, lam, 8 * c) : 0.f;
+#pragma unroll
+                for (int sb = 0; sb < kRows / 2; ++sb) {
+                    float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) {
+                        const uint4 x = kw[2 * sb][j], y = kw[2 * sb + 1][j];
+                        if constexpr (kE4m3) {
+                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                uint32_t a[4];
+                                e4m3x4_to_f16x4(xs[w], a[0], a[2]);
+                                e4m3x4_to_f16x4(ys[w], a[1], a[3]);
+                                mma_f16_16816(d[w & 1], a, qf[4 * j + w][0], qf[4 * j + w][1]);
+                            }
+                        } else {
+                            const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+                            mma_bf16_16816(d[0], a0, qf[2 * j][0], qf[2 * j][1]);
+                            mma_bf16_16816(d[1], a1, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {  // rows n + 8 (2 sb + i)
+                        const int row = 2 * sb + i, t = tok[row];
+                        float pe[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = (d[0][2 * i + e] + d[1][2 * i + e]) * (kE4m3 ? sc[e] * kf[row] : sc[e]);
+                            if (p.soft_cap_on) x = tanh_ex2(x) * p.cap_out;
+                            const bool see = t <= pos[e] && (p.window <= 0 || t >= pos[e] - p.window);
+                            pe[e] = see ? ex2(x - lc[e]) : 0.f;
+                        }
+                        sum[row] += kDiff ? fabsf(pe[0] - lm * pe[1]) : pe[0] + pe[1];
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+                sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+                const int ii = half * kRows + i;
+                if ((ii & 3) == c) own[ii >> 2] = sum[i];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (slot[u] != kNoRow) *at[u] = fmaf(p.decay, old[u], own[u]);
+    }
+}
+
+// fp32 pools: a warp takes 64 keys, eight at a time (8 lanes per row, two rows a lane group),
+// fp32 products on the CUDA cores.
+template <int D>
+__global__ void __launch_bounds__(256) weights_f32_kernel(const WeightsParams p) {
+    constexpr int kJ = D / 32;
+    const int lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3;
+    const int H = p.H_kv, g = p.g;
+    const long long blocks = block_start(p.csr, p.csr.batch);
+    const long long nwarps = (long long)gridDim.x * (blockDim.x >> 5);
+    for (long long task = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); task < blocks * H; task += nwarps) {
+        const long long blk = task / H;
+        const int h = (int)(task - blk * H);
+        const int b = find_request(p.csr, blk, lane);
+        const Request rq = request(p.csr, b);
+        const long long first = (blk - block_start(p.csr, b)) * kTaskTokens;
+        if (first >= rq.len) continue;
+        const Queries qs = queries(p, b);
+        const int off = rq.len - qs.n;
+        for (int t0 = (int)first; t0 < min(rq.len, (int)first + kTaskTokens); t0 += 8) {
+            float4 kw[2][kJ];
+            uint32_t slot[2];
+            int tok[2], page[2] = {0, 0}, place[2] = {0, 0};
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                tok[u] = t0 + sub + 4 * u;
+                slot[u] = tok[u] < rq.len ? slot_of(p.csr, rq, tok[u], page[u], place[u]) : kNoRow;
+                const float4 *kr = reinterpret_cast<const float4 *>(static_cast<const float *>(p.k) + ((size_t)(slot[u] != kNoRow ? slot[u] : 0) * H + h) * D) + l8;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) kw[u][j] = slot[u] != kNoRow ? __ldg(kr + 8 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            const int i_lo = max(0, t0 - off), i_hi = p.window > 0 ? (int)min((long long)qs.n, (long long)t0 + 8 + p.window - off) : qs.n;
+            for (int i = i_lo; i < i_hi; ++i)
+                for (int r = 0; r < g; ++r) {
+                    const size_t qrow = (size_t)(qs.q0 + i) * p.H_qo + (size_t)h * g + r;
+                    const float4 *qp = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + qrow * D) + l8;
+                    const float lse = __ldg(p.lse + qrow);
+                    float d[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) {
+                        const float4 x = __ldg(qp + 8 * j);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            d[u] = fmaf(x.x, kw[u][j].x, fmaf(x.y, kw[u][j].y, fmaf(x.z, kw[u][j].z, fmaf(x.w, kw[u][j].w, d[u]))));
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1) d[u] += __shfl_xor_sync(0xffffffffu, d[u], o);
+                        const float x = p.soft_cap_on ? tanh_ex2(d[u] * p.cap_in) * p.cap_out : d[u] * p.scale_log2;
+                        const bool see = tok[u] <= off + i && (p.window <= 0 || tok[u] >= off + i - p.window) && lse != -INFINITY;
+                        if (see) sum[u] += exp2f(x - lse * kLog2e);
+                    }
+                }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (slot[u] != kNoRow && l8 == 0) {
+                    float *at = p.weights + ((size_t)page[u] * H + h) * p.csr.ps + place[u];
+                    const float old = tok[u] < off && p.decay != 0.f ? *at : 0.f;
+                    *at = fmaf(p.decay, old, sum[u]);
+                }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- choice of the tokens to keep
+// Per (request, kv head) the n = min(tokens, budget, max_keep) tokens of the largest weights,
+// protected ones (the first `sinks`, the last `recent`) counting as +inf, NaN as -inf, equal
+// weights by the lower position; written as ascending positions. A radix selection of the n-th
+// largest key over 11 + 11 + 10 bits, then one stable compaction. A cluster of CTAs takes one
+// row of tokens, a contiguous part each, its keys in shared memory (those beyond kKeys are read
+// again in every pass); histograms and counts are read from the other CTAs' shared memory.
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+
+struct SelectParams {
+    Csr csr;
+    const float *weights;
+    const int32_t *budget;
+    int32_t *kept, *new_lens;
+    int H, max_keep, sinks, recent;
+    int cap_keys;  // keys that a CTA's shared memory holds
+};
+
+struct SelectShared {
+    int hist[3][kBins];
+    int counts[2];           // keys above the threshold and equal to it, this CTA
+    int warp_sum[kSelWarps], warp_eq[kSelWarps];
+    int digit, above;
+};
+
+// Order-preserving whole number of a weight
+__device__ __forceinline__ uint32_t order_key(float x) {
+    if (x != x) x = -INFINITY;
+    const uint32_t u = __float_as_uint(x + 0.f);  // -0 counts as 0
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+    extern __shared__ __align__(16) uint8_t sel_smem[];
+    SelectShared &sh = *reinterpret_cast<SelectShared *>(sel_smem);
+    uint32_t *keys = reinterpret_cast<uint32_t *>(sel_smem + sizeof(SelectShared));
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.x / C, b = row / p.H, h = row - b * p.H;
+    const Request rq = request(p.csr, b);
+    const int n = min(min(rq.len, max(__ldg(p.budget + b), 0)), p.max_keep);
+    int32_t *kept = p.kept + (size_t)row * p.max_keep;
+    if (h == 0 && rank == 0 && tid == 0) p.new_lens[b] = n;
+    const int gt = rank * kSelThreads + tid, gn = C * kSelThreads;
+    for (int j = n + gt; j < p.max_keep; j += gn) kept[j] = -1;
+    if (n == rq.len || n == 0) {  // the same for the whole cluster
+        for (int j = gt; j < n; j += gn) kept[j] = j;
+        return;
+    }
+    const int part = ((rq.len + C - 1) / C + 31) & ~31;  // tokens per CTA
+    const int t_lo = min(rank * part, rq.len), t_hi = min(t_lo + part, rq.len), m = t_hi - t_lo;
+    auto read_key = [&](int t) -> uint32_t {
+        if (t < p.sinks || t >= rq.len - p.recent) return order_key(INFINITY);
+        int page, place;
+        const uint32_t s = slot_of(p.csr, rq, t, page, place);
+        return order_key(s != kNoRow ? __ldg(p.weights + ((size_t)page * p.H + h) * p.csr.ps + place) : -INFINITY);
+    };
+    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+    __syncthreads();
+    auto key_at = [&](int i) -> uint32_t { return i < p.cap_keys ? keys[i] : read_key(t_lo + i); };
+
+    uint32_t prefix = 0;
+    int need = n;  // how many of the keys that match the prefix are still to be taken
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        int *hist = sh.hist[pass];
+        for (int i = tid; i < m; i += kSelThreads) {
+            uint32_t k;
+            if (pass == 0) {
+                k = read_key(t_lo + i);
+                if (i < p.cap_keys) keys[i] = k;
+            } else {
+                k = key_at(i);
+                if ((k >> (shift + bits)) != prefix) continue;
+            }
+            atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+        }
+        if (C > 1) cl.sync();
+        else __syncthreads();
+        // four bins per thread, the highest first
+        int cnt[4], mine = 0;
+        const int hi_bin = (kBins - 1) - 4 * tid;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            cnt[i] = 0;
+            if (C > 1) {
+                for (int r = 0; r < C; ++r) cnt[i] += *cl.map_shared_rank(hist + hi_bin - i, r);
+            } else {
+                cnt[i] = hist[hi_bin - i];
+            }
+            mine += cnt[i];
+        }
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        if (lane == 31) sh.warp_sum[warp] = inc;
+        __syncthreads();
+        int before = inc - mine;
+        for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+        if (before < need && before + mine >= need) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (before < need && before + cnt[i] >= need) {
+                    sh.digit = hi_bin - i;
+                    sh.above = before;
+                }
+                before += cnt[i];
+            }
+        }
+        __syncthreads();
+        prefix = (prefix << bits) | (uint32_t)sh.digit;
+        need -= sh.above;
+        __syncthreads();
+    }
+    // prefix: the n-th largest key; `need` of those equal to it are taken, the lowest positions
+    const int seg = ((m + kSelWarps - 1) / kSelWarps + 31) & ~31;
+    const int s_lo = min(warp * seg, m), s_hi = min(s_lo + seg, m);
+    int n_gt = 0, n_eq = 0;
+    for (int i0 = s_lo; i0 < s_hi; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < s_hi ? key_at(i) : 0u;
+        n_gt += __popc(__ballot_sync(0xffffffffu, i < s_hi && k > prefix));
+        n_eq += __popc(__ballot_sync(0xffffffffu, i < s_hi && k == prefix));
+    }
+    if (lane == 0) {
+        sh.warp_sum[warp] = n_gt;
+        sh.warp_eq[warp] = n_eq;
+    }
+    __syncthreads();
+    int above = 0, equal = 0, all_above = 0, all_equal = 0;
+    for (int w = 0; w < kSelWarps; ++w) {
+        if (w == warp) { above = all_above; equal = all_equal; }
+        all_above += sh.warp_sum[w];
+        all_equal += sh.warp_eq[w];
+    }
+    if (C > 1) {
+        if (tid == 0) {
+            sh.counts[0] = all_above;
+            sh.counts[1] = all_equal;
+        }
+        cl.sync();
+        for (int r = 0; r < rank; ++r) {
+            above += *cl.map_shared_rank(&sh.counts[0], r);
+            equal += *cl.map_shared_rank(&sh.counts[1], r);
+        }
+        cl.sync();  // nobody's shared memory is read behind this
+    }
+    for (int i0 = s_lo; i0 < s_hi; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < s_hi ? key_at(i) : 0u;
+        const bool is_gt = i < s_hi && k > prefix, is_eq = i < s_hi && k == prefix;
+        const unsigned mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
+        const unsigned lt = (1u << lane) - 1;
+        const int g = above + __popc(mg & lt), e = equal + __popc(me & lt);
+        if (is_gt || (is_eq && e < need)) kept[g + min(e, need)] = t_lo + i;
+        above += __popc(mg);
+        equal += __popc(me);
+    }
+}
+
+// ---------------------------------------------------------------- the move of the kept rows
+// Row kept[j] of a request and kv head goes to place j. Places ascend, so kept[j] >= j: tiles of
+// rows taken in order never overwrite a row that a later tile reads, and inside a tile every row
+// is read before the first is written. One CTA takes one stream of rows: (request, kv head,
+// 128-byte slice of K or V, or the weights).
+constexpr int kMoveThreads = 256;
+constexpr int kMoveTile = 256;                       // rows per tile
+constexpr int kMoveU = kMoveTile * 8 / kMoveThreads; // 16-byte pieces of a tile per thread
+constexpr int kChunkRows = 16384;                    // e4m3: rows whose factors shared memory holds
+static_assert(kMoveTile == kMoveThreads, "a thread looks up one row of a tile");
+
+struct MoveParams {
+    Csr csr;
+    const int32_t *kept, *new_lens;
+    uint8_t *k, *v;
+    int8_t *k_exp, *v_exp;
+    float *weights;
+    int H, max_keep, row_bytes, slices;
+};
+
+// Source and destination slots of row j, or kNoRow where nothing moves. (A position below j, one
+// behind the request, or a page outside the pool: the row stays.)
+__device__ __forceinline__ void move_slots(const Csr &c, const Request &rq, const int32_t *kept, int j, bool in_place,
+                                           uint32_t &src, uint32_t &dst) {
+    const int i = __ldg(kept + j);
+    src = dst = kNoRow;
+    if (i < j || i >= rq.len || (i == j && !in_place)) return;
+    int page, place;
+    const uint32_t s = slot_of(c, rq, i, page, place), d = slot_of(c, rq, j, page, place);
+    if (s != kNoRow && d != kNoRow) {
+        src = s;
+        dst = d;
+    }
+}
+
+__device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float s) {
+    uint32_t h0, h1;
+    e4m3x4_to_f16x4(w, h0, h1);
+    const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&h0)), b = __half22float2(*reinterpret_cast<__half2 *>(&h1));
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(a.y * s), "f"(a.x * s));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(b.y * s), "f"(b.x * s));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// kExp: e4m3 codes with an exponent per (page, kv head). A page's exponent becomes the largest
+// of those that its rows had; codes are scaled by the difference and rounded to nearest even.
+template <bool kExp>
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const MoveParams p) {
+    extern __shared__ int8_t factor[];  // kExp: [kChunkRows] exponents, then factors, of a chunk's rows
+    __shared__ uint32_t s_src[2][kMoveTile], s_dst[2][kMoveTile];
+    const int tid = threadIdx.x, H = p.H, ps = p.csr.ps;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const Request rq = request(p.csr, b);
+    const int n = min(min(max(__ldg(p.new_lens + b), 0), p.max_keep), rq.len);
+    if (n == 0) return;
+    const int32_t *kept = p.kept + ((size_t)b * H + h) * p.max_keep;
+    const int slices = p.slices;
+    if ((int)blockIdx.x == 2 * slices) {
+        // ---- weights: one value per row
+        for (int j0 = 0; j0 < n; j0 += kMoveThreads) {
+            const int j = j0 + tid;
+            uint32_t src = kNoRow, dst = kNoRow;
+            if (j < n) move_slots(p.csr, rq, kept, j, false, src, dst);
+            auto at = [&](uint32_t s) -> size_t { return ((size_t)(s / (uint32_t)ps) * H + h) * ps + s % (uint32_t)ps; };
+            const float x = src != kNoRow ? p.weights[at(src)] : 0.f;
+            __syncthreads();
+            if (src != kNoRow) p.weights[at(dst)] = x;
+            __syncthreads();
+        }
+        return;
+    }
+    const bool is_v = (int)blockIdx.x >= slices;
+    const int slice = (int)blockIdx.x - (is_v ? slices : 0);
+    const int off = slice * 128 + (tid & 7) * 16;  // this thread's piece of a row
+    const bool live = off < p.row_bytes;
+    uint8_t *base = (is_v ? p.v : p.k) + (size_t)h * p.row_bytes + off;
+    const size_t stride = (size_t)H * p.row_bytes;
+    int8_t *exps = is_v ? p.v_exp : p.k_exp;
+    const int chunk = kExp ? kChunkRows / ps * ps : n;  // (host: ps <= kChunkRows)
+    for (int c0 = 0; c0 < n; c0 += chunk) {
+        const int c1 = min(n, c0 + chunk);
+        if constexpr (kExp) {
+            // the rows' exponents, each page's largest, the pages' new exponents. (Pages of this chunk's
+            // places are read by no later chunk: its rows come from places at or behind its own.)
+            for (int j = c0 + tid; j < c1; j += kMoveThreads) {
+                uint32_t src, dst;
+                move_slots(p.csr, rq, kept, j, true, src, dst);
+                int page, place;
+                if (src != kNoRow) factor[j - c0] = exps[(size_t)(src / (uint32_t)ps) * H + h];
+                else factor[j - c0] = slot_of(p.csr, rq, j, page, place) != kNoRow ? exps[(size_t)page * H + h] : (int8_t)-128;  // stays
+            }
+            __syncthreads();
+            for (int q0 = c0 + tid * ps; q0 < c1; q0 += kMoveThreads * ps) {
+                int e = -128;
+                const int q1 = min(q0 + ps, c1);
+                for (int j = q0; j < q1; ++j) e = max(e, (int)factor[j - c0]);
+                for (int j = q0; j < q1; ++j) factor[j - c0] = (int8_t)max((int)factor[j - c0] - e, -100);
+                int page, place;
+                const uint32_t d = slot_of(p.csr, rq, q0, page, place);
+                if (d != kNoRow) exps[(size_t)page * H + h] = (int8_t)e;
+            }
+            __syncthreads();
+        }
+        uint4 x[2][kMoveU];
+        auto look_up = [&](int t, int buf) {
+            const int j = c0 + t * kMoveTile + tid;
+            uint32_t src = kNoRow, dst = kNoRow;
+            if (j < c1) move_slots(p.csr, rq, kept, j, kExp && factor[j - c0] != 0, src, dst);
+            s_src[buf][tid] = src;
+            s_dst[buf][tid] = dst;
+        };
+        auto load = [&](int buf, uint4 (&r)[kMoveU]) {
+#pragma unroll
+            for (int u = 0; u < kMoveU; ++u) {
+                const uint32_t s = s_src[buf][(tid >> 3) + 32 * u];
+                if (live && s != kNoRow) r[u] = *reinterpret_cast<const uint4 *>(base + (size_t)s * stride);
+            }
+        };
+        auto store = [&](int t, int buf, uint4 (&r)[kMoveU]) {
+#pragma unroll
+            for (int u = 0; u < kMoveU; ++u) {
+                const int jl = (tid >> 3) + 32 * u;
+                const uint32_t d = s_dst[buf][jl];
+                if (!live || d == kNoRow) continue;
+                if constexpr (kExp) {
+                    const int f = factor[t * kMoveTile + jl];
+                    if (f != 0) {
+                        const float s = pow2i(f);
+                        r[u].x = rescale_codes(r[u].x, s);
+                        r[u].y = rescale_codes(r[u].y, s);
+                        r[u].z = rescale_codes(r[u].z, s);
+                        r[u].w = rescale_codes(r[u].w, s);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(base + (size_t)d * stride) = r[u];
+            }
+        };
+        const int nt = (c1 - c0 + kMoveTile - 1) / kMoveTile;
+        look_up(0, 0);
+        __syncthreads();
+        load(0, x[0]);
+        if (nt > 1) look_up(1, 1);
+        for (int t = 0; t < nt; t += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (t + u >= nt) break;
+                __syncthreads();  // this tile is read; the next one is looked up
+                if (t + u + 1 < nt) load(u ^ 1, x[u ^ 1]);
+                store(t + u, u, x[u]);
+                __syncthreads();  // its slots are used
+                if (t + u + 2 < nt) look_up(t + u + 2, u);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+int current_sms(int *dev_out = nullptr) {
+    static int sms[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+    if (!sms[dev]) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+        sms[dev] = n;
+    }
+    if (dev_out) *dev_out = dev;
+    return sms[dev];
+}
+
+int launched(const char *what) {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? BSP_OK : fail(BSP_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
+}
+
+Csr make_csr(const int32_t *kv_indptr, const int32_t *kv_indices, const int32_t *last_page_len, int64_t max_pages, int batch,
+             int ps, int64_t num_pages) {
+    return {kv_indptr, kv_indices, last_page_len, (int)max_pages, batch, ps, (int)num_pages};
+}
+
+}  // namespace
+
+int launch_accumulate_weights(const bsp_problem *P, const void *q, const float *lse, int64_t n_tokens, const void *k_pages,
+                              const int8_t *k_exp, int64_t num_pages, float *weights, int32_t batch,
+                              const int32_t *qo_indptr, const int32_t *kv_indptr, const int32_t *kv_indices,
+                              int64_t max_table_pages, const int32_t *last_page_len, float sm_scale, float decay,
+                              const float *lambda, cudaStream_t stream) {
+    WeightsParams p;
+    p.csr = make_csr(kv_indptr, kv_indices, last_page_len, max_table_pages, batch, P->page_size, num_pages);
+    p.qo_indptr = qo_indptr;
+    p.q = q;
+    p.k = k_pages;
+    p.lse = lse;
+    p.lam = lambda;
+    p.k_exp = k_exp;
+    p.weights = weights;
+    p.n_tokens = (int)n_tokens;
+    p.H_qo = P->num_qo_heads;
+    p.H_kv = P->num_kv_heads;
+    p.g = p.H_qo / p.H_kv;
+    p.scale_log2 = sm_scale * kLog2e;
+    p.soft_cap_on = P->logits_soft_cap > 0.f;
+    p.cap_in = p.soft_cap_on ? sm_scale / P->logits_soft_cap : 0.f;
+    p.cap_out = P->logits_soft_cap * kLog2e;
+    p.decay = decay;
+    p.window = P->window_left;
+    const int sms = current_sms();
+    if (sms < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    const int64_t tasks = (max_table_pages * P->page_size / kTaskTokens + batch) * P->num_kv_heads;
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((tasks + 7) / 8, (int64_t)sms * 2));
+    const int D = P->head_dim;
+    if (P->dtype == BSP_DTYPE_F32) {
+        switch (D) {
+            case 32: weights_f32_kernel<32><<<grid, 256, 0, stream>>>(p); break;
+            case 64: weights_f32_kernel<64><<<grid, 256, 0, stream>>>(p); break;
+            case 128: weights_f32_kernel<128><<<grid, 256, 0, stream>>>(p); break;
+            default: weights_f32_kernel<256><<<grid, 256, 0, stream>>>(p); break;
+        }
+    } else if (k_exp) {
+        if (lambda) weights_kernel<128, true, true><<<grid, 256, 0, stream>>>(p);
+        else weights_kernel<128, true, false><<<grid, 256, 0, stream>>>(p);
+    } else if (D == 128) {
+        if (lambda) weights_kernel<128, false, true><<<grid, 256, 0, stream>>>(p);
+        else weights_kernel<128, false, false><<<grid, 256, 0, stream>>>(p);
+    } else {
+        if (lambda) weights_kernel<64, false, true><<<grid, 256, 0, stream>>>(p);
+        else weights_kernel<64, false, false><<<grid, 256, 0, stream>>>(p);
+    }
+    return launched("weights");
+}
+
+int launch_select_tokens(const float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t batch,
+                         const int32_t *kv_indptr, const int32_t *kv_indices, int64_t max_table_pages,
+                         const int32_t *last_page_len, const int32_t *budget, int32_t max_keep, int32_t sinks,
+                         int32_t recent, int32_t *kept, int32_t *new_lens, cudaStream_t stream) {
+    SelectParams p;
+    p.csr = make_csr(kv_indptr, kv_indices, last_page_len, max_table_pages, batch, page_size, num_pages);
+    p.weights = weights;
+    p.budget = budget;
+    p.kept = kept;
+    p.new_lens = new_lens;
+    p.H = num_kv_heads;
+    p.max_keep = max_keep;
+    p.sinks = sinks;
+    p.recent = recent;
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    // CTAs per row: more where rows are few and long
+    const int64_t rows = (int64_t)batch * num_kv_heads, mean = max_table_pages * page_size / batch;
+    int C = 1;
+    while (C < kMaxCluster && rows * C * 2 <= 2 * (int64_t)sms && mean / C >= 4096) C *= 2;
+    p.cap_keys = (int)std::min<int64_t>(40000, std::max<int64_t>(2048, (2 * mean / C + 31) / 32 * 32));
+    const int smem = (int)sizeof(SelectShared) + 4 * p.cap_keys;
+    static bool configured[64] = {false};
+    if (!configured[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("select smem attribute: ") + cudaGetErrorString(e));
+        configured[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * C));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, p);
+    if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("select launch: ") + cudaGetErrorString(e));
+    return launched("select");
+}
+
+int launch_compact_cache(const int32_t *kept, const int32_t *new_lens, int32_t max_keep, int32_t batch,
+                         const int32_t *kv_indptr, const int32_t *kv_indices, int64_t max_table_pages,
+                         const int32_t *last_page_len, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
+                         float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t row_bytes,
+                         cudaStream_t stream) {
+    MoveParams p;
+    p.csr = make_csr(kv_indptr, kv_indices, last_page_len, max_table_pages, batch, page_size, num_pages);
+    p.kept = kept;
+    p.new_lens = new_lens;
+    p.k = static_cast<uint8_t *>(k_pages);
+    p.v = static_cast<uint8_t *>(v_pages);
+    p.k_exp = k_exp;
+    p.v_exp = v_exp;
+    p.weights = weights;
+    p.H = num_kv_heads;
+    p.max_keep = max_keep;
+    p.row_bytes = row_bytes;
+    p.slices = (row_bytes + 127) / 128;
+    const dim3 grid(2 * p.slices + (weights ? 1 : 0), num_kv_heads, batch);
+    if (k_exp) {
+        if (page_size > kChunkRows) return fail(BSP_ERR_UNSUPPORTED, "compacting the 8-bit cache takes pages of at most 16384 tokens");
+        compact_kernel<true><<<grid, kMoveThreads, kChunkRows, stream>>>(p);
+    } else {
+        compact_kernel<false><<<grid, kMoveThreads, 0, stream>>>(p);
+    }
+    return launched("compact");
+}
+
+}  // namespace bsp

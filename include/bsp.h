@@ -519,6 +519,85 @@ size_t bsp_decode_fp8_region_size(const bsp_plan_info *plan);
 size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan);
 
 /*
+ * ---- eviction by gathered attention weight ----------------------------------
+ *
+ * (No counterpart on the pages.) Each cached token has a gathered weight per kv head,
+ * weights float [num_pages, H_kv, page_size]: how much attention it got so far. The loop,
+ * every call stream-ordered, capturable, without host data or scratch:
+ *   attention run               O and LSE of the step's queries
+ *   bsp_accumulate_weights      each key's weight grows by what the queries gave it
+ *   bsp_select_tokens           per request and kv head the tokens to keep
+ *   bsp_compact_cache           their rows move to the front of the request's pages; the
+ *                               caller sets its length to new_lens[b] and frees the pages
+ *                               from ceil(new_lens[b] / page_size) on
+ * Requests come as a page table in CSR form on the device, as bsp_build_page_tables writes
+ * it: kv_indptr int32 [batch + 1], kv_indices int32 [max_table_pages], last_page_len int32
+ * [batch] (tokens of the last page). Values out of range count as the nearest in range, and
+ * tokens of pages outside [0, num_pages) are left out: nothing is read or written outside
+ * the arrays. batch at most 65535, num_pages * page_size below 2^32 - 1.
+ */
+
+/*
+ * Gathered weights after an attention run over the same keys. For every key j of a request
+ * and kv head h
+ *     w[j, h] = base + sum over the queries i that see j and the g query heads r of h
+ *                      of exp(s_ijr - LSE_ir)
+ * with base = decay * w[j, h], or 0 for the request's last qo_len keys, the queries' own
+ * (their slots may hold anything), and for all keys where decay is 0. The sums are fp32, in
+ * one order every time.
+ *   problem      num_qo_heads, num_kv_heads, head_dim, page_size, dtype, window_left and
+ *                logits_soft_cap of the attention run (the other members are not read).
+ *                Queries see keys as under causal = 1 (bottom-right; a decode's query all)
+ *   q, lse       device, as the run got and gave them: [n_tokens, H_qo, D] and float
+ *                [n_tokens, H_qo]. A query with LSE = -inf gives nothing
+ *   k_pages      device, [num_pages, page_size, H_kv, D] in dtype, or with k_exp (int8
+ *                [num_pages, H_kv]) e4m3 codes, D = 128, value = code * 2^exp
+ *   qo_indptr    device, int32 [batch + 1], or NULL: one query per request, in order
+ *   lambda       NULL, or device float [H_qo]: the weights of a differential run
+ *                (bsp_decode_run_diff): lse float [n_tokens, H_qo, 2], and a head gives
+ *                |p1 - lambda p2| of its two maps' weights
+ * Supported: bf16 with D in {64, 128}, fp32 with D in {32, 64, 128, 256} (no lambda).
+ */
+int bsp_accumulate_weights(const bsp_problem *problem, const void *q, const float *lse, int64_t n_tokens,
+                           const void *k_pages, const int8_t *k_exp, int64_t num_pages, float *weights, int32_t batch,
+                           const int32_t *qo_indptr, const int32_t *kv_indptr, const int32_t *kv_indices,
+                           int64_t max_table_pages, const int32_t *last_page_len, float sm_scale, float decay,
+                           const float *lambda, bsp_stream_t stream);
+
+/*
+ * The tokens to keep: per request and kv head the n = min(tokens, max(budget[b], 0),
+ * max_keep) tokens of the largest weights. The first `sinks` and the last `recent` tokens
+ * count as +inf, NaN weights as -inf; of equal weights the lower positions come first.
+ *   budget       device, int32 [batch]
+ *   kept         device, int32 [batch, H_kv, max_keep], written: positions in the request,
+ *                ascending; -1 behind the n-th
+ *   new_lens     device, int32 [batch], written: n
+ */
+int bsp_select_tokens(const float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t batch,
+                      const int32_t *kv_indptr, const int32_t *kv_indices, int64_t max_table_pages,
+                      const int32_t *last_page_len, const int32_t *budget, int32_t max_keep, int32_t sinks,
+                      int32_t recent, int32_t *kept, int32_t *new_lens, bsp_stream_t stream);
+
+/*
+ * The kept tokens' rows of K, V and (weights not NULL) their weights move, in place, to
+ * places 0 .. new_lens[b] - 1 of their request, in the order of kept.
+ *   kept         device, int32 [batch, H_kv, max_keep]: of each row the first new_lens[b]
+ *                positions, strictly ascending (an entry below its own place or not below
+ *                the request's tokens moves nothing)
+ *   row_bytes    bytes of a row of K and of V: D times the element's size, a multiple of 16
+ *   k_exp, v_exp NULL, or the exponents of e4m3 pools (row_bytes 128): a page's exponent
+ *                becomes the largest of those that its kept rows had, and codes are rescaled
+ *                to it (rounded to nearest even)
+ * Rows behind the kept ones stay as they are. Pages that two requests share must not be
+ * compacted: a page belongs to one request of the batch.
+ */
+int bsp_compact_cache(const int32_t *kept, const int32_t *new_lens, int32_t max_keep, int32_t batch,
+                      const int32_t *kv_indptr, const int32_t *kv_indices, int64_t max_table_pages,
+                      const int32_t *last_page_len, void *k_pages, void *v_pages, int8_t *k_exp, int8_t *v_exp,
+                      float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t row_bytes,
+                      bsp_stream_t stream);
+
+/*
  * Decode run without any device allocation by the caller or the library.
  *
  * The paper has no counterpart: this is a convenience of this library. It is

@@ -9,6 +9,7 @@ do. It shares no code with the CUDA path.
 - ``plan.py``: the load-balanced plan in plain Python.
 - ``fp8.py``: values of e4m3 KV codes (for the e4m3 KV-cache decode).
 - ``kv_cache.py``: page tables and the quantising append of the 8-bit cache.
+- ``evict.py``: differential attention, gathered attention weights, tokens to keep, the move of their rows.
 
 ``build()`` compiles ``attention.c`` with gcc into ``liboracle.so`` next to it.
 """
@@ -21,6 +22,7 @@ import subprocess
 import numpy as np
 
 from . import fp8 as fp8  # noqa: F401  (re-export)
+from . import evict as evict  # noqa: F401  (re-export)
 from . import kv_cache as kv_cache  # noqa: F401  (re-export)
 from . import plan as plan  # noqa: F401  (re-export)
 
