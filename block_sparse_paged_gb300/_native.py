@@ -38,6 +38,7 @@ EXPORTED = ["bsp_default_num_ctas", "bsp_workspace_size", "bsp_host_staging_size
             "bsp_decode_run", "bsp_decode_run_fp8", "bsp_prefill_run", "bsp_run_attention", "bsp_run_merge_partials",
             "bsp_merge_state", "bsp_build_page_tables", "bsp_append_kv_fp8", "bsp_decode_run_fp8_block",
             "bsp_prefill_run_fp8_block", "bsp_decode_fp8_region_size", "bsp_prefill_fp8_region_size",
+            "bsp_decode_run_diff", "bsp_prefill_run_diff", "bsp_prefill_diff_region_size",
             "bsp_accumulate_weights", "bsp_select_tokens", "bsp_compact_cache", "bsp_decode_run_static", "bsp_check_device_error", "bsp_check_bounded_wait",
             "bsp_last_error", "bsp_version"]
 
@@ -70,6 +71,11 @@ class PlanInfo(ctypes.Structure):
                 ("off_gather", ctypes.c_uint64), ("gather_pool_bytes", ctypes.c_uint64)]
 
 
+class Differential(ctypes.Structure):
+    _fields_ = [("lam", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p), ("norm_eps", ctypes.c_float),
+                ("out_scale", ctypes.c_float)]
+
+
 # numpy views of the plan's staging image (bsp_work_item, bsp_merge_entry)
 WORK_ITEM_DTYPE = np.dtype([("b", "<i4"), ("tile", "<i4"), ("kv_head", "<i4"), ("kv_start", "<i4"),
                             ("kv_end", "<i4"), ("slot", "<i4"), ("q_tok0", "<i4"), ("n_pos", "<i4"),
@@ -100,6 +106,7 @@ def load():
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     P, C, PI = ctypes.POINTER(Problem), ctypes.POINTER(Capacity), ctypes.POINTER(PlanInfo)
+    DP = ctypes.POINTER(Differential)
     sig = {
         "bsp_default_num_ctas": ([i32, i32, ctypes.POINTER(i32)], ctypes.c_int),
         "bsp_workspace_size": ([P, C], ctypes.c_size_t),
@@ -121,6 +128,9 @@ def load():
         "bsp_prefill_run_fp8_block": ([PI, vp, vp, vp, vp, vp, vp, i64, f32, vp, vp, vp, ctypes.c_size_t, vp, vp],
                                       ctypes.c_int),
         "bsp_prefill_fp8_region_size": ([PI], ctypes.c_size_t),
+        "bsp_decode_run_diff": ([PI, DP, vp, vp, vp, vp, vp, vp, i64, f32, vp, vp, vp, ctypes.c_size_t, vp, vp], ctypes.c_int),
+        "bsp_prefill_run_diff": ([PI, DP, vp, vp, vp, vp, vp, vp, i64, f32, vp, vp, vp, ctypes.c_size_t, vp, vp], ctypes.c_int),
+        "bsp_prefill_diff_region_size": ([PI], ctypes.c_size_t),
         "bsp_accumulate_weights": ([P, vp, vp, i64, vp, vp, i64, vp, i32, vp, vp, vp, i64, vp, f32, f32, vp, vp],
                                    ctypes.c_int),
         "bsp_select_tokens": ([vp, i64, i32, i32, i32, vp, vp, i64, vp, vp, i32, i32, i32, vp, vp, vp], ctypes.c_int),

@@ -109,6 +109,7 @@ class PagedAttention:
     over an e4m3 cache with exponents convert its pages into it.
     schedule: "lpt" (the pages' plan) or "equal" (equal contiguous shares of
     the concatenated KV ranges per CTA, for batches of few, equal tiles).
+    differential: for run_differential instead of run (planned as two maps per head; bfloat16, head_dim 128).
     The workspace and pinned staging buffer are allocated once, for the
     given bounds; plan() may then be called once per step and run() once per
     layer, and run() can be captured in a CUDA graph. Runs of one object share
@@ -119,14 +120,17 @@ class PagedAttention:
                  causal: bool = False, dtype=torch.bfloat16, max_batch: int = 256,
                  max_qo_tokens: int | None = None, num_ctas: int | None = None, device=None,
                  window_left: int = -1, logits_soft_cap: float = 0.0, chunks_per_cta: int = 1,
-                 max_gather_pages: int = 0, schedule: str = "lpt"):
+                 max_gather_pages: int = 0, schedule: str = "lpt", differential: bool = False):
         self.lib = N.load()
         if mode not in ("decode", "prefill"):
             raise ValueError("mode must be 'decode' or 'prefill'")
         self.mode = N.BSP_MODE_DECODE if mode == "decode" else N.BSP_MODE_PREFILL
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.dtype = dtype
-        self.problem = make_problem(self.mode, num_qo_heads, num_kv_heads, head_dim, page_size, causal, dtype,
+        self.differential = bool(differential)
+        if differential and (dtype != torch.bfloat16 or head_dim != 128):
+            raise ValueError("differential attention takes bfloat16 and head_dim 128 (halves of 64)")
+        self.problem = make_problem(self.mode, num_qo_heads * (2 if differential else 1), num_kv_heads, head_dim, page_size, causal, dtype,
                                     window_left, logits_soft_cap)
         if num_ctas is None:
             num_ctas = default_num_ctas(self.mode, self.device.index)
@@ -144,7 +148,7 @@ class PagedAttention:
         self.staging = torch.zeros(st_bytes, dtype=torch.uint8, pin_memory=True)
         self._copied = None  # event after the last plan copy
         self._q_tail, self._page_tail = (num_qo_heads, head_dim), (page_size, num_kv_heads, head_dim)
-        self._default_scale = 1.0 / math.sqrt(head_dim)
+        self._default_scale = 1.0 / math.sqrt(head_dim // 2 if differential else head_dim)
         self.info = self._fp8_plan = self._fp8_shapes = None  # of the current plan
         self._sink_on = False  # its info points to a sink
 
@@ -207,6 +211,8 @@ class PagedAttention:
         where the call makes them, belong to `stream`."""
         if self.info is None:
             raise RuntimeError("plan() must be called before run()")
+        if self.differential:
+            raise RuntimeError("a differential object runs by run_differential()")
         if k_exp is not None or v_exp is not None:
             return self._run_fp8_block(q, k_pages, v_pages, k_exp, v_exp, kv_indices, sm_scale, out, lse, stream,
                                        return_lse, k_scale, v_scale, sink)
@@ -321,6 +327,75 @@ class PagedAttention:
         self._fp8_plan = (ref, fn, region, nbytes, ws)
         return self._fp8_plan
 
+    def run_differential(self, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, kv_indices: torch.Tensor,
+                         lam: torch.Tensor, sm_scale: float | None = None, norm_weight: torch.Tensor | None = None,
+                         norm_eps: float = 1e-5, out_scale: float = 1.0, out: torch.Tensor | None = None,
+                         lse: torch.Tensor | None = None, stream=None, return_lse: bool = True,
+                         k_exp: torch.Tensor | None = None, v_exp: torch.Tensor | None = None):
+        """Differential attention of the planned batch (bsp_decode_run_diff, bsp_prefill_run_diff): rows of q and k are
+        two halves of 64, o = (softmax(q1 k1) - lam softmax(q2 k2)) v, then o / rms(o) * norm_weight where that is given
+        (float32 [128]), times out_scale. lam: float32 [H_qo]. sm_scale: 1 / 8 by default. Returns out [n, H_qo, 128]
+        and lse float32 [n, H_qo, 2]. Pools and kv_indices as for run(): bfloat16, or an 8-bit cache with k_exp and
+        v_exp (a prefill over it converts its pages into a bf16 copy first, in the workspace's copy region where
+        max_gather_pages covers the page table, else in a temporary tensor of this call)."""
+        if self.info is None:
+            raise RuntimeError("plan() must be called before run_differential()")
+        if not self.differential:
+            raise RuntimeError("run_differential() needs an object made with differential=True")
+        dev, info = self.device, self.info
+        if (k_exp is None) != (v_exp is None):
+            raise ValueError("k_exp and v_exp are given together")
+        fp8 = k_exp is not None
+        q_shape, pool = q.shape, k_pages.shape
+        if len(q_shape) != 3 or q_shape[1:] != self._q_tail or q_shape[0] < info.num_qo_tokens:
+            raise ValueError(f"q must be [n_tokens, {self._q_tail[0]}, {self._q_tail[1]}] with the plan's tokens")
+        if len(pool) != 4 or pool[1:] != self._page_tail or v_pages.shape != pool:
+            raise ValueError("k_pages / v_pages must be [num_pages, %d, %d, %d]" % self._page_tail)
+        if fp8 and (k_exp.shape != (pool[0], pool[2]) or v_exp.shape != k_exp.shape):
+            raise ValueError(f"k_exp / v_exp must be [{pool[0]}, {pool[2]}]")
+        if kv_indices.dim() != 1 or kv_indices.shape[0] < info.num_table_pages:
+            raise ValueError(f"kv_indices must hold the plan's {info.num_table_pages} pages")
+        if lam.shape != (q_shape[1],):
+            raise ValueError(f"lam must be [{q_shape[1]}]")
+        if norm_weight is not None and norm_weight.shape != (q_shape[2],):
+            raise ValueError(f"norm_weight must be [{q_shape[2]}]")
+        bf16, f32 = torch.bfloat16, torch.float32
+        kv_dt = torch.float8_e4m3fn if fp8 else bf16
+        q_p, k_p, v_p = _addr(q, "q", bf16, dev), _addr(k_pages, "k_pages", kv_dt, dev), _addr(v_pages, "v_pages", kv_dt, dev)
+        diff = N.Differential(_addr(lam, "lam", f32, dev), None if norm_weight is None else _addr(norm_weight, "norm_weight", f32, dev),
+                              norm_eps, out_scale)
+        if out is None:
+            out = _new(stream, lambda: torch.empty_like(q))
+        elif out.shape != q_shape:
+            raise ValueError("out must have the shape of q")
+        if lse is None:
+            if return_lse:
+                lse = _new(stream, lambda: torch.empty(q_shape[0], q_shape[1], 2, dtype=f32, device=dev))
+        elif lse.shape != (q_shape[0], q_shape[1], 2):
+            raise ValueError("lse must be [n_tokens, H_qo, 2]")
+        lib, ref, ws = self.lib, ctypes.byref(info), self.workspace.data_ptr()
+        region, nbytes, copy = None, 0, None
+        if self.mode == N.BSP_MODE_DECODE:
+            fn = lib.bsp_decode_run_diff
+            nbytes = lib.bsp_decode_fp8_region_size(ref) if fp8 else 0
+        else:
+            fn = lib.bsp_prefill_run_diff
+            nbytes = lib.bsp_prefill_diff_region_size(ref) if fp8 else 0
+            if nbytes and self.capacity.max_gather_pages >= info.num_table_pages:
+                region, nbytes = ws + info.off_gather, 2 * info.gather_pool_bytes
+        if nbytes and region is None:  # scratch of this run alone
+            if stream is None:
+                copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            else:
+                with torch.cuda.stream(stream):
+                    copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            region = copy.data_ptr()
+        _call(dev, stream, fn, ref, ctypes.byref(diff), q_p, k_p, v_p, None if not fp8 else _addr(k_exp, "k_exp", torch.int8, dev),
+              None if not fp8 else _addr(v_exp, "v_exp", torch.int8, dev), _addr(kv_indices, "kv_indices", torch.int32, dev) or None,
+              pool[0], self._default_scale if sm_scale is None else sm_scale, _addr(out, "out", bf16, dev),
+              None if lse is None else _addr(lse, "lse", f32, dev), region, nbytes, ws)
+        return (out, lse) if return_lse else out
+
     def _set_sink(self, sink):
         self._sink_on = sink is not None
         if sink is None:
@@ -337,6 +412,8 @@ class PagedAttention:
         `events` = (e0, e1, e2) are recorded before, between and after them when
         given. out and lse must be preallocated."""
         dev = self.device
+        if self.differential:
+            raise RuntimeError("a differential object runs by run_differential()")
         with torch.cuda.device(dev):
             st = stream if stream is not None else torch.cuda.current_stream()
             s = ctypes.c_void_p(st.cuda_stream)

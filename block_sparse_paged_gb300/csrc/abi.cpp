@@ -158,6 +158,32 @@ int check_fp8_block(const bsp_plan_info *plan, int mode, const void *q, const vo
     return check_aligned16(q, k_pages, v_pages, o, workspace);
 }
 
+// Table entries that a decode's region holds (its exponents), or an error.
+int decode_region(const bsp_plan_info *plan, void *&region, size_t region_bytes, int64_t &entries) {
+    entries = 0;
+    if (!region) return BSP_OK;
+    if (reinterpret_cast<uintptr_t>(region) % 16 != 0) return fail(BSP_ERR_INVALID_ARG, "the region is not 16-byte aligned");
+    const size_t per_entry = 2 * (size_t)plan->problem.num_kv_heads;
+    entries = (int64_t)std::min<size_t>(region_bytes / per_entry, INT32_MAX) / 16 * 16;
+    if (entries < plan->num_table_pages) return fail(BSP_ERR_CAPACITY, "the region is too small for the plan's page table");
+    if (entries == 0) region = nullptr;
+    return BSP_OK;
+}
+
+// Pages that a prefill's region holds (its bf16 copy), or an error.
+int prefill_region(const bsp_plan_info *plan, void *&region, size_t region_bytes, int64_t &pages) {
+    pages = 0;
+    if (!region) return BSP_OK;
+    if (reinterpret_cast<uintptr_t>(region) % 32 != 0) return fail(BSP_ERR_INVALID_ARG, "the region is not 32-byte aligned");
+    if ((int64_t)plan->problem.page_size * plan->problem.num_kv_heads > kRegionPageRows)
+        return fail(BSP_ERR_UNSUPPORTED, "a copy takes pages of at most 2^27 rows over all heads: pass no region");
+    const size_t per_page = (size_t)plan->problem.page_size * plan->problem.num_kv_heads * 512;  // bf16 K and V
+    pages = (int64_t)std::min<size_t>(region_bytes / per_page, (size_t)(INT32_MAX / plan->problem.page_size));
+    if (pages < plan->num_table_pages) return fail(BSP_ERR_CAPACITY, "the region is too small for the plan's page table");
+    if (pages == 0) region = nullptr;
+    return BSP_OK;
+}
+
 }  // namespace
 
 extern "C" int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages,
@@ -169,15 +195,8 @@ extern "C" int bsp_decode_run_fp8_block(const bsp_plan_info *plan, const void *q
     int rc = check_fp8_block(plan, BSP_MODE_DECODE, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o,
                              workspace);
     if (rc != BSP_OK) return rc;
-    int64_t entries = 0;
-    if (region) {
-        if (reinterpret_cast<uintptr_t>(region) % 16 != 0)
-            return fail(BSP_ERR_INVALID_ARG, "the region is not 16-byte aligned");
-        const size_t per_entry = 2 * (size_t)plan->problem.num_kv_heads;
-        entries = (int64_t)std::min<size_t>(region_bytes / per_entry, INT32_MAX) / 16 * 16;
-        if (entries < plan->num_table_pages) return fail(BSP_ERR_CAPACITY, "the region is too small for the plan's page table");
-        if (entries == 0) region = nullptr;
-    }
+    int64_t entries;
+    if ((rc = decode_region(plan, region, region_bytes, entries)) != BSP_OK) return rc;
     return launch_decode_fp8_block(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse,
                                    region, entries, workspace, stream);
 }
@@ -213,21 +232,85 @@ extern "C" int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *
                              workspace);
     if (rc != BSP_OK) return rc;
     if (sm_scale <= 0.f) return fail(BSP_ERR_INVALID_ARG, "prefill needs a positive sm_scale");
-    int64_t pages = 0;
-    if (region) {
-        if (reinterpret_cast<uintptr_t>(region) % 32 != 0)
-            return fail(BSP_ERR_INVALID_ARG, "the region is not 32-byte aligned");
-        if ((int64_t)plan->problem.page_size * plan->problem.num_kv_heads > kRegionPageRows)
-            return fail(BSP_ERR_UNSUPPORTED, "a copy takes pages of at most 2^27 rows over all heads: pass no region");
-        const size_t per_page = (size_t)plan->problem.page_size * plan->problem.num_kv_heads * 512;  // bf16 K and V
-        pages = (int64_t)std::min<size_t>(region_bytes / per_page, (size_t)(INT32_MAX / plan->problem.page_size));
-        if (pages < plan->num_table_pages) return fail(BSP_ERR_CAPACITY, "the region is too small for the plan's page table");
-        if (pages == 0) region = nullptr;
-    }
+    int64_t pages;
+    if ((rc = prefill_region(plan, region, region_bytes, pages)) != BSP_OK) return rc;
     rc = launch_prefill_fp8_block(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse,
                                   region, pages, workspace, stream);
     if (rc != BSP_OK) return rc;
     return launch_reduce(plan, o, lse, workspace, stream);
+}
+
+namespace {
+
+// A differential run: a plan over pairs of maps, its arguments.
+int check_diff(const bsp_plan_info *plan, int mode, const bsp_differential *diff, const void *q, const void *k_pages,
+               const void *v_pages, const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
+               float sm_scale, const void *o, const void *workspace) {
+    clear_error();
+    int rc = check_plan(plan, mode, workspace);
+    if (rc != BSP_OK) return rc;
+    const bsp_problem &P = plan->problem;
+    if (P.dtype != BSP_DTYPE_BF16 || P.head_dim != 128)
+        return fail(BSP_ERR_UNSUPPORTED, "differential attention takes bf16 problems with head_dim 128 (halves of 64)");
+    if (plan->group % 2 != 0)
+        return fail(BSP_ERR_INVALID_ARG, "a differential plan has two of its query heads, the maps, per head: an even num_qo_heads / num_kv_heads");
+    if (P.sink) return fail(BSP_ERR_UNSUPPORTED, "differential attention takes no sink");
+    if (!diff || !diff->lambda) return fail(BSP_ERR_INVALID_ARG, "lambda is NULL");
+    if (!std::isfinite(diff->out_scale) || !std::isfinite(diff->norm_eps) || diff->norm_eps < 0.f)
+        return fail(BSP_ERR_INVALID_ARG, "out_scale and norm_eps must be finite, norm_eps >= 0");
+    if (reinterpret_cast<uintptr_t>(diff->norm_weight) % 16 != 0) return fail(BSP_ERR_INVALID_ARG, "norm_weight is not 16-byte aligned");
+    if (!std::isfinite(sm_scale) || (mode == BSP_MODE_PREFILL && sm_scale <= 0.f))
+        return fail(BSP_ERR_INVALID_ARG, "sm_scale must be finite, and positive for prefill");
+    if ((k_exp == nullptr) != (v_exp == nullptr)) return fail(BSP_ERR_INVALID_ARG, "k_exp and v_exp are given together");
+    if (!q || !k_pages || !v_pages || !o) return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
+    if (num_pages < 1 || num_pages > INT32_MAX) return fail(BSP_ERR_INVALID_ARG, "num_pages must be in [1, 2^31 - 1]");
+    if (k_exp && num_pages * P.page_size >= UINT32_MAX)
+        return fail(BSP_ERR_UNSUPPORTED, "the 8-bit cache takes at most 2^32 - 2 slots");
+    if (!kv_indices && plan->num_table_pages > 0)
+        return fail(BSP_ERR_INVALID_ARG, "kv_indices is NULL but the page table has pages");
+    return check_aligned16(q, k_pages, v_pages, o, workspace);
+}
+
+}  // namespace
+
+extern "C" int bsp_decode_run_diff(const bsp_plan_info *plan, const bsp_differential *diff, const void *q, const void *k_pages,
+                                   const void *v_pages, const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices,
+                                   int64_t num_pages, float sm_scale, void *o, float *lse, void *region, size_t region_bytes,
+                                   void *workspace, bsp_stream_t stream) {
+    if (no_queries(plan, BSP_MODE_DECODE, q, o)) return BSP_OK;
+    int rc = check_diff(plan, BSP_MODE_DECODE, diff, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, workspace);
+    if (rc != BSP_OK) return rc;
+    if (!k_exp) return launch_decode(plan, q, k_pages, v_pages, kv_indices, num_pages, sm_scale, o, lse, workspace, stream, diff);
+    int64_t entries;
+    if ((rc = decode_region(plan, region, region_bytes, entries)) != BSP_OK) return rc;
+    return launch_decode_fp8_block(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse, region,
+                                   entries, workspace, stream, diff);
+}
+
+extern "C" size_t bsp_prefill_diff_region_size(const bsp_plan_info *plan) {
+    clear_error();
+    if (!plan || plan->problem.mode != BSP_MODE_PREFILL || plan->num_table_pages <= 0) return 0;
+    return (size_t)plan->num_table_pages * plan->problem.page_size * plan->problem.num_kv_heads * 512;
+}
+
+extern "C" int bsp_prefill_run_diff(const bsp_plan_info *plan, const bsp_differential *diff, const void *q, const void *k_pages,
+                                    const void *v_pages, const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices,
+                                    int64_t num_pages, float sm_scale, void *o, float *lse, void *region, size_t region_bytes,
+                                    void *workspace, bsp_stream_t stream) {
+    if (no_queries(plan, BSP_MODE_PREFILL, q, o)) return BSP_OK;
+    int rc = check_diff(plan, BSP_MODE_PREFILL, diff, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, workspace);
+    if (rc != BSP_OK) return rc;
+    int64_t pages = 0;
+    if (k_exp && (rc = prefill_region(plan, region, region_bytes, pages)) != BSP_OK) return rc;
+    if (k_exp && !region && plan->num_table_pages > 0)
+        return fail(BSP_ERR_INVALID_ARG, "a differential prefill over the 8-bit cache needs a region");
+    if (k_exp && region)
+        rc = launch_prefill_fp8_block(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse, region,
+                                      pages, workspace, stream, diff);
+    else  // (an empty page table: no page is read)
+        rc = launch_prefill(plan, q, k_pages, v_pages, kv_indices, num_pages, sm_scale, o, lse, workspace, stream, diff);
+    if (rc != BSP_OK) return rc;
+    return launch_reduce(plan, o, lse, workspace, stream, diff);
 }
 
 extern "C" int bsp_run_attention(const bsp_plan_info *plan, const void *q, const void *k_pages,

@@ -75,25 +75,27 @@ int make_tmap(CUtensorMap *map, const void *base, int elem_bytes, uint64_t dim, 
 // Launchers (defined in the .cu files). They return BSP_OK or BSP_ERR_*.
 int launch_decode(const bsp_plan_info *plan, const void *q, const void *k_pages,
                   const void *v_pages, const int32_t *kv_indices, int64_t num_pages, float sm_scale,
-                  void *o, float *lse, void *workspace, cudaStream_t stream);
+                  void *o, float *lse, void *workspace, cudaStream_t stream, const bsp_differential *diff = nullptr);
+// (diff given: differential attention, the plan's heads being pairs of maps; arguments checked.)
 // Decode over e4m3 K/V pools with per-tensor scales (bf16 q and o).
 int launch_decode_fp8(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                       const int32_t *kv_indices, int64_t num_pages, float sm_scale, float k_scale, float v_scale,
                       void *o, float *lse, void *workspace, cudaStream_t stream);
 int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages,
                    const void *v_pages, const int32_t *kv_indices, int64_t num_pages,
-                   float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream);
+                   float sm_scale, void *o, float *lse, void *workspace, cudaStream_t stream,
+                   const bsp_differential *diff = nullptr);
 // Decode and prefill over an e4m3 cache with one exponent per (page, kv head); num_pages in 1 .. 2^31 - 1.
 // region (or NULL), decode: K exponents by table entry, then V's, of region_entries entries per head each.
 int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                             const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
                             float sm_scale, void *o, float *lse, void *region, int64_t region_entries, void *workspace,
-                            cudaStream_t stream);
+                            cudaStream_t stream, const bsp_differential *diff = nullptr);
 // region (or NULL), prefill: bf16 K copy, then V copy, of region_pages pages each.
 int launch_prefill_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                              const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
                              float sm_scale, void *o, float *lse, void *region, int64_t region_pages, void *workspace,
-                             cudaStream_t stream);
+                             cudaStream_t stream, const bsp_differential *diff = nullptr);
 // Copy the page table's first n_pages pages of K and V, in table order, into
 // the plan's gather region (prefill with a region); ids outside [0, num_pages)
 // give zero pages and set the workspace status word.
@@ -101,7 +103,7 @@ int launch_gather_pages(const bsp_plan_info *plan, const void *k_pages, const vo
                         const int32_t *kv_indices, int64_t num_pages, void *workspace, cudaStream_t stream);
 int launch_wait_probe(long long limit_cycles, int *status, cudaStream_t stream);
 int launch_reduce(const bsp_plan_info *plan, void *o, float *lse, void *workspace,
-                  cudaStream_t stream);
+                  cudaStream_t stream, const bsp_differential *diff = nullptr);
 int launch_merge_state(const void *o_a, const float *lse_a, const void *o_b, const float *lse_b,
                        void *o_out, float *lse_out, int64_t n_rows, int32_t num_heads,
                        int32_t head_dim, int32_t dtype, cudaStream_t stream);

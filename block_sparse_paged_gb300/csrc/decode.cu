@@ -184,6 +184,8 @@ struct DecodeParams {
     int num_pages;                // kBlk: page ids outside [0, num_pages) read as zero codes
     const int8_t *exp_table;      // kBlk, cp.async: exponents of the first exp_entries table
     int exp_entries;              // entries, [K, V][H_kv][exp_entries]; the further ones by page
+    const float *lam, *norm;      // kDiff: factor of the second map per head, norm weights [D] or null
+    float norm_eps, out_scale;
 };
 
 // Fold of one (row r, columns 4 cq .. 4 cq + 3) unit of a reduction-map entry
@@ -194,8 +196,9 @@ struct DecodeParams {
 // slots this is the fold with one common maximum; longer entries fold 8 slots
 // at a time, rescaling to the running maximum. Prm: DecodeParams or
 // ReduceParams (workspace offsets, outputs, shapes, sinks).
-template <int D, typename OutT, typename Prm>
-__device__ __forceinline__ void fold_unit(const Prm &p, const bsp_merge_entry &e, int r, int cq) {
+// The state before its division: acc, its factor inv and the row's LSE.
+template <int D, typename Prm>
+__device__ __forceinline__ float4 fold_state(const Prm &p, const bsp_merge_entry &e, int r, int cq, float &inv, float &lse_row) {
     constexpr int kQ = D / 4;     // column quads per row
     constexpr int kBatch = 8;     // slots whose loads are in flight together
     const float *plse = reinterpret_cast<const float *>(p.ws + p.off_plse);
@@ -234,8 +237,15 @@ __device__ __forceinline__ void fold_unit(const Prm &p, const bsp_merge_entry &e
             }
         }
     }
-    float inv = M != -INFINITY ? 1.f / L : 0.f;
-    float lse_row = M != -INFINITY ? M + logf(L) : -INFINITY;
+    inv = M != -INFINITY ? 1.f / L : 0.f;
+    lse_row = M != -INFINITY ? M + logf(L) : -INFINITY;
+    return acc;
+}
+
+template <int D, typename OutT, typename Prm>
+__device__ __forceinline__ void fold_unit(const Prm &p, const bsp_merge_entry &e, int r, int cq) {
+    float inv, lse_row;
+    const float4 acc = fold_state<D>(p, e, r, cq, inv, lse_row);
     if (p.sink) inv *= fold_sink(lse_row, p.sink[e.kv_head * p.g + r % p.g]);
     const size_t orow = (size_t)(e.q_tok0 + r / p.g) * p.H_qo + (size_t)e.kv_head * p.g + (r % p.g);
     OutT *dst = static_cast<OutT *>(p.o) + orow * D + cq * 4;
@@ -246,10 +256,49 @@ __device__ __forceinline__ void fold_unit(const Prm &p, const bsp_merge_entry &e
     if (cq == 0 && p.lse) p.lse[orow] = lse_row;
 }
 
+// Differential attention: a plan over 2 H_q "heads", of which a kv head's first g / 2 rows of a
+// tile are the first softmax maps of its g / 2 query heads and the others the second ones (half of
+// the tile's rows apart). q and o have H_qo / 2 heads, and the first maps' queries are the first
+// halves of q's rows against the first halves of K's. Out of the two states (O1, LSE1), (O2, LSE2):
+//   y = O1 - lam O2;   with norm weights y / sqrt(mean(y^2) + eps) * norm;   o = y * out_scale.
+// The lanes of a warp hold the 128 columns of a row, four each.
+template <typename Prm>
+__device__ __forceinline__ void write_diff_row(const Prm &p, float4 y, size_t orow, int lane) {
+    float f = p.out_scale;
+    if (p.norm) {
+        float ss = y.x * y.x + y.y * y.y + y.z * y.z + y.w * y.w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        f *= rsqrtf(ss * (1.f / 128.f) + p.norm_eps);
+        const float4 w = __ldg(reinterpret_cast<const float4 *>(p.norm) + lane);
+        y.x *= w.x; y.y *= w.y; y.z *= w.z; y.w *= w.w;
+    }
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + orow * 128 + lane * 4) =
+        make_uint2(pack_bf16(y.x * f, y.y * f), pack_bf16(y.z * f, y.w * f));
+}
+
+// A warp: rows r and r + second (the two maps of one head) of a reduction-map entry. gh: heads per kv head.
+template <typename Prm>
+__device__ __forceinline__ void fold_diff_row(const Prm &p, const bsp_merge_entry &e, int r, int second, int gh, int lane) {
+    float inv1, inv2, lse1, lse2;
+    const float4 a = fold_state<128>(p, e, r, lane, inv1, lse1), b = fold_state<128>(p, e, r + second, lane, inv2, lse2);
+    const int head = e.kv_head * gh + r % gh;
+    const size_t orow = (size_t)(e.q_tok0 + r / gh) * (p.H_qo / 2) + head;
+    const float lam = -__ldg(p.lam + head);
+    // (products rounded before the difference, so that equal maps cancel exactly)
+    auto y = [&](float x1, float x2) { return fmaf(lam, __fmul_rn(x2, inv2), __fmul_rn(x1, inv1)); };
+    write_diff_row(p, make_float4(y(a.x, b.x), y(a.y, b.y), y(a.z, b.z), y(a.w, b.w)), orow, lane);
+    if (lane == 0 && p.lse) reinterpret_cast<float2 *>(p.lse)[orow] = make_float2(lse1, lse2);
+}
+
 // Merge of one reduction-map entry by threads t = 0..nthreads-1 of the CTA that
 // wrote its last partial state: one (row, 4 columns) unit per thread.
-template <int D, typename OutT>
+template <int D, typename OutT, bool kDiff = false>
 __device__ __forceinline__ void merge_entry(const DecodeParams &p, const bsp_merge_entry &e, int t, int nthreads) {
+    if constexpr (kDiff) {  // whole warps; a decode tile is one position
+        for (int r = t >> 5; r < p.g / 2; r += nthreads >> 5) fold_diff_row(p, e, r, p.g / 2, p.g / 2, t & 31);
+        return;
+    }
     constexpr int kQ = D / 4;
     const int rows = e.n_pos * p.g;
     for (int u = t; u < rows * kQ; u += nthreads) fold_unit<D, OutT>(p, e, u / kQ, u % kQ);
@@ -291,12 +340,15 @@ __global__ void wait_probe_kernel(long long limit_cycles, int *status) {
 }
 
 // kNH (e4m3 only): 8-head tiles per kv head, ceil(g / 8)
-template <int D, bool kTma, bool kFp8 = false, int kNH = 1, bool kBlk = false>
+// kDiff: differential attention. A row of the tile is one map of one head: its q row is zero in the
+// other map's half, which leaves the products as they are (the tile's 16 rows hold up to 8 heads).
+template <int D, bool kTma, bool kFp8 = false, int kNH = 1, bool kBlk = false, bool kDiff = false>
 __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThreads, 1)
     decode_bf16_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                        const DecodeParams p) {
     static_assert(!kFp8 || ((kTma || kBlk) && D == 128), "e4m3 pools: head_dim 128; TMA gather or block exponents");
     static_assert(kFp8 || !kBlk, "block exponents belong to e4m3 pools");
+    static_assert(!kDiff || (D == 128 && (kBlk || !kFp8)), "differential: rows of two halves of 64");
     using LY = DecodeLayout<D, kTma, kFp8, kNH, kBlk>;
     constexpr int kSR = LY::kScrRows;
     constexpr int kStages = LY::kS;
@@ -638,6 +690,8 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
 
     // ---------------- consumers: warps 0..3 ----------------------------------
     const int g = p.g;
+    const int gq = kDiff ? g / 2 : g;  // rows of q per position and kv head
+    auto q_row = [&](int tok, int kv_head) -> size_t { return (size_t)tok * (kDiff ? p.H_qo / 2 : p.H_qo) + (size_t)kv_head * gq; };
     const int r0 = lane >> 2, r1 = r0 + 8;
     float *scratch = reinterpret_cast<float *>(smem + LY::kScratchOff);                      // [warp][16][D]
     float *stats = reinterpret_cast<float *>(smem + LY::kScratchOff + LY::kScratchBytes);  // [warp][16][m, l]
@@ -670,16 +724,16 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
             uint32_t qf[D / 16][kNH][2];
             float hs[kNH][2];
             {
-                const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q) +
-                                          ((size_t)w.q_tok0 * p.H_qo + (size_t)w.kv_head * g) * D;
+                const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q) + q_row(w.q_tok0, w.kv_head) * D;
 #pragma unroll
                 for (int nh = 0; nh < kNH; ++nh) {
-                    const int head = 8 * nh + qn;
-                    const uint32_t *qr = reinterpret_cast<const uint32_t *>(qb + (size_t)head * D);
+                    const int head = 8 * nh + qn, map = kDiff && head >= gq ? 1 : 0;
+                    const uint32_t *qr = reinterpret_cast<const uint32_t *>(qb + (size_t)(head - map * gq) * D);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const int c2 = (64 * (kk >> 2) + 16 * c + 4 * (kk & 3)) >> 1;  // index in bf16 pairs
-                        const uint32_t x = head < g ? __ldg(qr + c2) : 0u, y = head < g ? __ldg(qr + c2 + 1) : 0u;
+                        const bool in = head < g && (!kDiff || kk >> 2 == map);
+                        const uint32_t x = in ? __ldg(qr + c2) : 0u, y = in ? __ldg(qr + c2 + 1) : 0u;
                         qf[kk][nh][0] = kBlk ? x : pack_f16_sat(bf16_lo(x), bf16_hi(x));
                         qf[kk][nh][1] = kBlk ? y : pack_f16_sat(bf16_lo(y), bf16_hi(y));
                     }
@@ -1047,17 +1101,18 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
             // Q fragments of the g fused rows (rows >= g are zero)
             uint32_t qa[D / 16][4];
             {
-                const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q) +
-                                          ((size_t)w.q_tok0 * p.H_qo + (size_t)w.kv_head * g) * D;
-                const uint32_t *q0 = reinterpret_cast<const uint32_t *>(qb + (size_t)r0 * D);
-                const uint32_t *q1 = reinterpret_cast<const uint32_t *>(qb + (size_t)r1 * D);
+                const __nv_bfloat16 *qb = static_cast<const __nv_bfloat16 *>(p.q) + q_row(w.q_tok0, w.kv_head) * D;
+                const int map0 = kDiff && r0 >= gq ? 1 : 0, map1 = kDiff && r1 >= gq ? 1 : 0;
+                const uint32_t *q0 = reinterpret_cast<const uint32_t *>(qb + (size_t)(r0 - map0 * gq) * D);
+                const uint32_t *q1 = reinterpret_cast<const uint32_t *>(qb + (size_t)(r1 - map1 * gq) * D);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const int c2 = (kk * 16 + 2 * (lane & 3)) >> 1;  // index in bf16 pairs
-                    qa[kk][0] = r0 < g ? __ldg(q0 + c2) : 0u;
-                    qa[kk][1] = r1 < g ? __ldg(q1 + c2) : 0u;
-                    qa[kk][2] = r0 < g ? __ldg(q0 + c2 + 4) : 0u;
-                    qa[kk][3] = r1 < g ? __ldg(q1 + c2 + 4) : 0u;
+                    const bool in0 = r0 < g && (!kDiff || kk / (D / 32) == map0), in1 = r1 < g && (!kDiff || kk / (D / 32) == map1);
+                    qa[kk][0] = in0 ? __ldg(q0 + c2) : 0u;
+                    qa[kk][1] = in1 ? __ldg(q1 + c2) : 0u;
+                    qa[kk][2] = in0 ? __ldg(q0 + c2 + 4) : 0u;
+                    qa[kk][3] = in1 ? __ldg(q1 + c2 + 4) : 0u;
                 }
             }
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
@@ -1188,9 +1243,8 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                 *reinterpret_cast<float2 *>(scratch + (warp * kSR + r1) * D + col) = make_float2(acc[n][2], acc[n][3]);
             }
         }
-        if (warp == 0 && it + 1 < it1 && lane * 128 < g * D * 2) {  // the next item's g query rows
-            const char *qn = static_cast<const char *>(p.q) +
-                             ((size_t)w_next.q_tok0 * p.H_qo + (size_t)w_next.kv_head * g) * D * 2 + lane * 128;
+        if (warp == 0 && it + 1 < it1 && lane * 128 < gq * D * 2) {  // the next item's query rows
+            const char *qn = static_cast<const char *>(p.q) + q_row(w_next.q_tok0, w_next.kv_head) * D * 2 + lane * 128;
             asm volatile("prefetch.global.L1 [%0];\n" ::"l"(qn));
         }
         __syncwarp();
@@ -1225,7 +1279,30 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
         if (!__all_sync(0xffffffffu, wait_or_abort(merge_mid, merges & 1, abort_flag, status, kStatusMergeWait))) return;
         // one (row, 4 columns) unit per thread and pass: the warps' float4s
         // weighted and summed, then 4 bf16 of the output or a float4 of the partial
-        for (int u = ct; u < g * (D / 4); u += kConsumers * 32) {
+        if (kDiff && w.slot < 0) {  // a warp per head
+            for (int row = warp; row < gq; row += kConsumers) {
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                const size_t orow = q_row(w.q_tok0, w.kv_head) + row;
+                const float lam = -__ldg(p.lam + w.kv_head * gq + row);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int ww = 0; ww < kConsumers; ++ww) {
+                        const float fw = fac[ww * kSR + m * gq + row];
+                        const float4 x = reinterpret_cast<const float4 *>(scratch + (ww * kSR + m * gq + row) * D)[lane];
+                        acc.x = fmaf(fw, x.x, acc.x);
+                        acc.y = fmaf(fw, x.y, acc.y);
+                        acc.z = fmaf(fw, x.z, acc.z);
+                        acc.w = fmaf(fw, x.w, acc.w);
+                    }
+                    if (m == 0) y = acc;
+                    else y = make_float4(fmaf(lam, acc.x, y.x), fmaf(lam, acc.y, y.y), fmaf(lam, acc.z, y.z), fmaf(lam, acc.w, y.w));
+                }
+                write_diff_row(p, y, orow, lane);
+                if (lane == 0 && p.lse) reinterpret_cast<float2 *>(p.lse)[orow] = make_float2(rlse[row], rlse[gq + row]);
+            }
+        } else for (int u = ct; u < g * (D / 4); u += kConsumers * 32) {
             const int row = u / (D / 4), cq = u - row * (D / 4);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1252,26 +1329,33 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
         if (lane == 0) sm100::mbar_arrive(merge_out);
         if (!__all_sync(0xffffffffu, wait_or_abort(merge_out, merges & 1, abort_flag, status, kStatusMergeWait))) return;
         ++merges;
-        if (w.slot >= 0 && warp == 0 && lane == 0) {
+        if (w.slot >= 0 && warp == 0 && (kDiff || lane == 0)) {
             // Split output: count this partial in its reduction-map entry. Every
             // consumer thread wrote its partial rows before merge_out; one gpu-scope
             // fence here orders them all (fences are cumulative) before the count.
             // The CTA whose partial completes the count folds the entry after its
             // queue (nobody waits for another CTA, and no warp waits here for the
             // atomic's round trip).
+            // (kDiff: the whole warp, whose lanes fold a row together where the list is full.)
             __threadfence();
-            const int prev = atomicAdd(&mmap[w.merge].arrived, 1);
+            int prev = 0;
+            if (lane == 0) prev = atomicAdd(&mmap[w.merge].arrived, 1);
+            if constexpr (kDiff) prev = __shfl_sync(0xffffffffu, prev, 0);
             if (prev == mmap[w.merge].n_slots - 1) {
                 __threadfence();  // acquire: the other CTAs' partials, counted before their arrivals
                 const int n = pending[0];
+                if constexpr (kDiff) __syncwarp();  // every lane has read the count
                 if (n < kMaxPendingFolds) {
-                    pending[1 + n] = w.merge;
-                    pending[0] = n + 1;
-                } else {  // list full: fold this entry now, by this thread alone
-                    merge_entry<D, __nv_bfloat16>(p, mmap[w.merge], 0, 1);
-                    mmap[w.merge].arrived = 0;  // ready for the next run of the plan
+                    if (lane == 0) {
+                        pending[1 + n] = w.merge;
+                        pending[0] = n + 1;
+                    }
+                } else {  // list full: fold this entry now, by this thread (kDiff: warp) alone
+                    merge_entry<D, __nv_bfloat16, kDiff>(p, mmap[w.merge], kDiff ? lane : 0, kDiff ? 32 : 1);
+                    if (lane == 0) mmap[w.merge].arrived = 0;  // ready for the next run of the plan
                 }
             }
+            if constexpr (kDiff) __syncwarp();
         }
     }
     // ---- folds of the entries this CTA completed ----------------------------
@@ -1281,7 +1365,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
     const int n_pending = pending[0];
     for (int i = 0; i < n_pending; ++i) {
         const int ei = pending[1 + i];
-        merge_entry<D, __nv_bfloat16>(p, mmap[ei], warp * 32 + lane, kConsumers * 32);
+        merge_entry<D, __nv_bfloat16, kDiff>(p, mmap[ei], warp * 32 + lane, kConsumers * 32);
         if (warp == 0 && lane == 0) mmap[ei].arrived = 0;  // ready for the next run of the plan
     }
 }
@@ -1369,6 +1453,8 @@ struct ReduceParams {
     float *lse;
     int H_qo, g, tile_rows;
     const float *sink;  // per-qo-head sink logits, or null
+    const float *lam, *norm;  // differential attention
+    float norm_eps, out_scale;
 };
 
 template <int D, typename OutT>
@@ -1390,6 +1476,20 @@ __global__ void __launch_bounds__(256) reduce_kernel(const ReduceParams p) {
         const bsp_merge_entry &e = merges[rr / p.tile_rows];
         const int r = (int)(rr % p.tile_rows);
         if (r < e.n_pos * p.g) fold_unit<D, OutT>(p, e, r, cq);
+    }
+}
+
+// The same for differential attention: a warp per (entry, row of the first map).
+__global__ void __launch_bounds__(256) reduce_diff_kernel(const ReduceParams p) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const DevHeader *hdr = reinterpret_cast<const DevHeader *>(p.ws + p.off_header);
+    const bsp_merge_entry *merges = reinterpret_cast<const bsp_merge_entry *>(p.ws + p.off_merges);
+    const int half = p.tile_rows / 2, gh = p.g / 2, lane = threadIdx.x & 31;
+    const long long rows = (long long)hdr->num_merges * half;
+    for (long long u = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; u < rows; u += ((long long)gridDim.x * blockDim.x) >> 5) {
+        const bsp_merge_entry &e = merges[u / half];
+        const int r = (int)(u % half);
+        if (r < e.n_pos * gh) fold_diff_row(p, e, r, half, gh, lane);
     }
 }
 
@@ -1460,7 +1560,7 @@ int num_sms_of_current_device(int *dev_out) {
     return sms[dev];
 }
 
-template <int D, bool kTma, bool kFp8 = false, int kNH = 1, bool kBlk = false>
+template <int D, bool kTma, bool kFp8 = false, int kNH = 1, bool kBlk = false, bool kDiff = false>
 int launch_decode_bf16(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeParams &p, int grid,
                        cudaStream_t stream) {
     static bool configured[64] = {false};
@@ -1469,12 +1569,12 @@ int launch_decode_bf16(const CUtensorMap &tk, const CUtensorMap &tv, const Decod
     using LY = DecodeLayout<D, kTma, kFp8, kNH, kBlk>;
     constexpr int kSmem = LY::kSmemBytes;
     if (!configured[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(decode_bf16_kernel<D, kTma, kFp8, kNH, kBlk>,
+        cudaError_t e = cudaFuncSetAttribute(decode_bf16_kernel<D, kTma, kFp8, kNH, kBlk, kDiff>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("decode smem attribute: ") + cudaGetErrorString(e));
         configured[dev] = true;
     }
-    decode_bf16_kernel<D, kTma, kFp8, kNH, kBlk><<<grid, LY::kThreads, kSmem, stream>>>(tk, tv, p);
+    decode_bf16_kernel<D, kTma, kFp8, kNH, kBlk, kDiff><<<grid, LY::kThreads, kSmem, stream>>>(tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("decode launch: ") + cudaGetErrorString(e));
     return BSP_OK;
@@ -1488,8 +1588,7 @@ int launch_decode_f32(const DecodeParams &p, int grid, cudaStream_t stream) {
     return BSP_OK;
 }
 
-template <int D, typename OutT>
-int launch_reduce_t(const ReduceParams &p, int64_t units, cudaStream_t stream) {
+int launch_reduce_kernel(void (*kernel)(ReduceParams), const ReduceParams &p, int64_t units, cudaStream_t stream) {
     const int sms = num_sms_of_current_device(nullptr);
     if (sms < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
     // one unit per thread for this plan (every load in flight at once), at
@@ -1504,10 +1603,15 @@ int launch_reduce_t(const ReduceParams &p, int64_t units, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, reduce_kernel<D, OutT>, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("reduce launch: ") + cudaGetErrorString(e));
     return BSP_OK;
+}
+
+template <int D, typename OutT>
+int launch_reduce_t(const ReduceParams &p, int64_t units, cudaStream_t stream) {
+    return launch_reduce_kernel(reduce_kernel<D, OutT>, p, units, stream);
 }
 
 }  // namespace
@@ -1544,6 +1648,9 @@ int decode_params(const bsp_plan_info *plan, const void *q, const void *k_pages,
     p.num_pages = 0;
     p.exp_table = nullptr;
     p.exp_entries = 0;
+    p.lam = p.norm = nullptr;
+    p.norm_eps = 0.f;
+    p.out_scale = 1.f;
     p.window_left = P.window_left;
     p.soft_cap_on = P.logits_soft_cap > 0.f;
     p.cap_in = p.soft_cap_on ? qk_scale / P.logits_soft_cap : 0.f;
@@ -1563,15 +1670,23 @@ int decode_params(const bsp_plan_info *plan, const void *q, const void *k_pages,
     return (p.num_queues + p.queues_per_cta - 1) / p.queues_per_cta;
 }
 
+void set_diff(DecodeParams &p, const bsp_differential &d) {
+    p.lam = d.lambda;
+    p.norm = d.norm_weight;
+    p.norm_eps = d.norm_eps;
+    p.out_scale = d.out_scale;
+}
+
 }  // namespace
 
 int launch_decode(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                   const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o, float *lse,
-                  void *workspace, cudaStream_t stream) {
+                  void *workspace, cudaStream_t stream, const bsp_differential *diff) {
     const bsp_problem &P = plan->problem;
     DecodeParams p;
     const int grid = decode_params(plan, q, k_pages, v_pages, kv_indices, sm_scale, 1.f, 1.f, o, lse, workspace, p);
     if (grid < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    if (diff) set_diff(p, *diff);
     if (P.dtype == BSP_DTYPE_BF16) {
         if (p.g > kMmaRows) return fail(BSP_ERR_UNSUPPORTED, "bf16 decode needs num_qo_heads / num_kv_heads <= 16");
         if (P.head_dim != 128 && P.head_dim != 64) return fail(BSP_ERR_UNSUPPORTED, "bf16 decode supports head_dim 64 and 128");
@@ -1590,10 +1705,12 @@ int launch_decode(const bsp_plan_info *plan, const void *q, const void *k_pages,
             int rc = make_tmap_bf16(&tk, k_pages, P.head_dim, P.num_kv_heads, rows, 1, p.box_rows);
             if (rc == BSP_OK) rc = make_tmap_bf16(&tv, v_pages, P.head_dim, P.num_kv_heads, rows, 1, p.box_rows);
             if (rc != BSP_OK) return rc;
+            if (diff) return launch_decode_bf16<128, true, false, 1, false, true>(tk, tv, p, grid, stream);
             return P.head_dim == 128 ? launch_decode_bf16<128, true>(tk, tv, p, grid, stream)
                                      : launch_decode_bf16<64, true>(tk, tv, p, grid, stream);
         }
         p.box_rows = 0;
+        if (diff) return launch_decode_bf16<128, false, false, 1, false, true>(tk, tv, p, grid, stream);
         return P.head_dim == 128 ? launch_decode_bf16<128, false>(tk, tv, p, grid, stream)
                                  : launch_decode_bf16<64, false>(tk, tv, p, grid, stream);
     }
@@ -1637,7 +1754,7 @@ int launch_decode_fp8(const bsp_plan_info *plan, const void *q, const void *k_pa
 int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                             const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
                             float sm_scale, void *o, float *lse, void *region, int64_t region_entries, void *workspace,
-                            cudaStream_t stream) {
+                            cudaStream_t stream, const bsp_differential *diff) {
     const bsp_problem &P = plan->problem;
     if (P.dtype != BSP_DTYPE_BF16 || P.head_dim != 128)
         return fail(BSP_ERR_UNSUPPORTED, "e4m3 KV decode needs a bf16 problem (queries, outputs) with head_dim 128");
@@ -1645,6 +1762,7 @@ int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void
     DecodeParams p;
     const int grid = decode_params(plan, q, k_pages, v_pages, kv_indices, sm_scale, 1.f, 1.f, o, lse, workspace, p);
     if (grid < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    if (diff) set_diff(p, *diff);
     p.k_exp = k_exp;
     p.v_exp = v_exp;
     p.num_pages = (int)num_pages;
@@ -1660,6 +1778,9 @@ int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void
         int rc = make_tmap(&tk, k_pages, 1, P.head_dim, P.num_kv_heads, rows, 1, p.box_rows);
         if (rc == BSP_OK) rc = make_tmap(&tv, v_pages, 1, P.head_dim, P.num_kv_heads, rows, 1, p.box_rows);
         if (rc != BSP_OK) return rc;
+        if (diff)
+            return plan->group <= 8 ? launch_decode_bf16<128, true, true, 1, true, true>(tk, tv, p, grid, stream)
+                                    : launch_decode_bf16<128, true, true, 2, true, true>(tk, tv, p, grid, stream);
         return plan->group <= 8 ? launch_decode_bf16<128, true, true, 1, true>(tk, tv, p, grid, stream)
                                 : launch_decode_bf16<128, true, true, 2, true>(tk, tv, p, grid, stream);
     }
@@ -1674,6 +1795,9 @@ int launch_decode_fp8_block(const bsp_plan_info *plan, const void *q, const void
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("exponents launch: ") + cudaGetErrorString(e));
     }
+    if (diff)
+        return plan->group <= 8 ? launch_decode_bf16<128, false, true, 1, true, true>(tk, tv, p, grid, stream)
+                                : launch_decode_bf16<128, false, true, 2, true, true>(tk, tv, p, grid, stream);
     return plan->group <= 8 ? launch_decode_bf16<128, false, true, 1, true>(tk, tv, p, grid, stream)
                             : launch_decode_bf16<128, false, true, 2, true>(tk, tv, p, grid, stream);
 }
@@ -1685,7 +1809,8 @@ int launch_wait_probe(long long limit_cycles, int *status, cudaStream_t stream) 
     return BSP_OK;
 }
 
-int launch_reduce(const bsp_plan_info *plan, void *o, float *lse, void *workspace, cudaStream_t stream) {
+int launch_reduce(const bsp_plan_info *plan, void *o, float *lse, void *workspace, cudaStream_t stream,
+                  const bsp_differential *diff) {
     const bsp_problem &P = plan->problem;
     ReduceParams p;
     p.ws = static_cast<const uint8_t *>(workspace);
@@ -1699,6 +1824,16 @@ int launch_reduce(const bsp_plan_info *plan, void *o, float *lse, void *workspac
     p.g = plan->group;
     p.tile_rows = plan->tile_rows;
     p.sink = P.sink;
+    p.lam = p.norm = nullptr;
+    p.norm_eps = 0.f;
+    p.out_scale = 1.f;
+    if (diff) {
+        p.lam = diff->lambda;
+        p.norm = diff->norm_weight;
+        p.norm_eps = diff->norm_eps;
+        p.out_scale = diff->out_scale;
+        return launch_reduce_kernel(reduce_diff_kernel, p, (int64_t)plan->num_merges * plan->tile_rows * 16, stream);
+    }
     const bool bf = P.dtype == BSP_DTYPE_BF16;
     const int64_t u = (int64_t)plan->num_merges * plan->tile_rows * (P.head_dim / 4);
     switch (P.head_dim) {

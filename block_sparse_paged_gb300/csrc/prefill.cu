@@ -86,7 +86,9 @@ enum Bar {
     kKFull0, kKEmpty0 = kKFull0 + kKStages, kVFull0 = kKEmpty0 + kKStages, kVEmpty0 = kVFull0 + kVStages,
     kSFull0 = kVEmpty0 + kVStages, kSFull1, kPFull0, kPFull1, kODone0, kODone1, kOFree0, kOFree1, kNumBars,
     // e4m3 codes by TMA in the staging, K and V (behind the other words, whose places stay)
-    kRawFull0 = kNumBars + 2, kRawFull1, kRawEmpty0, kRawEmpty1, kEndBars
+    kRawFull0 = kNumBars + 2, kRawFull1, kRawEmpty0, kRawEmpty1, kEndBars,
+    // differential attention, in the places of the e4m3 kernel's: the two warps of 32 rows meet
+    kMeet0 = kRawFull0, kMeet1, kMeet2, kMeet3
 };
 constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmemSlot + 8;
@@ -122,6 +124,8 @@ struct PrefillParams {
     const int8_t *k_exp, *v_exp;  // e4m3 cache: exponents [num_pages][H_kv]
     int num_pages;                // e4m3 cache: page ids outside [0, num_pages) read as zero codes
     int raw_box;                  // e4m3 cache by TMA: rows of a box of codes
+    const float *lam, *norm;      // differential: factor of the second map per head, norm weights [128] or null
+    float norm_eps, out_scale;
 };
 
 struct Ctx {
@@ -209,7 +213,12 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, float s) {
 // come by TMA boxes (kTma) or cp.async, by the same rule.
 // kNan: a row whose sum is NaN is written as NaN (the e4m3 cache, its bf16 copy too; rows
 // over bf16 pools get an LSE of -inf then. Asking at run time cost those 0.5%).
-template <bool kTma, bool kVar, bool kFp8 = false, bool kNan = kFp8>
+// kDiff: differential attention. The two subtiles are the two softmax maps of the same 128 rows:
+// subtile 0 multiplies the first halves of the rows of Q and K (64 of 128 dimensions, one swizzled
+// slab each), subtile 1 the second ones, and both take the whole rows of V; so Q is one tile, the
+// products are those of the formula and no more. At an item's end each softmax group reads 64
+// columns of both O's and writes their difference. p.H_qo and p.g count heads, not maps.
+template <bool kTma, bool kVar, bool kFp8 = false, bool kNan = kFp8, bool kDiff = false>
 __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const PrefillParams p) {
@@ -234,7 +243,10 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
             const bool softmax_arrivals = i == kPFull0 || i == kPFull1 || i == kOFree0 || i == kOFree1;
             const bool kv_full = (i >= kKFull0 && i < kKFull0 + kKStages) || (i >= kVFull0 && i < kVFull0 + kVStages);
             // cp.async: one per lane; e4m3: one per converting warp
-            mbar_init(bar(i), softmax_arrivals ? 128 : (kv_full && (kFp8 || !kTma)) ? (kFp8 ? 4 : 32) : 1);
+            mbar_init(bar(i), softmax_arrivals ? (kDiff && i >= kOFree0 ? 256 : 128) : (kv_full && (kFp8 || !kTma)) ? (kFp8 ? 4 : 32) : 1);
+        }
+        if constexpr (kDiff) {
+            for (int i = 0; i < 4; ++i) mbar_init(bar(kMeet0 + i), 64);
         }
         if constexpr (kFp8 && kTma) {
             for (int v = 0; v < 2; ++v) {
@@ -337,9 +349,9 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
             if (!(ok = wait_bar_warp(ctx, bar(kQEmpty), (q_cnt & 1) ^ 1))) break;
             ++q_cnt;
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar(kQFull), kSub * kTile);
+                mbar_arrive_expect_tx(bar(kQFull), (kDiff ? 1 : kSub) * kTile);
 #pragma unroll
-                for (int sub = 0; sub < kSub; ++sub)
+                for (int sub = 0; sub < (kDiff ? 1 : kSub); ++sub)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         tma_load_3d(sb + kOffQ + sub * kTile + h * kHalf, &tq, bar(kQFull), h * 64, w.kv_head * g,
@@ -503,9 +515,10 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 return false;
             };
             auto issue_s = [&](int sub, int stage) {
-                const uint32_t sq = sb + kOffQ + sub * kTile, sk = sb + kOffK + stage * kTile;
+                const uint32_t sq = sb + kOffQ + sub * (kDiff ? kHalf : kTile);
+                const uint32_t sk = sb + kOffK + stage * kTile + (kDiff ? sub * kHalf : 0);
 #pragma unroll
-                for (int kk = 0; kk < kD / 16; ++kk) {
+                for (int kk = 0; kk < (kDiff ? kD / 32 : kD / 16); ++kk) {
                     const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
                     mma_bf16_ss(tmem + sub * 128, smem_desc_sw128(sq + o, 16, 1024), smem_desc_sw128(sk + o, 16, 1024),
                                 id_s, kk > 0);
@@ -582,13 +595,14 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
         const int sub = (warp - 2) >> 2;       // warps 2-5: subtile 0, warps 6-9: subtile 1
         const int q4 = warp & 3;               // TMEM lane quarter of this warp
         const int r = q4 * 32 + lane;          // row within the subtile
-        const int rt = sub * kRows + r;        // row within the 256-row tile
+        const int rt = kDiff ? r : sub * kRows + r;  // row within the 256-row tile (of the head's rows)
         const uint32_t tl = (uint32_t)(q4 * 32) << 16;
         const uint32_t tS = tmem + tl + sub * 128, tO = tmem + tl + 256 + sub * 128;
         float *plse = reinterpret_cast<float *>(const_cast<uint8_t *>(p.ws) + p.off_plse);
         float *po = reinterpret_cast<float *>(const_cast<uint8_t *>(p.ws) + p.off_po);
-        int s_cnt = 0, o_cnt = 0, j = 0;
+        int s_cnt = 0, o_cnt = 0, j = 0, meet = 0;
         bool ok = true;
+        (void)meet;
         // e4m3 cache: the group of subtile 0 converts K tiles, that of subtile 1 V tiles, 32
         // keys per warp, two tiles ahead of the one that it works on (the rings' depth), over
         // the CTA's items as one sequence. The codes come into the warp's staging buffer one
@@ -833,6 +847,89 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
             // ---- epilogue: O / l, LSE; final output or partial state ----
             // O leaves TMEM first, so that the next item's PV may start while
             // this one is written out.
+            if (kDiff && w.slot < 0) {
+                // both maps' O, 64 columns of each per group
+                const bool has = !(l <= 0.f);
+                const float lse_v = has ? (m + log2f(l)) * dev::kLn2 : -INFINITY;
+                const int head = w.kv_head * g + r % g;
+                float *x = reinterpret_cast<float *>(smem + kOffQ + kTile) + (o_cnt & 1) * 512;  // [factor, sum][sub][row]
+                const float lam = -__ldg(p.lam + head);
+                x[sub * kRows + r] = has ? 1.f / l : 0.f;
+                float y[64];
+#pragma unroll
+                for (int i = 0; i < 64; ++i) y[i] = 0.f;
+                float z[64];
+                if (nt > 0) {
+                    if (!(ok = wait_bar_warp(ctx, bar(kODone0), o_cnt & 1))) break;
+                    if (!(ok = wait_bar_warp(ctx, bar(kODone1), o_cnt & 1))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float v0[32], v1[32];
+                        tmem_ld32(tmem + tl + 256 + sub * 64 + c * 32, v0);
+                        tmem_ld32(tmem + tl + 384 + sub * 64 + c * 32, v1);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            y[c * 32 + i] = v0[i];
+                            z[c * 32 + i] = v1[i];
+                        }
+                    }
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    mbar_arrive(bar(kOFree0));
+                    mbar_arrive(bar(kOFree1));
+                    mbar_arrive(bar(kMeet0 + q4));
+                    if (!(ok = wait_bar_warp(ctx, bar(kMeet0 + q4), meet & 1))) break;
+                    ++meet;
+                    const float f0 = x[r], f1 = x[kRows + r];
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) y[i] = fmaf(lam, __fmul_rn(z[i], f1), __fmul_rn(y[i], f0));  // (equal maps cancel exactly)
+                    float f = p.out_scale;
+                    if (p.norm) {
+                        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) s4[i & 3] = fmaf(y[i], y[i], s4[i & 3]);
+                        x[256 + sub * kRows + r] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                        mbar_arrive(bar(kMeet0 + q4));
+                        if (!(ok = wait_bar_warp(ctx, bar(kMeet0 + q4), meet & 1))) break;
+                        ++meet;
+                        f *= rsqrtf((x[256 + r] + x[256 + kRows + r]) * (1.f / kD) + p.norm_eps);
+                        const float4 *nw = reinterpret_cast<const float4 *>(p.norm) + sub * 16;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float4 n4 = __ldg(nw + i);
+                            y[4 * i] *= n4.x; y[4 * i + 1] *= n4.y; y[4 * i + 2] *= n4.z; y[4 * i + 3] *= n4.w;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) y[i] *= f;
+                    ++o_cnt;
+                }
+                const size_t orow = (size_t)(w.q_tok0 + r / g) * p.H_qo + head;
+                const int n_rows = w.n_pos * g;
+                const uint32_t stg = sb + kOffStg + (warp - 2) * kStgWarp;
+                const int cc = lane & 7;
+                unsigned long long orr[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) orr[i] = __shfl_sync(0xffffffffu, (unsigned long long)orow, 4 * i + (lane >> 3));
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float *v = y + q * 8;
+                    st_shared_v4(stg + lane * 128 + ((q ^ (lane & 7)) << 4), dev::pack_bf16(v[0], v[1]), dev::pack_bf16(v[2], v[3]),
+                                 dev::pack_bf16(v[4], v[5]), dev::pack_bf16(v[6], v[7]));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = 4 * i + (lane >> 3);
+                    const uint4 val = ld_shared_v4(stg + rr * 128 + ((cc ^ (rr & 7)) << 4));
+                    if (q4 * 32 + rr < n_rows)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + orr[i] * kD + sub * 64 + cc * 8) = val;
+                }
+                __syncwarp();
+                if (r < n_rows && p.lse) p.lse[orow * 2 + sub] = lse_v;
+                continue;
+            }
             float ov[kD];
             if (nt > 0) {
                 if (!(ok = wait_bar_warp(ctx, bar(kODone0 + sub), o_cnt & 1))) break;
@@ -848,6 +945,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 tmem_wait_ld();
                 tc_fence_before();
                 mbar_arrive(bar(kOFree0 + sub));
+                if constexpr (kDiff) mbar_arrive(bar(kOFree0 + (sub ^ 1)));  // (this group reads nothing of the other's O)
             } else {
 #pragma unroll
                 for (int i = 0; i < kD; ++i) ov[i] = 0.f;
@@ -856,7 +954,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
             float inv = has ? 1.f / l : 0.f;
             float lse_v = has ? (m + log2f(l)) * dev::kLn2 : -INFINITY;
             const size_t orow = (size_t)(w.q_tok0 + rt / g) * p.H_qo + (size_t)w.kv_head * g + (rt % g);
-            const size_t prow = (size_t)w.slot * p.tile_rows + rt;
+            const size_t prow = (size_t)w.slot * p.tile_rows + (kDiff ? sub * kRows + r : rt);
             const int n_rows = w.n_pos * g;  // real rows of the tile
             if (p.sink && w.slot < 0 && rt < n_rows) inv *= dev::fold_sink(lse_v, p.sink[w.kv_head * g + rt % g]);
             if (kFp8 && w.slot < 0 && nt == 0) {
@@ -1074,14 +1172,15 @@ namespace {
 int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                        const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
                        float sm_scale, void *o, float *lse, void *region8, int64_t region_pages, void *workspace,
-                       cudaStream_t stream) {
+                       cudaStream_t stream, const bsp_differential *diff) {
     const bool copied = region8 != nullptr;                // e4m3 cache, converted into region8 first
     const bool fp8 = k_exp != nullptr && !copied;          // e4m3 cache, converted inside the kernel
     const bsp_problem &P = plan->problem;
-    const int g = plan->group;
+    const int maps = diff ? 2 : 1;                         // the plan's heads per head of q
+    const int g = plan->group / maps;
     if (P.dtype != BSP_DTYPE_BF16) return fail(BSP_ERR_UNSUPPORTED, "prefill supports bf16 only");
     if (P.head_dim != kD) return fail(BSP_ERR_UNSUPPORTED, "prefill supports head_dim 128 only");
-    if (plan->tile_rows != kSub * kRows || kRows % g != 0)
+    if (plan->tile_rows != kSub * kRows || kRows % plan->group != 0)
         return fail(BSP_ERR_UNSUPPORTED, "prefill needs 256-row tiles and 128 % g == 0");
     // Pages of 8 or more tokens (powers of two) are gathered by TMA, one tensor
     // copy per page box. Other page sizes: when the workspace has a gather
@@ -1098,7 +1197,7 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
     std::memset(&tk, 0, sizeof(tk));
     std::memset(&tv, 0, sizeof(tv));
     const int box_rows = gather || copied ? kKvTile : tma ? (ps < kKvTile ? ps : kKvTile) : 1;
-    int rc = make_tmap_bf16(&tq, q, kD, P.num_qo_heads, (uint64_t)(plan->num_qo_tokens > 0 ? plan->num_qo_tokens : 1), g,
+    int rc = make_tmap_bf16(&tq, q, kD, P.num_qo_heads / maps, (uint64_t)(plan->num_qo_tokens > 0 ? plan->num_qo_tokens : 1), g,
                       kRows / g);
     if (gather) {
         const uint8_t *region = static_cast<const uint8_t *>(workspace) + plan->off_gather;
@@ -1161,24 +1260,30 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
     p.num_pages = (int)num_pages;
     p.raw_box = ps < kKvTile ? ps : kKvTile;
     if (p.soft_cap_on) p.scale_log2 = P.logits_soft_cap * dev::kLog2e;
-    p.H_qo = P.num_qo_heads;
+    p.H_qo = P.num_qo_heads / maps;
     p.g = g;
+    p.lam = diff ? diff->lambda : nullptr;
+    p.norm = diff ? diff->norm_weight : nullptr;
+    p.norm_eps = diff ? diff->norm_eps : 0.f;
+    p.out_scale = diff ? diff->out_scale : 1.f;
     p.page_size = P.page_size;
     p.box_rows = box_rows;
     p.contig = gather || copied ? 1 : 0;
     p.causal = P.causal;
     p.tile_rows = plan->tile_rows;
 
-    static bool configured[10][64] = {{false}};
+    static bool configured[14][64] = {{false}};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(BSP_ERR_CUDA, "no current CUDA device");
     const bool var = P.window_left > 0 || P.logits_soft_cap > 0.f;
-    auto kern = tma8 ? (var ? prefill_kernel<true, true, true> : prefill_kernel<true, false, true>)
+    auto kern = diff ? (tma ? (var ? prefill_kernel<true, true, false, true, true> : prefill_kernel<true, false, false, true, true>)
+                            : (var ? prefill_kernel<false, true, false, true, true> : prefill_kernel<false, false, false, true, true>))
+                : tma8 ? (var ? prefill_kernel<true, true, true> : prefill_kernel<true, false, true>)
                 : fp8 ? (var ? prefill_kernel<false, true, true> : prefill_kernel<false, false, true>)
                 : copied ? (var ? prefill_kernel<true, true, false, true> : prefill_kernel<true, false, false, true>)
                 : tma ? (var ? prefill_kernel<true, true> : prefill_kernel<true, false>)
                     : (var ? prefill_kernel<false, true> : prefill_kernel<false, false>);
-    const int which = (copied ? 8 : tma8 ? 6 : fp8 ? 4 : tma ? 2 : 0) + (var ? 1 : 0);
+    const int which = (diff ? (tma ? 12 : 10) : copied ? 8 : tma8 ? 6 : fp8 ? 4 : tma ? 2 : 0) + (var ? 1 : 0);
     if (!configured[which][dev]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("prefill smem attribute: ") + cudaGetErrorString(e));
@@ -1201,17 +1306,17 @@ int launch_prefill_any(const bsp_plan_info *plan, const void *q, const void *k_p
 
 int launch_prefill(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                    const int32_t *kv_indices, int64_t num_pages, float sm_scale, void *o, float *lse,
-                   void *workspace, cudaStream_t stream) {
+                   void *workspace, cudaStream_t stream, const bsp_differential *diff) {
     return launch_prefill_any(plan, q, k_pages, v_pages, nullptr, nullptr, kv_indices, num_pages, sm_scale, o, lse,
-                              nullptr, 0, workspace, stream);
+                              nullptr, 0, workspace, stream, diff);
 }
 
 int launch_prefill_fp8_block(const bsp_plan_info *plan, const void *q, const void *k_pages, const void *v_pages,
                              const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
                              float sm_scale, void *o, float *lse, void *region, int64_t region_pages, void *workspace,
-                             cudaStream_t stream) {
+                             cudaStream_t stream, const bsp_differential *diff) {
     return launch_prefill_any(plan, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse, region,
-                              region_pages, workspace, stream);
+                              region_pages, workspace, stream, diff);
 }
 
 }  // namespace bsp

@@ -506,6 +506,49 @@ int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const vo
                               float sm_scale, void *o, float *lse, void *region, size_t region_bytes,
                               void *workspace, bsp_stream_t stream);
 
+/*
+ * ---- differential attention ---------------------------------------------------
+ *
+ * (No counterpart on the pages.) A row of q and of k is two halves of 64 values, and a
+ * head's output is the difference of the two halves' softmax maps on the whole rows of v:
+ *     s_mij = sm_scale * <q[i, h] half m, k_j half m>,  P_m = softmax over j,  LSE_m
+ *     y     = (P_1 - lambda[h] P_2) v
+ *     o     = y * out_scale, or with norm_weight y / sqrt(mean(y^2) + norm_eps) * norm_weight
+ *             * out_scale (mean over the head's 128 values; rounded once, at the end)
+ * Masks, window and soft-cap are the plan's and hold for both maps; a query without a
+ * visible key gets 0. The cache is laid out as for any other run, so page tables, appends
+ * and bsp_compact_cache are the same.
+ *   plan         from bsp_plan over twice the heads: problem.num_qo_heads = 2 * H_q (the
+ *                maps), head_dim 128, bf16, no sink
+ *   q, o         device, bf16 [n_tokens, H_q, 128]
+ *   lse          device, float [n_tokens, H_q, 2], LSE_1 and LSE_2; may be NULL
+ *   k_exp, v_exp NULL (bf16 pools), or the exponents of an 8-bit cache
+ *   region       as for bsp_decode_run_fp8_block (bsp_decode_fp8_region_size). A prefill over
+ *                the 8-bit cache needs one of bsp_prefill_diff_region_size bytes (32-byte
+ *                aligned; the workspace's copy region serves)
+ *   the other arguments as for bsp_decode_run / bsp_prefill_run, num_pages > 0
+ * Supported: decode H_q / H_kv <= 8, prefill 64 % (H_q / H_kv) == 0; any page size.
+ */
+typedef struct bsp_differential {
+    const float *lambda;      /* device [H_q]                                      */
+    const float *norm_weight; /* device [128], 16-byte aligned, or NULL: no norm   */
+    float norm_eps;           /* >= 0                                              */
+    float out_scale;          /* factor of the output                              */
+} bsp_differential;
+
+int bsp_decode_run_diff(const bsp_plan_info *plan, const bsp_differential *diff, const void *q, const void *k_pages,
+                        const void *v_pages, const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices,
+                        int64_t num_pages, float sm_scale, void *o, float *lse, void *region, size_t region_bytes,
+                        void *workspace, bsp_stream_t stream);
+int bsp_prefill_run_diff(const bsp_plan_info *plan, const bsp_differential *diff, const void *q, const void *k_pages,
+                         const void *v_pages, const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices,
+                         int64_t num_pages, float sm_scale, void *o, float *lse, void *region, size_t region_bytes,
+                         void *workspace, bsp_stream_t stream);
+
+/* Bytes of the region of a differential prefill over the 8-bit cache (a bf16 copy of its
+ * page table's K and V), 0 for an empty table. */
+size_t bsp_prefill_diff_region_size(const bsp_plan_info *plan);
+
 /* Bytes of the region that bsp_decode_run_fp8_block wants for this plan (pages of one
  * token and 2560 tokens of work or more per CTA, or of two and 5120), or 0 where it is
  * faster without. */
