@@ -14,49 +14,14 @@
 
 #include "bsp_internal.h"
 #include "device_common.cuh"
-#include "sm100.cuh"
+#include "evict.cuh"
 
 namespace bsp {
 namespace {
 
 using namespace dev;
+using namespace evict;
 namespace cg = cooperative_groups;
-
-constexpr uint32_t kNoRow = ~0u;  // a token that is not there, or whose page id is outside the pool
-
-// The page table of a batch. Values out of range are read as the nearest in range, so that a
-// malformed table reads and writes nothing outside the arrays.
-struct Csr {
-    const int32_t *kv_indptr, *kv_indices, *last_page_len;
-    int max_pages;  // entries of kv_indices
-    int batch, ps, num_pages;
-};
-
-struct Request {
-    int p0, len;  // first table entry, tokens
-};
-
-__device__ __forceinline__ int clamp_page(const Csr &c, int i) { return min(max(__ldg(c.kv_indptr + i), 0), c.max_pages); }
-
-__device__ __forceinline__ Request request(const Csr &c, int b) {
-    const int p0 = clamp_page(c, b), n = clamp_page(c, b + 1) - p0;
-    const int last = min(max(__ldg(c.last_page_len + b), 0), c.ps);
-    return {p0, n > 0 ? (int)min((long long)(n - 1) * c.ps + last, (long long)INT_MAX) : 0};
-}
-
-// Slot of token t of a request, or kNoRow (host: num_pages * ps < 2^32 - 1).
-__device__ __forceinline__ uint32_t slot_of(const Csr &c, const Request &r, int t, int &page, int &place) {
-    const int col = t / c.ps;
-    place = t - col * c.ps;
-    page = __ldg(c.kv_indices + r.p0 + col);
-    return (unsigned)page < (unsigned)c.num_pages ? (uint32_t)page * (uint32_t)c.ps + (uint32_t)place : kNoRow;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // 2^e for e in [-149, 127]
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float(e >= -126 ? (e + 127) << 23 : 0x00400000 >> (-127 - e)); }
@@ -67,47 +32,7 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float(e >= -126 
 // (differential: p = |p1 - lam_r p2|), base = decay * w[j, h], or 0 for the last qo_len keys,
 // the queries' own. Every key is summed by one thread group in one order: no atomics, the
 // same result every time.
-struct WeightsParams {
-    Csr csr;
-    const int32_t *qo_indptr;  // or null: one query per request
-    const void *q, *k;
-    const float *lse, *lam;
-    const int8_t *k_exp;
-    float *weights;
-    int n_tokens, H_qo, H_kv, g;
-    float scale_log2, cap_in, cap_out, decay;
-    int soft_cap_on, window;
-};
-
-// Virtual blocks of kTaskTokens tokens: request b's begin at floor(kv_indptr[b] * ps / kTaskTokens) + b,
-// which leaves room for ceil(len / kTaskTokens) of them without a prefix sum over the requests.
-constexpr int kTaskTokens = 64;
-
-__device__ __forceinline__ long long block_start(const Csr &c, int b) {
-    return (long long)clamp_page(c, b) * c.ps / kTaskTokens + b;
-}
-
-// A warp: the request of virtual block x (the last that begins at or before it).
-__device__ __forceinline__ int find_request(const Csr &c, long long x, int lane) {
-    int lo = 0, hi = c.batch;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, m = lo + (lane + 1) * step;
-        const unsigned le = __ballot_sync(0xffffffffu, m < hi && block_start(c, m) <= x);
-        lo += __popc(le) * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
-
-struct Queries {
-    int q0, n;  // first row of q, queries of the request
-};
-
-__device__ __forceinline__ Queries queries(const WeightsParams &p, int b) {
-    if (!p.qo_indptr) return {min(b, p.n_tokens), b < p.n_tokens ? 1 : 0};
-    const int a = min(max(__ldg(p.qo_indptr + b), 0), p.n_tokens), e = min(max(__ldg(p.qo_indptr + b + 1), a), p.n_tokens);
-    return {a, e - a};
-}
+constexpr int kTaskTokens = 64;  // keys of a warp's task
 
 // bf16 pools (and e4m3 ones with exponents): a warp takes 64 keys of one kv head. K rows go
 // straight from memory into the fragments of S = K Q^T (m16n8k16: keys on the M side, queries
@@ -123,14 +48,14 @@ __global__ void __launch_bounds__(256, 2) weights_kernel(const WeightsParams p) 
     constexpr int kCols = kDiff ? 4 : 8;        // (query, head) pairs per column tile
     const int lane = threadIdx.x & 31, c = lane & 3, n = lane >> 2;
     const int H = p.H_kv, g = p.g;
-    const long long blocks = block_start(p.csr, p.csr.batch);
+    const long long blocks = block_start<kTaskTokens>(p.csr, p.csr.batch);
     const long long nwarps = (long long)gridDim.x * (blockDim.x >> 5);
     for (long long task = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); task < blocks * H; task += nwarps) {
         const long long blk = task / H;
         const int h = (int)(task - blk * H);
-        const int b = find_request(p.csr, blk, lane);
+        const int b = find_request<kTaskTokens>(p.csr, blk, lane);
         const Request rq = request(p.csr, b);
-        const long long first = (blk - block_start(p.csr, b)) * kTaskTokens;
+        const long long first = (blk - block_start<kTaskTokens>(p.csr, b)) * kTaskTokens;
         if (first >= rq.len) continue;
         const int t0 = (int)first;
         const Queries qs = queries(p, b);
@@ -288,14 +213,14 @@ __global__ void __launch_bounds__(256) weights_f32_kernel(const WeightsParams p)
     constexpr int kJ = D / 32;
     const int lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3;
     const int H = p.H_kv, g = p.g;
-    const long long blocks = block_start(p.csr, p.csr.batch);
+    const long long blocks = block_start<kTaskTokens>(p.csr, p.csr.batch);
     const long long nwarps = (long long)gridDim.x * (blockDim.x >> 5);
     for (long long task = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); task < blocks * H; task += nwarps) {
         const long long blk = task / H;
         const int h = (int)(task - blk * H);
-        const int b = find_request(p.csr, blk, lane);
+        const int b = find_request<kTaskTokens>(p.csr, blk, lane);
         const Request rq = request(p.csr, b);
-        const long long first = (blk - block_start(p.csr, b)) * kTaskTokens;
+        const long long first = (blk - block_start<kTaskTokens>(p.csr, b)) * kTaskTokens;
         if (first >= rq.len) continue;
         const Queries qs = queries(p, b);
         const int off = rq.len - qs.n;
@@ -723,6 +648,8 @@ int launch_accumulate_weights(const bsp_problem *P, const void *q, const float *
     p.window = P->window_left;
     const int sms = current_sms();
     if (sms < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    if (!k_exp && weights_prefill_takes(P, num_pages, n_tokens, batch, qo_indptr))
+        return launch_weights_prefill(P, p, num_pages, max_table_pages, sms, stream);
     const int64_t tasks = (max_table_pages * P->page_size / kTaskTokens + batch) * P->num_kv_heads;
     const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((tasks + 7) / 8, (int64_t)sms * 2));
     const int D = P->head_dim;

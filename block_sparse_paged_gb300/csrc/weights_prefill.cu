@@ -1,0 +1,449 @@
+// Gathered attention weights of keys that many queries see (whole prompts, chunks, observation
+// windows), on the tcgen05 tensor cores: bf16 pools, head_dim 128, pages of a power of two from 8
+// tokens on. (What is summed: csrc/evict.cu, whose warp-level kernel takes everything else.)
+//
+// The score tile is transposed, S^T = K Q^T: 128 keys on the accumulator's lanes, 128 query rows
+// (positions x the g heads of the kv head) on its columns. A thread then owns a key and sums
+// exp(s - LSE) along its lane, so that a key's sum has one order without any exchange per tile, and LSE (a value per column) is read from shared memory four at a time, the same for
+// every lane. No maximum is searched (LSE is given) and nothing is multiplied by P, which leaves
+// per element one fused multiply-add, one exponential and one addition.
+//
+// A unit of work is 256 keys of one kv head and all query tiles that see any of them. 18 warps:
+//   warp 0      TMA: the unit's K (page boxes, 2 stages of 64 KB) and the Q tiles (2 stages of
+//               32 KB), and the tiles' -LSE log2 e (4 slots)
+//   warp 1      TMEM owner; one thread issues S^T of both 128-key halves per Q tile
+//   warps 2-9   keys 0..127, warps 10-17 keys 128..255: two threads per key, 64 columns of a tile
+//               each (one thread per key, 8 warps: 543 us for two prompts of about 7k, 512 so)
+// Each half has two accumulators, so that the tensor core fills one while the other is summed
+// (differential weights need both for the two maps of a tile).
+// Units go to CTAs in the order of the table; a request's first units have the most queries
+// under the causal mask. Long units run one per CTA, so that the block scheduler levels them.
+// Every wait is bounded; a wait that gives up makes NaN of the unit's weights.
+#include <cuda.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstring>
+#include <type_traits>
+
+#include "bsp_internal.h"
+#include "device_common.cuh"
+#include "evict.cuh"
+#include "sm100.cuh"
+
+namespace bsp {
+namespace {
+
+using namespace sm100;
+using namespace evict;
+
+constexpr int kD = 128;
+constexpr int kRows = 128;                 // keys of a half, query rows of a tile
+constexpr int kUnit = 256;                 // keys of a unit
+constexpr int kThreads = 576;
+constexpr int kSlab = 16384;               // [128 rows][64 bf16], 128-byte swizzle
+constexpr int kTile = 2 * kSlab;
+// Six tiles: long units have one stage of K (two tiles) and four of Q, so that Q's latency is
+// covered; short ones two of each, so that the next unit's K is.
+constexpr int kMaxKStages = 2, kMaxQStages = 4, kLSlots = 4;
+constexpr int kOffK = 0;
+constexpr int kOffL = 6 * kTile;                           // per slot: -LSE (both maps), lambda [128] each
+constexpr int kLBytes = 3 * kRows * 4;
+constexpr int kOffBar = kOffL + kLSlots * kLBytes;
+enum Bar {
+    kKFull0 = 0, kKEmpty0 = kKFull0 + kMaxKStages, kQFull0 = kKEmpty0 + kMaxKStages, kQEmpty0 = kQFull0 + kMaxQStages,
+    kLFull0 = kQEmpty0 + kMaxQStages, kLEmpty0 = kLFull0 + kLSlots,
+    kSFull0 = kLEmpty0 + kLSlots,  // [half][accumulator]
+    kSEmpty0 = kSFull0 + 4, kMeet0 = kSEmpty0 + 4,  // [half][lane quarter]
+    kNumBars = kMeet0 + 8
+};
+constexpr int kOffMisc = kOffBar + kNumBars * 8;           // TMEM slot, abort flag, odd-LSE flags of the slots
+constexpr int kOffPart = kOffMisc + 8 + 4 * kLSlots;         // [2 units][256 keys]: the second warps' sums
+constexpr int kSmemBytes = kOffPart + 2 * kUnit * 4 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "tiles exceed shared memory");
+constexpr uint32_t kTmemCols = 512;
+constexpr long long kWaitLimitCycles = 4000000000ll;       // about 2 s at 2 GHz: a fault, not a stall
+
+struct PrefillWeights {
+    WeightsParams w;
+    int box_rows;
+};
+
+// What every warp needs of a unit.
+struct Unit {
+    int b, h, t0;         // request, kv head, first key
+    Request rq;
+    Queries qs;
+    int off;              // position of the first query
+    int tile0, tiles;     // query tiles that see a key of the unit
+};
+
+// A warp: unit u, or false where the table's virtual block is empty.
+__device__ __forceinline__ bool unit_at(const WeightsParams &p, long long u, int lane, Unit &x) {
+    const long long blk = u / p.H_kv;
+    x.h = (int)(u - blk * p.H_kv);
+    x.b = find_request<kUnit>(p.csr, blk, lane);
+    x.rq = request(p.csr, x.b);
+    const long long first = (blk - block_start<kUnit>(p.csr, x.b)) * kUnit;
+    if (first >= x.rq.len) return false;
+    x.t0 = (int)first;
+    x.qs = queries(p, x.b);
+    x.off = x.rq.len - x.qs.n;
+    const int ppt = kRows / p.g;  // positions per tile
+    const int i_lo = max(0, x.t0 - x.off);
+    const int i_hi = p.window > 0 ? (int)min((long long)x.qs.n, (long long)x.t0 + kUnit + p.window - x.off) : x.qs.n;
+    x.tile0 = i_lo / ppt;
+    x.tiles = i_hi > i_lo ? (i_hi - x.tile0 * ppt + ppt - 1) / ppt : 0;
+    return true;
+}
+
+__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b, float c0, float c1) {
+    asm("{ .reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %4};\n mov.b64 rc, {%5, %6};\n"
+        " fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1) {
+    asm("{ .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rd, ra, rb;\n"
+        " mov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(d0), "f"(d1), "f"(a0), "f"(a1));
+}
+// kVar: soft-cap compiled in. kDiff: differential weights. kLong: units of many query tiles.
+template <bool kVar, bool kDiff, bool kLong>
+__global__ void __launch_bounds__(kThreads, 1)
+    weights_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const PrefillWeights pp) {
+    constexpr int kKStages = kLong ? 1 : 2, kQStages = kLong ? 4 : 2, kOffQ = kOffK + kKStages * 2 * kTile;
+    const WeightsParams &p = pp.w;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = dev::smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const long long units = block_start<kUnit>(p.csr, p.csr.batch) * p.H_kv;
+    // leave before anything is set up if no unit of this CTA holds a key
+    bool any = false;
+    Unit x;
+    long long u0 = blockIdx.x;
+    for (; u0 < units && !any; u0 += any ? 0 : gridDim.x) any = unit_at(p, u0, lane, x);
+    if (!any) return;  // (the same for every warp)
+
+    auto bar = [&](int i) { return sb + kOffBar + 8u * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
+    volatile int *odd = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
+    if (tid == 0) {
+        for (int i = 0; i < kNumBars; ++i)
+            mbar_init(bar(i), i >= kLFull0 && i < kLEmpty0 ? 32 : i >= kLEmpty0 && i < kSFull0 ? 16 : i >= kMeet0 ? 64 : i >= kSEmpty0 ? 8 : 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tq);
+        prefetch_tmap(&tk);
+    }
+    if (warp == 1) {
+        tmem_alloc(dev::smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait1 = [&](uint32_t b, uint32_t parity) -> bool {
+        if (mbar_wait_spin(b, parity, kWaitLimitCycles, abort_flag)) return true;
+        *abort_flag = 1;
+        return false;
+    };
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait1(b, parity)); };
+    const int g = p.g, ppt = kRows / g;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA
+        int kn = 0, n = 0;  // units and tiles so far
+        bool ok = true;
+        for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            if (!unit_at(p, u, lane, x) || x.tiles == 0) continue;
+            // K: box l of the unit (box_rows keys of a page) by lane l
+            const int ks = kn % kKStages;
+            const int t = x.t0 + lane * pp.box_rows;
+            uint32_t slot = kNoRow;
+            int page, place;
+            if (lane * pp.box_rows < kUnit && t < x.rq.len) slot = slot_of(p.csr, x.rq, t, page, place);
+            const int boxes = __popc(__ballot_sync(0xffffffffu, slot != kNoRow));
+            if (!(ok = wait(bar(kKEmpty0 + ks), ((kn / kKStages) & 1) ^ 1))) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(kKFull0 + ks), (uint32_t)boxes * pp.box_rows * 256);
+            __syncwarp();
+            if (slot != kNoRow) {
+                const int key = lane * pp.box_rows;  // (a box lies in one half: box_rows <= 128)
+                const uint32_t d = sb + kOffK + ks * 2 * kTile + (key >> 7) * kTile + (key & 127) * 128;
+                tma_load_3d(d, &tk, bar(kKFull0 + ks), 0, x.h, (int)slot);
+                tma_load_3d(d + kSlab, &tk, bar(kKFull0 + ks), 64, x.h, (int)slot);
+            }
+            ++kn;
+            // -LSE log2 e of a tile's columns, read a tile ahead
+            float a[4], a2[4], lm[4];
+            auto columns = [&](int i) {
+                const int pos0 = (x.tile0 + i) * ppt, rows = min(kRows, (x.qs.n - pos0) * g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = lane + 32 * j, i_c = c / g, r = c - i_c * g;
+                    const size_t row = (size_t)(x.qs.q0 + pos0 + i_c) * p.H_qo + (size_t)x.h * g + r;
+                    a[j] = a2[j] = lm[j] = 0.f;
+                    if (i < x.tiles && c < rows) {
+                        if (kDiff) {
+                            const float2 z = __ldg(reinterpret_cast<const float2 *>(p.lse) + row);
+                            a[j] = z.x;
+                            a2[j] = z.y;
+                            lm[j] = __ldg(p.lam + x.h * g + r);
+                        } else {
+                            a[j] = __ldg(p.lse + row);
+                        }
+                    }
+                }
+            };
+            columns(0);
+            for (int i = 0; i < x.tiles && ok; ++i, ++n) {
+                const int qst = n % kQStages, sl = n % kLSlots, pos0 = (x.tile0 + i) * ppt;
+                if (!(ok = wait(bar(kQEmpty0 + qst), ((n / kQStages) & 1) ^ 1))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(kQFull0 + qst), kTile);
+                    const uint32_t d = sb + kOffQ + qst * kTile;
+                    tma_load_3d(d, &tq, bar(kQFull0 + qst), 0, x.h * g, x.qs.q0 + pos0);
+                    tma_load_3d(d + kSlab, &tq, bar(kQFull0 + qst), 64, x.h * g, x.qs.q0 + pos0);
+                }
+                if (!(ok = wait(bar(kLEmpty0 + sl), ((n / kLSlots) & 1) ^ 1))) break;
+                float *l = reinterpret_cast<float *>(smem + kOffL + sl * kLBytes);
+                bool strange = false;  // a query that saw no key
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    strange |= a[j] == -INFINITY || a2[j] == -INFINITY;
+                    l[lane + 32 * j] = a[j] * -dev::kLog2e;
+                    if (kDiff) {
+                        l[kRows + lane + 32 * j] = a2[j] * -dev::kLog2e;
+                        l[2 * kRows + lane + 32 * j] = -lm[j];
+                    }
+                }
+                strange = __any_sync(0xffffffffu, strange);
+                if (lane == 0) odd[sl] = strange;
+                mbar_arrive(bar(kLFull0 + sl));
+                columns(i + 1);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        constexpr uint32_t id = idesc_bf16_f32(kRows, kRows, false, false);
+        int kn = 0, n = 0;
+        bool ok = true;
+        for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            if (!unit_at(p, u, lane, x) || x.tiles == 0) continue;
+            if (lane == 0) {
+                const int ks = kn % kKStages;
+                ok = wait1(bar(kKFull0 + ks), (kn / kKStages) & 1);
+                for (int i = 0; i < x.tiles && ok; ++i) {
+                    const int m = n + i, qst = m % kQStages;
+                    if (!(ok = wait1(bar(kQFull0 + qst), (m / kQStages) & 1))) break;
+                    const uint32_t sq = sb + kOffQ + qst * kTile, sk = sb + kOffK + ks * 2 * kTile;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        // accumulator m & 1 of the half; differential: both, one per map
+                        const int acc = kDiff ? 0 : m & 1, use = kDiff ? m : m >> 1;
+                        if (!(ok = wait1(bar(kSEmpty0 + 2 * half + acc), (use & 1) ^ 1))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < kD / 16; ++kk) {
+                            const uint32_t o = (kk >> 2) * kSlab + (kk & 3) * 32;
+                            mma_bf16_ss(tmem + half * 256 + (kDiff ? kk >> 2 : acc) * 128, smem_desc_sw128(sk + half * kTile + o, 16, 1024),
+                                        smem_desc_sw128(sq + o, 16, 1024), id, kDiff ? (kk & 3) > 0 : kk > 0);
+                        }
+                        mma_commit(bar(kSFull0 + 2 * half + acc));
+                    }
+                    if (ok) mma_commit(bar(kQEmpty0 + qst));
+                }
+                if (ok) mma_commit(bar(kKEmpty0 + ks));
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+            n += x.tiles;
+            ++kn;
+        }
+    } else {
+        // ------------------------------------------------------------ sums
+        const int half = (warp - 2) >> 3, q4 = warp & 3, col0 = ((warp - 2) >> 2 & 1) * 64;
+        const int key = half * kRows + q4 * 32 + lane;
+        const uint32_t tS = tmem + ((uint32_t)(q4 * 32) << 16) + half * 256;
+        int n = 0, meet = 0;
+        bool ok = true;
+        for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            if (!unit_at(p, u, lane, x)) continue;
+            const int t = x.t0 + key;
+            int page = 0, place = 0;
+            const uint32_t slot = t < x.rq.len ? slot_of(p.csr, x.rq, t, page, place) : kNoRow;
+            float *at = p.weights + ((size_t)page * p.H_kv + x.h) * p.csr.ps + place;
+            const float old = !col0 && slot != kNoRow && t < x.off && p.decay != 0.f ? *at : 0.f;
+            float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+            for (int i = 0; i < x.tiles; ++i, ++n) {
+                const int pos0 = (x.tile0 + i) * ppt, rows = min(kRows, (x.qs.n - pos0) * g);
+                const int acc = kDiff ? 0 : n & 1, use = kDiff ? n : n >> 1, sl = n % kLSlots;
+                if (!(ok = wait(bar(kLFull0 + sl), (n / kLSlots) & 1))) break;
+                if (!(ok = wait(bar(kSFull0 + 2 * half + acc), use & 1))) break;
+                tc_fence_after();
+                const float4 *lse = reinterpret_cast<const float4 *>(smem + kOffL + sl * kLBytes);
+                // columns that see this key: positions t .. t + window
+                const int c_lo = max(0, t - x.off - pos0) * g;
+                int c_hi = rows;
+                if (p.window > 0) c_hi = (int)max(0ll, min((long long)rows, ((long long)t - x.off - pos0 + p.window + 1) * g));
+                const bool full = __all_sync(0xffffffffu, c_lo <= 0 && c_hi == kRows) && !odd[sl];
+                const unsigned width = (unsigned)max(0, c_hi - c_lo);
+                const float scale = kVar && p.soft_cap_on ? p.cap_out : p.scale_log2;
+                // 32 columns from c on: v (and v2, the second map's)
+                auto add32 = [&](auto whole, int c, float (&v)[32], float (&v2)[kDiff ? 32 : 1]) {
+                    constexpr bool kFull = decltype(whole)::value;
+                    if (kVar && p.soft_cap_on) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            v[j] = dev::tanh_ex2(v[j] * p.cap_in);
+                            if constexpr (kDiff) v2[j] = dev::tanh_ex2(v2[j] * p.cap_in);
+                        }
+                    }
+                    float4 lr[8], l2r[kDiff ? 8 : 1], lmr[kDiff ? 8 : 1];  // all loads before the first use
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        lr[j] = lse[c / 4 + j];
+                        if constexpr (kDiff) {
+                            l2r[j] = lse[(kRows + c) / 4 + j];
+                            lmr[j] = lse[(2 * kRows + c) / 4 + j];
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 l = lr[j / 4];
+                        fma2(v[j], v[j + 1], v[j], v[j + 1], scale, l.x, l.y);
+                        fma2(v[j + 2], v[j + 3], v[j + 2], v[j + 3], scale, l.z, l.w);
+                        float e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) e[k] = ex2(v[j + k]);
+                        const float lc[4] = {l.x, l.y, l.z, l.w};
+                        if constexpr (kDiff) {
+                            const float4 l2 = l2r[j / 4], lm = lmr[j / 4];
+                            fma2(v2[j], v2[j + 1], v2[j], v2[j + 1], scale, l2.x, l2.y);
+                            fma2(v2[j + 2], v2[j + 3], v2[j + 2], v2[j + 3], scale, l2.z, l2.w);
+                            const float lc2[4] = {l2.x, l2.y, l2.z, l2.w}, lam[4] = {lm.x, lm.y, lm.z, lm.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float e2 = ex2(v2[j + k]);
+                                if constexpr (!kFull) {
+                                    e[k] = lc[k] == INFINITY ? 0.f : e[k];
+                                    e2 = lc2[k] == INFINITY ? 0.f : e2;
+                                }
+                                e[k] = fabsf(fmaf(lam[k], e2, e[k]));
+                            }
+                        }
+                        if constexpr (!kFull) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                e[k] = (unsigned)(c + j + k - c_lo) < width && (kDiff || lc[k] != INFINITY) ? e[k] : 0.f;
+                        }
+                        add2(s0, s1, e[0], e[1]);
+                        add2(s2, s3, e[2], e[3]);
+                    }
+                };
+                const uint32_t tA = tS + acc * 128;
+                // (two copies of the loop: with a branch per group of columns 756 us instead of 543)
+                auto add_tile = [&](auto whole) {
+                    if constexpr (kDiff) {
+#pragma unroll 1
+                        for (int c = col0; c < col0 + 64; c += 32) {
+                            float v[32], v2[32];
+                            tmem_ld32(tS + c, v);
+                            tmem_ld32(tS + 128 + c, v2);
+                            tmem_wait_ld();
+                            add32(whole, c, v, v2);
+                        }
+                    } else {
+                        float va[32], vb[32], none[1];
+                        tmem_ld32(tA + col0, va);
+                        tmem_wait_ld();
+                        tmem_ld32(tA + col0 + 32, vb);  // read while the first 32 are summed
+                        add32(whole, col0, va, none);
+                        tmem_wait_ld();
+                        add32(whole, col0 + 32, vb, none);
+                    }
+                };
+                if (full) add_tile(std::true_type{});
+                else add_tile(std::false_type{});
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(kSEmpty0 + 2 * half + acc));
+                    mbar_arrive(bar(kLEmpty0 + sl));
+                }
+            }
+            // the columns' two halves
+            float *part = reinterpret_cast<float *>(smem + kOffPart) + (meet & 1) * kUnit + key;
+            const float sum = (s0 + s1) + (s2 + s3);
+            if (col0) *part = sum;
+            mbar_arrive(bar(kMeet0 + half * 4 + q4));
+            ok = ok && wait(bar(kMeet0 + half * 4 + q4), meet & 1);
+            ++meet;
+            if (!col0 && slot != kNoRow) *at = ok ? fmaf(p.decay, old, sum + *part) : NAN;
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        // let copies and MMAs already in flight finish before TMEM is released
+        for (int i = 0; i < 100; ++i) __nanosleep(1000);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+}  // namespace
+
+bool weights_prefill_takes(const bsp_problem *P, int64_t num_pages, int64_t n_tokens, int32_t batch, const int32_t *qo_indptr) {
+    const int g = P->num_qo_heads / P->num_kv_heads, ps = P->page_size;
+    return qo_indptr && P->dtype == BSP_DTYPE_BF16 && P->head_dim == kD && kRows % g == 0 && ps >= 8 && (ps & (ps - 1)) == 0 &&
+           num_pages * (int64_t)ps <= INT32_MAX && n_tokens * g >= (int64_t)batch * 32;
+}
+
+int launch_weights_prefill(const bsp_problem *P, const evict::WeightsParams &w, int64_t num_pages, int64_t max_table_pages,
+                           int sms, cudaStream_t stream) {
+    PrefillWeights p;
+    p.w = w;
+    p.box_rows = std::min(P->page_size, kRows);
+    CUtensorMap tq, tk;
+    std::memset(&tq, 0, sizeof(tq));
+    std::memset(&tk, 0, sizeof(tk));
+    int rc = make_tmap_bf16(&tq, w.q, kD, P->num_qo_heads, (uint64_t)w.n_tokens, w.g, kRows / w.g);
+    if (rc == BSP_OK) rc = make_tmap_bf16(&tk, w.k, kD, P->num_kv_heads, (uint64_t)num_pages * P->page_size, 1, p.box_rows);
+    if (rc != BSP_OK) return rc;
+    const bool diff = w.lam != nullptr, var = w.soft_cap_on;
+    // units of many tiles: a CTA each; of few: persistent CTAs, whose next unit's K is on its way
+    const int64_t units = (max_table_pages * P->page_size / kUnit + w.csr.batch) * P->num_kv_heads;
+    const bool longer = (int64_t)w.n_tokens * w.g / w.csr.batch >= 8 * kRows;
+    auto pick = [&](auto l) {
+        constexpr bool kLong = decltype(l)::value;
+        return diff ? (var ? weights_prefill_kernel<true, true, kLong> : weights_prefill_kernel<false, true, kLong>)
+                    : (var ? weights_prefill_kernel<true, false, kLong> : weights_prefill_kernel<false, false, kLong>);
+    };
+    auto kern = longer ? pick(std::true_type{}) : pick(std::false_type{});
+    static bool configured[8][64] = {{false}};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    bool &done = configured[(longer ? 4 : 0) + (diff ? 2 : 0) + (var ? 1 : 0)][dev];
+    if (!done) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("weights smem attribute: ") + cudaGetErrorString(e));
+        done = true;
+    }
+    const unsigned grid = (unsigned)std::max<int64_t>(1, longer ? units : std::min<int64_t>(units, sms));
+    kern<<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("weights launch: ") + cudaGetErrorString(e));
+    return BSP_OK;
+}
+
+}  // namespace bsp
