@@ -15,6 +15,7 @@
 #include "bsp_internal.h"
 #include "device_common.cuh"
 #include "evict.cuh"
+#include "sm100.cuh"
 
 namespace bsp {
 namespace {
@@ -32,181 +33,317 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float(e >= -126 
 // (differential: p = |p1 - lam_r p2|), base = decay * w[j, h], or 0 for the last qo_len keys,
 // the queries' own. Every key is summed by one thread group in one order: no atomics, the
 // same result every time.
-constexpr int kTaskTokens = 64;  // keys of a warp's task
+// bf16 pools (and e4m3 ones with exponents), few queries per request: bound by the read of K.
+// One persistent CTA per SM takes a contiguous run of tasks (32 keys of one kv head, in the order
+// request, head, keys), so that every SM reads the same number of keys and a query's fragments
+// stay in a warp's registers from task to task.
+//   6 warps (8 over rows of 128 bytes) look tokens up, a task each in turn, and leave rows,
+//     weights and exponents in a ring: the chain of dependent reads (request, page id, weight) runs ahead of the
+//     warps that need it (4 warps: 109 us instead of 100 below, 46 instead of 37 over e4m3)
+//   12 (16) warps compute, a task each in turn: 16-byte asynchronous copies bring the rows of the
+//     next task into the warp's own two buffers (any page size alike) while one is worked on;
+//     S = K Q^T by m16n8k16, keys on the M side, queries on the N side. The order of the head
+//     dimension inside a product is free, so a lane's 16 adjacent bytes of a K row are fragment
+//     words as they are, and q is read the same way.
+// 64 requests up to 8192 tokens, us: warps that look up their own keys and load them into
+// registers 120, with a ring of bulk copies per warp 153, loader warps and bulk copies 198 (one
+// bulk copy per row: an SM starts one in about 25 cycles, whatever its size).
+constexpr int kTaskTokens = 32;
+constexpr long long kWaitLimitCycles = 4000000000ll;  // about 2 s at 2 GHz: a fault, not a stall
 
-// bf16 pools (and e4m3 ones with exponents): a warp takes 64 keys of one kv head. K rows go
-// straight from memory into the fragments of S = K Q^T (m16n8k16: keys on the M side, queries
-// on the N side): the order of the head dimension inside a product is free, so that a lane's
-// 16 adjacent bytes of a row are fragment words as they are, and q rows are read the same way.
-// Bound by the read of K: no shared memory, no barriers, 8 KB per warp in flight.
+template <int D, bool kE4m3>
+struct StreamLayout {
+    static constexpr int kRow = D * (kE4m3 ? 1 : 2);      // bytes of a K row
+    static constexpr int kLoaders = kRow == 256 ? 6 : 8, kCompute = 2 * kLoaders, kThreads = 32 * (kLoaders + kCompute);
+    static constexpr int kBufs = 2;                       // tasks' rows per compute warp
+    static constexpr int kBuf = kTaskTokens * kRow;
+    // ring of looked-up tasks: per token its weight's index, row, old weight and 2^exp; then
+    // request, head, first key, tokens
+    static constexpr int kStages = kBufs * kCompute + 2 * kLoaders;
+    static constexpr int kStageBytes = kTaskTokens * 20 + 16;
+    // A stage's look-ups have one order, and a barrier is never asked about a phase but the next: the
+    // stage always has the same loader, and a compute warp's task before comes from that loader too
+    // and not before the stage's previous one. (With 19 stages a loader could pass another one that
+    // still waited for the same stage.) A compute warp holds kBufs stages.
+    static_assert(kStages % kLoaders == 0 && kCompute % kLoaders == 0 && kStages >= kBufs * kCompute, "order of a stage's look-ups");
+    static constexpr int kRingOff = kCompute * kBufs * kBuf;
+    static constexpr int kBarOff = kRingOff + kStages * kStageBytes;
+    static constexpr int kSmem = kBarOff + 2 * kStages * 8 + 8;
+    static_assert(kSmem <= 227 * 1024, "weights ring exceeds shared memory");
+};
+
+// The queries' side of up to 8 columns: (query, head) pairs, differential 4 pairs of maps.
+template <int kSteps>
+struct Columns {
+    uint32_t q[kSteps][2];
+    float lse[2], scale[2], lam;  // of this lane's accumulator columns 2c, 2c + 1
+    int pos[2];                   // keys up to this place see them; -1: none
+};
+
 template <int D, bool kE4m3, bool kDiff>
-__global__ void __launch_bounds__(256, 2) weights_kernel(const WeightsParams p) {
-    constexpr int kRow = D * (kE4m3 ? 1 : 2);   // bytes of a K row
-    constexpr int kJ = kRow / 64;               // 16-byte chunks of a row per lane
-    constexpr int kRows = kJ >= 4 ? 4 : 8;      // rows of a lane in flight
-    constexpr int kSteps = D / 16;              // k16 steps of the product
-    constexpr int kCols = kDiff ? 4 : 8;        // (query, head) pairs per column tile
-    const int lane = threadIdx.x & 31, c = lane & 3, n = lane >> 2;
-    const int H = p.H_kv, g = p.g;
-    const long long blocks = block_start<kTaskTokens>(p.csr, p.csr.batch);
-    const long long nwarps = (long long)gridDim.x * (blockDim.x >> 5);
-    for (long long task = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); task < blocks * H; task += nwarps) {
-        const long long blk = task / H;
-        const int h = (int)(task - blk * H);
-        const int b = find_request<kTaskTokens>(p.csr, blk, lane);
-        const Request rq = request(p.csr, b);
-        const long long first = (blk - block_start<kTaskTokens>(p.csr, b)) * kTaskTokens;
-        if (first >= rq.len) continue;
-        const int t0 = (int)first;
-        const Queries qs = queries(p, b);
-        const int off = rq.len - qs.n;  // position of the first query
-        // this lane's own tokens (to look up and to write): t0 + n + 8 c and 32 further
-        uint32_t slot[2];
-        float *at[2];
-        float old[2];
+__device__ __forceinline__ void load_columns(const WeightsParams &p, const Queries &qs, int off, int h, int col, int col_hi,
+                                             int lane, Columns<D / 16> &x) {
+    constexpr int kJ = D * (kE4m3 ? 1 : 2) / 64, kSteps = D / 16;
+    const int c = lane & 3, n = lane >> 2, g = p.g;
+    // this lane's column of Q^T, n: its query row, and the half of it (differential)
+    const int cn = col + (kDiff ? n >> 1 : n);
+    const int qi = cn / g, r = cn - qi * g;
+    const bool in = cn < col_hi;
+    const size_t qrow = (size_t)(qs.q0 + (in ? qi : 0)) * p.H_qo + (size_t)h * g + (in ? r : 0);
+    float lse2 = in ? __ldg(p.lse + (kDiff ? 2 * qrow + (n & 1) : qrow)) : -INFINITY;
+    const bool live = lse2 != -INFINITY;
+    lse2 *= kLog2e;
+    const float lam = kDiff && in ? __ldg(p.lam + h * g + r) : 0.f;
+    float scale = p.soft_cap_on ? p.cap_in : p.scale_log2;
+    const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + qrow * D) + (kE4m3 ? 2 * c : c);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int t = t0 + n + 8 * c + 32 * u;
-            int page = 0, place = 0;
-            slot[u] = t < rq.len ? slot_of(p.csr, rq, t, page, place) : kNoRow;
-            at[u] = p.weights + ((size_t)page * H + h) * p.csr.ps + place;
-            old[u] = slot[u] != kNoRow && t < off && p.decay != 0.f ? *at[u] : 0.f;
+    for (int j = 0; j < kJ; ++j) {
+        const bool mine = in && (!kDiff || (j >= kJ / 2) == (n & 1));
+#pragma unroll
+        for (int e = 0; e < (kE4m3 ? 2 : 1); ++e) {
+            const uint4 w = mine ? __ldg(qp + j * (kE4m3 ? 8 : 4) + e) : make_uint4(0, 0, 0, 0);
+            const int st = kE4m3 ? 4 * j + 2 * e : 2 * j;
+            x.q[st][0] = w.x; x.q[st][1] = w.y;
+            x.q[st + 1][0] = w.z; x.q[st + 1][1] = w.w;
         }
-        const uint8_t *kb = static_cast<const uint8_t *>(p.k) + (size_t)h * kRow + c * 16;
-        const size_t row_stride = (size_t)H * kRow;
-        // columns (query i, head r) = i * g + r that any of the 64 keys can see
-        const int i_lo = max(0, t0 - off), i_hi = p.window > 0 ? (int)min((long long)qs.n, (long long)t0 + 64 + p.window - off) : qs.n;
-        const int col_lo = i_lo * g / kCols * kCols, col_hi = i_hi * g;  // (host: n_tokens * g < 2^31)
-        float own[2] = {0.f, 0.f};
-#pragma unroll
-        for (int half = 0; half < 8 / kRows; ++half) {
-            uint4 kw[kRows][kJ];
-            float kf[kRows];
-            int tok[kRows];
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int ii = half * kRows + i;  // row n + 8 ii
-                const uint32_t s = __shfl_sync(0xffffffffu, slot[ii >> 2], (lane & ~3) | (ii & 3));
-                tok[i] = t0 + n + 8 * ii;
-#pragma unroll
-                for (int j = 0; j < kJ; ++j)
-                    kw[i][j] = s != kNoRow ? __ldg(reinterpret_cast<const uint4 *>(kb + (size_t)s * row_stride + j * 64)) : make_uint4(0, 0, 0, 0);
-                kf[i] = 1.f;
-                if (kE4m3) kf[i] = s != kNoRow ? pow2i(__ldg(p.k_exp + (size_t)(s / (uint32_t)p.csr.ps) * H + h)) : 0.f;
-            }
-            float sum[kRows];
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) sum[i] = 0.f;
-            for (int col = col_lo; col < col_hi; col += kCols) {
-                // this lane's column of Q^T, n: its query row, and the half of it (differential)
-                const int cn = col + (kDiff ? n >> 1 : n);
-                const int qi = cn / g, r = cn - qi * g;
-                const bool in = cn < col_hi;
-                const size_t qrow = (size_t)(qs.q0 + (in ? qi : 0)) * p.H_qo + (size_t)h * g + (in ? r : 0);
-                float lse2 = in ? __ldg(p.lse + (kDiff ? 2 * qrow + (n & 1) : qrow)) : -INFINITY;
-                const bool live = lse2 != -INFINITY;
-                lse2 *= kLog2e;
-                const float lam = kDiff ? (in ? __ldg(p.lam + h * g + r) : 0.f) : 0.f;
-                float scale = p.soft_cap_on ? p.cap_in : p.scale_log2;
-                uint32_t qf[kSteps][2];
-                const uint4 *qp = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + qrow * D) + (kE4m3 ? 2 * c : c);
-#pragma unroll
-                for (int j = 0; j < kJ; ++j) {
-                    const bool mine = in && (!kDiff || (j >= kJ / 2) == (n & 1));
-#pragma unroll
-                    for (int e = 0; e < (kE4m3 ? 2 : 1); ++e) {
-                        const uint4 x = mine ? __ldg(qp + j * (kE4m3 ? 8 : 4) + e) : make_uint4(0, 0, 0, 0);
-                        const int st = kE4m3 ? 4 * j + 2 * e : 2 * j;
-                        qf[st][0] = x.x; qf[st][1] = x.y;
-                        qf[st + 1][0] = x.z; qf[st + 1][1] = x.w;
-                    }
-                }
-                if constexpr (kE4m3) {
-                    // bf16 -> f16: the row times the power of two that takes its largest value to
-                    // 2^14 .. 2^15 (values from 2^-31 of the largest on are exact); rows with an
-                    // infinity or NaN as they are
-                    uint32_t mx = 0;
-#pragma unroll
-                    for (int st = 0; st < kSteps; ++st)
-                        mx = __vmaxu2(mx, __vmaxu2(qf[st][0] & 0x7fff7fffu, qf[st][1] & 0x7fff7fffu));
-                    mx = max(mx & 0xffffu, mx >> 16);
-                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const int E = (int)(mx >> 7), up = E == 255 ? 0 : min(120, 141 - E);
-                    const float f = pow2i(up);
-#pragma unroll
-                    for (int st = 0; st < kSteps; ++st)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float lo = bf16_lo(qf[st][e]) * f, hi = bf16_hi(qf[st][e]) * f;
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(qf[st][e]) : "f"(hi), "f"(lo));
-                        }
-                    scale *= pow2i(-up);
-                }
-                // of the columns 2c and 2c + 1 of the product
-                float lc[2], sc[2];
-                int pos[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int from = 4 * (2 * c + e);
-                    lc[e] = __shfl_sync(0xffffffffu, lse2, from);
-                    sc[e] = __shfl_sync(0xffffffffu, scale, from);
-                    const int i = __shfl_sync(0xffffffffu, qi, from);
-                    const bool l = __shfl_sync(0xffffffffu, (int)live, from);
-                    pos[e] = l ? off + i : -1;  // keys up to this place; -1: no key
-                }
-                const float lm = kDiff ? __shfl_sync(0xffffffffu, lam, 8 * c) : 0.f;
-#pragma unroll
-                for (int sb = 0; sb < kRows / 2; ++sb) {
-                    float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-                    for (int j = 0; j < kJ; ++j) {
-                        const uint4 x = kw[2 * sb][j], y = kw[2 * sb + 1][j];
-                        if constexpr (kE4m3) {
-                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                uint32_t a[4];
-                                e4m3x4_to_f16x4(xs[w], a[0], a[2]);
-                                e4m3x4_to_f16x4(ys[w], a[1], a[3]);
-                                mma_f16_16816(d[w & 1], a, qf[4 * j + w][0], qf[4 * j + w][1]);
-                            }
-                        } else {
-                            const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-                            mma_bf16_16816(d[0], a0, qf[2 * j][0], qf[2 * j][1]);
-                            mma_bf16_16816(d[1], a1, qf[2 * j + 1][0], qf[2 * j + 1][1]);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {  // rows n + 8 (2 sb + i)
-                        const int row = 2 * sb + i, t = tok[row];
-                        float pe[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float x = (d[0][2 * i + e] + d[1][2 * i + e]) * (kE4m3 ? sc[e] * kf[row] : sc[e]);
-                            if (p.soft_cap_on) x = tanh_ex2(x) * p.cap_out;
-                            const bool see = t <= pos[e] && (p.window <= 0 || t >= pos[e] - p.window);
-                            pe[e] = see ? ex2(x - lc[e]) : 0.f;
-                        }
-                        sum[row] += kDiff ? fabsf(pe[0] - lm * pe[1]) : pe[0] + pe[1];
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-                sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-                const int ii = half * kRows + i;
-                if ((ii & 3) == c) own[ii >> 2] = sum[i];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            if (slot[u] != kNoRow) *at[u] = fmaf(p.decay, old[u], own[u]);
     }
+    if constexpr (kE4m3) {
+        // bf16 -> f16: the row times the power of two that takes its largest value to 2^14 .. 2^15
+        // (values from 2^-31 of the largest on are exact); rows with an infinity or NaN as they are
+        uint32_t mx = 0;
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) mx = __vmaxu2(mx, __vmaxu2(x.q[st][0] & 0x7fff7fffu, x.q[st][1] & 0x7fff7fffu));
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int E = (int)(mx >> 7), up = E == 255 ? 0 : min(120, 141 - E);
+        const float f = pow2i(up);
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float lo = bf16_lo(x.q[st][e]) * f, hi = bf16_hi(x.q[st][e]) * f;
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(x.q[st][e]) : "f"(hi), "f"(lo));
+            }
+        scale *= pow2i(-up);
+    }
+    // of the columns 2c and 2c + 1 of the product
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int from = 4 * (2 * c + e);
+        x.lse[e] = __shfl_sync(0xffffffffu, lse2, from);
+        x.scale[e] = __shfl_sync(0xffffffffu, scale, from);
+        const int i = __shfl_sync(0xffffffffu, qi, from);
+        const bool l = __shfl_sync(0xffffffffu, (int)live, from);
+        x.pos[e] = l ? off + i : -1;
+    }
+    x.lam = kDiff ? __shfl_sync(0xffffffffu, lam, 8 * c) : 0.f;
 }
 
-// fp32 pools: a warp takes 64 keys, eight at a time (8 lanes per row, two rows a lane group),
+// kVar: window and soft-cap compiled in.
+template <int D, bool kE4m3, bool kDiff, bool kVar>
+__global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_kernel(const WeightsParams p) {
+    using LY = StreamLayout<D, kE4m3>;
+    constexpr int kJ = LY::kRow / 64;           // 16-byte chunks of a row per lane
+    constexpr int kStages = LY::kStages;
+    constexpr int kCols = kDiff ? 4 : 8;        // (query, head) pairs per column tile
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = p.H_kv, g = p.g, ps = p.csr.ps;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + LY::kBarOff + 2 * kStages * 8);
+    const uint32_t full0 = smem_u32(smem) + LY::kBarOff, empty0 = full0 + kStages * 8;
+    const long long tasks = block_start<kTaskTokens>(p.csr, p.csr.batch) * H;
+    const long long task0 = tasks * blockIdx.x / gridDim.x, task1 = tasks * (blockIdx.x + 1) / gridDim.x;
+    const int count = (int)(task1 - task0);
+    if (count <= 0) return;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2 * kStages; ++s) sm100::mbar_init(full0 + 8 * s, 1);
+        *abort_flag = 0;
+        sm100::fence_barrier_init();
+    }
+    __syncthreads();
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        const bool ok = __all_sync(0xffffffffu, sm100::mbar_wait_spin(bar, parity, kWaitLimitCycles, abort_flag));
+        if (!ok) *abort_flag = 1;
+        return ok;
+    };
+
+    if (warp < LY::kLoaders) {
+        // this warp's place in the run: request, head, block of keys (kept in range for tables that
+        // do not ascend)
+        auto blocks_of = [&](int b) { return (int)max(1ll, block_start<kTaskTokens>(p.csr, b + 1) - block_start<kTaskTokens>(p.csr, b)); };
+        const long long first = min(task0 + warp, tasks - 1);
+        int b = find_request<kTaskTokens>(p.csr, first / H, lane);
+        Request rq = request(p.csr, b);
+        int nblk = blocks_of(b);
+        const long long in = max(0ll, first - block_start<kTaskTokens>(p.csr, b) * H);
+        int h = (int)min(in / nblk, (long long)H - 1), blk = (int)(in % nblk);
+        // two tasks on their way: asked for (page ids), then looked up (weights, exponents); each
+        // step's reads are in flight for a turn of the loop
+        struct { int b, h, t0, len, id, place; } ask = {0, 0, -1, 0, 0, 0};
+        struct { int b, h, t0, len, exp; uint32_t row; long long at; float old; } got = {0, 0, -1, 0, 0, kNoRow, -1, 0.f};
+        for (int k = warp - 2 * LY::kLoaders; k < count; k += LY::kLoaders) {
+            if (k >= 0) {
+                const int s = k % kStages;
+                if (!wait(empty0 + 8 * s, ((k / kStages) & 1) ^ 1)) return;
+                uint8_t *stage = smem + LY::kRingOff + s * LY::kStageBytes;
+                reinterpret_cast<long long *>(stage)[lane] = got.at;
+                reinterpret_cast<uint32_t *>(stage)[64 + lane] = got.row;
+                reinterpret_cast<float *>(stage)[96 + lane] = got.old;
+                reinterpret_cast<float *>(stage)[128 + lane] = kE4m3 ? pow2i(got.exp) : 1.f;
+                if (lane == 0) *reinterpret_cast<int4 *>(stage + kTaskTokens * 20) = make_int4(got.b, got.h, got.t0, got.len);
+                __syncwarp();
+                if (lane == 0) sm100::mbar_arrive(full0 + 8 * s);
+            }
+            // the page ids are here: rows, weights and exponents
+            got = {ask.b, ask.h, ask.t0, ask.len, 0, kNoRow, -1, 0.f};
+            if (ask.t0 >= 0 && ask.t0 + lane < ask.len && (unsigned)ask.id < (unsigned)p.csr.num_pages) {
+                got.row = (uint32_t)ask.id * (uint32_t)ps + (uint32_t)ask.place;
+                got.at = ((long long)ask.id * H + ask.h) * ps + ask.place;
+                if (kE4m3) got.exp = __ldg(p.k_exp + (size_t)ask.id * H + ask.h);
+                if (p.decay != 0.f) got.old = p.weights[got.at];  // (not used for the queries' own keys)
+            }
+            // the next task's page ids
+            ask.t0 = -1;
+            if (k + 2 * LY::kLoaders >= count || b >= p.csr.batch) continue;
+            const int t0 = blk * kTaskTokens, t = t0 + lane;
+            if (t0 < rq.len) {
+                const int col = p.csr.ps_shift >= 0 ? t >> p.csr.ps_shift : t / ps;
+                ask = {b, h, t0, rq.len, t < rq.len ? __ldg(p.csr.kv_indices + rq.p0 + col) : 0, t - col * ps};
+            }
+            blk += LY::kLoaders;
+            while (blk >= nblk && b < p.csr.batch) {
+                blk -= nblk;
+                if (++h == H) {
+                    h = 0;
+                    if (++b < p.csr.batch) {
+                        rq = request(p.csr, b);
+                        nblk = blocks_of(b);
+                    }
+                }
+            }
+        }
+        return;
+    }
+
+    const int c = lane & 3, n = lane >> 2;
+    int qb = -1, qh = -1;
+    Queries qs = {0, 0};
+    Columns<D / 16> x;
+    const uint32_t bufs = smem_u32(smem) + (warp - LY::kLoaders) * LY::kBufs * LY::kBuf;
+    // the rows of task k into buffer u, one group of copies (none behind the last task)
+    auto copy = [&](int k, int u) -> bool {
+        if (k < count) {
+            const int s = k % kStages;
+            if (!wait(full0 + 8 * s, (k / kStages) & 1)) return false;
+            const uint32_t *row = reinterpret_cast<const uint32_t *>(smem + LY::kRingOff + s * LY::kStageBytes) + 64;
+            const int h = *reinterpret_cast<const int *>(smem + LY::kRingOff + s * LY::kStageBytes + kTaskTokens * 20 + 4);
+            constexpr int kC = LY::kRow / 16, kT = 32 / kC;  // chunks of a row, rows per instruction
+            const int ch = lane % kC, sub = lane / kC;
+            const char *base = static_cast<const char *>(p.k) + (size_t)h * LY::kRow + ch * 16;
+            const size_t stride = (size_t)H * LY::kRow;
+#pragma unroll
+            for (int i = 0; i < kTaskTokens / kT; ++i) {
+                const int t = i * kT + sub;
+                const uint32_t r = row[t];
+                // (chunks of odd rows in the other half of their 128 bytes: the reads below meet no bank twice)
+                if (r != kNoRow) cp_async_16(bufs + u * LY::kBuf + t * LY::kRow + ((ch ^ ((t & 1) << 2)) << 4), base + r * stride, 16);
+            }
+        }
+        cp_async_commit();
+        return true;
+    };
+    const int k0 = warp - LY::kLoaders;
+    bool ok = copy(k0, 0);
+    for (int k = k0, u = 0; k < count && ok; k += LY::kCompute, u ^= 1) {
+        if (!(ok = copy(k + LY::kCompute, u ^ 1))) break;
+        cp_async_wait<1>();
+        __syncwarp();
+        const int s = k % kStages;
+        const uint8_t *stage = smem + LY::kRingOff + s * LY::kStageBytes;
+        const int4 m = *reinterpret_cast<const int4 *>(stage + kTaskTokens * 20);
+        const int b = m.x, h = m.y, t0 = m.z, len = m.w;
+        // 2^exponent of the rows n + 8 i, and this lane's own key, n + 8 c
+        float kf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kf[i] = kE4m3 ? reinterpret_cast<const float *>(stage)[128 + n + 8 * i] : 1.f;
+        const long long at = reinterpret_cast<const long long *>(stage)[n + 8 * c];
+        const float old = reinterpret_cast<const float *>(stage)[96 + n + 8 * c];
+        __syncwarp();  // the stage is read
+        if (lane == 0) sm100::mbar_arrive(empty0 + 8 * s);
+        const uint32_t rows = bufs + u * LY::kBuf + n * LY::kRow + ((c ^ ((n & 1) << 2)) << 4);
+        if (t0 < 0) continue;  // an empty block of the table
+
+        if (b != qb) qs = queries(p, b);
+        const int off = len - qs.n;  // position of the first query
+        // columns (query i, head r) = i * g + r that any of the 32 keys can see
+        const int i_lo = max(0, t0 - off);
+        const int i_hi = kVar && p.window > 0 ? (int)min((long long)qs.n, (long long)t0 + kTaskTokens + p.window - off) : qs.n;
+        const bool one = qs.n * g <= kCols;  // all in one tile, kept from task to task
+        const int col_lo = one ? 0 : i_lo * g / kCols * kCols, col_hi = one ? qs.n * g : i_hi * g;
+        if (one && (b != qb || h != qh)) load_columns<D, kE4m3, kDiff>(p, qs, off, h, 0, col_hi, lane, x);
+        qb = b;
+        qh = h;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int col = col_lo; col < col_hi; col += kCols) {
+            if (!one) load_columns<D, kE4m3, kDiff>(p, qs, off, h, col, col_hi, lane, x);
+#pragma unroll
+            for (int sb = 0; sb < 2; ++sb) {
+                float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                uint4 kw[2][kJ];  // rows n + 16 sb and 8 further
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) kw[i][j] = sm100::ld_shared_v4((rows + 8 * (2 * sb + i) * LY::kRow) ^ (j * 64));
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const uint4 u = kw[0][j], v = kw[1][j];
+                    if constexpr (kE4m3) {
+                        const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t a[4];
+                            e4m3x4_to_f16x4(us[e], a[0], a[2]);
+                            e4m3x4_to_f16x4(vs[e], a[1], a[3]);
+                            mma_f16_16816(d[e & 1], a, x.q[4 * j + e][0], x.q[4 * j + e][1]);
+                        }
+                    } else {
+                        const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+                        mma_bf16_16816(d[0], a0, x.q[2 * j][0], x.q[2 * j][1]);
+                        mma_bf16_16816(d[1], a1, x.q[2 * j + 1][0], x.q[2 * j + 1][1]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // rows n + 8 (2 sb + i)
+                    const int row = 2 * sb + i, tok = t0 + n + 8 * row;
+                    float pe[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = kE4m3 ? x.scale[e] * kf[row] : x.scale[e];
+                        float y = d[0][2 * i + e] + d[1][2 * i + e];
+                        if (kVar && p.soft_cap_on) y = fmaf(tanh_ex2(y * f), p.cap_out, -x.lse[e]);
+                        else y = fmaf(y, f, -x.lse[e]);
+                        const bool see = tok <= x.pos[e] && (!kVar || p.window <= 0 || tok >= x.pos[e] - p.window);
+                        pe[e] = see ? ex2(y) : 0.f;
+                    }
+                    sum[row] += kDiff ? fabsf(pe[0] - x.lam * pe[1]) : pe[0] + pe[1];
+                }
+            }
+        }
+        float own = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+            if (i == c) own = sum[i];
+        }
+        __syncwarp();  // the buffer is read
+        if (at >= 0) p.weights[at] = t0 + n + 8 * c < off && p.decay != 0.f ? fmaf(p.decay, old, own) : own;
+    }
+    cp_async_wait<0>();  // nothing in flight at exit
+}
+
+// fp32 pools: a warp takes a task's 32 keys, eight at a time (8 lanes per row, two rows a lane group),
 // fp32 products on the CUDA cores.
 template <int D>
 __global__ void __launch_bounds__(256) weights_f32_kernel(const WeightsParams p) {
@@ -617,7 +754,35 @@ int launched(const char *what) {
 
 Csr make_csr(const int32_t *kv_indptr, const int32_t *kv_indices, const int32_t *last_page_len, int64_t max_pages, int batch,
              int ps, int64_t num_pages) {
-    return {kv_indptr, kv_indices, last_page_len, (int)max_pages, batch, ps, (int)num_pages};
+    return {kv_indptr, kv_indices, last_page_len, (int)max_pages, batch, ps, (int)num_pages, (ps & (ps - 1)) == 0 ? __builtin_ctz(ps) : -1};
+}
+
+template <int D, bool kE4m3, bool kDiff, bool kVar>
+int launch_weights_kernel(const WeightsParams &p, int64_t tasks, int sms, cudaStream_t stream) {
+    using LY = StreamLayout<D, kE4m3>;
+    static bool configured[64] = {false};
+    int dev = 0;
+    if (current_sms(&dev) < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    auto kern = weights_kernel<D, kE4m3, kDiff, kVar>;
+    if (!configured[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kSmem);
+        if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("weights smem attribute: ") + cudaGetErrorString(e));
+        configured[dev] = true;
+    }
+    // (small calls: four tasks per CTA, so that every loader's first look-up runs at once)
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((tasks + 3) / 4, sms));
+    kern<<<grid, LY::kThreads, LY::kSmem, stream>>>(p);
+    return launched("weights");
+}
+
+template <int D, bool kE4m3>
+int launch_weights(const WeightsParams &p, int64_t tasks, int sms, cudaStream_t stream) {
+    const bool var = p.window > 0 || p.soft_cap_on;
+    if (p.lam)
+        return var ? launch_weights_kernel<D, kE4m3, true, true>(p, tasks, sms, stream)
+                   : launch_weights_kernel<D, kE4m3, true, false>(p, tasks, sms, stream);
+    return var ? launch_weights_kernel<D, kE4m3, false, true>(p, tasks, sms, stream)
+               : launch_weights_kernel<D, kE4m3, false, false>(p, tasks, sms, stream);
 }
 
 }  // namespace
@@ -651,26 +816,19 @@ int launch_accumulate_weights(const bsp_problem *P, const void *q, const float *
     if (!k_exp && weights_prefill_takes(P, num_pages, n_tokens, batch, qo_indptr))
         return launch_weights_prefill(P, p, num_pages, max_table_pages, sms, stream);
     const int64_t tasks = (max_table_pages * P->page_size / kTaskTokens + batch) * P->num_kv_heads;
-    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((tasks + 7) / 8, (int64_t)sms * 2));
     const int D = P->head_dim;
     if (P->dtype == BSP_DTYPE_F32) {
+        const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((tasks + 7) / 8, (int64_t)sms * 4));
         switch (D) {
             case 32: weights_f32_kernel<32><<<grid, 256, 0, stream>>>(p); break;
             case 64: weights_f32_kernel<64><<<grid, 256, 0, stream>>>(p); break;
             case 128: weights_f32_kernel<128><<<grid, 256, 0, stream>>>(p); break;
             default: weights_f32_kernel<256><<<grid, 256, 0, stream>>>(p); break;
         }
-    } else if (k_exp) {
-        if (lambda) weights_kernel<128, true, true><<<grid, 256, 0, stream>>>(p);
-        else weights_kernel<128, true, false><<<grid, 256, 0, stream>>>(p);
-    } else if (D == 128) {
-        if (lambda) weights_kernel<128, false, true><<<grid, 256, 0, stream>>>(p);
-        else weights_kernel<128, false, false><<<grid, 256, 0, stream>>>(p);
-    } else {
-        if (lambda) weights_kernel<64, false, true><<<grid, 256, 0, stream>>>(p);
-        else weights_kernel<64, false, false><<<grid, 256, 0, stream>>>(p);
+        return launched("weights");
     }
-    return launched("weights");
+    if (k_exp) return launch_weights<128, true>(p, tasks, sms, stream);
+    return D == 128 ? launch_weights<128, false>(p, tasks, sms, stream) : launch_weights<64, false>(p, tasks, sms, stream);
 }
 
 int launch_select_tokens(const float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t batch,

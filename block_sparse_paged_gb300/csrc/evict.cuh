@@ -19,6 +19,7 @@ struct Csr {
     const int32_t *kv_indptr, *kv_indices, *last_page_len;
     int max_pages;  // entries of kv_indices
     int batch, ps, num_pages;
+    int ps_shift;   // log2(ps), or -1
 };
 
 struct Request {
@@ -35,7 +36,7 @@ __device__ __forceinline__ Request request(const Csr &c, int b) {
 
 // Slot of token t of a request, or kNoRow (host: num_pages * ps < 2^32 - 1).
 __device__ __forceinline__ uint32_t slot_of(const Csr &c, const Request &r, int t, int &page, int &place) {
-    const int col = t / c.ps;
+    const int col = c.ps_shift >= 0 ? t >> c.ps_shift : t / c.ps;
     place = t - col * c.ps;
     page = __ldg(c.kv_indices + r.p0 + col);
     return (unsigned)page < (unsigned)c.num_pages ? (uint32_t)page * (uint32_t)c.ps + (uint32_t)place : kNoRow;
