@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
@@ -413,12 +414,21 @@ __global__ void __launch_bounds__(256) weights_f32_kernel(const WeightsParams p)
 // protected ones (the first `sinks`, the last `recent`) counting as +inf, NaN as -inf, equal
 // weights by the lower position; written as ascending positions. A radix selection of the n-th
 // largest key over 11 + 11 + 10 bits, then one stable compaction. A cluster of CTAs takes one
-// row of tokens, a contiguous part each, its keys in shared memory (those beyond kKeys are read
-// again in every pass); histograms and counts are read from the other CTAs' shared memory.
+// row of tokens, a contiguous part each; a thread holds 16 of its part's keys in registers (parts
+// beyond 8192 tokens are read again in every pass). The first CTA of the cluster adds up the
+// others' bins that are not empty and finds the digit (every CTA reading all histograms instead
+// took 60 of 91 thousand cycles: an SM reads others' shared memory at 10 bytes a cycle or so).
+//
+// Bound by instructions and latency, not by the 4 bytes per token: 64 requests x 8 heads x 5100
+// tokens on average, us: keys in shared memory and one read at a time 33, all reads of a thread in
+// flight together 25, keys in registers 19; one request of 131,072 tokens 57, 28, 19.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelKeys = 16;                       // keys per thread
+constexpr int kSelChunk = kSelThreads * kSelKeys;  // tokens of a part in registers
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
+static_assert(kBins == 4 * kSelThreads, "four bins per thread");
 
 struct SelectParams {
     Csr csr;
@@ -426,29 +436,42 @@ struct SelectParams {
     const int32_t *budget;
     int32_t *kept, *new_lens;
     int H, max_keep, sinks, recent;
-    int cap_keys;  // keys that a CTA's shared memory holds
 };
 
+// kOne: a CTA per row.
+template <bool kOne>
 struct SelectShared {
-    int hist[3][kBins];
-    int counts[2];           // keys above the threshold and equal to it, this CTA
-    int warp_sum[kSelWarps], warp_eq[kSelWarps];
-    int digit, above;
+    int hist[kBins];
+    int all[kOne ? 1 : 3][kOne ? 4 : kBins];  // the cluster's, per pass (of the first CTA)
+    int counts[2];             // keys above the threshold and equal to it, this CTA
+    int warp_sum[kSelWarps];
+    uint32_t totals[kSelKeys * kSelWarps];  // of a chunk, by group and warp: above | equal << 16
+    int2 found[3];  // digit of the n-th largest key, keys above it, per pass
 };
 
-// Order-preserving whole number of a weight
+// Order-preserving whole number of a weight; never 0
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x) x = -INFINITY;
     const uint32_t u = __float_as_uint(x + 0.f);  // -0 counts as 0
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-    extern __shared__ __align__(16) uint8_t sel_smem[];
-    SelectShared &sh = *reinterpret_cast<SelectShared *>(sel_smem);
-    uint32_t *keys = reinterpret_cast<uint32_t *>(sel_smem + sizeof(SelectShared));
+// Conditional additions to shared memory and stores as predicated instructions (as branches they
+// took three times the instructions; an SM's instructions are what the many rows wait for).
+__device__ __forceinline__ void add_shared_if(bool cond, uint32_t addr, int x) {
+    asm volatile("{ .reg .pred p;\n setp.ne.s32 p, %0, 0;\n @p red.shared.add.s32 [%1], %2;\n}" ::"r"((int)cond), "r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void store_if(bool cond, int32_t *p, int x) {
+    asm volatile("{ .reg .pred p;\n setp.ne.s32 p, %0, 0;\n @p st.global.s32 [%1], %2;\n}" ::"r"((int)cond), "l"(p), "r"(x) : "memory");
+}
+
+// kV: tokens per load, 4 (page sizes that are multiples of 4) or 1
+template <int kV, bool kOne>
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p) {
+    constexpr int kGroups = kSelKeys / kV;
+    __shared__ __align__(16) SelectShared<kOne> sh;
     cg::cluster_group cl = cg::this_cluster();
-    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    const int C = kOne ? 1 : (int)cl.num_blocks(), rank = kOne ? 0 : (int)cl.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / C, b = row / p.H, h = row - b * p.H;
     const Request rq = request(p.csr, b);
@@ -462,49 +485,96 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         return;
     }
     const int part = ((rq.len + C - 1) / C + 31) & ~31;  // tokens per CTA
-    const int t_lo = min(rank * part, rq.len), t_hi = min(t_lo + part, rq.len), m = t_hi - t_lo;
-    auto read_key = [&](int t) -> uint32_t {
-        if (t < p.sinks || t >= rq.len - p.recent) return order_key(INFINITY);
-        int page, place;
-        const uint32_t s = slot_of(p.csr, rq, t, page, place);
-        return order_key(s != kNoRow ? __ldg(p.weights + ((size_t)page * p.H + h) * p.csr.ps + place) : -INFINITY);
+    const int t_lo = min(rank * part, rq.len), m = min(part, rq.len - t_lo);
+    const int chunks = (m + kSelChunk - 1) / kSelChunk;
+    // groups of chunk c that hold a token (the same for all threads: the others are skipped)
+    auto groups = [&](int c) { return min(kGroups, (m - c * kSelChunk + kSelThreads * kV - 1) / (kSelThreads * kV)); };
+    reinterpret_cast<int4 *>(sh.hist)[tid] = make_int4(0, 0, 0, 0);
+    if (!kOne && rank == 0) {
+        for (int i = tid; i < 3 * kBins / 4; i += kSelThreads) reinterpret_cast<int4 *>(&sh.all[0][0])[i] = make_int4(0, 0, 0, 0);
+    }
+    // a chunk's keys: group u of this thread begins at token (u * threads + tid) * kV of it (the kV tokens
+    // lie in one page); 0 behind the part
+    uint32_t key[kSelKeys];
+    auto load = [&](int c) {
+        const int i0 = c * kSelChunk + tid * kV;
+        int page[kGroups], place[kGroups];
+        bool in[kGroups];
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            const int i = i0 + u * kSelThreads * kV;
+            page[u] = place[u] = 0;
+            in[u] = i < m && slot_of(p.csr, rq, t_lo + i, page[u], place[u]) != kNoRow;
+        }
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            const float *w = p.weights + ((size_t)page[u] * p.H + h) * p.csr.ps + place[u];
+            float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (in[u]) {
+                if (kV == 4) x = __ldg(reinterpret_cast<const float4 *>(w));
+                else x.x = __ldg(w);
+            }
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int v = 0; v < kV; ++v) key[u * kV + v] = __float_as_uint(xs[v]);
+        }
+        const int lo = p.sinks - t_lo, hi = min(m, rq.len - p.recent - t_lo);  // protected: i < lo or i >= hi
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            const int i = i0 + u * kSelThreads * kV;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) key[u * kV + v] = order_key(__uint_as_float(key[u * kV + v]));
+            if (i < lo || i + kV > hi) {
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    if (i + v < lo || i + v >= hi) key[u * kV + v] = order_key(INFINITY);
+                    if (i + v >= m) key[u * kV + v] = 0u;
+                }
+            }
+        }
     };
-    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
-    __syncthreads();
-    auto key_at = [&](int i) -> uint32_t { return i < p.cap_keys ? keys[i] : read_key(t_lo + i); };
+    if (chunks) load(0);
+    if (kOne) __syncthreads();
+    else cl.sync();
 
     uint32_t prefix = 0;
     int need = n;  // how many of the keys that match the prefix are still to be taken
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        int *hist = sh.hist[pass];
-        for (int i = tid; i < m; i += kSelThreads) {
-            uint32_t k;
-            if (pass == 0) {
-                k = read_key(t_lo + i);
-                if (i < p.cap_keys) keys[i] = k;
-            } else {
-                k = key_at(i);
-                if ((k >> (shift + bits)) != prefix) continue;
-            }
-            atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
-        }
-        if (C > 1) cl.sync();
-        else __syncthreads();
-        // four bins per thread, the highest first
-        int cnt[4], mine = 0;
-        const int hi_bin = (kBins - 1) - 4 * tid;
+    auto run_pass = [&](auto number) {
+        constexpr int pass = decltype(number)::value, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        int *hist = sh.hist;
+        const uint32_t hist_at = smem_u32(hist);
+        for (int c = 0; c < chunks; ++c) {
+            if (chunks > 1 && (pass > 0 || c > 0)) load(c);
+            const int G = groups(c);
+            const uint32_t lo = pass == 0 ? 0u : prefix << ((shift + bits) & 31);  // keys from lo on, of this prefix
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            cnt[i] = 0;
-            if (C > 1) {
-                for (int r = 0; r < C; ++r) cnt[i] += *cl.map_shared_rank(hist + hi_bin - i, r);
-            } else {
-                cnt[i] = hist[hi_bin - i];
+            for (int u = 0; u < kGroups; ++u) {
+                if (u >= G) break;
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    const uint32_t k = key[u * kV + v], d = k - lo;
+                    // (a key behind the part, 0, is below every prefix, and in bin 0 it counts for nothing)
+                    if (pass == 0) atomicAdd(&hist[k >> 21], 1);
+                    else add_shared_if(d >> ((shift + bits) & 31) == 0, hist_at + (d >> shift) * 4, 1);
+                }
             }
-            mine += cnt[i];
         }
+        __syncthreads();
+        // four bins per thread, the highest first; zero again for the next pass
+        const int lo_bin = kBins - 4 - 4 * tid;
+        int4 c4 = *reinterpret_cast<const int4 *>(hist + lo_bin);
+        *reinterpret_cast<int4 *>(hist + lo_bin) = make_int4(0, 0, 0, 0);
+        if constexpr (!kOne) {
+            int *all = cl.map_shared_rank(sh.all[pass], 0) + lo_bin;
+            if (c4.x) atomicAdd(all, c4.x);
+            if (c4.y) atomicAdd(all + 1, c4.y);
+            if (c4.z) atomicAdd(all + 2, c4.z);
+            if (c4.w) atomicAdd(all + 3, c4.w);
+            cl.sync();
+            c4 = rank == 0 ? *reinterpret_cast<const int4 *>(sh.all[pass] + lo_bin) : make_int4(0, 0, 0, 0);
+        }
+        const int cnt[4] = {c4.w, c4.z, c4.y, c4.x};
+        const int mine = (cnt[0] + cnt[1]) + (cnt[2] + cnt[3]);
         int inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -513,66 +583,118 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         }
         if (lane == 31) sh.warp_sum[warp] = inc;
         __syncthreads();
-        int before = inc - mine;
-        for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+        int before = inc - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane & (kSelWarps - 1)] : 0);
         if (before < need && before + mine >= need) {
+            int at = lo_bin + 3;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (before < need && before + cnt[i] >= need) {
-                    sh.digit = hi_bin - i;
-                    sh.above = before;
+            for (int i = 0; i < 3; ++i)
+                if (before + cnt[i] < need && at == lo_bin + 3 - i) {
+                    before += cnt[i];
+                    --at;
                 }
-                before += cnt[i];
+            sh.found[pass] = make_int2(at, before);
+        }
+        if (kOne) __syncthreads();
+        else cl.sync();
+        const int2 found = kOne ? sh.found[pass] : *cl.map_shared_rank(&sh.found[pass], 0);
+        prefix = (prefix << bits) | (uint32_t)found.x;
+        need -= found.y;
+    };
+    run_pass(std::integral_constant<int, 0>{});
+    run_pass(std::integral_constant<int, 1>{});
+    run_pass(std::integral_constant<int, 2>{});
+    // prefix: the n-th largest key; `need` of those equal to it are taken, the lowest positions
+    uint32_t sum[kGroups];  // of a chunk: keys above | equal << 16, by group, in the threads up to this one
+    auto count = [&](int c) {
+        if (chunks > 1) load(c);
+        uint32_t own[kGroups];
+        const int G = groups(c);
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            if (u >= G) {
+                if (lane == 31) sh.totals[u * kSelWarps + warp] = 0;
+                continue;
             }
+            own[u] = 0;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) own[u] += (key[u * kV + v] > prefix ? 1u : 0u) + (key[u * kV + v] == prefix ? 0x10000u : 0u);
+            sum[u] = own[u];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, sum[u], o);
+                if (lane >= o) sum[u] += x;
+            }
+            if (lane == 31) sh.totals[u * kSelWarps + warp] = sum[u];
+            sum[u] -= own[u];
         }
         __syncthreads();
-        prefix = (prefix << bits) | (uint32_t)sh.digit;
-        need -= sh.above;
-        __syncthreads();
-    }
-    // prefix: the n-th largest key; `need` of those equal to it are taken, the lowest positions
-    const int seg = ((m + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int s_lo = min(warp * seg, m), s_hi = min(s_lo + seg, m);
-    int n_gt = 0, n_eq = 0;
-    for (int i0 = s_lo; i0 < s_hi; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < s_hi ? key_at(i) : 0u;
-        n_gt += __popc(__ballot_sync(0xffffffffu, i < s_hi && k > prefix));
-        n_eq += __popc(__ballot_sync(0xffffffffu, i < s_hi && k == prefix));
-    }
-    if (lane == 0) {
-        sh.warp_sum[warp] = n_gt;
-        sh.warp_eq[warp] = n_eq;
-    }
-    __syncthreads();
-    int above = 0, equal = 0, all_above = 0, all_equal = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-        if (w == warp) { above = all_above; equal = all_equal; }
-        all_above += sh.warp_sum[w];
-        all_equal += sh.warp_eq[w];
-    }
-    if (C > 1) {
+    };
+    // (above, equal) over the first `upto` entries of totals, the same in every lane of a warp
+    auto total = [&](int upto) -> int2 {
+        int2 r = make_int2(0, 0);
+#pragma unroll
+        for (int e = 0; e < kGroups * kSelWarps; e += 32) {
+            const uint32_t x = e + lane < upto ? sh.totals[e + lane] : 0u;
+            r.x += x & 0xffff;
+            r.y += x >> 16;
+        }
+        return make_int2(__reduce_add_sync(0xffffffffu, r.x), __reduce_add_sync(0xffffffffu, r.y));
+    };
+    int above = 0, equal = 0;
+    if constexpr (!kOne) {  // what the CTAs before hold
+        int2 all = make_int2(0, 0);
+        for (int c = 0; c < chunks; ++c) {
+            count(c);
+            const int2 t = total(kGroups * kSelWarps);
+            all.x += t.x;
+            all.y += t.y;
+            if (chunks > 1) __syncthreads();
+        }
         if (tid == 0) {
-            sh.counts[0] = all_above;
-            sh.counts[1] = all_equal;
+            sh.counts[0] = all.x;
+            sh.counts[1] = all.y;
         }
         cl.sync();
-        for (int r = 0; r < rank; ++r) {
-            above += *cl.map_shared_rank(&sh.counts[0], r);
-            equal += *cl.map_shared_rank(&sh.counts[1], r);
+        int g = 0, e = 0;
+        if (lane < rank) {
+            g = *cl.map_shared_rank(&sh.counts[0], lane);
+            e = *cl.map_shared_rank(&sh.counts[1], lane);
         }
+        above = __reduce_add_sync(0xffffffffu, g);
+        equal = __reduce_add_sync(0xffffffffu, e);
         cl.sync();  // nobody's shared memory is read behind this
     }
-    for (int i0 = s_lo; i0 < s_hi; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < s_hi ? key_at(i) : 0u;
-        const bool is_gt = i < s_hi && k > prefix, is_eq = i < s_hi && k == prefix;
-        const unsigned mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
-        const unsigned lt = (1u << lane) - 1;
-        const int g = above + __popc(mg & lt), e = equal + __popc(me & lt);
-        if (is_gt || (is_eq && e < need)) kept[g + min(e, need)] = t_lo + i;
-        above += __popc(mg);
-        equal += __popc(me);
+    for (int c = 0; c < chunks; ++c) {
+        if (kOne || chunks > 1) count(c);
+        // by group: the chunk's groups and warps before this one
+        int2 at = total(warp);
+        const int G = groups(c);
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            if (u >= G) break;
+            int e = equal + at.y + (sum[u] >> 16);
+            int32_t *to = kept + (above + at.x + (sum[u] & 0xffff) + min(e, need));
+            const int t = t_lo + c * kSelChunk + (u * kSelThreads + tid) * kV;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                const uint32_t k = key[u * kV + v];
+                const bool is_eq = k == prefix, take = k > prefix || (is_eq && e < need);
+                store_if(take, to, t + v);
+                to += take;
+                e += is_eq;
+            }
+            if (u + 1 < G) {  // the rest of this group's warps, then the next group's before this one
+                const uint32_t x = lane < kSelWarps ? sh.totals[(u + (lane < warp)) * kSelWarps + lane] : 0u;
+                at.x += __reduce_add_sync(0xffffffffu, x & 0xffff);
+                at.y += __reduce_add_sync(0xffffffffu, x >> 16);
+            }
+        }
+        if (c + 1 < chunks) {
+            const int2 t = total(kGroups * kSelWarps);
+            above += t.x;
+            equal += t.y;
+            __syncthreads();
+        }
     }
 }
 
@@ -848,22 +970,22 @@ int launch_select_tokens(const float *weights, int64_t num_pages, int32_t page_s
     int dev = 0;
     const int sms = current_sms(&dev);
     if (sms < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
-    // CTAs per row: more where rows are few and long
+    // CTAs per row: enough to hold the mean row in registers, more where rows are few
     const int64_t rows = (int64_t)batch * num_kv_heads, mean = max_table_pages * page_size / batch;
     int C = 1;
-    while (C < kMaxCluster && rows * C * 2 <= 2 * (int64_t)sms && mean / C >= 4096) C *= 2;
-    p.cap_keys = (int)std::min<int64_t>(40000, std::max<int64_t>(2048, (2 * mean / C + 31) / 32 * 32));
-    const int smem = (int)sizeof(SelectShared) + 4 * p.cap_keys;
-    static bool configured[64] = {false};
-    if (!configured[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-        if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("select smem attribute: ") + cudaGetErrorString(e));
-        configured[dev] = true;
+    while (C < kMaxCluster && (mean > (int64_t)C * kSelChunk || (rows * C * 2 <= 2 * (int64_t)sms && mean / C >= 4096))) C *= 2;
+    const bool one = C == 1, vec = page_size % 4 == 0 && reinterpret_cast<uintptr_t>(weights) % 16 == 0;
+    auto kern = one ? (vec ? select_kernel<4, true> : select_kernel<1, true>) : (vec ? select_kernel<4, false> : select_kernel<1, false>);
+    static bool configured[4][64] = {{false}};
+    bool &done = configured[(one ? 2 : 0) + (vec ? 1 : 0)][dev];
+    if (!done) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("select cluster attribute: ") + cudaGetErrorString(e));
+        done = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -871,7 +993,7 @@ int launch_select_tokens(const float *weights, int64_t num_pages, int32_t page_s
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("select launch: ") + cudaGetErrorString(e));
     return launched("select");
 }
