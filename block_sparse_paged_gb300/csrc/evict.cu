@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_k
             if (k + 2 * LY::kLoaders >= count || b >= p.csr.batch) continue;
             const int t0 = blk * kTaskTokens, t = t0 + lane;
             if (t0 < rq.len) {
-                const int col = p.csr.ps_shift >= 0 ? t >> p.csr.ps_shift : t / ps;
+                const int col = div_ps(p.csr, t);
                 ask = {b, h, t0, rq.len, t < rq.len ? __ldg(p.csr.kv_indices + rq.p0 + col) : 0, t - col * ps};
             }
             blk += LY::kLoaders;
@@ -702,12 +702,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
 // Row kept[j] of a request and kv head goes to place j. Places ascend, so kept[j] >= j: tiles of
 // rows taken in order never overwrite a row that a later tile reads, and inside a tile every row
 // is read before the first is written. One CTA takes one stream of rows: (request, kv head,
-// 128-byte slice of K or V, or the weights).
-constexpr int kMoveThreads = 256;
-constexpr int kMoveTile = 256;                       // rows per tile
-constexpr int kMoveU = kMoveTile * 8 / kMoveThreads; // 16-byte pieces of a tile per thread
-constexpr int kChunkRows = 16384;                    // e4m3: rows whose factors shared memory holds
-static_assert(kMoveTile == kMoveThreads, "a thread looks up one row of a tile");
+// 128-byte slice of K or V, or the weights). Where the rows lie is looked up for 4096 rows at a
+// time, all reads of a thread in flight together; then the rows go through a ring of four tiles
+// in shared memory, filled by asynchronous copies. 512 threads and tiles of 16 KB, two CTAs to an
+// SM, or 1024 threads and tiles of 32 KB where there is a CTA per SM at most. Bound by the copy's
+// bandwidth where there are many streams, 64 requests x 2048 rows of 1 KB: 175 us (floor 160);
+// by a stream's own chain of reads, barriers and writes where there are few: four 8-bit prompts,
+// 96 streams, 17 us (floor 6; 39 with look-ups and copies one tile at a time, 26 with 256 threads
+// and a ring of ten tiles).
+constexpr int kMoveRows = 4096;                       // rows looked up at a time
 
 struct MoveParams {
     Csr csr;
@@ -718,21 +721,7 @@ struct MoveParams {
     int H, max_keep, row_bytes, slices;
 };
 
-// Source and destination slots of row j, or kNoRow where nothing moves. (A position below j, one
-// behind the request, or a page outside the pool: the row stays.)
-__device__ __forceinline__ void move_slots(const Csr &c, const Request &rq, const int32_t *kept, int j, bool in_place,
-                                           uint32_t &src, uint32_t &dst) {
-    const int i = __ldg(kept + j);
-    src = dst = kNoRow;
-    if (i < j || i >= rq.len || (i == j && !in_place)) return;
-    int page, place;
-    const uint32_t s = slot_of(c, rq, i, page, place), d = slot_of(c, rq, j, page, place);
-    if (s != kNoRow && d != kNoRow) {
-        src = s;
-        dst = d;
-    }
-}
-
+// Four codes times s (a power of two <= 1), rounded to nearest even.
 __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float s) {
     uint32_t h0, h1;
     e4m3x4_to_f16x4(w, h0, h1);
@@ -745,10 +734,24 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float s) {
 
 // kExp: e4m3 codes with an exponent per (page, kv head). A page's exponent becomes the largest
 // of those that its rows had; codes are scaled by the difference and rounded to nearest even.
-template <bool kExp>
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const MoveParams p) {
-    extern __shared__ int8_t factor[];  // kExp: [kChunkRows] exponents, then factors, of a chunk's rows
-    __shared__ uint32_t s_src[2][kMoveTile], s_dst[2][kMoveTile];
+template <bool kExp, int kThreads>
+struct MoveLayout {
+    static constexpr int kTile = kThreads / 4, kStages = 4;  // rows of a tile: two 16-byte pieces per thread
+    static constexpr int kTileBytes = kTile * 128;
+    static constexpr int kSrcOff = kStages * kTileBytes;  // behind the ring: source and destination slots
+    static constexpr int kFactorOff = kSrcOff + 8 * kMoveRows;
+    static constexpr int kSmem = kFactorOff + (kExp ? kMoveRows : 0);
+    static_assert(kSmem <= 227 * 1024 && kStages * kTileBytes >= 4 * kMoveRows, "the ring holds a largest exponent per row too");
+};
+
+template <bool kExp, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(const MoveParams p) {
+    using LY = MoveLayout<kExp, kThreads>;
+    constexpr int kU = kMoveRows / kThreads;  // rows looked up per thread
+    constexpr int kTile = LY::kTile, kStages = LY::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint32_t *s_src = reinterpret_cast<uint32_t *>(smem + LY::kSrcOff), *s_dst = s_src + kMoveRows;
+    int8_t *factor = reinterpret_cast<int8_t *>(smem + LY::kFactorOff);  // kExp: of the rows' codes
     const int tid = threadIdx.x, H = p.H, ps = p.csr.ps;
     const int h = blockIdx.y, b = blockIdx.z;
     const Request rq = request(p.csr, b);
@@ -756,16 +759,45 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const MoveParams 
     if (n == 0) return;
     const int32_t *kept = p.kept + ((size_t)b * H + h) * p.max_keep;
     const int slices = p.slices;
+
+    // this thread's rows r0 + tid + 256 u, below r1: the slots of their source and their place, or kNoRow.
+    // (A position below the place, one behind the request, or a page outside the pool: the row stays.)
+    auto look_up = [&](int r0, int r1, uint32_t (&src)[kU], uint32_t (&dst)[kU], int (&page)[kU]) {
+        int at[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int j = r0 + tid + u * kThreads;
+            at[u] = j < r1 ? __ldg(kept + j) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int j = r0 + tid + u * kThreads;
+            int place, to;
+            src[u] = at[u] >= j && at[u] < rq.len ? slot_of(p.csr, rq, at[u], page[u], place) : kNoRow;
+            dst[u] = j < r1 ? slot_of(p.csr, rq, j, to, place) : kNoRow;
+            if (src[u] == kNoRow || dst[u] == kNoRow) {  // stays: its source is its place
+                src[u] = dst[u];
+                page[u] = to;
+            }
+        }
+    };
     if ((int)blockIdx.x == 2 * slices) {
         // ---- weights: one value per row
-        for (int j0 = 0; j0 < n; j0 += kMoveThreads) {
-            const int j = j0 + tid;
-            uint32_t src = kNoRow, dst = kNoRow;
-            if (j < n) move_slots(p.csr, rq, kept, j, false, src, dst);
-            auto at = [&](uint32_t s) -> size_t { return ((size_t)(s / (uint32_t)ps) * H + h) * ps + s % (uint32_t)ps; };
-            const float x = src != kNoRow ? p.weights[at(src)] : 0.f;
+        auto at = [&](uint32_t s) -> float * {
+            const uint32_t pg = s / (uint32_t)ps;
+            return p.weights + ((size_t)pg * H + h) * ps + (s - pg * (uint32_t)ps);
+        };
+        for (int r0 = 0; r0 < n; r0 += kMoveRows) {
+            uint32_t src[kU], dst[kU];
+            int page[kU];
+            float x[kU];
+            look_up(r0, min(n, r0 + kMoveRows), src, dst, page);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) x[u] = src[u] != dst[u] ? __ldcg(at(src[u])) : 0.f;
             __syncthreads();
-            if (src != kNoRow) p.weights[at(dst)] = x;
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (src[u] != dst[u]) *at(dst[u]) = x[u];
             __syncthreads();
         }
         return;
@@ -777,82 +809,88 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const MoveParams 
     uint8_t *base = (is_v ? p.v : p.k) + (size_t)h * p.row_bytes + off;
     const size_t stride = (size_t)H * p.row_bytes;
     int8_t *exps = is_v ? p.v_exp : p.k_exp;
-    const int chunk = kExp ? kChunkRows / ps * ps : n;  // (host: ps <= kChunkRows)
-    for (int c0 = 0; c0 < n; c0 += chunk) {
-        const int c1 = min(n, c0 + chunk);
-        if constexpr (kExp) {
-            // the rows' exponents, each page's largest, the pages' new exponents. (Pages of this chunk's
-            // places are read by no later chunk: its rows come from places at or behind its own.)
-            for (int j = c0 + tid; j < c1; j += kMoveThreads) {
-                uint32_t src, dst;
-                move_slots(p.csr, rq, kept, j, true, src, dst);
-                int page, place;
-                if (src != kNoRow) factor[j - c0] = exps[(size_t)(src / (uint32_t)ps) * H + h];
-                else factor[j - c0] = slot_of(p.csr, rq, j, page, place) != kNoRow ? exps[(size_t)page * H + h] : (int8_t)-128;  // stays
-            }
-            __syncthreads();
-            for (int q0 = c0 + tid * ps; q0 < c1; q0 += kMoveThreads * ps) {
-                int e = -128;
-                const int q1 = min(q0 + ps, c1);
-                for (int j = q0; j < q1; ++j) e = max(e, (int)factor[j - c0]);
-                for (int j = q0; j < q1; ++j) factor[j - c0] = (int8_t)max((int)factor[j - c0] - e, -100);
-                int page, place;
-                const uint32_t d = slot_of(p.csr, rq, q0, page, place);
-                if (d != kNoRow) exps[(size_t)page * H + h] = (int8_t)e;
-            }
-            __syncthreads();
-        }
-        uint4 x[2][kMoveU];
-        auto look_up = [&](int t, int buf) {
-            const int j = c0 + t * kMoveTile + tid;
-            uint32_t src = kNoRow, dst = kNoRow;
-            if (j < c1) move_slots(p.csr, rq, kept, j, kExp && factor[j - c0] != 0, src, dst);
-            s_src[buf][tid] = src;
-            s_dst[buf][tid] = dst;
-        };
-        auto load = [&](int buf, uint4 (&r)[kMoveU]) {
+    const int chunk = kExp ? kMoveRows / ps * ps : kMoveRows;  // (host: ps <= kMoveRows)
+    for (int r0 = 0; r0 < n; r0 += chunk) {
+        const int r1 = min(n, r0 + chunk);
+        {
+            uint32_t src[kU], dst[kU];
+            int page[kU], f[kU];
+            look_up(r0, r1, src, dst, page);
+            if constexpr (kExp) {
+                // the rows' exponents, each page's largest (in the ring, which is not used yet), the pages' new
+                // exponents. (Pages of this chunk's places are read by no later chunk: its rows come from places
+                // at or behind its own.)
+                int *most = reinterpret_cast<int *>(smem);
 #pragma unroll
-            for (int u = 0; u < kMoveU; ++u) {
-                const uint32_t s = s_src[buf][(tid >> 3) + 32 * u];
-                if (live && s != kNoRow) r[u] = *reinterpret_cast<const uint4 *>(base + (size_t)s * stride);
-            }
-        };
-        auto store = [&](int t, int buf, uint4 (&r)[kMoveU]) {
-#pragma unroll
-            for (int u = 0; u < kMoveU; ++u) {
-                const int jl = (tid >> 3) + 32 * u;
-                const uint32_t d = s_dst[buf][jl];
-                if (!live || d == kNoRow) continue;
-                if constexpr (kExp) {
-                    const int f = factor[t * kMoveTile + jl];
-                    if (f != 0) {
-                        const float s = pow2i(f);
-                        r[u].x = rescale_codes(r[u].x, s);
-                        r[u].y = rescale_codes(r[u].y, s);
-                        r[u].z = rescale_codes(r[u].z, s);
-                        r[u].w = rescale_codes(r[u].w, s);
-                    }
+                for (int u = 0; u < kU; ++u) {
+                    f[u] = src[u] != kNoRow ? exps[(size_t)page[u] * H + h] : -128;
+                    most[tid + u * kThreads] = -128;
                 }
-                *reinterpret_cast<uint4 *>(base + (size_t)d * stride) = r[u];
-            }
-        };
-        const int nt = (c1 - c0 + kMoveTile - 1) / kMoveTile;
-        look_up(0, 0);
-        __syncthreads();
-        load(0, x[0]);
-        if (nt > 1) look_up(1, 1);
-        for (int t = 0; t < nt; t += 2) {
+                __syncthreads();
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (t + u >= nt) break;
-                __syncthreads();  // this tile is read; the next one is looked up
-                if (t + u + 1 < nt) load(u ^ 1, x[u ^ 1]);
-                store(t + u, u, x[u]);
-                __syncthreads();  // its slots are used
-                if (t + u + 2 < nt) look_up(t + u + 2, u);
+                for (int u = 0; u < kU; ++u) {
+                    const int j = tid + u * kThreads;
+                    if (r0 + j < r1) atomicMax(most + div_ps(p.csr, j), f[u]);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int j = tid + u * kThreads, q = div_ps(p.csr, j);
+                    if (r0 + j >= r1) continue;
+                    const int e = most[q];
+                    f[u] = max(f[u] - e, -100);
+                    factor[j] = (int8_t)f[u];
+                    if (j == q * ps && dst[u] != kNoRow) exps[(size_t)(dst[u] / (uint32_t)ps) * H + h] = (int8_t)e;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int j = r0 + tid + u * kThreads;
+                const bool moves = src[u] != dst[u] || (kExp && j < r1 && f[u] != 0);
+                s_src[j - r0] = moves ? src[u] : kNoRow;
+                s_dst[j - r0] = dst[u];
             }
         }
         __syncthreads();
+        const uint32_t ring = smem_u32(smem) + tid * 16;
+        const int nt = (r1 - r0 + kTile - 1) / kTile;
+        auto fetch = [&](int t) {  // a tile's pieces of this thread into its stage, one group of copies
+            if (t < nt && live) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t s = s_src[t * kTile + (tid >> 3) + u * (kThreads / 8)];
+                    if (s != kNoRow) cp_async_16(ring + t % kStages * LY::kTileBytes + u * kThreads * 16, base + (size_t)s * stride, 16);
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int t = 0; t < kStages - 1; ++t) fetch(t);
+        for (int t = 0; t < nt; ++t) {
+            fetch(t + kStages - 1);
+            cp_async_wait<kStages - 1>();
+            __syncthreads();  // every row of the tile is read
+            if (live) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int jl = t * kTile + (tid >> 3) + u * (kThreads / 8);
+                    if (s_src[jl] == kNoRow) continue;
+                    uint4 x = sm100::ld_shared_v4(ring + t % kStages * LY::kTileBytes + u * kThreads * 16);
+                    if constexpr (kExp) {
+                        const int f = factor[jl];
+                        if (f != 0) {
+                            const float s = pow2i(f);
+                            x.x = rescale_codes(x.x, s);
+                            x.y = rescale_codes(x.y, s);
+                            x.z = rescale_codes(x.z, s);
+                            x.w = rescale_codes(x.w, s);
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(base + (size_t)s_dst[jl] * stride) = x;
+                }
+            }
+        }
+        __syncthreads();  // the slots are used
     }
 }
 
@@ -876,7 +914,12 @@ int launched(const char *what) {
 
 Csr make_csr(const int32_t *kv_indptr, const int32_t *kv_indices, const int32_t *last_page_len, int64_t max_pages, int batch,
              int ps, int64_t num_pages) {
-    return {kv_indptr, kv_indices, last_page_len, (int)max_pages, batch, ps, (int)num_pages, (ps & (ps - 1)) == 0 ? __builtin_ctz(ps) : -1};
+    // ceil(2^(31 + k) / ps), k = ceil(log2(ps)): its excess over 2^(31 + k) / ps is below 1, so that t * excess stays
+    // below 2^31 <= 2^(31 + k) / ps * (distance of t / ps to the next whole number)
+    int k = 0;
+    while ((int64_t{1} << k) < ps) ++k;
+    const uint32_t mul = (uint32_t)(((uint64_t{1} << (31 + k)) + ps - 1) / ps);
+    return {kv_indptr, kv_indices, last_page_len, (int)max_pages, batch, ps, (int)num_pages, mul, 31 + k};
 }
 
 template <int D, bool kE4m3, bool kDiff, bool kVar>
@@ -905,6 +948,21 @@ int launch_weights(const WeightsParams &p, int64_t tasks, int sms, cudaStream_t 
                    : launch_weights_kernel<D, kE4m3, true, false>(p, tasks, sms, stream);
     return var ? launch_weights_kernel<D, kE4m3, false, true>(p, tasks, sms, stream)
                : launch_weights_kernel<D, kE4m3, false, false>(p, tasks, sms, stream);
+}
+
+template <bool kExp, int kThreads>
+int launch_compact(const MoveParams &p, dim3 grid, cudaStream_t stream) {
+    using LY = MoveLayout<kExp, kThreads>;
+    static bool configured[64] = {false};
+    int dev = 0;
+    if (current_sms(&dev) < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    if (!configured[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(compact_kernel<kExp, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kSmem);
+        if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("compact smem attribute: ") + cudaGetErrorString(e));
+        configured[dev] = true;
+    }
+    compact_kernel<kExp, kThreads><<<grid, kThreads, LY::kSmem, stream>>>(p);
+    return launched("compact");
 }
 
 }  // namespace
@@ -1017,13 +1075,12 @@ int launch_compact_cache(const int32_t *kept, const int32_t *new_lens, int32_t m
     p.row_bytes = row_bytes;
     p.slices = (row_bytes + 127) / 128;
     const dim3 grid(2 * p.slices + (weights ? 1 : 0), num_kv_heads, batch);
-    if (k_exp) {
-        if (page_size > kChunkRows) return fail(BSP_ERR_UNSUPPORTED, "compacting the 8-bit cache takes pages of at most 16384 tokens");
-        compact_kernel<true><<<grid, kMoveThreads, kChunkRows, stream>>>(p);
-    } else {
-        compact_kernel<false><<<grid, kMoveThreads, 0, stream>>>(p);
-    }
-    return launched("compact");
+    if (k_exp && page_size > kMoveRows) return fail(BSP_ERR_UNSUPPORTED, "compacting the 8-bit cache takes pages of at most 4096 tokens");
+    const int sms = current_sms();
+    if (sms < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
+    const bool few = (int64_t)grid.x * grid.y * grid.z <= sms;
+    if (k_exp) return few ? launch_compact<true, 1024>(p, grid, stream) : launch_compact<true, 512>(p, grid, stream);
+    return few ? launch_compact<false, 1024>(p, grid, stream) : launch_compact<false, 512>(p, grid, stream);
 }
 
 }  // namespace bsp

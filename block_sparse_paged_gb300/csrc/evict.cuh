@@ -19,7 +19,8 @@ struct Csr {
     const int32_t *kv_indptr, *kv_indices, *last_page_len;
     int max_pages;  // entries of kv_indices
     int batch, ps, num_pages;
-    int ps_shift;   // log2(ps), or -1
+    uint32_t div_mul;  // t / ps = t * div_mul >> div_shift for 0 <= t < 2^31
+    int div_shift;
 };
 
 struct Request {
@@ -34,9 +35,11 @@ __device__ __forceinline__ Request request(const Csr &c, int b) {
     return {p0, n > 0 ? (int)min((long long)(n - 1) * c.ps + last, (long long)INT_MAX) : 0};
 }
 
+__device__ __forceinline__ int div_ps(const Csr &c, int t) { return (int)(((uint64_t)(uint32_t)t * c.div_mul) >> c.div_shift); }
+
 // Slot of token t of a request, or kNoRow (host: num_pages * ps < 2^32 - 1).
 __device__ __forceinline__ uint32_t slot_of(const Csr &c, const Request &r, int t, int &page, int &place) {
-    const int col = c.ps_shift >= 0 ? t >> c.ps_shift : t / c.ps;
+    const int col = div_ps(c, t);
     place = t - col * c.ps;
     page = __ldg(c.kv_indices + r.p0 + col);
     return (unsigned)page < (unsigned)c.num_pages ? (uint32_t)page * (uint32_t)c.ps + (uint32_t)place : kNoRow;

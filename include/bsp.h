@@ -630,7 +630,7 @@ int bsp_select_tokens(const float *weights, int64_t num_pages, int32_t page_size
  *   row_bytes    bytes of a row of K and of V: D times the element's size, a multiple of 16
  *   k_exp, v_exp NULL, or the exponents of e4m3 pools (row_bytes 128): a page's exponent
  *                becomes the largest of those that its kept rows had, and codes are rescaled
- *                to it (rounded to nearest even)
+ *                to it (rounded to nearest even); pages of at most 4096 tokens
  * Rows behind the kept ones stay as they are. Pages that two requests share must not be
  * compacted: a page belongs to one request of the batch.
  */

@@ -127,5 +127,6 @@ def test_compact_refuses(native, kw):
 
 def test_compact_unsupported_and_nothing(native):
     assert compact(native, ke=P16, ve=P16) == native.BSP_ERR_UNSUPPORTED  # 256-byte rows of e4m3
+    assert compact(native, ke=P16, ve=P16, row=128, ps=4097) == native.BSP_ERR_UNSUPPORTED
     assert compact(native, batch=0, kept=None, new=None, kvp=None, kvi=None, last=None) == native.BSP_OK
     assert compact(native, most=0, kept=None) == native.BSP_OK
