@@ -149,7 +149,7 @@ class PagedAttention:
         self._copied = None  # event after the last plan copy
         self._q_tail, self._page_tail = (num_qo_heads, head_dim), (page_size, num_kv_heads, head_dim)
         self._default_scale = 1.0 / math.sqrt(head_dim // 2 if differential else head_dim)
-        self.info = self._fp8_plan = self._fp8_shapes = None  # of the current plan
+        self.info = self._fp8_plan = self._fp8_shapes = self._diff_plan = self._diff_shapes = None  # of the current plan
         self._sink_on = False  # its info points to a sink
 
     # ---- plan ---------------------------------------------------------------
@@ -182,7 +182,7 @@ class PagedAttention:
             ev.record(stream if stream is not None else torch.cuda.current_stream())
             self._copied = ev
         self.info = info
-        self._fp8_plan = self._fp8_shapes = None
+        self._fp8_plan = self._fp8_shapes = self._diff_plan = self._diff_shapes = None
         self._sink_on = False
         return info
 
@@ -338,63 +338,89 @@ class PagedAttention:
         and lse float32 [n, H_qo, 2]. Pools and kv_indices as for run(): bfloat16, or an 8-bit cache with k_exp and
         v_exp (a prefill over it converts its pages into a bf16 copy first, in the workspace's copy region where
         max_gather_pages covers the page table, else in a temporary tensor of this call)."""
-        if self.info is None:
-            raise RuntimeError("plan() must be called before run_differential()")
+        # (A short step's time is this function's: what depends on the plan and on shapes alone is looked at once per plan.)
         if not self.differential:
             raise RuntimeError("run_differential() needs an object made with differential=True")
-        dev, info = self.device, self.info
-        if (k_exp is None) != (v_exp is None):
-            raise ValueError("k_exp and v_exp are given together")
-        fp8 = k_exp is not None
+        dev, bf16, f32, fp8 = self.device, torch.bfloat16, torch.float32, k_exp is not None
         q_shape, pool = q.shape, k_pages.shape
-        if len(q_shape) != 3 or q_shape[1:] != self._q_tail or q_shape[0] < info.num_qo_tokens:
-            raise ValueError(f"q must be [n_tokens, {self._q_tail[0]}, {self._q_tail[1]}] with the plan's tokens")
-        if len(pool) != 4 or pool[1:] != self._page_tail or v_pages.shape != pool:
-            raise ValueError("k_pages / v_pages must be [num_pages, %d, %d, %d]" % self._page_tail)
-        if fp8 and (k_exp.shape != (pool[0], pool[2]) or v_exp.shape != k_exp.shape):
-            raise ValueError(f"k_exp / v_exp must be [{pool[0]}, {pool[2]}]")
-        if kv_indices.dim() != 1 or kv_indices.shape[0] < info.num_table_pages:
-            raise ValueError(f"kv_indices must hold the plan's {info.num_table_pages} pages")
-        if lam.shape != (q_shape[1],):
-            raise ValueError(f"lam must be [{q_shape[1]}]")
-        if norm_weight is not None and norm_weight.shape != (q_shape[2],):
-            raise ValueError(f"norm_weight must be [{q_shape[2]}]")
-        bf16, f32 = torch.bfloat16, torch.float32
+        shapes = (q_shape, pool, v_pages.shape, kv_indices.shape, lam.shape, None if norm_weight is None else norm_weight.shape,
+                  None if k_exp is None else k_exp.shape, None if v_exp is None else v_exp.shape)
+        if shapes != self._diff_shapes:
+            self._check_diff_shapes(*shapes)
+            self._diff_shapes = shapes
+        ref, fn, region, nbytes, ws, diff, diff_ref, at = self._diff_plan or self._look_at_diff_plan(fp8)
+        if at is not fp8:
+            ref, fn, region, nbytes, ws, diff, diff_ref, at = self._look_at_diff_plan(fp8)
         kv_dt = torch.float8_e4m3fn if fp8 else bf16
-        q_p, k_p, v_p = _addr(q, "q", bf16, dev), _addr(k_pages, "k_pages", kv_dt, dev), _addr(v_pages, "v_pages", kv_dt, dev)
-        diff = N.Differential(_addr(lam, "lam", f32, dev), None if norm_weight is None else _addr(norm_weight, "norm_weight", f32, dev),
-                              norm_eps, out_scale)
+        q_p = _addr(q, "q", bf16, dev)
+        diff.lam = _addr(lam, "lam", f32, dev)
+        diff.norm_weight = None if norm_weight is None else _addr(norm_weight, "norm_weight", f32, dev)
+        diff.norm_eps, diff.out_scale = norm_eps, out_scale
         if out is None:
-            out = _new(stream, lambda: torch.empty_like(q))
-        elif out.shape != q_shape:
-            raise ValueError("out must have the shape of q")
-        if lse is None:
-            if return_lse:
-                lse = _new(stream, lambda: torch.empty(q_shape[0], q_shape[1], 2, dtype=f32, device=dev))
-        elif lse.shape != (q_shape[0], q_shape[1], 2):
-            raise ValueError("lse must be [n_tokens, H_qo, 2]")
-        lib, ref, ws = self.lib, ctypes.byref(info), self.workspace.data_ptr()
-        region, nbytes, copy = None, 0, None
-        if self.mode == N.BSP_MODE_DECODE:
-            fn = lib.bsp_decode_run_diff
-            nbytes = lib.bsp_decode_fp8_region_size(ref) if fp8 else 0
+            out = torch.empty_like(q) if stream is None else _new(stream, lambda: torch.empty_like(q))
+            out_p = out.data_ptr()
         else:
-            fn = lib.bsp_prefill_run_diff
-            nbytes = lib.bsp_prefill_diff_region_size(ref) if fp8 else 0
-            if nbytes and self.capacity.max_gather_pages >= info.num_table_pages:
-                region, nbytes = ws + info.off_gather, 2 * info.gather_pool_bytes
-        if nbytes and region is None:  # scratch of this run alone
+            if out.shape != q_shape:
+                raise ValueError("out must have the shape of q")
+            out_p = _addr(out, "out", bf16, dev)
+        lse_p = None
+        if lse is not None:
+            if lse.shape != q_shape[:2] + (2,):
+                raise ValueError("lse must be [n_tokens, H_qo, 2]")
+            lse_p = _addr(lse, "lse", f32, dev)
+        elif return_lse:
+            shape = (q_shape[0], q_shape[1], 2)
+            lse = torch.empty(shape, dtype=f32, device=dev) if stream is None else _new(stream, lambda: torch.empty(shape, dtype=f32, device=dev))
+            lse_p = lse.data_ptr()
+        copy = None
+        if nbytes and region is None:  # scratch of this run alone: the plan's exponents, or a bf16 copy of its pages
             if stream is None:
                 copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             else:
                 with torch.cuda.stream(stream):
                     copy = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             region = copy.data_ptr()
-        _call(dev, stream, fn, ref, ctypes.byref(diff), q_p, k_p, v_p, None if not fp8 else _addr(k_exp, "k_exp", torch.int8, dev),
-              None if not fp8 else _addr(v_exp, "v_exp", torch.int8, dev), _addr(kv_indices, "kv_indices", torch.int32, dev) or None,
-              pool[0], self._default_scale if sm_scale is None else sm_scale, _addr(out, "out", bf16, dev),
-              None if lse is None else _addr(lse, "lse", f32, dev), region, nbytes, ws)
+        ke_p = ve_p = None
+        if fp8:
+            ke_p, ve_p = _addr(k_exp, "k_exp", torch.int8, dev), _addr(v_exp, "v_exp", torch.int8, dev)
+        _call(dev, stream, fn, ref, diff_ref, q_p, _addr(k_pages, "k_pages", kv_dt, dev), _addr(v_pages, "v_pages", kv_dt, dev), ke_p, ve_p,
+              _addr(kv_indices, "kv_indices", torch.int32, dev) or None, pool[0], self._default_scale if sm_scale is None else sm_scale,
+              out_p, lse_p, region, nbytes, ws)
         return (out, lse) if return_lse else out
+
+    def _check_diff_shapes(self, q, k_pages, v_pages, kv_indices, lam, norm_weight, k_exp, v_exp):
+        info = self.info
+        if info is None:
+            raise RuntimeError("plan() must be called before run_differential()")
+        if (k_exp is None) != (v_exp is None):
+            raise ValueError("k_exp and v_exp are given together")
+        if len(q) != 3 or q[1:] != self._q_tail or q[0] < info.num_qo_tokens:
+            raise ValueError(f"q must be [n_tokens, {self._q_tail[0]}, {self._q_tail[1]}] with the plan's tokens")
+        if len(k_pages) != 4 or k_pages[1:] != self._page_tail or v_pages != k_pages:
+            raise ValueError("k_pages / v_pages must be [num_pages, %d, %d, %d]" % self._page_tail)
+        if k_exp is not None and (k_exp != (k_pages[0], k_pages[2]) or v_exp != k_exp):
+            raise ValueError(f"k_exp / v_exp must be [{k_pages[0]}, {k_pages[2]}]")
+        if len(kv_indices) != 1 or kv_indices[0] < info.num_table_pages:
+            raise ValueError(f"kv_indices must hold the plan's {info.num_table_pages} pages")
+        if lam != (q[1],):
+            raise ValueError(f"lam must be [{q[1]}]")
+        if norm_weight is not None and norm_weight != (q[2],):
+            raise ValueError(f"norm_weight must be [{q[2]}]")
+
+    def _look_at_diff_plan(self, fp8):
+        """(plan info reference, entry, region in the workspace or None, region bytes, workspace, argument structure, its
+        reference, fp8) of the current plan."""
+        info, lib, ws, ref = self.info, self.lib, self.workspace.data_ptr(), ctypes.byref(self.info)
+        region = None
+        if self.mode == N.BSP_MODE_DECODE:
+            fn, nbytes = lib.bsp_decode_run_diff, lib.bsp_decode_fp8_region_size(ref) if fp8 else 0
+        else:
+            fn, nbytes = lib.bsp_prefill_run_diff, lib.bsp_prefill_diff_region_size(ref) if fp8 else 0
+            if nbytes and self.capacity.max_gather_pages >= info.num_table_pages:
+                region, nbytes = ws + info.off_gather, 2 * info.gather_pool_bytes  # the workspace's copy region
+        diff = N.Differential()
+        self._diff_plan = (ref, fn, region, nbytes, ws, diff, ctypes.byref(diff), fp8)
+        return self._diff_plan
 
     def _set_sink(self, sink):
         self._sink_on = sink is not None
@@ -605,12 +631,13 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_pages:
 
 def _table_args(kv_indptr, kv_indices, last_page_len, dev):
     """(batch, kv_indptr, kv_indices, its entries, last_page_len) of a page table in CSR form on the device."""
-    if kv_indptr.dim() != 1 or kv_indptr.shape[0] < 1 or kv_indices.dim() != 1:
+    rows, entries, i32 = kv_indptr.shape, kv_indices.shape, torch.int32
+    if len(rows) != 1 or rows[0] < 1 or len(entries) != 1:
         raise ValueError("kv_indptr must be [B + 1] and kv_indices one-dimensional")
-    B, i32 = kv_indptr.shape[0] - 1, torch.int32
+    B = rows[0] - 1
     if last_page_len.shape != (B,):
         raise ValueError(f"last_page_len must be [{B}]")
-    return (B, _addr(kv_indptr, "kv_indptr", i32, dev), _addr(kv_indices, "kv_indices", i32, dev), kv_indices.shape[0],
+    return (B, _addr(kv_indptr, "kv_indptr", i32, dev), _addr(kv_indices, "kv_indices", i32, dev), entries[0],
             _addr(last_page_len, "last_page_len", i32, dev))
 
 
@@ -627,13 +654,13 @@ def accumulate_weights(q: torch.Tensor, lse: torch.Tensor, k_pages: torch.Tensor
     float8_e4m3fn. weights: float32 [num_pages, H_kv, page_size]. kv_indptr, kv_indices, last_page_len, qo_indptr:
     int32 on the device, as build_page_tables gives them (qo_indptr None: one query per request). lam: float32 [H_qo]
     after run_differential, whose lse is [n_tokens, H_qo, 2]. sm_scale, window_left, logits_soft_cap: the run's."""
-    dev = k_pages.device
-    if q.dim() != 3 or k_pages.dim() != 4:
+    dev, q_shape, pool, dtype = k_pages.device, q.shape, k_pages.shape, q.dtype
+    if len(q_shape) != 3 or len(pool) != 4:
         raise ValueError("q must be [n_tokens, H_qo, D] and k_pages [num_pages, page_size, H_kv, D]")
-    (n, Hq, D), (P, ps, H, Dk) = q.shape, k_pages.shape
-    if Dk != D or Hq % H != 0:
+    (n, Hq, D), (P, ps, H, Dk) = q_shape, pool
+    if Dk != D or H == 0 or Hq % H != 0:
         raise ValueError(f"q has {Hq} heads of {D} values, k_pages {H} of {Dk}")
-    if q.dtype not in _DTYPES:
+    if dtype not in _DTYPES:
         raise ValueError("q must be bfloat16 or float32")
     if lse.shape != ((n, Hq) if lam is None else (n, Hq, 2)):
         raise ValueError("lse must be [n_tokens, H_qo], or [n_tokens, H_qo, 2] with lam")
@@ -652,10 +679,10 @@ def accumulate_weights(q: torch.Tensor, lse: torch.Tensor, k_pages: torch.Tensor
         raise ValueError(f"qo_indptr must be [{B + 1}]")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(D if lam is None else D // 2)
-    problem = N.Problem(N.BSP_MODE_DECODE, Hq, H, D, ps, 1, _DTYPES[q.dtype], int(window_left), float(logits_soft_cap))
-    _call(dev, stream, N.load().bsp_accumulate_weights, ctypes.byref(problem), _addr(q, "q", q.dtype, dev) or None,
+    problem = N.Problem(N.BSP_MODE_DECODE, Hq, H, D, ps, 1, _DTYPES[dtype], window_left, logits_soft_cap)
+    _call(dev, stream, N.load().bsp_accumulate_weights, ctypes.byref(problem), _addr(q, "q", dtype, dev) or None,
           _addr(lse, "lse", f32, dev) or None, n,
-          _addr(k_pages, "k_pages", torch.float8_e4m3fn if k_exp is not None else q.dtype, dev),
+          _addr(k_pages, "k_pages", torch.float8_e4m3fn if k_exp is not None else dtype, dev),
           None if k_exp is None else _addr(k_exp, "k_exp", torch.int8, dev), P, _addr(weights, "weights", f32, dev), B,
           None if qo_indptr is None else _addr(qo_indptr, "qo_indptr", torch.int32, dev), indptr, indices or None, entries,
           last or None, sm_scale, decay, None if lam is None else _addr(lam, "lam", f32, dev))
@@ -679,11 +706,13 @@ def select_tokens(weights: torch.Tensor, kv_indptr: torch.Tensor, kv_indices: to
     if max_keep < 0:
         raise ValueError("max_keep must not be negative")
     if kept is None:
-        kept = _new(stream, lambda: torch.empty((B, H, max_keep), dtype=i32, device=dev))
+        kept = torch.empty((B, H, max_keep), dtype=i32, device=dev) if stream is None else _new(
+            stream, lambda: torch.empty((B, H, max_keep), dtype=i32, device=dev))
     elif kept.shape != (B, H, max_keep):
         raise ValueError(f"kept must be [{B}, {H}, {max_keep}]")
     if new_lens is None:
-        new_lens = _new(stream, lambda: torch.empty((B,), dtype=i32, device=dev))
+        new_lens = torch.empty(B, dtype=i32, device=dev) if stream is None else _new(
+            stream, lambda: torch.empty(B, dtype=i32, device=dev))
     elif new_lens.shape != (B,):
         raise ValueError(f"new_lens must be [{B}]")
     _call(dev, stream, N.load().bsp_select_tokens, _addr(weights, "weights", torch.float32, dev), P, ps, H, B, indptr,
@@ -703,9 +732,10 @@ def compact_cache(kept: torch.Tensor, new_lens: torch.Tensor, kv_indptr: torch.T
     kept, new_lens: as select_tokens gives them. k_pages, v_pages: pools [num_pages, page_size, H_kv, D] of one type;
     with k_exp, v_exp (int8 [num_pages, H_kv]) e4m3 codes, whose pages take the largest exponent of their rows."""
     dev, i32 = k_pages.device, torch.int32
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype is not k_pages.dtype:
+    pool, dt = k_pages.shape, k_pages.dtype
+    if len(pool) != 4 or v_pages.shape != pool or v_pages.dtype is not dt:
         raise ValueError("k_pages / v_pages must be [num_pages, page_size, H_kv, D], of one type")
-    P, ps, H, D = k_pages.shape
+    P, ps, H, D = pool
     B, indptr, indices, entries, last = _table_args(kv_indptr, kv_indices, last_page_len, dev)
     if kept.dim() != 3 or kept.shape[:2] != (B, H) or new_lens.shape != (B,):
         raise ValueError(f"kept must be [{B}, {H}, max_keep] and new_lens [{B}]")
@@ -715,7 +745,8 @@ def compact_cache(kept: torch.Tensor, new_lens: torch.Tensor, kv_indptr: torch.T
         raise ValueError("k_exp and v_exp are given together")
     if k_exp is not None and (k_exp.shape != (P, H) or v_exp.shape != (P, H)):
         raise ValueError(f"k_exp / v_exp must be [{P}, {H}]")
-    dt = torch.float8_e4m3fn if k_exp is not None else k_pages.dtype
+    if k_exp is not None:
+        dt = torch.float8_e4m3fn
     _call(dev, stream, N.load().bsp_compact_cache, _addr(kept, "kept", i32, dev) or None,
           _addr(new_lens, "new_lens", i32, dev) or None, kept.shape[2], B, indptr, indices or None, entries, last or None,
           _addr(k_pages, "k_pages", dt, dev), _addr(v_pages, "v_pages", dt, dev),

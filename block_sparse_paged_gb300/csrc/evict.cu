@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(cons
     using LY = MoveLayout<kExp, kThreads>;
     constexpr int kU = kMoveRows / kThreads;  // rows looked up per thread
     constexpr int kTile = LY::kTile, kStages = LY::kStages;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint32_t *s_src = reinterpret_cast<uint32_t *>(smem + LY::kSrcOff), *s_dst = s_src + kMoveRows;
     int8_t *factor = reinterpret_cast<int8_t *>(smem + LY::kFactorOff);  // kExp: of the rows' codes
     const int tid = threadIdx.x, H = p.H, ps = p.csr.ps;

@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (kDiff) v2[j] = dev::tanh_ex2(v2[j] * p.cap_in);
                         }
                     }
-                    float4 lr[8], l2r[kDiff ? 8 : 1], lmr[kDiff ? 8 : 1];  // all loads before the first use
+                    float4 lr[8];  // all loads before the first use
+                    [[maybe_unused]] float4 l2r[kDiff ? 8 : 1], lmr[kDiff ? 8 : 1];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         lr[j] = lse[c / 4 + j];
