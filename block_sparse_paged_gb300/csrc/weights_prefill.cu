@@ -13,7 +13,8 @@
 //               32 KB), and the tiles' -LSE log2 e (4 slots)
 //   warp 1      TMEM owner; one thread issues S^T of both 128-key halves per Q tile
 //   warps 2-9   keys 0..127, warps 10-17 keys 128..255: two threads per key, 64 columns of a tile
-//               each (one thread per key, 8 warps: 543 us for two prompts of about 7k, 512 so)
+//               each (one thread per key, 8 warps: 543 us for two prompts of about 7k, 512 so; 499 with
+//               fewer instructions for waits and masks)
 // Each half has two accumulators, so that the tensor core fills one while the other is summed
 // (differential weights need both for the two maps of a tile).
 // Units go to CTAs in the order of the table; a request's first units have the most queries
@@ -154,7 +155,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 1;
         return false;
     };
-    auto wait = [&](uint32_t b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait1(b, parity)); };
+    // (the first try alone where it succeeds: a sum warp's own instructions are what a tile waits for)
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_try_wait(b, parity)) || __all_sync(0xffffffffu, wait1(b, parity));
+    };
     const int g = p.g, ppt = kRows / g;
 
     if (warp == 0) {
@@ -280,19 +284,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *at = p.weights + ((size_t)page * p.H_kv + x.h) * p.csr.ps + place;
             const float old = !col0 && slot != kNoRow && t < x.off && p.decay != 0.f ? *at : 0.f;
             float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+            // tiles all of whose queries see all keys of the unit
+            const int full_lo = p.window > 0 ? x.tiles : (max(0, x.t0 + kUnit - 1 - x.off) + ppt - 1) / ppt - x.tile0;
+            const int full_hi = x.qs.n / ppt - x.tile0;
             for (int i = 0; i < x.tiles; ++i, ++n) {
-                const int pos0 = (x.tile0 + i) * ppt, rows = min(kRows, (x.qs.n - pos0) * g);
                 const int acc = kDiff ? 0 : n & 1, use = kDiff ? n : n >> 1, sl = n % kLSlots;
                 if (!(ok = wait(bar(kLFull0 + sl), (n / kLSlots) & 1))) break;
                 if (!(ok = wait(bar(kSFull0 + 2 * half + acc), use & 1))) break;
                 tc_fence_after();
                 const float4 *lse = reinterpret_cast<const float4 *>(smem + kOffL + sl * kLBytes);
-                // columns that see this key: positions t .. t + window
-                const int c_lo = max(0, t - x.off - pos0) * g;
-                int c_hi = rows;
-                if (p.window > 0) c_hi = (int)max(0ll, min((long long)rows, ((long long)t - x.off - pos0 + p.window + 1) * g));
-                const bool full = __all_sync(0xffffffffu, c_lo <= 0 && c_hi == kRows) && !odd[sl];
-                const unsigned width = (unsigned)max(0, c_hi - c_lo);
+                const bool full = i >= full_lo && i < full_hi && !odd[sl];
+                int c_lo = 0;
+                unsigned width = kRows;
+                if (!full) {  // columns that see this key: positions t .. t + window
+                    const int pos0 = (x.tile0 + i) * ppt, rows = min(kRows, (x.qs.n - pos0) * g);
+                    c_lo = max(0, t - x.off - pos0) * g;
+                    int c_hi = rows;
+                    if (p.window > 0) c_hi = (int)max(0ll, min((long long)rows, ((long long)t - x.off - pos0 + p.window + 1) * g));
+                    width = (unsigned)max(0, c_hi - c_lo);
+                }
                 const float scale = kVar && p.soft_cap_on ? p.cap_out : p.scale_log2;
                 // 32 columns from c on: v (and v2, the second map's)
                 auto add32 = [&](auto whole, int c, float (&v)[32], float (&v2)[kDiff ? 32 : 1]) {
