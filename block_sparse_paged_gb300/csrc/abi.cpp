@@ -245,7 +245,7 @@ namespace {
 // A differential run: a plan over pairs of maps, its arguments.
 int check_diff(const bsp_plan_info *plan, int mode, const bsp_differential *diff, const void *q, const void *k_pages,
                const void *v_pages, const int8_t *k_exp, const int8_t *v_exp, const int32_t *kv_indices, int64_t num_pages,
-               float sm_scale, const void *o, const void *workspace) {
+               float sm_scale, const void *o, const float *lse, const void *workspace) {
     clear_error();
     int rc = check_plan(plan, mode, workspace);
     if (rc != BSP_OK) return rc;
@@ -259,6 +259,7 @@ int check_diff(const bsp_plan_info *plan, int mode, const bsp_differential *diff
     if (!std::isfinite(diff->out_scale) || !std::isfinite(diff->norm_eps) || diff->norm_eps < 0.f)
         return fail(BSP_ERR_INVALID_ARG, "out_scale and norm_eps must be finite, norm_eps >= 0");
     if (reinterpret_cast<uintptr_t>(diff->norm_weight) % 16 != 0) return fail(BSP_ERR_INVALID_ARG, "norm_weight is not 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(lse) % 8 != 0) return fail(BSP_ERR_INVALID_ARG, "lse is not 8-byte aligned");
     if (!std::isfinite(sm_scale) || (mode == BSP_MODE_PREFILL && sm_scale <= 0.f))
         return fail(BSP_ERR_INVALID_ARG, "sm_scale must be finite, and positive for prefill");
     if ((k_exp == nullptr) != (v_exp == nullptr)) return fail(BSP_ERR_INVALID_ARG, "k_exp and v_exp are given together");
@@ -278,7 +279,7 @@ extern "C" int bsp_decode_run_diff(const bsp_plan_info *plan, const bsp_differen
                                    int64_t num_pages, float sm_scale, void *o, float *lse, void *region, size_t region_bytes,
                                    void *workspace, bsp_stream_t stream) {
     if (no_queries(plan, BSP_MODE_DECODE, q, o)) return BSP_OK;
-    int rc = check_diff(plan, BSP_MODE_DECODE, diff, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, workspace);
+    int rc = check_diff(plan, BSP_MODE_DECODE, diff, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse, workspace);
     if (rc != BSP_OK) return rc;
     if (!k_exp) return launch_decode(plan, q, k_pages, v_pages, kv_indices, num_pages, sm_scale, o, lse, workspace, stream, diff);
     int64_t entries;
@@ -298,7 +299,7 @@ extern "C" int bsp_prefill_run_diff(const bsp_plan_info *plan, const bsp_differe
                                     int64_t num_pages, float sm_scale, void *o, float *lse, void *region, size_t region_bytes,
                                     void *workspace, bsp_stream_t stream) {
     if (no_queries(plan, BSP_MODE_PREFILL, q, o)) return BSP_OK;
-    int rc = check_diff(plan, BSP_MODE_PREFILL, diff, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, workspace);
+    int rc = check_diff(plan, BSP_MODE_PREFILL, diff, q, k_pages, v_pages, k_exp, v_exp, kv_indices, num_pages, sm_scale, o, lse, workspace);
     if (rc != BSP_OK) return rc;
     int64_t pages = 0;
     if (k_exp && (rc = prefill_region(plan, region, region_bytes, pages)) != BSP_OK) return rc;
@@ -462,6 +463,7 @@ extern "C" int bsp_accumulate_weights(const bsp_problem *problem, const void *q,
     if (batch == 0 || max_table_pages == 0) return BSP_OK;
     if (!k_pages || !weights || (n_tokens > 0 && (!q || !lse))) return fail(BSP_ERR_INVALID_ARG, "a tensor pointer is NULL");
     if ((rc = check_aligned16(q, k_pages, nullptr, nullptr, nullptr)) != BSP_OK) return rc;
+    if (lambda && reinterpret_cast<uintptr_t>(lse) % 8 != 0) return fail(BSP_ERR_INVALID_ARG, "lse of two maps is not 8-byte aligned");
     return launch_accumulate_weights(&P, q, lse, n_tokens, k_pages, k_exp, num_pages, weights, batch, qo_indptr, kv_indptr,
                                      kv_indices, max_table_pages, last_page_len, sm_scale, decay, lambda, stream);
 }

@@ -521,7 +521,8 @@ int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const vo
  *   plan         from bsp_plan over twice the heads: problem.num_qo_heads = 2 * H_q (the
  *                maps), head_dim 128, bf16, no sink
  *   q, o         device, bf16 [n_tokens, H_q, 128]
- *   lse          device, float [n_tokens, H_q, 2], LSE_1 and LSE_2; may be NULL
+ *   lse          device, float [n_tokens, H_q, 2], 8-byte aligned, LSE_1 and LSE_2; may be
+ *                NULL
  *   k_exp, v_exp NULL (bf16 pools), or the exponents of an 8-bit cache
  *   region       as for bsp_decode_run_fp8_block (bsp_decode_fp8_region_size). A prefill over
  *                the 8-bit cache needs one of bsp_prefill_diff_region_size bytes (32-byte
@@ -577,7 +578,9 @@ size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan);
  * it: kv_indptr int32 [batch + 1], kv_indices int32 [max_table_pages], last_page_len int32
  * [batch] (tokens of the last page). Values out of range count as the nearest in range, and
  * tokens of pages outside [0, num_pages) are left out: nothing is read or written outside
- * the arrays. batch at most 65535, num_pages * page_size below 2^32 - 1.
+ * the arrays. A page belongs to one request of the batch (the weights of one that two share
+ * would be whichever is written last). batch at most 65535, num_pages * page_size below
+ * 2^32 - 1.
  */
 
 /*
@@ -597,7 +600,7 @@ size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan);
  *                [num_pages, H_kv]) e4m3 codes, D = 128, value = code * 2^exp
  *   qo_indptr    device, int32 [batch + 1], or NULL: one query per request, in order
  *   lambda       NULL, or device float [H_qo]: the weights of a differential run
- *                (bsp_decode_run_diff): lse float [n_tokens, H_qo, 2], and a head gives
+ *                (bsp_decode_run_diff): lse float [n_tokens, H_qo, 2], 8-byte aligned, and a head gives
  *                |p1 - lambda p2| of its two maps' weights
  * Supported: bf16 with D in {64, 128}, fp32 with D in {32, 64, 128, 256} (no lambda).
  */

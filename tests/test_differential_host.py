@@ -45,7 +45,7 @@ def run(native, mode, info=None, lam=4096, norm=None, eps=1e-5, out=1.0, **kw):
 @pytest.mark.parametrize("kw", [
     dict(lam=None), dict(norm=4100), dict(eps=-1.0), dict(eps=float("nan")), dict(out=float("inf")), dict(q=None), dict(k=None),
     dict(v=None), dict(o=None), dict(ws=None), dict(idx=None), dict(pages=0), dict(scale=float("nan")), dict(ke=P16), dict(ve=P16),
-    dict(q=ctypes.c_void_p(4104)), dict(ke=P16, ve=P16, region=ctypes.c_void_p(4104), nbytes=1 << 20)], ids=str)
+    dict(q=ctypes.c_void_p(4104)), dict(lse=ctypes.c_void_p(4100)), dict(ke=P16, ve=P16, region=ctypes.c_void_p(4104), nbytes=1 << 20)], ids=str)
 def test_refuses(native, mode, kw):
     assert run(native, mode, **kw) == native.BSP_ERR_INVALID_ARG
     assert native.load().bsp_last_error()

@@ -74,7 +74,7 @@ def accumulate(native, **kw):
     dict(num_qo_heads=7), dict(page_size=0), dict(dtype=3), dict(batch=-1), dict(batch=70000), dict(pages=0), dict(cap=-1),
     dict(scale=float("nan")), dict(decay=-0.5), dict(decay=float("inf")), dict(n=-1), dict(q=None), dict(lse=None),
     dict(k=None), dict(w=None), dict(kvp=None), dict(kvi=None), dict(last=None), dict(k=ctypes.c_void_p(4104)),
-    dict(q=ctypes.c_void_p(4098)), dict(logits_soft_cap=-1.0), dict(n=1 << 31)], ids=str)
+    dict(q=ctypes.c_void_p(4098)), dict(logits_soft_cap=-1.0), dict(n=1 << 31), dict(lam=P16, lse=ctypes.c_void_p(4100))], ids=str)
 def test_accumulate_refuses(native, kw):
     assert accumulate(native, **kw) == native.BSP_ERR_INVALID_ARG
     assert native.load().bsp_last_error()
