@@ -104,6 +104,7 @@ constexpr long long kWaitLimitCycles = 4000000000ll;  // about 2 s at 2 GHz: a f
 constexpr int kStatusWait = 0x201;
 constexpr int kStatusPageIndex = 0x302;  // e4m3 cache: a page id outside the pool
 constexpr float kRescaleThreshold = 8.f;  // log2 units
+constexpr int kLoKeys = 64;  // kDiff: keys of a tile whose P keeps what its rounding took
 
 struct PrefillParams {
     const uint8_t *ws;
@@ -531,6 +532,12 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 for (int kk = 0; kk < kKvTile / 16; ++kk)
                     mma_bf16_ts(tmem + 256 + sub * 128, tmem + sub * 128 + kk * 8,
                                 smem_desc_sw128(sv + kk * 16 * 128, kHalf, 1024), id_pv, acc || kk > 0);
+                if constexpr (kDiff) {
+#pragma unroll
+                    for (int kk = 0; kk < kLoKeys / 16; ++kk)
+                        mma_bf16_ts(tmem + 256 + sub * 128, tmem + sub * 128 + 64 + kk * 8,
+                                    smem_desc_sw128(sv + kk * 16 * 128, kHalf, 1024), id_pv, 1);
+                }
             };
             // the next item's KV range is read one item ahead (its latency then
             // overlaps this item's MMAs instead of delaying the next item's first S)
@@ -802,12 +809,31 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 }
                 l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
                 // P (bf16 pairs) over the first 64 columns of S
+                if constexpr (kDiff) {
+                    // What the rounding takes from the first 64 keys of a tile, over the next 32 columns, is a second
+                    // operand of their product: in the difference of two outputs of about the same size the noise of
+                    // the rounded P stands out. Error against 64 bits (the output's own rounding is 0.0017) and time
+                    // of 16 ragged prompts: none 0.0026, 704 us; 64 of 128 keys 0.0022, 788 us; all 0.0017, 920 us.
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t pk[32];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) pk[i] = dev::pack_bf16(sv[c * 64 + 2 * i], sv[c * 64 + 2 * i + 1]);
-                    tmem_st32_u(tS + c * 32, pk);
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = sv[c * 32 + 2 * i], y = sv[c * 32 + 2 * i + 1];
+                            hi[i] = dev::pack_bf16(x, y);
+                            lo[i] = dev::pack_bf16(x - dev::bf16_lo(hi[i]), y - dev::bf16_hi(hi[i]));
+                        }
+                        tmem_st16_u(tS + c * 16, hi);
+                        if (c < kLoKeys / 32) tmem_st16_u(tS + 64 + c * 16, lo);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) pk[i] = dev::pack_bf16(sv[c * 64 + 2 * i], sv[c * 64 + 2 * i + 1]);
+                        tmem_st32_u(tS + c * 32, pk);
+                    }
                 }
                 // O rescale when the reference moved (PV(t-1) is complete: S(t) is)
                 if (t > 0 && __any_sync(0xffffffffu, move)) {
