@@ -497,12 +497,12 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
         asm volatile("cp.async.wait_all;\n" ::: "memory");  // nothing in flight at exit
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        // One thread issues everything: between MMA groups the tensor pipe
+        // One elected thread issues everything: between MMA groups the tensor pipe
         // drains, so every cycle spent on warp votes, redundant fences or index
         // arithmetic here is idle tensor time. The only fence needed is after
         // the P barrier (P arrives through tcgen05.st from other threads); K, V
         // and Q arrive through TMA (async proxy) with their mbarriers.
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id_s = idesc_bf16_f32(kRows, kKvTile, false, false);
             constexpr uint32_t id_pv = idesc_bf16_f32(kRows, kD, false, true);
             int q_cnt = 0, p_cnt0 = 0, p_cnt1 = 0, done = 0;
@@ -516,27 +516,26 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 return false;
             };
             auto issue_s = [&](int sub, int stage) {
-                const uint32_t sq = sb + kOffQ + sub * (kDiff ? kHalf : kTile);
-                const uint32_t sk = sb + kOffK + stage * kTile + (kDiff ? sub * kHalf : 0);
+                const uint64_t dq = smem_desc_sw128(sb + kOffQ + sub * (kDiff ? kHalf : kTile), 16, 1024);
+                const uint64_t dk = smem_desc_sw128(sb + kOffK + stage * kTile + (kDiff ? sub * kHalf : 0), 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < (kDiff ? kD / 32 : kD / 16); ++kk) {
-                    const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-                    mma_bf16_ss(tmem + sub * 128, smem_desc_sw128(sq + o, 16, 1024), smem_desc_sw128(sk + o, 16, 1024),
-                                id_s, kk > 0);
+                    const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                    mma_bf16_ss(tmem + sub * 128, dq + o, dk + o, id_s, kk > 0);
                 }
                 mma_commit(bar(kSFull0 + sub));
             };
             auto issue_pv = [&](int sub, int stage, bool acc) {
-                const uint32_t sv = sb + kOffV + stage * kTile;
+                const uint64_t dv = smem_desc_sw128(sb + kOffV + stage * kTile, kHalf, 1024);
 #pragma unroll
                 for (int kk = 0; kk < kKvTile / 16; ++kk)
                     mma_bf16_ts(tmem + 256 + sub * 128, tmem + sub * 128 + kk * 8,
-                                smem_desc_sw128(sv + kk * 16 * 128, kHalf, 1024), id_pv, acc || kk > 0);
+                                dv + ((kk * 16 * 128) >> 4), id_pv, acc || kk > 0);
                 if constexpr (kDiff) {
 #pragma unroll
                     for (int kk = 0; kk < kLoKeys / 16; ++kk)
                         mma_bf16_ts(tmem + 256 + sub * 128, tmem + sub * 128 + 64 + kk * 8,
-                                    smem_desc_sw128(sv + kk * 16 * 128, kHalf, 1024), id_pv, 1);
+                                    dv + ((kk * 16 * 128) >> 4), id_pv, 1);
                 }
             };
             // the next item's KV range is read one item ahead (its latency then

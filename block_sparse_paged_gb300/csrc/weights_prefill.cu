@@ -13,8 +13,8 @@
 //               32 KB), and the tiles' -LSE log2 e (4 slots)
 //   warp 1      TMEM owner; one thread issues S^T of both 128-key halves per Q tile
 //   warps 2-9   keys 0..127, warps 10-17 keys 128..255: two threads per key, 64 columns of a tile
-//               each (one thread per key, 8 warps: 543 us for two prompts of about 7k, 512 so; 499 with
-//               fewer instructions for waits and masks)
+//               each (one thread per key, 8 warps: 543 us for two prompts of about 7k, 512 so; 497 with
+//               fewer instructions for waits and masks, 478 with MMAs issued by an elected thread)
 // Each half has two accumulators, so that the tensor core fills one while the other is summed
 // (differential weights need both for the two maps of a tile).
 // Units go to CTAs in the order of the table; a request's first units have the most queries
@@ -240,24 +240,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
             if (!unit_at(p, u, lane, x) || x.tiles == 0) continue;
-            if (lane == 0) {
+            if (elect_one()) {
                 const int ks = kn % kKStages;
                 ok = wait1(bar(kKFull0 + ks), (kn / kKStages) & 1);
                 for (int i = 0; i < x.tiles && ok; ++i) {
                     const int m = n + i, qst = m % kQStages;
                     if (!(ok = wait1(bar(kQFull0 + qst), (m / kQStages) & 1))) break;
-                    const uint32_t sq = sb + kOffQ + qst * kTile, sk = sb + kOffK + ks * 2 * kTile;
+                    const uint64_t dq = smem_desc_sw128(sb + kOffQ + qst * kTile, 16, 1024);
+                    const uint64_t dk = smem_desc_sw128(sb + kOffK + ks * 2 * kTile, 16, 1024);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         // accumulator m & 1 of the half; differential: both, one per map
                         const int acc = kDiff ? 0 : m & 1, use = kDiff ? m : m >> 1;
                         if (!(ok = wait1(bar(kSEmpty0 + 2 * half + acc), (use & 1) ^ 1))) break;
                         tc_fence_after();
+                        const uint32_t d = tmem + half * 256 + acc * 128;
 #pragma unroll
                         for (int kk = 0; kk < kD / 16; ++kk) {
-                            const uint32_t o = (kk >> 2) * kSlab + (kk & 3) * 32;
-                            mma_bf16_ss(tmem + half * 256 + (kDiff ? kk >> 2 : acc) * 128, smem_desc_sw128(sk + half * kTile + o, 16, 1024),
-                                        smem_desc_sw128(sq + o, 16, 1024), id, kDiff ? (kk & 3) > 0 : kk > 0);
+                            const uint32_t o = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
+                            mma_bf16_ss(kDiff ? d + (kk >> 2) * 128 : d, dk + half * (kTile >> 4) + o, dq + o, id,
+                                        kDiff ? (kk & 3) > 0 : kk > 0);
                         }
                         mma_commit(bar(kSFull0 + 2 * half + acc));
                     }
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (ok) mma_commit(bar(kKEmpty0 + ks));
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+            ok = __all_sync(0xffffffffu, ok);
             n += x.tiles;
             ++kn;
         }
