@@ -238,6 +238,12 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo,
     return d;
 }
 
+// The same without a swizzle: core matrices of 8 rows x 16 bytes, 128 bytes each; lbo: bytes from the
+// first 8 columns to the next 8, sbo: from 8 rows to the next 8.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return smem_desc_sw128(addr, lbo, sbo) & ~((uint64_t)7 << 61);
+}
+
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 D.
 //   bits 4-5 D format (1 = f32), 7-9 A format (1 = bf16), 10-12 B format (1 = bf16),
 //   bit 15 A major (0 = K, 1 = MN), bit 16 B major, 17-22 N >> 3, 24-28 M >> 4.

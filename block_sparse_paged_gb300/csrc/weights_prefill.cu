@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <type_traits>
 
@@ -46,20 +47,28 @@ constexpr int kSlab = 16384;               // [128 rows][64 bf16], 128-byte swiz
 constexpr int kTile = 2 * kSlab;
 // Six tiles: long units have one stage of K (two tiles) and four of Q, so that Q's latency is
 // covered; short ones two of each, so that the next unit's K is.
-constexpr int kMaxKStages = 2, kMaxQStages = 4, kLSlots = 4;
+constexpr int kMaxKStages = 2, kMaxQStages = 4;
+constexpr int kSlots = 8;                                  // tiles whose column values lie in shared memory
+static_assert(kSlots >= kMaxQStages + 2, "a slot is written again when its tile's sums are done");
 constexpr int kOffK = 0;
-constexpr int kOffL = 6 * kTile;                           // per slot: -LSE (both maps), lambda [128] each
-constexpr int kLBytes = 3 * kRows * 4;
-constexpr int kOffBar = kOffL + kLSlots * kLBytes;
+constexpr int kAug = kRows * 16;                           // 8 columns of bf16, no swizzle
+constexpr int kOffAug = 6 * kTile;                         // per Q stage and map: -LSE / scale in three parts
+constexpr int kOffLam = kOffAug + kMaxQStages * 2 * kAug;  // per slot: -lambda of the columns
+constexpr int kOffL = kOffAug;                             // soft-cap, instead: per slot -LSE log2 e (both maps), -lambda
+constexpr int kOffOnes = kOffLam + kSlots * kRows * 4;     // 1, 1, 1, 0 .. in every row
+constexpr int kOffZeros = kOffOnes + kAug;
+static_assert(kOffL + kSlots * 3 * kRows * 4 <= kOffOnes, "both uses fit");
+constexpr int kOffBar = kOffZeros + kAug;
 enum Bar {
     kKFull0 = 0, kKEmpty0 = kKFull0 + kMaxKStages, kQFull0 = kKEmpty0 + kMaxKStages, kQEmpty0 = kQFull0 + kMaxQStages,
-    kLFull0 = kQEmpty0 + kMaxQStages, kLEmpty0 = kLFull0 + kLSlots,
-    kSFull0 = kLEmpty0 + kLSlots,  // [half][accumulator]
+    kSFull0 = kQEmpty0 + kMaxQStages,  // [half][accumulator]
     kSEmpty0 = kSFull0 + 4, kMeet0 = kSEmpty0 + 4,  // [half][lane quarter]
     kNumBars = kMeet0 + 8
 };
-constexpr int kOffMisc = kOffBar + kNumBars * 8;           // TMEM slot, abort flag, odd-LSE flags of the slots
-constexpr int kOffPart = kOffMisc + 8 + 4 * kLSlots;         // [2 units][256 keys]: the second warps' sums
+constexpr int kOffMisc = kOffBar + kNumBars * 8;           // TMEM slot, abort flag
+constexpr int kOddWords = 12;                              // any, (3 free), columns without keys: map 1, map 2
+constexpr int kOffOdd = kOffMisc + 8;
+constexpr int kOffPart = kOffOdd + kSlots * kOddWords * 4;  // [2 units][256 keys]: the second warps' sums
 constexpr int kSmemBytes = kOffPart + 2 * kUnit * 4 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "tiles exceed shared memory");
 constexpr uint32_t kTmemCols = 512;
@@ -104,11 +113,25 @@ __device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, f
         : "=f"(d0), "=f"(d1)
         : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
 }
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b) {
+    asm("{ .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %4};\n mul.rn.f32x2 rd, ra, rb;\n"
+        " mov.b64 {%0, %1}, rd;\n}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b));
+}
 __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1) {
     asm("{ .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rd, ra, rb;\n"
         " mov.b64 {%0, %1}, rd;\n}"
         : "=f"(d0), "=f"(d1)
         : "f"(d0), "f"(d1), "f"(a0), "f"(a1));
+}
+// lse * f as a sum of three bf16 values (of 24 bits together); 0 where no key was seen.
+__device__ __forceinline__ uint4 three_parts(float lse, float f) {
+    const float x = lse == -INFINITY ? 0.f : lse * f;
+    const uint32_t h = dev::pack_bf16(x, 0.f);
+    const float r = fabsf(dev::bf16_lo(h)) < INFINITY ? x - dev::bf16_lo(h) : 0.f;  // exact; (NaN and infinities: in the first part)
+    const uint32_t m = dev::pack_bf16(r, 0.f);
+    return make_uint4((h & 0xffffu) | (m << 16), dev::pack_bf16(r - dev::bf16_lo(m), 0.f), 0u, 0u);
 }
 // kVar: soft-cap compiled in. kDiff: differential weights. kLong: units of many query tiles.
 template <bool kVar, bool kDiff, bool kLong>
@@ -131,13 +154,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) { return sb + kOffBar + 8u * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
-    volatile int *odd = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(bar(i), i >= kLFull0 && i < kLEmpty0 ? 32 : i >= kLEmpty0 && i < kSFull0 ? 16 : i >= kMeet0 ? 64 : i >= kSEmpty0 ? 8 : 1);
+            mbar_init(bar(i), i >= kMeet0 ? 64 : i >= kSEmpty0 ? 8 : i >= kSFull0 || i >= kQEmpty0 ? 2 : i >= kQFull0 ? 33 : 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
+    for (int i = tid; i < 2 * kRows; i += kThreads)  // bf16 1, 1, 1, 0, ..; zeros behind
+        reinterpret_cast<uint4 *>(smem + kOffOnes)[i] = make_uint4(i < kRows ? 0x3f803f80u : 0u, i < kRows ? 0x3f80u : 0u, 0u, 0u);
+    fence_proxy_async_smem();
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tq);
         prefetch_tmap(&tk);
@@ -164,6 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ TMA
         int kn = 0, n = 0;  // units and tiles so far
+        const float neg_inv_scale = -dev::kLog2e / p.scale_log2;
+        (void)neg_inv_scale;
         bool ok = true;
         for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
             if (!unit_at(p, u, lane, x) || x.tiles == 0) continue;
@@ -207,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             columns(0);
             for (int i = 0; i < x.tiles && ok; ++i, ++n) {
-                const int qst = n % kQStages, sl = n % kLSlots, pos0 = (x.tile0 + i) * ppt;
+                const int qst = n % kQStages, sl = n % kSlots, pos0 = (x.tile0 + i) * ppt;
                 if (!(ok = wait(bar(kQEmpty0 + qst), ((n / kQStages) & 1) ^ 1))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar(kQFull0 + qst), kTile);
@@ -215,21 +242,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(d, &tq, bar(kQFull0 + qst), 0, x.h * g, x.qs.q0 + pos0);
                     tma_load_3d(d + kSlab, &tq, bar(kQFull0 + qst), 64, x.h * g, x.qs.q0 + pos0);
                 }
-                if (!(ok = wait(bar(kLEmpty0 + sl), ((n / kLSlots) & 1) ^ 1))) break;
-                float *l = reinterpret_cast<float *>(smem + kOffL + sl * kLBytes);
-                bool strange = false;  // a query that saw no key
+                uint32_t *od = reinterpret_cast<uint32_t *>(smem + kOffOdd) + sl * kOddWords;
+                uint32_t strange = 0;  // queries that saw no key
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    strange |= a[j] == -INFINITY || a2[j] == -INFINITY;
-                    l[lane + 32 * j] = a[j] * -dev::kLog2e;
-                    if (kDiff) {
-                        l[kRows + lane + 32 * j] = a2[j] * -dev::kLog2e;
-                        l[2 * kRows + lane + 32 * j] = -lm[j];
+                    const int c = lane + 32 * j;
+                    const uint32_t o1 = __ballot_sync(0xffffffffu, a[j] == -INFINITY);
+                    const uint32_t o2 = kDiff ? __ballot_sync(0xffffffffu, a2[j] == -INFINITY) : 0;
+                    strange |= o1 | o2;
+                    if (lane == 0) {
+                        od[4 + j] = o1;
+                        od[8 + j] = o2;
+                    }
+                    if constexpr (kVar) {
+                        float *l = reinterpret_cast<float *>(smem + kOffL) + sl * 3 * kRows;
+                        l[c] = a[j] * -dev::kLog2e;
+                        if constexpr (kDiff) {
+                            l[kRows + c] = a2[j] * -dev::kLog2e;
+                            l[2 * kRows + c] = -lm[j];
+                        }
+                    } else {
+                        uint4 *aug = reinterpret_cast<uint4 *>(smem + kOffAug + qst * 2 * kAug);
+                        aug[c] = three_parts(a[j], neg_inv_scale);
+                        if constexpr (kDiff) {
+                            aug[kRows + c] = three_parts(a2[j], neg_inv_scale);
+                            reinterpret_cast<float *>(smem + kOffLam)[sl * kRows + c] = -lm[j];
+                        }
                     }
                 }
-                strange = __any_sync(0xffffffffu, strange);
-                if (lane == 0) odd[sl] = strange;
-                mbar_arrive(bar(kLFull0 + sl));
+                if (lane == 0) od[0] = strange;
+                fence_proxy_async_smem();
+                mbar_arrive(bar(kQFull0 + qst));
                 columns(i + 1);
             }
         }
@@ -248,6 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = wait1(bar(kQFull0 + qst), (m / kQStages) & 1))) break;
                     const uint64_t dq = smem_desc_sw128(sb + kOffQ + qst * kTile, 16, 1024);
                     const uint64_t dk = smem_desc_sw128(sb + kOffK + ks * 2 * kTile, 16, 1024);
+                    // (the second 8 of an operand's 16 columns: the zeros)
+                    const uint32_t aug = kOffAug + qst * 2 * kAug;
+                    [[maybe_unused]] const uint64_t d_ones = smem_desc_plain(sb + kOffOnes, kOffZeros - kOffOnes, 128);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         // accumulator m & 1 of the half; differential: both, one per map
@@ -255,15 +301,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = wait1(bar(kSEmpty0 + 2 * half + acc), (use & 1) ^ 1))) break;
                         tc_fence_after();
                         const uint32_t d = tmem + half * 256 + acc * 128;
+                        mbar_arrive(bar(kSFull0 + 2 * half + acc));  // (hands on what warp 0 wrote for the tile)
 #pragma unroll
                         for (int kk = 0; kk < kD / 16; ++kk) {
                             const uint32_t o = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
                             mma_bf16_ss(kDiff ? d + (kk >> 2) * 128 : d, dk + half * (kTile >> 4) + o, dq + o, id,
                                         kDiff ? (kk & 3) > 0 : kk > 0);
                         }
+                        if constexpr (!kVar) {  // last, so that LSE goes through one addition
+#pragma unroll
+                            for (int map = 0; map < (kDiff ? 2 : 1); ++map) {
+                                const uint32_t o = aug + map * kAug;
+                                mma_bf16_ss(d + map * 128, d_ones, smem_desc_plain(sb + o, kOffZeros - o, 128), id, 1);
+                            }
+                        }
                         mma_commit(bar(kSFull0 + 2 * half + acc));
                     }
-                    if (ok) mma_commit(bar(kQEmpty0 + qst));
+                    if (ok) {
+                        mbar_arrive(bar(kQEmpty0 + qst));
+                        mma_commit(bar(kQEmpty0 + qst));
+                    }
                 }
                 if (ok) mma_commit(bar(kKEmpty0 + ks));
             }
@@ -290,12 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int full_lo = p.window > 0 ? x.tiles : (max(0, x.t0 + kUnit - 1 - x.off) + ppt - 1) / ppt - x.tile0;
             const int full_hi = x.qs.n / ppt - x.tile0;
             for (int i = 0; i < x.tiles; ++i, ++n) {
-                const int acc = kDiff ? 0 : n & 1, use = kDiff ? n : n >> 1, sl = n % kLSlots;
-                if (!(ok = wait(bar(kLFull0 + sl), (n / kLSlots) & 1))) break;
+                const int acc = kDiff ? 0 : n & 1, use = kDiff ? n : n >> 1, sl = n % kSlots;
                 if (!(ok = wait(bar(kSFull0 + 2 * half + acc), use & 1))) break;
                 tc_fence_after();
-                const float4 *lse = reinterpret_cast<const float4 *>(smem + kOffL + sl * kLBytes);
-                const bool full = i >= full_lo && i < full_hi && !odd[sl];
+                [[maybe_unused]] const float4 *lse = reinterpret_cast<const float4 *>(smem + kOffL) + sl * 3 * kRows / 4;
+                [[maybe_unused]] const float4 *lam4 =
+                    kVar ? lse + 2 * kRows / 4 : reinterpret_cast<const float4 *>(smem + kOffLam) + sl * kRows / 4;
+                const uint32_t *od = reinterpret_cast<const uint32_t *>(smem + kOffOdd) + sl * kOddWords;
+                const bool full = i >= full_lo && i < full_hi && od[0] == 0;
                 int c_lo = 0;
                 unsigned width = kRows;
                 if (!full) {  // columns that see this key: positions t .. t + window
@@ -316,44 +375,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (kDiff) v2[j] = dev::tanh_ex2(v2[j] * p.cap_in);
                         }
                     }
-                    float4 lr[8];  // all loads before the first use
-                    [[maybe_unused]] float4 l2r[kDiff ? 8 : 1], lmr[kDiff ? 8 : 1];
+                    [[maybe_unused]] float4 lr[kVar ? 8 : 1], l2r[kVar && kDiff ? 8 : 1], lmr[kDiff ? 8 : 1];  // all loads before the first use
+                    if constexpr (kVar || kDiff) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        lr[j] = lse[c / 4 + j];
-                        if constexpr (kDiff) {
-                            l2r[j] = lse[(kRows + c) / 4 + j];
-                            lmr[j] = lse[(2 * kRows + c) / 4 + j];
+                        for (int j = 0; j < 8; ++j) {
+                            if constexpr (kVar) lr[j] = lse[c / 4 + j];
+                            if constexpr (kVar && kDiff) l2r[j] = lse[(kRows + c) / 4 + j];
+                            if constexpr (kDiff) lmr[j] = lam4[c / 4 + j];
                         }
+                    }
+                    [[maybe_unused]] uint32_t see1 = 0, see2 = 0;  // of these columns: those that see the key in map 1, 2
+                    if constexpr (!kFull) {
+                        const int lo = min(max(c_lo - c, 0), 32), hi = min(max(c_lo + (int)width - c, 0), 32);
+                        const uint32_t in = hi > lo ? (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo) : 0;
+                        see1 = in & ~od[4 + c / 32];
+                        if constexpr (kDiff) see2 = in & ~od[8 + c / 32];
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        const float4 l = lr[j / 4];
-                        fma2(v[j], v[j + 1], v[j], v[j + 1], scale, l.x, l.y);
-                        fma2(v[j + 2], v[j + 3], v[j + 2], v[j + 3], scale, l.z, l.w);
+                        // scale * s - LSE, base 2 (kVar false: LSE went into s)
+                        auto exponents = [&](float *x, const float4 &l) {
+                            if constexpr (kVar) {
+                                fma2(x[0], x[1], x[0], x[1], scale, l.x, l.y);
+                                fma2(x[2], x[3], x[2], x[3], scale, l.z, l.w);
+                            } else {
+                                mul2(x[0], x[1], x[0], x[1], scale);
+                                mul2(x[2], x[3], x[2], x[3], scale);
+                            }
+                        };
+                        exponents(v + j, lr[kVar ? j / 4 : 0]);
                         float e[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) e[k] = ex2(v[j + k]);
-                        const float lc[4] = {l.x, l.y, l.z, l.w};
+                        for (int k = 0; k < 4; ++k) {
+                            e[k] = ex2(v[j + k]);
+                            if constexpr (!kFull) e[k] = see1 >> (j + k) & 1 ? e[k] : 0.f;
+                        }
                         if constexpr (kDiff) {
-                            const float4 l2 = l2r[j / 4], lm = lmr[j / 4];
-                            fma2(v2[j], v2[j + 1], v2[j], v2[j + 1], scale, l2.x, l2.y);
-                            fma2(v2[j + 2], v2[j + 3], v2[j + 2], v2[j + 3], scale, l2.z, l2.w);
-                            const float lc2[4] = {l2.x, l2.y, l2.z, l2.w}, lam[4] = {lm.x, lm.y, lm.z, lm.w};
+                            exponents(v2 + j, l2r[kVar ? j / 4 : 0]);
+                            const float4 lm = lmr[j / 4];
+                            const float lam[4] = {lm.x, lm.y, lm.z, lm.w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 float e2 = ex2(v2[j + k]);
-                                if constexpr (!kFull) {
-                                    e[k] = lc[k] == INFINITY ? 0.f : e[k];
-                                    e2 = lc2[k] == INFINITY ? 0.f : e2;
-                                }
+                                if constexpr (!kFull) e2 = see2 >> (j + k) & 1 ? e2 : 0.f;
                                 e[k] = fabsf(fmaf(lam[k], e2, e[k]));
                             }
-                        }
-                        if constexpr (!kFull) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                e[k] = (unsigned)(c + j + k - c_lo) < width && (kDiff || lc[k] != INFINITY) ? e[k] : 0.f;
                         }
                         add2(s0, s1, e[0], e[1]);
                         add2(s2, s3, e[2], e[3]);
@@ -385,10 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else add_tile(std::false_type{});
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(kSEmpty0 + 2 * half + acc));
-                    mbar_arrive(bar(kLEmpty0 + sl));
-                }
+                if (lane == 0) mbar_arrive(bar(kSEmpty0 + 2 * half + acc));
             }
             // the columns' two halves
             float *part = reinterpret_cast<float *>(smem + kOffPart) + (meet & 1) * kUnit + key;
@@ -436,7 +499,10 @@ int launch_weights_prefill(const bsp_problem *P, const evict::WeightsParams &w, 
     int rc = make_tmap_bf16(&tq, w.q, kD, P->num_qo_heads, (uint64_t)w.n_tokens, w.g, kRows / w.g);
     if (rc == BSP_OK) rc = make_tmap_bf16(&tk, w.k, kD, P->num_kv_heads, (uint64_t)num_pages * P->page_size, 1, p.box_rows);
     if (rc != BSP_OK) return rc;
-    const bool diff = w.lam != nullptr, var = w.soft_cap_on;
+    const bool diff = w.lam != nullptr;
+    // LSE / scale must not overflow nor vanish: other scales take the variant that subtracts LSE from scaled scores
+    const float size = std::fabs(w.scale_log2);
+    const bool var = w.soft_cap_on || !(size > 1e-10f && size < 1e10f);
     // units of many tiles: a CTA each; of few: persistent CTAs, whose next unit's K is on its way
     const int64_t units = (max_table_pages * P->page_size / kUnit + w.csr.batch) * P->num_kv_heads;
     const bool longer = (int64_t)w.n_tokens * w.g / w.csr.batch >= 8 * kRows;
