@@ -4,19 +4,27 @@
 //
 // The score tile is transposed, S^T = K Q^T: 128 keys on the accumulator's lanes, 128 query rows
 // (positions x the g heads of the kv head) on its columns. A thread then owns a key and sums
-// exp(s - LSE) along its lane, so that a key's sum has one order without any exchange per tile, and LSE (a value per column) is read from shared memory four at a time, the same for
-// every lane. No maximum is searched (LSE is given) and nothing is multiplied by P, which leaves
-// per element one fused multiply-add, one exponential and one addition.
+// exp(scale s - LSE) along its lane, so that a key's sum has one order without any exchange per
+// tile. LSE, a value per column, goes into the accumulator: x = -LSE / scale as three bf16 values
+// (24 bits together) in three columns of one more product, of K = 16, whose other operand is 1 there.
+// It is added last, so that the scores round as without it; exp2((s + x) scale log2 e) remains. No
+// maximum is searched (LSE is given) and nothing is multiplied by P: half a multiplication, one
+// exponential and half an addition per element. (A soft-cap stands between s and LSE, and LSE / scale
+// must not overflow: kVar subtracts LSE in registers, from shared memory.)
 //
 // A unit of work is 256 keys of one kv head and all query tiles that see any of them. 18 warps:
-//   warp 0      TMA: the unit's K (page boxes, 2 stages of 64 KB) and the Q tiles (2 stages of
-//               32 KB), and the tiles' -LSE log2 e (4 slots)
+//   warp 0      TMA: the unit's K (page boxes, 64 KB a stage) and the Q tiles (32 KB a stage); the
+//               columns' values and which of them saw no key (8 slots)
 //   warp 1      TMEM owner; one thread issues S^T of both 128-key halves per Q tile
 //   warps 2-9   keys 0..127, warps 10-17 keys 128..255: two threads per key, 64 columns of a tile
-//               each (one thread per key, 8 warps: 543 us for two prompts of about 7k, 512 so; 497 with
-//               fewer instructions for waits and masks, 478 with MMAs issued by an elected thread)
+//               each
 // Each half has two accumulators, so that the tensor core fills one while the other is summed
-// (differential weights need both for the two maps of a tile).
+// (differential weights need both for the two maps of a tile); one is free again before its last
+// columns are summed. Two prompts of about 7k, 32 / 8 heads, us: one thread per key (8 warps) 543, two
+// 512, fewer instructions for waits and masks 497, MMAs by an elected thread 478, LSE in the
+// accumulator 396, early release and first load 370. Bound by the sum warps' instructions and their
+// waits at a tile's begin (exponentials alone 230, products 255); one accumulator of 256 columns per
+// half was 507 (against 478), the next tile awaited inside a tile 397.
 // Units go to CTAs in the order of the table; a request's first units have the most queries
 // under the causal mask. Long units run one per CTA, so that the block scheduler levels them.
 // Every wait is bounded; a wait that gives up makes NaN of the unit's weights.
@@ -49,7 +57,7 @@ constexpr int kTile = 2 * kSlab;
 // covered; short ones two of each, so that the next unit's K is.
 constexpr int kMaxKStages = 2, kMaxQStages = 4;
 constexpr int kSlots = 8;                                  // tiles whose column values lie in shared memory
-static_assert(kSlots >= kMaxQStages + 2, "a slot is written again when its tile's sums are done");
+static_assert(kSlots >= kMaxQStages + 3, "a slot is written again when its tile's sums are done");
 constexpr int kOffK = 0;
 constexpr int kAug = kRows * 16;                           // 8 columns of bf16, no swizzle
 constexpr int kOffAug = 6 * kTile;                         // per Q stage and map: -LSE / scale in three parts
@@ -350,6 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int acc = kDiff ? 0 : n & 1, use = kDiff ? n : n >> 1, sl = n % kSlots;
                 if (!(ok = wait(bar(kSFull0 + 2 * half + acc), use & 1))) break;
                 tc_fence_after();
+                [[maybe_unused]] float va[32];
+                if constexpr (!kDiff) tmem_ld32(tS + acc * 128 + col0, va);
                 [[maybe_unused]] const float4 *lse = reinterpret_cast<const float4 *>(smem + kOffL) + sl * 3 * kRows / 4;
                 [[maybe_unused]] const float4 *lam4 =
                     kVar ? lse + 2 * kRows / 4 : reinterpret_cast<const float4 *>(smem + kOffLam) + sl * kRows / 4;
@@ -375,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (kDiff) v2[j] = dev::tanh_ex2(v2[j] * p.cap_in);
                         }
                     }
-                    [[maybe_unused]] float4 lr[kVar ? 8 : 1], l2r[kVar && kDiff ? 8 : 1], lmr[kDiff ? 8 : 1];  // all loads before the first use
+                    // all loads before the first use
+                    [[maybe_unused]] float4 lr[kVar ? 8 : 1], l2r[kVar && kDiff ? 8 : 1], lmr[kDiff ? 8 : 1];
                     if constexpr (kVar || kDiff) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -426,6 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 const uint32_t tA = tS + acc * 128;
+                // the accumulator is read, before the last 32 columns are summed
+                auto release = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kSEmpty0 + 2 * half + acc));
+                };
                 // (two copies of the loop: with a branch per group of columns 756 us instead of 543)
                 auto add_tile = [&](auto whole) {
                     if constexpr (kDiff) {
@@ -435,23 +452,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_ld32(tS + c, v);
                             tmem_ld32(tS + 128 + c, v2);
                             tmem_wait_ld();
+                            if (c > col0) release();
                             add32(whole, c, v, v2);
                         }
                     } else {
-                        float va[32], vb[32], none[1];
-                        tmem_ld32(tA + col0, va);
+                        float vb[32], none[1];
                         tmem_wait_ld();
                         tmem_ld32(tA + col0 + 32, vb);  // read while the first 32 are summed
                         add32(whole, col0, va, none);
                         tmem_wait_ld();
+                        release();
                         add32(whole, col0 + 32, vb, none);
                     }
                 };
                 if (full) add_tile(std::true_type{});
                 else add_tile(std::false_type{});
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kSEmpty0 + 2 * half + acc));
             }
             // the columns' two halves
             float *part = reinterpret_cast<float *>(smem + kOffPart) + (meet & 1) * kUnit + key;
@@ -480,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 // From 40 query rows per request on (mean). Measured, 32 / 8 heads, us (warp-level kernel / this one): 8 requests x
-// 4096 tokens, 8 queries (32 rows) 30 / 36, 16 queries 48 / 36, 64 queries 163 / 40; 8 x 16384, 8 queries 97 / 106, 16
-// queries 165 / 107; 64 x 4096, 8 queries 188 / 212, 16 queries 326 / 212.
+// 4096 tokens, 6 queries (24 rows) 26 / 34, 8 queries 30 / 34, 16 queries 48 / 34; 8 x 16384, 6 queries 81 / 100, 8
+// queries 96 / 100, 16 queries 166 / 100; 64 x 4096, 6 queries 157 / 201, 8 queries 189 / 201, 16 queries 326 / 202.
 bool weights_prefill_takes(const bsp_problem *P, int64_t num_pages, int64_t n_tokens, int32_t batch, const int32_t *qo_indptr) {
     const int g = P->num_qo_heads / P->num_kv_heads, ps = P->page_size;
     return qo_indptr && P->dtype == BSP_DTYPE_BF16 && P->head_dim == kD && kRows % g == 0 && ps >= 8 && (ps & (ps - 1)) == 0 &&
