@@ -22,9 +22,9 @@
 // (differential weights need both for the two maps of a tile); one is free again before its last
 // columns are summed. Two prompts of about 7k, 32 / 8 heads, us: one thread per key (8 warps) 543, two
 // 512, fewer instructions for waits and masks 497, MMAs by an elected thread 478, LSE in the
-// accumulator 396, early release and first load 370. Bound by the sum warps' instructions and their
-// waits at a tile's begin (exponentials alone 230, products 255); one accumulator of 256 columns per
-// half was 507 (against 478), the next tile awaited inside a tile 397.
+// accumulator 396, early release and first load 370, look-up a unit ahead 357. Bound by the sum
+// warps' instructions and their waits at a tile's begin (exponentials alone 230, products 255); one
+// accumulator of 256 columns per half was 507 (against 478), the next tile awaited inside a tile 397.
 // Units go to CTAs in the order of the table; a request's first units have the most queries
 // under the causal mask. Long units run one per CTA, so that the block scheduler levels them.
 // Every wait is bounded; a wait that gives up makes NaN of the unit's weights.
@@ -200,15 +200,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float neg_inv_scale = -dev::kLog2e / p.scale_log2;
         (void)neg_inv_scale;
         bool ok = true;
-        for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            if (!unit_at(p, u, lane, x) || x.tiles == 0) continue;
-            // K: box l of the unit (box_rows keys of a page) by lane l
+        // the next unit with tiles, from u on; its page under this lane's box: l of the unit, box_rows keys of a page
+        long long u = blockIdx.x;
+        Unit next;
+        int page = -1;
+        auto look_up = [&]() -> bool {
+            for (; u < units; u += gridDim.x) {
+                if (!unit_at(p, u, lane, next) || next.tiles == 0) continue;
+                const int t = next.t0 + lane * pp.box_rows;
+                page = lane * pp.box_rows < kUnit && t < next.rq.len ? __ldg(p.csr.kv_indices + next.rq.p0 + div_ps(p.csr, t)) : -1;
+                u += gridDim.x;
+                return true;
+            }
+            return false;
+        };
+        bool more = look_up();
+        while (more && ok) {
+            x = next;
             const int ks = kn % kKStages;
-            const int t = x.t0 + lane * pp.box_rows;
             uint32_t slot = kNoRow;
-            int page, place;
-            if (lane * pp.box_rows < kUnit && t < x.rq.len) slot = slot_of(p.csr, x.rq, t, page, place);
+            if ((unsigned)page < (unsigned)p.csr.num_pages) {
+                const int t = x.t0 + lane * pp.box_rows;
+                slot = (uint32_t)page * (uint32_t)p.csr.ps + (uint32_t)(t - div_ps(p.csr, t) * p.csr.ps);
+            }
             const int boxes = __popc(__ballot_sync(0xffffffffu, slot != kNoRow));
+            more = look_up();  // (the next unit's page is on its way during this one's tiles)
             if (!(ok = wait(bar(kKEmpty0 + ks), ((kn / kKStages) & 1) ^ 1))) break;
             if (lane == 0) mbar_arrive_expect_tx(bar(kKFull0 + ks), (uint32_t)boxes * pp.box_rows * 256);
             __syncwarp();
