@@ -812,8 +812,8 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                     // What the rounding takes from the first 64 keys of a tile, over the next 32 columns, is a second
                     // operand of their product: in the difference of two outputs of about the same size the noise of
                     // the rounded P stands out. Error against 64 bits (the output's own rounding is 0.0017) and time
-                    // of 16 ragged prompts (before MMAs were issued by an elected thread, now 731): none 0.0026,
-                    // 704 us; 64 of 128 keys 0.0022, 788 us; all 0.0017, 920 us.
+                    // of 16 ragged prompts: none 0.0026, 682 us; 32 of 128 keys 695 us; 64 keys 0.0021, 731 us; 96
+                    // keys 783 us; all 0.0017, 846 us.
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t hi[16], lo[16];
