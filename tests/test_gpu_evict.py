@@ -54,8 +54,9 @@ def bound(b, k, lse, scale, size, cap):
     sizes each, taken times log2 e, and 2^-22 for the exponential; a capped score by 2^-21 cap more (tanh). A weight is off by
     that relatively, and by the additions: 2^-24 per column and 4 more steps."""
     q = np.abs(values(b.q))
+    q = np.where(np.isfinite(q), q, 0.0)  # (such a query has LSE -inf and gives nothing)
     big = np.nanmax(np.where(np.isfinite(k), np.abs(k), 0.0))
-    s = scale * q.sum(axis=2).max() * big if q.size else 0.0  # >= scale * sum |q k|
+    s = abs(scale) * q.sum(axis=2).max() * big if q.size else 0.0  # >= scale * sum |q k|
     fin = np.abs(lse[np.isfinite(lse)])
     cols = int(np.diff(b.qo_indptr).max()) * b.q.shape[1] // k.shape[2] if b.q.size else 0
     rel = s * b.q.shape[2] * 2.0 ** -23 + 3 * (s + (fin.max() if fin.size else 0.0)) * 2.0 ** -23 + 2.0 ** -21
@@ -64,10 +65,10 @@ def bound(b, k, lse, scale, size, cap):
 
 
 def run_weights(bsp, seed, qo, kv, Hq, H, D, ps, dtype="bf16", f8=False, diff=False, window=-1, cap=0.0, decay=1.0, lse=None,
-                qo_none=False, change=None, pad=3):
+                qo_none=False, change=None, pad=3, scale=None):
     b = workloads.paged_batch(seed, qo, kv, Hq, H, D, ps, dtype, causal=True, extra_pages=4)
     rng = np.random.default_rng(seed)
-    scale = 1 / np.sqrt(D // 2 if diff else D)
+    scale = 1 / np.sqrt(D // 2 if diff else D) if scale is None else scale
     ke = None
     if f8:
         codes, e, _, _ = cache8(b, seed)
@@ -156,6 +157,35 @@ def test_weights_of_queries_without_keys(bsp):
     b, got, _ = run_weights(bsp, 17, [10, 4], [100, 40], 8, 4, 128, 16, change=change)
     pg, pl = ev.slots(b.kv_indptr, b.kv_indices, 1, 40, 16)
     assert np.isnan(got[pg, 0, pl][:37]).all() and not np.isnan(got[pg, 1:, pl][:37]).any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "diff"])
+@pytest.mark.parametrize("window,cap", [(-1, 0.0), (200, 0.0), (-1, 5.0), (333, 7.0)])
+def test_weights_of_long_prompts(bsp, kind, window, cap):
+    """From 1024 query rows per request on a unit of keys is a CTA's only one."""
+    run_weights(bsp, 23, [600, 520], [700, 520], 8, 2, 128, 16, diff=kind == "diff", window=window, cap=cap, decay=0.5)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "diff"])
+@pytest.mark.parametrize("qo", [[300, 100], [700, 400]], ids=str)
+def test_weights_of_prompts_with_strange_queries(bsp, qo, kind):
+    """Rows of q that hold NaN or infinities and have LSE -inf, one map's LSE alone, LSE +inf, in full and in partial tiles."""
+    def change(b, lse, w):
+        for i in (0, 7, 140, 299, 300, 399):
+            b.q[i] = float("nan") if i % 2 else float("inf")
+            lse[i] = -np.inf
+        lse[50, 3] = np.inf
+        if kind == "diff":
+            lse[60, 2, 0] = lse[70, 5, 1] = -np.inf
+    run_weights(bsp, 21, qo, [qo[0], 515], 8, 2, 128, 16, diff=kind == "diff", change=change)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "diff"])
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1e-12, 1e-9, 3e-4, 0.5])
+def test_weights_of_prompts_at_any_scale(bsp, scale, kind):
+    """LSE enters the products divided by the scale: 24 bits of it, rounded or cut a few times by 2^-23 of its size, which the
+    bound's share of LSE and of the columns' additions (hundreds times 2^-24) holds. Scales where that overflows subtract later."""
+    run_weights(bsp, 22, [200, 64], [200, 515], 8, 2, 128, 16, diff=kind == "diff", scale=scale, decay=0.5)
 
 
 def test_weights_without_qo_indptr_and_untouched_rows(bsp):
