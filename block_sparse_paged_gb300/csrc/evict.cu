@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_k
     const int H = p.H_kv, g = p.g, ps = p.csr.ps;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + LY::kBarOff + 2 * kStages * 8);
     const uint32_t full0 = smem_u32(smem) + LY::kBarOff, empty0 = full0 + kStages * 8;
-    const long long tasks = block_start<kTaskTokens>(p.csr, p.csr.batch) * H;
+    const long long start0 = block_start<kTaskTokens>(p.csr, 0);
+    const long long tasks = (block_start<kTaskTokens>(p.csr, p.csr.batch) - start0) * H;
     const long long task0 = tasks * blockIdx.x / gridDim.x, task1 = tasks * (blockIdx.x + 1) / gridDim.x;
     const int count = (int)(task1 - task0);
     if (count <= 0) return;
@@ -174,10 +175,10 @@ __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_k
         // do not ascend)
         auto blocks_of = [&](int b) { return (int)max(1ll, block_start<kTaskTokens>(p.csr, b + 1) - block_start<kTaskTokens>(p.csr, b)); };
         const long long first = min(task0 + warp, tasks - 1);
-        int b = find_request<kTaskTokens>(p.csr, first / H, lane);
+        int b = find_request<kTaskTokens>(p.csr, start0 + first / H, lane);
         Request rq = request(p.csr, b);
         int nblk = blocks_of(b);
-        const long long in = max(0ll, first - block_start<kTaskTokens>(p.csr, b) * H);
+        const long long in = max(0ll, first - (block_start<kTaskTokens>(p.csr, b) - start0) * H);
         int h = (int)min(in / nblk, (long long)H - 1), blk = (int)(in % nblk);
         // two tasks on their way: asked for (page ids), then looked up (weights, exponents); each
         // step's reads are in flight for a turn of the loop
@@ -351,15 +352,15 @@ __global__ void __launch_bounds__(256) weights_f32_kernel(const WeightsParams p)
     constexpr int kJ = D / 32;
     const int lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3;
     const int H = p.H_kv, g = p.g;
-    const long long blocks = block_start<kTaskTokens>(p.csr, p.csr.batch);
+    const long long start0 = block_start<kTaskTokens>(p.csr, 0), blocks = block_start<kTaskTokens>(p.csr, p.csr.batch) - start0;
     const long long nwarps = (long long)gridDim.x * (blockDim.x >> 5);
     for (long long task = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); task < blocks * H; task += nwarps) {
-        const long long blk = task / H;
-        const int h = (int)(task - blk * H);
+        const long long blk = start0 + task / H;
+        const int h = (int)(task % H);
         const int b = find_request<kTaskTokens>(p.csr, blk, lane);
         const Request rq = request(p.csr, b);
         const long long first = (blk - block_start<kTaskTokens>(p.csr, b)) * kTaskTokens;
-        if (first >= rq.len) continue;
+        if (first < 0 || first >= rq.len) continue;  // (below 0: a table that does not ascend)
         const Queries qs = queries(p, b);
         const int off = rq.len - qs.n;
         for (int t0 = (int)first; t0 < min(rq.len, (int)first + kTaskTokens); t0 += 8) {

@@ -64,7 +64,8 @@ struct WeightsParams {
 };
 
 // Virtual blocks of kTokens tokens: request b's begin at floor(kv_indptr[b] * ps / kTokens) + b, which
-// leaves room for ceil(len / kTokens) of them without a prefix sum over the requests.
+// leaves room for ceil(len / kTokens) of them without a prefix sum over the requests. The first is
+// block_start(0), which is not 0 where the table is a part of another (kv_indptr[0] > 0).
 template <int kTokens>
 __device__ __forceinline__ long long block_start(const Csr &c, int b) {
     return (long long)clamp_page(c, b) * c.ps / kTokens + b;

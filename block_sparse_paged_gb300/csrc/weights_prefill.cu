@@ -98,12 +98,12 @@ struct Unit {
 
 // A warp: unit u, or false where the table's virtual block is empty.
 __device__ __forceinline__ bool unit_at(const WeightsParams &p, long long u, int lane, Unit &x) {
-    const long long blk = u / p.H_kv;
-    x.h = (int)(u - blk * p.H_kv);
+    const long long blk = block_start<kUnit>(p.csr, 0) + u / p.H_kv;
+    x.h = (int)(u % p.H_kv);
     x.b = find_request<kUnit>(p.csr, blk, lane);
     x.rq = request(p.csr, x.b);
     const long long first = (blk - block_start<kUnit>(p.csr, x.b)) * kUnit;
-    if (first >= x.rq.len) return false;
+    if (first < 0 || first >= x.rq.len) return false;  // (below 0: a table that does not ascend)
     x.t0 = (int)first;
     x.qs = queries(p, x.b);
     x.off = x.rq.len - x.qs.n;
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = dev::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long units = block_start<kUnit>(p.csr, p.csr.batch) * p.H_kv;
+    const long long units = (block_start<kUnit>(p.csr, p.csr.batch) - block_start<kUnit>(p.csr, 0)) * p.H_kv;
     // leave before anything is set up if no unit of this CTA holds a key
     bool any = false;
     Unit x;

@@ -213,6 +213,42 @@ def test_weights_skip_pages_outside_the_pool(bsp):
     assert (np.abs(wt.cpu().numpy() - want) <= bound(b, k, lse, 0.1, size, 0.0)).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32", "prompts", "long"])
+def test_part_of_a_table(bsp, kind):
+    """A slice of the arrays: kv_indptr[0] and qo_indptr[0] are not 0, and what stands before belongs to others."""
+    qo = {"prompts": [100, 150, 70], "long": [100, 900, 400]}.get(kind, [1, 1, 1])
+    b = workloads.paged_batch(24, qo, [1300, 900, 433], 8, 2, 128, 16, "f32" if kind == "f32" else "bf16", causal=True, extra_pages=2)
+    ke = None
+    if kind == "e4m3":
+        codes, e, _, _ = cache8(b, 24)
+        k, kt, ke = kc.values(codes, e), dev(codes).view(F8), dev(e)
+    else:
+        k, kt = values(b.k_pages), b.k_pages.cuda()
+    lse = true_lse(b, k, 0.1, -1, 0.0, 1)
+    w = np.random.default_rng(24).exponential(size=(k.shape[0], 2, 16)).astype(np.float32)
+    indptr, indices, last = table(b)
+    part = indptr[1:].clone(), indices, last[1:].clone()
+    wt = dev(w)
+    bsp.accumulate_weights(b.q.cuda(), dev(lse), kt, wt, *part, qo_indptr=dev(b.qo_indptr[1:].astype(np.int32)), sm_scale=0.1,
+                           decay=0.5, k_exp=ke)
+    torch.cuda.synchronize()
+    host = b.kv_indptr[1:], b.kv_indices, b.last_page_len[1:]
+    want, size = ev.weights(values(b.q), lse.astype(np.float64), k, w, b.qo_indptr[1:], *host, 0.1, decay=0.5)
+    got = wt.cpu().numpy()
+    assert (np.abs(got - want) <= bound(b, k, lse, 0.1, size, 0.0)).all()
+    kept, new = bsp.select_tokens(wt, *part, dev(np.array([300, 100], np.int32)), 300)
+    K, N = ev.select(got, *host, np.array([300, 100]), 300, 4, 32)
+    assert np.array_equal(kept.cpu().numpy(), K) and np.array_equal(new.cpu().numpy(), N)
+    if ke is None:
+        v = b.v_pages.cuda()
+        bsp.compact_cache(kept, new, *part, kt, v, wt)
+        torch.cuda.synchronize()
+        kind_ = torch.int32 if kind == "f32" else torch.int16
+        for a, g in ((b.k_pages, kt), (b.v_pages, v)):
+            moved = ev.compact(a.view(kind_).numpy(), K, N, b.kv_indptr[1:], b.kv_indices, 16)
+            assert np.array_equal(g.view(kind_).cpu().numpy(), moved)
+
+
 def test_weights_of_many_requests(bsp):
     rng = np.random.default_rng(20)
     kv = rng.integers(0, 200, 1500)
