@@ -96,24 +96,75 @@ struct Unit {
     int tile0, tiles;     // query tiles that see a key of the unit
 };
 
-// A warp: unit u, or false where the table's virtual block is empty.
-__device__ __forceinline__ bool unit_at(const WeightsParams &p, long long u, int lane, Unit &x) {
-    const long long blk = block_start<kUnit>(p.csr, 0) + u / p.H_kv;
-    x.h = (int)(u % p.H_kv);
-    x.b = find_request<kUnit>(p.csr, blk, lane);
-    x.rq = request(p.csr, x.b);
-    const long long first = (blk - block_start<kUnit>(p.csr, x.b)) * kUnit;
-    if (first < 0 || first >= x.rq.len) return false;  // (below 0: a table that does not ascend)
-    x.t0 = (int)first;
-    x.qs = queries(p, x.b);
-    x.off = x.rq.len - x.qs.n;
-    const int ppt = kRows / p.g;  // positions per tile
-    const int i_lo = max(0, x.t0 - x.off);
-    const int i_hi = p.window > 0 ? (int)min((long long)x.qs.n, (long long)x.t0 + kUnit + p.window - x.off) : x.qs.n;
-    x.tile0 = i_lo / ppt;
-    x.tiles = i_hi > i_lo ? (i_hi - x.tile0 * ppt + ppt - 1) / ppt : 0;
-    return true;
+// a / b for a >= 0 and b a power of two: by a shift where it is done often (the other form leaves the long
+// tiles' loop its registers)
+template <bool kLong>
+__device__ __forceinline__ int over(int a, int b) {
+    return kLong ? a / b : a >> (31 - __clz(b));
 }
+
+// A CTA's units: u = blockIdx.x, blockIdx.x + gridDim.x, .. in the order (virtual block, head). Where there are
+// many (kLong false) they are walked without a division or, as a rule, a search per unit, which take 2,000 cycles
+// (64 requests x 4096 tokens with 16 queries 196 -> 170 us); where there is one, all that a warp keeps is u (two
+// prompts of about 7k 357 us, with the walk's registers 370).
+template <bool kLong>
+struct Walk {
+    uint32_t u;
+    int h, b;             // kv head, request
+    long long blk, next;  // virtual block; the first one behind its request's (kLong: neither kept)
+
+    __device__ __forceinline__ void find(const WeightsParams &p, int lane) {
+        blk = block_start<kUnit>(p.csr, 0) + (long long)u / p.H_kv;
+        h = (int)((long long)u % p.H_kv);
+        b = find_request<kUnit>(p.csr, blk, lane);
+    }
+    __device__ __forceinline__ void end(const WeightsParams &p) {
+        next = b + 1 < p.csr.batch ? block_start<kUnit>(p.csr, b + 1) : LLONG_MAX;
+    }
+    __device__ __forceinline__ Walk(const WeightsParams &p, int lane) : u(blockIdx.x) {
+        if constexpr (!kLong) {
+            find(p, lane);
+            end(p);
+        }
+    }
+    __device__ __forceinline__ void on(const WeightsParams &p, int lane) {
+        u += gridDim.x;
+        if constexpr (!kLong) {
+            blk += gridDim.x / (uint32_t)p.H_kv;
+            h += (int)(gridDim.x % (uint32_t)p.H_kv);
+            if (h >= p.H_kv) {
+                h -= p.H_kv;
+                ++blk;
+            }
+            if (blk >= next) {
+                ++b;
+                end(p);
+                if (blk >= next) {
+                    b = find_request<kUnit>(p.csr, blk, lane);
+                    end(p);
+                }
+            }
+        }
+    }
+    // the unit here, or false where the table's virtual block is empty
+    __device__ __forceinline__ bool unit(const WeightsParams &p, int lane, Unit &x) {
+        if constexpr (kLong) find(p, lane);
+        x.h = h;
+        x.b = b;
+        x.rq = request(p.csr, b);
+        const long long first = (blk - block_start<kUnit>(p.csr, b)) * kUnit;
+        if (first < 0 || first >= x.rq.len) return false;  // (below 0: a table that does not ascend)
+        x.t0 = (int)first;
+        x.qs = queries(p, b);
+        x.off = x.rq.len - x.qs.n;
+        const int ppt = kRows / p.g;  // positions per tile
+        const int i_lo = max(0, x.t0 - x.off);
+        const int i_hi = p.window > 0 ? (int)min((long long)x.qs.n, (long long)x.t0 + kUnit + p.window - x.off) : x.qs.n;
+        x.tile0 = over<kLong>(i_lo, ppt);
+        x.tiles = i_hi > i_lo ? over<kLong>(i_hi - x.tile0 * ppt + ppt - 1, ppt) : 0;
+        return true;
+    }
+};
 
 __device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b, float c0, float c1) {
     asm("{ .reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %4};\n mov.b64 rc, {%5, %6};\n"
@@ -151,12 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = dev::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long units = (block_start<kUnit>(p.csr, p.csr.batch) - block_start<kUnit>(p.csr, 0)) * p.H_kv;
+    const uint32_t units = (uint32_t)max(0ll, (block_start<kUnit>(p.csr, p.csr.batch) - block_start<kUnit>(p.csr, 0)) * p.H_kv);
     // leave before anything is set up if no unit of this CTA holds a key
     bool any = false;
     Unit x;
-    long long u0 = blockIdx.x;
-    for (; u0 < units && !any; u0 += any ? 0 : gridDim.x) any = unit_at(p, u0, lane, x);
+    for (Walk<kLong> w(p, lane); w.u < units && !any; w.on(p, lane)) any = w.unit(p, lane, x);
     if (!any) return;  // (the same for every warp)
 
     auto bar = [&](int i) { return sb + kOffBar + 8u * i; };
@@ -192,24 +242,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint32_t b, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_try_wait(b, parity)) || __all_sync(0xffffffffu, wait1(b, parity));
     };
-    const int g = p.g, ppt = kRows / g;
+    const int g = p.g, ppt = kRows / g;  // (powers of two)
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA
         int kn = 0, n = 0;  // units and tiles so far
+        const int g_shift = 31 - __clz(g);
         const float neg_inv_scale = -dev::kLog2e / p.scale_log2;
         (void)neg_inv_scale;
         bool ok = true;
         // the next unit with tiles, from u on; its page under this lane's box: l of the unit, box_rows keys of a page
-        long long u = blockIdx.x;
+        Walk<kLong> w(p, lane);
         Unit next;
         int page = -1;
         auto look_up = [&]() -> bool {
-            for (; u < units; u += gridDim.x) {
-                if (!unit_at(p, u, lane, next) || next.tiles == 0) continue;
+            for (; w.u < units; w.on(p, lane)) {
+                if (!w.unit(p, lane, next) || next.tiles == 0) continue;
                 const int t = next.t0 + lane * pp.box_rows;
                 page = lane * pp.box_rows < kUnit && t < next.rq.len ? __ldg(p.csr.kv_indices + next.rq.p0 + div_ps(p.csr, t)) : -1;
-                u += gridDim.x;
+                w.on(p, lane);
                 return true;
             }
             return false;
@@ -241,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int pos0 = (x.tile0 + i) * ppt, rows = min(kRows, (x.qs.n - pos0) * g);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int c = lane + 32 * j, i_c = c / g, r = c - i_c * g;
+                    const int c = lane + 32 * j, i_c = c >> g_shift, r = c & (g - 1);
                     const size_t row = (size_t)(x.qs.q0 + pos0 + i_c) * p.H_qo + (size_t)x.h * g + r;
                     a[j] = a2[j] = lm[j] = 0.f;
                     if (i < x.tiles && c < rows) {
@@ -305,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id = idesc_bf16_f32(kRows, kRows, false, false);
         int kn = 0, n = 0;
         bool ok = true;
-        for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            if (!unit_at(p, u, lane, x) || x.tiles == 0) continue;
+        for (Walk<kLong> w(p, lane); w.u < units && ok; w.on(p, lane)) {
+            if (!w.unit(p, lane, x) || x.tiles == 0) continue;
             if (elect_one()) {
                 const int ks = kn % kKStages;
                 ok = wait1(bar(kKFull0 + ks), (kn / kKStages) & 1);
@@ -359,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + ((uint32_t)(q4 * 32) << 16) + half * 256;
         int n = 0, meet = 0;
         bool ok = true;
-        for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            if (!unit_at(p, u, lane, x)) continue;
+        for (Walk<kLong> w(p, lane); w.u < units && ok; w.on(p, lane)) {
+            if (!w.unit(p, lane, x)) continue;
             const int t = x.t0 + key;
             int page = 0, place = 0;
             const uint32_t slot = t < x.rq.len ? slot_of(p.csr, x.rq, t, page, place) : kNoRow;
@@ -368,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float old = !col0 && slot != kNoRow && t < x.off && p.decay != 0.f ? *at : 0.f;
             float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
             // tiles all of whose queries see all keys of the unit
-            const int full_lo = p.window > 0 ? x.tiles : (max(0, x.t0 + kUnit - 1 - x.off) + ppt - 1) / ppt - x.tile0;
-            const int full_hi = x.qs.n / ppt - x.tile0;
+            const int full_lo = p.window > 0 ? x.tiles : over<kLong>(max(0, x.t0 + kUnit - 1 - x.off) + ppt - 1, ppt) - x.tile0;
+            const int full_hi = over<kLong>(x.qs.n, ppt) - x.tile0;
             for (int i = 0; i < x.tiles; ++i, ++n) {
                 const int acc = kDiff ? 0 : n & 1, use = kDiff ? n : n >> 1, sl = n % kSlots;
                 if (!(ok = wait(bar(kSFull0 + 2 * half + acc), use & 1))) break;
@@ -510,13 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-// From 40 query rows per request on (mean). Measured, 32 / 8 heads, us (warp-level kernel / this one): 8 requests x
-// 4096 tokens, 6 queries (24 rows) 26 / 34, 8 queries 30 / 34, 16 queries 48 / 34; 8 x 16384, 6 queries 81 / 100, 8
-// queries 96 / 100, 16 queries 166 / 100; 64 x 4096, 6 queries 157 / 201, 8 queries 189 / 201, 16 queries 326 / 202.
+// From 32 query rows per request on (mean). Measured, 32 / 8 heads, us (warp-level kernel / this one): 8 requests x
+// 4096 tokens, 6 queries (24 rows) 26 / 32, 8 queries 30 / 32, 16 queries 48 / 32; 8 x 16384, 6 queries 81 / 85, 8
+// queries 96 / 85, 16 queries 166 / 86; 64 x 4096, 6 queries 157 / 169, 8 queries 189 / 170, 16 queries 326 / 170.
 bool weights_prefill_takes(const bsp_problem *P, int64_t num_pages, int64_t n_tokens, int32_t batch, const int32_t *qo_indptr) {
     const int g = P->num_qo_heads / P->num_kv_heads, ps = P->page_size;
     return qo_indptr && P->dtype == BSP_DTYPE_BF16 && P->head_dim == kD && kRows % g == 0 && ps >= 8 && (ps & (ps - 1)) == 0 &&
-           num_pages * (int64_t)ps <= INT32_MAX && n_tokens * g >= (int64_t)batch * 40;
+           num_pages * (int64_t)ps <= INT32_MAX && n_tokens * g >= (int64_t)batch * 32;
 }
 
 int launch_weights_prefill(const bsp_problem *P, const evict::WeightsParams &w, int64_t num_pages, int64_t max_table_pages,
