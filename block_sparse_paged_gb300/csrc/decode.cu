@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                             for (int e = 0; e < 4; ++e) {
                                 const int tk = row0 + qn + 8 * (e >> 1);
                                 float x = (st[nh][0][e] + st[nh][1][e]) * (kf[e >> 1] * hs[nh][e & 1]);
-                                if (p.soft_cap_on) x = tanh_ex2(x) * p.cap_out;
+                                if (p.soft_cap_on) x = (kDiff ? tanh_f32(x) : tanh_ex2(x)) * p.cap_out;
                                 sv[sb][nh][e] = (tk < left && tk >= lo_stage) ? x : -INFINITY;
                                 so[sb][nh][e] = sv[sb][nh][e] + ve[e >> 1];
                             }
@@ -1167,7 +1167,8 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const int tk = n * 8 + 2 * (lane & 3) + (c & 1);
-                            const float x = p.soft_cap_on ? tanh_ex2(sc[n][c] * p.cap_in) * p.cap_out : sc[n][c] * p.scale_log2;
+                            const float y = sc[n][c] * p.cap_in;
+                            const float x = p.soft_cap_on ? (kDiff ? tanh_f32(y) : tanh_ex2(y)) * p.cap_out : sc[n][c] * p.scale_log2;
                             sc[n][c] = (tk < valid && tk >= lo_rel) ? x : -INFINITY;
                         }
                         mx0 = fmaxf(mx0, fmaxf(sc[n][0], sc[n][1]));

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_k
                     for (int e = 0; e < 2; ++e) {
                         const float f = kE4m3 ? x.scale[e] * kf[row] : x.scale[e];
                         float y = d[0][2 * i + e] + d[1][2 * i + e];
-                        if (kVar && p.soft_cap_on) y = fmaf(tanh_ex2(y * f), p.cap_out, -x.lse[e]);
+                        if (kVar && p.soft_cap_on) y = fmaf(tanh_f32(y * f), p.cap_out, -x.lse[e]);
                         else y = fmaf(y, f, -x.lse[e]);
                         const bool see = tok <= x.pos[e] && (!kVar || p.window <= 0 || tok >= x.pos[e] - p.window);
                         pe[e] = see ? ex2(y) : 0.f;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(256) weights_f32_kernel(const WeightsParams p)
                     for (int u = 0; u < 2; ++u) {
 #pragma unroll
                         for (int o = 1; o < 8; o <<= 1) d[u] += __shfl_xor_sync(0xffffffffu, d[u], o);
-                        const float x = p.soft_cap_on ? tanh_ex2(d[u] * p.cap_in) * p.cap_out : d[u] * p.scale_log2;
+                        const float x = p.soft_cap_on ? tanh_f32(d[u] * p.cap_in) * p.cap_out : d[u] * p.scale_log2;
                         const bool see = tok[u] <= off + i && (p.window <= 0 || tok[u] >= off + i - p.window) && lse != -INFINITY;
                         if (see) sum[u] += exp2f(x - lse * kLog2e);
                     }

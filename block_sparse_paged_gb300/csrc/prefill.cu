@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 tmem_wait_ld();
                 if (kVar && p.soft_cap_on) {  // technical review eq 8 (c * tanh(s / c), the factor c folded into scale_log2)
 #pragma unroll
-                    for (int c = 0; c < kKvTile; ++c) sv[c] = dev::tanh_ex2(sv[c] * p.cap_in);
+                    for (int c = 0; c < kKvTile; ++c) sv[c] = kDiff ? dev::tanh_f32(sv[c] * p.cap_in) : dev::tanh_ex2(sv[c] * p.cap_in);
                 }
                 const bool full = valid == kKvTile && tok0 + kKvTile - 1 <= lim && tok0 >= lo;
                 if (!full) {

@@ -448,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kVar && p.soft_cap_on) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            v[j] = dev::tanh_ex2(v[j] * p.cap_in);
-                            if constexpr (kDiff) v2[j] = dev::tanh_ex2(v2[j] * p.cap_in);
+                            v[j] = dev::tanh_f32(v[j] * p.cap_in);
+                            if constexpr (kDiff) v2[j] = dev::tanh_f32(v2[j] * p.cap_in);
                         }
                     }
                     // all loads before the first use
