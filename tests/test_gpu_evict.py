@@ -213,6 +213,20 @@ def test_weights_skip_pages_outside_the_pool(bsp):
     assert (np.abs(wt.cpu().numpy() - want) <= bound(b, k, lse, 0.1, size, 0.0)).all()
 
 
+@pytest.mark.parametrize("qo", [[60, 50], [700, 650]], ids=str)
+def test_weights_of_prompts_skip_pages_outside_the_pool(bsp, qo):
+    b = workloads.paged_batch(25, qo, [700, 650], 8, 2, 128, 16, "bf16", causal=True, extra_pages=2)
+    k, q = values(b.k_pages), values(b.q)
+    lse = true_lse(b, k, 0.1, -1, 0.0, 1)
+    w = np.ones((k.shape[0], 2, 16), np.float32)
+    b.kv_indices[3], b.kv_indices[20:24], b.kv_indices[-1] = 1 << 30, -7, k.shape[0]
+    wt = dev(w)
+    bsp.accumulate_weights(b.q.cuda(), dev(lse), b.k_pages.cuda(), wt, *table(b), qo_indptr=dev(b.qo_indptr.astype(np.int32)), sm_scale=0.1)
+    torch.cuda.synchronize()
+    want, size = ev.weights(q, lse.astype(np.float64), k, w, b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, 0.1)
+    assert (np.abs(wt.cpu().numpy() - want) <= bound(b, k, lse, 0.1, size, 0.0)).all()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32", "prompts", "long"])
 def test_part_of_a_table(bsp, kind):
     """A slice of the arrays: kv_indptr[0] and qo_indptr[0] are not 0, and what stands before belongs to others."""
