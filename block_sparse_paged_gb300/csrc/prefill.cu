@@ -104,7 +104,6 @@ constexpr long long kWaitLimitCycles = 4000000000ll;  // about 2 s at 2 GHz: a f
 constexpr int kStatusWait = 0x201;
 constexpr int kStatusPageIndex = 0x302;  // e4m3 cache: a page id outside the pool
 constexpr float kRescaleThreshold = 8.f;  // log2 units
-constexpr int kLoKeys = 64;  // kDiff: keys of a tile whose P keeps what its rounding took
 
 struct PrefillParams {
     const uint8_t *ws;
@@ -533,7 +532,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                                 dv + ((kk * 16 * 128) >> 4), id_pv, acc || kk > 0);
                 if constexpr (kDiff) {
 #pragma unroll
-                    for (int kk = 0; kk < kLoKeys / 16; ++kk)
+                    for (int kk = 0; kk < kKvTile / 16; ++kk)
                         mma_bf16_ts(tmem + 256 + sub * 128, tmem + sub * 128 + 64 + kk * 8,
                                     dv + ((kk * 16 * 128) >> 4), id_pv, 1);
                 }
@@ -809,11 +808,13 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
                 // P (bf16 pairs) over the first 64 columns of S
                 if constexpr (kDiff) {
-                    // What the rounding takes from the first 64 keys of a tile, over the next 32 columns, is a second
-                    // operand of their product: in the difference of two outputs of about the same size the noise of
-                    // the rounded P stands out. Error against 64 bits (the output's own rounding is 0.0017) and time
-                    // of 16 ragged prompts: none 0.0026, 682 us; 32 of 128 keys 695 us; 64 keys 0.0021, 731 us; 96
-                    // keys 783 us; all 0.0017, 846 us.
+                    // What the rounding takes, over the other 64 columns, is a second operand of the product: in the
+                    // difference of two outputs of about the same size the noise of the rounded P stands out. It is
+                    // kept for every key, so that a token's outputs do not depend on where in a tile its keys lie and
+                    // a prefill gives what decodes give. Error against 64 bits (the output's own rounding is 0.0017)
+                    // and time of 16 ragged prompts: none 0.0026, 682 us; 64 of 128 keys 0.0021, 740 us; all 0.0017,
+                    // 861 us (what is left of the period are MMAs: the rest handed over behind P, while P's own
+                    // product runs, 985 us).
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t hi[16], lo[16];
@@ -824,7 +825,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                             lo[i] = dev::pack_bf16(x - dev::bf16_lo(hi[i]), y - dev::bf16_hi(hi[i]));
                         }
                         tmem_st16_u(tS + c * 16, hi);
-                        if (c < kLoKeys / 32) tmem_st16_u(tS + 64 + c * 16, lo);
+                        tmem_st16_u(tS + 64 + c * 16, lo);
                     }
                 } else {
 #pragma unroll
