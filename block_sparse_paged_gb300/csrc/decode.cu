@@ -1246,6 +1246,10 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
             l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+            if constexpr (kDiff) {  // scores that are all NaN: not an empty state
+                if (l0 != l0 && m0 == -INFINITY) m0 = 0.f;
+                if (l1 != l1 && m1 == -INFINITY) m1 = 0.f;
+            }
             if ((lane & 3) == 0) {
                 stats[(warp * kSR + r0) * 2 + 0] = m0;
                 stats[(warp * kSR + r0) * 2 + 1] = l0;
@@ -1288,7 +1292,7 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
 #pragma unroll
             for (int ww = 0; ww < kConsumers; ++ww) fac[ww * kSR + ct] = f[ww] * inv;
             // (a partial state of NaN: +inf wins the fold's maximum and makes NaN of the row)
-            rlse[ct] = kBlk && w.slot >= 0 && lse_v != lse_v ? INFINITY : lse_v;
+            rlse[ct] = (kBlk || kDiff) && w.slot >= 0 && lse_v != lse_v ? INFINITY : lse_v;
         }
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(merge_mid);

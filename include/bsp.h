@@ -516,8 +516,9 @@ int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const vo
  *     o     = y * out_scale, or with norm_weight y / sqrt(mean(y^2) + norm_eps) * norm_weight
  *             * out_scale (mean over the head's 128 values; rounded once, at the end)
  * Masks, window and soft-cap are the plan's and hold for both maps; a query without a
- * visible key gets 0. The cache is laid out as for any other run, so page tables, appends
- * and bsp_compact_cache are the same.
+ * visible key gets 0; NaN scores make NaN of their map's LSE and of the head's output. The
+ * cache is laid out as for any other run, so page tables, appends and bsp_compact_cache are
+ * the same.
  *   plan         from bsp_plan over twice the heads: problem.num_qo_heads = 2 * H_q (the
  *                maps), head_dim 128, bf16, no sink
  *   q, o         device, bf16 [n_tokens, H_q, 128]
