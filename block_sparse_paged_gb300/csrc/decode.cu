@@ -269,7 +269,8 @@ __device__ __forceinline__ void write_diff_row(const Prm &p, float4 y, size_t or
         float ss = y.x * y.x + y.y * y.y + y.z * y.z + y.w * y.w;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        f *= rsqrtf(ss * (1.f / 128.f) + p.norm_eps);
+        const float ms = ss * (1.f / 128.f) + p.norm_eps;
+        f *= ms == 0.f ? 0.f : rsqrtf(ms);  // (a row of zeros stays one, with eps 0 too)
         const float4 w = __ldg(reinterpret_cast<const float4 *>(p.norm) + lane);
         y.x *= w.x; y.y *= w.y; y.z *= w.z; y.w *= w.w;
     }

@@ -920,7 +920,8 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                         mbar_arrive(bar(kMeet0 + q4));
                         if (!(ok = wait_bar_warp(ctx, bar(kMeet0 + q4), meet & 1))) break;
                         ++meet;
-                        f *= rsqrtf((x[256 + r] + x[256 + kRows + r]) * (1.f / kD) + p.norm_eps);
+                        const float ms = (x[256 + r] + x[256 + kRows + r]) * (1.f / kD) + p.norm_eps;
+                        f *= ms == 0.f ? 0.f : rsqrtf(ms);  // (a row of zeros stays one, with eps 0 too)
                         const float4 *nw = reinterpret_cast<const float4 *>(p.norm) + sub * 16;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {

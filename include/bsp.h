@@ -514,7 +514,8 @@ int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const vo
  *     s_mij = sm_scale * <q[i, h] half m, k_j half m>,  P_m = softmax over j,  LSE_m
  *     y     = (P_1 - lambda[h] P_2) v
  *     o     = y * out_scale, or with norm_weight y / sqrt(mean(y^2) + norm_eps) * norm_weight
- *             * out_scale (mean over the head's 128 values; rounded once, at the end)
+ *             * out_scale (mean over the head's 128 values; rounded once, at the end; 0 where
+ *             y is all 0, for norm_eps = 0 too)
  * Masks, window and soft-cap are the plan's and hold for both maps; a query without a
  * visible key gets 0; NaN scores make NaN of their map's LSE and of the head's output. The
  * cache is laid out as for any other run, so page tables, appends and bsp_compact_cache are

@@ -1,4 +1,5 @@
-"""Differential attention at the edges: queries of NaN."""
+"""Differential attention at the edges: norms of rows that are zero, queries of NaN."""
+import numpy as np
 import pytest
 import torch
 
@@ -13,6 +14,36 @@ POOLS = pytest.mark.parametrize("f8", [False, True], ids=["bf16", "e4m3"])
 @pytest.fixture(scope="module")
 def bsp():
     return lib()
+
+
+def sizes(mode):
+    """Requests without keys, with one, and with fewer keys than queries; outputs on one CTA and split."""
+    return ([1, 1, 1], [0, 1, 700]) if mode == "decode" else ([3, 70, 200], [0, 5, 700])
+
+
+@MODES
+@POOLS
+@pytest.mark.parametrize("num_ctas", [1, 40])
+def test_norm_of_rows_without_keys(bsp, mode, f8, num_ctas):
+    """A query without a visible key gets 0, its norm's eps being 0 too."""
+    qo, kv = sizes(mode)
+    r = Run(bsp, 71, qo, kv, 16, 4, 16, mode=mode, f8=f8, norm=True, num_ctas=num_ctas)
+    out, lse = r(norm_eps=0.0)
+    torch.cuda.synchronize()
+    got, none = out.float().cpu().numpy(), np.isneginf(lse.cpu().numpy()).all(axis=2)
+    rows = sum(max(0, q - k) for q, k in zip(qo, kv))
+    assert none.sum() == 16 * rows and (got[none] == 0).all() and np.isfinite(got).all()
+    r.check(*r())
+
+
+@MODES
+@POOLS
+def test_norm_of_maps_that_cancel(bsp, mode, f8):
+    """Equal maps and lambda 1: 0 over sqrt(0 + 0) is 0."""
+    r = Run(bsp, 72, [1, 1] if mode == "decode" else [50, 9], [300, 40], 16, 4, 16, mode=mode, f8=f8, lam=1.0, norm=True)
+    r.q[..., 64:] = r.q[..., :64]
+    r.k.view(torch.uint8 if f8 else torch.bfloat16)[..., 64:] = r.k.view(torch.uint8 if f8 else torch.bfloat16)[..., :64]
+    assert (r(norm_eps=0.0, return_lse=False) == 0).all()
 
 
 @MODES
