@@ -881,12 +881,15 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 const int head = w.kv_head * g + r % g;
                 float *x = reinterpret_cast<float *>(smem + kOffQ + kTile) + (o_cnt & 1) * 512;  // [factor, sum][sub][row]
                 const float lam = -__ldg(p.lam + head);
-                x[sub * kRows + r] = has ? 1.f / l : 0.f;
                 float y[64];
 #pragma unroll
                 for (int i = 0; i < 64; ++i) y[i] = 0.f;
                 float z[64];
                 if (nt > 0) {
+                    // (An item without keys must not write here: the other group may still read this buffer of two items
+                    // ago, where a split item, at which the groups do not meet, came between. One with keys has waited
+                    // for a product that needed the other group's P.)
+                    x[sub * kRows + r] = has ? 1.f / l : 0.f;
                     if (!(ok = wait_bar_warp(ctx, bar(kODone0), o_cnt & 1))) break;
                     if (!(ok = wait_bar_warp(ctx, bar(kODone1), o_cnt & 1))) break;
                     tc_fence_after();

@@ -1,4 +1,4 @@
-"""Differential attention at the edges: norms of rows that are zero, queries of NaN."""
+"""Differential attention at the edges: norms of rows that are zero, queries of NaN, the order of a queue's items."""
 import numpy as np
 import pytest
 import torch
@@ -75,3 +75,23 @@ def test_one_map_of_nan(bsp, mode, num_ctas):
     assert torch.isnan(out[1, 3]).all() and torch.isnan(lse[1, 3, 1]) and torch.equal(lse[1, 3, 0], wl[1, 3, 0])
     out[1, 3], lse[1, 3] = want[1, 3], wl[1, 3]
     assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("norm", [False, True], ids=["plain", "norm"])
+def test_items_without_keys_behind_split_ones(bsp, norm):
+    """Queues with a final output, then a partial state of one tile, then an output without keys, which writes none of what the
+    warps trade for the first: the same bits every time."""
+    r = Run(bsp, 77, [32] * 8 + [2] * 2 + [20] * 8, [60] * 8 + [500] * 2 + [0] * 8, 4, 1, 16, mode="prefill", num_ctas=8, chunks_per_cta=2,
+            norm=norm)
+    queue, items, _ = r.pa.plan_arrays()
+
+    def kind(w):
+        keys = w["kv_end"] - w["kv_start"]
+        return "none" if keys == 0 else "final" if w["slot"] < 0 else "tile" if keys <= 128 else "tiles"
+    of = [[kind(w) for w in items[a:b]] for a, b in zip(queue, queue[1:])]
+    assert any(q[i:i + 3] == ["final", "tile", "none"] for q in of for i in range(len(q)))
+    out, lse = (x.clone() for x in r())
+    r.check(out, lse)
+    for _ in range(50):
+        o, l = r()
+        assert torch.equal(o, out) and torch.equal(l, lse)
