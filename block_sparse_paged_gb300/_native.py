@@ -40,6 +40,7 @@ EXPORTED = ["bsp_default_num_ctas", "bsp_workspace_size", "bsp_host_staging_size
             "bsp_prefill_run_fp8_block", "bsp_decode_fp8_region_size", "bsp_prefill_fp8_region_size",
             "bsp_decode_run_diff", "bsp_prefill_run_diff", "bsp_prefill_diff_region_size",
             "bsp_accumulate_weights", "bsp_select_tokens", "bsp_compact_cache", "bsp_decode_run_static", "bsp_check_device_error", "bsp_check_bounded_wait",
+             "bsp_check_weights_wait",
             "bsp_last_error", "bsp_version"]
 
 
@@ -132,6 +133,8 @@ def load():
         "bsp_prefill_run_diff": ([PI, DP, vp, vp, vp, vp, vp, vp, i64, f32, vp, vp, vp, ctypes.c_size_t, vp, vp], ctypes.c_int),
         "bsp_prefill_diff_region_size": ([PI], ctypes.c_size_t),
         "bsp_accumulate_weights": ([P, vp, vp, i64, vp, vp, i64, vp, i32, vp, vp, vp, i64, vp, f32, f32, vp, vp],
+                                   ctypes.c_int),
+        "bsp_check_weights_wait": ([P, vp, vp, i64, vp, vp, i64, vp, i32, vp, vp, vp, i64, vp, f32, f32, i64, vp],
                                    ctypes.c_int),
         "bsp_select_tokens": ([vp, i64, i32, i32, i32, vp, vp, i64, vp, vp, i32, i32, i32, vp, vp, vp], ctypes.c_int),
         "bsp_compact_cache": ([vp, vp, i32, i32, vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp],

@@ -436,14 +436,12 @@ int check_table(int32_t batch, const int32_t *kv_indptr, const int32_t *kv_indic
     return BSP_OK;
 }
 
-}  // namespace
-
-extern "C" int bsp_accumulate_weights(const bsp_problem *problem, const void *q, const float *lse, int64_t n_tokens,
-                                      const void *k_pages, const int8_t *k_exp, int64_t num_pages, float *weights,
-                                      int32_t batch, const int32_t *qo_indptr, const int32_t *kv_indptr,
-                                      const int32_t *kv_indices, int64_t max_table_pages, const int32_t *last_page_len,
-                                      float sm_scale, float decay, const float *lambda, bsp_stream_t stream) {
-    clear_error();
+// bsp_accumulate_weights, or with a stall_limit bsp_check_weights_wait.
+int accumulate(const bsp_problem *problem, const void *q, const float *lse, int64_t n_tokens,
+               const void *k_pages, const int8_t *k_exp, int64_t num_pages, float *weights,
+               int32_t batch, const int32_t *qo_indptr, const int32_t *kv_indptr,
+               const int32_t *kv_indices, int64_t max_table_pages, const int32_t *last_page_len,
+               float sm_scale, float decay, const float *lambda, int64_t stall_limit, bsp_stream_t stream) {
     if (!problem) return fail(BSP_ERR_INVALID_ARG, "problem is NULL");
     bsp_problem P = *problem;
     P.mode = BSP_MODE_DECODE;  // (the mode's own limits say nothing here)
@@ -465,7 +463,33 @@ extern "C" int bsp_accumulate_weights(const bsp_problem *problem, const void *q,
     if ((rc = check_aligned16(q, k_pages, nullptr, nullptr, nullptr)) != BSP_OK) return rc;
     if (lambda && reinterpret_cast<uintptr_t>(lse) % 8 != 0) return fail(BSP_ERR_INVALID_ARG, "lse of two maps is not 8-byte aligned");
     return launch_accumulate_weights(&P, q, lse, n_tokens, k_pages, k_exp, num_pages, weights, batch, qo_indptr, kv_indptr,
-                                     kv_indices, max_table_pages, last_page_len, sm_scale, decay, lambda, stream);
+                                     kv_indices, max_table_pages, last_page_len, sm_scale, decay, lambda, stall_limit, stream);
+}
+
+}  // namespace
+
+extern "C" int bsp_accumulate_weights(const bsp_problem *problem, const void *q, const float *lse, int64_t n_tokens,
+                                      const void *k_pages, const int8_t *k_exp, int64_t num_pages, float *weights,
+                                      int32_t batch, const int32_t *qo_indptr, const int32_t *kv_indptr,
+                                      const int32_t *kv_indices, int64_t max_table_pages, const int32_t *last_page_len,
+                                      float sm_scale, float decay, const float *lambda, bsp_stream_t stream) {
+    clear_error();
+    return accumulate(problem, q, lse, n_tokens, k_pages, k_exp, num_pages, weights, batch, qo_indptr, kv_indptr, kv_indices,
+                      max_table_pages, last_page_len, sm_scale, decay, lambda, 0, stream);
+}
+
+extern "C" int bsp_check_weights_wait(const bsp_problem *problem, const void *q, const float *lse, int64_t n_tokens,
+                                      const void *k_pages, const int8_t *k_exp, int64_t num_pages, float *weights,
+                                      int32_t batch, const int32_t *qo_indptr, const int32_t *kv_indptr,
+                                      const int32_t *kv_indices, int64_t max_table_pages, const int32_t *last_page_len,
+                                      float sm_scale, float decay, int64_t limit_cycles, bsp_stream_t stream) {
+    clear_error();
+    if (limit_cycles < 1 || limit_cycles > (int64_t{1} << 33))
+        return fail(BSP_ERR_INVALID_ARG, "limit_cycles must be in [1, 2^33] (about 4 s)");
+    if (problem && (problem->dtype != BSP_DTYPE_BF16 || problem->head_dim != 128 || problem->window_left > 0 || problem->logits_soft_cap != 0.f))
+        return fail(BSP_ERR_UNSUPPORTED, "the self-test takes bf16 problems with head_dim 128, no window and no soft-cap");
+    return accumulate(problem, q, lse, n_tokens, k_pages, k_exp, num_pages, weights, batch, qo_indptr, kv_indptr, kv_indices,
+                      max_table_pages, last_page_len, sm_scale, decay, nullptr, limit_cycles, stream);
 }
 
 extern "C" int bsp_select_tokens(const float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads,

@@ -126,7 +126,7 @@ int launch_accumulate_weights(const bsp_problem *problem, const void *q, const f
                               const void *k_pages, const int8_t *k_exp, int64_t num_pages, float *weights, int32_t batch,
                               const int32_t *qo_indptr, const int32_t *kv_indptr, const int32_t *kv_indices,
                               int64_t max_table_pages, const int32_t *last_page_len, float sm_scale, float decay,
-                              const float *lambda, cudaStream_t stream);
+                              const float *lambda, int64_t stall_limit, cudaStream_t stream);  // (stall_limit: bsp_check_weights_wait's, or 0)
 int launch_select_tokens(const float *weights, int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t batch,
                          const int32_t *kv_indptr, const int32_t *kv_indices, int64_t max_table_pages,
                          const int32_t *last_page_len, const int32_t *budget, int32_t max_keep, int32_t sinks,

@@ -51,7 +51,6 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float(e >= -126 
 // bulk copy per row: an SM starts one in about 25 cycles, whatever its size), now 98 (5.85 TB/s);
 // 32 x 4096 tokens of an 8-bit cache 34 (4.2 TB/s).
 constexpr int kTaskTokens = 32;
-constexpr long long kWaitLimitCycles = 4000000000ll;  // about 2 s at 2 GHz: a fault, not a stall
 
 template <int D, bool kE4m3>
 struct StreamLayout {
@@ -142,8 +141,25 @@ __device__ __forceinline__ void load_columns(const WeightsParams &p, const Queri
     x.lam = kDiff ? __shfl_sync(0xffffffffu, lam, 8 * c) : 0.f;
 }
 
+// Where task x of a run's order (request, head, keys) lies; in range for tables that do not ascend. All lanes of a warp.
+struct Task {
+    int b, h, blk, nblk;  // request, head, block of keys, blocks of the request
+};
+__device__ __forceinline__ int blocks_of(const Csr &c, int b) {
+    return (int)max(1ll, block_start<kTaskTokens>(c, b + 1) - block_start<kTaskTokens>(c, b));
+}
+__device__ __forceinline__ Task find_task(const WeightsParams &p, long long start0, long long x, int lane) {
+    Task t;
+    t.b = find_request<kTaskTokens>(p.csr, start0 + x / p.H_kv, lane);
+    t.nblk = blocks_of(p.csr, t.b);
+    const long long in = max(0ll, x - (block_start<kTaskTokens>(p.csr, t.b) - start0) * p.H_kv);
+    t.h = (int)min(in / t.nblk, (long long)p.H_kv - 1);
+    t.blk = (int)(in % t.nblk);
+    return t;
+}
+
 // kVar: window and soft-cap compiled in.
-template <int D, bool kE4m3, bool kDiff, bool kVar>
+template <int D, bool kE4m3, bool kDiff, bool kVar, bool kStall>
 __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_kernel(const WeightsParams p) {
     using LY = StreamLayout<D, kE4m3>;
     constexpr int kJ = LY::kRow / 64;           // 16-byte chunks of a row per lane
@@ -166,21 +182,16 @@ __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_k
     }
     __syncthreads();
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        const bool ok = __all_sync(0xffffffffu, sm100::mbar_wait_spin(bar, parity, kWaitLimitCycles, abort_flag));
+        const bool ok = __all_sync(0xffffffffu, sm100::mbar_wait_spin(bar, parity, kStall ? p.wait_limit : kWaitLimitCycles, abort_flag));
         if (!ok) *abort_flag = 1;
         return ok;
     };
 
     if (warp < LY::kLoaders) {
-        // this warp's place in the run: request, head, block of keys (kept in range for tables that
-        // do not ascend)
-        auto blocks_of = [&](int b) { return (int)max(1ll, block_start<kTaskTokens>(p.csr, b + 1) - block_start<kTaskTokens>(p.csr, b)); };
-        const long long first = min(task0 + warp, tasks - 1);
-        int b = find_request<kTaskTokens>(p.csr, start0 + first / H, lane);
+        // this warp's place in the run: request, head, block of keys
+        const Task first = find_task(p, start0, min(task0 + warp, tasks - 1), lane);
+        int b = first.b, h = first.h, blk = first.blk, nblk = first.nblk;
         Request rq = request(p.csr, b);
-        int nblk = blocks_of(b);
-        const long long in = max(0ll, first - (block_start<kTaskTokens>(p.csr, b) - start0) * H);
-        int h = (int)min(in / nblk, (long long)H - 1), blk = (int)(in % nblk);
         // two tasks on their way: asked for (page ids), then looked up (weights, exponents); each
         // step's reads are in flight for a turn of the loop
         struct { int b, h, t0, len, id, place; } ask = {0, 0, -1, 0, 0, 0};
@@ -188,6 +199,7 @@ __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_k
         for (int k = warp - 2 * LY::kLoaders; k < count; k += LY::kLoaders) {
             if (k >= 0) {
                 const int s = k % kStages;
+                if (kStall && warp == 0 && k >= LY::kLoaders) return;
                 if (!wait(empty0 + 8 * s, ((k / kStages) & 1) ^ 1)) return;
                 uint8_t *stage = smem + LY::kRingOff + s * LY::kStageBytes;
                 reinterpret_cast<long long *>(stage)[lane] = got.at;
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_k
                     h = 0;
                     if (++b < p.csr.batch) {
                         rq = request(p.csr, b);
-                        nblk = blocks_of(b);
+                        nblk = blocks_of(p.csr, b);
                     }
                 }
             }
@@ -256,9 +268,9 @@ __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_k
         cp_async_commit();
         return true;
     };
-    const int k0 = warp - LY::kLoaders;
-    bool ok = copy(k0, 0);
-    for (int k = k0, u = 0; k < count && ok; k += LY::kCompute, u ^= 1) {
+    int k = warp - LY::kLoaders;
+    bool ok = copy(k, 0);
+    for (int u = 0; k < count && ok; k += LY::kCompute, u ^= 1) {
         if (!(ok = copy(k + LY::kCompute, u ^ 1))) break;
         cp_async_wait<1>();
         __syncwarp();
@@ -344,6 +356,13 @@ __global__ void __launch_bounds__(StreamLayout<D, kE4m3>::kThreads, 1) weights_k
         if (at >= 0) p.weights[at] = t0 + n + 8 * c < off && p.decay != 0.f ? fmaf(p.decay, old, own) : own;
     }
     cp_async_wait<0>();  // nothing in flight at exit
+    for (; !ok && k < count; k += LY::kCompute) {  // a wait gave up
+        const Task task = find_task(p, start0, task0 + k, lane);
+        const Request rq = request(p.csr, task.b);
+        const long long t = (long long)task.blk * kTaskTokens + lane;
+        int page, place;
+        if (t < rq.len && slot_of(p.csr, rq, (int)t, page, place) != kNoRow) p.weights[((size_t)page * H + task.h) * ps + place] = NAN;
+    }
 }
 
 // fp32 pools: a warp takes a task's 32 keys, eight at a time (8 lanes per row, two rows a lane group),
@@ -924,13 +943,13 @@ Csr make_csr(const int32_t *kv_indptr, const int32_t *kv_indices, const int32_t 
     return {kv_indptr, kv_indices, last_page_len, (int)max_pages, batch, ps, (int)num_pages, mul, 31 + k};
 }
 
-template <int D, bool kE4m3, bool kDiff, bool kVar>
+template <int D, bool kE4m3, bool kDiff, bool kVar, bool kStall = false>
 int launch_weights_kernel(const WeightsParams &p, int64_t tasks, int sms, cudaStream_t stream) {
     using LY = StreamLayout<D, kE4m3>;
     static bool configured[64] = {false};
     int dev = 0;
     if (current_sms(&dev) < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
-    auto kern = weights_kernel<D, kE4m3, kDiff, kVar>;
+    auto kern = weights_kernel<D, kE4m3, kDiff, kVar, kStall>;
     if (!configured[dev]) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kSmem);
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("weights smem attribute: ") + cudaGetErrorString(e));
@@ -973,8 +992,9 @@ int launch_accumulate_weights(const bsp_problem *P, const void *q, const float *
                               const int8_t *k_exp, int64_t num_pages, float *weights, int32_t batch,
                               const int32_t *qo_indptr, const int32_t *kv_indptr, const int32_t *kv_indices,
                               int64_t max_table_pages, const int32_t *last_page_len, float sm_scale, float decay,
-                              const float *lambda, cudaStream_t stream) {
+                              const float *lambda, int64_t stall_limit, cudaStream_t stream) {
     WeightsParams p;
+    p.wait_limit = stall_limit;
     p.csr = make_csr(kv_indptr, kv_indices, last_page_len, max_table_pages, batch, P->page_size, num_pages);
     p.qo_indptr = qo_indptr;
     p.q = q;
@@ -1009,6 +1029,9 @@ int launch_accumulate_weights(const bsp_problem *P, const void *q, const float *
         }
         return launched("weights");
     }
+    if (stall_limit > 0)
+        return k_exp ? launch_weights_kernel<128, true, false, false, true>(p, tasks, sms, stream)
+                     : launch_weights_kernel<128, false, false, false, true>(p, tasks, sms, stream);
     if (k_exp) return launch_weights<128, true>(p, tasks, sms, stream);
     return D == 128 ? launch_weights<128, false>(p, tasks, sms, stream) : launch_weights<64, false>(p, tasks, sms, stream);
 }

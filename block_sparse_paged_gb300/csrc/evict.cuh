@@ -61,7 +61,13 @@ struct WeightsParams {
     int n_tokens, H_qo, H_kv, g;
     float scale_log2, cap_in, cap_out, decay;
     int soft_cap_on, window;
+    long long wait_limit;  // kStall alone: SM clock cycles
 };
+
+// Every wait of these kernels is bounded. One that gives up (a fault, not a stall) ends the CTA's work, and what it had
+// not summed yet becomes NaN, so that no weight is left as it was unnoticed. kStall: the self-test's instantiations, where
+// the warps that bring the keys stop after the first few.
+constexpr long long kWaitLimitCycles = 4000000000ll;  // about 2 s at 2 GHz
 
 // Virtual blocks of kTokens tokens: request b's begin at floor(kv_indptr[b] * ps / kTokens) + b, which
 // leaves room for ceil(len / kTokens) of them without a prefix sum over the requests. The first is
@@ -99,6 +105,6 @@ __device__ __forceinline__ Queries queries(const WeightsParams &p, int b) {
 // csrc/weights_prefill.cu: whether its kernel takes a call, and its launch.
 bool weights_prefill_takes(const bsp_problem *problem, int64_t num_pages, int64_t n_tokens, int32_t batch, const int32_t *qo_indptr);
 int launch_weights_prefill(const bsp_problem *problem, const evict::WeightsParams &w, int64_t num_pages, int64_t max_table_pages,
-                           int sms, cudaStream_t stream);
+                           int sms, cudaStream_t stream);  // (w.wait_limit > 0: the self-test)
 
 }  // namespace bsp

@@ -27,7 +27,7 @@
 // accumulator of 256 columns per half was 507 (against 478), the next tile awaited inside a tile 397.
 // Units go to CTAs in the order of the table; a request's first units have the most queries
 // under the causal mask. Long units run one per CTA, so that the block scheduler levels them.
-// Every wait is bounded; a wait that gives up makes NaN of the unit's weights.
+// Every wait is bounded; one that gives up makes NaN of the weights that its CTA has not summed by then.
 #include <cuda.h>
 
 #include <algorithm>
@@ -80,7 +80,6 @@ constexpr int kOffPart = kOffOdd + kSlots * kOddWords * 4;  // [2 units][256 key
 constexpr int kSmemBytes = kOffPart + 2 * kUnit * 4 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "tiles exceed shared memory");
 constexpr uint32_t kTmemCols = 512;
-constexpr long long kWaitLimitCycles = 4000000000ll;       // about 2 s at 2 GHz: a fault, not a stall
 
 struct PrefillWeights {
     WeightsParams w;
@@ -193,7 +192,7 @@ __device__ __forceinline__ uint4 three_parts(float lse, float f) {
     return make_uint4((h & 0xffffu) | (m << 16), dev::pack_bf16(r - dev::bf16_lo(m), 0.f), 0u, 0u);
 }
 // kVar: soft-cap compiled in. kDiff: differential weights. kLong: units of many query tiles.
-template <bool kVar, bool kDiff, bool kLong>
+template <bool kVar, bool kDiff, bool kLong, bool kStall = false>
 __global__ void __launch_bounds__(kThreads, 1)
     weights_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const PrefillWeights pp) {
     constexpr int kKStages = kLong ? 1 : 2, kQStages = kLong ? 4 : 2, kOffQ = kOffK + kKStages * 2 * kTile;
@@ -234,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto wait1 = [&](uint32_t b, uint32_t parity) -> bool {
-        if (mbar_wait_spin(b, parity, kWaitLimitCycles, abort_flag)) return true;
+        if (mbar_wait_spin(b, parity, kStall ? p.wait_limit : kWaitLimitCycles, abort_flag)) return true;
         *abort_flag = 1;
         return false;
     };
@@ -310,6 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             columns(0);
             for (int i = 0; i < x.tiles && ok; ++i, ++n) {
                 const int qst = n % kQStages, sl = n % kSlots, pos0 = (x.tile0 + i) * ppt;
+                if (kStall && n == 3) {
+                    ok = false;
+                    break;
+                }
                 if (!(ok = wait(bar(kQEmpty0 + qst), ((n / kQStages) & 1) ^ 1))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar(kQFull0 + qst), kTile);
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + ((uint32_t)(q4 * 32) << 16) + half * 256;
         int n = 0, meet = 0;
         bool ok = true;
-        for (Walk<kLong> w(p, lane); w.u < units && ok; w.on(p, lane)) {
+        for (Walk<kLong> w(p, lane); w.u < units; w.on(p, lane)) {  // (behind a wait that gave up: NaN, without waiting)
             if (!w.unit(p, lane, x)) continue;
             const int t = x.t0 + key;
             int page = 0, place = 0;
@@ -421,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // tiles all of whose queries see all keys of the unit
             const int full_lo = p.window > 0 ? x.tiles : over<kLong>(max(0, x.t0 + kUnit - 1 - x.off) + ppt - 1, ppt) - x.tile0;
             const int full_hi = over<kLong>(x.qs.n, ppt) - x.tile0;
-            for (int i = 0; i < x.tiles; ++i, ++n) {
+            const bool live = ok;
+            for (int i = 0; i < x.tiles && ok; ++i, ++n) {
                 const int acc = kDiff ? 0 : n & 1, use = kDiff ? n : n >> 1, sl = n % kSlots;
                 if (!(ok = wait(bar(kSFull0 + 2 * half + acc), use & 1))) break;
                 tc_fence_after();
@@ -538,10 +542,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the columns' two halves
             float *part = reinterpret_cast<float *>(smem + kOffPart) + (meet & 1) * kUnit + key;
             const float sum = (s0 + s1) + (s2 + s3);
-            if (col0) *part = sum;
-            mbar_arrive(bar(kMeet0 + half * 4 + q4));
-            ok = ok && wait(bar(kMeet0 + half * 4 + q4), meet & 1);
-            ++meet;
+            if (live) {
+                if (col0) *part = ok ? sum : NAN;
+                mbar_arrive(bar(kMeet0 + half * 4 + q4));
+                ok = ok && wait(bar(kMeet0 + half * 4 + q4), meet & 1);
+                ++meet;
+            }
             if (!col0 && slot != kNoRow) *at = ok ? fmaf(p.decay, old, sum + *part) : NAN;
         }
     }
@@ -593,11 +599,13 @@ int launch_weights_prefill(const bsp_problem *P, const evict::WeightsParams &w, 
         return diff ? (var ? weights_prefill_kernel<true, true, kLong> : weights_prefill_kernel<false, true, kLong>)
                     : (var ? weights_prefill_kernel<true, false, kLong> : weights_prefill_kernel<false, false, kLong>);
     };
-    auto kern = longer ? pick(std::true_type{}) : pick(std::false_type{});
-    static bool configured[8][64] = {{false}};
+    const bool stall = w.wait_limit > 0;
+    auto kern = stall ? (longer ? weights_prefill_kernel<false, false, true, true> : weights_prefill_kernel<false, false, false, true>)
+                      : longer ? pick(std::true_type{}) : pick(std::false_type{});
+    static bool configured[10][64] = {{false}};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fail(BSP_ERR_CUDA, "no current CUDA device");
-    bool &done = configured[(longer ? 4 : 0) + (diff ? 2 : 0) + (var ? 1 : 0)][dev];
+    bool &done = configured[stall ? (longer ? 9 : 8) : (longer ? 4 : 0) + (diff ? 2 : 0) + (var ? 1 : 0)][dev];
     if (!done) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return fail(BSP_ERR_CUDA, std::string("weights smem attribute: ") + cudaGetErrorString(e));

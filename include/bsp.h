@@ -604,6 +604,8 @@ size_t bsp_prefill_fp8_region_size(const bsp_plan_info *plan);
  *   lambda       NULL, or device float [H_qo]: the weights of a differential run
  *                (bsp_decode_run_diff): lse float [n_tokens, H_qo, 2], 8-byte aligned, and a head gives
  *                |p1 - lambda p2| of its two maps' weights
+ * Waits inside are bounded: where one gives up (after about 2 s, a fault), the weights that were
+ * not yet summed become NaN.
  * Supported: bf16 with D in {64, 128}, fp32 with D in {32, 64, 128, 256} (no lambda).
  */
 int bsp_accumulate_weights(const bsp_problem *problem, const void *q, const float *lse, int64_t n_tokens,
@@ -695,6 +697,16 @@ int bsp_decode_run_static(const bsp_plan_info *plan, const void *host_staging, c
  * kernels use on the workspace status word, and the kernel returns: no fault,
  * the context stays usable. Stream-ordered; BSP_OK once launched. */
 int bsp_check_bounded_wait(int64_t limit_cycles, int32_t *status, bsp_stream_t stream);
+
+/* Self-test of bsp_accumulate_weights where a wait inside it gives up: the same call, in which the warps
+ * that bring the keys stop after the first few, with waits of limit_cycles SM clock cycles (1 .. 2^33).
+ * Afterwards each weight of the batch's tokens is what bsp_accumulate_weights makes of it or NaN; no
+ * fault, the context stays usable. bf16 problems with head_dim 128, no window, soft-cap or lambda. */
+int bsp_check_weights_wait(const bsp_problem *problem, const void *q, const float *lse, int64_t n_tokens,
+                           const void *k_pages, const int8_t *k_exp, int64_t num_pages, float *weights, int32_t batch,
+                           const int32_t *qo_indptr, const int32_t *kv_indptr, const int32_t *kv_indices,
+                           int64_t max_table_pages, const int32_t *last_page_len, float sm_scale, float decay,
+                           int64_t limit_cycles, bsp_stream_t stream);
 
 /* Read (and clear) the device error word that kernels set when a bounded wait
  * gives up or a bounds check trips (it lives in the workspace section at
