@@ -444,7 +444,8 @@ int accumulate(const bsp_problem *problem, const void *q, const float *lse, int6
                float sm_scale, float decay, const float *lambda, int64_t stall_limit, bsp_stream_t stream) {
     if (!problem) return fail(BSP_ERR_INVALID_ARG, "problem is NULL");
     bsp_problem P = *problem;
-    P.mode = BSP_MODE_DECODE;  // (the mode's own limits say nothing here)
+    P.mode = BSP_MODE_DECODE;  // (members that the call does not read, and their own limits)
+    P.causal = 1;
     if (!check_problem(&P)) return last_code();
     int rc = check_table(batch, kv_indptr, kv_indices, max_table_pages, last_page_len, num_pages, P.page_size, P.num_kv_heads);
     if (rc != BSP_OK) return rc;

@@ -92,6 +92,12 @@ def test_nothing_to_accumulate(native):
     assert accumulate(native, cap=0, kvi=None) == native.BSP_OK
 
 
+def test_accumulate_does_not_read_the_other_members(native):
+    """The mode, causal and sink of the problem say nothing here."""
+    for kw in (dict(mode=5), dict(causal=7), dict(causal=-1), dict(mode=1, num_qo_heads=12)):
+        assert accumulate(native, batch=0, **kw) == native.BSP_OK
+
+
 def select(native, **kw):
     a = dict(w=P16, pages=9, ps=16, H=2, batch=4, kvp=P16, kvi=P16, cap=9, last=P16, budget=P16, most=8, sinks=1, recent=2,
              kept=P16, new=P16)
