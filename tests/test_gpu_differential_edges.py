@@ -95,3 +95,28 @@ def test_items_without_keys_behind_split_ones(bsp, norm):
     for _ in range(50):
         o, l = r()
         assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@MODES
+@POOLS
+def test_replay_after_another_plan(bsp, mode, f8):
+    """A captured run follows a new plan in its workspace, and sets no status there."""
+    qo, kv = ([1] * 3, [700, 20, 300]) if mode == "decode" else ([200, 20, 1], [700, 20, 300])
+    r = Run(bsp, 78, qo, kv, 16, 4, 16, mode=mode, f8=f8, norm=True, max_gather_pages=100 if mode == "prefill" else 0)
+    r()
+    out, lse = torch.empty_like(r.q), torch.empty(r.q.shape[:2] + (2,), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r(out=out, lse=lse)
+    n = Run(bsp, 79, [1] * 3 if mode == "decode" else [100, 100, 21], [300, 600, 90], 16, 4, 16, mode=mode, f8=f8, norm=True)
+    pool, tab = n.k.shape[0], n.idx.numel()
+    assert n.q.shape == r.q.shape and pool <= r.k.shape[0] and tab <= r.idx.numel()
+    r.pa.plan(n.b.kv_indptr, n.b.last_page_len, qo_indptr=n.b.qo_indptr)
+    for mine, its in [(r.k.view(torch.uint8), n.k.view(torch.uint8)), (r.v.view(torch.uint8), n.v.view(torch.uint8)),
+                      (r.idx, n.idx)] + [(r.e[x], n.e[x]) for x in r.e]:
+        mine[:its.shape[0]] = its
+    for mine, its in ((r.q, n.q), (r.lam_t, n.lam_t), (r.norm_t, n.norm_t)):
+        mine.copy_(its)
+    graph.replay()
+    n.pa = r.pa  # (whose status word `check` asks)
+    n.check(out, lse)
