@@ -40,7 +40,7 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float(e >= -126 
 // stay in a warp's registers from task to task.
 //   6 warps (8 over rows of 128 bytes) look tokens up, a task each in turn, and leave rows, weights
 //     and exponents in a ring: the chain of dependent reads (request, page id, weight) runs ahead of
-//     the warps that need it (4 warps: 109 us instead of 100 below, 46 instead of 37 over e4m3)
+//     the warps that need it (with 4 of them 9 us more in both forms below)
 //   12 (16) warps compute, a task each in turn: 16-byte asynchronous copies bring the rows of the
 //     next task into the warp's own two buffers (any page size alike) while one is worked on;
 //     S = K Q^T by m16n8k16, keys on the M side, queries on the N side. The order of the head
@@ -48,8 +48,8 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float(e >= -126 
 //     words as they are, and q is read the same way.
 // 64 requests up to 8192 tokens, us: warps that look up their own keys and load them into
 // registers 120, with a ring of bulk copies per warp 153, loader warps and bulk copies 198 (one
-// bulk copy per row: an SM starts one in about 25 cycles, whatever its size), now 98 (5.85 TB/s);
-// 32 x 4096 tokens of an 8-bit cache 34 (4.2 TB/s).
+// bulk copy per row: an SM starts one in about 25 cycles, whatever its size), now 97-99 (5.8-5.9 TB/s);
+// 32 x 4096 tokens of an 8-bit cache 34.6 (4.1 TB/s).
 constexpr int kTaskTokens = 32;
 
 template <int D, bool kE4m3>
@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(cons
     const int32_t *kept = p.kept + ((size_t)b * H + h) * p.max_keep;
     const int slices = p.slices;
 
-    // this thread's rows r0 + tid + 256 u, below r1: the slots of their source and their place, or kNoRow.
+    // this thread's rows r0 + tid + kThreads u, below r1: the slots of their source and their place, or kNoRow.
     // (A position below the place, one behind the request, or a page outside the pool: the row stays.)
     auto look_up = [&](int r0, int r1, uint32_t (&src)[kU], uint32_t (&dst)[kU], int (&page)[kU]) {
         int at[kU];
@@ -1053,7 +1053,9 @@ int launch_select_tokens(const float *weights, int64_t num_pages, int32_t page_s
     int dev = 0;
     const int sms = current_sms(&dev);
     if (sms < 0) return fail(BSP_ERR_CUDA, "no current CUDA device");
-    // CTAs per row: enough to hold the mean row in registers, more where rows are few
+    // CTAs per row: enough to hold the mean row in registers, more where rows are few. (The mean over kv_indices' room,
+    // all that the host knows: a table with room, or one long row among many short ones, gets other clusters than it
+    // would need, and is slower.)
     const int64_t rows = (int64_t)batch * num_kv_heads, mean = max_table_pages * page_size / batch;
     int C = 1;
     while (C < kMaxCluster && (mean > (int64_t)C * kSelChunk || (rows * C * 2 <= 2 * (int64_t)sms && mean / C >= 4096))) C *= 2;

@@ -22,7 +22,7 @@
 // (differential weights need both for the two maps of a tile); one is free again before its last
 // columns are summed. Two prompts of about 7k, 32 / 8 heads, us: one thread per key (8 warps) 543, two
 // 512, fewer instructions for waits and masks 497, MMAs by an elected thread 478, LSE in the
-// accumulator 396, early release and first load 370, look-up a unit ahead 357. Bound by the sum
+// accumulator 396, early release and first load 370, look-up a unit ahead 357 (on other boxes 377-390). Bound by the sum
 // warps' instructions and their waits at a tile's begin (exponentials alone 230, products 255); one
 // accumulator of 256 columns per half was 507 (against 478), the next tile awaited inside a tile 397.
 // Units go to CTAs in the order of the table; a request's first units have the most queries
@@ -105,7 +105,7 @@ __device__ __forceinline__ int over(int a, int b) {
 // A CTA's units: u = blockIdx.x, blockIdx.x + gridDim.x, .. in the order (virtual block, head). Where there are
 // many (kLong false) they are walked without a division or, as a rule, a search per unit, which take 2,000 cycles
 // (64 requests x 4096 tokens with 16 queries 196 -> 170 us); where there is one, all that a warp keeps is u (two
-// prompts of about 7k 357 us, with the walk's registers 370).
+// prompts of about 7k 357 us, with the walk's registers 370, on one box).
 template <bool kLong>
 struct Walk {
     uint32_t u;

@@ -517,7 +517,7 @@ int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const vo
  *             * out_scale (mean over the head's 128 values; rounded once, at the end; 0 where
  *             y is all 0, for norm_eps = 0 too)
  * Masks, window and soft-cap are the plan's and hold for both maps; a query without a
- * visible key gets 0; NaN scores make NaN of their map's LSE and of the head's output. The
+ * visible key gets 0; NaN scores make NaN of LSE and of the head's output. The
  * cache is laid out as for any other run, so page tables, appends and bsp_compact_cache are
  * the same.
  *   plan         from bsp_plan over twice the heads: problem.num_qo_heads = 2 * H_q (the
