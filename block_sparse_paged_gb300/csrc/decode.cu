@@ -1137,7 +1137,20 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                 if (valid > 0) {
                     const uint32_t kb = sbase + s * LY::kStageBytes;
                     const uint32_t vb = kb + LY::kTileBytes;
-                    if (kTma && valid < 16) {
+                    if constexpr (kDiff) {
+                        // V rows of this warp before the window's edge, and those of the page boxes past the chunk end
+                        // (copied whole), may hold anything: zero them so that P = 0 meets finite values
+                        if (lo_rel > 0 || (kTma && valid < 16)) {
+#pragma unroll 1
+                            for (int e = lane; e < 16 * (D / 8); e += 32) {
+                                const int rr = e / (D / 8);
+                                if (rr < lo_rel || (kTma && rr >= valid))
+                                    *reinterpret_cast<uint4 *>(smem + (vb - sbase) + LY::chunk(row0 + rr, e % (D / 8))) =
+                                        make_uint4(0, 0, 0, 0);
+                            }
+                            __syncwarp();
+                        }
+                    } else if (kTma && valid < 16) {
                         // whole page boxes were copied: V rows of this warp past the chunk
                         // end may hold anything; zero them so that P = 0 meets finite values
                         for (int e = lane; e < (16 - valid) * (D / 8); e += 32) {

@@ -850,13 +850,15 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 }
                 tmem_wait_st();
                 const int vz_end = min(kKvTile, (valid + p.box_rows - 1) / p.box_rows * p.box_rows);
-                if (sub == 0 && valid < vz_end) {
+                // kDiff: rows before the first position's window edge, too
+                const int vz_lo = kDiff && kVar && p.window_left > 0 ? w.pos0 + w.kv_len - w.qo_len - p.window_left - tok0 : 0;
+                if (sub == 0 && (valid < vz_end || vz_lo > 0)) {
                     // rows of the last copied box past the chunk end may hold anything:
                     // zero them so that P = 0 meets finite values (rows past the box keep
                     // an earlier tile's finite values, the ring starts zeroed)
                     const int vst = j % kVStages, vrd = j / kVStages;
                     if (!(ok = wait_bar_warp(ctx, bar(kVFull0 + vst), vrd & 1))) break;
-                    if (r >= valid && r < vz_end) {
+                    if ((r >= valid && r < vz_end) || r < vz_lo) {
                         uint4 *v0 = reinterpret_cast<uint4 *>(smem + kOffV + vst * kTile + r * 128);
                         uint4 *v1 = reinterpret_cast<uint4 *>(smem + kOffV + vst * kTile + kHalf + r * 128);
 #pragma unroll

@@ -517,9 +517,10 @@ int bsp_prefill_run_fp8_block(const bsp_plan_info *plan, const void *q, const vo
  *             * out_scale (mean over the head's 128 values; rounded once, at the end; 0 where
  *             y is all 0, for norm_eps = 0 too)
  * Masks, window and soft-cap are the plan's and hold for both maps; a query without a
- * visible key gets 0; NaN scores make NaN of LSE and of the head's output. The
- * cache is laid out as for any other run, so page tables, appends and bsp_compact_cache are
- * the same.
+ * visible key gets 0; NaN scores make NaN of LSE and of the head's output; NaN and infinities
+ * of V reach the queries that see them, in a prefill also the others of their query tile (128 /
+ * (H_q / H_kv) positions), and nobody where no query of the tile sees them. The cache is laid
+ * out as for any other run, so page tables, appends and bsp_compact_cache are the same.
  *   plan         from bsp_plan over twice the heads: problem.num_qo_heads = 2 * H_q (the
  *                maps), head_dim 128, bf16, no sink
  *   q, o         device, bf16 [n_tokens, H_q, 128]

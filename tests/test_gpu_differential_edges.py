@@ -1,9 +1,11 @@
-"""Differential attention at the edges: norms of rows that are zero, queries of NaN, the order of a queue's items."""
+"""Differential attention at the edges: norms of rows that are zero, queries of NaN, values before a window, the order of a queue's
+items."""
 import numpy as np
 import pytest
 import torch
 
 from gpu_helpers import lib
+from oracle import evict as ev
 from test_gpu_differential import Run
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +122,26 @@ def test_replay_after_another_plan(bsp, mode, f8):
     graph.replay()
     n.pa = r.pa  # (whose status word `check` asks)
     n.check(out, lse)
+
+
+@MODES
+@POOLS
+@pytest.mark.parametrize("num_ctas", [1, 40])
+@pytest.mark.parametrize("ps,window", [(1, 50), (5, 51), (12, 300), (16, 50), (128, 303)])
+def test_values_before_a_window_reach_nobody(bsp, mode, f8, num_ctas, ps, window):
+    """The page that a window begins in holds older tokens: NaN of theirs changes no bit."""
+    qo, kv = ([1, 1, 1], [700, 900, 40]) if mode == "decode" else ([31, 5, 40], [700, 900, 40])
+    r = Run(bsp, 80, qo, kv, 16, 4, ps, mode=mode, f8=f8, window=window, num_ctas=num_ctas)
+    out, lse = (x.clone() for x in r())
+    r.check(out, lse)
+    for i, (n, L) in enumerate(zip(qo, kv)):
+        if L - n - window > 0:
+            pg, pl = (torch.from_numpy(x).cuda() for x in ev.slots(r.b.kv_indptr, r.b.kv_indices, i, L - n - window, ps))
+            for t in (r.k, r.v):
+                if f8:
+                    t.view(torch.uint8)[pg, pl] = 0x7f
+                else:
+                    t[pg, pl] = float("nan")
+    o, l = r()
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and torch.equal(l, lse)
