@@ -1138,13 +1138,13 @@ __global__ void __launch_bounds__(DecodeLayout<D, kTma, kFp8, kNH, kBlk>::kThrea
                     const uint32_t kb = sbase + s * LY::kStageBytes;
                     const uint32_t vb = kb + LY::kTileBytes;
                     if constexpr (kDiff) {
-                        // V rows of this warp before the window's edge, and those of the page boxes past the chunk end
-                        // (copied whole), may hold anything: zero them so that P = 0 meets finite values
-                        if (lo_rel > 0 || (kTma && valid < 16)) {
+                        // V rows of this warp before the window's edge and past the chunk end (of a page box, or of
+                        // another request's stage before) may hold anything: zero them so that P = 0 meets finite values
+                        if (lo_rel > 0 || valid < 16) {
 #pragma unroll 1
                             for (int e = lane; e < 16 * (D / 8); e += 32) {
                                 const int rr = e / (D / 8);
-                                if (rr < lo_rel || (kTma && rr >= valid))
+                                if (rr < lo_rel || rr >= valid)
                                     *reinterpret_cast<uint4 *>(smem + (vb - sbase) + LY::chunk(row0 + rr, e % (D / 8))) =
                                         make_uint4(0, 0, 0, 0);
                             }

@@ -400,9 +400,14 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                         tma_load_3d(d + kHalf, &tk, bar(kKFull0 + stage), 64, w.kv_head, row0);
                     }
                     if (!(ok = wait_bar_warp(ctx, bar(kVEmpty0 + vst), (vrd & 1) ^ 1))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(kVFull0 + vst), bytes);
+                    // kDiff: the boxes past the chunk end, whose rows are those of an earlier tile, of another request it
+                    // may be, are filled with zeros (a box in front of the pool), so that NaN and infinities of its V stay
+                    // there. (16 ragged prompts 858 -> 867 us; zeroed by the softmax warps 906.)
+                    const bool past = kDiff && lane >= nseg && lane < kKvTile / p.box_rows;
+                    if (past) row0 = -p.box_rows;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(kVFull0 + vst), kDiff ? (uint32_t)kTile : bytes);
                     __syncwarp();
-                    if (lane < nseg) {
+                    if (lane < nseg || past) {
                         const uint32_t d = sb + kOffV + vst * kTile + seg;
                         tma_load_3d(d, &tv, bar(kVFull0 + vst), 0, w.kv_head, row0);
                         tma_load_3d(d + kHalf, &tv, bar(kVFull0 + vst), 64, w.kv_head, row0);
@@ -485,9 +490,9 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 for (int ii = 0; ii < kKvTile / 2; ++ii) {
                     const int key = 2 * ii + (lane >> 4);  // key >> 5 == ii >> 4 for the whole warp
                     const uint64_t o = __shfl_sync(0xffffffffu, off[ii >> 4], key & 31);
-                    if (key < valid)
+                    if (kDiff || key < valid)  // (kDiff: zeros past the chunk end, as by TMA)
                         dev::cp_async_16(dst + (c >> 3) * kHalf + key * 128 + (((c & 7) ^ (key & 7)) << 4),
-                                         src + o + c * 16, 16);
+                                         src + o + c * 16, key < valid ? 16 : 0);
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(kVFull0 + vst))
                              : "memory");
@@ -855,7 +860,7 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 if (sub == 0 && (valid < vz_end || vz_lo > 0)) {
                     // rows of the last copied box past the chunk end may hold anything:
                     // zero them so that P = 0 meets finite values (rows past the box keep
-                    // an earlier tile's finite values, the ring starts zeroed)
+                    // an earlier tile's values, the ring starts zeroed; kDiff: they are zeros)
                     const int vst = j % kVStages, vrd = j / kVStages;
                     if (!(ok = wait_bar_warp(ctx, bar(kVFull0 + vst), vrd & 1))) break;
                     if ((r >= valid && r < vz_end) || r < vz_lo) {

@@ -1,5 +1,5 @@
-"""Differential attention at the edges: norms of rows that are zero, queries of NaN, values before a window, the order of a queue's
-items."""
+"""Differential attention at the edges: norms of rows that are zero, queries of NaN, values before a window and of other requests, the
+order of a queue's items."""
 import numpy as np
 import pytest
 import torch
@@ -145,3 +145,31 @@ def test_values_before_a_window_reach_nobody(bsp, mode, f8, num_ctas, ps, window
     o, l = r()
     torch.cuda.synchronize()
     assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@MODES
+@POOLS
+@pytest.mark.parametrize("num_ctas", [1, 40])
+@pytest.mark.parametrize("ps", [1, 5, 8, 16, 128])
+def test_a_request_of_nan_reaches_no_other(bsp, mode, f8, num_ctas, ps):
+    """K and V of one request are NaN: its outputs are, and every bit of the others' stays."""
+    qo, kv = ([1] * 5, [700, 901, 40, 17, 333]) if mode == "decode" else ([30, 5, 40, 17, 100], [700, 901, 40, 17, 333])
+    r = Run(bsp, 82, qo, kv, 16, 4, ps, mode=mode, f8=f8, num_ctas=num_ctas)
+    out, lse = (x.clone() for x in r())
+    r.check(out, lse)
+    clean = [t.clone() for t in (r.k, r.v)]
+    for i in range(5):
+        for t, c in zip((r.k, r.v), clean):
+            t.view(torch.uint8).copy_(c.view(torch.uint8))
+        pg, pl = (torch.from_numpy(x).cuda() for x in ev.slots(r.b.kv_indptr, r.b.kv_indices, i, kv[i], ps))
+        for t in (r.k, r.v):
+            if f8:
+                t.view(torch.uint8)[pg, pl] = 0x7f
+            else:
+                t[pg, pl] = float("nan")
+        o, l = r()
+        torch.cuda.synchronize()
+        its = slice(int(r.b.qo_indptr[i]), int(r.b.qo_indptr[i + 1]))
+        assert torch.isnan(o[its]).all() and torch.isnan(l[its]).all()
+        o[its], l[its] = out[its], lse[its]
+        assert torch.equal(o, out) and torch.equal(l, lse), i
