@@ -212,7 +212,8 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, float s) {
 // wait for their next S; everything behind the rings is the bf16 kernel. The codes
 // come by TMA boxes (kTma) or cp.async, by the same rule.
 // kNan: a row whose sum is NaN is written as NaN (the e4m3 cache, its bf16 copy too; rows
-// over bf16 pools get an LSE of -inf then. Asking at run time cost those 0.5%).
+// over bf16 pools get an LSE of -inf then. Asking at run time cost those 0.5%), and V rows
+// before a tile's windows are left out.
 // kDiff: differential attention. The two subtiles are the two softmax maps of the same 128 rows:
 // subtile 0 multiplies the first halves of the rows of Q and K (64 of 128 dimensions, one swizzled
 // slab each), subtile 1 the second ones, and both take the whole rows of V; so Q is one tile, the
@@ -855,8 +856,8 @@ __global__ void __launch_bounds__(kTma || kFp8 ? kThreads : kThreadsGather, 1)
                 }
                 tmem_wait_st();
                 const int vz_end = min(kKvTile, (valid + p.box_rows - 1) / p.box_rows * p.box_rows);
-                // kDiff: rows before the first position's window edge, too
-                const int vz_lo = kDiff && kVar && p.window_left > 0 ? w.pos0 + w.kv_len - w.qo_len - p.window_left - tok0 : 0;
+                // kNan: rows before the first position's window edge, too
+                const int vz_lo = kNan && kVar && p.window_left > 0 ? w.pos0 + w.kv_len - w.qo_len - p.window_left - tok0 : 0;
                 if (sub == 0 && (valid < vz_end || vz_lo > 0)) {
                     // rows of the last copied box past the chunk end may hold anything:
                     // zero them so that P = 0 meets finite values (rows past the box keep
